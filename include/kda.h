@@ -81,6 +81,7 @@ typedef enum { KDA_GATE_CHANNEL = 0, KDA_GATE_SCALAR = 1, KDA_GATE_NONE = 2 } kd
 #define KDA_DEV_OK 0
 #define KDA_DEV_BAD_CU_SEQLENS 1   /* cu[0] != 0, decreasing, or cu[N] != T_total */
 #define KDA_DEV_BAD_SLOT 2         /* a state slot outside [0, pool_size)          */
+#define KDA_DEV_BAD_POSITION 4     /* a position outside [0, max_position)         */
 
 /*
  * kda_prefill - chunkwise prefill of B equal-length sequences (K3 essay §四
@@ -487,6 +488,178 @@ size_t kda_varlen_prefill_backward_workspace_bytes(int N, int T_total, int H, in
 kda_status_t kda_selftest_bounded_wait(const void *q, const void *k, const void *v, const float *alpha,
                                        const float *beta, void *o, float *final_state, int T, int stall_chunk,
                                        kda_stream_t stream);
+
+/*
+ * ---- Linear attention with a decay, and the norm and rotation in front of it.
+ *
+ * The delta rule without its erase step and with one decay per head is linear
+ * attention (K3 essay §二.1, the state as a key -> value memory that is only
+ * written, with §四's decay):
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = scale S_t^T q_t.
+ *
+ * Decays come as natural logarithms g <= 0 (unlike the linear alpha of the
+ * calls above: the chunked form adds logarithms, and the gradient of a
+ * logarithm stays finite, zero, at a reset). g = -inf, or anything <= -128, is
+ * a reset: the state before the token is gone.
+ *
+ *   KDA_DECAY_TOKEN  log_decay [.., T, H]: one per token and head
+ *   KDA_DECAY_HEAD   log_decay [H]: one per head, the same for every token
+ *   KDA_DECAY_NONE   log_decay is not read and may be NULL: g = 0
+ *
+ * q, k, v may be views of a wider tensor (a fused projection): q_stride,
+ * k_stride, v_stride are the distances between tokens in elements, 0 standing
+ * for the contiguous H * d; the H heads of a token are contiguous, rows start
+ * on 16 bytes, and tokens (of all B sequences, or of the packed batch) follow
+ * one another at that distance. Outputs are contiguous. Sizes, types,
+ * alignment, streams and errors as for the calls above.
+ */
+typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1, KDA_DECAY_NONE = 2 } kda_decay_t;
+
+/*
+ * kda_linear_prefill - B sequences of T tokens.
+ *
+ *   q, k          [B, T, H, d_k]  qkv_dtype                    (read)
+ *   v             [B, T, H, d_v]  qkv_dtype                    (read)
+ *   initial_state [B, H, d_k, d_v] float32 or NULL (zeros)     (read)
+ *   o             [B, T, H, d_v]  qkv_dtype                    (written)
+ *   final_state   [B, H, d_k, d_v] float32 or NULL             (written)
+ *
+ * final_state may equal initial_state. T = 0 copies the initial state (or
+ * zeros). workspace: kda_linear_prefill_workspace_bytes, 256-byte aligned,
+ * DEVICE; it may be reused as soon as the work is queued on the same stream.
+ * fp32 inputs are computed to fp32 accuracy; with bf16 inputs the states are
+ * still accurate to fp32 and o is rounded once to bf16 after products with
+ * bf16 (or finer) operands. Two calls on the same inputs give the same bits.
+ */
+kda_status_t kda_linear_prefill(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, const float *log_decay, kda_decay_t decay,
+                                float scale, const float *initial_state, void *o, float *final_state, int B, int T,
+                                int H, int d_k, int d_v, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream);
+
+/* Workspace bytes kda_linear_prefill needs (0 for invalid arguments). */
+size_t kda_linear_prefill_workspace_bytes(int B, int T, int H, int d_k, int d_v, kda_dtype_t qkv_dtype);
+
+/*
+ * kda_linear_varlen_prefill - N sequences packed along the token axis
+ * (layouts and cu_seqlens as kda_varlen_prefill, log_decay [T_total, H] with
+ * KDA_DECAY_TOKEN). Every sequence has its own state and block grid: its
+ * results are those of kda_linear_prefill on it alone. A bad cu_seqlens writes
+ * KDA_DEV_BAD_CU_SEQLENS to device_status (DEVICE int32, nullable) and nothing
+ * else; otherwise KDA_DEV_OK is written.
+ */
+kda_status_t kda_linear_varlen_prefill(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                       kda_decay_t decay, float scale, const float *initial_state, void *o,
+                                       float *final_state, const int32_t *cu_seqlens, int N, int T_total, int H,
+                                       int d_k, int d_v, void *workspace, size_t workspace_bytes,
+                                       int32_t *device_status, kda_stream_t stream);
+
+/* Workspace bytes kda_linear_varlen_prefill needs (0 for invalid arguments). */
+size_t kda_linear_varlen_prefill_workspace_bytes(int N, int T_total, int H, int d_k, int d_v, kda_dtype_t qkv_dtype);
+
+/*
+ * kda_linear_prefill_backward - the gradients of kda_linear_prefill for
+ * L = sum <d_o, o> + <d_final_state, S_T>. d_o has o's shape and type,
+ * contiguous; d_final_state is float32 or NULL (zero).
+ *   dq, dk  [B, T, H, d_k], dv [B, T, H, d_v]   qkv_dtype, contiguous  (written)
+ *   dlog_decay  log_decay's shape, float32, or NULL (not wanted): with
+ *               KDA_DECAY_HEAD the sum over every token; zero at a reset
+ *   d_initial_state [B, H, d_k, d_v] float32 or NULL
+ * The gradients of q, k, v have their type, as the backward of the norm in
+ * front of this call takes them. Sums have a fixed order: two calls on the
+ * same inputs give the same bits. workspace:
+ * kda_linear_prefill_backward_workspace_bytes, 256-byte aligned.
+ */
+kda_status_t kda_linear_prefill_backward(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                         kda_decay_t decay, float scale, const float *initial_state, const void *d_o,
+                                         const float *d_final_state, void *dq, void *dk, void *dv, float *dlog_decay,
+                                         float *d_initial_state, int B, int T, int H, int d_k, int d_v,
+                                         void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes kda_linear_prefill_backward needs (0 for invalid arguments). */
+size_t kda_linear_prefill_backward_workspace_bytes(int B, int T, int H, int d_k, int d_v, kda_dtype_t qkv_dtype);
+
+/* kda_linear_varlen_prefill_backward - the gradients of
+ * kda_linear_varlen_prefill; layouts and device_status as there. */
+kda_status_t kda_linear_varlen_prefill_backward(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                                int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                                const float *log_decay, kda_decay_t decay, float scale,
+                                                const float *initial_state, const void *d_o,
+                                                const float *d_final_state, void *dq, void *dk, void *dv,
+                                                float *dlog_decay, float *d_initial_state, const int32_t *cu_seqlens,
+                                                int N, int T_total, int H, int d_k, int d_v, void *workspace,
+                                                size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/* Workspace bytes kda_linear_varlen_prefill_backward needs (0 for invalid arguments). */
+size_t kda_linear_varlen_prefill_backward_workspace_bytes(int N, int T_total, int H, int d_k, int d_v,
+                                                          kda_dtype_t qkv_dtype);
+
+/*
+ * kda_linear_decode_step - one token per sequence: q, k [N, H, d_k],
+ * v, o [N, H, d_v] qkv_dtype; log_decay [N, H] (KDA_DECAY_TOKEN) or [H];
+ * state [N, H, d_k, d_v] float32, updated in place. The strides are between
+ * sequences.
+ */
+kda_status_t kda_linear_decode_step(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                    int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                    kda_decay_t decay, float scale, float *state, void *o, int N, int H, int d_k,
+                                    int d_v, kda_stream_t stream);
+
+/* kda_linear_decode_step_slots - the same on state_pool[slots[n]] (slots,
+ * fresh slots and device_status as kda_decode_step_slots). */
+kda_status_t kda_linear_decode_step_slots(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                          int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *log_decay,
+                                          kda_decay_t decay, float scale, float *state_pool, const int32_t *slots,
+                                          int pool_size, void *o, int N, int H, int d_k, int d_v,
+                                          int32_t *device_status, kda_stream_t stream);
+
+/* Norm of a head: none, x / sqrt(sum x^2 + eps), x / sqrt(mean x^2 + eps). */
+typedef enum { KDA_NORM_NONE = 0, KDA_NORM_L2 = 1, KDA_NORM_RMS = 2 } kda_norm_t;
+/* Rotary pairs: channels (i, i + rotary / 2), or (2 i, 2 i + 1). */
+typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout_t;
+
+/*
+ * kda_qk_norm_rope - the norm of every query and key head and the rotary
+ * positions, in one pass over q and k:
+ *     n = w * x / norm(x),   out = n with channel pair i of its first `rotary`
+ *     channels (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i).
+ *   q [tokens, H_q, d], k [tokens, H_k, d]   dtype, token strides as above (read)
+ *   positions  [tokens] int32; a token whose position lies outside
+ *              [0, max_position) is left out and sets KDA_DEV_BAD_POSITION
+ *   rope_table [max_position, rotary] float32: rotary / 2 cosines, then sines
+ *              (scaling for long contexts is in the table)
+ *   rotary     a multiple of 16 up to d; 0: no rotation, positions and table unused
+ *   q_weight, k_weight  [d] float32 or NULL (ones), shared by the heads
+ *   q_out, k_out  contiguous, may be q and k themselves                (written)
+ * d is 64 or 128; eps > 0 unless norm is KDA_NORM_NONE.
+ */
+kda_status_t kda_qk_norm_rope(const void *q, const void *k, kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                              const int32_t *positions, const float *rope_table, int max_position, int rotary,
+                              kda_rope_layout_t layout, const float *q_weight, const float *k_weight, kda_norm_t norm,
+                              float eps, void *q_out, void *k_out, int64_t tokens, int H_q, int H_k, int d,
+                              int32_t *device_status, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope_backward - its gradients: q, k are the inputs, dq_out and
+ * dk_out the gradients of the outputs (contiguous); dq, dk in dtype,
+ * contiguous; dq_weight, dk_weight [d] float32 or NULL, summed over every
+ * token and head in a fixed order (a token with a bad position adds nothing).
+ * workspace (kda_qk_norm_rope_backward_workspace_bytes(d), 256-byte aligned)
+ * is needed when a weight gradient is wanted.
+ */
+kda_status_t kda_qk_norm_rope_backward(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                                       kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                       const int32_t *positions, const float *rope_table, int max_position, int rotary,
+                                       kda_rope_layout_t layout, const float *q_weight, const float *k_weight,
+                                       kda_norm_t norm, float eps, void *dq, void *dk, float *dq_weight,
+                                       float *dk_weight, int64_t tokens, int H_q, int H_k, int d, void *workspace,
+                                       size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/* Workspace bytes kda_qk_norm_rope_backward needs for weight gradients. */
+size_t kda_qk_norm_rope_backward_workspace_bytes(int d);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char *kda_last_error(void);

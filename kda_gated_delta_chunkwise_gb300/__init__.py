@@ -12,12 +12,22 @@ at once), ``varlen_prefill``,
 go through the native host-buffer pipeline (kda_prefill_host,
 kda_prefill_fp8_host); and for serving with a pool of states indexed by slot:
 ``varlen_prefill_slots``, ``decode_step_slots``; for training,
-``prefill_backward`` (the gradients of ``prefill``). Build the CUDA library with
+``prefill_backward`` (the gradients of ``prefill``). Linear attention with a
+decay (the update without its erase step): ``linear_prefill``,
+``linear_varlen_prefill``, their gradients ``linear_prefill_backward`` and
+``linear_varlen_prefill_backward``, ``linear_decode_step`` and
+``linear_decode_step_slots``; the norm of query and key heads with the rotary
+positions: ``qk_norm_rope``, ``qk_norm_rope_backward``, ``rope_table``. Build the CUDA library with
 ``kda_gated_delta_chunkwise_gb300.build.build()`` first.
 """
-from ._binding import (ALGOS, EXPORTS, GATES, KDA_DEV_BAD_CU_SEQLENS, KDA_DEV_BAD_SLOT,  # noqa: F401
+from ._binding import (ALGOS, EXPORTS, GATES, KDA_DEV_BAD_CU_SEQLENS, KDA_DEV_BAD_SLOT, KDA_DEV_BAD_POSITION,  # noqa: F401
                        KDA_DEV_OK, KdaError, decode_step, decode_step_slots, device_errors, lib_path, load,
                        prefill, prefill_backward, prefill_fp8, prefill_segmented, prefill_segmented_workspace_bytes,
                        prefill_workspace_bytes, segment_plan, selftest_bounded_wait, varlen_prefill,
                        varlen_prefill_backward,
                        varlen_prefill_slots, varlen_workspace_bytes)
+from ._linear import (DECAYS, NORMS, ROPE_LAYOUTS, linear_decode_step, linear_decode_step_slots,  # noqa: F401
+                      linear_prefill, linear_prefill_backward, linear_prefill_backward_workspace_bytes,
+                      linear_prefill_workspace_bytes, linear_varlen_prefill, linear_varlen_prefill_backward,
+                      linear_varlen_prefill_backward_workspace_bytes, linear_varlen_prefill_workspace_bytes,
+                      qk_norm_rope, qk_norm_rope_backward, rope_table)

@@ -24,7 +24,7 @@ KDA_F32, KDA_BF16 = 0, 1
 ALGOS = {"auto": 0, "simt": 1, "tc": 2}
 # gate kinds: per-channel (KDA), one per token-head (Gated DeltaNet), none (delta rule)
 GATES = {"channel": 0, "scalar": 1, "none": 2}
-KDA_DEV_OK, KDA_DEV_BAD_CU_SEQLENS, KDA_DEV_BAD_SLOT = 0, 1, 2
+KDA_DEV_OK, KDA_DEV_BAD_CU_SEQLENS, KDA_DEV_BAD_SLOT, KDA_DEV_BAD_POSITION = 0, 1, 2, 4
 
 EXPORTS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_gate", "kda_prefill_fp8", "kda_prefill_host",
            "kda_prefill_host_workspace_bytes", "kda_prefill_fp8_host", "kda_prefill_fp8_host_workspace_bytes",
@@ -34,6 +34,12 @@ EXPORTS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_gate", "kda_prefill_fp8
            "kda_decode_step", "kda_decode_step_slots", "kda_selftest_bounded_wait",
            "kda_prefill_backward", "kda_prefill_backward_gate", "kda_prefill_backward_workspace_bytes",
            "kda_varlen_prefill_backward", "kda_varlen_prefill_backward_workspace_bytes",
+           "kda_linear_prefill", "kda_linear_prefill_workspace_bytes", "kda_linear_varlen_prefill",
+           "kda_linear_varlen_prefill_workspace_bytes", "kda_linear_prefill_backward",
+           "kda_linear_prefill_backward_workspace_bytes", "kda_linear_varlen_prefill_backward",
+           "kda_linear_varlen_prefill_backward_workspace_bytes", "kda_linear_decode_step",
+           "kda_linear_decode_step_slots", "kda_qk_norm_rope", "kda_qk_norm_rope_backward",
+           "kda_qk_norm_rope_backward_workspace_bytes",
            "kda_device_errors", "kda_last_error", "kda_abi_version")
 
 _lock = threading.Lock()
@@ -116,6 +122,28 @@ def load(path: str | None = None):
         lib.kda_prefill_segment_plan.restype = i
         lib.kda_prefill_segment_plan.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int),
                                                  ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
+        sz, ll, fl = ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
+        qkv = [vp, vp, vp, i, ll, ll, ll, vp, i, fl]  # q, k, v, dtype, strides, log_decay, decay kind, scale
+        lib.kda_linear_prefill.argtypes = qkv + [vp, vp, vp, i, i, i, i, i, vp, sz, vp]
+        lib.kda_linear_varlen_prefill.argtypes = qkv + [vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp, vp]
+        lib.kda_linear_prefill_backward.argtypes = qkv + [vp] * 8 + [i, i, i, i, i, vp, sz, vp]
+        lib.kda_linear_varlen_prefill_backward.argtypes = qkv + [vp] * 9 + [i, i, i, i, i, vp, sz, vp, vp]
+        lib.kda_linear_decode_step.argtypes = qkv + [vp, vp, i, i, i, i, vp]
+        lib.kda_linear_decode_step_slots.argtypes = qkv + [vp, vp, i, vp, i, i, i, i, vp, vp]
+        rope = [vp, vp, i, i, i, vp, vp, i, fl]  # positions, table, max_position, rotary, layout, weights, norm, eps
+        lib.kda_qk_norm_rope.argtypes = [vp, vp, i, ll, ll] + rope + [vp, vp, ll, i, i, i, vp, vp]
+        lib.kda_qk_norm_rope_backward.argtypes = ([vp, vp, vp, vp, i, ll, ll] + rope +
+                                                  [vp, vp, vp, vp, ll, i, i, i, vp, sz, vp, vp])
+        for name in ("kda_linear_prefill", "kda_linear_varlen_prefill", "kda_linear_prefill_backward",
+                     "kda_linear_varlen_prefill_backward", "kda_linear_decode_step", "kda_linear_decode_step_slots",
+                     "kda_qk_norm_rope", "kda_qk_norm_rope_backward"):
+            getattr(lib, name).restype = i
+        for name in ("kda_linear_prefill", "kda_linear_varlen_prefill", "kda_linear_prefill_backward",
+                     "kda_linear_varlen_prefill_backward"):
+            getattr(lib, name + "_workspace_bytes").argtypes = [i, i, i, i, i, i]
+            getattr(lib, name + "_workspace_bytes").restype = sz
+        lib.kda_qk_norm_rope_backward_workspace_bytes.argtypes = [i]
+        lib.kda_qk_norm_rope_backward_workspace_bytes.restype = sz
         lib.kda_last_error.restype = ctypes.c_char_p
         lib.kda_last_error.argtypes = []
         lib.kda_abi_version.restype = ctypes.c_int

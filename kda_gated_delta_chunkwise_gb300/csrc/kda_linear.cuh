@@ -1,0 +1,160 @@
+// Declarations shared by the linear-attention operators, the query/key norm
+// with rotary positions, and the host checks in front of them.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ---------------------------------------------------------------- norm + rotation
+// Blocks of the backward's persistent grid at most: four of 256 threads on
+// each of the 152 SMs.
+constexpr int kNormRopeBwdBlocks = 152 * 4;
+
+struct NormRopeArgs {
+    kda_dtype_t dt;
+    const void *q, *k;            // token strides in elements, heads contiguous
+    int64_t q_stride, k_stride;
+    const void *dyq, *dyk;        // backward: gradients of the outputs, contiguous
+    void *yq, *yk, *dxq, *dxk;    // contiguous
+    const int32_t *positions;     // [tokens]
+    const float *table;           // [max_position][rot]: cosines, then sines
+    const float *wq, *wk;         // [d], nullable
+    float *dwq, *dwk, *partial;   // backward: [d], nullable; partial null when neither is wanted
+    int32_t *status;              // nullable
+    int64_t tokens;
+    int hq, hk, d, rot, max_position, norm, layout;
+    float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &p, bool back, cudaStream_t s);
+
+// ---------------------------------------------------------------- linear attention
+// A sequence is cut into blocks of at most `sb` tokens (its own grid, from its
+// first token). Packed batches keep a table of blocks, written on the device
+// by launch_linear_blocks; equal lengths need none.
+struct LinBlock {
+    int seq;    // sequence
+    int start;  // first token
+    int len;    // tokens (0: no such block, nothing to do)
+};
+struct LinGeom {
+    const int4 *blocks;        // packed: {seq, start, len, 0} per block, else null
+    const int32_t *seq_block;  // packed: first block of each sequence [N + 1]
+    const int32_t *status;     // packed: nonzero = bad cu_seqlens, nothing is written
+    int N, T, H;               // equal lengths: T tokens each; packed: T_total
+    int sb;                    // tokens per block, a multiple of kLinChunk
+    int per_seq;               // equal lengths: blocks per sequence
+    int nblocks;               // blocks (packed: an upper bound)
+};
+constexpr int kLinChunk = 64;
+
+__device__ __forceinline__ LinBlock lin_block(const LinGeom &g, int b) {
+    if (g.blocks) {
+        const int4 x = __ldg(g.blocks + b);
+        return {x.x, x.y, x.z};
+    }
+    const int n = b / g.per_seq, i = b - n * g.per_seq;
+    const int off = i * g.sb;
+    return {n, n * g.T + off, min(g.sb, g.T - off)};
+}
+// Blocks [first, last) of sequence n.
+__device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &first, int &last) {
+    if (g.blocks) {
+        first = __ldg(g.seq_block + n);
+        last = __ldg(g.seq_block + n + 1);
+    } else {
+        first = n * g.per_seq;
+        last = first + g.per_seq;
+    }
+}
+
+// Log decays. A sum over a block is taken in fixed point (2^-32 steps, exact
+// in 64 bits), so that the difference of two sums has no cancellation error
+// however far down the block it lies; it is handed on times log2(e) as a pair
+// of floats hi + lo. A decay of e^-128 already leaves nothing of an fp32 state
+// (2^-185 of its largest value), so every log decay is clamped there, -inf
+// (a reset) included, and sums of up to 2^20 tokens cannot overflow.
+constexpr float kMinLogDecay = -128.f;
+__device__ __forceinline__ long long decay_fixed(float g) {
+    return __float2ll_rn(fminf(fmaxf(g, kMinLogDecay), -kMinLogDecay) * 4294967296.f);
+}
+__device__ __forceinline__ float2 decay_pair(long long fixed) {
+    const double x = (double)fixed * (1.4426950408889634074 / 4294967296.0);
+    const float hi = (float)x;
+    return make_float2(hi, (float)(x - (double)hi));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// e^{a - b}
+__device__ __forceinline__ float decay_ratio(float2 a, float2 b) {
+    return exp2_approx((a.x - b.x) + (a.y - b.y));
+}
+// Prefix sums of a block's log decays: for threads 0 .. NT - 1 (all of them
+// call), a[i + 1] = sum of the first i + 1, a[0] = 0, for i < len; entries up
+// to `upto` repeat the total. `scan` is NT / 32 long longs of shared memory.
+// Ends with a barrier.
+template <int NT>
+__device__ __forceinline__ void decay_prefix(const float *log_decay, int kind, int64_t start, int H, int h, int len,
+                                             int upto, float2 *a, long long *scan) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long base = 0;
+    if (tid == 0) a[0] = make_float2(0.f, 0.f);
+    for (int i0 = 0; i0 < upto; i0 += NT) {
+        const int i = i0 + tid;
+        long long x = 0;
+        if (i < len && kind != KDA_DECAY_NONE)
+            x = decay_fixed(kind == KDA_DECAY_HEAD ? log_decay[h] : log_decay[(start + i) * H + h]);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        long long before = base, all = base;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+        }
+        if (i < upto) a[i + 1] = decay_pair(before + x);
+        base = all;
+        __syncthreads();
+    }
+}
+
+struct LinArgs {
+    kda_dtype_t dt;
+    const void *q, *k, *v;           // token strides in elements
+    int64_t q_stride, k_stride, v_stride;
+    const float *log_decay;
+    int decay;                       // kda_decay_t
+    const float *s0;                 // nullable
+    void *o;
+    float *sT;                       // nullable
+    float scale;
+    int dk, dv;
+    const int32_t *cu_seqlens;       // nullable
+    int N, T, H;
+    int32_t *status;                 // packed: the caller's, nullable
+    void *workspace;
+    // backward only
+    const void *d_o;
+    const float *dsT;                // nullable
+    void *dq, *dk_out, *dv_out;
+    float *d_decay, *ds0;            // nullable
+};
+size_t linear_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed);
+size_t linear_backward_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed);
+cudaError_t launch_linear(const LinArgs &a, cudaStream_t s);
+cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s);
+
+cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, kda_dtype_t dt, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const float *log_decay, int decay, float scale,
+                                 float *state, const int32_t *slots, int pool_size, int32_t *status, void *o, int N,
+                                 int H, int dk, int dv, cudaStream_t s);
+
+}  // namespace kda
