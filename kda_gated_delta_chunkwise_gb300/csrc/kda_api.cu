@@ -6,6 +6,7 @@
 #include <string>
 
 #include "kda_internal.cuh"
+#include "kda_linear_tc.cuh"
 
 namespace {
 
@@ -126,7 +127,11 @@ int kda_abi_version(void) { return KDA_ABI_VERSION; }
 
 kda_status_t kda_device_errors(int *errors, int reset) {
     if (!errors) return fail(KDA_ERR_INVALID_ARG, "errors must not be NULL");
-    return cuda_status(kda::read_device_error(errors, reset != 0), "reading the device error word");
+    int more = 0;
+    cudaError_t e = kda::read_device_error(errors, reset != 0);
+    if (e == cudaSuccess) e = kda::read_linear_error(&more, reset != 0);
+    *errors |= more;
+    return cuda_status(e, "reading the device error word");
 }
 
 kda_status_t kda_prefill_gate(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,

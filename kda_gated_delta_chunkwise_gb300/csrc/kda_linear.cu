@@ -28,6 +28,7 @@
 // fp32 output, and kept as one part (11 bits, against the 8 of the bf16 output)
 // where it would not. Accumulators, states and sums are fp32.
 #include "kda_linear.cuh"
+#include "kda_linear_tc.cuh"
 
 namespace kda {
 namespace {
@@ -105,7 +106,10 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 }
 // acc[m][n] (16 x 8 tiles at rows r0 + 16 m, columns c0 + 8 n) += sum_k a(r, k) b(k, c).
 // SA, SB: the operand is split in two tf32 parts (the product of the two low
-// parts, 2^-22 of the whole, is left out).
+// parts, 2^-22 of the whole, is left out). The tensor core cuts its sums off
+// where a CUDA core rounds them, which over K / 8 steps in one accumulator cost
+// 1.7e-6 to 4e-6 in the results; so with a split operand each step's products
+// are summed from zero and added to the accumulator in fp32.
 template <int K, int MT, int NT8, bool SA, bool SB, typename FA, typename FB>
 __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, int r0, int c0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -128,10 +132,16 @@ __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, in
             const uint32_t h0 = tf32(x0), h1 = tf32(x1);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (SA) mma_tf32(acc[m][n], al[m], h0, h1);
-                if (SB)
-                    mma_tf32(acc[m][n], ah[m], tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
-                mma_tf32(acc[m][n], ah[m], h0, h1);
+                if (!SA && !SB) {
+                    mma_tf32(acc[m][n], ah[m], h0, h1);
+                    continue;
+                }
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                if (SA) mma_tf32(d, al[m], h0, h1);
+                if (SB) mma_tf32(d, ah[m], tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
+                mma_tf32(d, ah[m], h0, h1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][n][e] += d[e];
             }
         }
     }
@@ -410,7 +420,8 @@ __global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
 // clamp) passes nothing on: its gradient is zero, not the sum's rounding.
 __global__ void __launch_bounds__(NT)
 lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int decay, const float *__restrict__ states,
-                      const float *__restrict__ grads, const float *__restrict__ total, int size4,
+                      const float *__restrict__ grads, const float *__restrict__ inner,
+                      const float *__restrict__ total, int size4,
                       const float *__restrict__ qdq, const float *__restrict__ kdk,
                       const float *__restrict__ kdk_state, float *__restrict__ dg, float *__restrict__ block_sum) {
     __shared__ float red[NT / 32];
@@ -434,11 +445,15 @@ lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int deca
         return;
     }
     float x = 0.f;
-    const float4 *S = reinterpret_cast<const float4 *>(states) + bh * size4;
-    const float4 *G = reinterpret_cast<const float4 *>(grads) + bh * size4;
-    for (int i = tid; i < size4; i += NT) {
-        const float4 s = __ldg(S + i), g = __ldg(G + i);
-        x += s.x * g.x + s.y * g.y + s.z * g.z + s.w * g.w;
+    if (inner) {  // <S, G> already summed up to kScanPartials pieces
+        if (tid < kScanPartials) x = __ldg(inner + bh * kScanPartials + tid);
+    } else {
+        const float4 *S = reinterpret_cast<const float4 *>(states) + bh * size4;
+        const float4 *G = reinterpret_cast<const float4 *>(grads) + bh * size4;
+        for (int i = tid; i < size4; i += NT) {
+            const float4 s = __ldg(S + i), g = __ldg(G + i);
+            x += s.x * g.x + s.y * g.y + s.z * g.z + s.w * g.w;
+        }
     }
     x *= total[bh];
     for (int i = tid; i < blk.len; i += NT) x += kdk_state[(int64_t)(blk.start + i) * geo.H + h];
@@ -508,9 +523,13 @@ struct Plan {
     int4 *blocks;
     int32_t *seq_block, *status;
     float *total, *states, *grads, *qdq, *kdk, *kdk_state, *block_sum;
+    __nv_bfloat16 *s_parts, *g_parts;  // tensor-core path: the joined states as bf16 parts
+    float *inner;                      // and <S, G> of every block, in pieces
+    int64_t part_stride;
     size_t bytes;
 };
-Plan make_plan(int N, int64_t T, int H, int dk, int dv, bool packed, bool back, void *ws) {
+bool use_tc(kda_dtype_t dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
+Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed, bool back, void *ws) {
     Plan p{};
     const int sb = block_tokens();
     const int64_t nb = max_blocks(N, T, packed, sb), tokens = packed ? T : N * T;
@@ -529,8 +548,17 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, bool packed, bool back, 
     const size_t state = (size_t)nb * H * dk * dv * 4;
     p.total = (float *)take((size_t)nb * H * 4);
     p.states = (float *)take(state);
-    if (back) {
+    p.part_stride = nb * H * dk * dv;
+    if (use_tc(dt, dk, dv)) {
+        p.s_parts = (__nv_bfloat16 *)take(state / 2 * (back ? 3 : 1));
+        if (back) {
+            p.g_parts = (__nv_bfloat16 *)take(state / 2 * 3);
+            p.inner = (float *)take((size_t)nb * H * kScanPartials * 4);
+        }
+    } else if (back) {
         p.grads = (float *)take(state);
+    }
+    if (back) {
         p.qdq = (float *)take((size_t)tokens * H * 4);
         p.kdk = (float *)take((size_t)tokens * H * 4);
         p.kdk_state = (float *)take((size_t)tokens * H * 4);
@@ -587,9 +615,85 @@ cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// bf16, d_k = d_v = 128: the same steps on the tensor cores.
+cudaError_t forward_tc(const LinArgs &a, cudaStream_t s) {
+    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, false, a.workspace);
+    const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
+    KDA_TRY(prepare_blocks(p, a, s));
+    if (tokens > 0)
+        KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
+                                p.total, s));
+    KDA_TRY(launch_scan_tc(p.geo, false, 1, p.states, p.total, a.s0, a.sT, 1.f, p.s_parts, p.part_stride, nullptr,
+                           nullptr, s));
+    if (tokens == 0) return cudaSuccess;
+    AttendTc t{};
+    t.geo = p.geo;
+    t.x = a.q; t.y = a.k; t.z = a.v;
+    t.x_stride = a.q_stride; t.y_stride = a.k_stride; t.z_stride = a.v_stride;
+    t.states = p.s_parts; t.part_stride = p.part_stride; t.tokens = tokens;
+    t.log_decay = a.log_decay; t.decay = a.decay;
+    t.out = a.o; t.c_state = a.scale; t.c_intra = a.scale;
+    return launch_attend_tc(t, s);
+}
+
+cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
+    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, a.workspace);
+    const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T, so = (int64_t)a.H * 128;
+    const bool dots = a.d_decay != nullptr, head = a.decay == KDA_DECAY_HEAD;
+    const int parts = dots ? 3 : 1;
+    KDA_TRY(prepare_blocks(p, a, s));
+    if (tokens > 0) {
+        KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
+                                p.total, s));
+        KDA_TRY(launch_scan_tc(p.geo, false, parts, p.states, p.total, a.s0, nullptr, 1.f, p.s_parts, p.part_stride,
+                               nullptr, nullptr, s));
+        // the blocks' own sums of the states are done with: those of the gradients take their place
+        KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.states,
+                                nullptr, s));
+    }
+    KDA_TRY(launch_scan_tc(p.geo, true, parts, p.states, p.total, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
+                           p.s_parts, p.inner, s));
+    if (tokens == 0)
+        return dots && head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
+    AttendTc t{};
+    t.geo = p.geo;
+    t.part_stride = p.part_stride; t.tokens = tokens;
+    t.log_decay = a.log_decay; t.decay = a.decay;
+    t.c_intra = a.scale;
+    AttendTc u = t;  // dv
+    u.rev = true;
+    u.x = a.k; u.y = a.q; u.z = a.d_o;
+    u.x_stride = a.k_stride; u.y_stride = a.q_stride; u.z_stride = so;
+    u.states = p.g_parts; u.out = a.dv_out; u.c_state = 1.f;
+    KDA_TRY(launch_attend_tc(u, s));
+    u = t;  // dq
+    u.state_t = true;
+    u.x = a.d_o; u.y = a.v; u.z = a.k; u.w = a.q;
+    u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride; u.w_stride = a.q_stride;
+    u.states = p.s_parts; u.out = a.dq; u.c_state = a.scale;
+    u.dot = dots ? p.qdq : nullptr;
+    KDA_TRY(launch_attend_tc(u, s));
+    u = t;  // dk
+    u.rev = u.state_t = true;
+    u.x = a.v; u.y = a.d_o; u.z = a.q; u.w = a.k;
+    u.x_stride = a.v_stride; u.y_stride = so; u.z_stride = a.q_stride; u.w_stride = a.k_stride;
+    u.states = p.g_parts; u.out = a.dk_out; u.c_state = 1.f;
+    u.dot = dots ? p.kdk : nullptr;
+    u.dot_state = dots ? p.kdk_state : nullptr;
+    KDA_TRY(launch_attend_tc(u, s));
+    if (!dots) return cudaSuccess;
+    lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
+        p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state,
+        head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
+    KDA_TRY(cudaGetLastError());
+    if (!head) return cudaSuccess;
+    lin_head_sum_kernel<<<a.H, NT, 0, s>>>(p.geo, p.block_sum, a.d_decay);
+    return cudaGetLastError();
+}
+
 template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cudaStream_t s) {
     constexpr bool F32 = sizeof(T) == 4;
-    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.cu_seqlens != nullptr, false, a.workspace);
+    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, false, a.workspace);
     KDA_TRY(prepare_blocks(p, a, s));
     if (p.geo.nblocks > 0)
         KDA_TRY((run_states<T, DK, DV, false>(p, a.k, a.k_stride, a.v, a.v_stride, a, p.states, s)));
@@ -606,7 +710,7 @@ template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cuda
 
 template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cudaStream_t s) {
     constexpr bool F32 = sizeof(T) == 4;
-    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.cu_seqlens != nullptr, true, a.workspace);
+    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, true, a.workspace);
     KDA_TRY(prepare_blocks(p, a, s));
     const int64_t so = (int64_t)a.H * DV;
     if (p.geo.nblocks > 0) {
@@ -644,7 +748,7 @@ template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cud
     if (!dots) return cudaSuccess;
     const bool head = a.decay == KDA_DECAY_HEAD;
     lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
-        p.geo, a.log_decay, a.decay, p.states, p.grads, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state,
+        p.geo, a.log_decay, a.decay, p.states, p.grads, nullptr, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state,
         head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
     KDA_TRY(cudaGetLastError());
     if (!head) return cudaSuccess;
@@ -655,20 +759,26 @@ template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cud
 }  // namespace
 
 size_t linear_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed) {
-    return make_plan(N, T, H, dk, dv, packed, false, nullptr).bytes;
+    return make_plan(N, T, H, dk, dv, dt, packed, false, nullptr).bytes;
 }
 size_t linear_backward_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed) {
-    return make_plan(N, T, H, dk, dv, packed, true, nullptr).bytes;
+    return make_plan(N, T, H, dk, dv, dt, packed, true, nullptr).bytes;
 }
 
 #define KDA_LINEAR_DISPATCH(FN)                                                                                 \
     const bool bf = a.dt == KDA_BF16;                                                                           \
-    if (a.dk == 128 && a.dv == 128) return bf ? FN<__nv_bfloat16, 128, 128>(a, s) : FN<float, 128, 128>(a, s);  \
+    if (a.dk == 128 && a.dv == 128) return FN<float, 128, 128>(a, s);                                           \
     if (a.dk == 64 && a.dv == 64) return bf ? FN<__nv_bfloat16, 64, 64>(a, s) : FN<float, 64, 64>(a, s);        \
     if (a.dk == 128) return bf ? FN<__nv_bfloat16, 128, 64>(a, s) : FN<float, 128, 64>(a, s);                   \
     return bf ? FN<__nv_bfloat16, 64, 128>(a, s) : FN<float, 64, 128>(a, s)
 
-cudaError_t launch_linear(const LinArgs &a, cudaStream_t s) { KDA_LINEAR_DISPATCH(forward); }
-cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s) { KDA_LINEAR_DISPATCH(backward); }
+cudaError_t launch_linear(const LinArgs &a, cudaStream_t s) {
+    if (use_tc(a.dt, a.dk, a.dv)) return forward_tc(a, s);
+    KDA_LINEAR_DISPATCH(forward);
+}
+cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s) {
+    if (use_tc(a.dt, a.dk, a.dv)) return backward_tc(a, s);
+    KDA_LINEAR_DISPATCH(backward);
+}
 
 }  // namespace kda

@@ -1,0 +1,918 @@
+// Linear attention with a decay on the tensor cores of sm_103a: bf16 inputs,
+// d_k = d_v = 128. The same three steps as the general kernels (a block's own
+// state, the scan over the blocks, the outputs), with tcgen05.mma, TMEM and TMA.
+//
+// Both kernels are persistent, one CTA per SM, with the pipeline running on
+// from one work item to the next; roles are warps that meet at mbarriers. Every
+// wait is bounded: a wait that runs out sets the device error word and the
+// CTA's abort flag, every role leaves its loop, and the CTA ends normally.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kda_linear.cuh"
+#include "kda_linear_tc.cuh"
+#include "kda_tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int D = 128;
+__device__ int g_lin_error;
+
+// ---------------------------------------------------------------- waits
+struct Abort {
+    volatile int *flag;  // shared memory
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (*flag) return false;
+            if (clock64() - t0 > kWaitCycles) {
+                *flag = 1;
+                atomicOr(&g_lin_error, 1);
+                return false;
+            }
+        }
+        return true;
+    }
+};
+// After an abort: copies that were on their way land before the CTA leaves.
+__device__ __forceinline__ void settle(const Abort &ab) {
+    if (*ab.flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 100000) {
+        }
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// x = h + m + l, each a bf16 (24 bits of x kept), two values at a time.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = pack2(x0, x1);
+    x0 -= lo_f(h), x1 -= hi_f(h);
+    m = pack2(x0, x1);
+    l = pack2(x0 - lo_f(m), x1 - hi_f(m));
+}
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {  // one 32-byte sector
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+// D[tmem] += A[tmem] * B[smem]: A holds two bf16 of K per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A warp's prefix sums of a block's log decays (fixed point): lane l holds
+// tokens l * per .. l * per + per - 1; `mine` receives its inclusive sums.
+template <int PER>
+__device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float *log_decay, int decay,
+                                                const LinBlock &blk, int h, long long (&mine)[PER]) {
+    const int lane = threadIdx.x & 31;
+    long long run = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int i = lane * PER + u;
+        if (i < blk.len && decay != KDA_DECAY_NONE)
+            run += decay_fixed(decay == KDA_DECAY_HEAD ? __ldg(log_decay + h)
+                                                       : __ldg(log_decay + (int64_t)(blk.start + i) * geo.H + h));
+        mine[u] = run;
+    }
+    long long x = run;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    const long long before = x - run;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) mine[u] += before;
+    return __shfl_sync(0xffffffffu, x, 31);
+}
+
+// ================================================================ a block's own state
+// out = sum_s w_s x_s y_s^T (see lin_state_kernel) as a GEMM with M = d_k,
+// N = d_v and the block's tokens as K, 64 at a time. x is scaled by w in fp32
+// and split in three bf16 parts, so the products keep 24 bits; the high part
+// and the two lower ones have accumulators of their own, since the tensor core
+// cuts a sum off at its accumulator's last bit: 48 lower products would cost
+// the high ones that many cuts. Bound by memory: 32 KB of k and v a tile.
+//
+// warp 0: TMA; 1: MMA; 2: weights, an item ahead; 4-7: accumulators out;
+// 8-15: x -> three parts (the high one in place).
+constexpr int ST_TOK = 64;
+constexpr int ST_TILE = ST_TOK * D * 2;       // 16 KB
+constexpr int ST_STAGE = 4 * ST_TILE;         // x (then its high part), y, middle, low
+constexpr int ST_STAGES = 3;
+constexpr int ST_THREADS = 512;
+constexpr int ST_W = ST_STAGES * ST_STAGE;                   // weights [2][kLinMaxBlock]
+constexpr int ST_BAR = ST_W + 2 * kLinMaxBlock * 4;
+enum { SB_FULL = 0, SB_CONV = 3, SB_EMPTY = 6, SB_ACC_FULL = 9, SB_ACC_EMPTY = 11, SB_W_FULL = 13, SB_W_EMPTY = 15,
+       SB_COUNT = 17 };
+constexpr int ST_SMEM = ST_BAR + SB_COUNT * 8 + 16 + 1024;
+
+struct StateTcArgs {
+    LinGeom geo;
+    const float *log_decay;
+    int decay;
+    float *out, *total;
+    int items;
+};
+
+template <bool REV>
+__global__ void __launch_bounds__(ST_THREADS, 1)
+lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + ST_BAR);
+    float *wts = reinterpret_cast<float *>(sm + ST_W);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + SB_COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const LinGeom &geo = p.geo;
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(bar + SB_FULL + i, 1);
+            mbar_init(bar + SB_CONV + i, 256);
+            mbar_init(bar + SB_EMPTY + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar + SB_ACC_FULL + i, 1);
+            mbar_init(bar + SB_ACC_EMPTY + i, 128);
+            mbar_init(bar + SB_W_FULL + i, 32);
+            mbar_init(bar + SB_W_EMPTY + i, 256);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&mx);
+            prefetch_tmap(&my);
+            int n = 0;  // tiles so far
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const LinBlock blk = lin_block(geo, it / geo.H);
+                const int h = it % geo.H;
+                for (int t0 = 0; t0 < blk.len; t0 += ST_TOK, ++n) {
+                    const int s = n % ST_STAGES, ph = (n / ST_STAGES) & 1;
+                    if (!(ok = ab.wait(bar + SB_EMPTY + s, ph ^ 1))) break;
+                    unsigned char *st = sm + s * ST_STAGE;
+                    mbar_arrive_expect_tx(bar + SB_FULL + s, 2 * ST_TILE);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tma_load_3d(st + c * (ST_TILE / 2), &mx, bar + SB_FULL + s, 64 * c, h, blk.start + t0);
+                        tma_load_3d(st + ST_TILE + c * (ST_TILE / 2), &my, bar + SB_FULL + s, 64 * c, h, blk.start + t0);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t I = idesc_bf16(128, 128, true, true);
+            int n = 0, q = 0;
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const LinBlock blk = lin_block(geo, it / geo.H);
+                if (blk.len <= 0) continue;
+                const int buf = q & 1;
+                if (!(ok = ab.wait(bar + SB_ACC_EMPTY + buf, ((q >> 1) & 1) ^ 1))) break;
+                const uint32_t hi = tmem + buf * 256, lo = hi + 128;
+                for (int t0 = 0; t0 < blk.len; t0 += ST_TOK, ++n) {
+                    const int s = n % ST_STAGES;
+                    if (!(ok = ab.wait(bar + SB_CONV + s, (n / ST_STAGES) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(sm + s * ST_STAGE), y = st + ST_TILE;
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {  // high, middle, low
+                        const uint32_t x = part == 0 ? st : st + (1 + part) * ST_TILE;
+#pragma unroll
+                        for (int ks = 0; ks < ST_TOK / 16; ++ks)
+                            umma_bf16(part == 0 ? hi : lo, sdesc_sw128(x + ks * 2048, ST_TILE / 2, 1024),
+                                      sdesc_sw128(y + ks * 2048, ST_TILE / 2, 1024), I,
+                                      t0 > 0 || ks > 0 || part == 2);
+                    }
+                    umma_commit(bar + SB_EMPTY + s);
+                }
+                if (!ok) break;
+                umma_commit(bar + SB_ACC_FULL + buf);
+                ++q;
+            }
+        }
+    } else if (warp == 2) {
+        int q = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const int b = it / geo.H, h = it % geo.H;
+            const LinBlock blk = lin_block(geo, b);
+            if (blk.len <= 0) continue;
+            constexpr int PER = kLinMaxBlock / 32;
+            long long a[PER];
+            const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, blk, h, a);
+            if (!REV && lane == 0 && p.total)
+                p.total[(int64_t)b * geo.H + h] = decay_ratio(decay_pair(all), make_float2(0.f, 0.f));
+            ok = ab.wait(bar + SB_W_EMPTY + (q & 1), ((q >> 1) & 1) ^ 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            float *w = wts + (q & 1) * kLinMaxBlock;
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                w[lane * PER + u] = decay_ratio(decay_pair(REV ? a[u] : all - a[u]), make_float2(0.f, 0.f));
+            mbar_arrive(bar + SB_W_FULL + (q & 1));
+            ++q;
+        }
+    } else if (warp >= 4 && warp < 8) {
+        int q = 0;
+        const int row = tid - 128;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const LinBlock blk = lin_block(geo, it / geo.H);
+            if (blk.len <= 0) continue;
+            const int buf = q & 1;
+            ok = ab.wait(bar + SB_ACC_FULL + buf, (q >> 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            float *dst = p.out + ((int64_t)it * D + row) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t x[32], y[32];
+                tmem_ld32(tmem + lanes + buf * 256 + c, x);
+                tmem_ld32(tmem + lanes + buf * 256 + 128 + c, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        r[e] = __float_as_uint(__uint_as_float(x[8 * u + e]) + __uint_as_float(y[8 * u + e]));
+                    st_v8(dst + c + 8 * u, r);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar + SB_ACC_EMPTY + buf);
+            ++q;
+        }
+    } else if (warp >= 8) {
+        const int t = tid - 256;
+        int n = 0, q = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const LinBlock blk = lin_block(geo, it / geo.H);
+            if (blk.len <= 0) continue;
+            ok = ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1);
+            const float *w = wts + (q & 1) * kLinMaxBlock;
+            for (int t0 = 0; t0 < blk.len && ok; t0 += ST_TOK, ++n) {
+                const int s = n % ST_STAGES, rows = blk.len - t0;
+                if (!(ok = ab.wait(bar + SB_FULL + s, (n / ST_STAGES) & 1))) break;
+                unsigned char *st = sm + s * ST_STAGE;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = t + 256 * i, row = c >> 4, c8 = c & 15;
+                    const uint32_t off = kmajor_chunk(row, c8, ST_TOK);
+                    uint4 *x = reinterpret_cast<uint4 *>(st + off);
+                    const uint4 v = *x;
+                    const float f = w[t0 + row];
+                    uint4 h = make_uint4(0u, 0u, 0u, 0u), m = h, l = h;
+                    if (row < rows) {
+                        split3(lo_f(v.x) * f, hi_f(v.x) * f, h.x, m.x, l.x);
+                        split3(lo_f(v.y) * f, hi_f(v.y) * f, h.y, m.y, l.y);
+                        split3(lo_f(v.z) * f, hi_f(v.z) * f, h.z, m.z, l.z);
+                        split3(lo_f(v.w) * f, hi_f(v.w) * f, h.w, m.w, l.w);
+                    } else {  // past the block's end: neither operand may hold what lies there
+                        *reinterpret_cast<uint4 *>(st + ST_TILE + off) = h;
+                    }
+                    *x = h;
+                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off) = m;
+                    *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off) = l;
+                }
+                fence_proxy_async();
+                mbar_arrive(bar + SB_CONV + s);
+            }
+            if (ok) mbar_arrive(bar + SB_W_EMPTY + (q & 1));
+            ++q;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ================================================================ joining the blocks
+// As lin_scan_kernel, with the states handed on as bf16 parts: the first one
+// is what the output kernels multiply with; PARTS = 3 keeps all 24 bits.
+constexpr int SC_THREADS = 256;
+template <bool REV, int PARTS>
+__global__ void __launch_bounds__(SC_THREADS)
+lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__restrict__ total,
+                   const float *__restrict__ s0, float *__restrict__ sT, float c, __nv_bfloat16 *__restrict__ parts,
+                   int64_t part_stride, const __nv_bfloat16 *__restrict__ other, float *__restrict__ inner) {
+    if (geo.status && *geo.status != KDA_DEV_OK) return;
+    constexpr int SIZE4 = D * D / 4, PER = SIZE4 / SC_THREADS;
+    const int64_t nh = blockIdx.x / PER;
+    const int n = (int)(nh / geo.H), h = (int)(nh % geo.H);
+    const int64_t e = (int64_t)(blockIdx.x % PER) * SC_THREADS + threadIdx.x;
+    int first, last;
+    lin_seq_blocks(geo, n, first, last);
+    float4 S = s0 ? reinterpret_cast<const float4 *>(s0)[nh * SIZE4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 *p = reinterpret_cast<const float4 *>(own);
+    const int count = last - first;
+    constexpr bool INNER = REV && PARTS == 3;  // <S, G> of every block: G is here, S in `other`
+    constexpr int AHEAD = INNER ? 4 : 8;
+    float4 x[AHEAD];
+    float f[AHEAD];
+    uint2 so[AHEAD][3];
+    auto at = [&](int i) { return (int64_t)(REV ? last - 1 - i : first + i) * geo.H + h; };
+    for (int i0 = 0; i0 < count; i0 += AHEAD) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (i0 + u < count) {
+                x[u] = __ldcs(p + at(i0 + u) * SIZE4 + e);
+                f[u] = __ldg(total + at(i0 + u));
+                if (INNER) {
+                    const uint2 *o = reinterpret_cast<const uint2 *>(other) + at(i0 + u) * SIZE4 + e;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) so[u][k] = __ldg(o + k * (part_stride / 4));
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (i0 + u < count) {
+                if (INNER) {
+                    float v = S.x * (lo_f(so[u][0].x) + lo_f(so[u][1].x) + lo_f(so[u][2].x)) +
+                              S.y * (hi_f(so[u][0].x) + hi_f(so[u][1].x) + hi_f(so[u][2].x)) +
+                              S.z * (lo_f(so[u][0].y) + lo_f(so[u][1].y) + lo_f(so[u][2].y)) +
+                              S.w * (hi_f(so[u][0].y) + hi_f(so[u][1].y) + hi_f(so[u][2].y));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                    if ((threadIdx.x & 31) == 0)
+                        inner[at(i0 + u) * kScanPartials + (blockIdx.x % PER) * (SC_THREADS / 32) + (threadIdx.x >> 5)] = v;
+                }
+                uint2 a, b, d;
+                split3(S.x, S.y, a.x, b.x, d.x);
+                split3(S.z, S.w, a.y, b.y, d.y);
+                uint2 *o = reinterpret_cast<uint2 *>(parts) + at(i0 + u) * SIZE4 + e;
+                *o = a;
+                if (PARTS == 3) {
+                    o[part_stride / 4] = b;
+                    o[part_stride / 2] = d;
+                }
+                if (f[u] == 0.f) S = make_float4(0.f, 0.f, 0.f, 0.f);  // a reset, whatever the state held
+                S.x = f[u] * S.x + c * x[u].x;
+                S.y = f[u] * S.y + c * x[u].y;
+                S.z = f[u] * S.z + c * x[u].z;
+                S.w = f[u] * S.w + c * x[u].w;
+            }
+    }
+    if (sT) reinterpret_cast<float4 *>(sT)[nh * SIZE4 + e] = S;
+}
+
+// ================================================================ outputs
+// One item is 128 output rows of a block and head; its operands pass through a
+// ring of six 32 KB slots in the order S, x, (y, z) of every 128-token tile of
+// the block that the rows see. Two contexts (an MMA-issuing warp, 128 row
+// threads, one O and one P accumulator in TMEM each) take turns with the items,
+// so that one context's products run while the other's rows are being scaled.
+//   O = x S, rows scaled by the decay from the block's edge (in TMEM);
+//   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place;
+//   O += P z, P read from TMEM.
+// P and S are the two roundings to bf16 (2^-9 relative each, as small as the
+// rounding of the result itself); sums are fp32. Bound by memory.
+//
+// DOTS adds w_i . out_i per row, for the gradient of the decay, to fp32
+// accuracy: its state part from all three parts of S, and the rest not from
+// the rounded P but as sum_j c D_ij (x_i . y_j) (w_i . z_j), both dots exact in
+// bf16 with fp32 sums. That takes the order S (3 parts), x, w, (y, z) and a
+// second score accumulator, so the scores go 64 columns at a time.
+//
+// x and w stay until the item's last scores. A block has at most two tiles,
+// so an item's last load is at most five after its x, and the ring of six
+// always has a slot for it. A slot has a full barrier for each context, so that
+// a context that waits for its own loads alone sees every phase of its barriers
+// (of one shared barrier it would miss those of the other's loads, and a
+// parity wait cannot tell a phase from the one two before it).
+static_assert(kLinMaxBlock <= 256, "the slot ring holds an item of two tiles");
+constexpr int AT_SLOT = 128 * D * 2;  // 32 KB
+constexpr int AT_SLOTS = 6;
+constexpr int AT_THREADS = 384;
+constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [2][kLinMaxBlock + 2]
+constexpr int AT_SCAN = AT_A + 2 * (kLinMaxBlock + 2) * 8;           // scan [2][4]
+constexpr int AT_BAR = AT_SCAN + 2 * 4 * 8;
+enum { AB_FULL = 0, AB_EMPTY = 12, AB_O_IN = 18, AB_O_FULL = 20, AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26,
+       AB_SCAN = 28, AB_PREFIX = 30, AB_COUNT = 32 };
+constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
+
+// Phases of a context's full barriers: `done` has a bit per slot, the parity of
+// the loads of the context's earlier items; an item whose first load is n0 uses
+// a slot a second time from its seventh load on.
+struct Loads {
+    uint64_t *full;
+    uint32_t done;
+    int n0;
+    __device__ __forceinline__ uint64_t *bar(int i) const { return full + i % AT_SLOTS; }
+    __device__ __forceinline__ uint32_t parity(int i) const {
+        return ((done >> (i % AT_SLOTS)) & 1u) ^ (i - n0 >= AT_SLOTS ? 1u : 0u);
+    }
+    __device__ __forceinline__ void next(int count) {  // the item is done
+        for (int i = n0; i < n0 + count; ++i) done ^= 1u << (i % AT_SLOTS);
+        n0 += count;
+    }
+    __device__ __forceinline__ void skip(int count) { n0 += count; }
+};
+
+struct AttendTcArgs {
+    LinGeom geo;
+    const float *log_decay;
+    int decay;
+    __nv_bfloat16 *out;
+    float c_state, c_intra;
+    float *dot, *dot_state;
+    int state_rows;    // rows of one part of S
+    int items, tiles;  // tiles: 128-row tiles per block
+};
+struct Item {
+    LinBlock blk;
+    int b, h, i0, first, count;  // first row; first tile of y, z and how many
+};
+template <bool REV> __device__ __forceinline__ Item item_of(const AttendTcArgs &p, int it) {
+    Item x;
+    x.h = it % p.geo.H;
+    const int r = it / p.geo.H;
+    x.b = r / p.tiles;
+    const int tile = r - x.b * p.tiles;
+    x.blk = lin_block(p.geo, x.b);
+    x.i0 = tile * 128;
+    if (x.i0 >= x.blk.len) {
+        x.first = x.count = 0;
+    } else if (REV) {
+        x.first = tile;
+        x.count = (x.blk.len + 127) / 128 - tile;
+    } else {
+        x.first = 0;
+        x.count = tile + 1;
+    }
+    return x;
+}
+
+template <bool REV, bool ST, bool DOTS>
+__global__ void __launch_bounds__(AT_THREADS, 1)
+lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                     const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap ms,
+                     const __grid_constant__ CUtensorMap mw) {
+    constexpr int SUB = DOTS ? 64 : 128;      // score columns at a time
+    constexpr int NS = DOTS ? 3 : 1;          // parts of S
+    constexpr int HEAD = DOTS ? NS + 2 : 2;   // loads before the first y
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + AT_BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + AB_COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const LinGeom &geo = p.geo;
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < AT_SLOTS; ++i) {
+            mbar_init(bar + AB_FULL + i, 1);
+            mbar_init(bar + AB_FULL + AT_SLOTS + i, 1);
+            mbar_init(bar + AB_EMPTY + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar + AB_O_IN + i, 1);
+            mbar_init(bar + AB_O_FULL + i, 1);
+            mbar_init(bar + AB_O_EMPTY + i, 128);
+            mbar_init(bar + AB_P_FULL + i, 1);
+            mbar_init(bar + AB_P_READY + i, 128);
+            mbar_init(bar + AB_SCAN + i, 128);
+            mbar_init(bar + AB_PREFIX + i, 128);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int n = 0, c = 0;
+            uint64_t *f = nullptr;  // the barrier of the slot's load
+            auto slot = [&]() -> unsigned char * {
+                const int s = n % AT_SLOTS;
+                if (!(ok = ab.wait(bar + AB_EMPTY + s, ((n / AT_SLOTS) & 1) ^ 1))) return nullptr;
+                f = bar + AB_FULL + c * AT_SLOTS + s;
+                mbar_arrive_expect_tx(f, AT_SLOT);
+                return sm + s * AT_SLOT;
+            };
+            auto rows = [&](const CUtensorMap *m, int h, int tok) {  // 128 tokens in 64-token, 64-channel boxes
+                unsigned char *d = slot();
+                if (!d) return;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) tma_load_3d(d + x * 16384 + t * 8192, m, f, 64 * x, h, tok + 64 * t);
+                ++n;
+            };
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const Item x = item_of<REV>(p, it);
+                if (x.count == 0) continue;
+                for (int part = 0; part < NS && ok; ++part)
+                    if (unsigned char *d = slot()) {
+                        const int row = part * p.state_rows + (x.b * geo.H + x.h) * D;
+                        tma_load_2d(d, &ms, f, 0, row);
+                        tma_load_2d(d + 16384, &ms, f, 64, row);
+                        ++n;
+                    }
+                if (ok) rows(&mx, x.h, x.blk.start + x.i0);
+                if (DOTS && ok) rows(&mw, x.h, x.blk.start + x.i0);
+                for (int j = 0; j < x.count && ok; ++j) {
+                    rows(&my, x.h, x.blk.start + (x.first + j) * 128);
+                    if (ok) rows(&mz, x.h, x.blk.start + (x.first + j) * 128);
+                }
+                c ^= 1;
+            }
+        }
+    } else if (warp == 1 || warp == 2) {
+        const int c = warp - 1;
+        if (lane == 0) {
+            constexpr uint32_t I_S = idesc_bf16(128, 128, false, !ST), I_P = idesc_bf16(128, SUB, false, false),
+                               I_O = idesc_bf16(128, 128, false, true);
+            const uint32_t to = tmem + c * 256, tp = to + 128, tp2 = tp + SUB;
+            Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
+            int k = 0, q = 0, np = 0;  // items so far, items and score tiles of this context
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const Item x = item_of<REV>(p, it);
+                if (x.count == 0) continue;
+                const int loads = HEAD + 2 * x.count;
+                if ((k++ & 1) != c) {
+                    ld.skip(loads);
+                    continue;
+                }
+                const int n = ld.n0;
+                auto full = [&](int i) { return ab.wait(ld.bar(i), ld.parity(i)); };
+                auto base = [&](int i) { return smem_u32(sm + (i % AT_SLOTS) * AT_SLOT); };
+                auto free_slot = [&](int i) { umma_commit(bar + AB_EMPTY + i % AT_SLOTS); };
+                if (!(ok = ab.wait(bar + AB_O_EMPTY + c, (q & 1) ^ 1) && full(n + NS))) break;
+                const uint32_t xs = base(n + NS);
+                for (int part = NS - 1; part >= 0 && ok; --part) {  // the lowest part first, while the sum is small
+                    if (!(ok = full(n + part))) break;
+                    tc_fence_after();
+                    const uint32_t ss = base(n + part);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16(to, sdesc_sw128(xs + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                  ST ? sdesc_sw128(ss + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024)
+                                     : sdesc_sw128(ss + ks * 2048, 16384, 1024),
+                                  I_S, part < NS - 1 || ks > 0);
+                    free_slot(n + part);
+                }
+                if (!ok) break;
+                umma_commit(bar + AB_O_IN + c);
+                if (DOTS && !(ok = full(n + NS + 1))) break;
+                const uint32_t ws = base(n + NS + 1);
+                for (int j = 0; j < x.count && ok; ++j) {
+                    const int ny = n + HEAD + 2 * j;
+                    if (!(ok = full(ny) && (!DOTS || full(ny + 1)))) break;
+                    const uint32_t ys = base(ny), zs = base(ny + 1);
+                    for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            umma_bf16(tp, sdesc_sw128(xs + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                      sdesc_sw128(ys + sub * 8192 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), I_P,
+                                      ks > 0);
+                        if (DOTS) {
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                umma_bf16(tp2, sdesc_sw128(ws + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                          sdesc_sw128(zs + sub * 8192 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                          I_P, ks > 0);
+                        }
+                        if (sub == 128 / SUB - 1) {
+                            free_slot(ny);
+                            if (j == x.count - 1) free_slot(n + NS);
+                        }
+                        umma_commit(bar + AB_P_FULL + c);
+                        if (!(ok = full(ny + 1) && ab.wait(bar + AB_P_READY + c, np & 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < SUB / 16; ++ks)
+                            umma_bf16_ts(to, tp + ks * 8, sdesc_sw128(zs + (sub * 4 + ks) * 2048, 16384, 1024), I_O, 1);
+                    }
+                    if (ok) free_slot(ny + 1);
+                }
+                if (!ok) break;
+                if (DOTS) free_slot(n + NS + 1);  // the row threads read it before their last P_READY
+                umma_commit(bar + AB_O_FULL + c);
+                ld.next(loads);
+                ++q;
+            }
+        }
+    } else if (warp >= 4) {
+        const int c = (warp - 4) >> 2, r = (tid - 128) & 127, w = warp & 3;
+        float2 *a = reinterpret_cast<float2 *>(sm + AT_A) + c * (kLinMaxBlock + 2);
+        long long *scan = reinterpret_cast<long long *>(sm + AT_SCAN) + c * 4;
+        const uint32_t to = tmem + c * 256 + ((uint32_t)w << 21), tp = to + 128, tp2 = tp + SUB;
+        auto wait = [&](uint64_t *b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(b, ph)); };
+        Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
+        int k = 0, q = 0, np = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x = item_of<REV>(p, it);
+            if (x.count == 0) continue;
+            const int loads = HEAD + 2 * x.count;
+            if ((k++ & 1) != c) {
+                ld.skip(loads);
+                continue;
+            }
+            const int n = ld.n0;
+            // prefix sums of the block's log decays: thread r holds tokens PER r ..
+            {
+                constexpr int PER = kLinMaxBlock / 128;
+                long long s[PER], run = 0;
+#pragma unroll
+                for (int u = 0; u < PER; ++u) {
+                    const int i = r * PER + u;
+                    if (i < x.blk.len && p.decay != KDA_DECAY_NONE)
+                        run += decay_fixed(p.decay == KDA_DECAY_HEAD
+                                               ? __ldg(p.log_decay + x.h)
+                                               : __ldg(p.log_decay + (int64_t)(x.blk.start + i) * geo.H + x.h));
+                    s[u] = run;
+                }
+                long long y = run;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long z = __shfl_up_sync(0xffffffffu, y, off);
+                    if (lane >= off) y += z;
+                }
+                // scan[] was last read before this context's previous PREFIX phase completed
+                if (lane == 31) scan[w] = y;
+                mbar_arrive(bar + AB_SCAN + c);
+                if (!wait(bar + AB_SCAN + c, q & 1)) break;
+                long long before = y - run;
+                for (int v = 0; v < w; ++v) before += scan[v];
+                if (r == 0) a[0] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < PER; ++u) a[r * PER + u + 1] = decay_pair(before + s[u]);
+                mbar_arrive(bar + AB_PREFIX + c);
+                if (!wait(bar + AB_PREFIX + c, q & 1)) break;
+            }
+            const int i = x.i0 + r, len = x.blk.len;
+            const float2 ai = a[min(i, len - 1) + 1];
+            const float f = p.c_state * (REV ? decay_ratio(a[len], ai) : decay_ratio(ai, make_float2(0.f, 0.f)));
+            float dot = 0.f, dot_state = 0.f;
+            if (DOTS && !wait(ld.bar(n + NS + 1), ld.parity(n + NS + 1))) break;
+            if (!wait(bar + AB_O_IN + c, q & 1)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(to + c0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[e]));  // a reset drops the state
+                tmem_st32(to + c0, v);
+                if (DOTS) {
+                    const unsigned char *wt = sm + ((n + NS + 1) % AT_SLOTS) * AT_SLOT;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint4 g = *reinterpret_cast<const uint4 *>(wt + kmajor_chunk(r, c0 / 8 + u, 128));
+                        const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dot_state += lo_f(gw[e]) * __uint_as_float(v[8 * u + 2 * e]) +
+                                         hi_f(gw[e]) * __uint_as_float(v[8 * u + 2 * e + 1]);
+                    }
+                }
+            }
+            for (int j = 0; j < x.count && ok; ++j) {
+                const int j0 = (x.first + j) * 128, nz = n + HEAD + 1 + 2 * j;
+                for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
+                    if (!wait(bar + AB_P_FULL + c, np & 1)) break;
+                    tc_fence_after();
+                    if (sub == 0 && len - j0 < 128) {  // what lies past the block's end must not meet P's zeros
+                        if (!wait(ld.bar(nz), ld.parity(nz))) break;
+                        if (r >= len - j0) {
+                            unsigned char *z = sm + (nz % AT_SLOTS) * AT_SLOT + r * 128;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<uint4 *>(z + 16384 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        fence_proxy_async();
+                    }
+#pragma unroll 1
+                    for (int c0 = 0; c0 < SUB; c0 += 32) {
+                        uint32_t v[32], v2[32], o[16];
+                        tmem_ld32(tp + c0, v);
+                        if (DOTS) tmem_ld32(tp2 + c0, v2);
+                        tmem_wait_ld();
+                        const int jc = j0 + sub * SUB + c0;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float y[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int jj = jc + e + u;
+                                const float2 aj = a[jj + 1];  // entries past the end repeat the total
+                                const float d = REV ? decay_ratio(aj, ai) : decay_ratio(ai, aj);
+                                const bool in = jj < len && (REV ? jj >= i : jj <= i);
+                                y[u] = in ? p.c_intra * d * __uint_as_float(v[e + u]) : 0.f;
+                                if (DOTS && in) dot += y[u] * __uint_as_float(v2[e + u]);
+                            }
+                            o[e / 2] = pack2(y[0], y[1]);
+                        }
+                        tmem_st16(tp + c0 / 2, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar + AB_P_READY + c);
+                }
+            }
+            if (!ok) break;
+            if (DOTS && i < len) {
+                const int64_t at = (int64_t)(x.blk.start + i) * geo.H + x.h;
+                p.dot[at] = dot + dot_state;
+                if (p.dot_state) p.dot_state[at] = dot_state;
+            }
+            if (!wait(bar + AB_O_FULL + c, q & 1)) break;
+            tc_fence_after();
+            __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + i) * geo.H + x.h) * D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(to + c0, v);
+                tmem_wait_ld();
+                if (i < len) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = pack2(__uint_as_float(v[16 * u + 2 * e]), __uint_as_float(v[16 * u + 2 * e + 1]));
+                        st_v8(dst + c0 + 16 * u, o);
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar + AB_O_EMPTY + c);
+            ld.next(loads);
+            ++q;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+// [tokens][H][128] bf16 with a token stride, boxes of 64 channels x 1 head x 64 tokens.
+bool token_map(CUtensorMap *m, const void *ptr, int64_t stride, int H, int64_t tokens) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {D, (cuuint64_t)H, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [rows][128] bf16 states, boxes of 64 columns x 128 rows.
+bool state_map(CUtensorMap *m, const void *ptr, int64_t rows) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {D, (cuuint64_t)rows}, strides[1] = {D * 2};
+    cuuint32_t box[2] = {64, 128}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+int sm_count() {
+    static int n = [] {
+        int dev = 0, v = 152;
+        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        return v;
+    }();
+    return n;
+}
+
+#define KDA_TRY(x)                        \
+    do {                                  \
+        const cudaError_t e_ = (x);       \
+        if (e_ != cudaSuccess) return e_; \
+    } while (0)
+
+}  // namespace
+
+cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
+                            int64_t tokens, const float *log_decay, int decay, float *out, float *total,
+                            cudaStream_t s) {
+    CUtensorMap mx, my;
+    if (!token_map(&mx, x, xs, geo.H, tokens) || !token_map(&my, y, ys, geo.H, tokens)) return cudaErrorInvalidValue;
+    StateTcArgs p{geo, log_decay, decay, out, total, geo.nblocks * geo.H};
+    auto k = rev ? lin_state_tc_kernel<true> : lin_state_tc_kernel<false>;
+    KDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ST_SMEM));
+    k<<<min(p.items, sm_count()), ST_THREADS, ST_SMEM, s>>>(p, mx, my);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scan_tc(const LinGeom &geo, bool rev, int parts, const float *own, const float *total,
+                           const float *s0, float *sT, float c, void *out, int64_t part_stride, const void *other,
+                           float *inner, cudaStream_t s) {
+    auto k = rev ? (parts == 3 ? lin_scan_tc_kernel<true, 3> : lin_scan_tc_kernel<true, 1>)
+                 : (parts == 3 ? lin_scan_tc_kernel<false, 3> : lin_scan_tc_kernel<false, 1>);
+    k<<<(unsigned)((int64_t)geo.N * geo.H * (D * D / 4 / SC_THREADS)), SC_THREADS, 0, s>>>(
+        geo, own, total, s0, sT, c, (__nv_bfloat16 *)out, part_stride, (const __nv_bfloat16 *)other, inner);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
+    const LinGeom &geo = a.geo;
+    const bool dots = a.dot != nullptr;
+    const int64_t rows = (int64_t)geo.nblocks * geo.H * D;
+    if (geo.sb > kLinMaxBlock || rows * 3 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    CUtensorMap mx, my, mz, ms, mw;
+    if (!token_map(&mx, a.x, a.x_stride, geo.H, a.tokens) || !token_map(&my, a.y, a.y_stride, geo.H, a.tokens) ||
+        !token_map(&mz, a.z, a.z_stride, geo.H, a.tokens) || !state_map(&ms, a.states, dots ? 3 * rows : rows))
+        return cudaErrorInvalidValue;
+    mw = mx;
+    if (dots && !token_map(&mw, a.w, a.w_stride, geo.H, a.tokens)) return cudaErrorInvalidValue;
+    AttendTcArgs p{geo, a.log_decay, a.decay, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.dot, a.dot_state,
+                   (int)rows, 0, geo.sb / 128};
+    p.items = geo.nblocks * geo.H * p.tiles;
+    auto k = !a.rev ? (!a.state_t ? lin_attend_tc_kernel<false, false, false>
+                       : dots     ? lin_attend_tc_kernel<false, true, true>
+                                  : lin_attend_tc_kernel<false, true, false>)
+                    : (!a.state_t ? lin_attend_tc_kernel<true, false, false>
+                       : dots     ? lin_attend_tc_kernel<true, true, true>
+                                  : lin_attend_tc_kernel<true, true, false>);
+    KDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM));
+    k<<<min(p.items, sm_count()), AT_THREADS, AT_SMEM, s>>>(p, mx, my, mz, ms, mw);
+    return cudaGetLastError();
+}
+
+cudaError_t read_linear_error(int *out, bool reset) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_lin_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    *out = v;
+    if (reset && v) {
+        const int z = 0;
+        e = cudaMemcpyToSymbol(g_lin_error, &z, sizeof(int));
+    }
+    return e;
+}
+
+}  // namespace kda
