@@ -68,27 +68,31 @@ __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &fir
     }
 }
 
-// Log decays. A sum over a block is taken in fixed point (2^-32 steps, exact
-// in 64 bits), so that the difference of two sums has no cancellation error
-// however far down the block it lies; it is handed on times log2(e) as a pair
-// of floats hi + lo. A decay of e^-128 already leaves nothing of an fp32 state
-// (2^-185 of its largest value), so every log decay is clamped there, -inf
-// (a reset) included, and sums of up to 2^20 tokens cannot overflow.
+// Log decays. A sum over a block is taken in fixed point (base 2, steps of
+// 2^-31, exact in 64 bits), so that the difference of two sums has no
+// cancellation error however far down the block it lies; it is handed on as a
+// pair of floats, its whole part and its fraction in [0, 1). (All conversions
+// are 32-bit ones: in fp64 this pair took 8 us of a warp's time for 256 tokens.)
+// A decay of e^-128 already leaves nothing of an fp32 state (2^-185 of its
+// largest value), so every log decay is clamped there, -inf (a reset) included,
+// and sums of up to 2^23 tokens keep an exact whole part.
 constexpr float kMinLogDecay = -128.f;
 __device__ __forceinline__ long long decay_fixed(float g) {
-    return __float2ll_rn(fminf(fmaxf(g, kMinLogDecay), -kMinLogDecay) * 4294967296.f);
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
+    const float x = fminf(fmaxf(g, kMinLogDecay), -kMinLogDecay);
+    const float hi = x * kLog2e, lo = fmaf(x, kLog2e, -hi) + x * kLog2eLow, whole = truncf(hi);
+    return (long long)(int)whole * (1ll << 31) + __float2int_rn((hi - whole) * 2147483648.f) +
+           __float2int_rn(lo * 2147483648.f);
 }
 __device__ __forceinline__ float2 decay_pair(long long fixed) {
-    const double x = (double)fixed * (1.4426950408889634074 / 4294967296.0);
-    const float hi = (float)x;
-    return make_float2(hi, (float)(x - (double)hi));
+    return make_float2((float)(int)(fixed >> 31), (float)(int)(fixed & 0x7fffffff) * (1.f / 2147483648.f));
 }
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// e^{a - b}
+// e^{a - b} of two sums
 __device__ __forceinline__ float decay_ratio(float2 a, float2 b) {
     return exp2_approx((a.x - b.x) + (a.y - b.y));
 }

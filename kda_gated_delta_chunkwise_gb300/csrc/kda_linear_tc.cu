@@ -38,6 +38,11 @@ struct Abort {
         return true;
     }
 };
+// One arrival for the warp, after all its lanes have come here.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 // After an abort: copies that were on their way land before the CTA leaves.
 __device__ __forceinline__ void settle(const Abort &ab) {
     if (*ab.flag) {
@@ -75,13 +80,30 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 // D[tmem] += A[tmem] * B[smem]: A holds two bf16 of K per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc)
+        : "memory");
+}
+// MMA descriptors of a tile, advanced by constants: the address field counts
+// 16-byte steps. One thread issues every MMA, so its instructions between two
+// of them are time the tensor core waits.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }     // K-major
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, uint32_t atom) { return sdesc_sw128(tile, atom, 1024); }
+// offset of step ks (16 of K): K-major tiles have 64 of K per atom of `atom` bytes
+__device__ __forceinline__ constexpr uint64_t step_k(int ks, uint32_t atom) {
+    return ((ks >> 2) * atom + (ks & 3) * 32) >> 4;
+}
+__device__ __forceinline__ constexpr uint64_t step_mn(int ks) { return (uint64_t)(ks * 2048) >> 4; }
+template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
 // A warp's prefix sums of a block's log decays (fixed point): lane l holds
@@ -90,15 +112,18 @@ template <int PER>
 __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float *log_decay, int decay,
                                                 const LinBlock &blk, int h, long long (&mine)[PER]) {
     const int lane = threadIdx.x & 31;
-    long long run = 0;
+    float g[PER];  // all loads first: one after the other they cost a memory latency each
+    const float head = decay == KDA_DECAY_HEAD ? __ldg(log_decay + h) : 0.f;
+    const bool token = decay == KDA_DECAY_TOKEN;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
         const int i = lane * PER + u;
-        if (i < blk.len && decay != KDA_DECAY_NONE)
-            run += decay_fixed(decay == KDA_DECAY_HEAD ? __ldg(log_decay + h)
-                                                       : __ldg(log_decay + (int64_t)(blk.start + i) * geo.H + h));
-        mine[u] = run;
+        g[u] = i < blk.len ? head : 0.f;
+        if (token && i < blk.len) g[u] = __ldg(log_decay + (int64_t)(blk.start + i) * geo.H + h);
     }
+    long long run = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) mine[u] = run += decay_fixed(g[u]);
     long long x = run;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -155,14 +180,14 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         *ab.flag = 0;
         for (int i = 0; i < 3; ++i) {
             mbar_init(bar + SB_FULL + i, 1);
-            mbar_init(bar + SB_CONV + i, 256);
+            mbar_init(bar + SB_CONV + i, 8);
             mbar_init(bar + SB_EMPTY + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + SB_ACC_FULL + i, 1);
-            mbar_init(bar + SB_ACC_EMPTY + i, 128);
-            mbar_init(bar + SB_W_FULL + i, 32);
-            mbar_init(bar + SB_W_EMPTY + i, 256);
+            mbar_init(bar + SB_ACC_EMPTY + i, 4);
+            mbar_init(bar + SB_W_FULL + i, 1);
+            mbar_init(bar + SB_W_EMPTY + i, 8);
         }
         fence_mbar_init();
     }
@@ -211,15 +236,21 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     const int s = n % ST_STAGES;
                     if (!(ok = ab.wait(bar + SB_CONV + s, (n / ST_STAGES) & 1))) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(sm + s * ST_STAGE), y = st + ST_TILE;
+                    const uint64_t x = desc_mn(smem_u32(sm + s * ST_STAGE), ST_TILE / 2);
+                    constexpr uint64_t Y = ST_TILE >> 4, M = 2 * Y, L = 3 * Y;  // y, middle, low part of x
+                    if (t0 == 0) {
+                        mma_ss<false>(hi, x, x + Y, I);
+                        mma_ss<false>(lo, x + M, x + Y, I);
+                    } else {
+                        mma_ss<true>(hi, x, x + Y, I);
+                        mma_ss<true>(lo, x + M, x + Y, I);
+                    }
+                    mma_ss<true>(lo, x + L, x + Y, I);
 #pragma unroll
-                    for (int part = 0; part < 3; ++part) {  // high, middle, low
-                        const uint32_t x = part == 0 ? st : st + (1 + part) * ST_TILE;
-#pragma unroll
-                        for (int ks = 0; ks < ST_TOK / 16; ++ks)
-                            umma_bf16(part == 0 ? hi : lo, sdesc_sw128(x + ks * 2048, ST_TILE / 2, 1024),
-                                      sdesc_sw128(y + ks * 2048, ST_TILE / 2, 1024), I,
-                                      t0 > 0 || ks > 0 || part == 2);
+                    for (int ks = 1; ks < ST_TOK / 16; ++ks) {
+                        mma_ss<true>(hi, x + step_mn(ks), x + Y + step_mn(ks), I);
+                        mma_ss<true>(lo, x + M + step_mn(ks), x + Y + step_mn(ks), I);
+                        mma_ss<true>(lo, x + L + step_mn(ks), x + Y + step_mn(ks), I);
                     }
                     umma_commit(bar + SB_EMPTY + s);
                 }
@@ -245,7 +276,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
 #pragma unroll
             for (int u = 0; u < PER; ++u)
                 w[lane * PER + u] = decay_ratio(decay_pair(REV ? a[u] : all - a[u]), make_float2(0.f, 0.f));
-            mbar_arrive(bar + SB_W_FULL + (q & 1));
+            warp_arrive(bar + SB_W_FULL + (q & 1));
             ++q;
         }
     } else if (warp >= 4 && warp < 8) {
@@ -276,45 +307,52 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar + SB_ACC_EMPTY + buf);
+            warp_arrive(bar + SB_ACC_EMPTY + buf);
             ++q;
         }
     } else if (warp >= 8) {
         const int t = tid - 256;
+        const uint32_t off = kmajor_chunk(t >> 4, t & 15, ST_TOK);
         int n = 0, q = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const LinBlock blk = lin_block(geo, it / geo.H);
             if (blk.len <= 0) continue;
-            ok = ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1));
             const float *w = wts + (q & 1) * kLinMaxBlock;
             for (int t0 = 0; t0 < blk.len && ok; t0 += ST_TOK, ++n) {
                 const int s = n % ST_STAGES, rows = blk.len - t0;
-                if (!(ok = ab.wait(bar + SB_FULL + s, (n / ST_STAGES) & 1))) break;
+                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + SB_FULL + s, (n / ST_STAGES) & 1)))) break;
                 unsigned char *st = sm + s * ST_STAGE;
+                uint4 v[4];
+                float f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // rows 16 i + t / 16, channels 8 (t % 16) ..
+                    v[i] = *reinterpret_cast<const uint4 *>(st + off + i * 2048);
+                    f[i] = w[t0 + 16 * i + (t >> 4)];
+                }
+                if (rows < ST_TOK) {  // past the block's end: neither operand may hold what lies there
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (16 * i + (t >> 4) >= rows) {
+                            v[i] = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = v[i];
+                        }
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int c = t + 256 * i, row = c >> 4, c8 = c & 15;
-                    const uint32_t off = kmajor_chunk(row, c8, ST_TOK);
-                    uint4 *x = reinterpret_cast<uint4 *>(st + off);
-                    const uint4 v = *x;
-                    const float f = w[t0 + row];
-                    uint4 h = make_uint4(0u, 0u, 0u, 0u), m = h, l = h;
-                    if (row < rows) {
-                        split3(lo_f(v.x) * f, hi_f(v.x) * f, h.x, m.x, l.x);
-                        split3(lo_f(v.y) * f, hi_f(v.y) * f, h.y, m.y, l.y);
-                        split3(lo_f(v.z) * f, hi_f(v.z) * f, h.z, m.z, l.z);
-                        split3(lo_f(v.w) * f, hi_f(v.w) * f, h.w, m.w, l.w);
-                    } else {  // past the block's end: neither operand may hold what lies there
-                        *reinterpret_cast<uint4 *>(st + ST_TILE + off) = h;
-                    }
-                    *x = h;
-                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off) = m;
-                    *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off) = l;
+                    uint4 h, m, l;
+                    split3(lo_f(v[i].x) * f[i], hi_f(v[i].x) * f[i], h.x, m.x, l.x);
+                    split3(lo_f(v[i].y) * f[i], hi_f(v[i].y) * f[i], h.y, m.y, l.y);
+                    split3(lo_f(v[i].z) * f[i], hi_f(v[i].z) * f[i], h.z, m.z, l.z);
+                    split3(lo_f(v[i].w) * f[i], hi_f(v[i].w) * f[i], h.w, m.w, l.w);
+                    *reinterpret_cast<uint4 *>(st + off + i * 2048) = h;
+                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = m;
+                    *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off + i * 2048) = l;
                 }
                 fence_proxy_async();
-                mbar_arrive(bar + SB_CONV + s);
+                warp_arrive(bar + SB_CONV + s);
             }
-            if (ok) mbar_arrive(bar + SB_W_EMPTY + (q & 1));
+            if (ok) warp_arrive(bar + SB_W_EMPTY + (q & 1));
             ++q;
         }
     }
@@ -425,11 +463,12 @@ static_assert(kLinMaxBlock <= 256, "the slot ring holds an item of two tiles");
 constexpr int AT_SLOT = 128 * D * 2;  // 32 KB
 constexpr int AT_SLOTS = 6;
 constexpr int AT_THREADS = 384;
-constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [2][kLinMaxBlock + 2]
-constexpr int AT_SCAN = AT_A + 2 * (kLinMaxBlock + 2) * 8;           // scan [2][4]
-constexpr int AT_BAR = AT_SCAN + 2 * 4 * 8;
+constexpr int AT_PREFIX = 4;                                         // items whose prefix sums are kept
+constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [AT_PREFIX][kLinMaxBlock + 2]
+constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // column factors [8 warps][kLinMaxBlock]
+constexpr int AT_BAR = AT_COL + 8 * kLinMaxBlock * 4;
 enum { AB_FULL = 0, AB_EMPTY = 12, AB_O_IN = 18, AB_O_FULL = 20, AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26,
-       AB_SCAN = 28, AB_PREFIX = 30, AB_COUNT = 32 };
+       AB_A_FULL = 28, AB_A_EMPTY = 32, AB_COUNT = 36 };
 constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
 
 // Phases of a context's full barriers: `done` has a bit per slot, the parity of
@@ -509,11 +548,13 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + AB_O_IN + i, 1);
             mbar_init(bar + AB_O_FULL + i, 1);
-            mbar_init(bar + AB_O_EMPTY + i, 128);
+            mbar_init(bar + AB_O_EMPTY + i, 4);
             mbar_init(bar + AB_P_FULL + i, 1);
-            mbar_init(bar + AB_P_READY + i, 128);
-            mbar_init(bar + AB_SCAN + i, 128);
-            mbar_init(bar + AB_PREFIX + i, 128);
+            mbar_init(bar + AB_P_READY + i, 4);
+        }
+        for (int i = 0; i < AT_PREFIX; ++i) {
+            mbar_init(bar + AB_A_FULL + i, 1);
+            mbar_init(bar + AB_A_EMPTY + i, 4);
         }
         fence_mbar_init();
     }
@@ -587,40 +628,39 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 auto base = [&](int i) { return smem_u32(sm + (i % AT_SLOTS) * AT_SLOT); };
                 auto free_slot = [&](int i) { umma_commit(bar + AB_EMPTY + i % AT_SLOTS); };
                 if (!(ok = ab.wait(bar + AB_O_EMPTY + c, (q & 1) ^ 1) && full(n + NS))) break;
-                const uint32_t xs = base(n + NS);
+                const uint64_t xd = desc_k(base(n + NS));
                 for (int part = NS - 1; part >= 0 && ok; --part) {  // the lowest part first, while the sum is small
                     if (!(ok = full(n + part))) break;
                     tc_fence_after();
-                    const uint32_t ss = base(n + part);
+                    const uint64_t sd = ST ? desc_k(base(n + part)) : desc_mn(base(n + part), 16384);
+                    if (part == NS - 1) mma_ss<false>(to, xd, sd, I_S);
+                    else mma_ss<true>(to, xd, sd, I_S);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16(to, sdesc_sw128(xs + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                  ST ? sdesc_sw128(ss + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024)
-                                     : sdesc_sw128(ss + ks * 2048, 16384, 1024),
-                                  I_S, part < NS - 1 || ks > 0);
+                    for (int ks = 1; ks < 8; ++ks)
+                        mma_ss<true>(to, xd + step_k(ks, 16384), sd + (ST ? step_k(ks, 16384) : step_mn(ks)), I_S);
                     free_slot(n + part);
                 }
                 if (!ok) break;
                 umma_commit(bar + AB_O_IN + c);
                 if (DOTS && !(ok = full(n + NS + 1))) break;
-                const uint32_t ws = base(n + NS + 1);
+                const uint64_t wd = desc_k(base(n + NS + 1));
                 for (int j = 0; j < x.count && ok; ++j) {
                     const int ny = n + HEAD + 2 * j;
                     if (!(ok = full(ny) && (!DOTS || full(ny + 1)))) break;
-                    const uint32_t ys = base(ny), zs = base(ny + 1);
+                    const uint64_t yd = desc_k(base(ny)), zk = desc_k(base(ny + 1)), zd = desc_mn(base(ny + 1), 16384);
+#pragma unroll
                     for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
                         tc_fence_after();
+                        constexpr uint64_t ROWS64 = 8192 >> 4;
+                        mma_ss<false>(tp, xd, yd + sub * ROWS64, I_P);
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            umma_bf16(tp, sdesc_sw128(xs + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                      sdesc_sw128(ys + sub * 8192 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), I_P,
-                                      ks > 0);
+                        for (int ks = 1; ks < 8; ++ks)
+                            mma_ss<true>(tp, xd + step_k(ks, 16384), yd + sub * ROWS64 + step_k(ks, 16384), I_P);
                         if (DOTS) {
+                            mma_ss<false>(tp2, wd, zk + sub * ROWS64, I_P);
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                umma_bf16(tp2, sdesc_sw128(ws + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                          sdesc_sw128(zs + sub * 8192 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                          I_P, ks > 0);
+                            for (int ks = 1; ks < 8; ++ks)
+                                mma_ss<true>(tp2, wd + step_k(ks, 16384), zk + sub * ROWS64 + step_k(ks, 16384), I_P);
                         }
                         if (sub == 128 / SUB - 1) {
                             free_slot(ny);
@@ -631,7 +671,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < SUB / 16; ++ks)
-                            umma_bf16_ts(to, tp + ks * 8, sdesc_sw128(zs + (sub * 4 + ks) * 2048, 16384, 1024), I_O, 1);
+                            umma_bf16_ts(to, tp + ks * 8, zd + step_mn(sub * 4 + ks), I_O);
                     }
                     if (ok) free_slot(ny + 1);
                 }
@@ -642,10 +682,28 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 ++q;
             }
         }
+    } else if (warp == 3) {
+        // prefix sums of the items' log decays, up to four items ahead
+        int k = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x = item_of<REV>(p, it);
+            if (x.count == 0) continue;
+            constexpr int PER = kLinMaxBlock / 32;
+            long long s[PER];
+            warp_decay<PER>(geo, p.log_decay, p.decay, x.blk, x.h, s);
+            const int slot = k % AT_PREFIX;
+            ok = __all_sync(0xffffffffu, ab.wait(bar + AB_A_EMPTY + slot, ((k / AT_PREFIX) & 1) ^ 1));
+            if (!ok) break;
+            float2 *a = reinterpret_cast<float2 *>(sm + AT_A) + slot * (kLinMaxBlock + 2);
+            if (lane == 0) a[0] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < PER; ++u) a[lane * PER + u + 1] = decay_pair(s[u]);
+            warp_arrive(bar + AB_A_FULL + slot);
+            ++k;
+        }
     } else if (warp >= 4) {
         const int c = (warp - 4) >> 2, r = (tid - 128) & 127, w = warp & 3;
-        float2 *a = reinterpret_cast<float2 *>(sm + AT_A) + c * (kLinMaxBlock + 2);
-        long long *scan = reinterpret_cast<long long *>(sm + AT_SCAN) + c * 4;
+        float *col = reinterpret_cast<float *>(sm + AT_COL) + (warp - 4) * kLinMaxBlock;
         const uint32_t to = tmem + c * 256 + ((uint32_t)w << 21), tp = to + 128, tp2 = tp + SUB;
         auto wait = [&](uint64_t *b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(b, ph)); };
         Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
@@ -654,45 +712,27 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             const Item x = item_of<REV>(p, it);
             if (x.count == 0) continue;
             const int loads = HEAD + 2 * x.count;
+            const int slot = k % AT_PREFIX, slot_ph = (k / AT_PREFIX) & 1;
             if ((k++ & 1) != c) {
                 ld.skip(loads);
                 continue;
             }
             const int n = ld.n0;
-            // prefix sums of the block's log decays: thread r holds tokens PER r ..
-            {
-                constexpr int PER = kLinMaxBlock / 128;
-                long long s[PER], run = 0;
-#pragma unroll
-                for (int u = 0; u < PER; ++u) {
-                    const int i = r * PER + u;
-                    if (i < x.blk.len && p.decay != KDA_DECAY_NONE)
-                        run += decay_fixed(p.decay == KDA_DECAY_HEAD
-                                               ? __ldg(p.log_decay + x.h)
-                                               : __ldg(p.log_decay + (int64_t)(x.blk.start + i) * geo.H + x.h));
-                    s[u] = run;
-                }
-                long long y = run;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long z = __shfl_up_sync(0xffffffffu, y, off);
-                    if (lane >= off) y += z;
-                }
-                // scan[] was last read before this context's previous PREFIX phase completed
-                if (lane == 31) scan[w] = y;
-                mbar_arrive(bar + AB_SCAN + c);
-                if (!wait(bar + AB_SCAN + c, q & 1)) break;
-                long long before = y - run;
-                for (int v = 0; v < w; ++v) before += scan[v];
-                if (r == 0) a[0] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int u = 0; u < PER; ++u) a[r * PER + u + 1] = decay_pair(before + s[u]);
-                mbar_arrive(bar + AB_PREFIX + c);
-                if (!wait(bar + AB_PREFIX + c, q & 1)) break;
-            }
+            if (!wait(bar + AB_A_FULL + slot, slot_ph)) break;
+            const float2 *a = reinterpret_cast<const float2 *>(sm + AT_A) + slot * (kLinMaxBlock + 2);
             const int i = x.i0 + r, len = x.blk.len;
             const float2 ai = a[min(i, len - 1) + 1];
             const float f = p.c_state * (REV ? decay_ratio(a[len], ai) : decay_ratio(ai, make_float2(0.f, 0.f)));
+            // D_ij = row factor x column factor for the columns on the far side of the warp's 32 rows, the
+            // decays to and from their edge (both <= 1); only the 32 x 32 piece on the diagonal takes an
+            // exponential per element
+            const int i32 = x.i0 + 32 * w;
+            const float2 edge = a[REV ? i32 + 32 : i32];
+            const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
+            for (int j = x.first * 128 + lane; j < (x.first + x.count) * 128; j += 32)
+                col[j] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
+                             : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
+            __syncwarp();
             float dot = 0.f, dot_state = 0.f;
             if (DOTS && !wait(ld.bar(n + NS + 1), ld.parity(n + NS + 1))) break;
             if (!wait(bar + AB_O_IN + c, q & 1)) break;
@@ -739,32 +779,55 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 #pragma unroll 1
                     for (int c0 = 0; c0 < SUB; c0 += 32) {
                         uint32_t v[32], v2[32], o[16];
+                        const int jc = j0 + sub * SUB + c0;
+                        if (REV ? jc < i32 || jc >= len : jc > i32) {  // outside the mask
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = 0u;
+                            tmem_st16(tp + c0 / 2, o);
+                            continue;
+                        }
                         tmem_ld32(tp + c0, v);
                         if (DOTS) tmem_ld32(tp2 + c0, v2);
                         tmem_wait_ld();
-                        const int jc = j0 + sub * SUB + c0;
+                        if (jc != i32 && (!REV || jc + 32 <= len)) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float y[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int jj = jc + e + u;
-                                const float2 aj = a[jj + 1];  // entries past the end repeat the total
-                                const float d = REV ? decay_ratio(aj, ai) : decay_ratio(ai, aj);
-                                const bool in = jj < len && (REV ? jj >= i : jj <= i);
-                                y[u] = in ? p.c_intra * d * __uint_as_float(v[e + u]) : 0.f;
-                                if (DOTS && in) dot += y[u] * __uint_as_float(v2[e + u]);
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 cf = *reinterpret_cast<const float4 *>(col + jc + e);
+                                const float y0 = rf * cf.x * __uint_as_float(v[e]);
+                                const float y1 = rf * cf.y * __uint_as_float(v[e + 1]);
+                                const float y2 = rf * cf.z * __uint_as_float(v[e + 2]);
+                                const float y3 = rf * cf.w * __uint_as_float(v[e + 3]);
+                                if (DOTS)
+                                    dot += y0 * __uint_as_float(v2[e]) + y1 * __uint_as_float(v2[e + 1]) +
+                                           y2 * __uint_as_float(v2[e + 2]) + y3 * __uint_as_float(v2[e + 3]);
+                                o[e / 2] = pack2(y0, y1);
+                                o[e / 2 + 1] = pack2(y2, y3);
                             }
-                            o[e / 2] = pack2(y[0], y[1]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float y[2];
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int jj = jc + e + u;
+                                    const float2 aj = a[jj + 1];  // entries past the end repeat the total
+                                    const float d = REV ? decay_ratio(aj, ai) : decay_ratio(ai, aj);
+                                    const bool in = jj < len && (REV ? jj >= i : jj <= i);
+                                    y[u] = in ? p.c_intra * d * __uint_as_float(v[e + u]) : 0.f;
+                                    if (DOTS && in) dot += y[u] * __uint_as_float(v2[e + u]);
+                                }
+                                o[e / 2] = pack2(y[0], y[1]);
+                            }
                         }
                         tmem_st16(tp + c0 / 2, o);
                     }
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(bar + AB_P_READY + c);
+                    warp_arrive(bar + AB_P_READY + c);
                 }
             }
             if (!ok) break;
+            warp_arrive(bar + AB_A_EMPTY + slot);
             if (DOTS && i < len) {
                 const int64_t at = (int64_t)(x.blk.start + i) * geo.H + x.h;
                 p.dot[at] = dot + dot_state;
@@ -790,7 +853,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar + AB_O_EMPTY + c);
+            warp_arrive(bar + AB_O_EMPTY + c);
             ld.next(loads);
             ++q;
         }
