@@ -423,7 +423,8 @@ lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int deca
                       const float *__restrict__ grads, const float *__restrict__ inner,
                       const float *__restrict__ total, int size4,
                       const float *__restrict__ qdq, const float *__restrict__ kdk,
-                      const float *__restrict__ kdk_state, float *__restrict__ dg, float *__restrict__ block_sum) {
+                      const float *__restrict__ kdk_state, int64_t dot_stride, float *__restrict__ dg,
+                      float *__restrict__ block_sum) {
     __shared__ float red[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / geo.H, h = blockIdx.x % geo.H;
@@ -456,12 +457,19 @@ lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int deca
         }
     }
     x *= total[bh];
-    for (int i = tid; i < blk.len; i += NT) x += kdk_state[(int64_t)(blk.start + i) * geo.H + h];
+    for (int i = tid; i < blk.len; i += NT) {
+        const int64_t at = (int64_t)(blk.start + i) * geo.H + h;
+        x += kdk_state[at] + (dot_stride ? kdk_state[at + dot_stride] : 0.f);
+    }
     float run = block_add(x), sum = 0.f;
     for (int i1 = (blk.len + NT - 1) / NT * NT; i1 > 0; i1 -= NT) {  // from the end, thread tid at i1 - 1 - tid
         const int i = i1 - 1 - tid;
         const int64_t at = (int64_t)(blk.start + i) * geo.H + h;
-        float v = i < blk.len ? qdq[at] - kdk[at] : 0.f;
+        float v = 0.f;
+        if (i < blk.len) {
+            v = qdq[at] - kdk[at];
+            if (dot_stride) v += qdq[at + dot_stride] - kdk[at + dot_stride];
+        }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float y = __shfl_up_sync(0xffffffffu, v, off);
@@ -525,7 +533,7 @@ struct Plan {
     float *total, *states, *grads, *qdq, *kdk, *kdk_state, *block_sum;
     __nv_bfloat16 *s_parts, *g_parts;  // tensor-core path: the joined states as bf16 parts
     float *inner;                      // and <S, G> of every block, in pieces
-    int64_t part_stride;
+    int64_t part_stride, dot_stride;
     size_t bytes;
 };
 bool use_tc(kda_dtype_t dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
@@ -559,9 +567,11 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
         p.grads = (float *)take(state);
     }
     if (back) {
-        p.qdq = (float *)take((size_t)tokens * H * 4);
-        p.kdk = (float *)take((size_t)tokens * H * 4);
-        p.kdk_state = (float *)take((size_t)tokens * H * 4);
+        const size_t halves = use_tc(dt, dk, dv) ? 2 : 1;  // row dots come in so many pieces
+        p.dot_stride = halves == 2 ? tokens * H : 0;
+        p.qdq = (float *)take(halves * tokens * H * 4);
+        p.kdk = (float *)take(halves * tokens * H * 4);
+        p.kdk_state = (float *)take(halves * tokens * H * 4);
         p.block_sum = (float *)take((size_t)nb * H * 4);
     }
     p.bytes = at;
@@ -683,7 +693,7 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
     KDA_TRY(launch_attend_tc(u, s));
     if (!dots) return cudaSuccess;
     lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
-        p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state,
+        p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
         head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
     KDA_TRY(cudaGetLastError());
     if (!head) return cudaSuccess;
@@ -748,7 +758,7 @@ template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cud
     if (!dots) return cudaSuccess;
     const bool head = a.decay == KDA_DECAY_HEAD;
     lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
-        p.geo, a.log_decay, a.decay, p.states, p.grads, nullptr, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state,
+        p.geo, a.log_decay, a.decay, p.states, p.grads, nullptr, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
         head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
     KDA_TRY(cudaGetLastError());
     if (!head) return cudaSuccess;

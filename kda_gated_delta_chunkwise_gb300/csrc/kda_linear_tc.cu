@@ -137,24 +137,29 @@ __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float 
 }
 
 // ================================================================ a block's own state
-// out = sum_s w_s x_s y_s^T (see lin_state_kernel) as a GEMM with M = d_k,
-// N = d_v and the block's tokens as K, 64 at a time. x is scaled by w in fp32
-// and split in three bf16 parts, so the products keep 24 bits; the high part
-// and the two lower ones have accumulators of their own, since the tensor core
-// cuts a sum off at its accumulator's last bit: 48 lower products would cost
-// the high ones that many cuts. Bound by memory: 32 KB of k and v a tile.
+// out = sum_s w_s x_s y_s^T (see lin_state_kernel) as a GEMM with M = d_v,
+// N = d_k and the block's tokens as K, 64 at a time (the transposed state, so
+// that a warp's 32 accumulator rows are 32 neighbours in memory). x is scaled by
+// w in fp32 and split in three bf16 parts, so the products keep 24 bits; the
+// high part and the two lower ones have accumulators of their own, since the
+// tensor core cuts a sum off at its accumulator's last bit: the lower products
+// would cost the high ones that many cuts. High and middle part lie side by
+// side, so one MMA with N = 256 takes both and reads y once.
+// Bound by memory: 32 KB of x and y a tile; next come the 176 KB that a tile
+// moves through shared memory.
 //
 // warp 0: TMA; 1: MMA; 2: weights, an item ahead; 4-7: accumulators out;
-// 8-15: x -> three parts (the high one in place).
+// 8-15 and 16-23: x -> three parts (the high one in place), tiles in turn. Each
+// of the two groups has full barriers of its own (see the output kernel).
 constexpr int ST_TOK = 64;
 constexpr int ST_TILE = ST_TOK * D * 2;       // 16 KB
-constexpr int ST_STAGE = 4 * ST_TILE;         // x (then its high part), y, middle, low
+constexpr int ST_STAGE = 4 * ST_TILE;         // x (then its high part), middle, low, y
 constexpr int ST_STAGES = 3;
-constexpr int ST_THREADS = 512;
+constexpr int ST_THREADS = 768;
 constexpr int ST_W = ST_STAGES * ST_STAGE;                   // weights [2][kLinMaxBlock]
 constexpr int ST_BAR = ST_W + 2 * kLinMaxBlock * 4;
-enum { SB_FULL = 0, SB_CONV = 3, SB_EMPTY = 6, SB_ACC_FULL = 9, SB_ACC_EMPTY = 11, SB_W_FULL = 13, SB_W_EMPTY = 15,
-       SB_COUNT = 17 };
+enum { SB_FULL = 0, SB_CONV = 6, SB_EMPTY = 9, SB_ACC_FULL = 12, SB_ACC_EMPTY = 14, SB_W_FULL = 16, SB_W_EMPTY = 18,
+       SB_COUNT = 20 };
 constexpr int ST_SMEM = ST_BAR + SB_COUNT * 8 + 16 + 1024;
 
 struct StateTcArgs {
@@ -180,6 +185,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         *ab.flag = 0;
         for (int i = 0; i < 3; ++i) {
             mbar_init(bar + SB_FULL + i, 1);
+            mbar_init(bar + SB_FULL + 3 + i, 1);
             mbar_init(bar + SB_CONV + i, 8);
             mbar_init(bar + SB_EMPTY + i, 1);
         }
@@ -187,7 +193,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             mbar_init(bar + SB_ACC_FULL + i, 1);
             mbar_init(bar + SB_ACC_EMPTY + i, 4);
             mbar_init(bar + SB_W_FULL + i, 1);
-            mbar_init(bar + SB_W_EMPTY + i, 8);
+            mbar_init(bar + SB_W_EMPTY + i, 16);
         }
         fence_mbar_init();
     }
@@ -213,18 +219,19 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     const int s = n % ST_STAGES, ph = (n / ST_STAGES) & 1;
                     if (!(ok = ab.wait(bar + SB_EMPTY + s, ph ^ 1))) break;
                     unsigned char *st = sm + s * ST_STAGE;
-                    mbar_arrive_expect_tx(bar + SB_FULL + s, 2 * ST_TILE);
+                    uint64_t *f = bar + SB_FULL + n % 6;
+                    mbar_arrive_expect_tx(f, 2 * ST_TILE);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        tma_load_3d(st + c * (ST_TILE / 2), &mx, bar + SB_FULL + s, 64 * c, h, blk.start + t0);
-                        tma_load_3d(st + ST_TILE + c * (ST_TILE / 2), &my, bar + SB_FULL + s, 64 * c, h, blk.start + t0);
+                        tma_load_3d(st + c * (ST_TILE / 2), &mx, f, 64 * c, h, blk.start + t0);
+                        tma_load_3d(st + 3 * ST_TILE + c * (ST_TILE / 2), &my, f, 64 * c, h, blk.start + t0);
                     }
                 }
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t I = idesc_bf16(128, 128, true, true);
+            constexpr uint32_t I2 = idesc_bf16(128, 256, true, true), I1 = idesc_bf16(128, 128, true, true);
             int n = 0, q = 0;
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const LinBlock blk = lin_block(geo, it / geo.H);
@@ -237,20 +244,14 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     if (!(ok = ab.wait(bar + SB_CONV + s, (n / ST_STAGES) & 1))) break;
                     tc_fence_after();
                     const uint64_t x = desc_mn(smem_u32(sm + s * ST_STAGE), ST_TILE / 2);
-                    constexpr uint64_t Y = ST_TILE >> 4, M = 2 * Y, L = 3 * Y;  // y, middle, low part of x
-                    if (t0 == 0) {
-                        mma_ss<false>(hi, x, x + Y, I);
-                        mma_ss<false>(lo, x + M, x + Y, I);
-                    } else {
-                        mma_ss<true>(hi, x, x + Y, I);
-                        mma_ss<true>(lo, x + M, x + Y, I);
-                    }
-                    mma_ss<true>(lo, x + L, x + Y, I);
+                    constexpr uint64_t L = (2 * ST_TILE) >> 4, Y = (3 * ST_TILE) >> 4;
+                    if (t0 == 0) mma_ss<false>(hi, x + Y, x, I2);
+                    else mma_ss<true>(hi, x + Y, x, I2);
+                    mma_ss<true>(lo, x + Y, x + L, I1);
 #pragma unroll
                     for (int ks = 1; ks < ST_TOK / 16; ++ks) {
-                        mma_ss<true>(hi, x + step_mn(ks), x + Y + step_mn(ks), I);
-                        mma_ss<true>(lo, x + M + step_mn(ks), x + Y + step_mn(ks), I);
-                        mma_ss<true>(lo, x + L + step_mn(ks), x + Y + step_mn(ks), I);
+                        mma_ss<true>(hi, x + Y + step_mn(ks), x + step_mn(ks), I2);
+                        mma_ss<true>(lo, x + Y + step_mn(ks), x + L + step_mn(ks), I1);
                     }
                     umma_commit(bar + SB_EMPTY + s);
                 }
@@ -290,7 +291,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             ok = ab.wait(bar + SB_ACC_FULL + buf, (q >> 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            float *dst = p.out + ((int64_t)it * D + row) * D;
+            float *dst = p.out + (int64_t)it * D * D + row;  // row: the value column
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t x[32], y[32];
@@ -298,20 +299,15 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                 tmem_ld32(tmem + lanes + buf * 256 + 128 + c, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t r[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        r[e] = __float_as_uint(__uint_as_float(x[8 * u + e]) + __uint_as_float(y[8 * u + e]));
-                    st_v8(dst + c + 8 * u, r);
-                }
+                for (int e = 0; e < 32; ++e)
+                    dst[(c + e) * D] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
             }
             tc_fence_before();
             warp_arrive(bar + SB_ACC_EMPTY + buf);
             ++q;
         }
     } else if (warp >= 8) {
-        const int t = tid - 256;
+        const int t = (tid - 256) & 255, group = (tid - 256) >> 8;
         const uint32_t off = kmajor_chunk(t >> 4, t & 15, ST_TOK);
         int n = 0, q = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
@@ -321,7 +317,8 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             const float *w = wts + (q & 1) * kLinMaxBlock;
             for (int t0 = 0; t0 < blk.len && ok; t0 += ST_TOK, ++n) {
                 const int s = n % ST_STAGES, rows = blk.len - t0;
-                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + SB_FULL + s, (n / ST_STAGES) & 1)))) break;
+                if ((n & 1) != group) continue;
+                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + SB_FULL + n % 6, (n / 6) & 1)))) break;
                 unsigned char *st = sm + s * ST_STAGE;
                 uint4 v[4];
                 float f[4];
@@ -335,7 +332,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     for (int i = 0; i < 4; ++i)
                         if (16 * i + (t >> 4) >= rows) {
                             v[i] = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = v[i];
+                            *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off + i * 2048) = v[i];
                         }
                 }
 #pragma unroll
@@ -346,8 +343,8 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     split3(lo_f(v[i].z) * f[i], hi_f(v[i].z) * f[i], h.z, m.z, l.z);
                     split3(lo_f(v[i].w) * f[i], hi_f(v[i].w) * f[i], h.w, m.w, l.w);
                     *reinterpret_cast<uint4 *>(st + off + i * 2048) = h;
-                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = m;
-                    *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off + i * 2048) = l;
+                    *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = m;
+                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = l;
                 }
                 fence_proxy_async();
                 warp_arrive(bar + SB_CONV + s);
@@ -438,11 +435,13 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 // ================================================================ outputs
 // One item is 128 output rows of a block and head; its operands pass through a
 // ring of six 32 KB slots in the order S, x, (y, z) of every 128-token tile of
-// the block that the rows see. Two contexts (an MMA-issuing warp, 128 row
+// the block that the rows see. Two contexts (an MMA-issuing warp, 256 row
 // threads, one O and one P accumulator in TMEM each) take turns with the items,
 // so that one context's products run while the other's rows are being scaled.
+// Two threads share a row, a half of the columns each.
 //   O = x S, rows scaled by the decay from the block's edge (in TMEM);
-//   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place;
+//   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place (each half
+//   of the columns into the front of its own half);
 //   O += P z, P read from TMEM.
 // P and S are the two roundings to bf16 (2^-9 relative each, as small as the
 // rounding of the result itself); sums are fp32. Bound by memory.
@@ -462,11 +461,11 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 static_assert(kLinMaxBlock <= 256, "the slot ring holds an item of two tiles");
 constexpr int AT_SLOT = 128 * D * 2;  // 32 KB
 constexpr int AT_SLOTS = 6;
-constexpr int AT_THREADS = 384;
+constexpr int AT_THREADS = 640;
 constexpr int AT_PREFIX = 4;                                         // items whose prefix sums are kept
 constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [AT_PREFIX][kLinMaxBlock + 2]
-constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // column factors [8 warps][kLinMaxBlock]
-constexpr int AT_BAR = AT_COL + 8 * kLinMaxBlock * 4;
+constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // column factors [16 warps][kLinMaxBlock / 2]
+constexpr int AT_BAR = AT_COL + 16 * kLinMaxBlock / 2 * 4;
 enum { AB_FULL = 0, AB_EMPTY = 12, AB_O_IN = 18, AB_O_FULL = 20, AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26,
        AB_A_FULL = 28, AB_A_EMPTY = 32, AB_COUNT = 36 };
 constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
@@ -496,8 +495,9 @@ struct AttendTcArgs {
     __nv_bfloat16 *out;
     float c_state, c_intra;
     float *dot, *dot_state;
-    int state_rows;    // rows of one part of S
-    int items, tiles;  // tiles: 128-row tiles per block
+    int64_t dot_stride;  // between the two column halves' sums
+    int state_rows;      // rows of one part of S
+    int items, tiles;    // tiles: 128-row tiles per block
 };
 struct Item {
     LinBlock blk;
@@ -548,13 +548,13 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + AB_O_IN + i, 1);
             mbar_init(bar + AB_O_FULL + i, 1);
-            mbar_init(bar + AB_O_EMPTY + i, 4);
+            mbar_init(bar + AB_O_EMPTY + i, 8);
             mbar_init(bar + AB_P_FULL + i, 1);
-            mbar_init(bar + AB_P_READY + i, 4);
+            mbar_init(bar + AB_P_READY + i, 8);
         }
         for (int i = 0; i < AT_PREFIX; ++i) {
             mbar_init(bar + AB_A_FULL + i, 1);
-            mbar_init(bar + AB_A_EMPTY + i, 4);
+            mbar_init(bar + AB_A_EMPTY + i, 8);
         }
         fence_mbar_init();
     }
@@ -671,7 +671,8 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < SUB / 16; ++ks)
-                            umma_bf16_ts(to, tp + ks * 8, zd + step_mn(sub * 4 + ks), I_O);
+                            umma_bf16_ts(to, tp + (ks * 16 / (SUB / 2)) * (SUB / 2) + (ks * 16 % (SUB / 2)) / 2,
+                                         zd + step_mn(sub * 4 + ks), I_O);
                     }
                     if (ok) free_slot(ny + 1);
                 }
@@ -702,8 +703,9 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             ++k;
         }
     } else if (warp >= 4) {
-        const int c = (warp - 4) >> 2, r = (tid - 128) & 127, w = warp & 3;
-        float *col = reinterpret_cast<float *>(sm + AT_COL) + (warp - 4) * kLinMaxBlock;
+        const int c = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, r = (tid - 128) & 127, w = warp & 3;
+        constexpr int HSUB = SUB / 2;  // this thread's score columns of a piece: from hf * HSUB
+        float *col = reinterpret_cast<float *>(sm + AT_COL) + (warp - 4) * (kLinMaxBlock / 2);
         const uint32_t to = tmem + c * 256 + ((uint32_t)w << 21), tp = to + 128, tp2 = tp + SUB;
         auto wait = [&](uint64_t *b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(b, ph)); };
         Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
@@ -729,33 +731,40 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             const int i32 = x.i0 + 32 * w;
             const float2 edge = a[REV ? i32 + 32 : i32];
             const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
-            for (int j = x.first * 128 + lane; j < (x.first + x.count) * 128; j += 32)
-                col[j] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
-                             : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
+#pragma unroll
+            for (int u = 0; u < kLinMaxBlock / 64; ++u) {  // the u-th 32 of this thread's columns
+                const int j = (x.first * 128 + (32 * u / HSUB) * SUB + hf * HSUB + 32 * u % HSUB + lane) % kLinMaxBlock;
+                col[32 * u + lane] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
+                                         : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
+            }
             __syncwarp();
             float dot = 0.f, dot_state = 0.f;
             if (DOTS && !wait(ld.bar(n + NS + 1), ld.parity(n + NS + 1))) break;
             if (!wait(bar + AB_O_IN + c, q & 1)) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(to + c0, v);
+            {
+                uint32_t v[2][32];
+                tmem_ld32(to + 64 * hf, v[0]);
+                tmem_ld32(to + 64 * hf + 32, v[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[e]));  // a reset drops the state
-                tmem_st32(to + c0, v);
-                if (DOTS) {
-                    const unsigned char *wt = sm + ((n + NS + 1) % AT_SLOTS) * AT_SLOT;
+                for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint4 g = *reinterpret_cast<const uint4 *>(wt + kmajor_chunk(r, c0 / 8 + u, 128));
-                        const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+                    for (int e = 0; e < 32; ++e)
+                        v[u][e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[u][e]));  // a reset drops S
+                    tmem_st32(to + 64 * hf + 32 * u, v[u]);
+                    if (DOTS) {
+                        const unsigned char *wt = sm + ((n + NS + 1) % AT_SLOTS) * AT_SLOT;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dot_state += lo_f(gw[e]) * __uint_as_float(v[8 * u + 2 * e]) +
-                                         hi_f(gw[e]) * __uint_as_float(v[8 * u + 2 * e + 1]);
+                        for (int k8 = 0; k8 < 4; ++k8) {
+                            const uint4 g =
+                                *reinterpret_cast<const uint4 *>(wt + kmajor_chunk(r, 8 * hf + 4 * u + k8, 128));
+                            const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dot_state += lo_f(gw[e]) * __uint_as_float(v[u][8 * k8 + 2 * e]) +
+                                             hi_f(gw[e]) * __uint_as_float(v[u][8 * k8 + 2 * e + 1]);
+                        }
                     }
                 }
             }
@@ -767,23 +776,21 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                     if (sub == 0 && len - j0 < 128) {  // what lies past the block's end must not meet P's zeros
                         if (!wait(ld.bar(nz), ld.parity(nz))) break;
                         if (r >= len - j0) {
-                            unsigned char *z = sm + (nz % AT_SLOTS) * AT_SLOT + r * 128;
+                            unsigned char *z = sm + (nz % AT_SLOTS) * AT_SLOT + hf * 16384 + r * 128;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 8; ++e)
                                 *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-                                *reinterpret_cast<uint4 *>(z + 16384 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-                            }
                         }
                         fence_proxy_async();
                     }
-#pragma unroll 1
-                    for (int c0 = 0; c0 < SUB; c0 += 32) {
+#pragma unroll
+                    for (int u = 0; u < HSUB / 32; ++u) {
                         uint32_t v[32], v2[32], o[16];
-                        const int jc = j0 + sub * SUB + c0;
+                        const int c0 = hf * HSUB + 32 * u, jc = j0 + sub * SUB + c0;
                         if (REV ? jc < i32 || jc >= len : jc > i32) {  // outside the mask
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = 0u;
-                            tmem_st16(tp + c0 / 2, o);
+                            tmem_st16(tp + hf * HSUB + 16 * u, o);  // inside this thread's own columns
                             continue;
                         }
                         tmem_ld32(tp + c0, v);
@@ -792,7 +799,8 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                         if (jc != i32 && (!REV || jc + 32 <= len)) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 cf = *reinterpret_cast<const float4 *>(col + jc + e);
+                                const float4 cf = *reinterpret_cast<const float4 *>(
+                                    col + j * 64 + sub * HSUB + 32 * u + e);
                                 const float y0 = rf * cf.x * __uint_as_float(v[e]);
                                 const float y1 = rf * cf.y * __uint_as_float(v[e + 1]);
                                 const float y2 = rf * cf.z * __uint_as_float(v[e + 2]);
@@ -819,7 +827,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                                 o[e / 2] = pack2(y[0], y[1]);
                             }
                         }
-                        tmem_st16(tp + c0 / 2, o);
+                        tmem_st16(tp + hf * HSUB + 16 * u, o);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -830,25 +838,26 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             warp_arrive(bar + AB_A_EMPTY + slot);
             if (DOTS && i < len) {
                 const int64_t at = (int64_t)(x.blk.start + i) * geo.H + x.h;
-                p.dot[at] = dot + dot_state;
-                if (p.dot_state) p.dot_state[at] = dot_state;
+                p.dot[hf * p.dot_stride + at] = dot + dot_state;
+                if (p.dot_state) p.dot_state[hf * p.dot_stride + at] = dot_state;
             }
             if (!wait(bar + AB_O_FULL + c, q & 1)) break;
             tc_fence_after();
             __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + i) * geo.H + x.h) * D;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(to + c0, v);
+            {
+                uint32_t v[2][32];
+                tmem_ld32(to + 64 * hf, v[0]);
+                tmem_ld32(to + 64 * hf + 32, v[1]);
                 tmem_wait_ld();
                 if (i < len) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < 4; ++u) {
                         uint32_t o[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            o[e] = pack2(__uint_as_float(v[16 * u + 2 * e]), __uint_as_float(v[16 * u + 2 * e + 1]));
-                        st_v8(dst + c0 + 16 * u, o);
+                            o[e] = pack2(__uint_as_float(v[u >> 1][16 * (u & 1) + 2 * e]),
+                                         __uint_as_float(v[u >> 1][16 * (u & 1) + 2 * e + 1]));
+                        st_v8(dst + 64 * hf + 16 * u, o);
                     }
                 }
             }
@@ -953,7 +962,7 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
     mw = mx;
     if (dots && !token_map(&mw, a.w, a.w_stride, geo.H, a.tokens)) return cudaErrorInvalidValue;
     AttendTcArgs p{geo, a.log_decay, a.decay, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.dot, a.dot_state,
-                   (int)rows, 0, geo.sb / 128};
+                   a.tokens * geo.H, (int)rows, 0, geo.sb / 128};
     p.items = geo.nblocks * geo.H * p.tiles;
     auto k = !a.rev ? (!a.state_t ? lin_attend_tc_kernel<false, false, false>
                        : dots     ? lin_attend_tc_kernel<false, true, true>

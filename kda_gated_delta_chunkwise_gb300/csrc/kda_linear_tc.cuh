@@ -34,7 +34,7 @@ struct AttendTc {
     int decay;
     void *out;
     float c_state, c_intra;
-    float *dot, *dot_state;  // [tokens][H], nullable
+    float *dot, *dot_state;  // [2][tokens][H], the sums of two column halves, nullable
 };
 cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s);
 // Reads (and optionally clears) the error word of these kernels' waits.
