@@ -27,6 +27,8 @@
 // operand is split in two tf32 parts (22 bits) where its error would reach an
 // fp32 output, and kept as one part (11 bits, against the 8 of the bf16 output)
 // where it would not. Accumulators, states and sums are fp32.
+#include <algorithm>
+
 #include "kda_linear.cuh"
 #include "kda_linear_tc.cuh"
 
@@ -575,7 +577,8 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
         p.block_sum = (float *)take((size_t)nb * H * 4);
     }
     p.bytes = at;
-    p.geo = {p.blocks, p.seq_block, p.status, N, (int)T, H, sb, (int)((T + sb - 1) / sb), (int)nb};
+    p.geo = {p.blocks, p.seq_block, p.status, N, (int)T, H, sb, (int)((T + sb - 1) / sb), (int)nb, FastDiv(H),
+             FastDiv((uint32_t)std::max<int64_t>(1, (T + sb - 1) / sb))};
     if (!packed) p.geo.blocks = nullptr, p.geo.seq_block = nullptr, p.geo.status = nullptr;
     return p;
 }

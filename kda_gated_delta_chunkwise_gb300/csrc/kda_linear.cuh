@@ -37,6 +37,19 @@ struct LinBlock {
     int start;  // first token
     int len;    // tokens (0: no such block, nothing to do)
 };
+// n / d by a multiplication, for 0 <= n < 2^31: with l = ceil(log2 d) and
+// m = floor(2^(31 + l) / d) + 1 <= 2^32, the error (m d - 2^(31 + l)) n / (d 2^(31 + l))
+// stays below 1 / d. (The divisions of a work item's number sat in front of
+// every item in the roles that run on one thread.)
+struct FastDiv {
+    uint32_t d, m, l;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div), l(0) {
+        while ((1ull << l) < div) ++l;
+        m = (uint32_t)((1ull << (31 + l)) / div + 1);  // div = 1: 2^31 + 1
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + l)); }
+};
 struct LinGeom {
     const int4 *blocks;        // packed: {seq, start, len, 0} per block, else null
     const int32_t *seq_block;  // packed: first block of each sequence [N + 1]
@@ -45,6 +58,7 @@ struct LinGeom {
     int sb;                    // tokens per block, a multiple of kLinChunk
     int per_seq;               // equal lengths: blocks per sequence
     int nblocks;               // blocks (packed: an upper bound)
+    FastDiv by_heads, by_seq;  // divisions by H and by per_seq
 };
 constexpr int kLinChunk = 64;
 
@@ -53,7 +67,7 @@ __device__ __forceinline__ LinBlock lin_block(const LinGeom &g, int b) {
         const int4 x = __ldg(g.blocks + b);
         return {x.x, x.y, x.z};
     }
-    const int n = b / g.per_seq, i = b - n * g.per_seq;
+    const int n = g.by_seq.div(b), i = b - n * g.per_seq;
     const int off = i * g.sb;
     return {n, n * g.T + off, min(g.sb, g.T - off)};
 }

@@ -213,8 +213,8 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             prefetch_tmap(&my);
             int n = 0;  // tiles so far
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-                const LinBlock blk = lin_block(geo, it / geo.H);
-                const int h = it % geo.H;
+                const int b = geo.by_heads.div(it), h = it - b * geo.H;
+                const LinBlock blk = lin_block(geo, b);
                 for (int t0 = 0; t0 < blk.len; t0 += ST_TOK, ++n) {
                     const int s = n % ST_STAGES, ph = (n / ST_STAGES) & 1;
                     if (!(ok = ab.wait(bar + SB_EMPTY + s, ph ^ 1))) break;
@@ -234,7 +234,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             constexpr uint32_t I2 = idesc_bf16(128, 256, true, true), I1 = idesc_bf16(128, 128, true, true);
             int n = 0, q = 0;
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-                const LinBlock blk = lin_block(geo, it / geo.H);
+                const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
                 if (blk.len <= 0) continue;
                 const int buf = q & 1;
                 if (!(ok = ab.wait(bar + SB_ACC_EMPTY + buf, ((q >> 1) & 1) ^ 1))) break;
@@ -263,7 +263,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
     } else if (warp == 2) {
         int q = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const int b = it / geo.H, h = it % geo.H;
+            const int b = geo.by_heads.div(it), h = it - b * geo.H;
             const LinBlock blk = lin_block(geo, b);
             if (blk.len <= 0) continue;
             constexpr int PER = kLinMaxBlock / 32;
@@ -285,7 +285,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         const int row = tid - 128;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const LinBlock blk = lin_block(geo, it / geo.H);
+            const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
             if (blk.len <= 0) continue;
             const int buf = q & 1;
             ok = ab.wait(bar + SB_ACC_FULL + buf, (q >> 1) & 1);
@@ -311,7 +311,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         const uint32_t off = kmajor_chunk(t >> 4, t & 15, ST_TOK);
         int n = 0, q = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const LinBlock blk = lin_block(geo, it / geo.H);
+            const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
             if (blk.len <= 0) continue;
             ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1));
             const float *w = wts + (q & 1) * kLinMaxBlock;
@@ -497,7 +497,7 @@ struct AttendTcArgs {
     float *dot, *dot_state;
     int64_t dot_stride;  // between the two column halves' sums
     int state_rows;      // rows of one part of S
-    int items, tiles;    // tiles: 128-row tiles per block
+    int items;           // two 128-row tiles per block and head
 };
 struct Item {
     LinBlock blk;
@@ -505,10 +505,10 @@ struct Item {
 };
 template <bool REV> __device__ __forceinline__ Item item_of(const AttendTcArgs &p, int it) {
     Item x;
-    x.h = it % p.geo.H;
-    const int r = it / p.geo.H;
-    x.b = r / p.tiles;
-    const int tile = r - x.b * p.tiles;
+    const int r = p.geo.by_heads.div(it);
+    x.h = it - r * p.geo.H;
+    x.b = r / 2;  // two tiles to a block
+    const int tile = r & 1;
     x.blk = lin_block(p.geo, x.b);
     x.i0 = tile * 128;
     if (x.i0 >= x.blk.len) {
@@ -954,7 +954,7 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
     const LinGeom &geo = a.geo;
     const bool dots = a.dot != nullptr;
     const int64_t rows = (int64_t)geo.nblocks * geo.H * D;
-    if (geo.sb > kLinMaxBlock || rows * 3 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (geo.sb != kLinMaxBlock || rows * 3 > INT32_MAX) return cudaErrorInvalidConfiguration;
     CUtensorMap mx, my, mz, ms, mw;
     if (!token_map(&mx, a.x, a.x_stride, geo.H, a.tokens) || !token_map(&my, a.y, a.y_stride, geo.H, a.tokens) ||
         !token_map(&mz, a.z, a.z_stride, geo.H, a.tokens) || !state_map(&ms, a.states, dots ? 3 * rows : rows))
@@ -962,8 +962,7 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
     mw = mx;
     if (dots && !token_map(&mw, a.w, a.w_stride, geo.H, a.tokens)) return cudaErrorInvalidValue;
     AttendTcArgs p{geo, a.log_decay, a.decay, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.dot, a.dot_state,
-                   a.tokens * geo.H, (int)rows, 0, geo.sb / 128};
-    p.items = geo.nblocks * geo.H * p.tiles;
+                   a.tokens * geo.H, (int)rows, geo.nblocks * geo.H * 2};
     auto k = !a.rev ? (!a.state_t ? lin_attend_tc_kernel<false, false, false>
                        : dots     ? lin_attend_tc_kernel<false, true, true>
                                   : lin_attend_tc_kernel<false, true, false>)
