@@ -13,11 +13,33 @@ ready on it.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
 
 import torch
 
-from ._binding import _check, _dtype_code, _need, _ptr, _stream, load
+from . import _binding
+from ._binding import _check, _dtype_code, _need
+
+# Host time counts for one token of one sequence: these stand for the
+# binding's helpers of the same names without the objects they make per call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def load():
+    return _binding._lib or _binding.load()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 # decay kinds: one log decay per token and head, one per head, none
 DECAYS = {"token": 0, "head": 1, "none": 2}
@@ -31,8 +53,11 @@ def _kind(kinds: dict, value: str, name: str) -> int:
     return kinds[value]
 
 
+_here = contextlib.nullcontext()
+
+
 def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
 def _view(t, name: str, lead: int, dtype=None, device=None) -> int:
@@ -44,13 +69,13 @@ def _view(t, name: str, lead: int, dtype=None, device=None) -> int:
         raise ValueError(f"{name} must have {lead + 2} dimensions, got {t.dim()}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    H, d = t.shape[-2:]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return 0
+    H, d = t.shape[-2:]
     step, want, even = None, None, (t.stride(-1) == 1 or d == 1) and (H == 1 or t.stride(-2) == d)
     for a in range(lead - 1, -1, -1):  # from the innermost lead axis outwards
         if t.shape[a] == 1:
@@ -351,6 +376,11 @@ def rope_table(max_position: int, rotary: int, *, base: float = 10000.0, scaling
     return table.to(device).contiguous()
 
 
+@functools.lru_cache(maxsize=None)
+def _weight_grad_bytes(d: int) -> int:
+    return int(load().kda_qk_norm_rope_backward_workspace_bytes(d))
+
+
 def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout):
     if q is None or q.dim() < 3:
         raise ValueError("q must be [.., H_q, d]")
@@ -429,7 +459,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope_table=None,
                "dk_weight": None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)}
         ws, size = None, 0
         if q_weight is not None or k_weight is not None:
-            ws, size = _space(workspace, int(lib.kda_qk_norm_rope_backward_workspace_bytes(d)), dev)
+            ws, size = _space(workspace, _weight_grad_bytes(d), dev)
     _check(lib, lib.kda_qk_norm_rope_backward(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), code, qs, ks,
                                               _ptr(positions), _ptr(rope_table), P, rot, lay, _ptr(q_weight),
                                               _ptr(k_weight), nk, float(eps), _ptr(out["dq"]), _ptr(out["dk"]),

@@ -520,9 +520,18 @@ lin_head_sum_kernel(LinGeom geo, const float *__restrict__ block_sum, float *__r
 // ---------------------------------------------------------------- host side
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The block length: long blocks mean few states to write and join, short ones
-// more work at once and less of it inside the block.
-int block_tokens() { return 256; }
+// The block length. The tensor-core kernels take 256 (kLinMaxBlock). The
+// general ones work on 64-token chunks one after the other, so a block is as
+// long as still leaves enough of them to fill the GPU (four CTAs' worth for
+// each of the 152 SMs): 257 tokens x 2 heads, fp32, d = 64, take 21 us of GPU
+// time in blocks of 64 and 40 in blocks of 256, while a long batch writes and
+// joins a quarter of the states with 256.
+int block_tokens(int64_t tokens, int H, bool tc) {
+    if (tc) return kLinMaxBlock;
+    int sb = 256;
+    while (sb > CH && tokens / sb * H < 4 * 152) sb /= 2;
+    return sb;
+}
 
 int64_t max_blocks(int N, int64_t T, bool packed, int sb) {
     return packed ? T / sb + N : (int64_t)N * ((T + sb - 1) / sb);
@@ -541,8 +550,9 @@ struct Plan {
 bool use_tc(kda_dtype_t dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
 Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed, bool back, void *ws) {
     Plan p{};
-    const int sb = block_tokens();
-    const int64_t nb = max_blocks(N, T, packed, sb), tokens = packed ? T : N * T;
+    const int64_t tokens = packed ? T : N * T;
+    const int sb = block_tokens(tokens, H, use_tc(dt, dk, dv));
+    const int64_t nb = max_blocks(N, T, packed, sb);
     unsigned char *base = static_cast<unsigned char *>(ws);
     size_t at = 0;
     auto take = [&](size_t n) {

@@ -6,6 +6,20 @@
 
 namespace kda {
 
+// n / d by a multiplication, for 0 <= n < 2^31: with l = ceil(log2 d) and
+// m = floor(2^(31 + l) / d) + 1 <= 2^32, the error (m d - 2^(31 + l)) n / (d 2^(31 + l))
+// stays below 1 / d. (The divisions of a work item's number sat in front of
+// every item in the roles that run on one thread.)
+struct FastDiv {
+    uint32_t d, m, l;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div), l(0) {
+        while ((1ull << l) < div) ++l;
+        m = (uint32_t)((1ull << (31 + l)) / div + 1);  // div = 1: 2^31 + 1
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + l)); }
+};
+
 // ---------------------------------------------------------------- norm + rotation
 // Blocks of the backward's persistent grid at most: four of 256 threads on
 // each of the 152 SMs.
@@ -36,19 +50,6 @@ struct LinBlock {
     int seq;    // sequence
     int start;  // first token
     int len;    // tokens (0: no such block, nothing to do)
-};
-// n / d by a multiplication, for 0 <= n < 2^31: with l = ceil(log2 d) and
-// m = floor(2^(31 + l) / d) + 1 <= 2^32, the error (m d - 2^(31 + l)) n / (d 2^(31 + l))
-// stays below 1 / d. (The divisions of a work item's number sat in front of
-// every item in the roles that run on one thread.)
-struct FastDiv {
-    uint32_t d, m, l;
-    FastDiv() = default;
-    explicit FastDiv(uint32_t div) : d(div), l(0) {
-        while ((1ull << l) < div) ++l;
-        m = (uint32_t)((1ull << (31 + l)) / div + 1);  // div = 1: 2^31 + 1
-    }
-    __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + l)); }
 };
 struct LinGeom {
     const int4 *blocks;        // packed: {seq, start, len, 0} per block, else null

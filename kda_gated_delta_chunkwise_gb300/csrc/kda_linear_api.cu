@@ -189,9 +189,9 @@ kda_status_t norm_rope(kda::NormRopeArgs &p, int64_t tokens) {
     if (p.rot > 0 && p.max_position <= 0) return fail(KDA_ERR_INVALID_ARG, "max_position must be positive");
     KDA_CHECK(stride(p.q_stride, p.hq, p.d, p.dt, "q_stride"));
     KDA_CHECK(stride(p.k_stride, p.hk, p.d, p.dt, "k_stride"));
-    // one warp takes at least eight rows of d = 64 bf16 or fewer of the rest, eight warps to a block
+    // a warp takes four rows of one token at a time at least
     const int64_t units = tokens * (((int64_t)p.hq + 3) / 4 + ((int64_t)p.hk + 3) / 4);
-    if (tokens > INT32_MAX || units > 8ll * INT32_MAX)
+    if (tokens > INT32_MAX || units > INT32_MAX)
         return fail(KDA_ERR_UNSUPPORTED, "too many tokens and heads for one launch");
     p.tokens = tokens;
     if (tokens > 0) {
@@ -199,11 +199,11 @@ kda_status_t norm_rope(kda::NormRopeArgs &p, int64_t tokens) {
         if (p.hk > 0) KDA_CHECK(need(p.k, "k"));
         if (p.rot > 0) {
             KDA_CHECK(need(p.positions, "positions", 4));
-            KDA_CHECK(need(p.table, "rope_table", 4));
+            KDA_CHECK(need(p.table, "rope_table"));
         }
     }
-    KDA_CHECK(maybe(p.wq, "q_weight", 4));
-    KDA_CHECK(maybe(p.wk, "k_weight", 4));
+    KDA_CHECK(maybe(p.wq, "q_weight"));
+    KDA_CHECK(maybe(p.wk, "k_weight"));
     return maybe(p.status, "device_status", 4);
 }
 

@@ -30,6 +30,7 @@ template <typename T> struct Vec {  // 16 bytes of a row
     static constexpr int N = 16 / sizeof(T);
     uint4 raw;
     __device__ __forceinline__ void load(const T *p) { raw = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    // plain loads, for what the same kernel may write
     __device__ __forceinline__ void load_rw(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void get(float (&x)[N]) const {
         const T *e = reinterpret_cast<const T *>(&raw);
@@ -50,27 +51,46 @@ template <int LANES> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {  // 4 N-byte aligned
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(p + e));
+            x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+        }
+    } else {
+        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+        x[0] = v.x, x[1] = v.y;
+    }
+}
 // This lane's cosines and sines: element e of the lane's channels sits in
 // pair (channel mod rot/2) of the half layout, channel / 2 of the interleaved.
+// sn is signed for the element it multiplies into: the first of a pair takes
+// its partner with a minus.
 template <int N>
 __device__ __forceinline__ void load_angles(const float *row, int c0, int rot, int layout, float (&cs)[N],
                                             float (&sn)[N]) {
     const int h = rot / 2;
+    if (c0 >= rot) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) cs[e] = 1.f, sn[e] = 0.f;
-    if (c0 >= rot) return;
-    if (layout == KDA_ROPE_HALF) {
+        for (int e = 0; e < N; ++e) cs[e] = 1.f, sn[e] = 0.f;
+    } else if (layout == KDA_ROPE_HALF) {
         const int i0 = c0 < h ? c0 : c0 - h;
-        // the first half's partner enters with a minus sign
-        const float sg = c0 < h ? -1.f : 1.f;
+        load_floats<N>(row + i0, cs);
+        load_floats<N>(row + h + i0, sn);
+        if (c0 < h) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) cs[e] = __ldg(row + i0 + e), sn[e] = sg * __ldg(row + h + i0 + e);
+            for (int e = 0; e < N; ++e) sn[e] = -sn[e];
+        }
     } else {
+        float c[N / 2], t[N / 2];
+        load_floats<N / 2>(row + c0 / 2, c);
+        load_floats<N / 2>(row + h + c0 / 2, t);
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            cs[e] = cs[e + 1] = __ldg(row + (c0 + e) / 2);
-            sn[e + 1] = __ldg(row + h + (c0 + e) / 2);
-            sn[e] = -sn[e + 1];
+        for (int e = 0; e < N / 2; ++e) {
+            cs[2 * e] = cs[2 * e + 1] = c[e];
+            sn[2 * e] = -t[e];
+            sn[2 * e + 1] = t[e];
         }
     }
 }
@@ -122,44 +142,37 @@ __device__ __forceinline__ float rnorm(float ss, int norm, float inv_d, float ep
 
 // A warp's unit: kPasses * ROWS consecutive rows (heads) of one token, taken
 // from q's heads or from k's (never both, so that a weight is one register set).
-struct Unit {
-    int64_t token;
-    int first, heads;
-    bool is_q;
+template <typename T, int D> constexpr int unit_rows() { return kPasses * (32 / (D / Vec<T>::N)); }
+struct Parts {
+    int q, k;              // units of a token
+    FastDiv by_all, by_q, by_k;
+    int64_t tokens;
 };
-template <int ROWS> __device__ __forceinline__ Unit unit_of(int64_t u, int hq, int hk) {
-    constexpr int R = kPasses * ROWS;
-    const int uq = (hq + R - 1) / R, uk = (hk + R - 1) / R;
-    Unit x;
-    x.token = u / (uq + uk);
-    const int part = (int)(u - x.token * (uq + uk));
-    x.is_q = part < uq;
-    x.first = (x.is_q ? part : part - uq) * R;
-    x.heads = x.is_q ? hq : hk;
-    return x;
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-kda_qk_norm_rope_kernel(NormRopeArgs p, int64_t units) {
+kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
     constexpr int N = Vec<T>::N, LANES = D / N, ROWS = 32 / LANES;
-    const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (u >= units) return;
+    const int64_t u64 = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (u64 >= units) return;
+    const int u = (int)u64, tok = parts.by_all.div(u), part = u - tok * (parts.q + parts.k);
     const Geometry g = geometry<T, D>(p.rot);
-    const Unit un = unit_of<ROWS>(u, p.hq, p.hk);
-    const T *x = un.is_q ? (const T *)p.q + un.token * p.q_stride : (const T *)p.k + un.token * p.k_stride;
-    T *y = un.is_q ? (T *)p.yq + un.token * (int64_t)p.hq * D : (T *)p.yk + un.token * (int64_t)p.hk * D;
-    const float *w = un.is_q ? p.wq : p.wk;
+    const bool is_q = part < parts.q;
+    const int64_t token = tok;
+    const int first = (is_q ? part : part - parts.q) * unit_rows<T, D>(), heads = is_q ? p.hq : p.hk;
+    const T *x = is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride;
+    T *y = is_q ? (T *)p.yq + token * (int64_t)p.hq * D : (T *)p.yk + token * (int64_t)p.hk * D;
+    const float *w = is_q ? p.wq : p.wk;
     Vec<T> v[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int row = un.first + i * ROWS + g.lane_row;
+        const int row = first + i * ROWS + g.lane_row;
         v[i].raw = make_uint4(0u, 0u, 0u, 0u);
-        if (row < un.heads) v[i].load_rw(x + (int64_t)row * D + g.c0);  // y may be x: no read-only path
+        if (row < heads) v[i].load_rw(x + (int64_t)row * D + g.c0);  // y may be x: no read-only path
     }
     float cs[N], sn[N];
     if (p.rot > 0) {
-        const int pos = __ldg(p.positions + un.token);
+        const int pos = __ldg(p.positions + token);
         if (pos < 0 || pos >= p.max_position) {  // uniform over the warp: the token's rows are left as they are
             if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
             return;
@@ -167,12 +180,16 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, int64_t units) {
         load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
     }
     float wv[N];
+    if (w) {
+        load_floats<N>(w + g.c0, wv);
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) wv[e] = w ? __ldg(w + g.c0 + e) : 1.f;
+        for (int e = 0; e < N; ++e) wv[e] = 1.f;
+    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        if (un.first + i * ROWS >= un.heads) break;  // uniform
-        const int row = un.first + i * ROWS + g.lane_row;
+        if (first + i * ROWS >= heads) break;  // uniform
+        const int row = first + i * ROWS + g.lane_row;
         float f[N], ss = 0.f;
         v[i].get(f);
 #pragma unroll
@@ -182,7 +199,7 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, int64_t units) {
         for (int e = 0; e < N; ++e) f[e] = f[e] * r * wv[e];
         if (p.rot > 0) turn<N>(f, cs, sn, 1.f, p.layout, g);
         v[i].put(f);
-        if (row < un.heads) v[i].store(y + (int64_t)row * D + g.c0);
+        if (row < heads) v[i].store(y + (int64_t)row * D + g.c0);
     }
 }
 
@@ -192,82 +209,84 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, int64_t units) {
 // kda_weight_sum_kernel adds in block order: the same bits on every call.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, int64_t units) {
+kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
     constexpr int N = Vec<T>::N, LANES = D / N, ROWS = 32 / LANES;
     __shared__ float red[kWarps][2][D];
     const Geometry g = geometry<T, D>(p.rot);
     const int warp = threadIdx.x >> 5;
-    float acc[2][N];
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {  // all rows of q, then all rows of k
+        const bool is_q = side == 0;
+        const int per = is_q ? parts.q : parts.k, heads = is_q ? p.hq : p.hk;
+        const FastDiv by = is_q ? parts.by_q : parts.by_k;
+        const int units = (int)(parts.tokens * per);
+        const float *w = is_q ? p.wq : p.wk;
+        float wv[N], acc[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[0][e] = acc[1][e] = 0.f;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
-        const Unit un = unit_of<ROWS>(u, p.hq, p.hk);
-        const T *x = un.is_q ? (const T *)p.q + un.token * p.q_stride : (const T *)p.k + un.token * p.k_stride;
-        const int64_t at = un.token * (int64_t)un.heads * D;
-        const T *dy = (un.is_q ? (const T *)p.dyq : (const T *)p.dyk) + at;
-        T *dx = (un.is_q ? (T *)p.dxq : (T *)p.dxk) + at;
-        const float *w = un.is_q ? p.wq : p.wk;
-        Vec<T> vx[kPasses], vd[kPasses];
+        for (int e = 0; e < N; ++e) wv[e] = 1.f, acc[e] = 0.f;
+        if (w) load_floats<N>(w + g.c0, wv);
+        for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
+            const int64_t token = by.div((int)u);
+            const int first = (int)(u - token * per) * unit_rows<T, D>();
+            const T *x = (is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride);
+            const int64_t at = token * (int64_t)heads * D;
+            const T *dy = (is_q ? (const T *)p.dyq : (const T *)p.dyk) + at;
+            T *dx = (is_q ? (T *)p.dxq : (T *)p.dxk) + at;
+            Vec<T> vx[kPasses], vd[kPasses];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int row = un.first + i * ROWS + g.lane_row;
-            vx[i].raw = vd[i].raw = make_uint4(0u, 0u, 0u, 0u);
-            if (row < un.heads) {
-                vx[i].load(x + (int64_t)row * D + g.c0);
-                vd[i].load_rw(dy + (int64_t)row * D + g.c0);  // dx may be dy
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = first + i * ROWS + g.lane_row;
+                vx[i].raw = vd[i].raw = make_uint4(0u, 0u, 0u, 0u);
+                if (row < heads) {
+                    vx[i].load(x + (int64_t)row * D + g.c0);
+                    vd[i].load(dy + (int64_t)row * D + g.c0);
+                }
+            }
+            float cs[N], sn[N];
+            if (p.rot > 0) {
+                const int pos = __ldg(p.positions + token);
+                if (pos < 0 || pos >= p.max_position) {
+                    if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
+                    continue;
+                }
+                load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
+            }
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                if (first + i * ROWS >= heads) break;
+                const int row = first + i * ROWS + g.lane_row;
+                float f[N], d[N], ss = 0.f, xd = 0.f;
+                vx[i].get(f);
+                vd[i].get(d);
+                if (p.rot > 0) turn<N>(d, cs, sn, -1.f, p.layout, g);
+#pragma unroll
+                for (int e = 0; e < N; ++e) ss += f[e] * f[e];
+                const float r = rnorm(row_sum<LANES>(ss), p.norm, 1.f / D, p.eps);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    acc[e] += d[e] * (f[e] * r);
+                    d[e] *= wv[e];
+                    xd += f[e] * d[e];
+                }
+                const float c = p.norm == KDA_NORM_NONE ? 0.f
+                                                        : row_sum<LANES>(xd) * (r * r * r) *
+                                                              (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) d[e] = r * d[e] - f[e] * c;
+                vd[i].put(d);
+                if (row < heads) vd[i].store(dx + (int64_t)row * D + g.c0);
             }
         }
-        float cs[N], sn[N];
-        if (p.rot > 0) {
-            const int pos = __ldg(p.positions + un.token);
-            if (pos < 0 || pos >= p.max_position) {
-                if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
-                continue;
-            }
-            load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
-        }
-        float wv[N];
+        // rows of the warp first (lanes LANES apart hold the same channels), then the warps
 #pragma unroll
-        for (int e = 0; e < N; ++e) wv[e] = w ? __ldg(w + g.c0 + e) : 1.f;
+        for (int e = 0; e < N; ++e) {
+            float a = acc[e];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            if (un.first + i * ROWS >= un.heads) break;
-            const int row = un.first + i * ROWS + g.lane_row;
-            float f[N], d[N], ss = 0.f, xd = 0.f;
-            vx[i].get(f);
-            vd[i].get(d);
-            if (p.rot > 0) turn<N>(d, cs, sn, -1.f, p.layout, g);
-#pragma unroll
-            for (int e = 0; e < N; ++e) ss += f[e] * f[e];
-            const float r = rnorm(row_sum<LANES>(ss), p.norm, 1.f / D, p.eps);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float t = d[e] * (f[e] * r);
-                if (un.is_q) acc[0][e] += t;
-                else acc[1][e] += t;
-                d[e] *= wv[e];
-                xd += f[e] * d[e];
-            }
-            const float c = p.norm == KDA_NORM_NONE ? 0.f
-                                                    : row_sum<LANES>(xd) * (r * r * r) *
-                                                          (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
-#pragma unroll
-            for (int e = 0; e < N; ++e) d[e] = r * d[e] - f[e] * c;
-            vd[i].put(d);
-            if (row < un.heads) vd[i].store(dx + (int64_t)row * D + g.c0);
+            for (int off = 16; off >= LANES; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+            if (g.lane_row == 0) red[warp][side][g.c0 + e] = a;
         }
     }
     if (!p.partial) return;
-    // rows of the warp first (lanes LANES apart hold the same channels), then the warps
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float a = acc[s][e];
-#pragma unroll
-            for (int off = 16; off >= LANES; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-            if (g.lane_row == 0) red[warp][s][g.c0 + e] = a;
-        }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
         float a = 0.f;
@@ -290,20 +309,23 @@ kda_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, floa
     if (lane == 0 && dst) dst[o % d] = a;
 }
 
-template <typename T, int D> int64_t count_units(const NormRopeArgs &p) {
-    constexpr int R = kPasses * (32 / (D / Vec<T>::N));
-    return p.tokens * ((p.hq + R - 1) / R + (p.hk + R - 1) / R);
-}
-
 template <typename T, int D> cudaError_t launch(const NormRopeArgs &p, bool back, cudaStream_t s) {
-    const int64_t units = count_units<T, D>(p), blocks = (units + kWarps - 1) / kWarps;
+    constexpr int R = unit_rows<T, D>();
+    Parts parts;
+    parts.q = (p.hq + R - 1) / R;
+    parts.k = (p.hk + R - 1) / R;
+    parts.by_all = FastDiv(parts.q + parts.k);
+    parts.by_q = FastDiv(parts.q > 0 ? parts.q : 1);
+    parts.by_k = FastDiv(parts.k > 0 ? parts.k : 1);
+    parts.tokens = p.tokens;
+    const int64_t units = p.tokens * (parts.q + parts.k), blocks = (units + kWarps - 1) / kWarps;
+    if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (!back) {
-        if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-        kda_qk_norm_rope_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(p, units);
+        kda_qk_norm_rope_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, (int)units);
         return cudaGetLastError();
     }
     const int grid = (int)(blocks < kNormRopeBwdBlocks ? blocks : kNormRopeBwdBlocks);
-    kda_qk_norm_rope_bwd_kernel<T, D><<<grid, kThreads, 0, s>>>(p, units);
+    kda_qk_norm_rope_bwd_kernel<T, D><<<grid, kThreads, 0, s>>>(p, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.partial) return e;
     kda_weight_sum_kernel<<<(2 * D + kWarps - 1) / kWarps, kThreads, 0, s>>>(p.partial, grid, D, p.dwq, p.dwk);
