@@ -137,9 +137,14 @@ def _space(workspace, nbytes: int, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _bytes(name: str, n: int, T: int, H: int, dk: int, dv: int, dtype) -> int:
-    code = _dtype_code(torch.empty(0, dtype=dtype))
+@functools.lru_cache(maxsize=256)
+def _size(name: str, n: int, T: int, H: int, dk: int, dv: int, code: int) -> int:
+    """Workspace bytes: a function of the sizes alone."""
     return int(getattr(load(), name + "_workspace_bytes")(n, T, H, dk, dv, code))
+
+
+def _bytes(name: str, n: int, T: int, H: int, dk: int, dv: int, dtype) -> int:
+    return _size(name, n, T, H, dk, dv, _dtype_code(torch.empty(0, dtype=dtype)))
 
 
 def linear_prefill_workspace_bytes(B: int, T: int, H: int, dk: int = 128, dv: int = 128, dtype=torch.bfloat16) -> int:
@@ -183,7 +188,7 @@ def _prefill(q, k, v, log_decay, cu_seqlens, initial_state, decay, scale, output
         out = _out(out, "out", tuple(v.shape), v.dtype, dev)
         if final_state is not None or output_final_state:
             final_state = _out(final_state, "final_state", (N, H, dk, dv), torch.float32, dev)
-        ws, size = _space(workspace, int(getattr(lib, name + "_workspace_bytes")(N, T, H, dk, dv, code)), dev)
+        ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), dev)
     head = (_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale), _ptr(initial_state), _ptr(out),
             _ptr(final_state))
     if packed:
@@ -253,7 +258,7 @@ def _backward(q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state,
                "dlog_decay": torch.empty_like(g) if g is not None and want_decay_grad else None,
                "d_initial_state": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
                if want_initial_state_grad else None}
-        ws, size = _space(workspace, int(getattr(lib, name + "_workspace_bytes")(N, T, H, dk, dv, code)), dev)
+        ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), dev)
     head = (_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale), _ptr(initial_state), _ptr(d_o),
             _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_decay"]),
             _ptr(out["d_initial_state"]))

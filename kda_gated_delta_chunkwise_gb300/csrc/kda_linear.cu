@@ -593,10 +593,6 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
     return p;
 }
 
-template <typename F> cudaError_t with_smem(F *kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 #define KDA_TRY(x)                              \
     do {                                        \
         const cudaError_t e_ = (x);             \
@@ -606,9 +602,11 @@ template <typename F> cudaError_t with_smem(F *kernel, size_t bytes) {
 template <typename T, int DK, int DV, bool REV>
 cudaError_t run_states(const Plan &p, const void *x, int64_t xs, const void *y, int64_t ys, const LinArgs &a,
                        float *out, cudaStream_t s) {
-    const size_t smem = CH * (ld_cols<T>(DK) + ld_cols<T>(DV)) * sizeof(T) + (p.geo.sb + 1) * sizeof(float2);
+    const size_t fixed = CH * (ld_cols<T>(DK) + ld_cols<T>(DV)) * sizeof(T);
+    const size_t smem = fixed + (p.geo.sb + 1) * sizeof(float2);
     auto k = lin_state_kernel<T, DK, DV, REV>;
-    KDA_TRY(with_smem(k, smem));
+    static std::atomic<uint64_t> allowed{0};
+    KDA_TRY(allow_smem(k, fixed + (kLinMaxBlock + 1) * sizeof(float2), allowed));
     k<<<(unsigned)((int64_t)p.geo.nblocks * p.geo.H), NT, smem, s>>>(p.geo, (const T *)x, xs, (const T *)y, ys,
                                                                      a.log_decay, a.decay, out, REV ? nullptr : p.total);
     return cudaGetLastError();
@@ -623,10 +621,11 @@ cudaError_t run_scan(const Plan &p, float *states, const float *s0, float *sT, f
 }
 template <typename T, int DC, int DO, bool REV, bool ST, bool EXACT>
 cudaError_t run_attend(const AttendArgs &p, cudaStream_t s) {
-    const size_t smem = 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (CH + 4) * 4 + CH * (DO + 8) * 4 +
-                        (p.geo.sb + 1) * sizeof(float2);
+    const size_t fixed = 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (CH + 4) * 4 + CH * (DO + 8) * 4;
+    const size_t smem = fixed + (p.geo.sb + 1) * sizeof(float2);
     auto k = lin_attend_kernel<T, DC, DO, REV, ST, EXACT>;
-    KDA_TRY(with_smem(k, smem));
+    static std::atomic<uint64_t> allowed{0};
+    KDA_TRY(allow_smem(k, fixed + (kLinMaxBlock + 1) * sizeof(float2), allowed));
     k<<<(unsigned)((int64_t)p.geo.nblocks * p.geo.H * (p.geo.sb / CH)), NT, smem, s>>>(p);
     return cudaGetLastError();
 }

@@ -2,6 +2,8 @@
 // with rotary positions, and the host checks in front of them.
 #pragma once
 
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -21,9 +23,22 @@ struct FastDiv {
 };
 
 // ---------------------------------------------------------------- norm + rotation
-// Blocks of the backward's persistent grid at most: four of 256 threads on
-// each of the 152 SMs.
-constexpr int kNormRopeBwdBlocks = 152 * 4;
+// Blocks of the backward's persistent grid at most: three of 256 threads on each
+// of the 152 SMs.
+constexpr int kNormRopeBwdBlocks = 152 * 3;
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once per device: the call
+// takes a microsecond of host time.
+template <typename F> inline cudaError_t allow_smem(F *kernel, size_t bytes, std::atomic<uint64_t> &devices) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 struct NormRopeArgs {
     kda_dtype_t dt;

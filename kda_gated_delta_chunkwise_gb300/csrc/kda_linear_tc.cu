@@ -935,7 +935,8 @@ cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t
     if (!token_map(&mx, x, xs, geo.H, tokens) || !token_map(&my, y, ys, geo.H, tokens)) return cudaErrorInvalidValue;
     StateTcArgs p{geo, log_decay, decay, out, total, geo.nblocks * geo.H};
     auto k = rev ? lin_state_tc_kernel<true> : lin_state_tc_kernel<false>;
-    KDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ST_SMEM));
+    static std::atomic<uint64_t> allowed[2];
+    KDA_TRY(allow_smem(k, ST_SMEM, allowed[rev]));
     k<<<min(p.items, sm_count()), ST_THREADS, ST_SMEM, s>>>(p, mx, my);
     return cudaGetLastError();
 }
@@ -969,7 +970,8 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
                     : (!a.state_t ? lin_attend_tc_kernel<true, false, false>
                        : dots     ? lin_attend_tc_kernel<true, true, true>
                                   : lin_attend_tc_kernel<true, true, false>);
-    KDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM));
+    static std::atomic<uint64_t> allowed[8];
+    KDA_TRY(allow_smem(k, AT_SMEM, allowed[a.rev * 4 + a.state_t * 2 + dots]));
     k<<<min(p.items, sm_count()), AT_THREADS, AT_SMEM, s>>>(p, mx, my, mz, ms, mw);
     return cudaGetLastError();
 }

@@ -9,13 +9,17 @@
 //   dx = r dn - x r^3 (x . dn) c,   c = 1 (L2), 1 / d (RMS), 0 (NONE).
 //
 // Bound by memory: forward one read and one write of q and k, backward two
-// reads and one write. A row (one head of one token) is held by 16 bytes in
-// each of d * sizeof(T) / 16 lanes, so a warp reads 512 contiguous bytes at a
-// time; every warp takes one token's rows four passes at once (2 KB in flight
-// per warp) and keeps that token's cosines and sines in registers. The
-// partner channel of the half layout comes from another lane by a shuffle.
-// Sums, norms and the rotation are in fp32; the only rounding to fewer bits
-// is the store.
+// reads and one write; right behind it come the instructions, so the
+// arithmetic goes two channels at a time (f32x2) and is arranged for few steps.
+// A row (one head of one token) is held by 16 bytes in each of
+// d * sizeof(T) / 16 lanes, so a warp reads 512 contiguous bytes at a time;
+// every warp takes one token's rows four passes at once (2 KB in flight per
+// warp) and keeps that token's angles in registers. With x' the partner of
+// channel x (the half layout's comes from another lane, as it was loaded, so a
+// shuffle moves two bf16 channels),
+//   y = r (A x + B x'),  A = cos w,  B = -+ sin w',
+// with A and B made once per token. Sums, norms and the rotation are in fp32;
+// the only rounding to fewer bits is the store.
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
 
@@ -26,23 +30,60 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPasses = 4;  // row groups of a warp in flight at once
 
-template <typename T> struct Vec {  // 16 bytes of a row
+// Two fp32 values, one instruction for both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+    float x, y;
+    f2_get(a, x, y);
+    return x + y;
+}
+
+template <typename T> struct Vec {  // 16 bytes of a row: N channels, as loaded and as pairs
     static constexpr int N = 16 / sizeof(T);
-    uint4 raw;
-    __device__ __forceinline__ void load(const T *p) { raw = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    // plain loads, for what the same kernel may write
-    __device__ __forceinline__ void load_rw(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float (&x)[N]) const {
-        const T *e = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+    uint32_t raw[4];
+    __device__ __forceinline__ void zero() { raw[0] = raw[1] = raw[2] = raw[3] = 0u; }
+    // a plain load: the same kernel may write there
+    __device__ __forceinline__ void load(const T *p) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        raw[0] = x.x, raw[1] = x.y, raw[2] = x.z, raw[3] = x.w;
     }
-    __device__ __forceinline__ void put(const float (&x)[N]) {
-        T *e = reinterpret_cast<T *>(&raw);
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = from_f32<T>(x[i]);
+    __device__ __forceinline__ void store(T *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(raw[0], raw[1], raw[2], raw[3]);
     }
-    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = raw; }
+    __device__ __forceinline__ F2 get(int i) const {  // channels 2 i, 2 i + 1
+        if constexpr (sizeof(T) == 2) return f2(__uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xffff0000u));
+        else return f2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+    }
+    __device__ __forceinline__ void put(int i, F2 x) {
+        float lo, hi;
+        f2_get(x, lo, hi);
+        if constexpr (sizeof(T) == 2) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(raw[i]) : "f"(hi), "f"(lo));
+        } else {
+            raw[2 * i] = __float_as_uint(lo);
+            raw[2 * i + 1] = __float_as_uint(hi);
+        }
+    }
 };
 
 template <int LANES> __device__ __forceinline__ float row_sum(float v) {
@@ -112,32 +153,45 @@ template <typename T, int D> __device__ __forceinline__ Geometry geometry(int ro
     g.rotated = g.c0 < rot;
     return g;
 }
-
-// y = cos * x + sin * partner (sgn = -1 turns back). Every lane of the warp
-// takes part in the shuffles; `src` is the lane of the partner channels. Lanes
-// outside the rotated channels keep theirs (no 0 * infinity).
-template <int N>
-__device__ __forceinline__ void turn(float (&x)[N], const float (&cs)[N], const float (&sn)[N], float sgn, int layout,
-                                     const Geometry &g) {
+// The partner channels of x. Every lane of the warp takes part in the
+// shuffles; lanes outside the rotated part get zeros (their B is zero, and zero
+// times an infinity of their own would not be).
+template <typename T> __device__ __forceinline__ Vec<T> partner(const Vec<T> &x, int layout, const Geometry &g) {
+    Vec<T> p;
     if (layout == KDA_ROPE_HALF) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float o = __shfl_sync(0xffffffffu, x[e], g.src);
-            if (g.rotated) x[e] = cs[e] * x[e] + sgn * sn[e] * o;
-        }
-    } else if (g.rotated) {
+        for (int i = 0; i < 4; ++i) p.raw[i] = __shfl_sync(0xffffffffu, x.raw[i], g.src);
+    } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            const float a = x[e], b = x[e + 1];
-            x[e] = cs[e] * a + sgn * sn[e] * b;
-            x[e + 1] = cs[e + 1] * b + sgn * sn[e + 1] * a;
-        }
+        for (int i = 0; i < 4; ++i) p.raw[i] = __byte_perm(x.raw[i], 0u, 0x1032);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.raw[i] = x.raw[i ^ 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.raw[i] = g.rotated ? p.raw[i] : 0u;
+    return p;
+}
+// Weights of this lane's channels and of their partners.
+template <int N>
+__device__ __forceinline__ void load_weights(const float *w, int layout, int rot, const Geometry &g, float (&own)[N],
+                                             float (&other)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) own[e] = other[e] = 1.f;
+    if (!w) return;
+    load_floats<N>(w + g.c0, own);
+    if (layout == KDA_ROPE_HALF) {
+        const int h = rot / 2;
+        load_floats<N>(w + (g.c0 < h ? g.c0 + h : g.rotated ? g.c0 - h : g.c0), other);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) other[e] = own[e ^ 1];
     }
 }
 
+// rsqrtf is within 2 ulp
 __device__ __forceinline__ float rnorm(float ss, int norm, float inv_d, float eps) {
-    // 1 / sqrtf, both correctly rounded, instead of the approximate reciprocal root
-    return norm == KDA_NORM_NONE ? 1.f : 1.f / sqrtf((norm == KDA_NORM_RMS ? ss * inv_d : ss) + eps);
+    return norm == KDA_NORM_NONE ? 1.f : rsqrtf((norm == KDA_NORM_RMS ? ss * inv_d : ss) + eps);
 }
 
 // A warp's unit: kPasses * ROWS consecutive rows (heads) of one token, taken
@@ -162,43 +216,46 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
     const int first = (is_q ? part : part - parts.q) * unit_rows<T, D>(), heads = is_q ? p.hq : p.hk;
     const T *x = is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride;
     T *y = is_q ? (T *)p.yq + token * (int64_t)p.hq * D : (T *)p.yk + token * (int64_t)p.hk * D;
-    const float *w = is_q ? p.wq : p.wk;
+    const int pos = p.rot > 0 ? __ldg(p.positions + token) : 0;
     Vec<T> v[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int row = first + i * ROWS + g.lane_row;
-        v[i].raw = make_uint4(0u, 0u, 0u, 0u);
-        if (row < heads) v[i].load_rw(x + (int64_t)row * D + g.c0);  // y may be x: no read-only path
+        v[i].zero();
+        if (row < heads) v[i].load(x + (int64_t)row * D + g.c0);
     }
-    float cs[N], sn[N];
-    if (p.rot > 0) {
-        const int pos = __ldg(p.positions + token);
-        if (pos < 0 || pos >= p.max_position) {  // uniform over the warp: the token's rows are left as they are
-            if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
-            return;
-        }
-        load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
-    }
-    float wv[N];
-    if (w) {
-        load_floats<N>(w + g.c0, wv);
-    } else {
+    F2 A[N / 2], B[N / 2];
+    {
+        float wo[N], wp[N], cs[N], sn[N];
+        load_weights<N>(is_q ? p.wq : p.wk, p.layout, p.rot, g, wo, wp);
+        if (p.rot > 0) {
+            if (pos < 0 || pos >= p.max_position) {  // uniform over the warp: the token's rows are left as they are
+                if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
+                return;
+            }
+            load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
+        } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) wv[e] = 1.f;
+            for (int e = 0; e < N; ++e) cs[e] = 1.f, sn[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            A[e / 2] = f2(cs[e] * wo[e], cs[e + 1] * wo[e + 1]);
+            B[e / 2] = f2(sn[e] * wp[e], sn[e + 1] * wp[e + 1]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         if (first + i * ROWS >= heads) break;  // uniform
         const int row = first + i * ROWS + g.lane_row;
-        float f[N], ss = 0.f;
-        v[i].get(f);
+        const Vec<T> o = partner(v[i], p.layout, g);
+        F2 ss = f2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss += f[e] * f[e];
-        const float r = rnorm(row_sum<LANES>(ss), p.norm, 1.f / D, p.eps);
+        for (int e = 0; e < N / 2; ++e) ss = fma2(v[i].get(e), v[i].get(e), ss);
+        const float r = rnorm(row_sum<LANES>(f2_sum(ss)), p.norm, 1.f / D, p.eps);
+        const F2 r2 = f2(r, r);
 #pragma unroll
-        for (int e = 0; e < N; ++e) f[e] = f[e] * r * wv[e];
-        if (p.rot > 0) turn<N>(f, cs, sn, 1.f, p.layout, g);
-        v[i].put(f);
+        for (int e = 0; e < N / 2; ++e) v[i].put(e, fma2(A[e], v[i].get(e), B[e] * o.get(e)) * r2);
         if (row < heads) v[i].store(y + (int64_t)row * D + g.c0);
     }
 }
@@ -221,11 +278,15 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
         const FastDiv by = is_q ? parts.by_q : parts.by_k;
         const int units = (int)(parts.tokens * per);
         const float *w = is_q ? p.wq : p.wk;
-        float wv[N], acc[N];
+        float wo[N], wp[N];
+        F2 acc[N / 2], wv[N / 2];
+        load_weights<N>(w, p.layout, p.rot, g, wo, wp);
 #pragma unroll
-        for (int e = 0; e < N; ++e) wv[e] = 1.f, acc[e] = 0.f;
-        if (w) load_floats<N>(w + g.c0, wv);
-        for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
+        for (int e = 0; e < N / 2; ++e) acc[e] = f2(0.f, 0.f), wv[e] = f2(wo[2 * e], wo[2 * e + 1]);
+        const int64_t step = (int64_t)gridDim.x * kWarps;
+        int64_t u = (int64_t)blockIdx.x * kWarps + warp;
+        int pos = p.rot > 0 && u < units ? __ldg(p.positions + by.div((int)u)) : 0;
+        for (; u < units; u += step) {
             const int64_t token = by.div((int)u);
             const int first = (int)(u - token * per) * unit_rows<T, D>();
             const T *x = (is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride);
@@ -236,51 +297,62 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int row = first + i * ROWS + g.lane_row;
-                vx[i].raw = vd[i].raw = make_uint4(0u, 0u, 0u, 0u);
+                vx[i].zero();
+                vd[i].zero();
                 if (row < heads) {
                     vx[i].load(x + (int64_t)row * D + g.c0);
                     vd[i].load(dy + (int64_t)row * D + g.c0);
                 }
             }
-            float cs[N], sn[N];
-            if (p.rot > 0) {
-                const int pos = __ldg(p.positions + token);
-                if (pos < 0 || pos >= p.max_position) {
-                    if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
-                    continue;
+            F2 cs[N / 2], sn[N / 2];  // turning back: the sines change sign
+            bool good = true;
+            {
+                float c[N], t[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e) c[e] = 1.f, t[e] = 0.f;
+                if (p.rot > 0) {
+                    good = pos >= 0 && pos < p.max_position;
+                    if (good) load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, c, t);
+                    else if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
+                    if (u + step < units) pos = __ldg(p.positions + by.div((int)(u + step)));
                 }
-                load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, cs, sn);
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) cs[e] = f2(c[2 * e], c[2 * e + 1]), sn[e] = f2(-t[2 * e], -t[2 * e + 1]);
             }
+            if (!good) continue;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 if (first + i * ROWS >= heads) break;
                 const int row = first + i * ROWS + g.lane_row;
-                float f[N], d[N], ss = 0.f, xd = 0.f;
-                vx[i].get(f);
-                vd[i].get(d);
-                if (p.rot > 0) turn<N>(d, cs, sn, -1.f, p.layout, g);
+                const Vec<T> o = partner(vd[i], p.layout, g);
+                F2 d[N / 2], ss = f2(0.f, 0.f), xd = ss;
 #pragma unroll
-                for (int e = 0; e < N; ++e) ss += f[e] * f[e];
-                const float r = rnorm(row_sum<LANES>(ss), p.norm, 1.f / D, p.eps);
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    acc[e] += d[e] * (f[e] * r);
-                    d[e] *= wv[e];
-                    xd += f[e] * d[e];
+                for (int e = 0; e < N / 2; ++e) {
+                    d[e] = fma2(cs[e], vd[i].get(e), sn[e] * o.get(e));
+                    const F2 xe = vx[i].get(e);
+                    ss = fma2(xe, xe, ss);
+                    xd = fma2(xe, d[e] * wv[e], xd);
                 }
+                const float r = rnorm(row_sum<LANES>(f2_sum(ss)), p.norm, 1.f / D, p.eps);
                 const float c = p.norm == KDA_NORM_NONE ? 0.f
-                                                        : row_sum<LANES>(xd) * (r * r * r) *
+                                                        : row_sum<LANES>(f2_sum(xd)) * (r * r * r) *
                                                               (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
+                const F2 r2 = f2(r, r), c2 = f2(-c, -c);
 #pragma unroll
-                for (int e = 0; e < N; ++e) d[e] = r * d[e] - f[e] * c;
-                vd[i].put(d);
+                for (int e = 0; e < N / 2; ++e) {
+                    const F2 xe = vx[i].get(e), dr = d[e] * r2;
+                    acc[e] = fma2(xe, dr, acc[e]);
+                    vd[i].put(e, fma2(dr, wv[e], xe * c2));
+                }
                 if (row < heads) vd[i].store(dx + (int64_t)row * D + g.c0);
             }
         }
         // rows of the warp first (lanes LANES apart hold the same channels), then the warps
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            float a = acc[e];
+            float a, b;
+            f2_get(acc[e / 2], a, b);
+            if (e & 1) a = b;
 #pragma unroll
             for (int off = 16; off >= LANES; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
             if (g.lane_row == 0) red[warp][side][g.c0 + e] = a;
