@@ -23,9 +23,9 @@ struct FastDiv {
 };
 
 // ---------------------------------------------------------------- norm + rotation
-// Blocks of the backward's persistent grid at most: three of 256 threads on each
+// Blocks of the backward's persistent grid at most: two of 256 threads on each
 // of the 152 SMs.
-constexpr int kNormRopeBwdBlocks = 152 * 3;
+constexpr int kNormRopeBwdBlocks = 152 * 2;
 
 // Lets `kernel` have `bytes` of dynamic shared memory, once per device: the call
 // takes a microsecond of host time.

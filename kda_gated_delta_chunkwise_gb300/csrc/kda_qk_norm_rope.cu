@@ -92,15 +92,16 @@ template <int LANES> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {  // 4 N-byte aligned
+// From global or shared memory, 4 N-byte aligned.
+template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(p + e));
+            const float4 v = *reinterpret_cast<const float4 *>(p + e);
             x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
         }
     } else {
-        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+        const float2 v = *reinterpret_cast<const float2 *>(p);
         x[0] = v.x, x[1] = v.y;
     }
 }
@@ -264,72 +265,114 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
 // keeps its share of the weight gradients in registers; the block's shares
 // are added in warp order and written to `partial` [blocks][2][D], which
 // kda_weight_sum_kernel adds in block order: the same bits on every call.
+// x, dy and the token's table row come by cp.async into a ring of the warp's
+// own, kStages units deep: 13 KB in flight per warp at no cost in registers
+// (held in registers instead, two blocks of eight warps fit on an SM with 4 KB
+// each, and 16384 x 32 rows of 128 bf16 channels took 110 us).
+constexpr int kStages = 3;
+constexpr int kUnitBytes = 2 * kPasses * 512 + 512;  // x, dy, table row
+constexpr int kBwdSmem = kWarps * kStages * kUnitBytes;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {  // zeros where not there
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
     constexpr int N = Vec<T>::N, LANES = D / N, ROWS = 32 / LANES;
-    __shared__ float red[kWarps][2][D];
+    extern __shared__ __align__(16) unsigned char smem[];
     const Geometry g = geometry<T, D>(p.rot);
-    const int warp = threadIdx.x >> 5;
-#pragma unroll 1
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned char *ring = smem + warp * kStages * kUnitBytes;
+    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    float sums[2][N];
+#pragma unroll
     for (int side = 0; side < 2; ++side) {  // all rows of q, then all rows of k
         const bool is_q = side == 0;
         const int per = is_q ? parts.q : parts.k, heads = is_q ? p.hq : p.hk;
         const FastDiv by = is_q ? parts.by_q : parts.by_k;
-        const int units = (int)(parts.tokens * per);
-        const float *w = is_q ? p.wq : p.wk;
+        const int64_t units = parts.tokens * per, x_stride = is_q ? p.q_stride : p.k_stride;
+        const T *xb = (const T *)(is_q ? p.q : p.k), *dyb = (const T *)(is_q ? p.dyq : p.dyk);
+        T *dxb = (T *)(is_q ? p.dxq : p.dxk);
         float wo[N], wp[N];
         F2 acc[N / 2], wv[N / 2];
-        load_weights<N>(w, p.layout, p.rot, g, wo, wp);
+        load_weights<N>(is_q ? p.wq : p.wk, p.layout, p.rot, g, wo, wp);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) acc[e] = f2(0.f, 0.f), wv[e] = f2(wo[2 * e], wo[2 * e + 1]);
-        const int64_t step = (int64_t)gridDim.x * kWarps;
+        auto position = [&](int64_t u) { return p.rot > 0 && u < units ? __ldg(p.positions + by.div((int)u)) : 0; };
+        auto in_table = [&](int pos) { return pos >= 0 && pos < p.max_position; };
+        auto fetch = [&](int64_t u, int pos, int stage) {  // one group of copies, empty past the last unit
+            if (u < units) {
+                const int64_t token = by.div((int)u);
+                const int first = (int)(u - token * per) * unit_rows<T, D>();
+                const uint32_t dst = ring_s + stage * kUnitBytes + lane * 16;
+                const T *x = xb + token * x_stride, *dy = dyb + token * (int64_t)heads * D;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int row = first + i * ROWS + g.lane_row;
+                    const bool there = row < heads;
+                    const int64_t at = there ? (int64_t)row * D + g.c0 : 0;
+                    copy16(dst + i * 512, x + at, there);
+                    copy16(dst + (kPasses + i) * 512, dy + at, there);
+                }
+                if (4 * lane < p.rot)
+                    copy16(dst + 2 * kPasses * 512, p.table + (in_table(pos) ? (int64_t)pos * p.rot + 4 * lane : 0),
+                           in_table(pos));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         int64_t u = (int64_t)blockIdx.x * kWarps + warp;
-        int pos = p.rot > 0 && u < units ? __ldg(p.positions + by.div((int)u)) : 0;
+        int pos[kStages];  // of the units in the ring; the next one's is loaded a unit ahead of its copies
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) pos[i] = position(u + i * step);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(u + i * step, pos[i], i);
+        int stage = 0;
         for (; u < units; u += step) {
+            const int next = stage == 0 ? kStages - 1 : stage - 1;  // the stage read last
+            __syncwarp();  // by every lane
+            fetch(u + (kStages - 1) * step, pos[kStages - 1], next);
+            const int ahead = position(u + kStages * step);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+            const unsigned char *buf = ring + stage * kUnitBytes;
+            const bool good = p.rot == 0 || in_table(pos[0]);
+#pragma unroll
+            for (int i = 0; i + 1 < kStages; ++i) pos[i] = pos[i + 1];
+            pos[kStages - 1] = ahead;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            if (!good) {  // the token is left out
+                if (lane == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
+                continue;
+            }
             const int64_t token = by.div((int)u);
             const int first = (int)(u - token * per) * unit_rows<T, D>();
-            const T *x = (is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride);
-            const int64_t at = token * (int64_t)heads * D;
-            const T *dy = (is_q ? (const T *)p.dyq : (const T *)p.dyk) + at;
-            T *dx = (is_q ? (T *)p.dxq : (T *)p.dxk) + at;
-            Vec<T> vx[kPasses], vd[kPasses];
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int row = first + i * ROWS + g.lane_row;
-                vx[i].zero();
-                vd[i].zero();
-                if (row < heads) {
-                    vx[i].load(x + (int64_t)row * D + g.c0);
-                    vd[i].load(dy + (int64_t)row * D + g.c0);
-                }
-            }
+            T *dx = dxb + token * (int64_t)heads * D;
             F2 cs[N / 2], sn[N / 2];  // turning back: the sines change sign
-            bool good = true;
             {
                 float c[N], t[N];
 #pragma unroll
                 for (int e = 0; e < N; ++e) c[e] = 1.f, t[e] = 0.f;
-                if (p.rot > 0) {
-                    good = pos >= 0 && pos < p.max_position;
-                    if (good) load_angles<N>(p.table + (int64_t)pos * p.rot, g.c0, p.rot, p.layout, c, t);
-                    else if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
-                    if (u + step < units) pos = __ldg(p.positions + by.div((int)(u + step)));
-                }
+                if (p.rot > 0)
+                    load_angles<N>(reinterpret_cast<const float *>(buf + 2 * kPasses * 512), g.c0, p.rot, p.layout, c, t);
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) cs[e] = f2(c[2 * e], c[2 * e + 1]), sn[e] = f2(-t[2 * e], -t[2 * e + 1]);
             }
-            if (!good) continue;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 if (first + i * ROWS >= heads) break;
                 const int row = first + i * ROWS + g.lane_row;
-                const Vec<T> o = partner(vd[i], p.layout, g);
+                Vec<T> vx, vd;
+                vx.load(reinterpret_cast<const T *>(buf + i * 512 + lane * 16));
+                vd.load(reinterpret_cast<const T *>(buf + (kPasses + i) * 512 + lane * 16));
+                const Vec<T> o = partner(vd, p.layout, g);
                 F2 d[N / 2], ss = f2(0.f, 0.f), xd = ss;
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {
-                    d[e] = fma2(cs[e], vd[i].get(e), sn[e] * o.get(e));
-                    const F2 xe = vx[i].get(e);
+                    d[e] = fma2(cs[e], vd.get(e), sn[e] * o.get(e));
+                    const F2 xe = vx.get(e);
                     ss = fma2(xe, xe, ss);
                     xd = fma2(xe, d[e] * wv[e], xd);
                 }
@@ -340,14 +383,16 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
                 const F2 r2 = f2(r, r), c2 = f2(-c, -c);
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {
-                    const F2 xe = vx[i].get(e), dr = d[e] * r2;
+                    const F2 xe = vx.get(e), dr = d[e] * r2;
                     acc[e] = fma2(xe, dr, acc[e]);
-                    vd[i].put(e, fma2(dr, wv[e], xe * c2));
+                    vd.put(e, fma2(dr, wv[e], xe * c2));
                 }
-                if (row < heads) vd[i].store(dx + (int64_t)row * D + g.c0);
+                if (row < heads) vd.store(dx + (int64_t)row * D + g.c0);
             }
         }
-        // rows of the warp first (lanes LANES apart hold the same channels), then the warps
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        // rows of the warp first (lanes LANES apart hold the same channels)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             float a, b;
@@ -355,15 +400,20 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
             if (e & 1) a = b;
 #pragma unroll
             for (int off = 16; off >= LANES; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-            if (g.lane_row == 0) red[warp][side][g.c0 + e] = a;
+            sums[side][e] = a;
         }
     }
     if (!p.partial) return;
+    float *red = reinterpret_cast<float *>(ring);  // [2][D] in each warp's own ring
+    if (g.lane_row == 0) {
+#pragma unroll
+        for (int e = 0; e < 2 * N; ++e) red[(e / N) * D + g.c0 + e % N] = sums[e / N][e % N];
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
         float a = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) a += red[k][i / D][i % D];
+        for (int k = 0; k < kWarps; ++k) a += reinterpret_cast<const float *>(smem + k * kStages * kUnitBytes)[i];
         p.partial[(int64_t)blockIdx.x * 2 * D + i] = a;
     }
 }
@@ -375,6 +425,7 @@ kda_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, floa
     const int o = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (o >= 2 * d) return;
     float a = 0.f;
+#pragma unroll 10
     for (int b = lane; b < blocks; b += 32) a += partial[(int64_t)b * 2 * d + o];
     a = row_sum<32>(a);
     float *dst = o < d ? dwq : dwk;
@@ -397,8 +448,11 @@ template <typename T, int D> cudaError_t launch(const NormRopeArgs &p, bool back
         return cudaGetLastError();
     }
     const int grid = (int)(blocks < kNormRopeBwdBlocks ? blocks : kNormRopeBwdBlocks);
-    kda_qk_norm_rope_bwd_kernel<T, D><<<grid, kThreads, 0, s>>>(p, parts);
-    cudaError_t e = cudaGetLastError();
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kda_qk_norm_rope_bwd_kernel<T, D>, kBwdSmem, allowed);
+    if (e != cudaSuccess) return e;
+    kda_qk_norm_rope_bwd_kernel<T, D><<<grid, kThreads, kBwdSmem, s>>>(p, parts);
+    e = cudaGetLastError();
     if (e != cudaSuccess || !p.partial) return e;
     kda_weight_sum_kernel<<<(2 * D + kWarps - 1) / kWarps, kThreads, 0, s>>>(p.partial, grid, D, p.dwq, p.dwk);
     return cudaGetLastError();
