@@ -38,7 +38,18 @@ namespace {
 constexpr int NT = 256;  // threads of the three main kernels
 constexpr int CH = kLinChunk;
 
+// The segment length where the state is carried along inside (lin_roll_tc): a
+// function of the sequence's own length, so that a sequence gives the same bits
+// alone and in any batch. A segment costs its 128-token chunks and about two
+// more (its first state, its share of the scan), so short ones pay for being
+// many and long ones leave a small batch on few of the 152 SMs.
+constexpr int kLeastSegment = 512;
+__host__ __device__ constexpr int segment_tokens(int64_t len) {
+    return len <= 2048 ? kLeastSegment : len <= 16384 ? 1024 : len <= 65536 ? 2048 : 4096;
+}
+
 // ---------------------------------------------------------------- packed batches: the table of blocks
+// sb = 0: segments of segment_tokens(length).
 constexpr int kPrepThreads = 1024;
 __global__ void __launch_bounds__(kPrepThreads)
 lin_blocks_kernel(const int32_t *__restrict__ cu, int N, int T_total, int sb, int nblocks, int4 *blocks,
@@ -60,7 +71,11 @@ lin_blocks_kernel(const int32_t *__restrict__ cu, int N, int T_total, int sb, in
     int base = 0;
     for (int i0 = 0; i0 < N; i0 += kPrepThreads) {
         const int i = i0 + tid;
-        int x = (i < N && !b) ? (cu[i + 1] - cu[i] + sb - 1) / sb : 0;
+        int x = 0;
+        if (i < N && !b) {
+            const int len = cu[i + 1] - cu[i], per = sb ? sb : segment_tokens(len);
+            x = (len + per - 1) / per;
+        }
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
@@ -87,8 +102,9 @@ lin_blocks_kernel(const int32_t *__restrict__ cu, int N, int T_total, int sb, in
                 if (seq_block[m] <= j) lo = m;
                 else hi = m - 1;
             }
-            const int off = (j - seq_block[lo]) * sb, start = cu[lo] + off;
-            e = make_int4(lo, start, min(sb, cu[lo + 1] - start), 0);
+            const int per = sb ? sb : segment_tokens(cu[lo + 1] - cu[lo]);
+            const int start = cu[lo] + (j - seq_block[lo]) * per;
+            e = make_int4(lo, start, min(per, cu[lo + 1] - start), 0);
         }
         blocks[j] = e;
     }
@@ -520,18 +536,11 @@ lin_head_sum_kernel(LinGeom geo, const float *__restrict__ block_sum, float *__r
 // ---------------------------------------------------------------- host side
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The block length. The tensor-core kernels take 256 (kLinMaxBlock). The
-// general ones work on 64-token chunks one after the other, so a block is as
-// long as still leaves enough of them to fill the GPU (four CTAs' worth for
-// each of the 152 SMs): 257 tokens x 2 heads, fp32, d = 64, take 21 us of GPU
-// time in blocks of 64 and 40 in blocks of 256, while a long batch writes and
-// joins a quarter of the states with 256.
-int block_tokens(int64_t tokens, int H, bool tc) {
-    if (tc) return kLinMaxBlock;
-    int sb = 256;
-    while (sb > CH && tokens / sb * H < 4 * 152) sb /= 2;
-    return sb;
-}
+// The block length of the general kernels, which work on 64-token chunks one
+// after the other: one chunk a block gives the most blocks at once (257 tokens
+// x 2 heads, fp32, d = 64: 21 us of GPU time in blocks of 64, 40 in blocks of
+// 256). One length for all, so that a sequence gives the same bits in any batch.
+constexpr int kGeneralBlock = 64;
 
 int64_t max_blocks(int N, int64_t T, bool packed, int sb) {
     return packed ? T / sb + N : (int64_t)N * ((T + sb - 1) / sb);
@@ -548,10 +557,13 @@ struct Plan {
     size_t bytes;
 };
 bool use_tc(kda_dtype_t dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
-Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed, bool back, void *ws) {
+// `rolled`: the tensor-core path with the state carried along inside segments
+// (the forward, and the backward without the decay's gradient).
+Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed, bool back, bool rolled, void *ws) {
     Plan p{};
     const int64_t tokens = packed ? T : N * T;
-    const int sb = block_tokens(tokens, H, use_tc(dt, dk, dv));
+    const bool tc = use_tc(dt, dk, dv);
+    const int sb = !tc ? kGeneralBlock : !rolled ? kLinMaxBlock : packed ? kLeastSegment : segment_tokens(T);
     const int64_t nb = max_blocks(N, T, packed, sb);
     unsigned char *base = static_cast<unsigned char *>(ws);
     size_t at = 0;
@@ -569,18 +581,15 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
     p.total = (float *)take((size_t)nb * H * 4);
     p.states = (float *)take(state);
     p.part_stride = nb * H * dk * dv;
-    if (use_tc(dt, dk, dv)) {
-        p.s_parts = (__nv_bfloat16 *)take(state / 2 * (back ? 3 : 1));
-        if (back) {
-            p.g_parts = (__nv_bfloat16 *)take(state / 2 * 3);
-            p.inner = (float *)take((size_t)nb * H * kScanPartials * 4);
-        }
-    } else if (back) {
-        p.grads = (float *)take(state);
+    if (back && (!tc || rolled)) p.grads = (float *)take(state);
+    if (back && tc && !rolled) {
+        p.s_parts = (__nv_bfloat16 *)take(state / 2 * 3);
+        p.g_parts = (__nv_bfloat16 *)take(state / 2 * 3);
+        p.inner = (float *)take((size_t)nb * H * kScanPartials * 4);
     }
-    if (back) {
-        const size_t halves = use_tc(dt, dk, dv) ? 2 : 1;  // row dots come in so many pieces
-        p.dot_stride = halves == 2 ? tokens * H : 0;
+    if (back && !rolled) {
+        const size_t halves = tc ? 2 : 1;  // row dots come in so many pieces
+        p.dot_stride = tc ? tokens * H : 0;
         p.qdq = (float *)take(halves * tokens * H * 4);
         p.kdk = (float *)take(halves * tokens * H * 4);
         p.kdk_state = (float *)take(halves * tokens * H * 4);
@@ -630,53 +639,96 @@ cudaError_t run_attend(const AttendArgs &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, cudaStream_t s) {
+cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, bool rolled, cudaStream_t s) {
     if (!a.cu_seqlens) return cudaSuccess;
-    lin_blocks_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, p.geo.sb, p.geo.nblocks, p.blocks,
+    lin_blocks_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, rolled ? 0 : p.geo.sb, p.geo.nblocks, p.blocks,
                                                  p.seq_block, p.status, a.status);
     return cudaGetLastError();
 }
 
 // bf16, d_k = d_v = 128: the same steps on the tensor cores.
 cudaError_t forward_tc(const LinArgs &a, cudaStream_t s) {
-    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, false, a.workspace);
+    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, false, use_tc(a.dt, a.dk, a.dv), a.workspace);
     const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
-    KDA_TRY(prepare_blocks(p, a, s));
-    if (tokens > 0)
+    KDA_TRY(prepare_blocks(p, a, true, s));
+    // one segment a sequence and no final state asked for: the first states are all there is
+    const bool need_states = a.sT || a.cu_seqlens || p.geo.per_seq > 1;
+    if (tokens > 0 && need_states)
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
                                 p.total, s));
-    KDA_TRY(launch_scan_tc(p.geo, false, 1, p.states, p.total, a.s0, a.sT, 1.f, p.s_parts, p.part_stride, nullptr,
-                           nullptr, s));
+    KDA_TRY(run_scan<false>(p, p.states, a.s0, a.sT, 1.f, 128, 128, s));
     if (tokens == 0) return cudaSuccess;
-    AttendTc t{};
+    RollTc t{};
     t.geo = p.geo;
     t.x = a.q; t.y = a.k; t.z = a.v;
     t.x_stride = a.q_stride; t.y_stride = a.k_stride; t.z_stride = a.v_stride;
-    t.states = p.s_parts; t.part_stride = p.part_stride; t.tokens = tokens;
+    t.states = p.states; t.tokens = tokens;
     t.log_decay = a.log_decay; t.decay = a.decay;
-    t.out = a.o; t.c_state = a.scale; t.c_intra = a.scale;
-    return launch_attend_tc(t, s);
+    t.out = a.o; t.c_state = a.scale; t.c_intra = a.scale; t.c_roll = 1.f;
+    return launch_roll_tc(t, s);
 }
 
-cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
-    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, a.workspace);
+// Backward without the decay's gradient: three passes with the state carried along.
+cudaError_t backward_rolled_tc(const LinArgs &a, cudaStream_t s) {
+    constexpr bool rolled = true;
+    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
     const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T, so = (int64_t)a.H * 128;
-    const bool dots = a.d_decay != nullptr, head = a.decay == KDA_DECAY_HEAD;
-    const int parts = dots ? 3 : 1;
-    KDA_TRY(prepare_blocks(p, a, s));
+    KDA_TRY(prepare_blocks(p, a, true, s));
     if (tokens > 0) {
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
                                 p.total, s));
-        KDA_TRY(launch_scan_tc(p.geo, false, parts, p.states, p.total, a.s0, nullptr, 1.f, p.s_parts, p.part_stride,
+        KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.grads,
+                                nullptr, s));
+        KDA_TRY(run_scan<false>(p, p.states, a.s0, nullptr, 1.f, 128, 128, s));
+    }
+    KDA_TRY(run_scan<true>(p, p.grads, a.dsT, a.ds0, a.scale, 128, 128, s));
+    if (tokens == 0) return cudaSuccess;
+    RollTc t{};
+    t.geo = p.geo;
+    t.tokens = tokens;
+    t.log_decay = a.log_decay; t.decay = a.decay;
+    t.c_intra = a.scale;
+    RollTc u = t;  // dq
+    u.state_t = true;
+    u.x = a.d_o; u.y = a.v; u.z = a.k;
+    u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride;
+    u.states = p.states; u.out = a.dq; u.c_state = a.scale; u.c_roll = 1.f;
+    KDA_TRY(launch_roll_tc(u, s));
+    u = t;  // dk
+    u.rev = u.state_t = true;
+    u.x = a.v; u.y = a.d_o; u.z = a.q;
+    u.x_stride = a.v_stride; u.y_stride = so; u.z_stride = a.q_stride;
+    u.states = p.grads; u.out = a.dk_out; u.c_state = 1.f; u.c_roll = a.scale;
+    KDA_TRY(launch_roll_tc(u, s));
+    u = t;  // dv
+    u.rev = true;
+    u.x = a.k; u.y = a.q; u.z = a.d_o;
+    u.x_stride = a.k_stride; u.y_stride = a.q_stride; u.z_stride = so;
+    u.states = p.grads; u.out = a.dv_out; u.c_state = 1.f; u.c_roll = a.scale;
+    return launch_roll_tc(u, s);
+}
+
+// Backward with the decay's gradient: blocks of kLinMaxBlock, every block's
+// states in three bf16 parts, and the row dots.
+cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
+    constexpr bool rolled = false;
+    const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
+    const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T, so = (int64_t)a.H * 128;
+    const bool head = a.decay == KDA_DECAY_HEAD;
+    KDA_TRY(prepare_blocks(p, a, false, s));
+    if (tokens > 0) {
+        KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
+                                p.total, s));
+        KDA_TRY(launch_scan_tc(p.geo, false, p.states, p.total, a.s0, nullptr, 1.f, p.s_parts, p.part_stride,
                                nullptr, nullptr, s));
         // the blocks' own sums of the states are done with: those of the gradients take their place
         KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.states,
                                 nullptr, s));
     }
-    KDA_TRY(launch_scan_tc(p.geo, true, parts, p.states, p.total, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
+    KDA_TRY(launch_scan_tc(p.geo, true, p.states, p.total, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
                            p.s_parts, p.inner, s));
     if (tokens == 0)
-        return dots && head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
+        return head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
     AttendTc t{};
     t.geo = p.geo;
     t.part_stride = p.part_stride; t.tokens = tokens;
@@ -693,17 +745,16 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
     u.x = a.d_o; u.y = a.v; u.z = a.k; u.w = a.q;
     u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride; u.w_stride = a.q_stride;
     u.states = p.s_parts; u.out = a.dq; u.c_state = a.scale;
-    u.dot = dots ? p.qdq : nullptr;
+    u.dot = p.qdq;
     KDA_TRY(launch_attend_tc(u, s));
     u = t;  // dk
     u.rev = u.state_t = true;
     u.x = a.v; u.y = a.d_o; u.z = a.q; u.w = a.k;
     u.x_stride = a.v_stride; u.y_stride = so; u.z_stride = a.q_stride; u.w_stride = a.k_stride;
     u.states = p.g_parts; u.out = a.dk_out; u.c_state = 1.f;
-    u.dot = dots ? p.kdk : nullptr;
-    u.dot_state = dots ? p.kdk_state : nullptr;
+    u.dot = p.kdk;
+    u.dot_state = p.kdk_state;
     KDA_TRY(launch_attend_tc(u, s));
-    if (!dots) return cudaSuccess;
     lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
         p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
         head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
@@ -715,8 +766,8 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
 
 template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cudaStream_t s) {
     constexpr bool F32 = sizeof(T) == 4;
-    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, false, a.workspace);
-    KDA_TRY(prepare_blocks(p, a, s));
+    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, false, use_tc(a.dt, a.dk, a.dv), a.workspace);
+    KDA_TRY(prepare_blocks(p, a, false, s));
     if (p.geo.nblocks > 0)
         KDA_TRY((run_states<T, DK, DV, false>(p, a.k, a.k_stride, a.v, a.v_stride, a, p.states, s)));
     KDA_TRY((run_scan<false>(p, p.states, a.s0, a.sT, 1.f, DK, DV, s)));
@@ -731,9 +782,9 @@ template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cuda
 }
 
 template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cudaStream_t s) {
-    constexpr bool F32 = sizeof(T) == 4;
-    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, true, a.workspace);
-    KDA_TRY(prepare_blocks(p, a, s));
+    constexpr bool F32 = sizeof(T) == 4, rolled = false;
+    const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
+    KDA_TRY(prepare_blocks(p, a, false, s));
     const int64_t so = (int64_t)a.H * DV;
     if (p.geo.nblocks > 0) {
         KDA_TRY((run_states<T, DK, DV, false>(p, a.k, a.k_stride, a.v, a.v_stride, a, p.states, s)));
@@ -781,10 +832,12 @@ template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cud
 }  // namespace
 
 size_t linear_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed) {
-    return make_plan(N, T, H, dk, dv, dt, packed, false, nullptr).bytes;
+    return make_plan(N, T, H, dk, dv, dt, packed, false, use_tc(dt, dk, dv), nullptr).bytes;
 }
 size_t linear_backward_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed) {
-    return make_plan(N, T, H, dk, dv, dt, packed, true, nullptr).bytes;
+    size_t n = make_plan(N, T, H, dk, dv, dt, packed, true, false, nullptr).bytes;
+    if (use_tc(dt, dk, dv)) n = std::max(n, make_plan(N, T, H, dk, dv, dt, packed, true, true, nullptr).bytes);
+    return n;
 }
 
 #define KDA_LINEAR_DISPATCH(FN)                                                                                 \
@@ -799,7 +852,7 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t s) {
     KDA_LINEAR_DISPATCH(forward);
 }
 cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s) {
-    if (use_tc(a.dt, a.dk, a.dv)) return backward_tc(a, s);
+    if (use_tc(a.dt, a.dk, a.dv)) return a.d_decay ? backward_tc(a, s) : backward_rolled_tc(a, s);
     KDA_LINEAR_DISPATCH(backward);
 }
 

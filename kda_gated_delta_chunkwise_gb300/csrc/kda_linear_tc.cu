@@ -79,6 +79,12 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
         : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {  // into L2
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // D[tmem] += A[tmem] * B[smem]: A holds two bf16 of K per 32-bit column.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
     asm volatile(
@@ -149,6 +155,8 @@ __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float 
 // moves through shared memory.
 //
 // warp 0: TMA; 1: MMA; 2: weights, an item ahead; 4-7: accumulators out;
+// A block longer than kLinMaxBlock goes in parts of that length, joined by the
+// decays of the parts, as the blocks are by the scan.
 // 8-15 and 16-23: x -> three parts (the high one in place), tiles in turn. Each
 // of the two groups has full barriers of its own (see the output kernel).
 constexpr int ST_TOK = 64;
@@ -177,6 +185,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
     unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + ST_BAR);
     float *wts = reinterpret_cast<float *>(sm + ST_W);
+    __shared__ float join[4];
     uint32_t *tm = reinterpret_cast<uint32_t *>(bar + SB_COUNT);
     const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -236,49 +245,56 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
                 if (blk.len <= 0) continue;
-                const int buf = q & 1;
-                if (!(ok = ab.wait(bar + SB_ACC_EMPTY + buf, ((q >> 1) & 1) ^ 1))) break;
-                const uint32_t hi = tmem + buf * 256, lo = hi + 128;
-                for (int t0 = 0; t0 < blk.len; t0 += ST_TOK, ++n) {
-                    const int s = n % ST_STAGES;
-                    if (!(ok = ab.wait(bar + SB_CONV + s, (n / ST_STAGES) & 1))) break;
-                    tc_fence_after();
-                    const uint64_t x = desc_mn(smem_u32(sm + s * ST_STAGE), ST_TILE / 2);
-                    constexpr uint64_t L = (2 * ST_TILE) >> 4, Y = (3 * ST_TILE) >> 4;
-                    if (t0 == 0) mma_ss<false>(hi, x + Y, x, I2);
-                    else mma_ss<true>(hi, x + Y, x, I2);
-                    mma_ss<true>(lo, x + Y, x + L, I1);
+                for (int p0 = 0; p0 < blk.len && ok; p0 += kLinMaxBlock, ++q) {
+                    const int buf = q & 1, end = min(blk.len, p0 + kLinMaxBlock);
+                    if (!(ok = ab.wait(bar + SB_ACC_EMPTY + buf, ((q >> 1) & 1) ^ 1))) break;
+                    const uint32_t hi = tmem + buf * 256, lo = hi + 128;
+                    for (int t0 = p0; t0 < end; t0 += ST_TOK, ++n) {
+                        const int s = n % ST_STAGES;
+                        if (!(ok = ab.wait(bar + SB_CONV + s, (n / ST_STAGES) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t x = desc_mn(smem_u32(sm + s * ST_STAGE), ST_TILE / 2);
+                        constexpr uint64_t L = (2 * ST_TILE) >> 4, Y = (3 * ST_TILE) >> 4;
+                        if (t0 == p0) mma_ss<false>(hi, x + Y, x, I2);
+                        else mma_ss<true>(hi, x + Y, x, I2);
+                        mma_ss<true>(lo, x + Y, x + L, I1);
 #pragma unroll
-                    for (int ks = 1; ks < ST_TOK / 16; ++ks) {
-                        mma_ss<true>(hi, x + Y + step_mn(ks), x + step_mn(ks), I2);
-                        mma_ss<true>(lo, x + Y + step_mn(ks), x + L + step_mn(ks), I1);
+                        for (int ks = 1; ks < ST_TOK / 16; ++ks) {
+                            mma_ss<true>(hi, x + Y + step_mn(ks), x + step_mn(ks), I2);
+                            mma_ss<true>(lo, x + Y + step_mn(ks), x + L + step_mn(ks), I1);
+                        }
+                        umma_commit(bar + SB_EMPTY + s);
                     }
-                    umma_commit(bar + SB_EMPTY + s);
+                    if (!ok) break;
+                    umma_commit(bar + SB_ACC_FULL + buf);
                 }
-                if (!ok) break;
-                umma_commit(bar + SB_ACC_FULL + buf);
-                ++q;
             }
         }
     } else if (warp == 2) {
-        int q = 0;
+        int q = 0;  // parts so far
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const int b = geo.by_heads.div(it), h = it - b * geo.H;
             const LinBlock blk = lin_block(geo, b);
-            if (blk.len <= 0) continue;
-            constexpr int PER = kLinMaxBlock / 32;
-            long long a[PER];
-            const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, blk, h, a);
-            if (!REV && lane == 0 && p.total)
-                p.total[(int64_t)b * geo.H + h] = decay_ratio(decay_pair(all), make_float2(0.f, 0.f));
-            ok = ab.wait(bar + SB_W_EMPTY + (q & 1), ((q >> 1) & 1) ^ 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            float *w = wts + (q & 1) * kLinMaxBlock;
+            long long sum = 0;  // over the block's earlier parts
+            for (int p0 = 0; p0 < blk.len; p0 += kLinMaxBlock, ++q) {
+                constexpr int PER = kLinMaxBlock / 32;
+                long long a[PER];
+                const LinBlock part{blk.seq, blk.start + p0, min(kLinMaxBlock, blk.len - p0)};
+                const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, part, h, a);
+                ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_EMPTY + (q & 1), ((q >> 1) & 1) ^ 1));
+                if (!ok) break;
+                float *w = wts + (q & 1) * kLinMaxBlock;
 #pragma unroll
-            for (int u = 0; u < PER; ++u)
-                w[lane * PER + u] = decay_ratio(decay_pair(REV ? a[u] : all - a[u]), make_float2(0.f, 0.f));
-            warp_arrive(bar + SB_W_FULL + (q & 1));
-            ++q;
+                for (int u = 0; u < PER; ++u)
+                    w[lane * PER + u] = decay_ratio(decay_pair(REV ? a[u] : all - a[u]), make_float2(0.f, 0.f));
+                // what the sum so far (forward) or this part (reverse) is multiplied by when they are joined
+                if (lane == 0)
+                    join[q & 3] = decay_ratio(decay_pair(REV ? sum : all), make_float2(0.f, 0.f));
+                warp_arrive(bar + SB_W_FULL + (q & 1));
+                sum += all;
+            }
+            if (!REV && lane == 0 && p.total && blk.len > 0)
+                p.total[(int64_t)b * geo.H + h] = decay_ratio(decay_pair(sum), make_float2(0.f, 0.f));
         }
     } else if (warp >= 4 && warp < 8) {
         int q = 0;
@@ -287,24 +303,38 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
             if (blk.len <= 0) continue;
-            const int buf = q & 1;
-            ok = ab.wait(bar + SB_ACC_FULL + buf, (q >> 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
             float *dst = p.out + (int64_t)it * D * D + row;  // row: the value column
+            for (int p0 = 0; p0 < blk.len; p0 += kLinMaxBlock, ++q) {
+                const int buf = q & 1;
+                ok = __all_sync(0xffffffffu, ab.wait(bar + SB_ACC_FULL + buf, (q >> 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                // a later part joins the sum in memory (in L2: it is this CTA's own 64 KB), in fp32 sums that
+                // round, where the tensor core's would cut
+                const float f = join[q & 3], f_old = REV ? 1.f : f, f_new = REV ? f : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t x[32], y[32];
-                tmem_ld32(tmem + lanes + buf * 256 + c, x);
-                tmem_ld32(tmem + lanes + buf * 256 + 128 + c, y);
-                tmem_wait_ld();
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32(tmem + lanes + buf * 256 + c, x);
+                    tmem_ld32(tmem + lanes + buf * 256 + 128 + c, y);
+                    tmem_wait_ld();
+                    if (p0 == 0) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    dst[(c + e) * D] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
+                        for (int e = 0; e < 32; ++e)
+                            dst[(c + e) * D] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
+                    } else {
+                        float old[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) old[e] = dst[(c + e) * D];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            dst[(c + e) * D] =
+                                f_old * old[e] + f_new * (__uint_as_float(x[e]) + __uint_as_float(y[e]));
+                    }
+                }
+                tc_fence_before();
+                warp_arrive(bar + SB_ACC_EMPTY + buf);
             }
-            tc_fence_before();
-            warp_arrive(bar + SB_ACC_EMPTY + buf);
-            ++q;
         }
     } else if (warp >= 8) {
         const int t = (tid - 256) & 255, group = (tid - 256) >> 8;
@@ -313,44 +343,46 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const LinBlock blk = lin_block(geo, geo.by_heads.div(it));
             if (blk.len <= 0) continue;
-            ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1));
-            const float *w = wts + (q & 1) * kLinMaxBlock;
-            for (int t0 = 0; t0 < blk.len && ok; t0 += ST_TOK, ++n) {
-                const int s = n % ST_STAGES, rows = blk.len - t0;
-                if ((n & 1) != group) continue;
-                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + SB_FULL + n % 6, (n / 6) & 1)))) break;
-                unsigned char *st = sm + s * ST_STAGE;
-                uint4 v[4];
-                float f[4];
+            for (int p0 = 0; p0 < blk.len && ok; p0 += kLinMaxBlock, ++q) {
+                ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_FULL + (q & 1), (q >> 1) & 1));
+                const float *w = wts + (q & 1) * kLinMaxBlock;
+                const int end = min(blk.len, p0 + kLinMaxBlock);
+                for (int t0 = p0; t0 < end && ok; t0 += ST_TOK, ++n) {
+                    const int s = n % ST_STAGES, rows = blk.len - t0;
+                    if ((n & 1) != group) continue;
+                    if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + SB_FULL + n % 6, (n / 6) & 1)))) break;
+                    unsigned char *st = sm + s * ST_STAGE;
+                    uint4 v[4];
+                    float f[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // rows 16 i + t / 16, channels 8 (t % 16) ..
-                    v[i] = *reinterpret_cast<const uint4 *>(st + off + i * 2048);
-                    f[i] = w[t0 + 16 * i + (t >> 4)];
-                }
-                if (rows < ST_TOK) {  // past the block's end: neither operand may hold what lies there
+                    for (int i = 0; i < 4; ++i) {  // rows 16 i + t / 16, channels 8 (t % 16) ..
+                        v[i] = *reinterpret_cast<const uint4 *>(st + off + i * 2048);
+                        f[i] = w[t0 - p0 + 16 * i + (t >> 4)];
+                    }
+                    if (rows < ST_TOK) {  // past the block's end: neither operand may hold what lies there
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (16 * i + (t >> 4) >= rows) {
-                            v[i] = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off + i * 2048) = v[i];
-                        }
-                }
+                        for (int i = 0; i < 4; ++i)
+                            if (16 * i + (t >> 4) >= rows) {
+                                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<uint4 *>(st + 3 * ST_TILE + off + i * 2048) = v[i];
+                            }
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint4 h, m, l;
-                    split3(lo_f(v[i].x) * f[i], hi_f(v[i].x) * f[i], h.x, m.x, l.x);
-                    split3(lo_f(v[i].y) * f[i], hi_f(v[i].y) * f[i], h.y, m.y, l.y);
-                    split3(lo_f(v[i].z) * f[i], hi_f(v[i].z) * f[i], h.z, m.z, l.z);
-                    split3(lo_f(v[i].w) * f[i], hi_f(v[i].w) * f[i], h.w, m.w, l.w);
-                    *reinterpret_cast<uint4 *>(st + off + i * 2048) = h;
-                    *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = m;
-                    *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = l;
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 h, m, l;
+                        split3(lo_f(v[i].x) * f[i], hi_f(v[i].x) * f[i], h.x, m.x, l.x);
+                        split3(lo_f(v[i].y) * f[i], hi_f(v[i].y) * f[i], h.y, m.y, l.y);
+                        split3(lo_f(v[i].z) * f[i], hi_f(v[i].z) * f[i], h.z, m.z, l.z);
+                        split3(lo_f(v[i].w) * f[i], hi_f(v[i].w) * f[i], h.w, m.w, l.w);
+                        *reinterpret_cast<uint4 *>(st + off + i * 2048) = h;
+                        *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = m;
+                        *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = l;
+                    }
+                    fence_proxy_async();
+                    warp_arrive(bar + SB_CONV + s);
                 }
-                fence_proxy_async();
-                warp_arrive(bar + SB_CONV + s);
+                if (ok) warp_arrive(bar + SB_W_EMPTY + (q & 1));
             }
-            if (ok) warp_arrive(bar + SB_W_EMPTY + (q & 1));
-            ++q;
         }
     }
     __syncwarp();
@@ -364,10 +396,11 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
 }
 
 // ================================================================ joining the blocks
-// As lin_scan_kernel, with the states handed on as bf16 parts: the first one
-// is what the output kernels multiply with; PARTS = 3 keeps all 24 bits.
+// As lin_scan_kernel, with the states handed on as three bf16 parts (24 bits),
+// which the output kernel with row dots multiplies with; the first part alone
+// is the state rounded to bf16.
 constexpr int SC_THREADS = 256;
-template <bool REV, int PARTS>
+template <bool REV>
 __global__ void __launch_bounds__(SC_THREADS)
 lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__restrict__ total,
                    const float *__restrict__ s0, float *__restrict__ sT, float c, __nv_bfloat16 *__restrict__ parts,
@@ -382,7 +415,7 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
     float4 S = s0 ? reinterpret_cast<const float4 *>(s0)[nh * SIZE4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
     const float4 *p = reinterpret_cast<const float4 *>(own);
     const int count = last - first;
-    constexpr bool INNER = REV && PARTS == 3;  // <S, G> of every block: G is here, S in `other`
+    constexpr bool INNER = REV;  // <S, G> of every block: G is here, S in `other`
     constexpr int AHEAD = INNER ? 4 : 8;
     float4 x[AHEAD];
     float f[AHEAD];
@@ -418,10 +451,8 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
                 split3(S.z, S.w, a.y, b.y, d.y);
                 uint2 *o = reinterpret_cast<uint2 *>(parts) + at(i0 + u) * SIZE4 + e;
                 *o = a;
-                if (PARTS == 3) {
-                    o[part_stride / 4] = b;
-                    o[part_stride / 2] = d;
-                }
+                o[part_stride / 4] = b;
+                o[part_stride / 2] = d;
                 if (f[u] == 0.f) S = make_float4(0.f, 0.f, 0.f, 0.f);  // a reset, whatever the state held
                 S.x = f[u] * S.x + c * x[u].x;
                 S.y = f[u] * S.y + c * x[u].y;
@@ -877,6 +908,477 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
     }
 }
 
+// ================================================================ outputs, the state carried along
+// One item is a segment (a block of any length) and head. The state lives in
+// TMEM in fp32 and moves on by 128 tokens at a time, so a segment reads its
+// tokens once and no state goes through memory but the segment's first:
+//   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place;
+//   O = x Sb, Sb the state rounded to bf16; rows scaled by the decay from the
+//   chunk's edge; O += P z;
+//   S <- e^{L_end} S + (w y)^T z, w y in two bf16 parts (16 bits: the state in
+//   here only feeds bf16 products).
+// In reverse time (REV) the chunks go from the segment's end, the state is the
+// gradient after the chunk, and the mask and the decays are mirrored. ST: the
+// first state is read transposed. P, Sb and the result are the roundings to
+// bf16. Bound by memory; a 128-token chunk costs 40 tensor-core steps, and two
+// loops run from one chunk to the next, each to stay under the time that the
+// chunk's 128 KB take: S -> Sb, scale -> MMA -> S, and x Sb -> scale -> P z -> out.
+// Everything else of a chunk is done ahead of them: P (two in TMEM), its mask,
+// and y's two parts (the low one waits in registers for its 64-token buffer).
+//
+// warp 0: TMA of x and y (two tiles of 32 KB each); 1: MMA of P and O; 2: TMA of
+// z (one tile, its next one already in L2) and MMA of S; 3: prefix sums, four
+// chunks ahead; 4-11: rows of P and O, two threads a row; 12-19: y -> two parts
+// (the high one in place), and S -> Sb. Every barrier is waited on by its
+// waiters in every phase, and no phase comes twice between two waits (checked
+// with a model of the roles).
+constexpr int RL_TILE = 128 * D * 2;                 // 32 KB
+constexpr int RL_X = 0, RL_Y = 2 * RL_TILE, RL_Z = 4 * RL_TILE, RL_SB = 5 * RL_TILE, RL_LO = 6 * RL_TILE;
+constexpr int RL_A = RL_LO + RL_TILE / 2;            // prefix sums [4][130]
+constexpr int RL_COL = RL_A + 4 * 130 * 8;           // column factors [8 warps][64]
+constexpr int RL_BAR = RL_COL + 8 * 64 * 4;
+constexpr int RL_THREADS = 640;
+enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_FZ = 10, RB_EZ, RB_PR, RB_YD, RB_OIN, RB_OF, RB_OE, RB_SR,
+       RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF, RB_AE = RB_AF + 4, RB_COUNT = RB_AE + 4 };
+constexpr int RL_SMEM = RL_BAR + RB_COUNT * 8 + 16 + 1024;
+static_assert(RL_SMEM <= 232448, "shared memory of a block");
+
+struct RollTcArgs {
+    LinGeom geo;
+    const float *log_decay;
+    int decay;
+    const float *states;  // [block][head][128][128]
+    __nv_bfloat16 *out;
+    float c_state, c_intra, c_roll;  // c_roll: what y z products enter the state with
+    int items;
+};
+
+template <bool REV, bool ST>
+__global__ void __launch_bounds__(RL_THREADS, 1)
+lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                   const __grid_constant__ CUtensorMap mz) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + RL_BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + RB_COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const LinGeom &geo = p.geo;
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < RB_COUNT; ++i) {
+            uint32_t n = 1;
+            if (i == RB_EZ) n = 2;                                             // both MMA warps
+            if (i == RB_PR || i == RB_OE || i == RB_ZZ) n = 8;                 // the row warps
+            if (i == RB_SR || i == RB_SS || i == RB_KC) n = 8;                 // the state warps
+            if (i >= RB_AE) n = 16;                                            // both
+            mbar_init(bar + i, n);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm;  // S | O | P, two of them
+    bool ok = true;
+    // g: chunks so far over all items; a walk goes through them in order
+    struct Walk {
+        LinBlock blk;
+        int it, h, n, c;  // item, head, chunks of the item, chunk
+    };
+    auto enter = [&](Walk &x) {  // the first chunk of the first item from x.it on that has one
+        for (; x.it < p.items; x.it += gridDim.x) {
+            const int b = geo.by_heads.div(x.it);
+            x.h = x.it - b * geo.H;
+            x.blk = lin_block(geo, b);
+            x.n = (x.blk.len + 127) / 128;
+            x.c = 0;
+            if (x.n > 0) return;
+        }
+    };
+    auto start = [&]() {
+        Walk x;
+        x.it = blockIdx.x;
+        enter(x);
+        return x;
+    };
+    auto more = [&](const Walk &x) { return x.it < p.items; };
+    auto next = [&](Walk &x) {
+        if (++x.c < x.n) return;
+        x.it += gridDim.x;
+        enter(x);
+    };
+    auto first_token = [&](const Walk &x) { return (REV ? x.n - 1 - x.c : x.c) * 128; };
+    auto tile = [&](const CUtensorMap *m, unsigned char *d, uint64_t *full, const Walk &x) {
+        mbar_arrive_expect_tx(full, RL_TILE);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                tma_load_3d(d + c * 16384 + t * 8192, m, full, 64 * c, x.h, x.blk.start + first_token(x) + 64 * t);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int g = 0;
+            for (Walk x = start(); more(x); next(x), ++g) {
+                const int s = g & 1;
+                const uint32_t ph = ((g >> 1) & 1) ^ 1;
+                if (!(ok = ab.wait(bar + RB_EX + s, ph))) break;
+                tile(&mx, sm + RL_X + s * RL_TILE, bar + RB_FX + s, x);
+                if (!(ok = ab.wait(bar + RB_EY + s, ph))) break;
+                tile(&my, sm + RL_Y + s * RL_TILE, bar + RB_FY + s, x);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        tma_prefetch_3d(&mz, 64 * c, x.h, x.blk.start + first_token(x) + 64 * t);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t I_P = idesc_bf16(128, 128, false, false), I_O = idesc_bf16(128, 128, false, true);
+            const uint64_t sd = desc_mn(smem_u32(sm + RL_SB), 16384), zd = desc_mn(smem_u32(sm + RL_Z), 16384);
+            const uint32_t to = tmem + 128;
+            auto scores = [&](const Walk &x, int g) {
+                const int s = g & 1;
+                const uint32_t ph = (g >> 1) & 1, tp = tmem + 256 + 128 * s;
+                if (!(ok = ab.wait(bar + RB_FX + s, ph) && ab.wait(bar + RB_FY + s, ph))) return;
+                tc_fence_after();
+                const uint64_t xd = desc_k(smem_u32(sm + RL_X + s * RL_TILE)),
+                               yd = desc_k(smem_u32(sm + RL_Y + s * RL_TILE));
+                mma_ss<false>(tp, xd, yd, I_P);
+#pragma unroll
+                for (int ks = 1; ks < 8; ++ks) mma_ss<true>(tp, xd + step_k(ks, 16384), yd + step_k(ks, 16384), I_P);
+                umma_commit(bar + RB_PF + s);
+                umma_commit(bar + (x.c == x.n - 1 ? RB_EY + s : RB_YD));  // the last chunk's y makes no state
+            };
+            int g = 0;
+            Walk ahead = start();
+            if (more(ahead)) {
+                scores(ahead, 0);
+                next(ahead);
+            }
+            for (Walk x = start(); more(x) && ok; next(x), ++g) {
+                const int s = g & 1;
+                if (!(ok = ab.wait(bar + RB_SR, g & 1) && ab.wait(bar + RB_OE, (g & 1) ^ 1))) break;
+                tc_fence_after();
+                const uint64_t xd = desc_k(smem_u32(sm + RL_X + s * RL_TILE));
+                mma_ss<false>(to, xd, sd, I_O);
+#pragma unroll
+                for (int ks = 1; ks < 8; ++ks) mma_ss<true>(to, xd + step_k(ks, 16384), sd + step_mn(ks), I_O);
+                umma_commit(bar + RB_OIN);
+                umma_commit(bar + RB_SBF);
+                umma_commit(bar + RB_EX + s);
+                if (more(ahead)) {
+                    scores(ahead, g + 1);
+                    if (!ok) break;
+                    next(ahead);
+                }
+                if (!(ok = ab.wait(bar + RB_FZ, g & 1) && ab.wait(bar + RB_PR, g & 1))) break;
+                tc_fence_after();
+                const uint32_t tp = tmem + 256 + 128 * s;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)  // each half of P's columns lies in the front of its 64
+                    umma_bf16_ts(to, tp + (ks >> 2) * 64 + (ks & 3) * 8, zd + step_mn(ks), I_O);
+                umma_commit(bar + RB_OF);
+                umma_commit(bar + RB_EZ);
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            constexpr uint32_t I_S = idesc_bf16(128, 128, true, true);
+            const uint64_t lo = desc_mn(smem_u32(sm + RL_LO), 8192), zd = desc_mn(smem_u32(sm + RL_Z), 16384);
+            int g = 0, m = 0, zz = 0;
+            for (Walk x = start(); more(x); next(x), ++g) {
+                const int s = g & 1;
+                if (!(ok = ab.wait(bar + RB_EZ, (g & 1) ^ 1))) break;  // z's one slot is this warp's to fill
+                tile(&mz, sm + RL_Z, bar + RB_FZ, x);
+                if (!(ok = ab.wait(bar + RB_FZ, g & 1))) break;
+                if (x.c == x.n - 1) {
+                    mbar_arrive(bar + RB_EZ);
+                    continue;
+                }
+                // the segment's ragged end (first in reverse): its rows past the end are zeroed first
+                if (x.blk.len - first_token(x) < 128 && !(ok = ab.wait(bar + RB_ZZ, zz++ & 1))) break;
+                if (!(ok = ab.wait(bar + RB_SS, m & 1))) break;
+                const uint64_t yd = desc_mn(smem_u32(sm + RL_Y + s * RL_TILE), 16384);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok = ab.wait(bar + RB_KC, h))) break;
+                    tc_fence_after();
+                    constexpr uint64_t ROWS64 = 8192 >> 4;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        mma_ss<true>(tmem, lo + step_mn(ks), zd + h * ROWS64 + step_mn(ks), I_S);
+                        mma_ss<true>(tmem, yd + h * ROWS64 + step_mn(ks), zd + h * ROWS64 + step_mn(ks), I_S);
+                    }
+                    umma_commit(bar + RB_LOF);
+                }
+                if (!ok) break;
+                umma_commit(bar + RB_SF);
+                umma_commit(bar + RB_EY + s);
+                umma_commit(bar + RB_EZ);
+                ++m;
+            }
+        }
+    } else if (warp == 3) {
+        int g = 0;
+        for (Walk x = start(); more(x); next(x), ++g) {
+            const int t0 = first_token(x);
+            const LinBlock part{x.blk.seq, x.blk.start + t0, min(128, x.blk.len - t0)};
+            long long sums[4];
+            warp_decay<4>(geo, p.log_decay, p.decay, part, x.h, sums);
+            ok = __all_sync(0xffffffffu, ab.wait(bar + RB_AE + (g & 3), ((g >> 2) & 1) ^ 1));
+            if (!ok) break;
+            float2 *a = reinterpret_cast<float2 *>(sm + RL_A) + (g & 3) * 130;
+            if (lane == 0) a[0] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) a[lane * 4 + u + 1] = decay_pair(sums[u]);
+            warp_arrive(bar + RB_AF + (g & 3));
+        }
+    } else if (warp < 12) {  // rows of P and O
+        const int hf = (warp - 4) >> 2, w = warp & 3, r = 32 * w + lane, i32 = 32 * w;
+        float *col = reinterpret_cast<float *>(sm + RL_COL) + (warp - 4) * 64;
+        const uint32_t tl = tmem + ((uint32_t)w << 21), to = tl + 128 + 64 * hf;
+        auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
+        // P of chunk g to bf16; returns the factor of its rows' state part
+        auto mask = [&](const Walk &x, int g) -> float {
+            const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
+            const uint32_t tp = tl + 256 + 128 * s + 64 * hf;
+            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) return 0.f;
+            const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
+            const float2 ai = a[r + 1], edge = a[REV ? i32 + 32 : i32], zero = make_float2(0.f, 0.f);
+            const float f = p.c_state * (REV ? decay_ratio(a[128], ai) : decay_ratio(ai, zero));
+            // row and column factors, as in the kernel above
+            const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = 64 * hf + 32 * u + lane;
+                col[32 * u + lane] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
+                                         : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
+            }
+            __syncwarp();
+            if (!wait(RB_PF + s, (g >> 1) & 1)) return 0.f;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32], o[16];
+                const int jc = 64 * hf + 32 * u;
+                if (REV ? jc < i32 || jc >= rows : jc > i32) {  // outside the mask
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                    tmem_st16(tp + 16 * u, o);
+                    continue;
+                }
+                tmem_ld32(tp + 32 * u, v);
+                tmem_wait_ld();
+                if (jc != i32 && (!REV || jc + 32 <= rows)) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 cf = *reinterpret_cast<const float4 *>(col + 32 * u + e);
+                        o[e / 2] = pack2(rf * cf.x * __uint_as_float(v[e]), rf * cf.y * __uint_as_float(v[e + 1]));
+                        o[e / 2 + 1] =
+                            pack2(rf * cf.z * __uint_as_float(v[e + 2]), rf * cf.w * __uint_as_float(v[e + 3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float y[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = jc + e + k;
+                            const float d = REV ? decay_ratio(a[j + 1], ai) : decay_ratio(ai, a[j + 1]);
+                            const bool in = j < rows && (REV ? j >= r : j <= r);
+                            y[k] = in ? p.c_intra * d * __uint_as_float(v[e + k]) : 0.f;
+                        }
+                        o[e / 2] = pack2(y[0], y[1]);
+                    }
+                }
+                tmem_st16(tp + 16 * u, o);
+            }
+            tmem_wait_st();
+            warp_arrive(bar + RB_AE + (g & 3));
+            return f;
+        };
+        int g = 0;
+        Walk x = start(), ahead = x;
+        float f = 0.f;
+        if (more(ahead)) {
+            f = mask(ahead, 0);
+            next(ahead);
+        }
+        for (; more(x) && ok; next(x), ++g) {
+            const int t0 = first_token(x), rows = min(128, x.blk.len - t0);
+            if (!wait(RB_OIN, g & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32];
+                tmem_ld32(to + 32 * u, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[e]));  // a reset drops the state
+                tmem_st32(to + 32 * u, v);
+            }
+            if (rows < 128) {  // what lies past the segment's end must not meet zeros
+                if (!wait(RB_FZ, g & 1)) break;
+                if (r >= rows) {
+                    unsigned char *z = sm + RL_Z + hf * 16384 + r * 128;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                if (x.c < x.n - 1) warp_arrive(bar + RB_ZZ);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(bar + RB_PR);
+            if (more(ahead)) {
+                f = mask(ahead, g + 1);
+                if (!ok) break;
+                next(ahead);
+            }
+            if (!wait(RB_OF, g & 1)) break;
+            tc_fence_after();
+            __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + t0 + r) * geo.H + x.h) * D + 64 * hf;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32];
+                tmem_ld32(to + 32 * u, v);
+                tmem_wait_ld();
+                if (r < rows) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = pack2(__uint_as_float(v[16 * k + 2 * e]), __uint_as_float(v[16 * k + 2 * e + 1]));
+                        st_v8(dst + 32 * u + 16 * k, o);
+                    }
+                }
+            }
+            tc_fence_before();
+            warp_arrive(bar + RB_OE);
+        }
+    } else {  // y -> two parts, S -> Sb
+        const int hf = (warp - 12) >> 2, w = warp & 3, r = 32 * w + lane, t = tid - 384, c8 = t & 15;
+        const uint32_t ts = tmem + ((uint32_t)w << 21) + 64 * hf;
+        auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
+        int g = 0, m = 0;
+        for (Walk x = start(); more(x); next(x), ++g) {
+            const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
+            const bool last = x.c == x.n - 1;
+            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) break;
+            const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
+            const float2 end = a[128], zero = make_float2(0.f, 0.f);
+            const float fs = decay_ratio(end, zero);
+            uint4 lo[2][4];  // the low parts of this thread's pieces of both halves
+            auto put_low = [&](int h) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(sm + RL_LO + kmajor_chunk(16 * i + (t >> 4), c8, 64)) = lo[h][i];
+                fence_proxy_async();
+                warp_arrive(bar + RB_KC);
+            };
+            if (!last) {
+                if (!wait(RB_YD, m & 1)) break;
+                unsigned char *y = sm + RL_Y + s * RL_TILE;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4 v[4];
+                    float f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 64 * h + 16 * i + (t >> 4);
+                        v[i] = *reinterpret_cast<const uint4 *>(y + kmajor_chunk(row, c8, 128));
+                        f[i] = p.c_roll * (REV ? decay_ratio(a[row + 1], zero) : decay_ratio(end, a[row + 1]));
+                        if (row >= rows) v[i] = make_uint4(0u, 0u, 0u, 0u);  // past the segment's end
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t hi[4], l[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x0 = lo_f(in[e]) * f[i], x1 = hi_f(in[e]) * f[i];
+                            hi[e] = pack2(x0, x1);
+                            l[e] = pack2(x0 - lo_f(hi[e]), x1 - hi_f(hi[e]));
+                        }
+                        *reinterpret_cast<uint4 *>(y + kmajor_chunk(64 * h + 16 * i + (t >> 4), c8, 128)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        lo[h][i] = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                }
+                if (m > 0 && !wait(RB_LOF, 1)) break;  // the state's last products have read the buffer
+                put_low(0);
+            }
+            // the state before this chunk: to bf16 for O, and on by the chunk's decay for S
+            if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
+            if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
+            tc_fence_after();
+            const float *S0 = p.states + (int64_t)x.it * D * D;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32];
+                if (x.c > 0) {
+                    tmem_ld32(ts + 32 * u, v);
+                    tmem_wait_ld();
+                } else if (ST) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
+                        v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
+                        v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
+                    }
+                }
+                unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack2(__uint_as_float(v[8 * k + 2 * e]), __uint_as_float(v[8 * k + 2 * e + 1]));
+                    *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                if (!last) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = fs == 0.f ? 0u : __float_as_uint(fs * __uint_as_float(v[e]));
+                    tmem_st32(ts + 32 * u, v);
+                }
+            }
+            fence_proxy_async();
+            tmem_wait_st();
+            tc_fence_before();
+            if (!last) warp_arrive(bar + RB_SS);
+            warp_arrive(bar + RB_SR);
+            if (!last) {
+                if (!wait(RB_LOF, 0)) break;
+                put_low(1);
+                ++m;
+            }
+            warp_arrive(bar + RB_AE + (g & 3));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -941,13 +1443,28 @@ cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan_tc(const LinGeom &geo, bool rev, int parts, const float *own, const float *total,
+cudaError_t launch_scan_tc(const LinGeom &geo, bool rev, const float *own, const float *total,
                            const float *s0, float *sT, float c, void *out, int64_t part_stride, const void *other,
                            float *inner, cudaStream_t s) {
-    auto k = rev ? (parts == 3 ? lin_scan_tc_kernel<true, 3> : lin_scan_tc_kernel<true, 1>)
-                 : (parts == 3 ? lin_scan_tc_kernel<false, 3> : lin_scan_tc_kernel<false, 1>);
+    auto k = rev ? lin_scan_tc_kernel<true> : lin_scan_tc_kernel<false>;
     k<<<(unsigned)((int64_t)geo.N * geo.H * (D * D / 4 / SC_THREADS)), SC_THREADS, 0, s>>>(
         geo, own, total, s0, sT, c, (__nv_bfloat16 *)out, part_stride, (const __nv_bfloat16 *)other, inner);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_roll_tc(const RollTc &a, cudaStream_t s) {
+    const LinGeom &geo = a.geo;
+    CUtensorMap mx, my, mz;
+    if (!token_map(&mx, a.x, a.x_stride, geo.H, a.tokens) || !token_map(&my, a.y, a.y_stride, geo.H, a.tokens) ||
+        !token_map(&mz, a.z, a.z_stride, geo.H, a.tokens))
+        return cudaErrorInvalidValue;
+    RollTcArgs p{geo, a.log_decay, a.decay, a.states, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.c_roll,
+                 geo.nblocks * geo.H};
+    auto k = a.rev ? (a.state_t ? lin_roll_tc_kernel<true, true> : lin_roll_tc_kernel<true, false>)
+                   : (a.state_t ? lin_roll_tc_kernel<false, true> : lin_roll_tc_kernel<false, false>);
+    static std::atomic<uint64_t> allowed[4];
+    KDA_TRY(allow_smem(k, RL_SMEM, allowed[a.rev * 2 + a.state_t]));
+    k<<<min(p.items, sm_count()), RL_THREADS, RL_SMEM, s>>>(p, mx, my, mz);
     return cudaGetLastError();
 }
 
@@ -964,14 +1481,12 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
     if (dots && !token_map(&mw, a.w, a.w_stride, geo.H, a.tokens)) return cudaErrorInvalidValue;
     AttendTcArgs p{geo, a.log_decay, a.decay, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.dot, a.dot_state,
                    a.tokens * geo.H, (int)rows, geo.nblocks * geo.H * 2};
-    auto k = !a.rev ? (!a.state_t ? lin_attend_tc_kernel<false, false, false>
-                       : dots     ? lin_attend_tc_kernel<false, true, true>
-                                  : lin_attend_tc_kernel<false, true, false>)
-                    : (!a.state_t ? lin_attend_tc_kernel<true, false, false>
-                       : dots     ? lin_attend_tc_kernel<true, true, true>
-                                  : lin_attend_tc_kernel<true, true, false>);
-    static std::atomic<uint64_t> allowed[8];
-    KDA_TRY(allow_smem(k, AT_SMEM, allowed[a.rev * 4 + a.state_t * 2 + dots]));
+    if (dots != a.state_t) return cudaErrorInvalidValue;  // what the backward asks for: dq, dk with dots, dv without
+    auto k = !a.rev ? lin_attend_tc_kernel<false, true, true>
+             : dots ? lin_attend_tc_kernel<true, true, true>
+                    : lin_attend_tc_kernel<true, false, false>;
+    static std::atomic<uint64_t> allowed[4];
+    KDA_TRY(allow_smem(k, AT_SMEM, allowed[a.rev * 2 + dots]));
     k<<<min(p.items, sm_count()), AT_THREADS, AT_SMEM, s>>>(p, mx, my, mz, ms, mw);
     return cudaGetLastError();
 }
