@@ -8,6 +8,34 @@
 
 namespace kda {
 
+// Two fp32 values, one instruction for both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+    float x, y;
+    f2_get(a, x, y);
+    return x + y;
+}
+
 // n / d by a multiplication, for 0 <= n < 2^31: with l = ceil(log2 d) and
 // m = floor(2^(31 + l) / d) + 1 <= 2^32, the error (m d - 2^(31 + l)) n / (d 2^(31 + l))
 // stays below 1 / d. (The divisions of a work item's number sat in front of

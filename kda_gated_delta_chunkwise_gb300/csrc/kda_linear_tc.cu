@@ -60,12 +60,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ F2 pair_f(uint32_t x) { return f2(lo_f(x), hi_f(x)); }  // two bf16
+__device__ __forceinline__ F2 pair_w(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint32_t pack2(F2 x) {
+    float a, b;
+    f2_get(x, a, b);
+    return pack2(a, b);
+}
+__device__ __forceinline__ F2 minus(F2 x, F2 y) { return fma2(y, f2(-1.f, -1.f), x); }
 // x = h + m + l, each a bf16 (24 bits of x kept), two values at a time.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l) {
-    h = pack2(x0, x1);
-    x0 -= lo_f(h), x1 -= hi_f(h);
-    m = pack2(x0, x1);
-    l = pack2(x0 - lo_f(m), x1 - hi_f(m));
+__device__ __forceinline__ void split3(F2 x, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = pack2(x);
+    x = minus(x, pair_f(h));
+    m = pack2(x);
+    l = pack2(minus(x, pair_f(m)));
+}
+// v *= f, 32 accumulator columns; f = 0 (a reset) leaves zeros whatever v held.
+__device__ __forceinline__ void scale32(uint32_t (&v)[32], float f) {
+    if (__any_sync(0xffffffffu, f == 0.f)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = f == 0.f ? 0u : v[e];
+    }
+    const F2 ff = f2(f, f);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float a, b;
+        f2_get(pair_w(v[e], v[e + 1]) * ff, a, b);
+        v[e] = __float_as_uint(a), v[e + 1] = __float_as_uint(b);
+    }
 }
 __device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {  // one 32-byte sector
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -370,10 +392,11 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint4 h, m, l;
-                        split3(lo_f(v[i].x) * f[i], hi_f(v[i].x) * f[i], h.x, m.x, l.x);
-                        split3(lo_f(v[i].y) * f[i], hi_f(v[i].y) * f[i], h.y, m.y, l.y);
-                        split3(lo_f(v[i].z) * f[i], hi_f(v[i].z) * f[i], h.z, m.z, l.z);
-                        split3(lo_f(v[i].w) * f[i], hi_f(v[i].w) * f[i], h.w, m.w, l.w);
+                        const F2 ff = f2(f[i], f[i]);
+                        split3(pair_f(v[i].x) * ff, h.x, m.x, l.x);
+                        split3(pair_f(v[i].y) * ff, h.y, m.y, l.y);
+                        split3(pair_f(v[i].z) * ff, h.z, m.z, l.z);
+                        split3(pair_f(v[i].w) * ff, h.w, m.w, l.w);
                         *reinterpret_cast<uint4 *>(st + off + i * 2048) = h;
                         *reinterpret_cast<uint4 *>(st + ST_TILE + off + i * 2048) = m;
                         *reinterpret_cast<uint4 *>(st + 2 * ST_TILE + off + i * 2048) = l;
@@ -447,8 +470,8 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
                         inner[at(i0 + u) * kScanPartials + (blockIdx.x % PER) * (SC_THREADS / 32) + (threadIdx.x >> 5)] = v;
                 }
                 uint2 a, b, d;
-                split3(S.x, S.y, a.x, b.x, d.x);
-                split3(S.z, S.w, a.y, b.y, d.y);
+                split3(f2(S.x, S.y), a.x, b.x, d.x);
+                split3(f2(S.z, S.w), a.y, b.y, d.y);
                 uint2 *o = reinterpret_cast<uint2 *>(parts) + at(i0 + u) * SIZE4 + e;
                 *o = a;
                 o[part_stride / 4] = b;
@@ -769,6 +792,8 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                                          : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
             }
             __syncwarp();
+            const F2 rf2 = f2(rf, rf);
+            F2 dots = f2(0.f, 0.f);
             float dot = 0.f, dot_state = 0.f;
             if (DOTS && !wait(ld.bar(n + NS + 1), ld.parity(n + NS + 1))) break;
             if (!wait(bar + AB_O_IN + c, q & 1)) break;
@@ -780,9 +805,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 tmem_wait_ld();
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        v[u][e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[u][e]));  // a reset drops S
+                    scale32(v[u], f);
                     tmem_st32(to + 64 * hf + 32 * u, v[u]);
                     if (DOTS) {
                         const unsigned char *wt = sm + ((n + NS + 1) % AT_SLOTS) * AT_SLOT;
@@ -832,15 +855,14 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 cf = *reinterpret_cast<const float4 *>(
                                     col + j * 64 + sub * HSUB + 32 * u + e);
-                                const float y0 = rf * cf.x * __uint_as_float(v[e]);
-                                const float y1 = rf * cf.y * __uint_as_float(v[e + 1]);
-                                const float y2 = rf * cf.z * __uint_as_float(v[e + 2]);
-                                const float y3 = rf * cf.w * __uint_as_float(v[e + 3]);
-                                if (DOTS)
-                                    dot += y0 * __uint_as_float(v2[e]) + y1 * __uint_as_float(v2[e + 1]) +
-                                           y2 * __uint_as_float(v2[e + 2]) + y3 * __uint_as_float(v2[e + 3]);
-                                o[e / 2] = pack2(y0, y1);
-                                o[e / 2 + 1] = pack2(y2, y3);
+                                const F2 y0 = pair_w(v[e], v[e + 1]) * f2(cf.x, cf.y) * rf2;
+                                const F2 y1 = pair_w(v[e + 2], v[e + 3]) * f2(cf.z, cf.w) * rf2;
+                                if (DOTS) {
+                                    dots = fma2(y0, pair_w(v2[e], v2[e + 1]), dots);
+                                    dots = fma2(y1, pair_w(v2[e + 2], v2[e + 3]), dots);
+                                }
+                                o[e / 2] = pack2(y0);
+                                o[e / 2 + 1] = pack2(y1);
                             }
                         } else {
 #pragma unroll
@@ -869,7 +891,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             warp_arrive(bar + AB_A_EMPTY + slot);
             if (DOTS && i < len) {
                 const int64_t at = (int64_t)(x.blk.start + i) * geo.H + x.h;
-                p.dot[hf * p.dot_stride + at] = dot + dot_state;
+                p.dot[hf * p.dot_stride + at] = dot + f2_sum(dots) + dot_state;
                 if (p.dot_state) p.dot_state[hf * p.dot_stride + at] = dot_state;
             }
             if (!wait(bar + AB_O_FULL + c, q & 1)) break;
@@ -1156,6 +1178,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const float f = p.c_state * (REV ? decay_ratio(a[128], ai) : decay_ratio(ai, zero));
             // row and column factors, as in the kernel above
             const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
+            const F2 rf2 = f2(rf, rf);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int j = 64 * hf + 32 * u + lane;
@@ -1165,41 +1188,46 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             __syncwarp();
             if (!wait(RB_PF + s, (g >> 1) & 1)) return 0.f;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                uint32_t v[32], o[16];
                 const int jc = 64 * hf + 32 * u;
                 if (REV ? jc < i32 || jc >= rows : jc > i32) {  // outside the mask
+                    uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0u;
                     tmem_st16(tp + 16 * u, o);
-                    continue;
-                }
-                tmem_ld32(tp + 32 * u, v);
-                tmem_wait_ld();
-                if (jc != i32 && (!REV || jc + 32 <= rows)) {
+                } else if (jc != i32 && (!REV || jc + 32 <= rows)) {
+                    uint32_t v[32], o[16];
+                    tmem_ld32(tp + 32 * u, v);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 cf = *reinterpret_cast<const float4 *>(col + 32 * u + e);
-                        o[e / 2] = pack2(rf * cf.x * __uint_as_float(v[e]), rf * cf.y * __uint_as_float(v[e + 1]));
-                        o[e / 2 + 1] =
-                            pack2(rf * cf.z * __uint_as_float(v[e + 2]), rf * cf.w * __uint_as_float(v[e + 3]));
+                        o[e / 2] = pack2(pair_w(v[e], v[e + 1]) * f2(cf.x, cf.y) * rf2);
+                        o[e / 2 + 1] = pack2(pair_w(v[e + 2], v[e + 3]) * f2(cf.z, cf.w) * rf2);
                     }
+                    tmem_st16(tp + 16 * u, o);
                 } else {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {  // 8 columns into 4, behind the reads
+                        uint32_t v[8], o[4];
+                        tmem_ld8(tp + 32 * u + 8 * q, v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float y[2];
+                        for (int e = 0; e < 8; e += 2) {
+                            float y[2];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = jc + e + k;
-                            const float d = REV ? decay_ratio(a[j + 1], ai) : decay_ratio(ai, a[j + 1]);
-                            const bool in = j < rows && (REV ? j >= r : j <= r);
-                            y[k] = in ? p.c_intra * d * __uint_as_float(v[e + k]) : 0.f;
+                            for (int k = 0; k < 2; ++k) {
+                                const int j = jc + 8 * q + e + k;
+                                const float d = REV ? decay_ratio(a[j + 1], ai) : decay_ratio(ai, a[j + 1]);
+                                const bool in = j < rows && (REV ? j >= r : j <= r);
+                                y[k] = in ? p.c_intra * d * __uint_as_float(v[e + k]) : 0.f;
+                            }
+                            o[e / 2] = pack2(y[0], y[1]);
                         }
-                        o[e / 2] = pack2(y[0], y[1]);
+                        tmem_st4(tp + 16 * u + 4 * q, o);
                     }
                 }
-                tmem_st16(tp + 16 * u, o);
             }
             tmem_wait_st();
             warp_arrive(bar + RB_AE + (g & 3));
@@ -1216,14 +1244,12 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const int t0 = first_token(x), rows = min(128, x.blk.len - t0);
             if (!wait(RB_OIN, g & 1)) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 uint32_t v[32];
                 tmem_ld32(to + 32 * u, v);
                 tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[e] = f == 0.f ? 0u : __float_as_uint(f * __uint_as_float(v[e]));  // a reset drops the state
+                scale32(v, f);
                 tmem_st32(to + 32 * u, v);
             }
             if (rows < 128) {  // what lies past the segment's end must not meet zeros
@@ -1247,7 +1273,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             if (!wait(RB_OF, g & 1)) break;
             tc_fence_after();
             __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + t0 + r) * geo.H + x.h) * D + 64 * hf;
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 uint32_t v[32];
                 tmem_ld32(to + 32 * u, v);
@@ -1278,19 +1304,12 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
             const float2 end = a[128], zero = make_float2(0.f, 0.f);
             const float fs = decay_ratio(end, zero);
-            uint4 lo[2][4];  // the low parts of this thread's pieces of both halves
-            auto put_low = [&](int h) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(sm + RL_LO + kmajor_chunk(16 * i + (t >> 4), c8, 64)) = lo[h][i];
-                fence_proxy_async();
-                warp_arrive(bar + RB_KC);
-            };
-            if (!last) {
-                if (!wait(RB_YD, m & 1)) break;
-                unsigned char *y = sm + RL_Y + s * RL_TILE;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+            unsigned char *y = sm + RL_Y + s * RL_TILE;
+            if (!last && !wait(RB_YD, m & 1)) break;
+            // (loops that stay loops: the roles' code together has to fit the instruction cache)
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (!last) {  // 64 tokens of y, scaled: the high part in place, the low one to its buffer
                     uint4 v[4];
                     float f[4];
 #pragma unroll
@@ -1306,66 +1325,68 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                         uint32_t hi[4], l[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float x0 = lo_f(in[e]) * f[i], x1 = hi_f(in[e]) * f[i];
-                            hi[e] = pack2(x0, x1);
-                            l[e] = pack2(x0 - lo_f(hi[e]), x1 - hi_f(hi[e]));
+                            const F2 xw = pair_f(in[e]) * f2(f[i], f[i]);
+                            hi[e] = pack2(xw);
+                            l[e] = pack2(minus(xw, pair_f(hi[e])));
                         }
                         *reinterpret_cast<uint4 *>(y + kmajor_chunk(64 * h + 16 * i + (t >> 4), c8, 128)) =
                             make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        lo[h][i] = make_uint4(l[0], l[1], l[2], l[3]);
+                        v[i] = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                    // the products with the buffer's last contents are done
+                    if (2 * m + h > 0 && !wait(RB_LOF, (h + 1) & 1)) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(sm + RL_LO + kmajor_chunk(16 * i + (t >> 4), c8, 64)) = v[i];
+                    fence_proxy_async();
+                    warp_arrive(bar + RB_KC);
+                }
+                if (h == 1) break;
+                // the state before this chunk: to bf16 for O, and on by the chunk's decay for S
+                if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
+                if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
+                tc_fence_after();
+                const float *S0 = p.states + (int64_t)x.it * D * D;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t v[32];
+                    if (x.c > 0) {
+                        tmem_ld32(ts + 32 * u, v);
+                        tmem_wait_ld();
+                    } else if (ST) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
+                            v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
+                            v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
+                        }
+                    }
+                    unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = pack2(pair_w(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                        *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    if (!last) {
+                        scale32(v, fs);
+                        tmem_st32(ts + 32 * u, v);
                     }
                 }
-                if (m > 0 && !wait(RB_LOF, 1)) break;  // the state's last products have read the buffer
-                put_low(0);
+                fence_proxy_async();
+                tmem_wait_st();
+                tc_fence_before();
+                if (!last) warp_arrive(bar + RB_SS);
+                warp_arrive(bar + RB_SR);
             }
-            // the state before this chunk: to bf16 for O, and on by the chunk's decay for S
-            if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
-            if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
-            tc_fence_after();
-            const float *S0 = p.states + (int64_t)x.it * D * D;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t v[32];
-                if (x.c > 0) {
-                    tmem_ld32(ts + 32 * u, v);
-                    tmem_wait_ld();
-                } else if (ST) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
-                        v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
-                        v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
-                    }
-                }
-                unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = pack2(__uint_as_float(v[8 * k + 2 * e]), __uint_as_float(v[8 * k + 2 * e + 1]));
-                    *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-                if (!last) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        v[e] = fs == 0.f ? 0u : __float_as_uint(fs * __uint_as_float(v[e]));
-                    tmem_st32(ts + 32 * u, v);
-                }
-            }
-            fence_proxy_async();
-            tmem_wait_st();
-            tc_fence_before();
-            if (!last) warp_arrive(bar + RB_SS);
-            warp_arrive(bar + RB_SR);
-            if (!last) {
-                if (!wait(RB_LOF, 0)) break;
-                put_low(1);
-                ++m;
-            }
+            if (!ok) break;
+            if (!last) ++m;
             warp_arrive(bar + RB_AE + (g & 3));
         }
     }
