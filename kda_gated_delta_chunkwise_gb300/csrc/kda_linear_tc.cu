@@ -951,7 +951,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // warp 0: TMA of x and y (two tiles of 32 KB each); 1: MMA of P and O; 2: TMA of
 // z (one tile, its next one already in L2) and MMA of S; 3: prefix sums, four
 // chunks ahead; 4-11: rows of P and O, two threads a row; 12-19: y -> two parts
-// (the high one in place), and S -> Sb. Every barrier is waited on by its
+// (the high one in place); 20-27: S -> Sb. Every barrier is waited on by its
 // waiters in every phase, and no phase comes twice between two waits (checked
 // with a model of the roles).
 constexpr int RL_TILE = 128 * D * 2;                 // 32 KB
@@ -959,9 +959,9 @@ constexpr int RL_X = 0, RL_Y = 2 * RL_TILE, RL_Z = 4 * RL_TILE, RL_SB = 5 * RL_T
 constexpr int RL_A = RL_LO + RL_TILE / 2;            // prefix sums [4][130]
 constexpr int RL_COL = RL_A + 4 * 130 * 8;           // column factors [8 warps][64]
 constexpr int RL_BAR = RL_COL + 8 * 64 * 4;
-constexpr int RL_THREADS = 640;
-enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_FZ = 10, RB_EZ, RB_PR, RB_YD, RB_OIN, RB_OF, RB_OE, RB_SR,
-       RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF, RB_AE = RB_AF + 4, RB_COUNT = RB_AE + 4 };
+constexpr int RL_THREADS = 896;
+enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_YD = 10, RB_FZ = 12, RB_EZ, RB_PR, RB_OIN, RB_OF, RB_OE,
+       RB_SR, RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF, RB_AE = RB_AF + 4, RB_COUNT = RB_AE + 4 };
 constexpr int RL_SMEM = RL_BAR + RB_COUNT * 8 + 16 + 1024;
 static_assert(RL_SMEM <= 232448, "shared memory of a block");
 
@@ -992,8 +992,8 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             uint32_t n = 1;
             if (i == RB_EZ) n = 2;                                             // both MMA warps
             if (i == RB_PR || i == RB_OE || i == RB_ZZ) n = 8;                 // the row warps
-            if (i == RB_SR || i == RB_SS || i == RB_KC) n = 8;                 // the state warps
-            if (i >= RB_AE) n = 16;                                            // both
+            if (i == RB_SR || i == RB_SS || i == RB_KC) n = 8;                 // the state warps; those of y
+            if (i >= RB_AE) n = 24;                                            // all three
             mbar_init(bar + i, n);
         }
         fence_mbar_init();
@@ -1066,6 +1066,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             constexpr uint32_t I_P = idesc_bf16(128, 128, false, false), I_O = idesc_bf16(128, 128, false, true);
             const uint64_t sd = desc_mn(smem_u32(sm + RL_SB), 16384), zd = desc_mn(smem_u32(sm + RL_Z), 16384);
             const uint32_t to = tmem + 128;
+            int m = 0;  // chunks whose y makes state
             auto scores = [&](const Walk &x, int g) {
                 const int s = g & 1;
                 const uint32_t ph = (g >> 1) & 1, tp = tmem + 256 + 128 * s;
@@ -1077,7 +1078,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
 #pragma unroll
                 for (int ks = 1; ks < 8; ++ks) mma_ss<true>(tp, xd + step_k(ks, 16384), yd + step_k(ks, 16384), I_P);
                 umma_commit(bar + RB_PF + s);
-                umma_commit(bar + (x.c == x.n - 1 ? RB_EY + s : RB_YD));  // the last chunk's y makes no state
+                umma_commit(bar + (x.c == x.n - 1 ? RB_EY + s : RB_YD + (m++ & 1)));  // the last chunk's y makes none
             };
             int g = 0;
             Walk ahead = start();
@@ -1197,9 +1198,10 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                     for (int e = 0; e < 16; ++e) o[e] = 0u;
                     tmem_st16(tp + 16 * u, o);
                 } else if (jc != i32 && (!REV || jc + 32 <= rows)) {
-                    uint32_t v[32], o[16];
+                    uint32_t v[32];
                     tmem_ld32(tp + 32 * u, v);
                     tmem_wait_ld();
+                    uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 cf = *reinterpret_cast<const float4 *>(col + 32 * u + e);
@@ -1292,24 +1294,21 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             tc_fence_before();
             warp_arrive(bar + RB_OE);
         }
-    } else {  // y -> two parts, S -> Sb
-        const int hf = (warp - 12) >> 2, w = warp & 3, r = 32 * w + lane, t = tid - 384, c8 = t & 15;
-        const uint32_t ts = tmem + ((uint32_t)w << 21) + 64 * hf;
+    } else if (warp < 20) {  // y -> two parts
+        const int t = tid - 384, c8 = t & 15;
         auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
         int g = 0, m = 0;
         for (Walk x = start(); more(x); next(x), ++g) {
             const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
-            const bool last = x.c == x.n - 1;
             if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) break;
-            const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
-            const float2 end = a[128], zero = make_float2(0.f, 0.f);
-            const float fs = decay_ratio(end, zero);
-            unsigned char *y = sm + RL_Y + s * RL_TILE;
-            if (!last && !wait(RB_YD, m & 1)) break;
-            // (loops that stay loops: the roles' code together has to fit the instruction cache)
+            if (x.c < x.n - 1) {
+                const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
+                const float2 end = a[128], zero = make_float2(0.f, 0.f);
+                unsigned char *y = sm + RL_Y + s * RL_TILE;
+                if (!wait(RB_YD + (m & 1), (m >> 1) & 1)) break;
+                // (a loop that stays one: the roles' code together has to fit the instruction cache)
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                if (!last) {  // 64 tokens of y, scaled: the high part in place, the low one to its buffer
+                for (int h = 0; h < 2; ++h) {  // 64 tokens: the high part in place, the low one to its buffer
                     uint4 v[4];
                     float f[4];
 #pragma unroll
@@ -1341,53 +1340,64 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                     fence_proxy_async();
                     warp_arrive(bar + RB_KC);
                 }
-                if (h == 1) break;
-                // the state before this chunk: to bf16 for O, and on by the chunk's decay for S
-                if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
-                if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
-                tc_fence_after();
-                const float *S0 = p.states + (int64_t)x.it * D * D;
+                if (!ok) break;
+                ++m;
+            }
+            warp_arrive(bar + RB_AE + (g & 3));
+        }
+    } else {  // the state before a chunk: to bf16 for O, and on by the chunk's decay for S
+        const int hf = (warp - 20) >> 2, w = warp & 3, r = 32 * w + lane;
+        const uint32_t ts = tmem + ((uint32_t)w << 21) + 64 * hf;
+        auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
+        int g = 0, m = 0;
+        for (Walk x = start(); more(x); next(x), ++g) {
+            const bool last = x.c == x.n - 1;
+            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) break;
+            const float fs = decay_ratio((reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130)[128],
+                                         make_float2(0.f, 0.f));
+            warp_arrive(bar + RB_AE + (g & 3));
+            if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
+            if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
+            tc_fence_after();
+            const float *S0 = p.states + (int64_t)x.it * D * D;
 #pragma unroll 1
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t v[32];
-                    if (x.c > 0) {
-                        tmem_ld32(ts + 32 * u, v);
-                        tmem_wait_ld();
-                    } else if (ST) {
+            for (int u = 0; u < 2; ++u) {
+                uint32_t v[32];
+                if (x.c > 0) {
+                    tmem_ld32(ts + 32 * u, v);
+                    tmem_wait_ld();
+                } else if (ST) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
-                    } else {
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
-                            v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
-                            v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
-                        }
-                    }
-                    unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = pack2(pair_w(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
-                        *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    if (!last) {
-                        scale32(v, fs);
-                        tmem_st32(ts + 32 * u, v);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
+                        v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
+                        v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
                     }
                 }
-                fence_proxy_async();
-                tmem_wait_st();
-                tc_fence_before();
-                if (!last) warp_arrive(bar + RB_SS);
-                warp_arrive(bar + RB_SR);
+                unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = pack2(pair_w(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                    *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                if (!last) {
+                    scale32(v, fs);
+                    tmem_st32(ts + 32 * u, v);
+                }
             }
-            if (!ok) break;
-            if (!last) ++m;
-            warp_arrive(bar + RB_AE + (g & 3));
+            tmem_wait_st();
+            tc_fence_before();
+            if (!last) {
+                warp_arrive(bar + RB_SS);
+                ++m;
+            }
+            fence_proxy_async();
+            warp_arrive(bar + RB_SR);
         }
     }
     __syncwarp();
