@@ -89,6 +89,19 @@ __device__ __forceinline__ void scale32(uint32_t (&v)[32], float f) {
         v[e] = __float_as_uint(a), v[e + 1] = __float_as_uint(b);
     }
 }
+__device__ __forceinline__ void scale16(uint32_t (&v)[16], float f) {  // the same for 16 columns
+    if (f == 0.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0u;
+    }
+    const F2 ff = f2(f, f);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float a, b;
+        f2_get(pair_w(v[e], v[e + 1]) * ff, a, b);
+        v[e] = __float_as_uint(a), v[e + 1] = __float_as_uint(b);
+    }
+}
 __device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {  // one 32-byte sector
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -949,19 +962,36 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // and y's two parts (the low one waits in registers for its 64-token buffer).
 //
 // warp 0: TMA of x and y (two tiles of 32 KB each); 1: MMA of P and O; 2: TMA of
-// z (one tile, its next one already in L2) and MMA of S; 3: prefix sums, four
-// chunks ahead; 4-11: rows of P and O, two threads a row; 12-19: y -> two parts
+// z (one tile, its next one already in L2) and MMA of S; 3: the tables of
+// the decays, three chunks ahead; 4-11: rows of P and O, two threads a row; 12-19: y -> two parts
 // (the high one in place); 20-27: S -> Sb. Every barrier is waited on by its
 // waiters in every phase, and no phase comes twice between two waits (checked
 // with a model of the roles).
 constexpr int RL_TILE = 128 * D * 2;                 // 32 KB
 constexpr int RL_X = 0, RL_Y = 2 * RL_TILE, RL_Z = 4 * RL_TILE, RL_SB = 5 * RL_TILE, RL_LO = 6 * RL_TILE;
-constexpr int RL_A = RL_LO + RL_TILE / 2;            // prefix sums [4][130]
-constexpr int RL_COL = RL_A + 4 * 130 * 8;           // column factors [8 warps][64]
-constexpr int RL_BAR = RL_COL + 8 * 64 * 4;
+constexpr int RL_T = RL_LO + RL_TILE / 2;            // tables of the decays, RL_SLOTS chunks
+constexpr int RL_SLOTS = 3;
 constexpr int RL_THREADS = 896;
+// The decays of one chunk, as its roles use them (made by one warp, ahead of
+// them; every role on its own spent 1,700 of a chunk's 8,000 cycles on them).
+// P's D_ij is a row factor times a column factor, with the edge of the row's 32
+// rows as their meeting point: both are <= 1 off the diagonal, and inside the
+// 32 x 32 piece on it the column factor grows by at most 2^60 as long as the
+// piece decays by less than that (`mild`; else an exponential per element).
+struct RollTable {
+    float state[128];     // row i's factor of the state part, c_state included
+    float row[128];       // D's row factor, c_intra included
+    float weight[128];    // what token s enters the state with, c_roll included
+    float col[4][128];    // D's column factors for the rows of each quarter
+    float mild[4];
+    float total;          // e^{L_end}
+    float pad[3];
+    float2 a[130];        // prefix sums
+};
+constexpr int RL_BAR = RL_T + RL_SLOTS * (int)sizeof(RollTable);
 enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_YD = 10, RB_FZ = 12, RB_EZ, RB_PR, RB_OIN, RB_OF, RB_OE,
-       RB_SR, RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF, RB_AE = RB_AF + 4, RB_COUNT = RB_AE + 4 };
+       RB_SR, RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF,
+       RB_AE = RB_AF + RL_SLOTS, RB_COUNT = RB_AE + RL_SLOTS };
 constexpr int RL_SMEM = RL_BAR + RB_COUNT * 8 + 16 + 1024;
 static_assert(RL_SMEM <= 232448, "shared memory of a block");
 
@@ -1034,6 +1064,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
         x.it += gridDim.x;
         enter(x);
     };
+    auto table = [&](int g) { return reinterpret_cast<RollTable *>(sm + RL_T) + g % RL_SLOTS; };
     auto first_token = [&](const Walk &x) { return (REV ? x.n - 1 - x.c : x.c) * 128; };
     auto tile = [&](const CUtensorMap *m, unsigned char *d, uint64_t *full, const Walk &x) {
         mbar_arrive_expect_tx(full, RL_TILE);
@@ -1155,84 +1186,110 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const int t0 = first_token(x);
             const LinBlock part{x.blk.seq, x.blk.start + t0, min(128, x.blk.len - t0)};
             long long sums[4];
-            warp_decay<4>(geo, p.log_decay, p.decay, part, x.h, sums);
-            ok = __all_sync(0xffffffffu, ab.wait(bar + RB_AE + (g & 3), ((g >> 2) & 1) ^ 1));
+            const long long all = warp_decay<4>(geo, p.log_decay, p.decay, part, x.h, sums);
+            ok = __all_sync(0xffffffffu, ab.wait(bar + RB_AE + g % RL_SLOTS, ((g / RL_SLOTS) & 1) ^ 1));
             if (!ok) break;
-            float2 *a = reinterpret_cast<float2 *>(sm + RL_A) + (g & 3) * 130;
-            if (lane == 0) a[0] = make_float2(0.f, 0.f);
+            RollTable *t = table(g);
+            const float2 zero = make_float2(0.f, 0.f), end = decay_pair(all);
+            float2 a[4];  // this lane's tokens 4 lane ..
 #pragma unroll
-            for (int u = 0; u < 4; ++u) a[lane * 4 + u + 1] = decay_pair(sums[u]);
-            warp_arrive(bar + RB_AF + (g & 3));
+            for (int u = 0; u < 4; ++u) a[u] = decay_pair(sums[u]);
+            float2 before = make_float2(__shfl_up_sync(0xffffffffu, a[3].x, 1), __shfl_up_sync(0xffffffffu, a[3].y, 1));
+            if (lane == 0) before = zero;
+            auto four = [](float *d, float x, float y, float z, float w) {
+                *reinterpret_cast<float4 *>(d) = make_float4(x, y, z, w);
+            };
+            if (lane == 0) t->a[0] = zero, t->total = decay_ratio(end, zero);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) t->a[4 * lane + u + 1] = a[u];
+            const float cs = p.c_state, ci = p.c_intra, cr = p.c_roll;
+            float v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = cs * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
+            four(t->state + 4 * lane, v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = cr * (REV ? decay_ratio(a[u], zero) : decay_ratio(end, a[u]));
+            four(t->weight + 4 * lane, v[0], v[1], v[2], v[3]);
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {  // the quarter's rows start at token 32 w
+                const float2 lo = make_float2(__shfl_sync(0xffffffffu, before.x, 8 * w),
+                                              __shfl_sync(0xffffffffu, before.y, 8 * w));
+                const float2 hi = make_float2(__shfl_sync(0xffffffffu, a[3].x, 8 * w + 7),
+                                              __shfl_sync(0xffffffffu, a[3].y, 8 * w + 7));
+                const float2 edge = REV ? hi : lo;
+                if (lane >> 3 == w) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v[u] = ci * (REV ? decay_ratio(edge, a[u]) : decay_ratio(a[u], edge));
+                    four(t->row + 4 * lane, v[0], v[1], v[2], v[3]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] = REV ? decay_ratio(a[u], edge) : decay_ratio(edge, a[u]);
+                four(t->col[w] + 4 * lane, v[0], v[1], v[2], v[3]);
+                if (lane == 0) t->mild[w] = (lo.x - hi.x) + (lo.y - hi.y) < 60.f ? 1.f : 0.f;
+            }
+            warp_arrive(bar + RB_AF + g % RL_SLOTS);
         }
     } else if (warp < 12) {  // rows of P and O
         const int hf = (warp - 4) >> 2, w = warp & 3, r = 32 * w + lane, i32 = 32 * w;
-        float *col = reinterpret_cast<float *>(sm + RL_COL) + (warp - 4) * 64;
         const uint32_t tl = tmem + ((uint32_t)w << 21), to = tl + 128 + 64 * hf;
         auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
         // P of chunk g to bf16; returns the factor of its rows' state part
         auto mask = [&](const Walk &x, int g) -> float {
             const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
             const uint32_t tp = tl + 256 + 128 * s + 64 * hf;
-            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) return 0.f;
-            const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
-            const float2 ai = a[r + 1], edge = a[REV ? i32 + 32 : i32], zero = make_float2(0.f, 0.f);
-            const float f = p.c_state * (REV ? decay_ratio(a[128], ai) : decay_ratio(ai, zero));
-            // row and column factors, as in the kernel above
-            const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
+            if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) return 0.f;
+            const RollTable *t = table(g);
+            const float f = t->state[r], rf = t->row[r];
             const F2 rf2 = f2(rf, rf);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int j = 64 * hf + 32 * u + lane;
-                col[32 * u + lane] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
-                                         : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
-            }
-            __syncwarp();
+            const bool mild = t->mild[w] != 0.f;
             if (!wait(RB_PF + s, (g >> 1) & 1)) return 0.f;
             tc_fence_after();
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int jc = 64 * hf + 32 * u;
-                if (REV ? jc < i32 || jc >= rows : jc > i32) {  // outside the mask
-                    uint32_t o[16];
+            for (int u = 0; u < 4; ++u) {  // 16 columns: short loops, for the instruction cache
+                const int jc = 64 * hf + 16 * u, jb = jc & ~31;  // the 32 columns they belong to
+                uint32_t o[8];
+                if (REV ? jb < i32 || jc >= rows : jb > i32) {  // outside the mask
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
-                    tmem_st16(tp + 16 * u, o);
-                } else if (jc != i32 && (!REV || jc + 32 <= rows)) {
-                    uint32_t v[32];
-                    tmem_ld32(tp + 32 * u, v);
+                    for (int e = 0; e < 8; ++e) o[e] = 0u;
+                } else if ((jb != i32 || mild) && (!REV || jc + 16 <= rows)) {
+                    uint32_t v[16];
+                    tmem_ld16(tp + 16 * u, v);
                     tmem_wait_ld();
-                    uint32_t o[16];
+                    if (jb == i32) {
+                        const int l = lane - (jc & 31);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 cf = *reinterpret_cast<const float4 *>(col + 32 * u + e);
+                        for (int e = 0; e < 16; ++e) v[e] = (REV ? e >= l : e <= l) ? v[e] : 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 cf = *reinterpret_cast<const float4 *>(t->col[w] + jc + e);
                         o[e / 2] = pack2(pair_w(v[e], v[e + 1]) * f2(cf.x, cf.y) * rf2);
                         o[e / 2 + 1] = pack2(pair_w(v[e + 2], v[e + 3]) * f2(cf.z, cf.w) * rf2);
                     }
-                    tmem_st16(tp + 16 * u, o);
                 } else {
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {  // 8 columns into 4, behind the reads
-                        uint32_t v[8], o[4];
-                        tmem_ld8(tp + 32 * u + 8 * q, v);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[4];
+                        tmem_ld4(tp + 16 * u + 4 * q, v);
                         tmem_wait_ld();
+                        float y[4];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            float y[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int j = jc + 8 * q + e + k;
-                                const float d = REV ? decay_ratio(a[j + 1], ai) : decay_ratio(ai, a[j + 1]);
-                                const bool in = j < rows && (REV ? j >= r : j <= r);
-                                y[k] = in ? p.c_intra * d * __uint_as_float(v[e + k]) : 0.f;
-                            }
-                            o[e / 2] = pack2(y[0], y[1]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = jc + 4 * q + e;
+                            const float d = REV ? decay_ratio(t->a[j + 1], t->a[r + 1])
+                                                : decay_ratio(t->a[r + 1], t->a[j + 1]);
+                            const bool in = j < rows && (REV ? j >= r : j <= r);
+                            y[e] = in ? p.c_intra * d * __uint_as_float(v[e]) : 0.f;
                         }
-                        tmem_st4(tp + 16 * u + 4 * q, o);
+                        const uint32_t w2[2] = {pack2(y[0], y[1]), pack2(y[2], y[3])};
+                        tmem_st2(tp + 8 * u + 2 * q, w2);  // behind the reads
                     }
+                    continue;
                 }
+                tmem_st8(tp + 8 * u, o);
             }
             tmem_wait_st();
-            warp_arrive(bar + RB_AE + (g & 3));
+            warp_arrive(bar + RB_AE + g % RL_SLOTS);
             return f;
         };
         int g = 0;
@@ -1247,12 +1304,12 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             if (!wait(RB_OIN, g & 1)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                uint32_t v[32];
-                tmem_ld32(to + 32 * u, v);
+            for (int u = 0; u < 4; ++u) {
+                uint32_t v[16];
+                tmem_ld16(to + 16 * u, v);
                 tmem_wait_ld();
-                scale32(v, f);
-                tmem_st32(to + 32 * u, v);
+                scale16(v, f);  // a reset drops the state
+                tmem_st16(to + 16 * u, v);
             }
             if (rows < 128) {  // what lies past the segment's end must not meet zeros
                 if (!wait(RB_FZ, g & 1)) break;
@@ -1276,20 +1333,13 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             tc_fence_after();
             __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + t0 + r) * geo.H + x.h) * D + 64 * hf;
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                uint32_t v[32];
-                tmem_ld32(to + 32 * u, v);
+            for (int u = 0; u < 4; ++u) {
+                uint32_t v[16], o[8];
+                tmem_ld16(to + 16 * u, v);
                 tmem_wait_ld();
-                if (r < rows) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o[e] = pack2(__uint_as_float(v[16 * k + 2 * e]), __uint_as_float(v[16 * k + 2 * e + 1]));
-                        st_v8(dst + 32 * u + 16 * k, o);
-                    }
-                }
+                for (int e = 0; e < 8; ++e) o[e] = pack2(pair_w(v[2 * e], v[2 * e + 1]));
+                if (r < rows) st_v8(dst + 16 * u, o);
             }
             tc_fence_before();
             warp_arrive(bar + RB_OE);
@@ -1300,50 +1350,50 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
         int g = 0, m = 0;
         for (Walk x = start(); more(x); next(x), ++g) {
             const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
-            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) break;
+            if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) break;
             if (x.c < x.n - 1) {
-                const float2 *a = reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130;
-                const float2 end = a[128], zero = make_float2(0.f, 0.f);
-                unsigned char *y = sm + RL_Y + s * RL_TILE;
+                const float *weight = table(g)->weight;
+                unsigned char *yt = sm + RL_Y + s * RL_TILE + kmajor_chunk(t >> 4, c8, 128),
+                              *lt = sm + RL_LO + kmajor_chunk(t >> 4, c8, 64);
                 if (!wait(RB_YD + (m & 1), (m >> 1) & 1)) break;
                 // (a loop that stays one: the roles' code together has to fit the instruction cache)
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {  // 64 tokens: the high part in place, the low one to its buffer
-                    uint4 v[4];
-                    float f[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 64 * h + 16 * i + (t >> 4);
-                        v[i] = *reinterpret_cast<const uint4 *>(y + kmajor_chunk(row, c8, 128));
-                        f[i] = p.c_roll * (REV ? decay_ratio(a[row + 1], zero) : decay_ratio(end, a[row + 1]));
-                        if (row >= rows) v[i] = make_uint4(0u, 0u, 0u, 0u);  // past the segment's end
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t hi[4], l[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const F2 xw = pair_f(in[e]) * f2(f[i], f[i]);
-                            hi[e] = pack2(xw);
-                            l[e] = pack2(minus(xw, pair_f(hi[e])));
-                        }
-                        *reinterpret_cast<uint4 *>(y + kmajor_chunk(64 * h + 16 * i + (t >> 4), c8, 128)) =
-                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        v[i] = make_uint4(l[0], l[1], l[2], l[3]);
-                    }
-                    // the products with the buffer's last contents are done
+                    // the products with the low buffer's last contents are done
                     if (2 * m + h > 0 && !wait(RB_LOF, (h + 1) & 1)) break;
+#pragma unroll 1
+                    for (int i = 0; i < 4; i += 2) {
+                        uint4 v[2];
+                        float f[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(sm + RL_LO + kmajor_chunk(16 * i + (t >> 4), c8, 64)) = v[i];
+                        for (int q = 0; q < 2; ++q) {
+                            const int row = 64 * h + 16 * (i + q) + (t >> 4);
+                            v[q] = *reinterpret_cast<const uint4 *>(yt + h * 8192 + (i + q) * 2048);
+                            f[q] = weight[row];
+                            if (row >= rows) v[q] = make_uint4(0u, 0u, 0u, 0u);  // past the segment's end
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+                            uint32_t hi[4], l[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const F2 xw = pair_f(in[e]) * f2(f[q], f[q]);
+                                hi[e] = pack2(xw);
+                                l[e] = pack2(minus(xw, pair_f(hi[e])));
+                            }
+                            *reinterpret_cast<uint4 *>(yt + h * 8192 + (i + q) * 2048) =
+                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4 *>(lt + (i + q) * 2048) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
+                    }
                     fence_proxy_async();
                     warp_arrive(bar + RB_KC);
                 }
                 if (!ok) break;
                 ++m;
             }
-            warp_arrive(bar + RB_AE + (g & 3));
+            warp_arrive(bar + RB_AE + g % RL_SLOTS);
         }
     } else {  // the state before a chunk: to bf16 for O, and on by the chunk's decay for S
         const int hf = (warp - 20) >> 2, w = warp & 3, r = 32 * w + lane;
@@ -1352,42 +1402,41 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
         int g = 0, m = 0;
         for (Walk x = start(); more(x); next(x), ++g) {
             const bool last = x.c == x.n - 1;
-            if (!wait(RB_AF + (g & 3), (g >> 2) & 1)) break;
-            const float fs = decay_ratio((reinterpret_cast<const float2 *>(sm + RL_A) + (g & 3) * 130)[128],
-                                         make_float2(0.f, 0.f));
-            warp_arrive(bar + RB_AE + (g & 3));
+            if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) break;
+            const float fs = table(g)->total;
+            warp_arrive(bar + RB_AE + g % RL_SLOTS);
             if (x.c > 0 && !wait(RB_SF, (m - 1) & 1)) break;
             if (g > 0 && !wait(RB_SBF, (g - 1) & 1)) break;
             tc_fence_after();
             const float *S0 = p.states + (int64_t)x.it * D * D;
+            unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                uint32_t v[32];
+            for (int u = 0; u < 4; ++u) {
+                uint32_t v[16];
                 if (x.c > 0) {
-                    tmem_ld32(ts + 32 * u, v);
+                    tmem_ld16(ts + 16 * u, v);
                     tmem_wait_ld();
                 } else if (ST) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 32 * u + e) * D + r));
+                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__ldg(S0 + (64 * hf + 16 * u + e) * D + r));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 32 * u + e));
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 q = __ldg(reinterpret_cast<const float4 *>(S0 + r * D + 64 * hf + 16 * u + e));
                         v[e] = __float_as_uint(q.x), v[e + 1] = __float_as_uint(q.y);
                         v[e + 2] = __float_as_uint(q.z), v[e + 3] = __float_as_uint(q.w);
                     }
                 }
-                unsigned char *sb = sm + RL_SB + hf * 16384 + r * 128;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = pack2(pair_w(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
-                    *reinterpret_cast<uint4 *>(sb + (((4 * u + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(sb + (((2 * u + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 if (!last) {
-                    scale32(v, fs);
-                    tmem_st32(ts + 32 * u, v);
+                    scale16(v, fs);
+                    tmem_st16(ts + 16 * u, v);
                 }
             }
             tmem_wait_st();
