@@ -38,6 +38,16 @@ struct Abort {
         return true;
     }
 };
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {  // two bf16 products, each rounded once
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 // One arrival for the warp, after all its lanes have come here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
@@ -947,9 +957,11 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // One item is a segment (a block of any length) and head. The state lives in
 // TMEM in fp32 and moves on by 128 tokens at a time, so a segment reads its
 // tokens once and no state goes through memory but the segment's first:
-//   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place;
-//   O = x Sb, Sb the state rounded to bf16; rows scaled by the decay from the
-//   chunk's edge; O += P z;
+//   P = x y^T, masked, times a column factor e^{-L_j}, rounded to bf16 in place;
+//   O = x Sb + P z, Sb the state rounded to bf16; row i times e^{L_i} on its way
+//   out, which makes D_ij of the column factor and the state's own factor at once
+//   (in a chunk that decays by less than 2^80; one that decays by more takes D_ij
+//   itself in P, an exponential per element, and has x Sb scaled in between);
 //   S <- e^{L_end} S + (w y)^T z, w y in two bf16 parts (16 bits: the state in
 //   here only feeds bf16 products).
 // In reverse time (REV) the chunks go from the segment's end, the state is the
@@ -959,7 +971,8 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // loops run from one chunk to the next, each to stay under the time that the
 // chunk's 128 KB take: S -> Sb, scale -> MMA -> S, and x Sb -> scale -> P z -> out.
 // Everything else of a chunk is done ahead of them: P (two in TMEM), its mask,
-// and y's two parts (the low one waits in registers for its 64-token buffer).
+// and y's two parts. Instructions are the next bound: twenty-eight warps of
+// seven roles share an SM's instruction caches, so the loops are short.
 //
 // warp 0: TMA of x and y (two tiles of 32 KB each); 1: MMA of P and O; 2: TMA of
 // z (one tile, its next one already in L2) and MMA of S; 3: the tables of
@@ -974,22 +987,17 @@ constexpr int RL_SLOTS = 3;
 constexpr int RL_THREADS = 896;
 // The decays of one chunk, as its roles use them (made by one warp, ahead of
 // them; every role on its own spent 1,700 of a chunk's 8,000 cycles on them).
-// P's D_ij is a row factor times a column factor, with the edge of the row's 32
-// rows as their meeting point: both are <= 1 off the diagonal, and inside the
-// 32 x 32 piece on it the column factor grows by at most 2^60 as long as the
-// piece decays by less than that (`mild`; else an exponential per element).
 struct RollTable {
-    float state[128];     // row i's factor of the state part, c_state included
-    float row[128];       // D's row factor, c_intra included
-    float weight[128];    // what token s enters the state with, c_roll included
-    float col[4][128];    // D's column factors for the rows of each quarter
-    float mild[4];
-    float total;          // e^{L_end}
-    float pad[3];
+    float row[128];       // row i's factor on its way out (mild) or of the state part, c_state included
+    float col[128];       // column factors of P, c_intra / c_state included (mild)
+    uint2 weight[128];    // what token s enters the state with, c_roll included: two bf16 parts, each twice
+    float mild, total;    // whether the chunk decays by less than 2^80; e^{L_end}
+    float pad[2];
     float2 a[130];        // prefix sums
 };
+constexpr float kMild = 80.f;
 constexpr int RL_BAR = RL_T + RL_SLOTS * (int)sizeof(RollTable);
-enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_YD = 10, RB_FZ = 12, RB_EZ, RB_PR, RB_OIN, RB_OF, RB_OE,
+enum { RB_FX = 0, RB_EX = 2, RB_FY = 4, RB_EY = 6, RB_PF = 8, RB_YD = 10, RB_PR = 12, RB_FZ = 14, RB_EZ, RB_OIN, RB_OF, RB_OE,
        RB_SR, RB_SS, RB_SBF, RB_KC, RB_LOF, RB_SF, RB_ZZ, RB_AF,
        RB_AE = RB_AF + RL_SLOTS, RB_COUNT = RB_AE + RL_SLOTS };
 constexpr int RL_SMEM = RL_BAR + RB_COUNT * 8 + 16 + 1024;
@@ -1001,7 +1009,7 @@ struct RollTcArgs {
     int decay;
     const float *states;  // [block][head][128][128]
     __nv_bfloat16 *out;
-    float c_state, c_intra, c_roll;  // c_roll: what y z products enter the state with
+    float c_state, c_intra, c_ratio, c_roll;  // c_intra / c_state; what y z products enter the state with
     int items;
 };
 
@@ -1021,7 +1029,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
         for (int i = 0; i < RB_COUNT; ++i) {
             uint32_t n = 1;
             if (i == RB_EZ) n = 2;                                             // both MMA warps
-            if (i == RB_PR || i == RB_OE || i == RB_ZZ) n = 8;                 // the row warps
+            if (i == RB_PR || i == RB_PR + 1 || i == RB_OE || i == RB_ZZ) n = 8;  // the row warps
             if (i == RB_SR || i == RB_SS || i == RB_KC) n = 8;                 // the state warps; those of y
             if (i >= RB_AE) n = 24;                                            // all three
             mbar_init(bar + i, n);
@@ -1133,7 +1141,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                     if (!ok) break;
                     next(ahead);
                 }
-                if (!(ok = ab.wait(bar + RB_FZ, g & 1) && ab.wait(bar + RB_PR, g & 1))) break;
+                if (!(ok = ab.wait(bar + RB_FZ, g & 1) && ab.wait(bar + RB_PR + s, (g >> 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t tp = tmem + 256 + 128 * s;
 #pragma unroll
@@ -1194,55 +1202,49 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             float2 a[4];  // this lane's tokens 4 lane ..
 #pragma unroll
             for (int u = 0; u < 4; ++u) a[u] = decay_pair(sums[u]);
-            float2 before = make_float2(__shfl_up_sync(0xffffffffu, a[3].x, 1), __shfl_up_sync(0xffffffffu, a[3].y, 1));
-            if (lane == 0) before = zero;
             auto four = [](float *d, float x, float y, float z, float w) {
                 *reinterpret_cast<float4 *>(d) = make_float4(x, y, z, w);
             };
-            if (lane == 0) t->a[0] = zero, t->total = decay_ratio(end, zero);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) t->a[4 * lane + u + 1] = a[u];
-            const float cs = p.c_state, ci = p.c_intra, cr = p.c_roll;
-            float v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = cs * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
-            four(t->state + 4 * lane, v[0], v[1], v[2], v[3]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = cr * (REV ? decay_ratio(a[u], zero) : decay_ratio(end, a[u]));
-            four(t->weight + 4 * lane, v[0], v[1], v[2], v[3]);
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {  // the quarter's rows start at token 32 w
-                const float2 lo = make_float2(__shfl_sync(0xffffffffu, before.x, 8 * w),
-                                              __shfl_sync(0xffffffffu, before.y, 8 * w));
-                const float2 hi = make_float2(__shfl_sync(0xffffffffu, a[3].x, 8 * w + 7),
-                                              __shfl_sync(0xffffffffu, a[3].y, 8 * w + 7));
-                const float2 edge = REV ? hi : lo;
-                if (lane >> 3 == w) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) v[u] = ci * (REV ? decay_ratio(edge, a[u]) : decay_ratio(a[u], edge));
-                    four(t->row + 4 * lane, v[0], v[1], v[2], v[3]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = REV ? decay_ratio(a[u], edge) : decay_ratio(edge, a[u]);
-                four(t->col[w] + 4 * lane, v[0], v[1], v[2], v[3]);
-                if (lane == 0) t->mild[w] = (lo.x - hi.x) + (lo.y - hi.y) < 60.f ? 1.f : 0.f;
+            if (lane == 0) {
+                t->a[0] = zero;
+                t->total = decay_ratio(end, zero);
+                t->mild = -(end.x + end.y) < kMild ? 1.f : 0.f;
             }
+            float v[4];
+            uint32_t wt[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                t->a[4 * lane + u + 1] = a[u];
+                const float w = p.c_roll * (REV ? decay_ratio(a[u], zero) : decay_ratio(end, a[u]));
+                wt[2 * u] = pack2(w, w);
+                const float low = w - lo_f(wt[2 * u]);
+                wt[2 * u + 1] = pack2(low, low);
+            }
+            *reinterpret_cast<uint4 *>(t->weight + 4 * lane) = make_uint4(wt[0], wt[1], wt[2], wt[3]);
+            *reinterpret_cast<uint4 *>(t->weight + 4 * lane + 2) = make_uint4(wt[4], wt[5], wt[6], wt[7]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = p.c_state * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
+            four(t->row + 4 * lane, v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = p.c_ratio * (REV ? decay_ratio(a[u], end) : decay_ratio(zero, a[u]));
+            four(t->col + 4 * lane, v[0], v[1], v[2], v[3]);
             warp_arrive(bar + RB_AF + g % RL_SLOTS);
         }
     } else if (warp < 12) {  // rows of P and O
         const int hf = (warp - 4) >> 2, w = warp & 3, r = 32 * w + lane, i32 = 32 * w;
         const uint32_t tl = tmem + ((uint32_t)w << 21), to = tl + 128 + 64 * hf;
         auto wait = [&](int b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(bar + b, ph)); };
-        // P of chunk g to bf16; returns the factor of its rows' state part
-        auto mask = [&](const Walk &x, int g) -> float {
+        // P of chunk g to bf16; returns its rows' factor and whether the chunk is mild
+        float f = 0.f;
+        bool mild = true;
+        auto mask = [&](const Walk &x, int g) {
             const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
             const uint32_t tp = tl + 256 + 128 * s + 64 * hf;
-            if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) return 0.f;
+            if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) return;
             const RollTable *t = table(g);
-            const float f = t->state[r], rf = t->row[r];
-            const F2 rf2 = f2(rf, rf);
-            const bool mild = t->mild[w] != 0.f;
-            if (!wait(RB_PF + s, (g >> 1) & 1)) return 0.f;
+            f = t->row[r];
+            mild = t->mild != 0.f;
+            if (!wait(RB_PF + s, (g >> 1) & 1)) return;
             tc_fence_after();
 #pragma unroll 1
             for (int u = 0; u < 4; ++u) {  // 16 columns: short loops, for the instruction cache
@@ -1251,7 +1253,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                 if (REV ? jb < i32 || jc >= rows : jb > i32) {  // outside the mask
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = 0u;
-                } else if ((jb != i32 || mild) && (!REV || jc + 16 <= rows)) {
+                } else if (mild && (!REV || jc + 16 <= rows)) {
                     uint32_t v[16];
                     tmem_ld16(tp + 16 * u, v);
                     tmem_wait_ld();
@@ -1262,9 +1264,9 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                     }
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
-                        const float4 cf = *reinterpret_cast<const float4 *>(t->col[w] + jc + e);
-                        o[e / 2] = pack2(pair_w(v[e], v[e + 1]) * f2(cf.x, cf.y) * rf2);
-                        o[e / 2 + 1] = pack2(pair_w(v[e + 2], v[e + 3]) * f2(cf.z, cf.w) * rf2);
+                        const float4 cf = *reinterpret_cast<const float4 *>(t->col + jc + e);
+                        o[e / 2] = pack2(pair_w(v[e], v[e + 1]) * f2(cf.x, cf.y));
+                        o[e / 2 + 1] = pack2(pair_w(v[e + 2], v[e + 3]) * f2(cf.z, cf.w));
                     }
                 } else {
 #pragma unroll 1
@@ -1276,10 +1278,11 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = jc + 4 * q + e;
-                            const float d = REV ? decay_ratio(t->a[j + 1], t->a[r + 1])
-                                                : decay_ratio(t->a[r + 1], t->a[j + 1]);
+                            const float d = mild ? t->col[j]
+                                            : p.c_intra * (REV ? decay_ratio(t->a[j + 1], t->a[r + 1])
+                                                               : decay_ratio(t->a[r + 1], t->a[j + 1]));
                             const bool in = j < rows && (REV ? j >= r : j <= r);
-                            y[e] = in ? p.c_intra * d * __uint_as_float(v[e]) : 0.f;
+                            y[e] = in ? d * __uint_as_float(v[e]) : 0.f;
                         }
                         const uint32_t w2[2] = {pack2(y[0], y[1]), pack2(y[2], y[3])};
                         tmem_st2(tp + 8 * u + 2 * q, w2);  // behind the reads
@@ -1290,47 +1293,55 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             }
             tmem_wait_st();
             warp_arrive(bar + RB_AE + g % RL_SLOTS);
-            return f;
+            if (mild && rows == 128) {  // nothing more to do before P z
+                tc_fence_before();
+                warp_arrive(bar + RB_PR + s);
+            }
         };
         int g = 0;
         Walk x = start(), ahead = x;
-        float f = 0.f;
         if (more(ahead)) {
-            f = mask(ahead, 0);
+            mask(ahead, 0);
             next(ahead);
         }
         for (; more(x) && ok; next(x), ++g) {
             const int t0 = first_token(x), rows = min(128, x.blk.len - t0);
+            const float out = mild ? f : 1.f;
             if (!wait(RB_OIN, g & 1)) break;
-            tc_fence_after();
+            if (!mild || rows < 128) {
+                tc_fence_after();
+                if (!mild) {  // scaled now, not on the way out
 #pragma unroll 1
-            for (int u = 0; u < 4; ++u) {
-                uint32_t v[16];
-                tmem_ld16(to + 16 * u, v);
-                tmem_wait_ld();
-                scale16(v, f);  // a reset drops the state
-                tmem_st16(to + 16 * u, v);
-            }
-            if (rows < 128) {  // what lies past the segment's end must not meet zeros
-                if (!wait(RB_FZ, g & 1)) break;
-                if (r >= rows) {
-                    unsigned char *z = sm + RL_Z + hf * 16384 + r * 128;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t v[16];
+                        tmem_ld16(to + 16 * u, v);
+                        tmem_wait_ld();
+                        scale16(v, f);  // a reset drops the state
+                        tmem_st16(to + 16 * u, v);
+                    }
                 }
-                fence_proxy_async();
-                if (x.c < x.n - 1) warp_arrive(bar + RB_ZZ);
+                if (rows < 128) {  // what lies past the segment's end must not meet zeros
+                    if (!wait(RB_FZ, g & 1)) break;
+                    if (r >= rows) {
+                        unsigned char *z = sm + RL_Z + hf * 16384 + r * 128;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
+                    if (x.c < x.n - 1) warp_arrive(bar + RB_ZZ);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar + RB_PR + (g & 1));
             }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(bar + RB_PR);
             if (more(ahead)) {
-                f = mask(ahead, g + 1);
+                mask(ahead, g + 1);
                 if (!ok) break;
                 next(ahead);
             }
             if (!wait(RB_OF, g & 1)) break;
             tc_fence_after();
+            const F2 out2 = f2(out, out);
             __nv_bfloat16 *dst = p.out + ((int64_t)(x.blk.start + t0 + r) * geo.H + x.h) * D + 64 * hf;
 #pragma unroll 1
             for (int u = 0; u < 4; ++u) {
@@ -1338,7 +1349,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                 tmem_ld16(to + 16 * u, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = pack2(pair_w(v[2 * e], v[2 * e + 1]));
+                for (int e = 0; e < 8; ++e) o[e] = pack2(pair_w(v[2 * e], v[2 * e + 1]) * out2);
                 if (r < rows) st_v8(dst + 16 * u, o);
             }
             tc_fence_before();
@@ -1352,7 +1363,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const int s = g & 1, rows = min(128, x.blk.len - first_token(x));
             if (!wait(RB_AF + g % RL_SLOTS, (g / RL_SLOTS) & 1)) break;
             if (x.c < x.n - 1) {
-                const float *weight = table(g)->weight;
+                const uint2 *weight = table(g)->weight;
                 unsigned char *yt = sm + RL_Y + s * RL_TILE + kmajor_chunk(t >> 4, c8, 128),
                               *lt = sm + RL_LO + kmajor_chunk(t >> 4, c8, 64);
                 if (!wait(RB_YD + (m & 1), (m >> 1) & 1)) break;
@@ -1364,7 +1375,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
 #pragma unroll 1
                     for (int i = 0; i < 4; i += 2) {
                         uint4 v[2];
-                        float f[2];
+                        uint2 f[2];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const int row = 64 * h + 16 * (i + q) + (t >> 4);
@@ -1376,11 +1387,11 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
                         for (int q = 0; q < 2; ++q) {
                             const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
                             uint32_t hi[4], l[4];
+                            // two channels an instruction: hi = y w_h rounded, what that left off, plus y w_l
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const F2 xw = pair_f(in[e]) * f2(f[q], f[q]);
-                                hi[e] = pack2(xw);
-                                l[e] = pack2(minus(xw, pair_f(hi[e])));
+                                hi[e] = bf2_mul(in[e], f[q].x);
+                                l[e] = bf2_fma(in[e], f[q].y, bf2_fma(in[e], f[q].x, hi[e] ^ 0x80008000u));
                             }
                             *reinterpret_cast<uint4 *>(yt + h * 8192 + (i + q) * 2048) =
                                 make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -1538,7 +1549,8 @@ cudaError_t launch_roll_tc(const RollTc &a, cudaStream_t s) {
     if (!token_map(&mx, a.x, a.x_stride, geo.H, a.tokens) || !token_map(&my, a.y, a.y_stride, geo.H, a.tokens) ||
         !token_map(&mz, a.z, a.z_stride, geo.H, a.tokens))
         return cudaErrorInvalidValue;
-    RollTcArgs p{geo, a.log_decay, a.decay, a.states, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.c_roll,
+    const float ratio = a.c_intra == a.c_state ? 1.f : a.c_intra / a.c_state;  // c_state is c_intra or 1
+    RollTcArgs p{geo, a.log_decay, a.decay, a.states, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, ratio, a.c_roll,
                  geo.nblocks * geo.H};
     auto k = a.rev ? (a.state_t ? lin_roll_tc_kernel<true, true> : lin_roll_tc_kernel<true, false>)
                    : (a.state_t ? lin_roll_tc_kernel<false, true> : lin_roll_tc_kernel<false, false>);
