@@ -6,20 +6,19 @@ strides, outputs and workspaces through PyTorch, raw pointers and a CUDA
 stream. There is no fallback.
 
 q, k and v may be slices of a wider tensor (a fused projection): their last two
-axes must be contiguous and their tokens evenly spaced. With ``stream`` the
-outputs and the workspace are allocated for that stream; the inputs must be
-ready on it.
+axes must be contiguous and their tokens evenly spaced. Every call also takes
+``stream``: it then runs there, its outputs and workspace are allocated for that
+stream, and the inputs must be ready on it.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 import math
 
 import torch
 
 from . import _binding
-from ._binding import _check, _dtype_code, _need
+from ._binding import _check, _dtype_code
 
 # Host time counts for one token of one sequence: these stand for the
 # binding's helpers of the same names without the objects they make per call.
@@ -34,12 +33,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+def _stream(index: int):
+    """The device's current stream."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
 
 # decay kinds: one log decay per token and head, one per head, none
 DECAYS = {"token": 0, "head": 1, "none": 2}
@@ -53,24 +50,31 @@ def _kind(kinds: dict, value: str, name: str) -> int:
     return kinds[value]
 
 
-_here = contextlib.nullcontext()
+def _plain(t, name: str, dtype, index: int, shape=None):
+    """Checks a contiguous tensor on CUDA device ``index``."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on(stream):
-    return _here if stream is None else torch.cuda.stream(stream)
-
-
-def _view(t, name: str, lead: int, dtype=None, device=None) -> int:
-    """The token stride of ``t`` [*lead axes, H, d], whose heads are contiguous
-    and whose tokens are evenly spaced over all lead axes."""
+def _view(t, name: str, lead: int, dtype=None, index: int = -1) -> int:
+    """The token stride of ``t`` [*lead axes, H, d] (0: contiguous), whose heads
+    are contiguous and whose tokens are evenly spaced over all lead axes."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dim() != lead + 2:
         raise ValueError(f"{name} must have {lead + 2} dimensions, got {t.dim()}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if index >= 0 and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.is_contiguous() or t.numel() == 0:
@@ -90,50 +94,44 @@ def _view(t, name: str, lead: int, dtype=None, device=None) -> int:
     return step or 0
 
 
-def _check_decay(decay: str, log_decay, lead: tuple, H: int, dev):
-    kind = _kind(DECAYS, decay, "decay")
+def _check_decay(decay: str, log_decay, lead: tuple, H: int, index: int):
     if decay == "none":
-        return kind, None
-    _need(log_decay, "log_decay", torch.float32, dev)
-    want = tuple(lead) + (H,) if decay == "token" else (H,)
-    if tuple(log_decay.shape) != want:
-        raise ValueError(f"log_decay must be {want} for decay={decay!r}, got {tuple(log_decay.shape)}")
+        return 2, None
+    kind = _kind(DECAYS, decay, "decay")
+    _plain(log_decay, "log_decay", torch.float32, index)
+    want = (*lead, H) if kind == 0 else (H,)
+    if log_decay.shape != want:
+        raise ValueError(f"log_decay must be {tuple(want)} for decay={decay!r}, got {tuple(log_decay.shape)}")
     return kind, log_decay
 
 
 def _qkv(q, k, v, lead: int):
-    """Checks q, k, v; returns (device, lead shape, H, d_k, d_v, the three token strides)."""
+    """Checks q, k, v; returns (device index, lead shape, H, d_k, d_v, the three token strides)."""
     qs = _view(q, "q", lead)
-    dev = q.device
-    ks, vs = _view(k, "k", lead, q.dtype, dev), _view(v, "v", lead, q.dtype, dev)
-    H, dk = q.shape[-2:]
-    dv = v.shape[-1]
-    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    ks, vs = _view(k, "k", lead, dtype, index), _view(v, "v", lead, dtype, index)
+    if k.shape != shape or v.shape[:-1] != shape[:-1]:
         raise ValueError("shape mismatch among q, k, v")
-    return dev, tuple(q.shape[:lead]), H, dk, dv, (qs, ks, vs)
+    return index, shape[:lead], shape[-2], shape[-1], v.shape[-1], (qs, ks, vs)
 
 
-def _state(t, name: str, shape: tuple, dev):
+def _state(t, name: str, shape: tuple, index: int):
     if t is not None:
-        _need(t, name, torch.float32, dev)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        _plain(t, name, torch.float32, index, shape)
 
 
-def _out(t, name: str, shape: tuple, dtype, dev):
+def _out(t, name: str, like, shape, dtype, index: int):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _plain(t, name, dtype, index, torch.Size(shape))
     return t
 
 
-def _space(workspace, nbytes: int, dev):
+def _space(workspace, nbytes: int, like):
     """The caller's workspace or a new one; (tensor, bytes)."""
     if workspace is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev), nbytes
-    _need(workspace, "workspace", None, dev)
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device), nbytes
+    _plain(workspace, "workspace", None, like.get_device())
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -145,6 +143,17 @@ def _size(name: str, n: int, T: int, H: int, dk: int, dv: int, code: int) -> int
 
 def _bytes(name: str, n: int, T: int, H: int, dk: int, dv: int, dtype) -> int:
     return _size(name, n, T, H, dk, dv, _dtype_code(torch.empty(0, dtype=dtype)))
+
+
+def _on_stream(f):
+    """Runs ``f`` with its ``stream`` current, so that what it allocates belongs to that stream."""
+    @functools.wraps(f)
+    def g(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return g
 
 
 def linear_prefill_workspace_bytes(B: int, T: int, H: int, dk: int = 128, dv: int = 128, dtype=torch.bfloat16) -> int:
@@ -167,41 +176,46 @@ def linear_varlen_prefill_backward_workspace_bytes(N: int, T_total: int, H: int,
 
 
 def _prefill(q, k, v, log_decay, cu_seqlens, initial_state, decay, scale, output_final_state, out, final_state,
-             workspace, device_status, stream):
+             workspace, device_status):
     lib = load()
     packed = cu_seqlens is not None
-    dev, lead, H, dk, dv, strides = _qkv(q, k, v, 1 if packed else 2)
+    index, lead, H, dk, dv, strides = _qkv(q, k, v, 1 if packed else 2)
     code = _dtype_code(q)
-    kind, g = _check_decay(decay, log_decay, lead, H, dev)
+    kind, g = _check_decay(decay, log_decay, lead, H, index)
     if packed:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be one-dimensional with N + 1 entries")
-        N, T = cu_seqlens.numel() - 1, lead[0]
-        if device_status is not None:
-            _need(device_status, "device_status", torch.int32, dev)
+        N, T = _packed(cu_seqlens, device_status, index), lead[0]
     else:
         N, T = lead
-    _state(initial_state, "initial_state", (N, H, dk, dv), dev)
+    _state(initial_state, "initial_state", (N, H, dk, dv), index)
     name = "kda_linear_varlen_prefill" if packed else "kda_linear_prefill"
-    with _on(stream):
-        out = _out(out, "out", tuple(v.shape), v.dtype, dev)
-        if final_state is not None or output_final_state:
-            final_state = _out(final_state, "final_state", (N, H, dk, dv), torch.float32, dev)
-        ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), dev)
-    head = (_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale), _ptr(initial_state), _ptr(out),
-            _ptr(final_state))
+    out = _out(out, "out", v, v.shape, v.dtype, index)
+    if final_state is not None or output_final_state:
+        final_state = _out(final_state, "final_state", v, (N, H, dk, dv), torch.float32, index)
+    ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), v)
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, *strides, _ptr(g), kind, scale, _ptr(initial_state),
+            out.data_ptr(), _ptr(final_state))
     if packed:
-        st = lib.kda_linear_varlen_prefill(*head, _ptr(cu_seqlens), N, T, H, dk, dv, _ptr(ws), size,
-                                           _ptr(device_status), _stream(stream))
+        st = lib.kda_linear_varlen_prefill(*head, cu_seqlens.data_ptr(), N, T, H, dk, dv, ws.data_ptr(), size,
+                                           _ptr(device_status), _stream(index))
     else:
-        st = lib.kda_linear_prefill(*head, N, T, H, dk, dv, _ptr(ws), size, _stream(stream))
+        st = lib.kda_linear_prefill(*head, N, T, H, dk, dv, ws.data_ptr(), size, _stream(index))
     _check(lib, st)
     return out, final_state
 
 
+def _packed(cu_seqlens, device_status, index: int) -> int:
+    """Checks the arguments of a packed batch; returns the number of sequences."""
+    _plain(cu_seqlens, "cu_seqlens", torch.int32, index)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be one-dimensional with N + 1 entries")
+    if device_status is not None:
+        _plain(device_status, "device_status", torch.int32, index)
+    return cu_seqlens.numel() - 1
+
+
+@_on_stream
 def linear_prefill(q, k, v, log_decay=None, initial_state=None, *, decay: str = "token", scale: float = 1.0,
-                   output_final_state: bool = True, out=None, final_state=None, workspace=None, stream=None):
+                   output_final_state: bool = True, out=None, final_state=None, workspace=None):
     """Linear attention with a decay over B equal-length sequences:
     S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
 
@@ -212,12 +226,13 @@ def linear_prefill(q, k, v, log_decay=None, initial_state=None, *, decay: str = 
     Returns (o [B, T, H, d_v] in v's type, final_state fp32 or None).
     """
     return _prefill(q, k, v, log_decay, None, initial_state, decay, scale, output_final_state, out, final_state,
-                    workspace, None, stream)
+                    workspace, None)
 
 
+@_on_stream
 def linear_varlen_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, *, decay: str = "token",
                           scale: float = 1.0, output_final_state: bool = True, out=None, final_state=None,
-                          workspace=None, device_status=None, stream=None):
+                          workspace=None, device_status=None):
     """``linear_prefill`` over N sequences packed along the token axis:
     q, k: [T_total, H, d_k]; v: [T_total, H, d_v]; log_decay [T_total, H]
     (decay="token"); cu_seqlens: int32 [N + 1] on the device; initial_state:
@@ -226,54 +241,46 @@ def linear_varlen_prefill(q, k, v, log_decay, cu_seqlens, initial_state=None, *,
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _prefill(q, k, v, log_decay, cu_seqlens, initial_state, decay, scale, output_final_state, out, final_state,
-                    workspace, device_status, stream)
+                    workspace, device_status)
 
 
 def _backward(q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state, decay, scale, want_decay_grad,
-              want_initial_state_grad, workspace, device_status, stream):
+              want_initial_state_grad, workspace, device_status):
     lib = load()
     packed = cu_seqlens is not None
-    dev, lead, H, dk, dv, strides = _qkv(q, k, v, 1 if packed else 2)
+    index, lead, H, dk, dv, strides = _qkv(q, k, v, 1 if packed else 2)
     code = _dtype_code(q)
-    kind, g = _check_decay(decay, log_decay, lead, H, dev)
-    _need(d_o, "d_o", q.dtype, dev)
-    if d_o.shape != v.shape:
-        raise ValueError(f"d_o must be {tuple(v.shape)}, got {tuple(d_o.shape)}")
+    kind, g = _check_decay(decay, log_decay, lead, H, index)
+    _plain(d_o, "d_o", q.dtype, index, v.shape)
     if packed:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be one-dimensional with N + 1 entries")
-        N, T = cu_seqlens.numel() - 1, lead[0]
-        if device_status is not None:
-            _need(device_status, "device_status", torch.int32, dev)
+        N, T = _packed(cu_seqlens, device_status, index), lead[0]
     else:
         N, T = lead
     for t, n in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
-        _state(t, n, (N, H, dk, dv), dev)
+        _state(t, n, (N, H, dk, dv), index)
     name = "kda_linear_varlen_prefill_backward" if packed else "kda_linear_prefill_backward"
-    with _on(stream):
-        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
-               "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
-               "dv": torch.empty(v.shape, dtype=q.dtype, device=dev),
-               "dlog_decay": torch.empty_like(g) if g is not None and want_decay_grad else None,
-               "d_initial_state": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-               if want_initial_state_grad else None}
-        ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), dev)
-    head = (_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale), _ptr(initial_state), _ptr(d_o),
-            _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_decay"]),
-            _ptr(out["d_initial_state"]))
+    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+           "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
+           "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device),
+           "dlog_decay": torch.empty_like(g) if g is not None and want_decay_grad else None,
+           "d_initial_state": torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+           if want_initial_state_grad else None}
+    ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), q)
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, *strides, _ptr(g), kind, scale, _ptr(initial_state),
+            d_o.data_ptr(), _ptr(d_final_state), *(_ptr(t) for t in out.values()))
     if packed:
-        st = lib.kda_linear_varlen_prefill_backward(*head, _ptr(cu_seqlens), N, T, H, dk, dv, _ptr(ws), size,
-                                                    _ptr(device_status), _stream(stream))
+        st = lib.kda_linear_varlen_prefill_backward(*head, cu_seqlens.data_ptr(), N, T, H, dk, dv, ws.data_ptr(), size,
+                                                    _ptr(device_status), _stream(index))
     else:
-        st = lib.kda_linear_prefill_backward(*head, N, T, H, dk, dv, _ptr(ws), size, _stream(stream))
+        st = lib.kda_linear_prefill_backward(*head, N, T, H, dk, dv, ws.data_ptr(), size, _stream(index))
     _check(lib, st)
     return out
 
 
+@_on_stream
 def linear_prefill_backward(q, k, v, log_decay, d_o, initial_state=None, d_final_state=None, *, decay: str = "token",
                             scale: float = 1.0, want_decay_grad: bool = True, want_initial_state_grad: bool = True,
-                            workspace=None, stream=None):
+                            workspace=None):
     """Gradients of ``linear_prefill`` for L = sum <d_o, o> + <d_final_state, S_T>.
 
     d_o: o's shape and type; d_final_state: fp32 or None (zero). Returns a dict:
@@ -281,59 +288,58 @@ def linear_prefill_backward(q, k, v, log_decay, d_o, initial_state=None, d_final
     None without a decay or when not wanted; with decay="head" the sum over
     every token) and ``d_initial_state`` (fp32; None when not wanted)."""
     return _backward(q, k, v, log_decay, d_o, None, initial_state, d_final_state, decay, scale, want_decay_grad,
-                     want_initial_state_grad, workspace, None, stream)
+                     want_initial_state_grad, workspace, None)
 
 
+@_on_stream
 def linear_varlen_prefill_backward(q, k, v, log_decay, d_o, cu_seqlens, initial_state=None, d_final_state=None, *,
                                    decay: str = "token", scale: float = 1.0, want_decay_grad: bool = True,
-                                   want_initial_state_grad: bool = True, workspace=None, device_status=None,
-                                   stream=None):
+                                   want_initial_state_grad: bool = True, workspace=None, device_status=None):
     """Gradients of ``linear_varlen_prefill`` (packed sequences): the dict of
     ``linear_prefill_backward``."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _backward(q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state, decay, scale, want_decay_grad,
-                     want_initial_state_grad, workspace, device_status, stream)
+                     want_initial_state_grad, workspace, device_status)
 
 
-def linear_decode_step(q, k, v, log_decay, state, *, decay: str = "token", scale: float = 1.0, out=None, stream=None):
+@_on_stream
+def linear_decode_step(q, k, v, log_decay, state, *, decay: str = "token", scale: float = 1.0, out=None):
     """One token of ``linear_prefill`` per (sequence, head); ``state`` [N, H,
     d_k, d_v] fp32 is updated in place. q, k: [N, H, d_k]; v: [N, H, d_v];
     log_decay [N, H], [H] or None. Returns o [N, H, d_v]."""
     lib = load()
-    dev, (N,), H, dk, dv, strides = _qkv(q, k, v, 1)
-    code = _dtype_code(q)
-    kind, g = _check_decay(decay, log_decay, (N,), H, dev)
-    if state is None:
-        raise ValueError("state is required")
-    _state(state, "state", (N, H, dk, dv), dev)
-    with _on(stream):
-        out = _out(out, "out", tuple(v.shape), v.dtype, dev)
-    _check(lib, lib.kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale),
-                                           _ptr(state), _ptr(out), N, H, dk, dv, _stream(stream)))
+    index, (N,), H, dk, dv, strides = _qkv(q, k, v, 1)
+    kind, g = _check_decay(decay, log_decay, (N,), H, index)
+    _plain(state, "state", torch.float32, index, (N, H, dk, dv))
+    out = _out(out, "out", v, v.shape, v.dtype, index)
+    _check(lib, lib.kda_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), *strides, _ptr(g),
+                                           kind, scale, state.data_ptr(), out.data_ptr(), N, H, dk, dv,
+                                           _stream(index)))
     return out
 
 
+@_on_stream
 def linear_decode_step_slots(q, k, v, log_decay, state_pool, slots, *, decay: str = "token", scale: float = 1.0,
-                             out=None, device_status=None, stream=None):
+                             out=None, device_status=None):
     """``linear_decode_step`` on ``state_pool[slots[n]]`` ([P, H, d_k, d_v] fp32,
     updated in place; slots int32 [N], ``-1 - s`` starts slot s from zeros). A
     slot outside [0, P) is skipped and sets KDA_DEV_BAD_SLOT in ``device_status``."""
     lib = load()
-    dev, (N,), H, dk, dv, strides = _qkv(q, k, v, 1)
-    code = _dtype_code(q)
-    kind, g = _check_decay(decay, log_decay, (N,), H, dev)
-    _need(slots, "slots", torch.int32, dev)
-    _need(state_pool, "state_pool", torch.float32, dev)
-    if slots.shape != (N,) or state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, dk, dv):
-        raise ValueError("shape mismatch among q, k, v, slots, state_pool")
+    index, (N,), H, dk, dv, strides = _qkv(q, k, v, 1)
+    kind, g = _check_decay(decay, log_decay, (N,), H, index)
+    _plain(slots, "slots", torch.int32, index, (N,))
+    _plain(state_pool, "state_pool", torch.float32, index)
+    pool = state_pool.shape
+    if len(pool) != 4 or pool[1:] != (H, dk, dv):
+        raise ValueError(f"state_pool must be [P, {H}, {dk}, {dv}], got {tuple(pool)}")
     if device_status is not None:
-        _need(device_status, "device_status", torch.int32, dev)
-    with _on(stream):
-        out = _out(out, "out", tuple(v.shape), v.dtype, dev)
-    _check(lib, lib.kda_linear_decode_step_slots(_ptr(q), _ptr(k), _ptr(v), code, *strides, _ptr(g), kind, float(scale),
-                                                 _ptr(state_pool), _ptr(slots), state_pool.shape[0], _ptr(out), N, H,
-                                                 dk, dv, _ptr(device_status), _stream(stream)))
+        _plain(device_status, "device_status", torch.int32, index)
+    out = _out(out, "out", v, v.shape, v.dtype, index)
+    _check(lib, lib.kda_linear_decode_step_slots(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), *strides,
+                                                 _ptr(g), kind, scale, state_pool.data_ptr(), slots.data_ptr(),
+                                                 pool[0], out.data_ptr(), N, H, dk, dv, _ptr(device_status),
+                                                 _stream(index)))
     return out
 
 
@@ -386,36 +392,38 @@ def _weight_grad_bytes(d: int) -> int:
     return int(load().kda_qk_norm_rope_backward_workspace_bytes(d))
 
 
-def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout):
+def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout, device_status):
     if q is None or q.dim() < 3:
         raise ValueError("q must be [.., H_q, d]")
     lead = q.dim() - 2
     qs = _view(q, "q", lead)
-    dev = q.device
-    ks = _view(k, "k", lead, q.dtype, dev)
-    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+    index, shape = q.get_device(), q.shape
+    ks = _view(k, "k", lead, q.dtype, index)
+    if k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]:
         raise ValueError("q and k must have the same leading axes and head size")
-    n, d = math.prod(q.shape[:-2]), q.shape[-1]
+    n, d = (shape[0] if lead == 1 else math.prod(shape[:-2])), shape[-1]
     rot, max_position = 0, 0
     if table is not None:
-        _need(table, "rope_table", torch.float32, dev)
-        _need(positions, "positions", torch.int32, dev)
-        if table.dim() != 2 or positions.shape != q.shape[:-2]:
+        _plain(table, "rope_table", torch.float32, index)
+        _plain(positions, "positions", torch.int32, index)
+        if table.dim() != 2 or positions.shape != shape[:-2]:
             raise ValueError("rope_table must be [max_position, rotary] and positions have q's leading axes")
         max_position, rot = table.shape
     elif positions is not None:
         raise ValueError("positions need a rope_table")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.float32, dev)
-            if w.shape != (d,):
-                raise ValueError(f"{name} must be {(d,)}, got {tuple(w.shape)}")
-    return (dev, n, d, q.shape[-2], k.shape[-2], _dtype_code(q), qs, ks, max_position, rot,
+    if q_weight is not None:
+        _plain(q_weight, "q_weight", torch.float32, index, (d,))
+    if k_weight is not None:
+        _plain(k_weight, "k_weight", torch.float32, index, (d,))
+    if device_status is not None:
+        _plain(device_status, "device_status", torch.int32, index)
+    return (index, n, d, shape[-2], k.shape[-2], _dtype_code(q), qs, ks, max_position, rot,
             _kind(ROPE_LAYOUTS, layout, "layout"), _kind(NORMS, norm, "norm"))
 
 
+@_on_stream
 def qk_norm_rope(q, k, positions=None, rope_table=None, q_weight=None, k_weight=None, *, norm: str = "rms",
-                 eps: float = 1e-6, layout: str = "half", q_out=None, k_out=None, device_status=None, stream=None):
+                 eps: float = 1e-6, layout: str = "half", q_out=None, k_out=None, device_status=None):
     """The norm of every query and key head and the rotary positions, in one
     pass: w * x / norm(x), then the first ``rope_table.shape[1]`` channels turned.
 
@@ -429,45 +437,37 @@ def qk_norm_rope(q, k, positions=None, rope_table=None, q_weight=None, k_weight=
     outside the table is left out and sets KDA_DEV_BAD_POSITION in
     ``device_status`` (int32 [1])."""
     lib = load()
-    dev, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
-                                                                         k_weight, norm, layout)
-    if device_status is not None:
-        _need(device_status, "device_status", torch.int32, dev)
-    with _on(stream):
-        q_out = _out(q_out, "q_out", tuple(q.shape), q.dtype, dev)
-        k_out = _out(k_out, "k_out", tuple(k.shape), q.dtype, dev)
-    _check(lib, lib.kda_qk_norm_rope(_ptr(q), _ptr(k), code, qs, ks, _ptr(positions), _ptr(rope_table), P, rot, lay,
-                                     _ptr(q_weight), _ptr(k_weight), nk, float(eps), _ptr(q_out), _ptr(k_out), n, hq,
-                                     hk, d, _ptr(device_status), _stream(stream)))
+    index, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
+                                                                           k_weight, norm, layout, device_status)
+    q_out = _out(q_out, "q_out", q, q.shape, q.dtype, index)
+    k_out = _out(k_out, "k_out", k, k.shape, q.dtype, index)
+    _check(lib, lib.kda_qk_norm_rope(q.data_ptr(), k.data_ptr(), code, qs, ks, _ptr(positions), _ptr(rope_table), P, rot,
+                                     lay, _ptr(q_weight), _ptr(k_weight), nk, eps, q_out.data_ptr(), k_out.data_ptr(),
+                                     n, hq, hk, d, _ptr(device_status), _stream(index)))
     return q_out, k_out
 
 
+@_on_stream
 def qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope_table=None, q_weight=None, k_weight=None, *,
                           norm: str = "rms", eps: float = 1e-6, layout: str = "half", workspace=None,
-                          device_status=None, stream=None):
+                          device_status=None):
     """Gradients of ``qk_norm_rope`` for L = sum <dq_out, q_out> + <dk_out, k_out>
     (dq_out, dk_out contiguous, in q's type). Returns a dict: ``dq``, ``dk`` in
     q's type, ``dq_weight``, ``dk_weight`` (fp32 [d]; None without that weight)."""
     lib = load()
-    dev, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
-                                                                         k_weight, norm, layout)
-    for t, x, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        _need(t, name, q.dtype, dev)
-        if t.shape != x.shape:
-            raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(t.shape)}")
-    if device_status is not None:
-        _need(device_status, "device_status", torch.int32, dev)
-    with _on(stream):
-        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
-               "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
-               "dq_weight": None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev),
-               "dk_weight": None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)}
-        ws, size = None, 0
-        if q_weight is not None or k_weight is not None:
-            ws, size = _space(workspace, _weight_grad_bytes(d), dev)
-    _check(lib, lib.kda_qk_norm_rope_backward(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), code, qs, ks,
-                                              _ptr(positions), _ptr(rope_table), P, rot, lay, _ptr(q_weight),
-                                              _ptr(k_weight), nk, float(eps), _ptr(out["dq"]), _ptr(out["dk"]),
-                                              _ptr(out["dq_weight"]), _ptr(out["dk_weight"]), n, hq, hk, d, _ptr(ws),
-                                              size, _ptr(device_status), _stream(stream)))
+    index, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
+                                                                           k_weight, norm, layout, device_status)
+    _plain(dq_out, "dq_out", q.dtype, index, q.shape)
+    _plain(dk_out, "dk_out", q.dtype, index, k.shape)
+    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+           "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
+           "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+           "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
+    ws, size = None, 0
+    if q_weight is not None or k_weight is not None:
+        ws, size = _space(workspace, _weight_grad_bytes(d), q)
+    _check(lib, lib.kda_qk_norm_rope_backward(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), code, qs,
+                                              ks, _ptr(positions), _ptr(rope_table), P, rot, lay, _ptr(q_weight),
+                                              _ptr(k_weight), nk, eps, *(_ptr(t) for t in out.values()), n, hq, hk, d,
+                                              _ptr(ws), size, _ptr(device_status), _stream(index)))
     return out
