@@ -95,9 +95,10 @@ struct LinBlock {
     int len;    // tokens (0: no such block, nothing to do)
 };
 struct LinGeom {
-    const int4 *blocks;        // packed: {seq, start, len, 0} per block, else null
+    const int4 *blocks;        // packed: {seq, start, len, 0} per block, in the order they are worked on, else null
     const int32_t *seq_block;  // packed: first block of each sequence [N + 1]
     const int32_t *status;     // packed: nonzero = bad cu_seqlens, nothing is written
+    const int32_t *place;      // packed, nullable: where in `blocks` the i-th block from the front of the batch is
     int N, T, H;               // equal lengths: T tokens each; packed: T_total
     int sb;                    // tokens per block, a multiple of kLinChunk
     int per_seq;               // equal lengths: blocks per sequence
@@ -115,7 +116,7 @@ __device__ __forceinline__ LinBlock lin_block(const LinGeom &g, int b) {
     const int off = i * g.sb;
     return {n, n * g.T + off, min(g.sb, g.T - off)};
 }
-// Blocks [first, last) of sequence n.
+// Blocks [first, last) of sequence n, counted from the front of the batch.
 __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &first, int &last) {
     if (g.blocks) {
         first = __ldg(g.seq_block + n);
