@@ -510,60 +510,44 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 }
 
 // ================================================================ outputs
-// One item is 128 output rows of a block and head; its operands pass through a
-// ring of six 32 KB slots in the order S, x, (y, z) of every 128-token tile of
-// the block that the rows see. Two contexts (an MMA-issuing warp, 256 row
-// threads, one O and one P accumulator in TMEM each) take turns with the items,
-// so that one context's products run while the other's rows are being scaled.
+// What the backward with a gradient of the log decay runs: dv, and dq and dk
+// with their row dots. One item is a block of one or two 128-token tiles, and a
+// head. Two contexts (an MMA-issuing warp, 256 row threads, one O and one P
+// accumulator in TMEM each) take its two tiles of rows: the near one sees its own
+// tokens alone, the far one those of both tiles (in reverse time the second tile
+// is the near one); they change places from item to item. The operands pass
+// through a ring of six 32 KB slots: S, the near tile's x, the far one's, then y
+// and z of the near tile and of the far one, all but x read by both.
 // Two threads share a row, a half of the columns each.
 //   O = x S, rows scaled by the decay from the block's edge (in TMEM);
 //   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place (each half
 //   of the columns into the front of its own half);
 //   O += P z, P read from TMEM.
 // P and S are the two roundings to bf16 (2^-9 relative each, as small as the
-// rounding of the result itself); sums are fp32. Bound by memory.
+// rounding of the result itself); sums are fp32.
 //
 // DOTS adds w_i . out_i per row, for the gradient of the decay, to fp32
 // accuracy: its state part from all three parts of S, and the rest not from
 // the rounded P but as sum_j c D_ij (x_i . y_j) (w_i . z_j), both dots exact in
-// bf16 with fp32 sums. That takes the order S (3 parts), x, w, (y, z) and a
+// bf16 with fp32 sums. That takes S in three parts, w after each x, and a
 // second score accumulator, so the scores go 64 columns at a time.
 //
-// x and w stay until the item's last scores. A block has at most two tiles,
-// so an item's last load is at most five after its x, and the ring of six
-// always has a slot for it. A slot has a full barrier for each context, so that
-// a context that waits for its own loads alone sees every phase of its barriers
-// (of one shared barrier it would miss those of the other's loads, and a
-// parity wait cannot tell a phase from the one two before it).
+// A slot is filled again when both contexts are done with it; both wait for
+// every load in turn, used or not, and so see every phase of the slots' barriers
+// (a parity wait cannot tell a phase from the one two before it). x and w stay
+// until their tile's last scores; the order of the loads lets a far y or z take
+// a near x's or w's place (checked with a model of the roles).
 static_assert(kLinMaxBlock <= 256, "the slot ring holds an item of two tiles");
 constexpr int AT_SLOT = 128 * D * 2;  // 32 KB
 constexpr int AT_SLOTS = 6;
 constexpr int AT_THREADS = 640;
-constexpr int AT_PREFIX = 4;                                         // items whose prefix sums are kept
+constexpr int AT_PREFIX = 4;                                         // blocks whose prefix sums are kept
 constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [AT_PREFIX][kLinMaxBlock + 2]
 constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // column factors [16 warps][kLinMaxBlock / 2]
 constexpr int AT_BAR = AT_COL + 16 * kLinMaxBlock / 2 * 4;
-enum { AB_FULL = 0, AB_EMPTY = 12, AB_O_IN = 18, AB_O_FULL = 20, AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26,
-       AB_A_FULL = 28, AB_A_EMPTY = 32, AB_COUNT = 36 };
+enum { AB_FULL = 0, AB_EMPTY = 6, AB_O_IN = 12, AB_O_FULL = 14, AB_O_EMPTY = 16, AB_P_FULL = 18, AB_P_READY = 20,
+       AB_A_FULL = 22, AB_A_EMPTY = 26, AB_COUNT = 30 };
 constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
-
-// Phases of a context's full barriers: `done` has a bit per slot, the parity of
-// the loads of the context's earlier items; an item whose first load is n0 uses
-// a slot a second time from its seventh load on.
-struct Loads {
-    uint64_t *full;
-    uint32_t done;
-    int n0;
-    __device__ __forceinline__ uint64_t *bar(int i) const { return full + i % AT_SLOTS; }
-    __device__ __forceinline__ uint32_t parity(int i) const {
-        return ((done >> (i % AT_SLOTS)) & 1u) ^ (i - n0 >= AT_SLOTS ? 1u : 0u);
-    }
-    __device__ __forceinline__ void next(int count) {  // the item is done
-        for (int i = n0; i < n0 + count; ++i) done ^= 1u << (i % AT_SLOTS);
-        n0 += count;
-    }
-    __device__ __forceinline__ void skip(int count) { n0 += count; }
-};
 
 struct AttendTcArgs {
     LinGeom geo;
@@ -574,29 +558,21 @@ struct AttendTcArgs {
     float *dot, *dot_state;
     int64_t dot_stride;  // between the two column halves' sums
     int state_rows;      // rows of one part of S
-    int items;           // two 128-row tiles per block and head
+    int items;           // blocks and heads
 };
 struct Item {
     LinBlock blk;
-    int b, h, i0, first, count;  // first row; first tile of y, z and how many
+    int b, h, tiles, near;
+    // the t-th tile: the near one, then the far one
+    __device__ __forceinline__ int tile(int t) const { return t ? 1 - near : near; }
 };
 template <bool REV> __device__ __forceinline__ Item item_of(const AttendTcArgs &p, int it) {
     Item x;
-    const int r = p.geo.by_heads.div(it);
-    x.h = it - r * p.geo.H;
-    x.b = r / 2;  // two tiles to a block
-    const int tile = r & 1;
+    x.b = p.geo.by_heads.div(it);
+    x.h = it - x.b * p.geo.H;
     x.blk = lin_block(p.geo, x.b);
-    x.i0 = tile * 128;
-    if (x.i0 >= x.blk.len) {
-        x.first = x.count = 0;
-    } else if (REV) {
-        x.first = tile;
-        x.count = (x.blk.len + 127) / 128 - tile;
-    } else {
-        x.first = 0;
-        x.count = tile + 1;
-    }
+    x.tiles = (x.blk.len + 127) / 128;
+    x.near = REV ? x.tiles - 1 : 0;
     return x;
 }
 
@@ -607,7 +583,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                      const __grid_constant__ CUtensorMap mw) {
     constexpr int SUB = DOTS ? 64 : 128;      // score columns at a time
     constexpr int NS = DOTS ? 3 : 1;          // parts of S
-    constexpr int HEAD = DOTS ? NS + 2 : 2;   // loads before the first y
+    constexpr int XW = DOTS ? 2 : 1;          // loads of a tile's rows
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + AT_BAR);
@@ -619,8 +595,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         *ab.flag = 0;
         for (int i = 0; i < AT_SLOTS; ++i) {
             mbar_init(bar + AB_FULL + i, 1);
-            mbar_init(bar + AB_FULL + AT_SLOTS + i, 1);
-            mbar_init(bar + AB_EMPTY + i, 1);
+            mbar_init(bar + AB_EMPTY + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + AB_O_IN + i, 1);
@@ -631,7 +606,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         }
         for (int i = 0; i < AT_PREFIX; ++i) {
             mbar_init(bar + AB_A_FULL + i, 1);
-            mbar_init(bar + AB_A_EMPTY + i, 8);
+            mbar_init(bar + AB_A_EMPTY + i, 16);
         }
         fence_mbar_init();
     }
@@ -647,13 +622,14 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 
     if (warp == 0) {
         if (lane == 0) {
-            int n = 0, c = 0;
+            int n = 0;
             uint64_t *f = nullptr;  // the barrier of the slot's load
             auto slot = [&]() -> unsigned char * {
                 const int s = n % AT_SLOTS;
-                if (!(ok = ab.wait(bar + AB_EMPTY + s, ((n / AT_SLOTS) & 1) ^ 1))) return nullptr;
-                f = bar + AB_FULL + c * AT_SLOTS + s;
+                if (!(ok = ok && ab.wait(bar + AB_EMPTY + s, ((n / AT_SLOTS) & 1) ^ 1))) return nullptr;
+                f = bar + AB_FULL + s;
                 mbar_arrive_expect_tx(f, AT_SLOT);
+                ++n;
                 return sm + s * AT_SLOT;
             };
             auto rows = [&](const CUtensorMap *m, int h, int tok) {  // 128 tokens in 64-token, 64-channel boxes
@@ -663,25 +639,23 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) tma_load_3d(d + x * 16384 + t * 8192, m, f, 64 * x, h, tok + 64 * t);
-                ++n;
             };
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const Item x = item_of<REV>(p, it);
-                if (x.count == 0) continue;
-                for (int part = 0; part < NS && ok; ++part)
+                for (int part = NS - 1; part >= 0 && x.tiles > 0; --part)  // the lowest part first
                     if (unsigned char *d = slot()) {
                         const int row = part * p.state_rows + (x.b * geo.H + x.h) * D;
                         tma_load_2d(d, &ms, f, 0, row);
                         tma_load_2d(d + 16384, &ms, f, 64, row);
-                        ++n;
                     }
-                if (ok) rows(&mx, x.h, x.blk.start + x.i0);
-                if (DOTS && ok) rows(&mw, x.h, x.blk.start + x.i0);
-                for (int j = 0; j < x.count && ok; ++j) {
-                    rows(&my, x.h, x.blk.start + (x.first + j) * 128);
-                    if (ok) rows(&mz, x.h, x.blk.start + (x.first + j) * 128);
+                for (int t = 0; t < x.tiles; ++t) {
+                    rows(&mx, x.h, x.blk.start + 128 * x.tile(t));
+                    if (DOTS) rows(&mw, x.h, x.blk.start + 128 * x.tile(t));
                 }
-                c ^= 1;
+                for (int t = 0; t < x.tiles; ++t) {
+                    rows(&my, x.h, x.blk.start + 128 * x.tile(t));
+                    rows(&mz, x.h, x.blk.start + 128 * x.tile(t));
+                }
             }
         }
     } else if (warp == 1 || warp == 2) {
@@ -690,40 +664,47 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             constexpr uint32_t I_S = idesc_bf16(128, 128, false, !ST), I_P = idesc_bf16(128, SUB, false, false),
                                I_O = idesc_bf16(128, 128, false, true);
             const uint32_t to = tmem + c * 256, tp = to + 128, tp2 = tp + SUB;
-            Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
-            int k = 0, q = 0, np = 0;  // items so far, items and score tiles of this context
+            int n = 0, k = 0, q = 0, np = 0;  // loads and items before this one, tiles and pieces of this context
+            auto full = [&](int i) { return ok = ab.wait(bar + AB_FULL + i % AT_SLOTS, (i / AT_SLOTS) & 1); };
+            auto base = [&](int i) { return smem_u32(sm + (i % AT_SLOTS) * AT_SLOT); };
+            auto free_slot = [&](int i) { umma_commit(bar + AB_EMPTY + i % AT_SLOTS); };
+            auto skip = [&](int first, int last) {  // loads that only the other context uses
+                for (int i = first; i < last && ok; ++i)
+                    if (full(i)) mbar_arrive(bar + AB_EMPTY + i % AT_SLOTS);
+            };
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const Item x = item_of<REV>(p, it);
-                if (x.count == 0) continue;
-                const int loads = HEAD + 2 * x.count;
-                if ((k++ & 1) != c) {
-                    ld.skip(loads);
+                if (x.tiles == 0) continue;
+                const bool near = (k++ & 1) == c;
+                const int ny0 = n + NS + XW * x.tiles, end = ny0 + 2 * x.tiles;
+                if (!near && x.tiles == 1) {
+                    skip(n, end);
+                    n = end;
                     continue;
                 }
-                const int n = ld.n0;
-                auto full = [&](int i) { return ab.wait(ld.bar(i), ld.parity(i)); };
-                auto base = [&](int i) { return smem_u32(sm + (i % AT_SLOTS) * AT_SLOT); };
-                auto free_slot = [&](int i) { umma_commit(bar + AB_EMPTY + i % AT_SLOTS); };
-                if (!(ok = ab.wait(bar + AB_O_EMPTY + c, (q & 1) ^ 1) && full(n + NS))) break;
-                const uint64_t xd = desc_k(base(n + NS));
-                for (int part = NS - 1; part >= 0 && ok; --part) {  // the lowest part first, while the sum is small
-                    if (!(ok = full(n + part))) break;
-                    tc_fence_after();
-                    const uint64_t sd = ST ? desc_k(base(n + part)) : desc_mn(base(n + part), 16384);
-                    if (part == NS - 1) mma_ss<false>(to, xd, sd, I_S);
+                const int count = near ? 1 : 2, nx = n + NS + (near ? 0 : XW);
+                if (!(ok = ab.wait(bar + AB_O_EMPTY + c, (q & 1) ^ 1))) break;
+                for (int i = n; i < n + NS && ok; ++i) full(i);
+                skip(n + NS, nx);
+                if (!ok || !full(nx)) break;
+                tc_fence_after();
+                const uint64_t xd = desc_k(base(nx));
+                for (int i = 0; i < NS; ++i) {  // the lowest part first, while the sum is small
+                    const uint64_t sd = ST ? desc_k(base(n + i)) : desc_mn(base(n + i), 16384);
+                    if (i == 0) mma_ss<false>(to, xd, sd, I_S);
                     else mma_ss<true>(to, xd, sd, I_S);
 #pragma unroll
                     for (int ks = 1; ks < 8; ++ks)
                         mma_ss<true>(to, xd + step_k(ks, 16384), sd + (ST ? step_k(ks, 16384) : step_mn(ks)), I_S);
-                    free_slot(n + part);
+                    free_slot(n + i);
                 }
-                if (!ok) break;
                 umma_commit(bar + AB_O_IN + c);
-                if (DOTS && !(ok = full(n + NS + 1))) break;
-                const uint64_t wd = desc_k(base(n + NS + 1));
-                for (int j = 0; j < x.count && ok; ++j) {
-                    const int ny = n + HEAD + 2 * j;
-                    if (!(ok = full(ny) && (!DOTS || full(ny + 1)))) break;
+                if (DOTS && !full(nx + 1)) break;
+                const uint64_t wd = desc_k(base(nx + XW - 1));
+                if (near) skip(nx + XW, ny0);
+                for (int j = 0; j < count && ok; ++j) {
+                    const int ny = ny0 + 2 * j;
+                    if (!full(ny) || (DOTS && !full(ny + 1))) break;
                     const uint64_t yd = desc_k(base(ny)), zk = desc_k(base(ny + 1)), zd = desc_mn(base(ny + 1), 16384);
 #pragma unroll
                     for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
@@ -741,10 +722,11 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                         }
                         if (sub == 128 / SUB - 1) {
                             free_slot(ny);
-                            if (j == x.count - 1) free_slot(n + NS);
+                            if (j == count - 1) free_slot(nx);
                         }
                         umma_commit(bar + AB_P_FULL + c);
-                        if (!(ok = full(ny + 1) && ab.wait(bar + AB_P_READY + c, np & 1))) break;
+                        if (!DOTS && !full(ny + 1)) break;
+                        if (!(ok = ab.wait(bar + AB_P_READY + c, np & 1))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < SUB / 16; ++ks)
@@ -754,18 +736,19 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                     if (ok) free_slot(ny + 1);
                 }
                 if (!ok) break;
-                if (DOTS) free_slot(n + NS + 1);  // the row threads read it before their last P_READY
+                if (DOTS) free_slot(nx + 1);  // the row threads read it before their last P_READY
                 umma_commit(bar + AB_O_FULL + c);
-                ld.next(loads);
+                skip(ny0 + 2 * count, end);
+                n = end;
                 ++q;
             }
         }
     } else if (warp == 3) {
-        // prefix sums of the items' log decays, up to four items ahead
+        // prefix sums of the items' log decays, up to four of them ahead
         int k = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x = item_of<REV>(p, it);
-            if (x.count == 0) continue;
+            if (x.tiles == 0) continue;
             constexpr int PER = kLinMaxBlock / 32;
             long long s[PER];
             warp_decay<PER>(geo, p.log_decay, p.decay, x.blk, x.h, s);
@@ -785,32 +768,34 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         float *col = reinterpret_cast<float *>(sm + AT_COL) + (warp - 4) * (kLinMaxBlock / 2);
         const uint32_t to = tmem + c * 256 + ((uint32_t)w << 21), tp = to + 128, tp2 = tp + SUB;
         auto wait = [&](uint64_t *b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(b, ph)); };
-        Loads ld{bar + AB_FULL + c * AT_SLOTS, 0u, 0};
-        int k = 0, q = 0, np = 0;
+        auto full = [&](int i) { return wait(bar + AB_FULL + i % AT_SLOTS, (i / AT_SLOTS) & 1); };
+        int n = 0, k = 0, q = 0, np = 0;  // loads and items before this one, tiles and pieces of this context
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x = item_of<REV>(p, it);
-            if (x.count == 0) continue;
-            const int loads = HEAD + 2 * x.count;
-            const int slot = k % AT_PREFIX, slot_ph = (k / AT_PREFIX) & 1;
-            if ((k++ & 1) != c) {
-                ld.skip(loads);
+            if (x.tiles == 0) continue;
+            const int slot = k % AT_PREFIX;
+            if (!wait(bar + AB_A_FULL + slot, (k / AT_PREFIX) & 1)) break;
+            const bool near = (k++ & 1) == c;
+            const int ny0 = n + NS + XW * x.tiles, nw = n + NS + (near ? 1 : XW + 1), count = near ? 1 : 2;
+            n = ny0 + 2 * x.tiles;
+            if (!near && x.tiles == 1) {
+                warp_arrive(bar + AB_A_EMPTY + slot);
                 continue;
             }
-            const int n = ld.n0;
-            if (!wait(bar + AB_A_FULL + slot, slot_ph)) break;
             const float2 *a = reinterpret_cast<const float2 *>(sm + AT_A) + slot * (kLinMaxBlock + 2);
-            const int i = x.i0 + r, len = x.blk.len;
+            const int i0 = 128 * x.tile(near ? 0 : 1), i = i0 + r, len = x.blk.len;
             const float2 ai = a[min(i, len - 1) + 1];
             const float f = p.c_state * (REV ? decay_ratio(a[len], ai) : decay_ratio(ai, make_float2(0.f, 0.f)));
             // D_ij = row factor x column factor for the columns on the far side of the warp's 32 rows, the
             // decays to and from their edge (both <= 1); only the 32 x 32 piece on the diagonal takes an
             // exponential per element
-            const int i32 = x.i0 + 32 * w;
+            const int i32 = i0 + 32 * w;
             const float2 edge = a[REV ? i32 + 32 : i32];
             const float rf = p.c_intra * (REV ? decay_ratio(edge, ai) : decay_ratio(ai, edge));
 #pragma unroll
             for (int u = 0; u < kLinMaxBlock / 64; ++u) {  // the u-th 32 of this thread's columns
-                const int j = (x.first * 128 + (32 * u / HSUB) * SUB + hf * HSUB + 32 * u % HSUB + lane) % kLinMaxBlock;
+                const int o = (32 * u / HSUB) * SUB + hf * HSUB + 32 * u % HSUB + lane;
+                const int j = 128 * x.tile(o >> 7) + (o & 127);
                 col[32 * u + lane] = REV ? (j >= i32 + 32 ? decay_ratio(a[j + 1], edge) : 0.f)
                                          : (j < i32 ? decay_ratio(edge, a[j + 1]) : 0.f);
             }
@@ -818,8 +803,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             const F2 rf2 = f2(rf, rf);
             F2 dots = f2(0.f, 0.f);
             float dot = 0.f, dot_state = 0.f;
-            if (DOTS && !wait(ld.bar(n + NS + 1), ld.parity(n + NS + 1))) break;
-            if (!wait(bar + AB_O_IN + c, q & 1)) break;
+            if (!wait(bar + AB_O_IN + c, q & 1) || (DOTS && !full(nw))) break;
             tc_fence_after();
             {
                 uint32_t v[2][32];
@@ -831,7 +815,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                     scale32(v[u], f);
                     tmem_st32(to + 64 * hf + 32 * u, v[u]);
                     if (DOTS) {
-                        const unsigned char *wt = sm + ((n + NS + 1) % AT_SLOTS) * AT_SLOT;
+                        const unsigned char *wt = sm + (nw % AT_SLOTS) * AT_SLOT;
 #pragma unroll
                         for (int k8 = 0; k8 < 4; ++k8) {
                             const uint4 g =
@@ -845,13 +829,13 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                     }
                 }
             }
-            for (int j = 0; j < x.count && ok; ++j) {
-                const int j0 = (x.first + j) * 128, nz = n + HEAD + 1 + 2 * j;
+            for (int j = 0; j < count && ok; ++j) {
+                const int j0 = 128 * x.tile(j), nz = ny0 + 2 * j + 1;
                 for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
                     if (!wait(bar + AB_P_FULL + c, np & 1)) break;
                     tc_fence_after();
                     if (sub == 0 && len - j0 < 128) {  // what lies past the block's end must not meet P's zeros
-                        if (!wait(ld.bar(nz), ld.parity(nz))) break;
+                        if (!full(nz)) break;
                         if (r >= len - j0) {
                             unsigned char *z = sm + (nz % AT_SLOTS) * AT_SLOT + hf * 16384 + r * 128;
 #pragma unroll
@@ -939,7 +923,6 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             }
             tc_fence_before();
             warp_arrive(bar + AB_O_EMPTY + c);
-            ld.next(loads);
             ++q;
         }
     }
@@ -1572,7 +1555,7 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
     mw = mx;
     if (dots && !token_map(&mw, a.w, a.w_stride, geo.H, a.tokens)) return cudaErrorInvalidValue;
     AttendTcArgs p{geo, a.log_decay, a.decay, (__nv_bfloat16 *)a.out, a.c_state, a.c_intra, a.dot, a.dot_state,
-                   a.tokens * geo.H, (int)rows, geo.nblocks * geo.H * 2};
+                   a.tokens * geo.H, (int)rows, geo.nblocks * geo.H};
     if (dots != a.state_t) return cudaErrorInvalidValue;  // what the backward asks for: dq, dk with dots, dv without
     auto k = !a.rev ? lin_attend_tc_kernel<false, true, true>
              : dots ? lin_attend_tc_kernel<true, true, true>
