@@ -52,7 +52,7 @@ __host__ __device__ constexpr int segment_tokens(int64_t len) {
 // sb = 0: segments of segment_tokens(length).
 constexpr int kPrepThreads = 1024;
 __global__ void __launch_bounds__(kPrepThreads)
-lin_blocks_kernel(const int32_t *__restrict__ cu, int N, int T_total, int sb, int nblocks, int4 *blocks,
+lin_blocks_kernel(const int32_t *cu, int N, int T_total, int sb, int nblocks, int4 *blocks,
                   int32_t *seq_block, int32_t *place, int32_t *status, int32_t *user_status) {
     constexpr int kBuckets = 66;
     __shared__ int bad;
@@ -190,15 +190,26 @@ __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, in
     }
 }
 
+// Global to shared memory without waiting (joined by loads_done); `bytes` short
+// of the size: the rest is zero.
+template <int SIZE> __device__ __forceinline__ void load_async(void *dst, const void *src, int bytes) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (SIZE == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void loads_done() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+}
 // Rows of a [64][D] tile into shared memory; rows past `rows` are zero.
 template <typename T, int D>
 __device__ __forceinline__ void load_tile(T *dst, int ld, const T *src, int64_t stride, int rows) {
     constexpr int V = 16 / sizeof(T), PER = D / V;
     for (int i = threadIdx.x; i < CH * PER; i += NT) {
         const int r = i / PER, c = (i % PER) * V;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) x = __ldg(reinterpret_cast<const uint4 *>(src + r * stride + c));
-        *reinterpret_cast<uint4 *>(dst + r * ld + c) = x;
+        load_async<16>(dst + r * ld + c, src + min(r, rows - 1) * stride + c, r < rows ? 16 : 0);
     }
 }
 // Leading dimensions that keep the fragment reads free of bank conflicts:
@@ -210,10 +221,15 @@ template <typename T> __host__ __device__ constexpr int ld_cols(int d) { return 
 // out[block][head] = sum_s w_s x_s y_s^T over the block's tokens: forward
 // w_s = e^{L_end - L_s} with (x, y) = (k, v); reverse w_s = e^{L_s} with
 // (q, do). Also e^{L_end} of the block (forward).
-template <typename T, int DK, int DV, bool REV>
-__global__ void __launch_bounds__(NT)
-lin_state_kernel(LinGeom geo, const T *__restrict__ x, int64_t x_stride, const T *__restrict__ y, int64_t y_stride,
-                 const float *__restrict__ log_decay, int decay, float *__restrict__ out, float *__restrict__ total) {
+template <typename T> struct StateArgs {
+    LinGeom geo;
+    const T *x, *y;
+    int64_t x_stride, y_stride;
+    const float *log_decay;
+    int decay;
+    float *out, *total;
+};
+template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void block_state(const StateArgs<T> &p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int WM = DK / 32, WN = NT / 32 / WM, COLS = DV / WN, N8 = COLS / 8;
     constexpr int LDX = ld_cols<T>(DK), LDY = ld_cols<T>(DV);
@@ -223,31 +239,27 @@ lin_state_kernel(LinGeom geo, const T *__restrict__ x, int64_t x_stride, const T
     float2 *a = reinterpret_cast<float2 *>(ys + CH * LDY);
     __shared__ long long scan[NT / 32];
     __shared__ float w[CH];
+    const LinGeom &geo = p.geo;
     const int b = blockIdx.x / geo.H, h = blockIdx.x % geo.H;
-    const LinBlock blk = lin_block(geo, b);
+    const LinBlock blk = lin_block<true>(geo, b);
     if (blk.len <= 0) return;
-    decay_prefix<NT>(log_decay, decay, blk.start, geo.H, h, blk.len, blk.len, a, scan);
+    load_tile<T, DK>(xs, LDX, p.x + blk.start * p.x_stride + h * DK, p.x_stride, blk.len);
+    load_tile<T, DV>(ys, LDY, p.y + blk.start * p.y_stride + h * DV, p.y_stride, blk.len);
+    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan);
     const float2 end = a[blk.len];
-    if (total && threadIdx.x == 0) total[(int64_t)b * geo.H + h] = decay_ratio(end, make_float2(0.f, 0.f));
+    if (p.total && threadIdx.x == 0) p.total[(int64_t)b * geo.H + h] = decay_ratio(end, make_float2(0.f, 0.f));
+    if (threadIdx.x < CH) {
+        const int s = min((int)threadIdx.x, blk.len - 1);
+        w[threadIdx.x] = REV ? decay_ratio(a[s + 1], make_float2(0.f, 0.f)) : decay_ratio(end, a[s + 1]);
+    }
+    loads_done();
     const int warp = threadIdx.x >> 5, r0 = (warp % WM) * 32, c0 = (warp / WM) * COLS;
     float acc[2][N8][4] = {};
-    for (int j0 = 0; j0 < blk.len; j0 += CH) {
-        const int rows = min(CH, blk.len - j0);
-        const int64_t tok = blk.start + j0;
-        __syncthreads();
-        load_tile<T, DK>(xs, LDX, x + tok * x_stride + h * DK, x_stride, rows);
-        load_tile<T, DV>(ys, LDY, y + tok * y_stride + h * DV, y_stride, rows);
-        if (threadIdx.x < CH) {
-            const int s = min(j0 + (int)threadIdx.x, blk.len - 1);
-            w[threadIdx.x] = REV ? decay_ratio(a[s + 1], make_float2(0.f, 0.f)) : decay_ratio(end, a[s + 1]);
-        }
-        __syncthreads();
-        product<CH, 2, N8, true, F32>(
-            acc, [&](int r, int k) { return to_f32(xs[k * LDX + r]) * w[k]; },
-            [&](int k, int c) { return to_f32(ys[k * LDY + c]); }, r0, c0);
-    }
+    product<CH, 2, N8, true, F32>(
+        acc, [&](int r, int k) { return to_f32(xs[k * LDX + r]) * w[k]; },
+        [&](int k, int c) { return to_f32(ys[k * LDY + c]); }, r0, c0);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float *dst = out + ((int64_t)b * geo.H + h) * DK * DV;
+    float *dst = p.out + ((int64_t)b * geo.H + h) * DK * DV;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -258,32 +270,45 @@ lin_state_kernel(LinGeom geo, const T *__restrict__ x, int64_t x_stride, const T
         }
 }
 
+// The backward needs both directions and neither fills the GPU: one launch.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(NT) lin_state_kernel(const StateArgs<T> fwd, const StateArgs<T> rev) {
+    after_previous();
+    if (blockIdx.y == 0) block_state<T, DK, DV, false>(fwd);
+    else block_state<T, DK, DV, true>(rev);
+}
+
 // ---------------------------------------------------------------- joining the blocks
 // In place, along each (sequence, head): forward, every block's own sum gives
 // way to the state before the block, S <- e^{L_end} S + c own, and the last S
 // is the final state; reverse, to the gradient of the state after the block.
 // Elementwise over the state: one float4 per thread, the blocks in turn, four
 // loads ahead.
+struct ScanArgs {
+    float *states;
+    const float *s0;  // nullable
+    float *sT;        // nullable
+    float c;
+};
 template <bool REV>
-__global__ void __launch_bounds__(NT)
-lin_scan_kernel(LinGeom geo, float *__restrict__ states, const float *__restrict__ total, const float *__restrict__ s0,
-                float *__restrict__ sT, float c, int size4) {
+__device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &q, const float *total, int size4) {
+    const float c = q.c;
     if (geo.status && *geo.status != KDA_DEV_OK) return;
     const int per = size4 / NT;
     const int64_t nh = blockIdx.x / per;
     const int n = (int)(nh / geo.H), h = (int)(nh % geo.H);
     const int64_t e = (int64_t)(blockIdx.x % per) * NT + threadIdx.x;
     int first, last;
-    lin_seq_blocks(geo, n, first, last);
-    float4 S = s0 ? reinterpret_cast<const float4 *>(s0)[nh * size4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 *p = reinterpret_cast<float4 *>(states);
+    lin_seq_blocks<true>(geo, n, first, last);
+    float4 S = q.s0 ? reinterpret_cast<const float4 *>(q.s0)[nh * size4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 *p = reinterpret_cast<float4 *>(q.states);
     const int count = last - first;
     constexpr int AHEAD = 4;
     float4 own[AHEAD];
     float f[AHEAD];
     auto at = [&](int i) {
         const int b = REV ? last - 1 - i : first + i;
-        return (int64_t)(geo.place ? __ldg(geo.place + b) : b) * geo.H + h;
+        return (int64_t)(geo.place ? geo.place[b] : b) * geo.H + h;
     };
     for (int i0 = 0; i0 < count; i0 += AHEAD) {
 #pragma unroll
@@ -303,7 +328,18 @@ lin_scan_kernel(LinGeom geo, float *__restrict__ states, const float *__restrict
                 S.w = f[u] * S.w + c * own[u].w;
             }
     }
-    if (sT) reinterpret_cast<float4 *>(sT)[nh * size4 + e] = S;
+    if (q.sT) reinterpret_cast<float4 *>(q.sT)[nh * size4 + e] = S;
+}
+
+// The backward's two directions do not depend on each other: one launch (blockIdx.y).
+__global__ void __launch_bounds__(NT)
+lin_scan_kernel(const LinGeom geo, const ScanArgs fwd, const ScanArgs rev, const float *total, int size4) {
+    after_previous();
+    if (blockIdx.y == 0) {
+        if (fwd.states) scan_blocks<false>(geo, fwd, total, size4);
+    } else {
+        scan_blocks<true>(geo, rev, total, size4);
+    }
 }
 
 // ---------------------------------------------------------------- outputs
@@ -326,60 +362,79 @@ struct AttendArgs {
 // tokens j <= i of the block (reverse: j >= i); S is [DC][DO], or stored
 // [DO][DC] and read transposed (ST).
 // EXACT: the fp32 operands P and S are split too, for the row dots.
+template <typename T, int DC, int DO> constexpr size_t attend_smem() {
+    return 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (DO + 8) * 4 + CH * ld_cols<T>(DO) * sizeof(T) + (CH + 1) * 8;
+}
 template <typename T, int DC, int DO, bool REV, bool ST, bool EXACT>
-__global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
+__device__ __forceinline__ void attend_block(const AttendArgs &p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int LDX = ld_rows<T>(DC), LDZ = ld_cols<T>(DO), LDS = DO + 8, LDP = CH + 4, N8 = DO / 16;
+    static_assert(CH * LDP * 4 <= 2 * CH * LDX * (int)sizeof(T), "P takes the place of x and y");
     extern __shared__ __align__(16) unsigned char smem[];
     T *xs = reinterpret_cast<T *>(smem);
     T *ys = xs + CH * LDX;
-    float *ps = reinterpret_cast<float *>(ys + CH * LDX);
-    float *ss = ps + CH * LDP;               // a 64-row piece of the state, then the z tile
-    T *zs = reinterpret_cast<T *>(ss);
-    float2 *a = reinterpret_cast<float2 *>(ss + CH * LDS);
+    float *ps = reinterpret_cast<float *>(smem);
+    float *ss = reinterpret_cast<float *>(ys + CH * LDX);  // a 64-row piece of the state
+    T *zs = reinterpret_cast<T *>(ss + CH * LDS);
+    float2 *a = reinterpret_cast<float2 *>(zs + CH * LDZ);
     __shared__ long long scan[NT / 32];
     __shared__ float dots[2][2][CH];
     const LinGeom &geo = p.geo;
-    const int tiles = geo.sb / CH;
-    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % geo.H, b = blockIdx.x / tiles / geo.H;
-    const LinBlock blk = lin_block(geo, b);
-    const int i0 = tile * CH;
-    if (i0 >= blk.len) return;
-    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan);
+    const int h = blockIdx.x % geo.H, b = blockIdx.x / geo.H;
+    const LinBlock blk = lin_block<true>(geo, b);
+    const int len = blk.len;
+    if (len <= 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int r0 = (warp & 3) * 16, half = warp >> 2, c0 = half * (DO / 2);
-    const int irows = min(CH, blk.len - i0);
-    load_tile<T, DC>(xs, LDX, (const T *)p.x + (int64_t)(blk.start + i0) * p.x_stride + h * DC, p.x_stride, irows);
-
-    // the state part, 64 rows of the contraction at a time
-    float acc[1][N8][4] = {};
+    const int r0 = (warp & 3) * 16, half = warp >> 2, c0 = half * (DO / 2), s0 = half * 32;
+    const int64_t tok = blk.start;
     const float *S = p.states + ((int64_t)b * geo.H + h) * DC * DO;
-    for (int k0 = 0; k0 < DC; k0 += CH) {
-        __syncthreads();
+    auto load_state = [&](int k0) {
         if (!ST) {
             for (int i = threadIdx.x; i < CH * DO / 4; i += NT) {
                 const int r = i / (DO / 4), c = (i % (DO / 4)) * 4;
-                *reinterpret_cast<float4 *>(ss + r * LDS + c) =
-                    __ldg(reinterpret_cast<const float4 *>(S + (int64_t)(k0 + r) * DO + c));
+                load_async<16>(ss + r * LDS + c, S + (int64_t)(k0 + r) * DO + c, 16);
             }
         } else {
             for (int i = threadIdx.x; i < CH * DO; i += NT) {
                 const int r = i % CH, c = i / CH;
-                ss[r * LDS + c] = __ldg(S + (int64_t)c * DC + k0 + r);
+                load_async<4>(ss + r * LDS + c, S + (int64_t)c * DC + k0 + r, 4);
             }
         }
-        __syncthreads();
+    };
+    load_tile<T, DC>(xs, LDX, (const T *)p.x + tok * p.x_stride + h * DC, p.x_stride, len);
+    load_state(0);
+    load_tile<T, DC>(ys, LDX, (const T *)p.y + tok * p.y_stride + h * DC, p.y_stride, len);
+    load_tile<T, DO>(zs, LDZ, (const T *)p.z + tok * p.z_stride + h * DO, p.z_stride, len);
+    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, len, len, a, scan);
+    loads_done();
+
+    // the state part, 64 rows of the contraction at a time, and the scores
+    float acc[1][N8][4] = {}, sc[1][4][4] = {};
+    auto state_part = [&](int k0) {
         product<CH, 1, N8, F32, EXACT>(
             acc, [&](int r, int k) { return to_f32(xs[r * LDX + k0 + k]); },
             [&](int k, int c) { return ss[k * LDS + c]; }, r0, c0);
+    };
+    state_part(0);
+    if (DC > CH) {
+        __syncthreads();
+        load_state(CH);
     }
+    product<DC, 1, 4, F32, F32>(
+        sc, [&](int r, int k) { return to_f32(xs[r * LDX + k]); },
+        [&](int k, int c) { return to_f32(ys[c * LDX + k]); }, r0, s0);
+    if (DC > CH) {
+        loads_done();
+        state_part(CH);
+    }
+    __syncthreads();  // x and y are read: P may take their place
     auto row_dots = [&](float *dst) {  // w_i . acc_i over this warp's columns
         float d[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = r0 + g + 8 * e;
-            if (r < irows) {
-                const T *w = (const T *)p.w + (int64_t)(blk.start + i0 + r) * p.w_stride + h * DO;
+            if (r < len) {
+                const T *w = (const T *)p.w + (tok + r) * p.w_stride + h * DO;
 #pragma unroll
                 for (int n = 0; n < N8; ++n) {
                     const int c = c0 + 8 * n + 2 * t;
@@ -393,8 +448,8 @@ __global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
     };
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int i = min(i0 + r0 + g + 8 * e, blk.len - 1);
-        const float f = p.c_state * (REV ? decay_ratio(a[blk.len], a[i + 1])
+        const int i = min(r0 + g + 8 * e, len - 1);
+        const float f = p.c_state * (REV ? decay_ratio(a[len], a[i + 1])
                                          : decay_ratio(a[i + 1], make_float2(0.f, 0.f)));
 #pragma unroll
         for (int n = 0; n < N8; ++n) {
@@ -405,41 +460,26 @@ __global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
     if (p.dot_state) row_dots(dots[0][half]);
 
     // the block's own tokens
-    const int jfirst = REV ? i0 : 0, jlast = REV ? blk.len : i0 + CH;
-    for (int j0 = jfirst; j0 < jlast; j0 += CH) {
-        const int jrows = min(CH, blk.len - j0);
-        const int64_t tok = blk.start + j0;
-        __syncthreads();
-        load_tile<T, DC>(ys, LDX, (const T *)p.y + tok * p.y_stride + h * DC, p.y_stride, jrows);
-        load_tile<T, DO>(zs, LDZ, (const T *)p.z + tok * p.z_stride + h * DO, p.z_stride, jrows);
-        __syncthreads();
-        float sc[1][4][4] = {};
-        const int s0 = half * 32;
-        product<DC, 1, 4, F32, F32>(
-            sc, [&](int r, int k) { return to_f32(xs[r * LDX + k]); },
-            [&](int k, int c) { return to_f32(ys[c * LDX + k]); }, r0, s0);
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = r0 + g + 8 * (e >> 1), c = s0 + 8 * n + 2 * t + (e & 1);
-                const int i = i0 + r, j = j0 + c;
-                float v = 0.f;  // chosen, not multiplied: what lies past the end may be anything
-                if (i < blk.len && j < blk.len && (REV ? j >= i : j <= i))
-                    v = p.c_intra * sc[0][n][e] * (REV ? decay_ratio(a[j + 1], a[i + 1]) : decay_ratio(a[i + 1], a[j + 1]));
-                ps[r * LDP + c] = v;
-            }
-        __syncthreads();
-        product<CH, 1, N8, EXACT, F32>(
-            acc, [&](int r, int k) { return ps[r * LDP + k]; },
-            [&](int k, int c) { return to_f32(zs[k * LDZ + c]); }, r0, c0);
-    }
+        for (int e = 0; e < 4; ++e) {
+            const int i = r0 + g + 8 * (e >> 1), j = s0 + 8 * n + 2 * t + (e & 1);
+            float v = 0.f;  // chosen, not multiplied: what lies past the end may be anything
+            if (i < len && j < len && (REV ? j >= i : j <= i))
+                v = p.c_intra * sc[0][n][e] * (REV ? decay_ratio(a[j + 1], a[i + 1]) : decay_ratio(a[i + 1], a[j + 1]));
+            ps[i * LDP + j] = v;
+        }
+    __syncthreads();
+    product<CH, 1, N8, EXACT, F32>(
+        acc, [&](int r, int k) { return ps[r * LDP + k]; },
+        [&](int k, int c) { return to_f32(zs[k * LDZ + c]); }, r0, c0);
     if (p.dot) row_dots(dots[1][half]);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int r = r0 + g + 8 * e;
-        if (r >= irows) continue;
-        T *o = (T *)p.out + ((int64_t)(blk.start + i0 + r) * geo.H + h) * DO;
+        if (r >= len) continue;
+        T *o = (T *)p.out + ((tok + r) * geo.H + h) * DO;
 #pragma unroll
         for (int n = 0; n < N8; ++n) {
             const int c = c0 + 8 * n + 2 * t;
@@ -452,12 +492,27 @@ __global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
     }
     if (p.dot) {
         __syncthreads();
-        if ((int)threadIdx.x < irows) {
-            const int64_t i = (int64_t)(blk.start + i0 + threadIdx.x) * geo.H + h;
+        if ((int)threadIdx.x < len) {
+            const int64_t i = (tok + threadIdx.x) * geo.H + h;
             p.dot[i] = dots[1][0][threadIdx.x] + dots[1][1][threadIdx.x];
             if (p.dot_state) p.dot_state[i] = dots[0][0][threadIdx.x] + dots[0][1][threadIdx.x];
         }
     }
+}
+
+template <typename T, int DK, int DV> __global__ void __launch_bounds__(NT) lin_attend_kernel(const AttendArgs p) {
+    after_previous();
+    attend_block<T, DK, DV, false, false, sizeof(T) == 4>(p);
+}
+// The backward's three passes, each too small for the GPU, in one launch, the
+// longest first. EXACT: for the row dots.
+template <typename T, int DK, int DV, bool EXACT>
+__global__ void __launch_bounds__(NT)
+lin_attend_back_kernel(const AttendArgs dk, const AttendArgs dq, const AttendArgs dv) {
+    after_previous();
+    if (blockIdx.y == 0) attend_block<T, DV, DK, true, true, EXACT>(dk);
+    else if (blockIdx.y == 1) attend_block<T, DV, DK, false, true, EXACT>(dq);
+    else attend_block<T, DK, DV, true, false, sizeof(T) == 4>(dv);
 }
 
 // ---------------------------------------------------------------- gradient of the log decay
@@ -465,16 +520,17 @@ __global__ void __launch_bounds__(NT) lin_attend_kernel(AttendArgs p) {
 // X = e^{L_end} <S, G> + sum_j kdk_state_j. A reset (log decay at or below the
 // clamp) passes nothing on: its gradient is zero, not the sum's rounding.
 __global__ void __launch_bounds__(NT)
-lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int decay, const float *__restrict__ states,
-                      const float *__restrict__ grads, const float *__restrict__ inner,
-                      const float *__restrict__ total, int size4,
-                      const float *__restrict__ qdq, const float *__restrict__ kdk,
-                      const float *__restrict__ kdk_state, int64_t dot_stride, float *__restrict__ dg,
-                      float *__restrict__ block_sum) {
+lin_decay_grad_kernel(LinGeom geo, const float *log_decay, int decay, const float *states,
+                      const float *grads, const float *inner,
+                      const float *total, int size4,
+                      const float *qdq, const float *kdk,
+                      const float *kdk_state, int64_t dot_stride, float *dg,
+                      float *block_sum) {
+    after_previous();
     __shared__ float red[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / geo.H, h = blockIdx.x % geo.H;
-    const LinBlock blk = lin_block(geo, b);
+    const LinBlock blk = lin_block<true>(geo, b);
     const int64_t bh = (int64_t)b * geo.H + h;
     auto block_add = [&](float v) {
 #pragma unroll
@@ -493,12 +549,12 @@ lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int deca
     }
     float x = 0.f;
     if (inner) {  // <S, G> already summed up to kScanPartials pieces
-        if (tid < kScanPartials) x = __ldg(inner + bh * kScanPartials + tid);
+        if (tid < kScanPartials) x = inner[bh * kScanPartials + tid];
     } else {
         const float4 *S = reinterpret_cast<const float4 *>(states) + bh * size4;
         const float4 *G = reinterpret_cast<const float4 *>(grads) + bh * size4;
         for (int i = tid; i < size4; i += NT) {
-            const float4 s = __ldg(S + i), g = __ldg(G + i);
+            const float4 s = S[i], g = G[i];
             x += s.x * g.x + s.y * g.y + s.z * g.z + s.w * g.w;
         }
     }
@@ -546,7 +602,8 @@ lin_decay_grad_kernel(LinGeom geo, const float *__restrict__ log_decay, int deca
 
 // One decay per head: its gradient is the sum over every token, in block order.
 __global__ void __launch_bounds__(NT)
-lin_head_sum_kernel(LinGeom geo, const float *__restrict__ block_sum, float *__restrict__ dg) {
+lin_head_sum_kernel(LinGeom geo, const float *block_sum, float *dg) {
+    after_previous();
     __shared__ float red[NT];
     if (geo.status && *geo.status != KDA_DEV_OK) return;
     const int h = blockIdx.x;
@@ -638,55 +695,45 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
         if (e_ != cudaSuccess) return e_;       \
     } while (0)
 
-template <typename T, int DK, int DV, bool REV>
-cudaError_t run_states(const Plan &p, const void *x, int64_t xs, const void *y, int64_t ys, const LinArgs &a,
-                       float *out, cudaStream_t s) {
-    const size_t fixed = CH * (ld_cols<T>(DK) + ld_cols<T>(DV)) * sizeof(T);
-    const size_t smem = fixed + (p.geo.sb + 1) * sizeof(float2);
-    auto k = lin_state_kernel<T, DK, DV, REV>;
+// One direction (`back` false: the forward's) or both.
+template <typename T, int DK, int DV>
+cudaError_t run_states(const Plan &p, const LinArgs &a, bool back, Launches &l) {
+    constexpr size_t smem = CH * (ld_cols<T>(DK) + ld_cols<T>(DV)) * sizeof(T) + (CH + 1) * sizeof(float2);
+    auto k = lin_state_kernel<T, DK, DV>;
     static std::atomic<uint64_t> allowed{0};
-    KDA_TRY(allow_smem(k, fixed + (kLinMaxBlock + 1) * sizeof(float2), allowed));
-    k<<<(unsigned)((int64_t)p.geo.nblocks * p.geo.H), NT, smem, s>>>(p.geo, (const T *)x, xs, (const T *)y, ys,
-                                                                     a.log_decay, a.decay, out, REV ? nullptr : p.total);
-    return cudaGetLastError();
+    KDA_TRY(allow_smem(k, smem, allowed));
+    const StateArgs<T> f{p.geo, (const T *)a.k, (const T *)a.v, a.k_stride, a.v_stride, a.log_decay, a.decay, p.states,
+                         p.total};
+    const StateArgs<T> r{p.geo, (const T *)a.q, (const T *)a.d_o, a.q_stride, (int64_t)a.H * DV, a.log_decay, a.decay,
+                         p.grads, nullptr};
+    const dim3 grid((unsigned)((int64_t)p.geo.nblocks * p.geo.H), back ? 2 : 1);
+    return l.next(k, grid, NT, smem, f, r);
 }
-template <bool REV>
-cudaError_t run_scan(const Plan &p, float *states, const float *s0, float *sT, float c, int dk, int dv,
-                     cudaStream_t s) {
+// `rev` null: forward alone.
+cudaError_t run_scan(const Plan &p, const ScanArgs &fwd, const ScanArgs *rev, int dk, int dv, Launches &l) {
     const int size4 = dk * dv / 4;
-    lin_scan_kernel<REV><<<(unsigned)((int64_t)p.geo.N * p.geo.H * (size4 / NT)), NT, 0, s>>>(p.geo, states, p.total,
-                                                                                            s0, sT, c, size4);
-    return cudaGetLastError();
-}
-template <typename T, int DC, int DO, bool REV, bool ST, bool EXACT>
-cudaError_t run_attend(const AttendArgs &p, cudaStream_t s) {
-    const size_t fixed = 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (CH + 4) * 4 + CH * (DO + 8) * 4;
-    const size_t smem = fixed + (p.geo.sb + 1) * sizeof(float2);
-    auto k = lin_attend_kernel<T, DC, DO, REV, ST, EXACT>;
-    static std::atomic<uint64_t> allowed{0};
-    KDA_TRY(allow_smem(k, fixed + (kLinMaxBlock + 1) * sizeof(float2), allowed));
-    k<<<(unsigned)((int64_t)p.geo.nblocks * p.geo.H * (p.geo.sb / CH)), NT, smem, s>>>(p);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)((int64_t)p.geo.N * p.geo.H * (size4 / NT)), rev ? 2 : 1);
+    return l.next(lin_scan_kernel, grid, NT, 0, p.geo, fwd, rev ? *rev : ScanArgs{}, p.total, size4);
 }
 
-cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, bool rolled, cudaStream_t s) {
+cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, bool rolled, Launches &l) {
     if (!a.cu_seqlens) return cudaSuccess;
-    lin_blocks_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, rolled ? 0 : p.geo.sb, p.geo.nblocks, p.blocks,
-                                                 p.seq_block, p.place, p.status, a.status);
-    return cudaGetLastError();
+    return l.next(lin_blocks_kernel, 1, kPrepThreads, 0, a.cu_seqlens, a.N, a.T, rolled ? 0 : p.geo.sb, p.geo.nblocks,
+             p.blocks, p.seq_block, p.place, p.status, a.status);
 }
 
 // bf16, d_k = d_v = 128: the same steps on the tensor cores.
 cudaError_t forward_tc(const LinArgs &a, cudaStream_t s) {
+    Launches l{s};
     const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, false, use_tc(a.dt, a.dk, a.dv), a.workspace);
     const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T;
-    KDA_TRY(prepare_blocks(p, a, true, s));
+    KDA_TRY(prepare_blocks(p, a, true, l));
     // one segment a sequence and no final state asked for: the first states are all there is
     const bool need_states = a.sT || a.cu_seqlens || p.geo.per_seq > 1;
     if (tokens > 0 && need_states)
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, s));
-    KDA_TRY(run_scan<false>(p, p.states, a.s0, a.sT, 1.f, 128, 128, s));
+                                p.total, l));
+    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f}, nullptr, 128, 128, l));
     if (tokens == 0) return cudaSuccess;
     RollTc t{};
     t.geo = p.geo;
@@ -695,23 +742,24 @@ cudaError_t forward_tc(const LinArgs &a, cudaStream_t s) {
     t.states = p.states; t.tokens = tokens;
     t.log_decay = a.log_decay; t.decay = a.decay;
     t.out = a.o; t.c_state = a.scale; t.c_intra = a.scale; t.c_roll = 1.f;
-    return launch_roll_tc(t, s);
+    return launch_roll_tc(t, l);
 }
 
 // Backward without the decay's gradient: three passes with the state carried along.
 cudaError_t backward_rolled_tc(const LinArgs &a, cudaStream_t s) {
+    Launches l{s};
     constexpr bool rolled = true;
     const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
     const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T, so = (int64_t)a.H * 128;
-    KDA_TRY(prepare_blocks(p, a, true, s));
+    KDA_TRY(prepare_blocks(p, a, true, l));
     if (tokens > 0) {
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, s));
+                                p.total, l));
         KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.grads,
-                                nullptr, s));
-        KDA_TRY(run_scan<false>(p, p.states, a.s0, nullptr, 1.f, 128, 128, s));
+                                nullptr, l));
     }
-    KDA_TRY(run_scan<true>(p, p.grads, a.dsT, a.ds0, a.scale, 128, 128, s));
+    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale};
+    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f}, &grads, 128, 128, l));
     if (tokens == 0) return cudaSuccess;
     RollTc t{};
     t.geo = p.geo;
@@ -723,40 +771,41 @@ cudaError_t backward_rolled_tc(const LinArgs &a, cudaStream_t s) {
     u.x = a.d_o; u.y = a.v; u.z = a.k;
     u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride;
     u.states = p.states; u.out = a.dq; u.c_state = a.scale; u.c_roll = 1.f;
-    KDA_TRY(launch_roll_tc(u, s));
+    KDA_TRY(launch_roll_tc(u, l));
     u = t;  // dk
     u.rev = u.state_t = true;
     u.x = a.v; u.y = a.d_o; u.z = a.q;
     u.x_stride = a.v_stride; u.y_stride = so; u.z_stride = a.q_stride;
     u.states = p.grads; u.out = a.dk_out; u.c_state = 1.f; u.c_roll = a.scale;
-    KDA_TRY(launch_roll_tc(u, s));
+    KDA_TRY(launch_roll_tc(u, l));
     u = t;  // dv
     u.rev = true;
     u.x = a.k; u.y = a.q; u.z = a.d_o;
     u.x_stride = a.k_stride; u.y_stride = a.q_stride; u.z_stride = so;
     u.states = p.grads; u.out = a.dv_out; u.c_state = 1.f; u.c_roll = a.scale;
-    return launch_roll_tc(u, s);
+    return launch_roll_tc(u, l);
 }
 
 // Backward with the decay's gradient: blocks of kLinMaxBlock, every block's
 // states in three bf16 parts, and the row dots.
 cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
+    Launches l{s};
     constexpr bool rolled = false;
     const Plan p = make_plan(a.N, a.T, a.H, 128, 128, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
     const int64_t tokens = a.cu_seqlens ? a.T : (int64_t)a.N * a.T, so = (int64_t)a.H * 128;
     const bool head = a.decay == KDA_DECAY_HEAD;
-    KDA_TRY(prepare_blocks(p, a, false, s));
+    KDA_TRY(prepare_blocks(p, a, false, l));
     if (tokens > 0) {
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, s));
+                                p.total, l));
         KDA_TRY(launch_scan_tc(p.geo, false, p.states, p.total, a.s0, nullptr, 1.f, p.s_parts, p.part_stride,
-                               nullptr, nullptr, s));
+                               nullptr, nullptr, l));
         // the blocks' own sums of the states are done with: those of the gradients take their place
         KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.states,
-                                nullptr, s));
+                                nullptr, l));
     }
     KDA_TRY(launch_scan_tc(p.geo, true, p.states, p.total, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
-                           p.s_parts, p.inner, s));
+                           p.s_parts, p.inner, l));
     if (tokens == 0)
         return head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
     AttendTc t{};
@@ -769,14 +818,14 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
     u.x = a.k; u.y = a.q; u.z = a.d_o;
     u.x_stride = a.k_stride; u.y_stride = a.q_stride; u.z_stride = so;
     u.states = p.g_parts; u.out = a.dv_out; u.c_state = 1.f;
-    KDA_TRY(launch_attend_tc(u, s));
+    KDA_TRY(launch_attend_tc(u, l));
     u = t;  // dq
     u.state_t = true;
     u.x = a.d_o; u.y = a.v; u.z = a.k; u.w = a.q;
     u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride; u.w_stride = a.q_stride;
     u.states = p.s_parts; u.out = a.dq; u.c_state = a.scale;
     u.dot = p.qdq;
-    KDA_TRY(launch_attend_tc(u, s));
+    KDA_TRY(launch_attend_tc(u, l));
     u = t;  // dk
     u.rev = u.state_t = true;
     u.x = a.v; u.y = a.d_o; u.z = a.q; u.w = a.k;
@@ -784,23 +833,22 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
     u.states = p.g_parts; u.out = a.dk_out; u.c_state = 1.f;
     u.dot = p.kdk;
     u.dot_state = p.kdk_state;
-    KDA_TRY(launch_attend_tc(u, s));
-    lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
-        p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
-        head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
-    KDA_TRY(cudaGetLastError());
+    KDA_TRY(launch_attend_tc(u, l));
+    KDA_TRY(l.next(lin_decay_grad_kernel, (unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0,
+              p.geo, a.log_decay, a.decay, nullptr, nullptr, p.inner, p.total, 0, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
+        head ? nullptr : a.d_decay, head ? p.block_sum : nullptr));
     if (!head) return cudaSuccess;
-    lin_head_sum_kernel<<<a.H, NT, 0, s>>>(p.geo, p.block_sum, a.d_decay);
-    return cudaGetLastError();
+    return l.next(lin_head_sum_kernel, a.H, NT, 0, p.geo, p.block_sum, a.d_decay);
 }
 
 template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cudaStream_t s) {
+    Launches l{s};
     constexpr bool F32 = sizeof(T) == 4;
     const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, false, use_tc(a.dt, a.dk, a.dv), a.workspace);
-    KDA_TRY(prepare_blocks(p, a, false, s));
+    KDA_TRY(prepare_blocks(p, a, false, l));
     if (p.geo.nblocks > 0)
-        KDA_TRY((run_states<T, DK, DV, false>(p, a.k, a.k_stride, a.v, a.v_stride, a, p.states, s)));
-    KDA_TRY((run_scan<false>(p, p.states, a.s0, a.sT, 1.f, DK, DV, s)));
+        KDA_TRY((run_states<T, DK, DV>(p, a, false, l)));
+    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f}, nullptr, DK, DV, l));
     if (p.geo.nblocks == 0) return cudaSuccess;
     AttendArgs t{};
     t.geo = p.geo;
@@ -808,55 +856,57 @@ template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cuda
     t.x_stride = a.q_stride; t.y_stride = a.k_stride; t.z_stride = a.v_stride;
     t.log_decay = a.log_decay; t.decay = a.decay; t.states = p.states;
     t.out = a.o; t.c_state = a.scale; t.c_intra = a.scale;
-    return run_attend<T, DK, DV, false, false, F32>(t, s);
+    constexpr size_t smem = attend_smem<T, DK, DV>();
+    auto k = lin_attend_kernel<T, DK, DV>;
+    static std::atomic<uint64_t> allowed{0};
+    KDA_TRY(allow_smem(k, smem, allowed));
+    return l.next(k, (unsigned)((int64_t)p.geo.nblocks * a.H), NT, smem, t);
 }
 
+template <typename T, int DK, int DV, bool EXACT>
+cudaError_t run_attend_back(const AttendArgs &dk, const AttendArgs &dq, const AttendArgs &dv, Launches &l) {
+    constexpr size_t smem = std::max(attend_smem<T, DK, DV>(), attend_smem<T, DV, DK>());
+    auto k = lin_attend_back_kernel<T, DK, DV, EXACT>;
+    static std::atomic<uint64_t> allowed{0};
+    KDA_TRY(allow_smem(k, smem, allowed));
+    return l.next(k, dim3((unsigned)((int64_t)dk.geo.nblocks * dk.geo.H), 3), NT, smem, dk, dq, dv);
+}
 template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cudaStream_t s) {
-    constexpr bool F32 = sizeof(T) == 4, rolled = false;
+    Launches l{s};
+    constexpr bool rolled = false;
     const Plan p = make_plan(a.N, a.T, a.H, DK, DV, a.dt, a.cu_seqlens != nullptr, true, rolled, a.workspace);
-    KDA_TRY(prepare_blocks(p, a, false, s));
+    KDA_TRY(prepare_blocks(p, a, false, l));
     const int64_t so = (int64_t)a.H * DV;
-    if (p.geo.nblocks > 0) {
-        KDA_TRY((run_states<T, DK, DV, false>(p, a.k, a.k_stride, a.v, a.v_stride, a, p.states, s)));
-        KDA_TRY((run_states<T, DK, DV, true>(p, a.q, a.q_stride, a.d_o, so, a, p.grads, s)));
-        KDA_TRY((run_scan<false>(p, p.states, a.s0, nullptr, 1.f, DK, DV, s)));
-    }
-    KDA_TRY((run_scan<true>(p, p.grads, a.dsT, a.ds0, a.scale, DK, DV, s)));
-    if (p.geo.nblocks == 0) return a.d_decay && a.decay == KDA_DECAY_HEAD
-                                       ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
-    const bool dots = a.d_decay != nullptr;
+    if (p.geo.nblocks > 0) KDA_TRY((run_states<T, DK, DV>(p, a, true, l)));
+    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale};
+    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f}, &grads, DK, DV, l));
+    const bool dots = a.d_decay != nullptr, head = a.decay == KDA_DECAY_HEAD;
+    if (p.geo.nblocks == 0) return dots && head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
     AttendArgs t{};
     t.geo = p.geo;
     t.log_decay = a.log_decay; t.decay = a.decay;
     t.c_intra = a.scale;
-    AttendArgs u = t;  // dv: keys attend, in reverse time, to the queries of later tokens
-    u.x = a.k; u.y = a.q; u.z = a.d_o;
-    u.x_stride = a.k_stride; u.y_stride = a.q_stride; u.z_stride = so;
-    u.states = p.grads; u.out = a.dv_out; u.c_state = 1.f;
-    KDA_TRY((run_attend<T, DK, DV, true, false, F32>(u, s)));
-    u = t;  // dq
-    u.x = a.d_o; u.y = a.v; u.z = a.k;
-    u.x_stride = so; u.y_stride = a.v_stride; u.z_stride = a.k_stride;
-    u.states = p.states; u.out = a.dq; u.c_state = a.scale;
-    u.w = a.q; u.w_stride = a.q_stride; u.dot = dots ? p.qdq : nullptr;
-    KDA_TRY((F32 || dots ? run_attend<T, DV, DK, false, true, true>(u, s)
-                         : run_attend<T, DV, DK, false, true, F32>(u, s)));
-    u = t;  // dk
-    u.x = a.v; u.y = a.d_o; u.z = a.q;
-    u.x_stride = a.v_stride; u.y_stride = so; u.z_stride = a.q_stride;
-    u.states = p.grads; u.out = a.dk_out; u.c_state = 1.f;
-    u.w = a.k; u.w_stride = a.k_stride; u.dot = dots ? p.kdk : nullptr; u.dot_state = dots ? p.kdk_state : nullptr;
-    KDA_TRY((F32 || dots ? run_attend<T, DV, DK, true, true, true>(u, s)
-                         : run_attend<T, DV, DK, true, true, F32>(u, s)));
-    if (!dots) return cudaSuccess;
-    const bool head = a.decay == KDA_DECAY_HEAD;
-    lin_decay_grad_kernel<<<(unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, s>>>(
-        p.geo, a.log_decay, a.decay, p.states, p.grads, nullptr, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
-        head ? nullptr : a.d_decay, head ? p.block_sum : nullptr);
-    KDA_TRY(cudaGetLastError());
+    AttendArgs dv = t;  // keys attend, in reverse time, to the queries of later tokens
+    dv.x = a.k; dv.y = a.q; dv.z = a.d_o;
+    dv.x_stride = a.k_stride; dv.y_stride = a.q_stride; dv.z_stride = so;
+    dv.states = p.grads; dv.out = a.dv_out; dv.c_state = 1.f;
+    AttendArgs dq = t;
+    dq.x = a.d_o; dq.y = a.v; dq.z = a.k;
+    dq.x_stride = so; dq.y_stride = a.v_stride; dq.z_stride = a.k_stride;
+    dq.states = p.states; dq.out = a.dq; dq.c_state = a.scale;
+    dq.w = a.q; dq.w_stride = a.q_stride; dq.dot = dots ? p.qdq : nullptr;
+    AttendArgs dk = t;
+    dk.x = a.v; dk.y = a.d_o; dk.z = a.q;
+    dk.x_stride = a.v_stride; dk.y_stride = so; dk.z_stride = a.q_stride;
+    dk.states = p.grads; dk.out = a.dk_out; dk.c_state = 1.f;
+    dk.w = a.k; dk.w_stride = a.k_stride; dk.dot = dots ? p.kdk : nullptr; dk.dot_state = dots ? p.kdk_state : nullptr;
+    if (!dots) return run_attend_back<T, DK, DV, sizeof(T) == 4>(dk, dq, dv, l);
+    KDA_TRY((run_attend_back<T, DK, DV, true>(dk, dq, dv, l)));
+    KDA_TRY(l.next(lin_decay_grad_kernel, (unsigned)((int64_t)p.geo.nblocks * a.H), NT, 0, p.geo, a.log_decay, a.decay,
+              p.states, p.grads, nullptr, p.total, DK * DV / 4, p.qdq, p.kdk, p.kdk_state, p.dot_stride,
+              head ? nullptr : a.d_decay, head ? p.block_sum : nullptr));
     if (!head) return cudaSuccess;
-    lin_head_sum_kernel<<<a.H, NT, 0, s>>>(p.geo, p.block_sum, a.d_decay);
-    return cudaGetLastError();
+    return l.next(lin_head_sum_kernel, a.H, NT, 0, p.geo, p.block_sum, a.d_decay);
 }
 
 }  // namespace

@@ -1506,27 +1506,25 @@ int sm_count() {
 
 cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
                             int64_t tokens, const float *log_decay, int decay, float *out, float *total,
-                            cudaStream_t s) {
+                            Launches &l) {
     CUtensorMap mx, my;
     if (!token_map(&mx, x, xs, geo.H, tokens) || !token_map(&my, y, ys, geo.H, tokens)) return cudaErrorInvalidValue;
     StateTcArgs p{geo, log_decay, decay, out, total, geo.nblocks * geo.H};
     auto k = rev ? lin_state_tc_kernel<true> : lin_state_tc_kernel<false>;
     static std::atomic<uint64_t> allowed[2];
     KDA_TRY(allow_smem(k, ST_SMEM, allowed[rev]));
-    k<<<min(p.items, sm_count()), ST_THREADS, ST_SMEM, s>>>(p, mx, my);
-    return cudaGetLastError();
+    return l.whole(k, min(p.items, sm_count()), ST_THREADS, ST_SMEM, p, mx, my);
 }
 
 cudaError_t launch_scan_tc(const LinGeom &geo, bool rev, const float *own, const float *total,
                            const float *s0, float *sT, float c, void *out, int64_t part_stride, const void *other,
-                           float *inner, cudaStream_t s) {
+                           float *inner, Launches &l) {
     auto k = rev ? lin_scan_tc_kernel<true> : lin_scan_tc_kernel<false>;
-    k<<<(unsigned)((int64_t)geo.N * geo.H * (D * D / 4 / SC_THREADS)), SC_THREADS, 0, s>>>(
-        geo, own, total, s0, sT, c, (__nv_bfloat16 *)out, part_stride, (const __nv_bfloat16 *)other, inner);
-    return cudaGetLastError();
+    return l.whole(k, (unsigned)((int64_t)geo.N * geo.H * (D * D / 4 / SC_THREADS)), SC_THREADS, 0, geo, own, total, s0, sT,
+                   c, (__nv_bfloat16 *)out, part_stride, (const __nv_bfloat16 *)other, inner);
 }
 
-cudaError_t launch_roll_tc(const RollTc &a, cudaStream_t s) {
+cudaError_t launch_roll_tc(const RollTc &a, Launches &l) {
     const LinGeom &geo = a.geo;
     CUtensorMap mx, my, mz;
     if (!token_map(&mx, a.x, a.x_stride, geo.H, a.tokens) || !token_map(&my, a.y, a.y_stride, geo.H, a.tokens) ||
@@ -1539,11 +1537,10 @@ cudaError_t launch_roll_tc(const RollTc &a, cudaStream_t s) {
                    : (a.state_t ? lin_roll_tc_kernel<false, true> : lin_roll_tc_kernel<false, false>);
     static std::atomic<uint64_t> allowed[4];
     KDA_TRY(allow_smem(k, RL_SMEM, allowed[a.rev * 2 + a.state_t]));
-    k<<<min(p.items, sm_count()), RL_THREADS, RL_SMEM, s>>>(p, mx, my, mz);
-    return cudaGetLastError();
+    return l.whole(k, min(p.items, sm_count()), RL_THREADS, RL_SMEM, p, mx, my, mz);
 }
 
-cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
+cudaError_t launch_attend_tc(const AttendTc &a, Launches &l) {
     const LinGeom &geo = a.geo;
     const bool dots = a.dot != nullptr;
     const int64_t rows = (int64_t)geo.nblocks * geo.H * D;
@@ -1562,8 +1559,7 @@ cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s) {
                     : lin_attend_tc_kernel<true, false, false>;
     static std::atomic<uint64_t> allowed[4];
     KDA_TRY(allow_smem(k, AT_SMEM, allowed[a.rev * 2 + dots]));
-    k<<<min(p.items, sm_count()), AT_THREADS, AT_SMEM, s>>>(p, mx, my, mz, ms, mw);
-    return cudaGetLastError();
+    return l.whole(k, min(p.items, sm_count()), AT_THREADS, AT_SMEM, p, mx, my, mz, ms, mw);
 }
 
 cudaError_t read_linear_error(int *out, bool reset) {

@@ -11,13 +11,13 @@ constexpr int kLinMaxBlock = 256;  // tokens per block at most (two 128-row tile
 // [block][head] = e^{L_end} (forward only).
 cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
                             int64_t tokens, const float *log_decay, int decay, float *out, float *total,
-                            cudaStream_t s);
+                            Launches &l);
 // The scan over the blocks: own states -> three bf16 arrays, part_stride
 // elements apart, of the states before (reverse: the gradients after) each
 // block; the last state to sT. Reverse: also <S, G> of every block, S in `other`.
 cudaError_t launch_scan_tc(const LinGeom &geo, bool rev, const float *own, const float *total,
                            const float *s0, float *sT, float c, void *out, int64_t part_stride, const void *other,
-                           float *inner, cudaStream_t s);
+                           float *inner, Launches &l);
 constexpr int kScanPartials = 128;  // partial sums of <S, G> per block and head
 
 // out = c_state f x S + c_intra (D o x y^T) z; state_t: S is read transposed.
@@ -36,7 +36,7 @@ struct AttendTc {
     float c_state, c_intra;
     float *dot, *dot_state;  // [2][tokens][H], the sums of two column halves, nullable
 };
-cudaError_t launch_attend_tc(const AttendTc &a, cudaStream_t s);
+cudaError_t launch_attend_tc(const AttendTc &a, Launches &l);
 // The same over blocks of any length with the state carried along inside:
 // states holds every block's first state (reverse: the gradient after its last
 // token) in fp32; c_roll multiplies what the block's tokens add to it.
@@ -52,7 +52,7 @@ struct RollTc {
     void *out;
     float c_state, c_intra, c_roll;
 };
-cudaError_t launch_roll_tc(const RollTc &a, cudaStream_t s);
+cudaError_t launch_roll_tc(const RollTc &a, Launches &l);
 // Reads (and optionally clears) the error word of these kernels' waits.
 cudaError_t read_linear_error(int *out, bool reset);
 
