@@ -122,6 +122,8 @@ def _state(t, name: str, shape: tuple, index: int):
 
 def _out(t, name: str, like, shape, dtype, index: int):
     if t is None:
+        if like.shape == shape and like.dtype == dtype and like.is_contiguous():
+            return torch.empty_like(like)  # the same tensor, half a microsecond sooner
         return torch.empty(shape, dtype=dtype, device=like.device)
     _plain(t, name, dtype, index, torch.Size(shape))
     return t
@@ -190,7 +192,8 @@ def _prefill(q, k, v, log_decay, cu_seqlens, initial_state, decay, scale, output
     name = "kda_linear_varlen_prefill" if packed else "kda_linear_prefill"
     out = _out(out, "out", v, v.shape, v.dtype, index)
     if final_state is not None or output_final_state:
-        final_state = _out(final_state, "final_state", v, (N, H, dk, dv), torch.float32, index)
+        final_state = _out(final_state, "final_state", v if initial_state is None else initial_state, (N, H, dk, dv),
+                           torch.float32, index)
     ws, size = _space(workspace, _size(name, N, T, H, dk, dv, code), v)
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, *strides, _ptr(g), kind, scale, _ptr(initial_state),
             out.data_ptr(), _ptr(final_state))

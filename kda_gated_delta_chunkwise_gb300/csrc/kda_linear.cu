@@ -39,20 +39,26 @@ constexpr int NT = 256;  // threads of the three main kernels
 constexpr int CH = kLinChunk;
 
 // The segment length where the state is carried along inside (lin_roll_tc): a
-// function of the sequence's own length, so that a sequence gives the same bits
-// alone and in any batch. A segment costs its 128-token chunks and about two
-// more (its first state, its share of the scan), so short ones pay for being
-// many and long ones leave a small batch on few of the 152 SMs.
+// function of the sequence's own length and the heads, so that a sequence gives
+// the same bits alone and in any batch. A segment costs its 128-token chunks and
+// about two more (its first state, its share of the scan), so short ones pay for
+// being many; long ones leave a small batch on few of the 152 SMs, so one
+// sequence is cut into at least 64 (or into the shortest). bf16, d = 128:
+//   4 x 4096 tokens x 16 heads: 512 136 us, 1024 123, 2048 117;
+//   1 x 16384 x 2: 512 41, 1024 61; 1 x 65536 x 1: 1024 68, 2048 105;
+//   16 sequences of 20011 tokens in all x 16: 512 172, by this rule 171-175.
 constexpr int kLeastSegment = 512;
-__host__ __device__ constexpr int segment_tokens(int64_t len) {
-    return len <= 2048 ? kLeastSegment : len <= 16384 ? 1024 : len <= 65536 ? 2048 : 4096;
+__host__ __device__ constexpr int segment_tokens(int64_t len, int H) {
+    int n = len <= 2048 ? kLeastSegment : len <= 16384 ? 1024 : len <= 65536 ? 2048 : 4096;
+    while (n > kLeastSegment && (int64_t)n * 64 > len * H) n /= 2;
+    return n;
 }
 
 // ---------------------------------------------------------------- packed batches: the table of blocks
 // sb = 0: segments of segment_tokens(length).
 constexpr int kPrepThreads = 1024;
 __global__ void __launch_bounds__(kPrepThreads)
-lin_blocks_kernel(const int32_t *cu, int N, int T_total, int sb, int nblocks, int4 *blocks,
+lin_blocks_kernel(const int32_t *cu, int N, int T_total, int H, int sb, int nblocks, int4 *blocks,
                   int32_t *seq_block, int32_t *place, int32_t *status, int32_t *user_status) {
     constexpr int kBuckets = 66;
     __shared__ int bad;
@@ -76,7 +82,7 @@ lin_blocks_kernel(const int32_t *cu, int N, int T_total, int sb, int nblocks, in
         const int i = i0 + tid;
         int x = 0;
         if (i < N && !b) {
-            const int len = cu[i + 1] - cu[i], per = sb ? sb : segment_tokens(len);
+            const int len = cu[i + 1] - cu[i], per = sb ? sb : segment_tokens(len, H);
             x = (len + per - 1) / per;
         }
         for (int off = 1; off < 32; off <<= 1) {
@@ -104,7 +110,7 @@ lin_blocks_kernel(const int32_t *cu, int N, int T_total, int sb, int nblocks, in
             if (seq_block[m] <= j) lo = m;
             else hi = m - 1;
         }
-        const int per = sb ? sb : segment_tokens(cu[lo + 1] - cu[lo]);
+        const int per = sb ? sb : segment_tokens(cu[lo + 1] - cu[lo], H);
         const int start = cu[lo] + (j - seq_block[lo]) * per;
         return make_int4(lo, start, min(per, cu[lo + 1] - start), 0);
     };
@@ -648,7 +654,7 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
     Plan p{};
     const int64_t tokens = packed ? T : N * T;
     const bool tc = use_tc(dt, dk, dv);
-    const int sb = !tc ? kGeneralBlock : !rolled ? kLinMaxBlock : packed ? kLeastSegment : segment_tokens(T);
+    const int sb = !tc ? kGeneralBlock : !rolled ? kLinMaxBlock : packed ? kLeastSegment : segment_tokens(T, H);
     const int64_t nb = max_blocks(N, T, packed, sb);
     unsigned char *base = static_cast<unsigned char *>(ws);
     size_t at = 0;
@@ -718,7 +724,7 @@ cudaError_t run_scan(const Plan &p, const ScanArgs &fwd, const ScanArgs *rev, in
 
 cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, bool rolled, Launches &l) {
     if (!a.cu_seqlens) return cudaSuccess;
-    return l.next(lin_blocks_kernel, 1, kPrepThreads, 0, a.cu_seqlens, a.N, a.T, rolled ? 0 : p.geo.sb, p.geo.nblocks,
+    return l.next(lin_blocks_kernel, 1, kPrepThreads, 0, a.cu_seqlens, a.N, a.T, a.H, rolled ? 0 : p.geo.sb, p.geo.nblocks,
              p.blocks, p.seq_block, p.place, p.status, a.status);
 }
 
