@@ -9,13 +9,16 @@
 // and nothing overflows however strong the decay. Three launches:
 //   lin_state_kernel   every block's own sum over j, all blocks at once;
 //   lin_scan_kernel    joins them along each sequence, one pass, elementwise;
-//   lin_attend_kernel  every 64-token tile of outputs, all tiles at once.
+//   lin_attend_kernel  every block's outputs, all blocks at once.
+// A block of the general kernels is 64 tokens, one CTA; where the shapes allow
+// it the tensor-core kernels (kda_linear_tc.cu) take the place of the first and
+// the last.
 // Backward, with G the gradient of the state after a token
 // (G_t = scale q_t do_t^T + e^{g_{t+1}} G_{t+1}): dq_t = scale S_t do_t,
 // dk_t = G_t v_t, dv_t = G_t^T k_t. These are three more attentions of the
 // same form: dq with (do, v, k) for (q, k, v) and S transposed, dk with
 // (v, do, q) and dv with (k, q, do) in reverse time with G for S; so the same
-// three kernels run them. The gradient of a log decay is everything that
+// three kernels run them, both directions (all three attentions) in one launch. The gradient of a log decay is everything that
 // passes over the step into its token,
 //   dg_t = sum_{i >= t > j} M_ij + sum_{i >= t} q_i.dq_i(S part)
 //        + sum_{j < t} k_j.dk_j(G part) + e^{L_end} <S, G>    (inside a block)
@@ -226,7 +229,10 @@ template <typename T> __host__ __device__ constexpr int ld_cols(int d) { return 
 // ---------------------------------------------------------------- a block's own state
 // out[block][head] = sum_s w_s x_s y_s^T over the block's tokens: forward
 // w_s = e^{L_end - L_s} with (x, y) = (k, v); reverse w_s = e^{L_s} with
-// (q, do). Also e^{L_end} of the block (forward).
+// (q, do). Also e^{L_end} of the block (forward). Bound by latency at the sizes
+// that this path is for: a load of the tiles and the decays (all in flight at
+// once), one 64-token product, one store. 2 x 999 tokens x 4 heads, fp32, 64 x 128,
+// both directions: 256 CTAs, 11 us on cold caches.
 template <typename T> struct StateArgs {
     LinGeom geo;
     const T *x, *y;
@@ -289,7 +295,9 @@ __global__ void __launch_bounds__(NT) lin_state_kernel(const StateArgs<T> fwd, c
 // way to the state before the block, S <- e^{L_end} S + c own, and the last S
 // is the final state; reverse, to the gradient of the state after the block.
 // Elementwise over the state: one float4 per thread, the blocks in turn, four
-// loads ahead.
+// loads ahead. Bound by memory, or by the latency of a turn where the sequences
+// are few and long: 4 x 4096 tokens x 16 heads in segments of 1024, 10 us;
+// 131072 x 32 in segments of 4096 (67 MB each way), 18 us, 7.5 TB/s (L2 helps).
 struct ScanArgs {
     float *states;
     const float *s0;  // nullable
@@ -368,6 +376,11 @@ struct AttendArgs {
 // tokens j <= i of the block (reverse: j >= i); S is [DC][DO], or stored
 // [DO][DC] and read transposed (ST).
 // EXACT: the fp32 operands P and S are split too, for the row dots.
+// Bound by latency and, in fp32, by the three products of every split operand.
+// Everything a block reads is in flight at once; P takes the place of x and y,
+// which leaves room for two CTAs on an SM. 2 x 999 tokens x 4 heads, fp32, 64 x 128:
+// the backward's three passes took 85 us as launches of their own, with loads
+// and products in turn; the whole backward went from 102 to 63 us.
 template <typename T, int DC, int DO> constexpr size_t attend_smem() {
     return 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (DO + 8) * 4 + CH * ld_cols<T>(DO) * sizeof(T) + (CH + 1) * 8;
 }
@@ -627,11 +640,11 @@ lin_head_sum_kernel(LinGeom geo, const float *block_sum, float *dg) {
 // ---------------------------------------------------------------- host side
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The block length of the general kernels, which work on 64-token chunks one
-// after the other: one chunk a block gives the most blocks at once (257 tokens
-// x 2 heads, fp32, d = 64: 21 us of GPU time in blocks of 64, 40 in blocks of
-// 256). One length for all, so that a sequence gives the same bits in any batch.
-constexpr int kGeneralBlock = 64;
+// The block length of the general kernels: one chunk a block gives the most
+// blocks at once (257 tokens x 2 heads, fp32, d = 64: the call took 34.5 us in
+// blocks of 64, 53.8 in blocks of 256). One length for all, so that a sequence
+// gives the same bits in any batch.
+constexpr int kGeneralBlock = CH;
 
 int64_t max_blocks(int N, int64_t T, bool packed, int sb) {
     return packed ? T / sb + N : (int64_t)N * ((T + sb - 1) / sb);
@@ -816,7 +829,7 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
         return head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
     AttendTc t{};
     t.geo = p.geo;
-    t.part_stride = p.part_stride; t.tokens = tokens;
+    t.tokens = tokens;
     t.log_decay = a.log_decay; t.decay = a.decay;
     t.c_intra = a.scale;
     AttendTc u = t;  // dv

@@ -197,13 +197,16 @@ __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float 
 // would cost the high ones that many cuts. High and middle part lie side by
 // side, so one MMA with N = 256 takes both and reads y once.
 // Bound by memory: 32 KB of x and y a tile; next come the 176 KB that a tile
-// moves through shared memory.
-//
-// warp 0: TMA; 1: MMA; 2: weights, an item ahead; 4-7: accumulators out;
+// moves through shared memory. 4 x 4096 tokens x 16 heads, d = 128: 39-42 us for
+// 135 MB (3.4 TB/s, a block or two per SM and its first loads unhidden);
+// 131072 x 32: 450-466 us for 2.15 GB (4.7 TB/s, 70 % of a copy).
 // A block longer than kLinMaxBlock goes in parts of that length, joined by the
 // decays of the parts, as the blocks are by the scan.
+//
+// warp 0: TMA; 1: MMA; 2: weights, an item ahead; 4-7: accumulators out;
 // 8-15 and 16-23: x -> three parts (the high one in place), tiles in turn. Each
-// of the two groups has full barriers of its own (see the output kernel).
+// of the two groups has full barriers of its own (of a shared one it would miss
+// the phases of the other's tiles).
 constexpr int ST_TOK = 64;
 constexpr int ST_TILE = ST_TOK * D * 2;       // 16 KB
 constexpr int ST_STAGE = 4 * ST_TILE;         // x (then its high part), middle, low, y
@@ -444,7 +447,9 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
 // ================================================================ joining the blocks
 // As lin_scan_kernel, with the states handed on as three bf16 parts (24 bits),
 // which the output kernel with row dots multiplies with; the first part alone
-// is the state rounded to bf16.
+// is the state rounded to bf16. In reverse also <S, G> of every block. Bound by
+// memory: 1024 blocks and heads of 128 x 128, 24 us forward (67 MB in, 101 out:
+// 7.0 TB/s), 40-42 us in reverse (another 101 MB in: 6.4-6.7 TB/s).
 constexpr int SC_THREADS = 256;
 template <bool REV>
 __global__ void __launch_bounds__(SC_THREADS)
@@ -525,6 +530,14 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 //   O += P z, P read from TMEM.
 // P and S are the two roundings to bf16 (2^-9 relative each, as small as the
 // rounding of the result itself); sums are fp32.
+// 4 x 4096 tokens x 16 heads, 256-token blocks: dv 54 us (236 MB, 4.4 TB/s), dq
+// and dk with their dots 106-113 (304-371 MB read, 3.3 TB/s). What bounds it: the
+// ring holds no more than the item at work, so loads and products take turns (of
+// about 30,000 cycles an item, 10,000 pass until S is there, 8,000 more until
+// the far w is). Prefetching the next item into L2 did not help (454 us for the
+// whole backward became 458, or 510 issued earlier: the prefetches queue before
+// the loads). Items of their own for the two contexts, each with its own S, y
+// and z: dq 123, dk 129, dv 65 us.
 //
 // DOTS adds w_i . out_i per row, for the gradient of the decay, to fp32
 // accuracy: its state part from all three parts of S, and the rest not from
@@ -950,7 +963,9 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // In reverse time (REV) the chunks go from the segment's end, the state is the
 // gradient after the chunk, and the mask and the decays are mirrored. ST: the
 // first state is read transposed. P, Sb and the result are the roundings to
-// bf16. Bound by memory; a 128-token chunk costs 40 tensor-core steps, and two
+// bf16. Bound by memory in principle (4 x 4096 tokens x 16 heads: 75 us, 268 MB,
+// 3.5 TB/s; 131072 x 32: 862 us, 4.3 GB, 5.0 TB/s, 74 % of a copy); a 128-token chunk
+// costs 40 tensor-core steps, and two
 // loops run from one chunk to the next, each to stay under the time that the
 // chunk's 128 KB take: S -> Sb, scale -> MMA -> S, and x Sb -> scale -> P z -> out.
 // Everything else of a chunk is done ahead of them: P (two in TMEM), its mask,

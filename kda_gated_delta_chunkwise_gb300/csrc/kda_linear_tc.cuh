@@ -28,7 +28,6 @@ struct AttendTc {
     const void *x, *y, *z, *w;
     int64_t x_stride, y_stride, z_stride, w_stride;
     const void *states;
-    int64_t part_stride;  // elements between the parts of S
     int64_t tokens;
     const float *log_decay;
     int decay;
