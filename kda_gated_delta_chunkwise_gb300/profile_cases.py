@@ -16,6 +16,12 @@ CASE is one of:
   varlen_64seq_1m     the same lengths scaled to 2^20 tokens
   backward_4x16x4096  the gradients of the benchmark workload (kda_prefill_backward)
   backward_1x16x1024  a small case of it, for full ncu captures
+  linear_4x16x4096    linear attention with a decay per token, the benchmark's batch
+  linear_1x32x131072  one long sequence of it
+  linear_backward_4x16x4096  its gradients, the decay's too
+  linear_decode_256x32       one token of it for 256 sequences x 32 heads
+  norm_rope_65536x16  norm and rotary positions of 65,536 tokens, 16 + 16 heads,
+                      d = 128, bf16, and their gradients
   hostlink            no kernel: the host link's copy rates (page-locked host
                       memory to the device, back, and both at once), printed
 
@@ -29,6 +35,7 @@ import argparse
 import torch
 
 from . import _binding as kda
+from . import _linear as linear
 from . import workloads as W
 
 
@@ -166,7 +173,45 @@ def _hostlink(reps: int):
               f"{max(reps, 5)})")
 
 
+def _linear(B: int, T: int, H: int, back: bool, reps: int):
+    q, k, v = (torch.randn(B, T, H, 128, device="cuda").bfloat16() for _ in range(3))
+    k = k * 128 ** -0.5
+    g = -torch.rand(B, T, H, device="cuda") * 0.05
+    s0 = torch.zeros(B, H, 128, 128, device="cuda")
+    for _ in range(reps):
+        if back:
+            linear.linear_prefill_backward(q, k, v, g, v, s0)
+        else:
+            linear.linear_prefill(q, k, v, g, s0)
+    torch.cuda.synchronize()
+
+
+def _linear_decode(N: int, reps: int):
+    q, k, v = (torch.randn(N, 32, 128, device="cuda").bfloat16() for _ in range(3))
+    g = -torch.rand(N, 32, device="cuda") * 0.05
+    state = torch.zeros(N, 32, 128, 128, device="cuda")
+    for _ in range(reps):
+        linear.linear_decode_step(q, k * 128 ** -0.5, v, g, state)
+    torch.cuda.synchronize()
+
+
+def _norm_rope(tokens: int, heads: int, reps: int):
+    q, k = (torch.randn(tokens, heads, 128, device="cuda").bfloat16() for _ in range(2))
+    w = torch.ones(128, device="cuda")
+    table = linear.rope_table(4096, 128)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda") % 4096
+    for _ in range(reps):
+        linear.qk_norm_rope(q, k, pos, table, w, w)
+        linear.qk_norm_rope_backward(q, k, q, k, pos, table, w, w)
+    torch.cuda.synchronize()
+
+
 CASES = {
+    "linear_4x16x4096": lambda r: _linear(4, 4096, 16, False, r),
+    "linear_1x32x131072": lambda r: _linear(1, 131072, 32, False, r),
+    "linear_backward_4x16x4096": lambda r: _linear(4, 4096, 16, True, r),
+    "linear_decode_256x32": lambda r: _linear_decode(256, r),
+    "norm_rope_65536x16": lambda r: _norm_rope(65536, 16, r),
     "prefill_4x16x4096": lambda r: _prefill(4, r),
     "prefill_1x16x4096": lambda r: _prefill(1, r),
     "variants_4x16x4096": _variants,
