@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(NT) lin_state_kernel(const StateArgs<T> fwd, c
 // is the final state; reverse, to the gradient of the state after the block.
 // Elementwise over the state: one float4 per thread, the blocks in turn, four
 // loads ahead. Bound by memory, or by the latency of a turn where the sequences
-// are few and long: 4 x 4096 tokens x 16 heads in segments of 1024, 10 us;
+// are few and long: 4 x 4096 tokens x 16 heads in segments of 1024, 8-10 us;
 // 131072 x 32 in segments of 4096 (67 MB each way), 18 us, 7.5 TB/s (L2 helps).
 struct ScanArgs {
     float *states;
