@@ -520,9 +520,10 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 // head. Two contexts (an MMA-issuing warp, 256 row threads, one O and one P
 // accumulator in TMEM each) take its two tiles of rows: the near one sees its own
 // tokens alone, the far one those of both tiles (in reverse time the second tile
-// is the near one); they change places from item to item. The operands pass
-// through a ring of six 32 KB slots: S, the near tile's x, the far one's, then y
-// and z of the near tile and of the far one, all but x read by both.
+// is the near one); they change places from item to item. The operands come
+// through two rings: x (and w) of the near tile and of the far one, which stay
+// until their tile's last scores, and S, then y and z of the near tile and of the
+// far one, which flow past and are read by both contexts.
 // Two threads share a row, a half of the columns each.
 //   O = x S, rows scaled by the decay from the block's edge (in TMEM);
 //   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place (each half
@@ -530,14 +531,14 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 //   O += P z, P read from TMEM.
 // P and S are the two roundings to bf16 (2^-9 relative each, as small as the
 // rounding of the result itself); sums are fp32.
-// 4 x 4096 tokens x 16 heads, 256-token blocks: dv 54 us (236 MB, 4.4 TB/s), dq
-// and dk with their dots 106-113 (304-371 MB read, 3.3 TB/s). What bounds it: the
-// ring holds no more than the item at work, so loads and products take turns (of
-// about 30,000 cycles an item, 10,000 pass until S is there, 8,000 more until
-// the far w is). Prefetching the next item into L2 did not help (454 us for the
-// whole backward became 458, or 510 issued earlier: the prefetches queue before
-// the loads). Items of their own for the two contexts, each with its own S, y
-// and z: dq 123, dk 129, dv 65 us.
+// 4 x 4096 tokens x 16 heads, 256-token blocks: dq 97 us and dk 108 with their
+// dots (371 MB, 3.4 to 3.8 TB/s), dv 59 (236 MB, 4.0 TB/s). Bound by the latency
+// of its loads: shared memory holds one item's operands and the first of the
+// next one's. Measured before: one ring of six 32 KB slots, which gave the next S
+// no room before the item's end, 106-113, 111 and 54 us; and items of their own
+// for the two contexts, each loading its own S, y and z, 123, 129 and 65. With
+// that one ring, prefetching the next item into L2 made the whole backward 458 us
+// from 454, or 510 issued earlier: the prefetches queue before the loads.
 //
 // DOTS adds w_i . out_i per row, for the gradient of the decay, to fp32
 // accuracy: its state part from all three parts of S, and the rest not from
@@ -546,21 +547,28 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 // second score accumulator, so the scores go 64 columns at a time.
 //
 // A slot is filled again when both contexts are done with it; both wait for
-// every load in turn, used or not, and so see every phase of the slots' barriers
-// (a parity wait cannot tell a phase from the one two before it). x and w stay
-// until their tile's last scores; the order of the loads lets a far y or z take
-// a near x's or w's place (checked with a model of the roles).
-static_assert(kLinMaxBlock <= 256, "the slot ring holds an item of two tiles");
-constexpr int AT_SLOT = 128 * D * 2;  // 32 KB
-constexpr int AT_SLOTS = 6;
+// every load of a ring in turn, used or not, and so see every phase of the
+// slots' barriers (a parity wait cannot tell a phase from the one two before it;
+// checked with a model of the roles).
+static_assert(kLinMaxBlock <= 256, "an item is one or two tiles");
+// Rings in shared memory: `ROWS` slots of 32 KB for x and w, then `FLOW` of 16 KB
+// (DOTS: half a part of S, or 64 tokens of y or z) or 32 KB (S whole, 128 tokens).
+template <bool DOTS> struct AttendRings {
+    static constexpr int SUB = DOTS ? 64 : 128;  // tokens of a flow slot, score columns at a time
+    static constexpr int ROWS = DOTS ? 4 : 2, FLOW = DOTS ? 5 : 4;
+    static constexpr int ROW_SLOT = 128 * D * 2, FLOW_SLOT = SUB * D * 2, HALF = FLOW_SLOT / 2;  // HALF: 64 channels
+    static constexpr int FLOW_AT = ROWS * ROW_SLOT;
+};
 constexpr int AT_THREADS = 640;
 constexpr int AT_PREFIX = 4;                                         // blocks whose prefix sums are kept
-constexpr int AT_A = AT_SLOTS * AT_SLOT;                             // prefix sums [AT_PREFIX][kLinMaxBlock + 2]
-constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // column factors [16 warps][kLinMaxBlock / 2]
+constexpr int AT_A = AttendRings<true>::FLOW_AT + AttendRings<true>::FLOW * AttendRings<true>::FLOW_SLOT;
+static_assert(AT_A >= AttendRings<false>::FLOW_AT + AttendRings<false>::FLOW * AttendRings<false>::FLOW_SLOT, "rings");
+constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // AT_A: prefix sums; column factors [16 warps][128]
 constexpr int AT_BAR = AT_COL + 16 * kLinMaxBlock / 2 * 4;
-enum { AB_FULL = 0, AB_EMPTY = 6, AB_O_IN = 12, AB_O_FULL = 14, AB_O_EMPTY = 16, AB_P_FULL = 18, AB_P_READY = 20,
-       AB_A_FULL = 22, AB_A_EMPTY = 26, AB_COUNT = 30 };
+enum { AB_ROW_FULL = 0, AB_ROW_EMPTY = 4, AB_FLOW_FULL = 8, AB_FLOW_EMPTY = 13, AB_O_IN = 18, AB_O_FULL = 20,
+       AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26, AB_A_FULL = 28, AB_A_EMPTY = 32, AB_COUNT = 36 };
 constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
+static_assert(AT_SMEM <= 232448, "shared memory of an SM");
 
 struct AttendTcArgs {
     LinGeom geo;
@@ -594,9 +602,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                      const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap ms,
                      const __grid_constant__ CUtensorMap mw) {
-    constexpr int SUB = DOTS ? 64 : 128;      // score columns at a time
-    constexpr int NS = DOTS ? 3 : 1;          // parts of S
-    constexpr int XW = DOTS ? 2 : 1;          // loads of a tile's rows
+    using R = AttendRings<DOTS>;
+    constexpr int SUB = R::SUB;
+    constexpr int NS = DOTS ? 6 : 1;          // loads of S: three parts, a half of the columns each
+    constexpr int XW = DOTS ? 2 : 1;          // row loads of a tile
+    constexpr int YZ = 2 * (128 / SUB);       // flow loads of a tile
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + AT_BAR);
@@ -606,9 +616,13 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
     const LinGeom &geo = p.geo;
     if (tid == 0) {
         *ab.flag = 0;
-        for (int i = 0; i < AT_SLOTS; ++i) {
-            mbar_init(bar + AB_FULL + i, 1);
-            mbar_init(bar + AB_EMPTY + i, 2);
+        for (int i = 0; i < R::ROWS; ++i) {
+            mbar_init(bar + AB_ROW_FULL + i, 1);
+            mbar_init(bar + AB_ROW_EMPTY + i, 2);
+        }
+        for (int i = 0; i < R::FLOW; ++i) {
+            mbar_init(bar + AB_FLOW_FULL + i, 1);
+            mbar_init(bar + AB_FLOW_EMPTY + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar + AB_O_IN + i, 1);
@@ -633,42 +647,42 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
     const uint32_t tmem = *tm;
     bool ok = true;
 
-    if (warp == 0) {
+    auto row_at = [&](int i) { return sm + (i % R::ROWS) * R::ROW_SLOT; };
+    auto flow_at = [&](int i) { return sm + R::FLOW_AT + (i % R::FLOW) * R::FLOW_SLOT; };
+
+    if (warp == 0) {  // S, y and z
         if (lane == 0) {
             int n = 0;
             uint64_t *f = nullptr;  // the barrier of the slot's load
             auto slot = [&]() -> unsigned char * {
-                const int s = n % AT_SLOTS;
-                if (!(ok = ok && ab.wait(bar + AB_EMPTY + s, ((n / AT_SLOTS) & 1) ^ 1))) return nullptr;
-                f = bar + AB_FULL + s;
-                mbar_arrive_expect_tx(f, AT_SLOT);
-                ++n;
-                return sm + s * AT_SLOT;
+                const int s = n % R::FLOW;
+                if (!(ok = ok && ab.wait(bar + AB_FLOW_EMPTY + s, ((n / R::FLOW) & 1) ^ 1))) return nullptr;
+                f = bar + AB_FLOW_FULL + s;
+                mbar_arrive_expect_tx(f, R::FLOW_SLOT);
+                return flow_at(n++);
             };
-            auto rows = [&](const CUtensorMap *m, int h, int tok) {  // 128 tokens in 64-token, 64-channel boxes
+            auto tokens = [&](const CUtensorMap *m, int h, int tok) {  // SUB tokens
                 unsigned char *d = slot();
                 if (!d) return;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) tma_load_3d(d + x * 16384 + t * 8192, m, f, 64 * x, h, tok + 64 * t);
+                    for (int t = 0; t < SUB / 64; ++t)
+                        tma_load_3d(d + x * R::HALF + t * 8192, m, f, 64 * x, h, tok + 64 * t);
             };
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const Item x = item_of<REV>(p, it);
-                for (int part = NS - 1; part >= 0 && x.tiles > 0; --part)  // the lowest part first
+                for (int i = 0; i < NS && x.tiles > 0; ++i)  // the lowest part first
                     if (unsigned char *d = slot()) {
-                        const int row = part * p.state_rows + (x.b * geo.H + x.h) * D;
-                        tma_load_2d(d, &ms, f, 0, row);
-                        tma_load_2d(d + 16384, &ms, f, 64, row);
+                        const int row = (DOTS ? 2 - i / 2 : 0) * p.state_rows + (x.b * geo.H + x.h) * D;
+                        tma_load_2d(d, &ms, f, DOTS ? 64 * (i & 1) : 0, row);
+                        if (!DOTS) tma_load_2d(d + R::HALF, &ms, f, 64, row);
                     }
-                for (int t = 0; t < x.tiles; ++t) {
-                    rows(&mx, x.h, x.blk.start + 128 * x.tile(t));
-                    if (DOTS) rows(&mw, x.h, x.blk.start + 128 * x.tile(t));
-                }
-                for (int t = 0; t < x.tiles; ++t) {
-                    rows(&my, x.h, x.blk.start + 128 * x.tile(t));
-                    rows(&mz, x.h, x.blk.start + 128 * x.tile(t));
-                }
+                for (int t = 0; t < x.tiles; ++t)
+                    for (int u = 0; u < 128; u += SUB) {
+                        tokens(&my, x.h, x.blk.start + 128 * x.tile(t) + u);
+                        tokens(&mz, x.h, x.blk.start + 128 * x.tile(t) + u);
+                    }
             }
         }
     } else if (warp == 1 || warp == 2) {
@@ -676,89 +690,110 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
         if (lane == 0) {
             constexpr uint32_t I_S = idesc_bf16(128, 128, false, !ST), I_P = idesc_bf16(128, SUB, false, false),
                                I_O = idesc_bf16(128, 128, false, true);
+            static_assert(!DOTS || ST, "halves of a part of S are read transposed");
             const uint32_t to = tmem + c * 256, tp = to + 128, tp2 = tp + SUB;
-            int n = 0, k = 0, q = 0, np = 0;  // loads and items before this one, tiles and pieces of this context
-            auto full = [&](int i) { return ok = ab.wait(bar + AB_FULL + i % AT_SLOTS, (i / AT_SLOTS) & 1); };
-            auto base = [&](int i) { return smem_u32(sm + (i % AT_SLOTS) * AT_SLOT); };
-            auto free_slot = [&](int i) { umma_commit(bar + AB_EMPTY + i % AT_SLOTS); };
-            auto skip = [&](int first, int last) {  // loads that only the other context uses
-                for (int i = first; i < last && ok; ++i)
-                    if (full(i)) mbar_arrive(bar + AB_EMPTY + i % AT_SLOTS);
+            // row and flow loads and items before this one, tiles and pieces of this context
+            int nr = 0, nf = 0, k = 0, q = 0, np = 0;
+            auto row_full = [&](int i) { return ok = ok && ab.wait(bar + AB_ROW_FULL + i % R::ROWS, (i / R::ROWS) & 1); };
+            auto flow_full = [&](int i) {
+                return ok = ok && ab.wait(bar + AB_FLOW_FULL + i % R::FLOW, (i / R::FLOW) & 1);
+            };
+            auto row_free = [&](int i) { umma_commit(bar + AB_ROW_EMPTY + i % R::ROWS); };
+            auto flow_free = [&](int i) { umma_commit(bar + AB_FLOW_EMPTY + i % R::FLOW); };
+            // loads that only the other context uses
+            auto row_skip = [&](int first, int last) {
+                for (int i = first; i < last && row_full(i); ++i) mbar_arrive(bar + AB_ROW_EMPTY + i % R::ROWS);
+            };
+            auto flow_skip = [&](int first, int last) {
+                for (int i = first; i < last && flow_full(i); ++i) mbar_arrive(bar + AB_FLOW_EMPTY + i % R::FLOW);
             };
             for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
                 const Item x = item_of<REV>(p, it);
                 if (x.tiles == 0) continue;
                 const bool near = (k++ & 1) == c;
-                const int ny0 = n + NS + XW * x.tiles, end = ny0 + 2 * x.tiles;
+                const int r0 = nr, f0 = nf;
+                nr += XW * x.tiles;
+                nf += NS + YZ * x.tiles;
                 if (!near && x.tiles == 1) {
-                    skip(n, end);
-                    n = end;
+                    row_skip(r0, nr);
+                    flow_skip(f0, nf);
                     continue;
                 }
-                const int count = near ? 1 : 2, nx = n + NS + (near ? 0 : XW);
+                const int count = near ? 1 : 2, nx = r0 + (near ? 0 : XW);
                 if (!(ok = ab.wait(bar + AB_O_EMPTY + c, (q & 1) ^ 1))) break;
-                for (int i = n; i < n + NS && ok; ++i) full(i);
-                skip(n + NS, nx);
-                if (!ok || !full(nx)) break;
-                tc_fence_after();
-                const uint64_t xd = desc_k(base(nx));
+                row_skip(r0, nx);
+                if (!row_full(nx)) break;
+                const uint64_t xd = desc_k(smem_u32(row_at(nx)));
                 for (int i = 0; i < NS; ++i) {  // the lowest part first, while the sum is small
-                    const uint64_t sd = ST ? desc_k(base(n + i)) : desc_mn(base(n + i), 16384);
-                    if (i == 0) mma_ss<false>(to, xd, sd, I_S);
-                    else mma_ss<true>(to, xd, sd, I_S);
+                    if (!flow_full(f0 + i)) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(flow_at(f0 + i));
+                    const uint64_t sd = ST ? desc_k(sa) : desc_mn(sa, R::HALF);
+                    const uint64_t xh = xd + (DOTS && (i & 1) ? step_k(4, 16384) : 0);
+                    if (i == 0) mma_ss<false>(to, xh, sd, I_S);
+                    else mma_ss<true>(to, xh, sd, I_S);
 #pragma unroll
-                    for (int ks = 1; ks < 8; ++ks)
-                        mma_ss<true>(to, xd + step_k(ks, 16384), sd + (ST ? step_k(ks, 16384) : step_mn(ks)), I_S);
-                    free_slot(n + i);
+                    for (int ks = 1; ks < (DOTS ? 4 : 8); ++ks)
+                        mma_ss<true>(to, xh + step_k(ks, 16384), sd + (ST ? step_k(ks, R::HALF) : step_mn(ks)), I_S);
+                    flow_free(f0 + i);
                 }
+                if (!ok) break;
                 umma_commit(bar + AB_O_IN + c);
-                if (DOTS && !full(nx + 1)) break;
-                const uint64_t wd = desc_k(base(nx + XW - 1));
-                if (near) skip(nx + XW, ny0);
+                if (DOTS && !row_full(nx + 1)) break;
+                const uint64_t wd = desc_k(smem_u32(row_at(nx + XW - 1)));
+                int ny = f0 + NS;
                 for (int j = 0; j < count && ok; ++j) {
-                    const int ny = ny0 + 2 * j;
-                    if (!full(ny) || (DOTS && !full(ny + 1))) break;
-                    const uint64_t yd = desc_k(base(ny)), zk = desc_k(base(ny + 1)), zd = desc_mn(base(ny + 1), 16384);
 #pragma unroll
-                    for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
+                    for (int sub = 0; sub < 128 / SUB; ++sub, ++np, ny += 2) {
+                        if (!flow_full(ny) || (DOTS && !flow_full(ny + 1))) break;
+                        const uint64_t yd = desc_k(smem_u32(flow_at(ny))), zk = desc_k(smem_u32(flow_at(ny + 1))),
+                                       zd = desc_mn(smem_u32(flow_at(ny + 1)), R::HALF);
                         tc_fence_after();
-                        constexpr uint64_t ROWS64 = 8192 >> 4;
-                        mma_ss<false>(tp, xd, yd + sub * ROWS64, I_P);
+                        mma_ss<false>(tp, xd, yd, I_P);
 #pragma unroll
                         for (int ks = 1; ks < 8; ++ks)
-                            mma_ss<true>(tp, xd + step_k(ks, 16384), yd + sub * ROWS64 + step_k(ks, 16384), I_P);
+                            mma_ss<true>(tp, xd + step_k(ks, 16384), yd + step_k(ks, R::HALF), I_P);
                         if (DOTS) {
-                            mma_ss<false>(tp2, wd, zk + sub * ROWS64, I_P);
+                            mma_ss<false>(tp2, wd, zk, I_P);
 #pragma unroll
                             for (int ks = 1; ks < 8; ++ks)
-                                mma_ss<true>(tp2, wd + step_k(ks, 16384), zk + sub * ROWS64 + step_k(ks, 16384), I_P);
+                                mma_ss<true>(tp2, wd + step_k(ks, 16384), zk + step_k(ks, R::HALF), I_P);
                         }
-                        if (sub == 128 / SUB - 1) {
-                            free_slot(ny);
-                            if (j == count - 1) free_slot(nx);
-                        }
+                        flow_free(ny);
+                        if (sub == 128 / SUB - 1 && j == count - 1) row_free(nx);
                         umma_commit(bar + AB_P_FULL + c);
-                        if (!DOTS && !full(ny + 1)) break;
+                        if (!DOTS && !flow_full(ny + 1)) break;
                         if (!(ok = ab.wait(bar + AB_P_READY + c, np & 1))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < SUB / 16; ++ks)
                             umma_bf16_ts(to, tp + (ks * 16 / (SUB / 2)) * (SUB / 2) + (ks * 16 % (SUB / 2)) / 2,
-                                         zd + step_mn(sub * 4 + ks), I_O);
+                                         zd + step_mn(ks), I_O);
+                        flow_free(ny + 1);
                     }
-                    if (ok) free_slot(ny + 1);
                 }
                 if (!ok) break;
-                if (DOTS) free_slot(nx + 1);  // the row threads read it before their last P_READY
+                if (DOTS) row_free(nx + 1);  // the row threads read it before their last P_READY
                 umma_commit(bar + AB_O_FULL + c);
-                skip(ny0 + 2 * count, end);
-                n = end;
+                row_skip(nx + XW, nr);
+                flow_skip(ny, nf);
                 ++q;
             }
         }
     } else if (warp == 3) {
-        // prefix sums of the items' log decays, up to four of them ahead
-        int k = 0;
+        // an item's prefix sums of the log decays, then its x and w
+        int k = 0, n = 0;
+        auto rows = [&](const CUtensorMap *m, int h, int tok) {  // 128 tokens in 64-token, 64-channel boxes
+            const int s = n % R::ROWS;
+            if (!(ok = ok && ab.wait(bar + AB_ROW_EMPTY + s, ((n / R::ROWS) & 1) ^ 1))) return;
+            unsigned char *d = row_at(n++);
+            mbar_arrive_expect_tx(bar + AB_ROW_FULL + s, R::ROW_SLOT);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    tma_load_3d(d + x * 16384 + t * 8192, m, bar + AB_ROW_FULL + s, 64 * x, h, tok + 64 * t);
+        };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x = item_of<REV>(p, it);
             if (x.tiles == 0) continue;
@@ -774,23 +809,31 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             for (int u = 0; u < PER; ++u) a[lane * PER + u + 1] = decay_pair(s[u]);
             warp_arrive(bar + AB_A_FULL + slot);
             ++k;
+            if (lane == 0)
+                for (int t = 0; t < x.tiles; ++t) {
+                    rows(&mx, x.h, x.blk.start + 128 * x.tile(t));
+                    if (DOTS) rows(&mw, x.h, x.blk.start + 128 * x.tile(t));
+                }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         }
-    } else if (warp >= 4) {
+    } else {
         const int c = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, r = (tid - 128) & 127, w = warp & 3;
         constexpr int HSUB = SUB / 2;  // this thread's score columns of a piece: from hf * HSUB
         float *col = reinterpret_cast<float *>(sm + AT_COL) + (warp - 4) * (kLinMaxBlock / 2);
         const uint32_t to = tmem + c * 256 + ((uint32_t)w << 21), tp = to + 128, tp2 = tp + SUB;
         auto wait = [&](uint64_t *b, uint32_t ph) { return ok = __all_sync(0xffffffffu, ab.wait(b, ph)); };
-        auto full = [&](int i) { return wait(bar + AB_FULL + i % AT_SLOTS, (i / AT_SLOTS) & 1); };
-        int n = 0, k = 0, q = 0, np = 0;  // loads and items before this one, tiles and pieces of this context
+        // row and flow loads and items before this one, tiles and pieces of this context
+        int nr = 0, nf = 0, k = 0, q = 0, np = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x = item_of<REV>(p, it);
             if (x.tiles == 0) continue;
             const int slot = k % AT_PREFIX;
             if (!wait(bar + AB_A_FULL + slot, (k / AT_PREFIX) & 1)) break;
             const bool near = (k++ & 1) == c;
-            const int ny0 = n + NS + XW * x.tiles, nw = n + NS + (near ? 1 : XW + 1), count = near ? 1 : 2;
-            n = ny0 + 2 * x.tiles;
+            const int nw = nr + (near ? 1 : XW + 1), count = near ? 1 : 2;
+            int nz = nf + NS + 1;
+            nr += XW * x.tiles;
+            nf += NS + YZ * x.tiles;
             if (!near && x.tiles == 1) {
                 warp_arrive(bar + AB_A_EMPTY + slot);
                 continue;
@@ -816,7 +859,9 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             const F2 rf2 = f2(rf, rf);
             F2 dots = f2(0.f, 0.f);
             float dot = 0.f, dot_state = 0.f;
-            if (!wait(bar + AB_O_IN + c, q & 1) || (DOTS && !full(nw))) break;
+            if (!wait(bar + AB_O_IN + c, q & 1) ||
+                (DOTS && !wait(bar + AB_ROW_FULL + nw % R::ROWS, (nw / R::ROWS) & 1)))
+                break;
             tc_fence_after();
             {
                 uint32_t v[2][32];
@@ -828,7 +873,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                     scale32(v[u], f);
                     tmem_st32(to + 64 * hf + 32 * u, v[u]);
                     if (DOTS) {
-                        const unsigned char *wt = sm + (nw % AT_SLOTS) * AT_SLOT;
+                        const unsigned char *wt = row_at(nw);
 #pragma unroll
                         for (int k8 = 0; k8 < 4; ++k8) {
                             const uint4 g =
@@ -843,14 +888,15 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
                 }
             }
             for (int j = 0; j < count && ok; ++j) {
-                const int j0 = 128 * x.tile(j), nz = ny0 + 2 * j + 1;
-                for (int sub = 0; sub < 128 / SUB; ++sub, ++np) {
+                const int j0 = 128 * x.tile(j);
+                for (int sub = 0; sub < 128 / SUB; ++sub, ++np, nz += 2) {
                     if (!wait(bar + AB_P_FULL + c, np & 1)) break;
                     tc_fence_after();
-                    if (sub == 0 && len - j0 < 128) {  // what lies past the block's end must not meet P's zeros
-                        if (!full(nz)) break;
-                        if (r >= len - j0) {
-                            unsigned char *z = sm + (nz % AT_SLOTS) * AT_SLOT + hf * 16384 + r * 128;
+                    const int left = len - j0 - sub * SUB;
+                    if (left < SUB) {  // what lies past the block's end must not meet P's zeros
+                        if (!wait(bar + AB_FLOW_FULL + nz % R::FLOW, (nz / R::FLOW) & 1)) break;
+                        if (r < SUB && r >= left) {
+                            unsigned char *z = flow_at(nz) + hf * R::HALF + r * 128;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 *reinterpret_cast<uint4 *>(z + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
