@@ -162,7 +162,8 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 // where a CUDA core rounds them, which over K / 8 steps in one accumulator cost
 // 1.7e-6 to 4e-6 in the results; so with a split operand each step's products
 // are summed from zero and added to the accumulator in fp32.
-template <int K, int MT, int NT8, bool SA, bool SB, typename FA, typename FB>
+// TA, TB: the operand is exact in tf32 as it is (a bf16 value).
+template <int K, int MT, int NT8, bool SA, bool SB, bool TA, bool TB, typename FA, typename FB>
 __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, int r0, int c0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll 2
@@ -174,14 +175,14 @@ __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, in
             const float x[4] = {a(r, k + t), a(r + 8, k + t), a(r, k + t + 4), a(r + 8, k + t + 4)};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                ah[m][u] = tf32(x[u]);
+                ah[m][u] = TA ? __float_as_uint(x[u]) : tf32(x[u]);
                 if (SA) al[m][u] = tf32(x[u] - __uint_as_float(ah[m][u]));
             }
         }
 #pragma unroll
         for (int n = 0; n < NT8; ++n) {
             const float x0 = b(k + t, c0 + 8 * n + g), x1 = b(k + t + 4, c0 + 8 * n + g);
-            const uint32_t h0 = tf32(x0), h1 = tf32(x1);
+            const uint32_t h0 = TB ? __float_as_uint(x0) : tf32(x0), h1 = TB ? __float_as_uint(x1) : tf32(x1);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 if (!SA && !SB) {
@@ -195,6 +196,32 @@ __device__ __forceinline__ void product(float (&acc)[MT][NT8][4], FA a, FB b, in
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][n][e] += d[e];
             }
+        }
+    }
+}
+
+// acc[n] += x_r . y_c over K channels, both [row][K] in shared memory with leading
+// dimension ld: bf16 products, exact, 16 channels an instruction and two a load
+// (as tf32 the same scores took a load and a conversion an element).
+template <int K, int NT8>
+__device__ __forceinline__ void row_products(float (&acc)[1][NT8][4], const __nv_bfloat16 *x, const __nv_bfloat16 *y,
+                                             int ld, int r0, int c0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    auto two = [&](const __nv_bfloat16 *p, int row, int k) {
+        return *reinterpret_cast<const uint32_t *>(p + row * ld + k + 2 * t);
+    };
+#pragma unroll 2
+    for (int k = 0; k < K; k += 16) {
+        const uint32_t a[4] = {two(x, r0 + g, k), two(x, r0 + g + 8, k), two(x, r0 + g, k + 8), two(x, r0 + g + 8, k + 8)};
+#pragma unroll
+        for (int n = 0; n < NT8; ++n) {
+            float(&d)[4] = acc[0][n];
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                "{%0,%1,%2,%3};"
+                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(two(y, c0 + 8 * n + g, k)),
+                  "r"(two(y, c0 + 8 * n + g, k + 8)));
         }
     }
 }
@@ -267,7 +294,7 @@ template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void 
     loads_done();
     const int warp = threadIdx.x >> 5, r0 = (warp % WM) * 32, c0 = (warp / WM) * COLS;
     float acc[2][N8][4] = {};
-    product<CH, 2, N8, true, F32>(
+    product<CH, 2, N8, true, F32, false, !F32>(
         acc, [&](int r, int k) { return to_f32(xs[k * LDX + r]) * w[k]; },
         [&](int k, int c) { return to_f32(ys[k * LDY + c]); }, r0, c0);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -381,6 +408,10 @@ struct AttendArgs {
 // which leaves room for two CTAs on an SM. 2 x 999 tokens x 4 heads, fp32, 64 x 128:
 // the backward's three passes took 85 us as launches of their own, with loads
 // and products in turn; the whole backward went from 102 to 63 us.
+// In bf16 bound by instructions (8 x 2048 tokens x 16 heads, 64 x 64: 72 % of the
+// issue slots, mostly loads of single values and conversions): 154 us for the
+// whole forward, 137 with the scores as bf16 products and no conversions of
+// values that are exact as they are.
 template <typename T, int DC, int DO> constexpr size_t attend_smem() {
     return 2 * CH * ld_rows<T>(DC) * sizeof(T) + CH * (DO + 8) * 4 + CH * ld_cols<T>(DO) * sizeof(T) + (CH + 1) * 8;
 }
@@ -430,7 +461,7 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
     // the state part, 64 rows of the contraction at a time, and the scores
     float acc[1][N8][4] = {}, sc[1][4][4] = {};
     auto state_part = [&](int k0) {
-        product<CH, 1, N8, F32, EXACT>(
+        product<CH, 1, N8, F32, EXACT, !F32, false>(
             acc, [&](int r, int k) { return to_f32(xs[r * LDX + k0 + k]); },
             [&](int k, int c) { return ss[k * LDS + c]; }, r0, c0);
     };
@@ -439,9 +470,11 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
         __syncthreads();
         load_state(CH);
     }
-    product<DC, 1, 4, F32, F32>(
-        sc, [&](int r, int k) { return to_f32(xs[r * LDX + k]); },
-        [&](int k, int c) { return to_f32(ys[c * LDX + k]); }, r0, s0);
+    if constexpr (F32)
+        product<DC, 1, 4, true, true, false, false>(
+            sc, [&](int r, int k) { return xs[r * LDX + k]; }, [&](int k, int c) { return ys[c * LDX + k]; }, r0, s0);
+    else
+        row_products<DC, 4>(sc, xs, ys, LDX, r0, s0);
     if (DC > CH) {
         loads_done();
         state_part(CH);
@@ -490,7 +523,7 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
             ps[i * LDP + j] = v;
         }
     __syncthreads();
-    product<CH, 1, N8, EXACT, F32>(
+    product<CH, 1, N8, EXACT, F32, false, !F32>(
         acc, [&](int r, int k) { return ps[r * LDP + k]; },
         [&](int k, int c) { return to_f32(zs[k * LDZ + c]); }, r0, c0);
     if (p.dot) row_dots(dots[1][half]);
