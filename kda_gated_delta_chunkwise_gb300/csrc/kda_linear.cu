@@ -26,10 +26,10 @@
 //   X = e^{L_end} <S, G> + sum_j k_j.dk_j(G part),
 // so it needs the row dots that the dq and dk passes have at hand.
 //
-// The products run on mma.sync tf32. bf16 values are exact in tf32; an fp32
-// operand is split in two tf32 parts (22 bits) where its error would reach an
-// fp32 output, and kept as one part (11 bits, against the 8 of the bf16 output)
-// where it would not. Accumulators, states and sums are fp32.
+// The products run on mma.sync tf32 (scores of bf16 inputs: bf16, exact). bf16
+// values are exact in tf32; an fp32 operand is split in two tf32 parts (22 bits)
+// where its error would reach an fp32 output, and kept as one part (11 bits,
+// against the 8 of the bf16 output) where it would not. Accumulators, states and sums are fp32.
 #include <algorithm>
 
 #include "kda_linear.cuh"
