@@ -211,6 +211,14 @@ constexpr int ST_TOK = 64;
 constexpr int ST_TILE = ST_TOK * D * 2;       // 16 KB
 constexpr int ST_STAGE = 4 * ST_TILE;         // x (then its high part), middle, low, y
 constexpr int ST_STAGES = 3;
+// The parts' join factors, from the weights' warp to the accumulator warps. The
+// ring needs no barrier of its own: the factor of part q is written once part
+// q - 2 is converted, so its last tile, n, is in shared memory and tile
+// n - ST_STAGES, of part q - 5 or a later one, multiplied; that part's
+// accumulators were free, so those of part q - 7 had been read out, and its
+// factor with them. Seven factors may be waiting to be read.
+constexpr int ST_JOIN = 8;
+static_assert(ST_STAGES == 3 && ST_JOIN >= 7, "factors that may be waiting");
 constexpr int ST_THREADS = 768;
 constexpr int ST_W = ST_STAGES * ST_STAGE;                   // weights [2][kLinMaxBlock]
 constexpr int ST_BAR = ST_W + 2 * kLinMaxBlock * 4;
@@ -233,7 +241,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
     unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + ST_BAR);
     float *wts = reinterpret_cast<float *>(sm + ST_W);
-    __shared__ float join[4];
+    __shared__ float join[ST_JOIN];
     uint32_t *tm = reinterpret_cast<uint32_t *>(bar + SB_COUNT);
     const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -337,7 +345,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                     w[lane * PER + u] = decay_ratio(decay_pair(REV ? a[u] : all - a[u]), make_float2(0.f, 0.f));
                 // what the sum so far (forward) or this part (reverse) is multiplied by when they are joined
                 if (lane == 0)
-                    join[q & 3] = decay_ratio(decay_pair(REV ? sum : all), make_float2(0.f, 0.f));
+                    join[q % ST_JOIN] = decay_ratio(decay_pair(REV ? sum : all), make_float2(0.f, 0.f));
                 warp_arrive(bar + SB_W_FULL + (q & 1));
                 sum += all;
             }
@@ -359,7 +367,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                 tc_fence_after();
                 // a later part joins the sum in memory (in L2: it is this CTA's own 64 KB), in fp32 sums that
                 // round, where the tensor core's would cut
-                const float f = join[q & 3], f_old = REV ? 1.f : f, f_new = REV ? f : 1.f;
+                const float f = join[q % ST_JOIN], f_old = REV ? 1.f : f, f_new = REV ? f : 1.f;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t x[32], y[32];
