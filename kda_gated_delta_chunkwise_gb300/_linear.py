@@ -6,8 +6,9 @@ strides, outputs and workspaces through PyTorch, raw pointers and a CUDA
 stream. There is no fallback.
 
 q, k and v may be slices of a wider tensor (a fused projection): their last two
-axes must be contiguous and their tokens evenly spaced. Every call also takes
-``stream``: it then runs there, its outputs and workspace are allocated for that
+axes must be contiguous and their tokens evenly spaced. A call runs on its
+tensors' device, current or not. Every call also takes ``stream``, of that
+device: it then runs there, its outputs and workspace are allocated for that
 stream, and the inputs must be ready on it.
 """
 from __future__ import annotations
@@ -148,13 +149,21 @@ def _bytes(name: str, n: int, T: int, H: int, dk: int, dv: int, dtype) -> int:
 
 
 def _on_stream(f):
-    """Runs ``f`` with its ``stream`` current, so that what it allocates belongs to that stream."""
+    """Runs ``f`` on q's device, with its ``stream`` current where one is given, so that what it allocates belongs to
+    that stream. A launch goes to the current device, whatever the pointers and the stream's handle belong to."""
     @functools.wraps(f)
     def g(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
+        q = args[0] if args else kw.get("q")
+        index = q.get_device() if isinstance(q, torch.Tensor) else -1  # -1: not a CUDA tensor, refused by f
+        if stream is not None:
+            if index >= 0 and stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, q on cuda:{index}")
+            with torch.cuda.stream(stream):
+                return f(*args, **kw)
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return f(*args, **kw)
+        return f(*args, **kw)
     return g
 
 
