@@ -12,6 +12,7 @@ copied back to the host.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -164,6 +165,25 @@ def device_errors(reset: bool = True) -> int:
     return v.value
 
 
+def _on_device(f):
+    """Runs ``f`` with q's device current: a launch goes to the current device, whatever the pointers belong to."""
+    @functools.wraps(f)
+    def g(*args, **kw):
+        q = args[0] if args else kw.get("q")
+        index = q.get_device() if isinstance(q, torch.Tensor) else -1  # -1: host tensors, or refused by f
+        if index < 0:
+            return f(*args, **kw)
+        stream = kw.get("stream")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, q on cuda:{index}")
+        if index == torch.cuda.current_device():
+            return f(*args, **kw)
+        with torch.cuda.device(index):
+            return f(*args, **kw)
+    return g
+
+
+@_on_device
 def selftest_bounded_wait(q, k, v, alpha, beta, stall_chunk: int, *, stream=None):
     """Diagnostic: the tensor-core prefill of one bf16 sequence of one head
     (q, k, v [T, 128], alpha [T, 128], beta [T]) with its state chain stalled
@@ -329,6 +349,7 @@ def _check_gate(gate: str, alpha, lead: tuple, dk: int, dev):
     return alpha
 
 
+@_on_device
 def prefill(q, k, v, alpha, beta, initial_state=None, *, output_final_state: bool = True,
             algo: str = "auto", gate: str = "channel", out=None, final_state=None, stream=None,
             piece_tokens: int = 0):
@@ -395,6 +416,7 @@ def prefill_segmented_workspace_bytes(T: int, H: int, dk: int = 128, dv: int = 1
     return int(load().kda_prefill_segmented_workspace_bytes(B, T, H, dk, dv, code, segments))
 
 
+@_on_device
 def prefill_segmented(q, k, v, alpha, beta, initial_state=None, *, segments: int = 0, gate: str = "channel",
                       output_final_state: bool = True, out=None, final_state=None, workspace=None, stream=None):
     """Prefill of one long sequence with its token axis cut into segments that
@@ -434,6 +456,7 @@ def varlen_workspace_bytes(N: int, H: int, dk: int = 128, dv: int = 128) -> int:
     return int(load().kda_varlen_workspace_bytes(N, H, dk, dv))
 
 
+@_on_device
 def varlen_prefill(q, k, v, alpha, beta, cu_seqlens, initial_state=None, *,
                    output_final_state: bool = True, out=None, final_state=None, workspace=None,
                    device_status=None, stream=None):
@@ -479,6 +502,7 @@ def varlen_prefill(q, k, v, alpha, beta, cu_seqlens, initial_state=None, *,
     return out, final_state
 
 
+@_on_device
 def decode_step(q, k, v, alpha, beta, state, *, out=None, stream=None):
     """One recurrent KDA step per (sequence, head); ``state`` is updated in place.
 
@@ -511,6 +535,7 @@ def decode_step(q, k, v, alpha, beta, state, *, out=None, stream=None):
     return out
 
 
+@_on_device
 def varlen_prefill_slots(q, k, v, alpha, beta, cu_seqlens, state_pool, slots, *, gate: str = "channel",
                          out=None, workspace=None, device_status=None, stream=None):
     """Packed prefill whose states live in a pool: sequence n starts from
@@ -550,6 +575,7 @@ def varlen_prefill_slots(q, k, v, alpha, beta, cu_seqlens, state_pool, slots, *,
     return out
 
 
+@_on_device
 def decode_step_slots(q, k, v, alpha, beta, state_pool, slots, *, gate: str = "channel", out=None,
                       device_status=None, stream=None):
     """One recurrent step per (sequence, head) on ``state_pool[slots[n]]``
@@ -582,6 +608,7 @@ def decode_step_slots(q, k, v, alpha, beta, state_pool, slots, *, gate: str = "c
     return out
 
 
+@_on_device
 def prefill_fp8(q, k, v, q_scale, k_scale, v_scale, alpha, beta, initial_state=None, *, gate: str = "channel",
                 output_final_state: bool = True, out=None, final_state=None, stream=None, piece_tokens: int = 0):
     """``prefill`` on FP8 inputs in the MX block format: q, k, v are uint8
@@ -621,6 +648,7 @@ def prefill_fp8(q, k, v, q_scale, k_scale, v_scale, alpha, beta, initial_state=N
     return out, final_state
 
 
+@_on_device
 def prefill_backward(q, k, v, alpha, beta, d_o, initial_state=None, d_final_state=None, *,
                      gate: str = "channel", want_initial_state_grad: bool = True, workspace=None, stream=None):
     """Gradients of ``prefill`` (equal-length batches) for
@@ -663,6 +691,7 @@ def prefill_backward(q, k, v, alpha, beta, d_o, initial_state=None, d_final_stat
     return out
 
 
+@_on_device
 def varlen_prefill_backward(q, k, v, alpha, beta, d_o, cu_seqlens, initial_state=None, d_final_state=None, *,
                             gate: str = "channel", workspace=None, device_status=None, stream=None):
     """Gradients of ``varlen_prefill`` (sequences packed by ``cu_seqlens``):
