@@ -501,7 +501,10 @@ kda_status_t kda_selftest_bounded_wait(const void *q, const void *k, const void 
  * Decays come as natural logarithms g <= 0 (unlike the linear alpha of the
  * calls above: the chunked form adds logarithms, and the gradient of a
  * logarithm stays finite, zero, at a reset). g = -inf, or anything <= -128, is
- * a reset: the state before the token is gone.
+ * a reset: the state before the token is gone. A NaN makes the state NaN, from
+ * its token to the next reset, and so the outputs there and what depends on
+ * them; no other sequence or head. (The gradient of the log decays is NaN there
+ * too, and may be for other tokens of the 256 around the NaN.)
  *
  *   KDA_DECAY_TOKEN  log_decay [.., T, H]: one per token and head
  *   KDA_DECAY_HEAD   log_decay [H]: one per head, the same for every token

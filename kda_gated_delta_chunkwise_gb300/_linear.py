@@ -234,7 +234,7 @@ def linear_prefill(q, k, v, log_decay=None, initial_state=None, *, decay: str = 
     q, k: [B, T, H, d_k]; v: [B, T, H, d_v] (bf16 or fp32, the same type);
     log_decay: natural logarithms <= 0, fp32 [B, T, H] (decay="token"), [H]
     (decay="head") or None (decay="none"); -inf, or anything <= -128, resets
-    the state; initial_state: [B, H, d_k, d_v] fp32 or None (zeros).
+    the state, a NaN makes it NaN up to the next reset; initial_state: [B, H, d_k, d_v] fp32 or None (zeros).
     Returns (o [B, T, H, d_v] in v's type, final_state fp32 or None).
     """
     return _prefill(q, k, v, log_decay, None, initial_state, decay, scale, output_final_state, out, final_state,

@@ -30,6 +30,8 @@
 // values are exact in tf32; an fp32 operand is split in two tf32 parts (22 bits)
 // where its error would reach an fp32 output, and kept as one part (11 bits,
 // against the 8 of the bf16 output) where it would not. Accumulators, states and sums are fp32.
+#include <math_constants.h>
+
 #include <algorithm>
 
 #include "kda_linear.cuh"
@@ -266,7 +268,7 @@ template <typename T> struct StateArgs {
     int64_t x_stride, y_stride;
     const float *log_decay;
     int decay;
-    float *out, *total;
+    float *out, *total, *total_rev;  // e^{L_end} as the forward scan and as the reverse one passes over it, nullable
 };
 template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void block_state(const StateArgs<T> &p) {
     constexpr bool F32 = sizeof(T) == 4;
@@ -277,6 +279,7 @@ template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void 
     T *ys = xs + CH * LDX;
     float2 *a = reinterpret_cast<float2 *>(ys + CH * LDY);
     __shared__ long long scan[NT / 32];
+    __shared__ DecayEvents events;
     __shared__ float w[CH];
     const LinGeom &geo = p.geo;
     const int b = blockIdx.x / geo.H, h = blockIdx.x % geo.H;
@@ -284,9 +287,14 @@ template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void 
     if (blk.len <= 0) return;
     load_tile<T, DK>(xs, LDX, p.x + blk.start * p.x_stride + h * DK, p.x_stride, blk.len);
     load_tile<T, DV>(ys, LDY, p.y + blk.start * p.y_stride + h * DV, p.y_stride, blk.len);
-    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan);
+    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan, &events);
     const float2 end = a[blk.len];
-    if (p.total && threadIdx.x == 0) p.total[(int64_t)b * geo.H + h] = decay_ratio(end, make_float2(0.f, 0.f));
+    if (threadIdx.x == 0) {
+        const int64_t at = (int64_t)b * geo.H + h;
+        const float total = decay_ratio(end, make_float2(0.f, 0.f));
+        if (p.total) p.total[at] = events.nan_before(blk.len - 1) ? CUDART_NAN_F : total;
+        if (p.total_rev) p.total_rev[at] = events.nan_after(-1) ? CUDART_NAN_F : total;
+    }
     if (threadIdx.x < CH) {
         const int s = min((int)threadIdx.x, blk.len - 1);
         w[threadIdx.x] = REV ? decay_ratio(a[s + 1], make_float2(0.f, 0.f)) : decay_ratio(end, a[s + 1]);
@@ -330,10 +338,12 @@ struct ScanArgs {
     const float *s0;  // nullable
     float *sT;        // nullable
     float c;
+    const float *total;  // the decay over every block
 };
 template <bool REV>
-__device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &q, const float *total, int size4) {
+__device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &q, int size4) {
     const float c = q.c;
+    const float *total = q.total;
     if (geo.status && *geo.status != KDA_DEV_OK) return;
     const int per = size4 / NT;
     const int64_t nh = blockIdx.x / per;
@@ -374,12 +384,12 @@ __device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &
 
 // The backward's two directions do not depend on each other: one launch (blockIdx.y).
 __global__ void __launch_bounds__(NT)
-lin_scan_kernel(const LinGeom geo, const ScanArgs fwd, const ScanArgs rev, const float *total, int size4) {
+lin_scan_kernel(const LinGeom geo, const ScanArgs fwd, const ScanArgs rev, int size4) {
     after_previous();
     if (blockIdx.y == 0) {
-        if (fwd.states) scan_blocks<false>(geo, fwd, total, size4);
+        if (fwd.states) scan_blocks<false>(geo, fwd, size4);
     } else {
-        scan_blocks<true>(geo, rev, total, size4);
+        scan_blocks<true>(geo, rev, size4);
     }
 }
 
@@ -428,6 +438,7 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
     T *zs = reinterpret_cast<T *>(ss + CH * LDS);
     float2 *a = reinterpret_cast<float2 *>(zs + CH * LDZ);
     __shared__ long long scan[NT / 32];
+    __shared__ DecayEvents events;
     __shared__ float dots[2][2][CH];
     const LinGeom &geo = p.geo;
     const int h = blockIdx.x % geo.H, b = blockIdx.x / geo.H;
@@ -455,7 +466,7 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
     load_state(0);
     load_tile<T, DC>(ys, LDX, (const T *)p.y + tok * p.y_stride + h * DC, p.y_stride, len);
     load_tile<T, DO>(zs, LDZ, (const T *)p.z + tok * p.z_stride + h * DO, p.z_stride, len);
-    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, len, len, a, scan);
+    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, len, len, a, scan, &events);
     loads_done();
 
     // the state part, 64 rows of the contraction at a time, and the scores
@@ -501,8 +512,8 @@ __device__ __forceinline__ void attend_block(const AttendArgs &p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = min(r0 + g + 8 * e, len - 1);
-        const float f = p.c_state * (REV ? decay_ratio(a[len], a[i + 1])
-                                         : decay_ratio(a[i + 1], make_float2(0.f, 0.f)));
+        float f = p.c_state * (REV ? decay_ratio(a[len], a[i + 1]) : decay_ratio(a[i + 1], make_float2(0.f, 0.f)));
+        if (REV ? events.nan_after(i) : events.nan_before(i)) f = CUDART_NAN_F;
 #pragma unroll
         for (int n = 0; n < N8; ++n) {
             acc[0][n][2 * e] = f == 0.f ? 0.f : acc[0][n][2 * e] * f;  // a reset, whatever the state held
@@ -610,7 +621,7 @@ lin_decay_grad_kernel(LinGeom geo, const float *log_decay, int decay, const floa
             x += s.x * g.x + s.y * g.y + s.z * g.z + s.w * g.w;
         }
     }
-    x *= total[bh];
+    x = total[bh] == 0.f ? 0.f : x * total[bh];  // a reset, whatever the state held
     for (int i = tid; i < blk.len; i += NT) {
         const int64_t at = (int64_t)(blk.start + i) * geo.H + h;
         x += kdk_state[at] + (dot_stride ? kdk_state[at + dot_stride] : 0.f);
@@ -687,7 +698,7 @@ struct Plan {
     LinGeom geo;
     int4 *blocks;
     int32_t *seq_block, *status, *place;
-    float *total, *states, *grads, *qdq, *kdk, *kdk_state, *block_sum;
+    float *total, *total_rev, *states, *grads, *qdq, *kdk, *kdk_state, *block_sum;
     __nv_bfloat16 *s_parts, *g_parts;  // tensor-core path: the joined states as bf16 parts
     float *inner;                      // and <S, G> of every block, in pieces
     int64_t part_stride, dot_stride;
@@ -717,6 +728,7 @@ Plan make_plan(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
     }
     const size_t state = (size_t)nb * H * dk * dv * 4;
     p.total = (float *)take((size_t)nb * H * 4);
+    if (back) p.total_rev = (float *)take((size_t)nb * H * 4);
     p.states = (float *)take(state);
     p.part_stride = nb * H * dk * dv;
     if (back && (!tc || rolled)) p.grads = (float *)take(state);
@@ -755,9 +767,9 @@ cudaError_t run_states(const Plan &p, const LinArgs &a, bool back, Launches &l) 
     static std::atomic<uint64_t> allowed{0};
     KDA_TRY(allow_smem(k, smem, allowed));
     const StateArgs<T> f{p.geo, (const T *)a.k, (const T *)a.v, a.k_stride, a.v_stride, a.log_decay, a.decay, p.states,
-                         p.total};
+                         p.total, p.total_rev};
     const StateArgs<T> r{p.geo, (const T *)a.q, (const T *)a.d_o, a.q_stride, (int64_t)a.H * DV, a.log_decay, a.decay,
-                         p.grads, nullptr};
+                         p.grads, nullptr, nullptr};
     const dim3 grid((unsigned)((int64_t)p.geo.nblocks * p.geo.H), back ? 2 : 1);
     return l.next(k, grid, NT, smem, f, r);
 }
@@ -765,7 +777,7 @@ cudaError_t run_states(const Plan &p, const LinArgs &a, bool back, Launches &l) 
 cudaError_t run_scan(const Plan &p, const ScanArgs &fwd, const ScanArgs *rev, int dk, int dv, Launches &l) {
     const int size4 = dk * dv / 4;
     const dim3 grid((unsigned)((int64_t)p.geo.N * p.geo.H * (size4 / NT)), rev ? 2 : 1);
-    return l.next(lin_scan_kernel, grid, NT, 0, p.geo, fwd, rev ? *rev : ScanArgs{}, p.total, size4);
+    return l.next(lin_scan_kernel, grid, NT, 0, p.geo, fwd, rev ? *rev : ScanArgs{}, size4);
 }
 
 cudaError_t prepare_blocks(const Plan &p, const LinArgs &a, bool rolled, Launches &l) {
@@ -784,8 +796,8 @@ cudaError_t forward_tc(const LinArgs &a, cudaStream_t s) {
     const bool need_states = a.sT || a.cu_seqlens || p.geo.per_seq > 1;
     if (tokens > 0 && need_states)
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, l));
-    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f}, nullptr, 128, 128, l));
+                                p.total, nullptr, l));
+    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f, p.total}, nullptr, 128, 128, l));
     if (tokens == 0) return cudaSuccess;
     RollTc t{};
     t.geo = p.geo;
@@ -806,12 +818,12 @@ cudaError_t backward_rolled_tc(const LinArgs &a, cudaStream_t s) {
     KDA_TRY(prepare_blocks(p, a, true, l));
     if (tokens > 0) {
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, l));
+                                p.total, p.total_rev, l));
         KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.grads,
-                                nullptr, l));
+                                nullptr, nullptr, l));
     }
-    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale};
-    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f}, &grads, 128, 128, l));
+    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale, p.total_rev};
+    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f, p.total}, &grads, 128, 128, l));
     if (tokens == 0) return cudaSuccess;
     RollTc t{};
     t.geo = p.geo;
@@ -849,14 +861,14 @@ cudaError_t backward_tc(const LinArgs &a, cudaStream_t s) {
     KDA_TRY(prepare_blocks(p, a, false, l));
     if (tokens > 0) {
         KDA_TRY(launch_state_tc(p.geo, false, a.k, a.k_stride, a.v, a.v_stride, tokens, a.log_decay, a.decay, p.states,
-                                p.total, l));
+                                p.total, p.total_rev, l));
         KDA_TRY(launch_scan_tc(p.geo, false, p.states, p.total, a.s0, nullptr, 1.f, p.s_parts, p.part_stride,
                                nullptr, nullptr, l));
         // the blocks' own sums of the states are done with: those of the gradients take their place
         KDA_TRY(launch_state_tc(p.geo, true, a.q, a.q_stride, a.d_o, so, tokens, a.log_decay, a.decay, p.states,
-                                nullptr, l));
+                                nullptr, nullptr, l));
     }
-    KDA_TRY(launch_scan_tc(p.geo, true, p.states, p.total, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
+    KDA_TRY(launch_scan_tc(p.geo, true, p.states, p.total_rev, a.dsT, a.ds0, a.scale, p.g_parts, p.part_stride,
                            p.s_parts, p.inner, l));
     if (tokens == 0)
         return head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
@@ -900,7 +912,7 @@ template <typename T, int DK, int DV> cudaError_t forward(const LinArgs &a, cuda
     KDA_TRY(prepare_blocks(p, a, false, l));
     if (p.geo.nblocks > 0)
         KDA_TRY((run_states<T, DK, DV>(p, a, false, l)));
-    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f}, nullptr, DK, DV, l));
+    KDA_TRY(run_scan(p, {p.states, a.s0, a.sT, 1.f, p.total}, nullptr, DK, DV, l));
     if (p.geo.nblocks == 0) return cudaSuccess;
     AttendArgs t{};
     t.geo = p.geo;
@@ -930,8 +942,8 @@ template <typename T, int DK, int DV> cudaError_t backward(const LinArgs &a, cud
     KDA_TRY(prepare_blocks(p, a, false, l));
     const int64_t so = (int64_t)a.H * DV;
     if (p.geo.nblocks > 0) KDA_TRY((run_states<T, DK, DV>(p, a, true, l)));
-    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale};
-    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f}, &grads, DK, DV, l));
+    const ScanArgs grads{p.grads, a.dsT, a.ds0, a.scale, p.total_rev};
+    KDA_TRY(run_scan(p, {p.states, a.s0, nullptr, 1.f, p.total}, &grads, DK, DV, l));
     const bool dots = a.d_decay != nullptr, head = a.decay == KDA_DECAY_HEAD;
     if (p.geo.nblocks == 0) return dots && head ? cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s) : cudaSuccess;
     AttendArgs t{};

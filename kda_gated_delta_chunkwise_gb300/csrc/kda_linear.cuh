@@ -176,6 +176,10 @@ __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &fir
 // A decay of e^-128 already leaves nothing of an fp32 state (2^-185 of its
 // largest value), so every log decay is clamped there, -inf (a reset) included,
 // and sums of up to 2^23 tokens keep an exact whole part.
+// A NaN is clamped too, so that sums and ratios stay numbers; it is carried on
+// beside them (nan_before, nan_after): the decay of a stretch is NaN where the
+// stretch's NaN nearest to the token it leads to has no reset in between, as in
+// the recurrence, where the state is NaN from a NaN decay to the next reset.
 constexpr float kMinLogDecay = -128.f;
 __device__ __forceinline__ long long decay_fixed(float g) {
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
@@ -196,21 +200,46 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ float decay_ratio(float2 a, float2 b) {
     return exp2_approx((a.x - b.x) + (a.y - b.y));
 }
+// The NaN and the reset log decays among 64 tokens, one bit each.
+struct DecayEvents {
+    uint32_t nan[2], reset[2];
+    __device__ __forceinline__ bool any_nan() const { return (nan[0] | nan[1]) != 0u; }
+    __device__ __forceinline__ unsigned long long nans() const { return nan[0] | (unsigned long long)nan[1] << 32; }
+    __device__ __forceinline__ unsigned long long all() const {
+        return nans() | reset[0] | (unsigned long long)reset[1] << 32;
+    }
+    // the decay over tokens 0 .. i is NaN
+    __device__ __forceinline__ bool nan_before(int i) const {
+        if (!any_nan()) return false;
+        const unsigned long long e = all() & ((2ull << i) - 1);
+        return e && (nans() >> (63 - __clzll((long long)e)) & 1);
+    }
+    // the decay over tokens i + 1 .. 63 is NaN
+    __device__ __forceinline__ bool nan_after(int i) const {
+        if (!any_nan()) return false;
+        const unsigned long long e = i < 0 ? all() : all() & ~((2ull << i) - 1);
+        return e && (nans() >> (__ffsll((long long)e) - 1) & 1);
+    }
+};
 // Prefix sums of a block's log decays: for threads 0 .. NT - 1 (all of them
 // call), a[i + 1] = sum of the first i + 1, a[0] = 0, for i < len; entries up
-// to `upto` repeat the total. `scan` is NT / 32 long longs of shared memory.
-// Ends with a barrier.
+// to `upto` (64 at most) repeat the total. `scan` is NT / 32 long longs of shared
+// memory, and so is `events`. Ends with a barrier.
 template <int NT>
 __device__ __forceinline__ void decay_prefix(const float *log_decay, int kind, int64_t start, int H, int h, int len,
-                                             int upto, float2 *a, long long *scan) {
+                                             int upto, float2 *a, long long *scan, DecayEvents *events) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long base = 0;
     if (tid == 0) a[0] = make_float2(0.f, 0.f);
     for (int i0 = 0; i0 < upto; i0 += NT) {
         const int i = i0 + tid;
-        long long x = 0;
-        if (i < len && kind != KDA_DECAY_NONE)
-            x = decay_fixed(kind == KDA_DECAY_HEAD ? log_decay[h] : log_decay[(start + i) * H + h]);
+        float g = 0.f;
+        if (i < len && kind != KDA_DECAY_NONE) g = kind == KDA_DECAY_HEAD ? log_decay[h] : log_decay[(start + i) * H + h];
+        long long x = decay_fixed(g);
+        if (warp < 2) {
+            const uint32_t n = __ballot_sync(0xffffffffu, g != g), r = __ballot_sync(0xffffffffu, g <= kMinLogDecay);
+            if (lane == 0) events->nan[warp] = n, events->reset[warp] = r;
+        }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, x, off);

@@ -8,6 +8,7 @@
 // CTA's abort flag, every role leaves its loop, and the CTA ends normally.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <math_constants.h>
 
 #include "kda_linear.cuh"
 #include "kda_linear_tc.cuh"
@@ -157,11 +158,49 @@ template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t 
         "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
+// NaN log decays among a warp's tokens (laid out as in warp_decay): which of the
+// decays are NaN, by the rule at kMinLogDecay.
+struct WarpNan {
+    uint32_t before;    // bit u: the decay over the tokens up to this lane's u-th, that one included
+    uint32_t after;     // bit u: over those behind it
+    bool event;         // there is a NaN or a reset
+    bool first, last;   // the first of them, the last of them is a NaN: the decay over all, in reverse and forward
+};
+template <int PER> __device__ __forceinline__ WarpNan warp_nan(const float (&g)[PER]) {
+    WarpNan r{0u, 0u, false, false, false};
+    uint32_t nan = 0, events = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        nan |= (g[u] != g[u] ? 1u : 0u) << u;
+        events |= (!(g[u] > kMinLogDecay) ? 1u : 0u) << u;
+    }
+    const uint32_t lanes = __ballot_sync(0xffffffffu, events != 0u);
+    r.event = lanes != 0u;
+    if (!__any_sync(0xffffffffu, nan != 0u)) return r;
+    const uint32_t ends = __ballot_sync(0xffffffffu, events && (nan >> (31 - __clz(events)) & 1)),
+                   starts = __ballot_sync(0xffffffffu, events && (nan >> (__ffs(events) - 1) & 1)),
+                   lane = threadIdx.x & 31, earlier = lanes & ((1u << lane) - 1), later = lanes & ~((2u << lane) - 1);
+    r.first = starts >> (__ffs(lanes) - 1) & 1;
+    r.last = ends >> (31 - __clz(lanes)) & 1;
+    uint32_t on = earlier ? ends >> (31 - __clz(earlier)) & 1 : 0u;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        if (events >> u & 1) on = nan >> u & 1;
+        r.before |= on << u;
+    }
+    on = later ? starts >> (__ffs(later) - 1) & 1 : 0u;
+#pragma unroll
+    for (int u = PER - 1; u >= 0; --u) {
+        r.after |= on << u;
+        if (events >> u & 1) on = nan >> u & 1;
+    }
+    return r;
+}
 // A warp's prefix sums of a block's log decays (fixed point): lane l holds
 // tokens l * per .. l * per + per - 1; `mine` receives its inclusive sums.
 template <int PER>
 __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float *log_decay, int decay,
-                                                const LinBlock &blk, int h, long long (&mine)[PER]) {
+                                                const LinBlock &blk, int h, long long (&mine)[PER], WarpNan &nan) {
     const int lane = threadIdx.x & 31;
     float g[PER];  // all loads first: one after the other they cost a memory latency each
     const float head = decay == KDA_DECAY_HEAD ? __ldg(log_decay + h) : 0.f;
@@ -172,6 +211,7 @@ __device__ __forceinline__ long long warp_decay(const LinGeom &geo, const float 
         g[u] = i < blk.len ? head : 0.f;
         if (token && i < blk.len) g[u] = __ldg(log_decay + (int64_t)(blk.start + i) * geo.H + h);
     }
+    nan = warp_nan<PER>(g);
     long long run = 0;
 #pragma unroll
     for (int u = 0; u < PER; ++u) mine[u] = run += decay_fixed(g[u]);
@@ -230,7 +270,7 @@ struct StateTcArgs {
     LinGeom geo;
     const float *log_decay;
     int decay;
-    float *out, *total;
+    float *out, *total, *total_rev;
     int items;
 };
 
@@ -332,11 +372,18 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             const int b = geo.by_heads.div(it), h = it - b * geo.H;
             const LinBlock blk = lin_block(geo, b);
             long long sum = 0;  // over the block's earlier parts
+            WarpNan seen{};
             for (int p0 = 0; p0 < blk.len; p0 += kLinMaxBlock, ++q) {
                 constexpr int PER = kLinMaxBlock / 32;
                 long long a[PER];
                 const LinBlock part{blk.seq, blk.start + p0, min(kLinMaxBlock, blk.len - p0)};
-                const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, part, h, a);
+                WarpNan nan;
+                const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, part, h, a, nan);
+                if (nan.event) {
+                    seen.first = seen.event ? seen.first : nan.first;
+                    seen.last = nan.last;
+                    seen.event = true;
+                }
                 ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_EMPTY + (q & 1), ((q >> 1) & 1) ^ 1));
                 if (!ok) break;
                 float *w = wts + (q & 1) * kLinMaxBlock;
@@ -349,8 +396,12 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                 warp_arrive(bar + SB_W_FULL + (q & 1));
                 sum += all;
             }
-            if (!REV && lane == 0 && p.total && blk.len > 0)
-                p.total[(int64_t)b * geo.H + h] = decay_ratio(decay_pair(sum), make_float2(0.f, 0.f));
+            if (!REV && lane == 0 && blk.len > 0) {
+                const int64_t at = (int64_t)b * geo.H + h;
+                const float total = decay_ratio(decay_pair(sum), make_float2(0.f, 0.f));
+                if (p.total) p.total[at] = seen.last ? CUDART_NAN_F : total;
+                if (p.total_rev) p.total_rev[at] = seen.first ? CUDART_NAN_F : total;
+            }
         }
     } else if (warp >= 4 && warp < 8) {
         int q = 0;
@@ -572,7 +623,8 @@ constexpr int AT_PREFIX = 4;                                         // blocks w
 constexpr int AT_A = AttendRings<true>::FLOW_AT + AttendRings<true>::FLOW * AttendRings<true>::FLOW_SLOT;
 static_assert(AT_A >= AttendRings<false>::FLOW_AT + AttendRings<false>::FLOW * AttendRings<false>::FLOW_SLOT, "rings");
 constexpr int AT_COL = AT_A + AT_PREFIX * (kLinMaxBlock + 2) * 8;    // AT_A: prefix sums; column factors [16 warps][128]
-constexpr int AT_BAR = AT_COL + 16 * kLinMaxBlock / 2 * 4;
+constexpr int AT_NAN = AT_COL + 16 * kLinMaxBlock / 2 * 4;           // whether the state's decay is NaN, a bit a token
+constexpr int AT_BAR = AT_NAN + AT_PREFIX * kLinMaxBlock / 8;
 enum { AB_ROW_FULL = 0, AB_ROW_EMPTY = 4, AB_FLOW_FULL = 8, AB_FLOW_EMPTY = 13, AB_O_IN = 18, AB_O_FULL = 20,
        AB_O_EMPTY = 22, AB_P_FULL = 24, AB_P_READY = 26, AB_A_FULL = 28, AB_A_EMPTY = 32, AB_COUNT = 36 };
 constexpr int AT_SMEM = AT_BAR + AB_COUNT * 8 + 16 + 1024;
@@ -807,7 +859,9 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             if (x.tiles == 0) continue;
             constexpr int PER = kLinMaxBlock / 32;
             long long s[PER];
-            warp_decay<PER>(geo, p.log_decay, p.decay, x.blk, x.h, s);
+            WarpNan nan;
+            warp_decay<PER>(geo, p.log_decay, p.decay, x.blk, x.h, s, nan);
+            static_assert(PER == 8, "a lane's bits make a byte");
             const int slot = k % AT_PREFIX;
             ok = __all_sync(0xffffffffu, ab.wait(bar + AB_A_EMPTY + slot, ((k / AT_PREFIX) & 1) ^ 1));
             if (!ok) break;
@@ -815,6 +869,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             if (lane == 0) a[0] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < PER; ++u) a[lane * PER + u + 1] = decay_pair(s[u]);
+            sm[AT_NAN + slot * (kLinMaxBlock / 8) + lane] = (unsigned char)(REV ? nan.after : nan.before);
             warp_arrive(bar + AB_A_FULL + slot);
             ++k;
             if (lane == 0)
@@ -849,7 +904,8 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             const float2 *a = reinterpret_cast<const float2 *>(sm + AT_A) + slot * (kLinMaxBlock + 2);
             const int i0 = 128 * x.tile(near ? 0 : 1), i = i0 + r, len = x.blk.len;
             const float2 ai = a[min(i, len - 1) + 1];
-            const float f = p.c_state * (REV ? decay_ratio(a[len], ai) : decay_ratio(ai, make_float2(0.f, 0.f)));
+            float f = p.c_state * (REV ? decay_ratio(a[len], ai) : decay_ratio(ai, make_float2(0.f, 0.f)));
+            if (sm[AT_NAN + slot * (kLinMaxBlock / 8) + (i >> 3)] >> (i & 7) & 1) f = CUDART_NAN_F;
             // D_ij = row factor x column factor for the columns on the far side of the warp's 32 rows, the
             // decays to and from their edge (both <= 1); only the 32 x 32 piece on the diagonal takes an
             // exponential per element
@@ -1246,7 +1302,8 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             const int t0 = first_token(x);
             const LinBlock part{x.blk.seq, x.blk.start + t0, min(128, x.blk.len - t0)};
             long long sums[4];
-            const long long all = warp_decay<4>(geo, p.log_decay, p.decay, part, x.h, sums);
+            WarpNan nan;
+            const long long all = warp_decay<4>(geo, p.log_decay, p.decay, part, x.h, sums, nan);
             ok = __all_sync(0xffffffffu, ab.wait(bar + RB_AE + g % RL_SLOTS, ((g / RL_SLOTS) & 1) ^ 1));
             if (!ok) break;
             RollTable *t = table(g);
@@ -1259,7 +1316,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             };
             if (lane == 0) {
                 t->a[0] = zero;
-                t->total = decay_ratio(end, zero);
+                t->total = (REV ? nan.first : nan.last) ? CUDART_NAN_F : decay_ratio(end, zero);
                 t->mild = -(end.x + end.y) < kMild ? 1.f : 0.f;
             }
             float v[4];
@@ -1275,7 +1332,10 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             *reinterpret_cast<uint4 *>(t->weight + 4 * lane) = make_uint4(wt[0], wt[1], wt[2], wt[3]);
             *reinterpret_cast<uint4 *>(t->weight + 4 * lane + 2) = make_uint4(wt[4], wt[5], wt[6], wt[7]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = p.c_state * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
+            for (int u = 0; u < 4; ++u) {
+                v[u] = p.c_state * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
+                if ((REV ? nan.after : nan.before) >> u & 1) v[u] = CUDART_NAN_F;  // such a chunk is never mild
+            }
             four(t->row + 4 * lane, v[0], v[1], v[2], v[3]);
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[u] = p.c_ratio * (REV ? decay_ratio(a[u], end) : decay_ratio(zero, a[u]));
@@ -1575,10 +1635,10 @@ int sm_count() {
 
 cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
                             int64_t tokens, const float *log_decay, int decay, float *out, float *total,
-                            Launches &l) {
+                            float *total_rev, Launches &l) {
     CUtensorMap mx, my;
     if (!token_map(&mx, x, xs, geo.H, tokens) || !token_map(&my, y, ys, geo.H, tokens)) return cudaErrorInvalidValue;
-    StateTcArgs p{geo, log_decay, decay, out, total, geo.nblocks * geo.H};
+    StateTcArgs p{geo, log_decay, decay, out, total, total_rev, geo.nblocks * geo.H};
     auto k = rev ? lin_state_tc_kernel<true> : lin_state_tc_kernel<false>;
     static std::atomic<uint64_t> allowed[2];
     KDA_TRY(allow_smem(k, ST_SMEM, allowed[rev]));

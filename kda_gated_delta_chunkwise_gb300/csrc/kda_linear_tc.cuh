@@ -7,11 +7,12 @@ namespace kda {
 
 constexpr int kLinMaxBlock = 256;  // tokens per block at most (two 128-row tiles, see lin_attend_tc_kernel)
 
-// Every block's own state: out [block][head][128][128] fp32, total
-// [block][head] = e^{L_end} (forward only).
+// Every block's own state: out [block][head][128][128] fp32; total and total_rev
+// [block][head] = e^{L_end} as the forward and the reverse scan pass over it
+// (forward only, nullable).
 cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
                             int64_t tokens, const float *log_decay, int decay, float *out, float *total,
-                            Launches &l);
+                            float *total_rev, Launches &l);
 // The scan over the blocks: own states -> three bf16 arrays, part_stride
 // elements apart, of the states before (reverse: the gradients after) each
 // block; the last state to sT. Reverse: also <S, G> of every block, S in `other`.
