@@ -54,7 +54,7 @@ constexpr int CH = kLinChunk;
 //   16 sequences of 20011 tokens in all x 16: 512 172, by this rule 171-175.
 constexpr int kLeastSegment = 512;
 __host__ __device__ constexpr int segment_tokens(int64_t len, int H) {
-    int n = len <= 2048 ? kLeastSegment : len <= 16384 ? 1024 : len <= 65536 ? 2048 : 4096;
+    int n = len <= 2048 ? kLeastSegment : len <= 16384 ? 1024 : len <= 65536 ? 2048 : kLongestSegment;
     while (n > kLeastSegment && (int64_t)n * 64 > len * H) n /= 2;
     return n;
 }

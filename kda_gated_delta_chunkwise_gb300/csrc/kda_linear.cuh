@@ -174,13 +174,17 @@ __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &fir
 // pair of floats, its whole part and its fraction in [0, 1). (All conversions
 // are 32-bit ones: in fp64 this pair took 8 us of a warp's time for 256 tokens.)
 // A decay of e^-128 already leaves nothing of an fp32 state (2^-185 of its
-// largest value), so every log decay is clamped there, -inf (a reset) included,
-// and sums of up to 2^23 tokens keep an exact whole part.
+// largest value), so every log decay is clamped there, -inf (a reset) included.
+// That is 184.7 octaves a token, so the whole part of a sum is exact in a
+// float's 24 bits over 90,000 tokens at most; kLongestSegment is the longest
+// stretch that is ever summed.
 // A NaN is clamped too, so that sums and ratios stay numbers; it is carried on
 // beside them (nan_before, nan_after): the decay of a stretch is NaN where the
 // stretch's NaN nearest to the token it leads to has no reset in between, as in
 // the recurrence, where the state is NaN from a NaN decay to the next reset.
 constexpr float kMinLogDecay = -128.f;
+constexpr int kLongestSegment = 4096;
+static_assert(kLongestSegment <= (1 << 24) / 185, "whole parts of sums are exact as floats");
 __device__ __forceinline__ long long decay_fixed(float g) {
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
     const float x = fminf(fmaxf(g, kMinLogDecay), -kMinLogDecay);
