@@ -268,7 +268,7 @@ template <typename T> struct StateArgs {
     int64_t x_stride, y_stride;
     const float *log_decay;
     int decay;
-    float *out, *total, *total_rev;  // e^{L_end} as the forward scan and as the reverse one passes over it, nullable
+    float *out, *total, *total_rev;  // the block's decay_total as the forward and as the reverse scan use it, nullable
 };
 template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void block_state(const StateArgs<T> &p) {
     constexpr bool F32 = sizeof(T) == 4;
@@ -287,11 +287,12 @@ template <typename T, int DK, int DV, bool REV> __device__ __forceinline__ void 
     if (blk.len <= 0) return;
     load_tile<T, DK>(xs, LDX, p.x + blk.start * p.x_stride + h * DK, p.x_stride, blk.len);
     load_tile<T, DV>(ys, LDY, p.y + blk.start * p.y_stride + h * DV, p.y_stride, blk.len);
-    decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan, &events);
+    const long long sum =
+        decay_prefix<NT>(p.log_decay, p.decay, blk.start, geo.H, h, blk.len, blk.len, a, scan, &events);
     const float2 end = a[blk.len];
     if (threadIdx.x == 0) {
         const int64_t at = (int64_t)b * geo.H + h;
-        const float total = decay_ratio(end, make_float2(0.f, 0.f));
+        const float total = decay_total(sum);
         if (p.total) p.total[at] = events.nan_before(blk.len - 1) ? CUDART_NAN_F : total;
         if (p.total_rev) p.total_rev[at] = events.nan_after(-1) ? CUDART_NAN_F : total;
     }
@@ -338,7 +339,7 @@ struct ScanArgs {
     const float *s0;  // nullable
     float *sT;        // nullable
     float c;
-    const float *total;  // the decay over every block
+    const float *total;  // every block's decay_total
 };
 template <bool REV>
 __device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &q, int size4) {
@@ -351,7 +352,7 @@ __device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &
     const int64_t e = (int64_t)(blockIdx.x % per) * NT + threadIdx.x;
     int first, last;
     lin_seq_blocks<true>(geo, n, first, last);
-    float4 S = q.s0 ? reinterpret_cast<const float4 *>(q.s0)[nh * size4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    ScanElements S(q.s0 ? reinterpret_cast<const float4 *>(q.s0)[nh * size4 + e] : make_float4(0.f, 0.f, 0.f, 0.f));
     float4 *p = reinterpret_cast<float4 *>(q.states);
     const int count = last - first;
     constexpr int AHEAD = 4;
@@ -362,24 +363,31 @@ __device__ __forceinline__ void scan_blocks(const LinGeom &geo, const ScanArgs &
         return (int64_t)(geo.place ? geo.place[b] : b) * geo.H + h;
     };
     for (int i0 = 0; i0 < count; i0 += AHEAD) {
+        float4 *dst[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
             if (i0 + u < count) {
-                own[u] = p[at(i0 + u) * size4 + e];
+                dst[u] = p + at(i0 + u) * size4 + e;
+                own[u] = *dst[u];
                 f[u] = total[at(i0 + u)];
             }
+        if (S.finite(own, f, count - i0)) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i0 + u < count) {
-                p[at(i0 + u) * size4 + e] = S;
-                if (f[u] == 0.f) S = make_float4(0.f, 0.f, 0.f, 0.f);  // a reset, whatever the state held
-                S.x = f[u] * S.x + c * own[u].x;
-                S.y = f[u] * S.y + c * own[u].y;
-                S.z = f[u] * S.z + c * own[u].z;
-                S.w = f[u] * S.w + c * own[u].w;
-            }
+            for (int u = 0; u < AHEAD; ++u)
+                if (i0 + u < count) {
+                    *dst[u] = S.value();
+                    S.step(f[u], c, own[u]);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i0 + u < count) {
+                    *dst[u] = S.value();
+                    S.step_any(f[u], c, own[u]);
+                }
+        }
     }
-    if (q.sT) reinterpret_cast<float4 *>(q.sT)[nh * size4 + e] = S;
+    if (q.sT) reinterpret_cast<float4 *>(q.sT)[nh * size4 + e] = S.value();
 }
 
 // The backward's two directions do not depend on each other: one launch (blockIdx.y).
@@ -621,7 +629,7 @@ lin_decay_grad_kernel(LinGeom geo, const float *log_decay, int decay, const floa
             x += s.x * g.x + s.y * g.y + s.z * g.z + s.w * g.w;
         }
     }
-    x = total[bh] == 0.f ? 0.f : x * total[bh];  // a reset, whatever the state held
+    x = decay_times(total[bh], x);
     for (int i = tid; i < blk.len; i += NT) {
         const int64_t at = (int64_t)(blk.start + i) * geo.H + h;
         x += kdk_state[at] + (dot_stride ? kdk_state[at + dot_stride] : 0.f);

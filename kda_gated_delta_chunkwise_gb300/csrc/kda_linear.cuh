@@ -169,10 +169,13 @@ __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &fir
 }
 
 // Log decays. A sum over a block is taken in fixed point (base 2, steps of
-// 2^-31, exact in 64 bits), so that the difference of two sums has no
+// 2^-40, exact in 64 bits), so that the difference of two sums has no
 // cancellation error however far down the block it lies; it is handed on as a
-// pair of floats, its whole part and its fraction in [0, 1). (All conversions
-// are 32-bit ones: in fp64 this pair took 8 us of a warp's time for 256 tokens.)
+// pair of floats, the nearest whole number and the rest. (All conversions are
+// 32-bit ones: in fp64 this pair took 8 us of a warp's time for 256 tokens.) A
+// token's rounding comes out the same for every token where the decay is
+// constant: with steps of 2^-31 the initial state was 1.9e-5 off after 131,072
+// tokens of g = -3e-6.
 // A decay of e^-128 already leaves nothing of an fp32 state (2^-185 of its
 // largest value), so every log decay is clamped there, -inf (a reset) included.
 // That is 184.7 octaves a token, so the whole part of a sum is exact in a
@@ -183,17 +186,26 @@ __device__ __forceinline__ void lin_seq_blocks(const LinGeom &g, int n, int &fir
 // stretch's NaN nearest to the token it leads to has no reset in between, as in
 // the recurrence, where the state is NaN from a NaN decay to the next reset.
 constexpr float kMinLogDecay = -128.f;
+constexpr int kDecayBits = 40;
 constexpr int kLongestSegment = 4096;
 static_assert(kLongestSegment <= (1 << 24) / 185, "whole parts of sums are exact as floats");
+static_assert(kLongestSegment <= (1ll << (62 - kDecayBits)) / 185, "sums fit in 64 bits");
 __device__ __forceinline__ long long decay_fixed(float g) {
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
     const float x = fminf(fmaxf(g, kMinLogDecay), -kMinLogDecay);
     const float hi = x * kLog2e, lo = fmaf(x, kLog2e, -hi) + x * kLog2eLow, whole = truncf(hi);
-    return (long long)(int)whole * (1ll << 31) + __float2int_rn((hi - whole) * 2147483648.f) +
-           __float2int_rn(lo * 2147483648.f);
+    // hi's fraction in steps of 2^-31, then what is left of it and lo
+    const float part = (hi - whole) * 2147483648.f;
+    const int p = __float2int_rn(part);
+    return (long long)(int)whole * (1ll << kDecayBits) + (long long)p * (1ll << (kDecayBits - 31)) +
+           __float2int_rn((part - (float)p) * 512.f + lo * 1099511627776.f);
 }
+static_assert(kDecayBits == 40, "the constants of decay_fixed and decay_pair");
 __device__ __forceinline__ float2 decay_pair(long long fixed) {
-    return make_float2((float)(int)(fixed >> 31), (float)(int)(fixed & 0x7fffffff) * (1.f / 2147483648.f));
+    const unsigned long long q = (unsigned long long)fixed + (1ull << (kDecayBits - 1));
+    const uint32_t lo = (uint32_t)q, hi = (uint32_t)(q >> 32);
+    const int whole = (int)hi >> 8, rest = (int)(__funnelshift_r(lo, hi, 8) ^ 0x80000000u);  // 2^-32 steps from the half up
+    return make_float2((float)whole, (float)rest * (1.f / 4294967296.f));
 }
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -225,12 +237,69 @@ struct DecayEvents {
         return e && (nans() >> (__ffsll((long long)e) - 1) & 1);
     }
 };
+// The decay f over a whole block, for the scan. A slow decay is a number close to
+// one, the same for every block where it is constant, and its rounding then adds
+// up with the blocks: so f - 1 stands for an f above 2^-1/2 (negative, or -0), and
+// f itself (0 or positive) for the others.
+__device__ __forceinline__ float decay_total(long long fixed) {
+    if (fixed > 0 || fixed < -(1ll << (kDecayBits - 1))) return decay_ratio(decay_pair(fixed), make_float2(0.f, 0.f));
+    return fixed ? expm1f((float)fixed * (0.693147181f / 1099511627776.f)) : -0.f;
+}
+__device__ __forceinline__ float decay_times(float total, float s) {  // f s; a reset leaves nothing, whatever s held
+    const int bits = __float_as_int(total);
+    return bits == 0 ? 0.f : bits > 0 ? total * s : fmaf(total, s, s);
+}
+// Four elements of the scan, S <- f S + c own. The rounding of S itself adds up
+// with the blocks too: what a slow decay takes off is the same few units of S's
+// last place from block to block, and so is what rounds away of it (2048 blocks
+// of 64 tokens at g = -3e-8: 5e-5 of S). So under a slow decay what a sum rounds
+// off is put into the next one (Kahan 1965). f is the same for a whole CTA.
+struct ScanElements {
+    float s[4], e[4];
+    __device__ __forceinline__ explicit ScanElements(float4 x) {
+        s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
+        e[0] = e[1] = e[2] = e[3] = 0.f;
+    }
+    __device__ __forceinline__ float4 value() const { return make_float4(s[0], s[1], s[2], s[3]); }
+    // Whether the state, the next COUNT blocks' own states and their totals are all numbers.
+    template <int COUNT>
+    __device__ __forceinline__ bool finite(const float4 (&own)[COUNT], const float (&total)[COUNT], int count) const {
+        float z = 0.f;  // 0 times anything else is NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z = fmaf(0.f, s[i], z);
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u)
+            if (u < count)
+                z = fmaf(0.f, own[u].x, fmaf(0.f, own[u].y, fmaf(0.f, own[u].z, fmaf(0.f, own[u].w, fmaf(0.f, total[u], z)))));
+        return z == 0.f;
+    }
+    // a slow decay: s + y with y = (f - 1) s + e + c own; another: y = f (s + e) + c own alone
+    __device__ __forceinline__ void step(float total, float c, float4 own) {
+        const bool slow = __float_as_int(total) < 0;
+        const float x[4] = {own.x, own.y, own.z, own.w}, keep = slow ? 1.f : 0.f, ef = slow ? 1.f : total;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float y = fmaf(c, x[i], fmaf(total, s[i], e[i] * ef)), t = fmaf(s[i], keep, y);
+            e[i] = __fsub_rn(y, fmaf(-keep, s[i], t));
+            s[i] = t;
+        }
+    }
+    // with infinities or NaN: a reset leaves nothing of them, another decay leaves them as they are
+    __device__ __forceinline__ void step_any(float total, float c, float4 own) {
+        const float f = __float_as_int(total) < 0 ? 1.f + total : total, x[4] = {own.x, own.y, own.z, own.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = fmaf(c, x[i], f == 0.f ? 0.f : f * s[i]);
+            e[i] = 0.f;
+        }
+    }
+};
 // Prefix sums of a block's log decays: for threads 0 .. NT - 1 (all of them
 // call), a[i + 1] = sum of the first i + 1, a[0] = 0, for i < len; entries up
 // to `upto` (64 at most) repeat the total. `scan` is NT / 32 long longs of shared
-// memory, and so is `events`. Ends with a barrier.
+// memory; `events` lies there too. Returns the total. Ends with a barrier.
 template <int NT>
-__device__ __forceinline__ void decay_prefix(const float *log_decay, int kind, int64_t start, int H, int h, int len,
+__device__ __forceinline__ long long decay_prefix(const float *log_decay, int kind, int64_t start, int H, int h, int len,
                                              int upto, float2 *a, long long *scan, DecayEvents *events) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long base = 0;
@@ -261,6 +330,7 @@ __device__ __forceinline__ void decay_prefix(const float *log_decay, int kind, i
         base = all;
         __syncthreads();
     }
+    return base;
 }
 
 struct LinArgs {

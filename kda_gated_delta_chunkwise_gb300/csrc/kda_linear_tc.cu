@@ -161,39 +161,46 @@ template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t 
 // NaN log decays among a warp's tokens (laid out as in warp_decay): which of the
 // decays are NaN, by the rule at kMinLogDecay.
 struct WarpNan {
-    uint32_t before;    // bit u: the decay over the tokens up to this lane's u-th, that one included
-    uint32_t after;     // bit u: over those behind it
-    bool event;         // there is a NaN or a reset
-    bool first, last;   // the first of them, the last of them is a NaN: the decay over all, in reverse and forward
+    uint32_t bits;  // below; 0 where there is no NaN
+    bool event;     // there is a NaN or a reset
+    // bit u: the decay over the tokens up to this lane's u-th, that one included; over those behind it
+    __device__ __forceinline__ uint32_t before() const { return bits & 0xff; }
+    __device__ __forceinline__ uint32_t after() const { return bits >> 8 & 0xff; }
+    // the first of them, the last of them is a NaN: the decay over all, in reverse and forward
+    __device__ __forceinline__ bool first() const { return bits >> 16 & 1; }
+    __device__ __forceinline__ bool last() const { return bits >> 17 & 1; }
 };
+// Out of line: the kernels' loops are short for the instruction cache.
+__device__ __noinline__ uint32_t warp_nan_bits(uint32_t nan, uint32_t events) {
+    const uint32_t lanes = __ballot_sync(0xffffffffu, events != 0u),
+                   ends = __ballot_sync(0xffffffffu, events && (nan >> (31 - __clz(events)) & 1)),
+                   starts = __ballot_sync(0xffffffffu, events && (nan >> (__ffs(events) - 1) & 1)),
+                   lane = threadIdx.x & 31, earlier = lanes & ((1u << lane) - 1), later = lanes & ~((2u << lane) - 1);
+    uint32_t r = (starts >> (__ffs(lanes) - 1) & 1) << 16 | (ends >> (31 - __clz(lanes)) & 1) << 17;
+    uint32_t on = earlier ? ends >> (31 - __clz(earlier)) & 1 : 0u;
+#pragma unroll 1
+    for (int u = 0; u < 8; ++u) {
+        if (events >> u & 1) on = nan >> u & 1;
+        r |= on << u;
+    }
+    on = later ? starts >> (__ffs(later) - 1) & 1 : 0u;
+#pragma unroll 1
+    for (int u = 7; u >= 0; --u) {
+        r |= on << (8 + u);
+        if (events >> u & 1) on = nan >> u & 1;
+    }
+    return r;
+}
 template <int PER> __device__ __forceinline__ WarpNan warp_nan(const float (&g)[PER]) {
-    WarpNan r{0u, 0u, false, false, false};
+    static_assert(PER <= 8, "bits of a lane");
     uint32_t nan = 0, events = 0;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
         nan |= (g[u] != g[u] ? 1u : 0u) << u;
         events |= (!(g[u] > kMinLogDecay) ? 1u : 0u) << u;
     }
-    const uint32_t lanes = __ballot_sync(0xffffffffu, events != 0u);
-    r.event = lanes != 0u;
-    if (!__any_sync(0xffffffffu, nan != 0u)) return r;
-    const uint32_t ends = __ballot_sync(0xffffffffu, events && (nan >> (31 - __clz(events)) & 1)),
-                   starts = __ballot_sync(0xffffffffu, events && (nan >> (__ffs(events) - 1) & 1)),
-                   lane = threadIdx.x & 31, earlier = lanes & ((1u << lane) - 1), later = lanes & ~((2u << lane) - 1);
-    r.first = starts >> (__ffs(lanes) - 1) & 1;
-    r.last = ends >> (31 - __clz(lanes)) & 1;
-    uint32_t on = earlier ? ends >> (31 - __clz(earlier)) & 1 : 0u;
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        if (events >> u & 1) on = nan >> u & 1;
-        r.before |= on << u;
-    }
-    on = later ? starts >> (__ffs(later) - 1) & 1 : 0u;
-#pragma unroll
-    for (int u = PER - 1; u >= 0; --u) {
-        r.after |= on << u;
-        if (events >> u & 1) on = nan >> u & 1;
-    }
+    WarpNan r{0u, __any_sync(0xffffffffu, events != 0u) != 0};
+    if (r.event && __any_sync(0xffffffffu, nan != 0u)) r.bits = warp_nan_bits(nan, events);
     return r;
 }
 // A warp's prefix sums of a block's log decays (fixed point): lane l holds
@@ -372,7 +379,7 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             const int b = geo.by_heads.div(it), h = it - b * geo.H;
             const LinBlock blk = lin_block(geo, b);
             long long sum = 0;  // over the block's earlier parts
-            WarpNan seen{};
+            bool event = false, first = false, last = false;  // as in WarpNan, over the block
             for (int p0 = 0; p0 < blk.len; p0 += kLinMaxBlock, ++q) {
                 constexpr int PER = kLinMaxBlock / 32;
                 long long a[PER];
@@ -380,9 +387,9 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
                 WarpNan nan;
                 const long long all = warp_decay<PER>(geo, p.log_decay, p.decay, part, h, a, nan);
                 if (nan.event) {
-                    seen.first = seen.event ? seen.first : nan.first;
-                    seen.last = nan.last;
-                    seen.event = true;
+                    first = event ? first : nan.first();
+                    last = nan.last();
+                    event = true;
                 }
                 ok = __all_sync(0xffffffffu, ab.wait(bar + SB_W_EMPTY + (q & 1), ((q >> 1) & 1) ^ 1));
                 if (!ok) break;
@@ -398,9 +405,9 @@ lin_state_tc_kernel(StateTcArgs p, const __grid_constant__ CUtensorMap mx, const
             }
             if (!REV && lane == 0 && blk.len > 0) {
                 const int64_t at = (int64_t)b * geo.H + h;
-                const float total = decay_ratio(decay_pair(sum), make_float2(0.f, 0.f));
-                if (p.total) p.total[at] = seen.last ? CUDART_NAN_F : total;
-                if (p.total_rev) p.total_rev[at] = seen.first ? CUDART_NAN_F : total;
+                const float total = decay_total(sum);
+                if (p.total) p.total[at] = last ? CUDART_NAN_F : total;
+                if (p.total_rev) p.total_rev[at] = first ? CUDART_NAN_F : total;
             }
         }
     } else if (warp >= 4 && warp < 8) {
@@ -522,11 +529,11 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
     const int64_t e = (int64_t)(blockIdx.x % PER) * SC_THREADS + threadIdx.x;
     int first, last;
     lin_seq_blocks(geo, n, first, last);
-    float4 S = s0 ? reinterpret_cast<const float4 *>(s0)[nh * SIZE4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    ScanElements state(s0 ? reinterpret_cast<const float4 *>(s0)[nh * SIZE4 + e] : make_float4(0.f, 0.f, 0.f, 0.f));
     const float4 *p = reinterpret_cast<const float4 *>(own);
     const int count = last - first;
     constexpr bool INNER = REV;  // <S, G> of every block: G is here, S in `other`
-    constexpr int AHEAD = INNER ? 4 : 8;
+    constexpr int AHEAD = 4;
     float4 x[AHEAD];
     float f[AHEAD];
     uint2 so[AHEAD][3];
@@ -543,9 +550,11 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
                     for (int k = 0; k < 3; ++k) so[u][k] = __ldg(o + k * (part_stride / 4));
                 }
             }
+        const bool finite = state.finite(x, f, count - i0);
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
             if (i0 + u < count) {
+                const float4 S = state.value();
                 if (INNER) {
                     float v = S.x * (lo_f(so[u][0].x) + lo_f(so[u][1].x) + lo_f(so[u][2].x)) +
                               S.y * (hi_f(so[u][0].x) + hi_f(so[u][1].x) + hi_f(so[u][2].x)) +
@@ -563,14 +572,11 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
                 *o = a;
                 o[part_stride / 4] = b;
                 o[part_stride / 2] = d;
-                if (f[u] == 0.f) S = make_float4(0.f, 0.f, 0.f, 0.f);  // a reset, whatever the state held
-                S.x = f[u] * S.x + c * x[u].x;
-                S.y = f[u] * S.y + c * x[u].y;
-                S.z = f[u] * S.z + c * x[u].z;
-                S.w = f[u] * S.w + c * x[u].w;
+                if (finite) state.step(f[u], c, x[u]);
+                else state.step_any(f[u], c, x[u]);
             }
     }
-    if (sT) reinterpret_cast<float4 *>(sT)[nh * SIZE4 + e] = S;
+    if (sT) reinterpret_cast<float4 *>(sT)[nh * SIZE4 + e] = state.value();
 }
 
 // ================================================================ outputs
@@ -869,7 +875,7 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
             if (lane == 0) a[0] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < PER; ++u) a[lane * PER + u + 1] = decay_pair(s[u]);
-            sm[AT_NAN + slot * (kLinMaxBlock / 8) + lane] = (unsigned char)(REV ? nan.after : nan.before);
+            sm[AT_NAN + slot * (kLinMaxBlock / 8) + lane] = (unsigned char)(REV ? nan.after() : nan.before());
             warp_arrive(bar + AB_A_FULL + slot);
             ++k;
             if (lane == 0)
@@ -1316,7 +1322,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
             };
             if (lane == 0) {
                 t->a[0] = zero;
-                t->total = (REV ? nan.first : nan.last) ? CUDART_NAN_F : decay_ratio(end, zero);
+                t->total = (REV ? nan.first() : nan.last()) ? CUDART_NAN_F : decay_ratio(end, zero);
                 t->mild = -(end.x + end.y) < kMild ? 1.f : 0.f;
             }
             float v[4];
@@ -1334,7 +1340,7 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 v[u] = p.c_state * (REV ? decay_ratio(end, a[u]) : decay_ratio(a[u], zero));
-                if ((REV ? nan.after : nan.before) >> u & 1) v[u] = CUDART_NAN_F;  // such a chunk is never mild
+                if ((REV ? nan.after() : nan.before()) >> u & 1) v[u] = CUDART_NAN_F;  // such a chunk is never mild
             }
             four(t->row + 4 * lane, v[0], v[1], v[2], v[3]);
 #pragma unroll

@@ -8,7 +8,7 @@ namespace kda {
 constexpr int kLinMaxBlock = 256;  // tokens per block at most (two 128-row tiles, see lin_attend_tc_kernel)
 
 // Every block's own state: out [block][head][128][128] fp32; total and total_rev
-// [block][head] = e^{L_end} as the forward and the reverse scan pass over it
+// [block][head]: its decay_total as the forward and as the reverse scan use it
 // (forward only, nullable).
 cudaError_t launch_state_tc(const LinGeom &geo, bool rev, const void *x, int64_t xs, const void *y, int64_t ys,
                             int64_t tokens, const float *log_decay, int decay, float *out, float *total,
