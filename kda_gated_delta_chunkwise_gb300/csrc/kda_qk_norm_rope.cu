@@ -6,7 +6,7 @@
 // with R turning channel pairs of the first `rot` channels by the angles whose
 // cosines and sines the token's table row holds. Backward, for u = R^T dy:
 //   dw = sum over rows of u n,   dn = w u,
-//   dx = r dn - x r^3 (x . dn) c,   c = 1 (L2), 1 / d (RMS), 0 (NONE).
+//   dx = r (dn - n (n . dn) c),   c = 1 (L2), 1 / d (RMS), 0 (NONE).
 //
 // Bound by memory: forward one read and one write of q and k, backward two
 // reads and one write; right behind it come the instructions, so the
@@ -342,24 +342,27 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
                 vx.load(reinterpret_cast<const T *>(buf + i * 512 + lane * 16));
                 vd.load(reinterpret_cast<const T *>(buf + (kPasses + i) * 512 + lane * 16));
                 const Vec<T> o = partner(vd, p.layout, g);
-                F2 d[N / 2], ss = f2(0.f, 0.f), xd = ss;
+                F2 d[N / 2], dn[N / 2], ss = f2(0.f, 0.f), xd = ss;
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {
                     d[e] = fma2(cs[e], vd.get(e), sn[e] * o.get(e));
+                    dn[e] = d[e] * wv[e];
                     const F2 xe = vx.get(e);
                     ss = fma2(xe, xe, ss);
-                    xd = fma2(xe, d[e] * wv[e], xd);
+                    xd = fma2(xe, dn[e], xd);
                 }
                 const float r = rnorm(row_sum<LANES>(f2_sum(ss)), p.norm, 1.f / D, p.eps);
-                const float c = p.norm == KDA_NORM_NONE ? 0.f
-                                                        : row_sum<LANES>(f2_sum(xd)) * (r * r * r) *
-                                                              (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
+                // n . dn c: r meets x before it meets itself, since r^3 has a third of fp32's range (a zero row
+                // under eps = 1e-30, a row of 1e13)
+                const float c = p.norm == KDA_NORM_NONE
+                                    ? 0.f
+                                    : row_sum<LANES>(f2_sum(xd)) * r * (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
                 const F2 r2 = f2(r, r), c2 = f2(-c, -c);
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {
-                    const F2 xe = vx.get(e), dr = d[e] * r2;
-                    acc[e] = fma2(xe, dr, acc[e]);
-                    vd.put(e, fma2(dr, wv[e], xe * c2));
+                    const F2 n = vx.get(e) * r2;
+                    acc[e] = fma2(n, d[e], acc[e]);
+                    vd.put(e, fma2(n, c2, dn[e]) * r2);
                 }
                 if (row < heads) vd.store(dx + (int64_t)row * D + g.c0);
             }
