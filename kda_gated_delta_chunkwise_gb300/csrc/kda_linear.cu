@@ -689,6 +689,8 @@ lin_head_sum_kernel(LinGeom geo, const float *block_sum, float *dg) {
     if (threadIdx.x == 0) dg[h] = red[0];
 }
 
+__global__ void lin_status_kernel(int32_t *status, int value) { *status = value; }
+
 // ---------------------------------------------------------------- host side
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1006,6 +1008,11 @@ cudaError_t launch_linear(const LinArgs &a, cudaStream_t s) {
 cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s) {
     if (use_tc(a.dt, a.dk, a.dv)) return a.d_decay ? backward_tc(a, s) : backward_rolled_tc(a, s);
     KDA_LINEAR_DISPATCH(backward);
+}
+
+cudaError_t launch_linear_status(int32_t *status, int value, cudaStream_t s) {
+    lin_status_kernel<<<1, 1, 0, s>>>(status, value);
+    return cudaGetLastError();
 }
 
 }  // namespace kda

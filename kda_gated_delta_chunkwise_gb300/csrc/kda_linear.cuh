@@ -358,6 +358,7 @@ size_t linear_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype
 size_t linear_backward_workspace_bytes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool packed);
 cudaError_t launch_linear(const LinArgs &a, cudaStream_t s);
 cudaError_t launch_linear_backward(const LinArgs &a, cudaStream_t s);
+cudaError_t launch_linear_status(int32_t *status, int value, cudaStream_t s);
 
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, kda_dtype_t dt, int64_t q_stride,
                                  int64_t k_stride, int64_t v_stride, const float *log_decay, int decay, float scale,

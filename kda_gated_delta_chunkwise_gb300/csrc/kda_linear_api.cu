@@ -85,13 +85,31 @@ kda_status_t workspace_ok(const void *ws, size_t have, size_t want) {
     return KDA_OK;
 }
 
+// A call on no sequences: of a packed batch with tokens all the same, the
+// offsets cannot be right; the sum of a head's gradients over no token is zero.
+kda_status_t nothing(const kda::LinArgs &a, bool packed, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (packed) {
+        KDA_CHECK(maybe(a.status, "device_status", 4));
+        if (a.status)
+            e = a.T > 0 ? kda::launch_linear_status(a.status, KDA_DEV_BAD_CU_SEQLENS, s)
+                        : cudaMemsetAsync(a.status, 0, sizeof(int32_t), s);
+        if (a.T > 0) return cuda_status(e, "status");
+    }
+    if (e == cudaSuccess && a.d_decay && a.decay == KDA_DECAY_HEAD) {
+        KDA_CHECK(need(a.d_decay, "dlog_decay", 4));
+        e = cudaMemsetAsync(a.d_decay, 0, sizeof(float) * a.H, s);
+    }
+    return cuda_status(e, "results of no sequences");
+}
+
 kda_status_t prefill(kda::LinArgs a, bool packed, size_t workspace_bytes, cudaStream_t s) {
     KDA_CHECK(common(a.dt, a.decay, a.N, a.T, a.H, a.dk, a.dv, a.scale));
     KDA_CHECK(sizes(a.N, a.T, a.H, packed));
     KDA_CHECK(stride(a.q_stride, a.H, a.dk, a.dt, "q_stride"));
     KDA_CHECK(stride(a.k_stride, a.H, a.dk, a.dt, "k_stride"));
     KDA_CHECK(stride(a.v_stride, a.H, a.dv, a.dt, "v_stride"));
-    if (a.N == 0) return ok();
+    if (a.N == 0) return nothing(a, packed, s);
     const int64_t tokens = packed ? a.T : (int64_t)a.N * a.T;
     if (packed) {
         KDA_CHECK(need(a.cu_seqlens, "cu_seqlens", 4));
@@ -118,7 +136,7 @@ kda_status_t backward(kda::LinArgs a, bool packed, size_t workspace_bytes, cudaS
     KDA_CHECK(stride(a.k_stride, a.H, a.dk, a.dt, "k_stride"));
     KDA_CHECK(stride(a.v_stride, a.H, a.dv, a.dt, "v_stride"));
     if (a.decay == KDA_DECAY_NONE) a.d_decay = nullptr;
-    if (a.N == 0) return ok();
+    if (a.N == 0) return nothing(a, packed, s);
     const int64_t tokens = packed ? a.T : (int64_t)a.N * a.T;
     if (packed) {
         KDA_CHECK(need(a.cu_seqlens, "cu_seqlens", 4));
@@ -150,7 +168,10 @@ kda_status_t decode(const void *q, const void *k, const void *v, kda_dtype_t dt,
     KDA_CHECK(stride(qs, H, dk, dt, "q_stride"));
     KDA_CHECK(stride(ks, H, dk, dt, "k_stride"));
     KDA_CHECK(stride(vs, H, dv, dt, "v_stride"));
-    if (N == 0) return ok();
+    if (N == 0) {
+        KDA_CHECK(maybe(status, "device_status", 4));
+        return cuda_status(status ? cudaMemsetAsync(status, 0, sizeof(int32_t), s) : cudaSuccess, "status reset");
+    }
     if ((int64_t)N * H * 4 > INT32_MAX) return fail(KDA_ERR_UNSUPPORTED, "N * H * 4 must fit in int32");
     KDA_CHECK(need(q, "q"));
     KDA_CHECK(need(k, "k"));
