@@ -63,13 +63,19 @@ kda_status_t common(kda_dtype_t dt, int decay, int N, int64_t T, int H, int dk, 
     return KDA_OK;
 }
 
+// a * b * c <= INT32_MAX, for factors >= 0 whose product may not fit in 64 bits
+bool fits(int64_t a, int64_t b, int64_t c = 1) {
+    if (a == 0 || b == 0 || c == 0) return true;
+    return a <= INT32_MAX && b <= INT32_MAX / a && c <= INT32_MAX / (a * b);
+}
+
 // The token count, and the grids: one block per (chunk, head) at most, and
 // dk * dv / 1024 per (sequence, head).
 kda_status_t sizes(int N, int64_t T, int H, bool packed) {
     const int64_t tokens = packed ? T : N * T;
     if (tokens > INT32_MAX) return fail(KDA_ERR_UNSUPPORTED, "the token count must fit in int32");
     const int64_t chunks = packed ? T / kda::kLinChunk + 8ll * N + 8 : N * (T / kda::kLinChunk + 8);
-    if (chunks * H > INT32_MAX || (int64_t)N * H * 16 > INT32_MAX)
+    if (!fits(chunks, H) || !fits(N, H, 16))
         return fail(KDA_ERR_UNSUPPORTED, "the 64-token chunks of all sequences times H must fit in int32");
     return KDA_OK;
 }
@@ -172,7 +178,7 @@ kda_status_t decode(const void *q, const void *k, const void *v, kda_dtype_t dt,
         KDA_CHECK(maybe(status, "device_status", 4));
         return cuda_status(status ? cudaMemsetAsync(status, 0, sizeof(int32_t), s) : cudaSuccess, "status reset");
     }
-    if ((int64_t)N * H * 4 > INT32_MAX) return fail(KDA_ERR_UNSUPPORTED, "N * H * 4 must fit in int32");
+    if (!fits(N, H, 4)) return fail(KDA_ERR_UNSUPPORTED, "N * H * 4 must fit in int32");
     KDA_CHECK(need(q, "q"));
     KDA_CHECK(need(k, "k"));
     KDA_CHECK(need(v, "v"));
