@@ -364,10 +364,13 @@ def rope_table(max_position: int, rotary: int, *, base: float = 10000.0, scaling
     Channel pair i turns by base^(-2 i / rotary) per position. ``scaling``:
     "linear" divides every frequency by ``factor``; "ntk" scales the base so that
     the slowest pair is divided by ``factor`` and the fastest keeps its pace;
-    "yarn" (Peng et al. 2023) divides the pairs that turn fewer than
-    ``beta_slow`` times over ``original_max_position``, keeps those that turn
-    more than ``beta_fast`` times, blends in between, and multiplies cosines and
-    sines by 0.1 ln(factor) + 1."""
+    "yarn" (Peng et al. 2023) divides by ``factor`` the frequencies of the pairs
+    that turn fewer than ``beta_slow`` times over ``original_max_position``, keeps
+    those of the pairs that turn more than ``beta_fast`` times, blends in between
+    in proportion to the number of turns, as the paper's formula does, and
+    multiplies cosines and sines by 0.1 ln(factor) + 1. (A model that was trained
+    with the blend in proportion to the pair's index i needs a table made by that
+    rule: the two agree outside the blend alone.)"""
     if rotary <= 0 or rotary % 2 or max_position <= 0:
         raise ValueError("max_position must be positive and rotary a positive even number")
     if not factor >= 1.0:
@@ -385,6 +388,8 @@ def rope_table(max_position: int, rotary: int, *, base: float = 10000.0, scaling
     elif scaling == "yarn":
         if original_max_position <= 0:
             raise ValueError("scaling='yarn' needs original_max_position")
+        if not 0.0 <= beta_slow < beta_fast < math.inf:
+            raise ValueError("scaling='yarn' needs 0 <= beta_slow < beta_fast")
         f = base ** -i
         turns = original_max_position * f / (2 * math.pi)
         keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
