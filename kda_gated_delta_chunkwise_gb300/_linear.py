@@ -9,7 +9,8 @@ q, k and v may be slices of a wider tensor (a fused projection): their last two
 axes must be contiguous and their tokens evenly spaced. A call runs on its
 tensors' device, current or not. Every call also takes ``stream``, of that
 device: it then runs there, its outputs and workspace are allocated for that
-stream, and the inputs must be ready on it.
+stream, and the inputs must be ready on it. They may be let go of after the call,
+though they come from another stream.
 """
 from __future__ import annotations
 
@@ -159,7 +160,11 @@ def _on_stream(f):
             if index >= 0 and stream.device.index != index:
                 raise ValueError(f"stream is on {stream.device}, q on cuda:{index}")
             with torch.cuda.stream(stream):
-                return f(*args, **kw)
+                out = f(*args, **kw)
+            for t in (*args, *kw.values()):  # the allocator keeps their memory until the stream is past the call
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+            return out
         if index >= 0 and index != torch.cuda.current_device():
             with torch.cuda.device(index):
                 return f(*args, **kw)

@@ -15,8 +15,13 @@ class OnDevice1(torch.Tensor):
     is_cuda = True
     device = torch.device("cuda", 1)
 
+    recorded = []  # (storage, stream) of the tensors that a stream was recorded for
+
     def get_device(self):
         return 1
+
+    def record_stream(self, stream):
+        OnDevice1.recorded.append((self.data_ptr(), stream))
 
     @classmethod
     def __torch_function__(cls, func, types, args=(), kwargs=None):
@@ -99,3 +104,21 @@ def test_a_stream_of_another_device_is_refused(launches, name):
     with pytest.raises(ValueError, match="stream is on cuda:0"):
         _calls()[name](stream=Stream(0))
     assert len(launches) == 1
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_inputs_of_a_call_on_a_stream_are_kept_for_it(launches, name, monkeypatch):
+    """A tensor that is let go of after the call keeps its memory until the stream is past it."""
+    stream, given = Stream(1), []
+    entry = getattr(kda, name[4:])
+
+    def note(*args, **kw):
+        given.extend(t.data_ptr() for t in (*args, *kw.values()) if isinstance(t, torch.Tensor))
+        return entry(*args, **kw)
+    monkeypatch.setattr(kda, name[4:], note)
+    OnDevice1.recorded.clear()
+    _calls()[name]()
+    assert given and not OnDevice1.recorded
+    given.clear()
+    _calls()[name](stream=stream)
+    assert sorted(p for p, s in OnDevice1.recorded if s is stream) == sorted(given)
