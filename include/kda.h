@@ -516,6 +516,12 @@ kda_status_t kda_selftest_bounded_wait(const void *q, const void *k, const void 
  * on 16 bytes, and tokens (of all B sequences, or of the packed batch) follow
  * one another at that distance. Outputs are contiguous. Sizes, types,
  * alignment, streams and errors as for the calls above.
+ *
+ * q, k, v are numbers. An infinity or a NaN in them may reach the outputs of
+ * every token of its sequence and head, earlier ones and ones behind a reset
+ * included (the sums over a block of tokens multiply it by zero), but no other
+ * sequence or head. A state or a sum that is not finite is dropped by a reset,
+ * or by a stretch whose decay is 0 in float32.
  */
 typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1, KDA_DECAY_NONE = 2 } kda_decay_t;
 
@@ -531,9 +537,12 @@ typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1, KDA_DECAY_NONE = 2 } kda
  * final_state may equal initial_state. T = 0 copies the initial state (or
  * zeros). workspace: kda_linear_prefill_workspace_bytes, 256-byte aligned,
  * DEVICE; it may be reused as soon as the work is queued on the same stream.
- * fp32 inputs are computed to fp32 accuracy; with bf16 inputs the states are
- * still accurate to fp32 and o is rounded once to bf16 after products with
- * bf16 (or finer) operands. Two calls on the same inputs give the same bits.
+ * fp32 inputs are computed to fp32 accuracy (relative 2-norm below 1e-5, 1e-6 as
+ * measured). With bf16 inputs the states have that accuracy too, and o is
+ * rounded once to bf16, 1.7e-3 in the 2-norm; with d_k = d_v = 128 the scores and
+ * the state as an operand of o are rounded to bf16 as well, 2.4e-3 in all, with
+ * other sizes they keep 11 bits or more (1.7e-3). Two calls on the same inputs
+ * give the same bits.
  */
 kda_status_t kda_linear_prefill(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype, int64_t q_stride,
                                 int64_t k_stride, int64_t v_stride, const float *log_decay, kda_decay_t decay,
@@ -571,9 +580,12 @@ size_t kda_linear_varlen_prefill_workspace_bytes(int N, int T_total, int H, int 
  *               KDA_DECAY_HEAD the sum over every token; zero at a reset
  *   d_initial_state [B, H, d_k, d_v] float32 or NULL
  * The gradients of q, k, v have their type, as the backward of the norm in
- * front of this call takes them. Sums have a fixed order: two calls on the
- * same inputs give the same bits. workspace:
- * kda_linear_prefill_backward_workspace_bytes, 256-byte aligned.
+ * front of this call takes them, and o's accuracy (bf16, d_k = d_v = 128: 2.4e-3;
+ * dq and dk 1.9e-3 to 2.3e-3 where the decay's gradient is asked for);
+ * dlog_decay and d_initial_state are accurate to fp32 (within 2e-5 and 1e-5,
+ * 1e-6 as measured). Sums have a fixed order: two calls on the same inputs give
+ * the same bits. workspace: kda_linear_prefill_backward_workspace_bytes,
+ * 256-byte aligned.
  */
 kda_status_t kda_linear_prefill_backward(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
                                          int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *log_decay,

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(NT) lin_state_kernel(const StateArgs<T> fwd, c
 // way to the state before the block, S <- e^{L_end} S + c own, and the last S
 // is the final state; reverse, to the gradient of the state after the block.
 // Elementwise over the state: one float4 per thread, the blocks in turn, four
-// loads ahead. Bound by memory, or by the latency of a turn where the sequences
+// loads ahead, with the errors of its sums (ScanElements). Bound by memory, or by the latency of a turn where the sequences
 // are few and long: 4 x 4096 tokens x 16 heads in segments of 1024, 8-10 us;
 // 131072 x 32 in segments of 4096 (67 MB each way), 18 us, 7.5 TB/s (L2 helps).
 struct ScanArgs {
@@ -425,7 +425,8 @@ struct AttendArgs {
 // Everything a block reads is in flight at once; P takes the place of x and y,
 // which leaves room for two CTAs on an SM. 2 x 999 tokens x 4 heads, fp32, 64 x 128:
 // the backward's three passes took 85 us as launches of their own, with loads
-// and products in turn; the whole backward went from 102 to 63 us.
+// and products in turn; the whole backward went from 102 to 63 us (66 since the
+// scan carries its rounding along).
 // In bf16 bound by instructions (8 x 2048 tokens x 16 heads, 64 x 64: 72 % of the
 // issue slots, mostly loads of single values and conversions): 154 us for the
 // whole forward, 137 with the scores as bf16 products and no conversions of

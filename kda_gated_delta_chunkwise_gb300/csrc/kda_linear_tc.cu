@@ -2,8 +2,9 @@
 // d_k = d_v = 128. The same three steps as the general kernels (a block's own
 // state, the scan over the blocks, the outputs), with tcgen05.mma, TMEM and TMA.
 //
-// Both kernels are persistent, one CTA per SM, with the pipeline running on
-// from one work item to the next; roles are warps that meet at mbarriers. Every
+// The state, attend and roll kernels are persistent, one CTA per SM, with the
+// pipeline running on from one work item to the next; roles are warps that meet
+// at mbarriers. Every
 // wait is bounded: a wait that runs out sets the device error word and the
 // CTA's abort flag, every role leaves its loop, and the CTA ends normally.
 #include <cuda.h>
@@ -595,7 +596,9 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 //   of the columns into the front of its own half);
 //   O += P z, P read from TMEM.
 // P and S are the two roundings to bf16 (2^-9 relative each, as small as the
-// rounding of the result itself); sums are fp32.
+// rounding of the result itself: dv is 2.35e-3 from 64 bits in the 2-norm, the
+// result's rounding alone 1.66e-3); sums are fp32. With DOTS S is exact to 24
+// bits and P alone is rounded: dq and dk 1.9e-3 to 2.3e-3.
 // 4 x 4096 tokens x 16 heads, 256-token blocks: dq 97 us and dk 108 with their
 // dots (371 MB, 3.4 to 3.8 TB/s), dv 59 (236 MB, 4.0 TB/s). Bound by the latency
 // of its loads: shared memory holds one item's operands and the first of the
@@ -1082,8 +1085,10 @@ lin_attend_tc_kernel(AttendTcArgs p, const __grid_constant__ CUtensorMap mx, con
 // In reverse time (REV) the chunks go from the segment's end, the state is the
 // gradient after the chunk, and the mask and the decays are mirrored. ST: the
 // first state is read transposed. P, Sb and the result are the roundings to
-// bf16. Bound by memory in principle (4 x 4096 tokens x 16 heads: 75 us, 268 MB,
-// 3.5 TB/s; 131072 x 32: 862 us, 4.3 GB, 5.0 TB/s, 74 % of a copy); a 128-token chunk
+// bf16 (2.35e-3 from 64 bits in the 2-norm, the result's alone 1.66e-3; P or Sb
+// in two parts would add 8 of a chunk's 40 tensor-core steps each, and Sb 32 KB
+// of shared memory that is not there). Bound by memory in principle (4 x 4096 tokens x 16 heads: 75 us, 268 MB,
+// 3.5 TB/s; 131072 x 32: 885 us, 4.3 GB, 4.9 TB/s, 72 % of a copy); a 128-token chunk
 // costs 40 tensor-core steps, and two
 // loops run from one chunk to the next, each to stay under the time that the
 // chunk's 128 KB take: S -> Sb, scale -> MMA -> S, and x Sb -> scale -> P z -> out.

@@ -21,7 +21,7 @@
 // with A and B made once per token. Sums, norms and the rotation are in fp32;
 // the only rounding to fewer bits is the store. 16384 tokens x (16 + 16) heads
 // of 128 bf16 channels: forward 51.3 us (5.3 TB/s, 78 % of a copy), backward with
-// both weights' gradients 81.6 (5.0 TB/s, 73 %), the last sum (8 us on cold caches) included.
+// both weights' gradients 81.3 (5.0 TB/s, 74 %), the last sum (8-10 us on cold caches) included.
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
 
