@@ -676,6 +676,196 @@ kda_status_t kda_qk_norm_rope_backward(const void *q, const void *k, const void 
 /* Workspace bytes kda_qk_norm_rope_backward needs for weight gradients. */
 size_t kda_qk_norm_rope_backward_workspace_bytes(int d);
 
+/*
+ * kda_qk_norm_rope_axes - kda_qk_norm_rope with a position on each of several
+ * axes (time, height, width of a picture's token): channel pair i turns by the
+ * angle that the table's row of its own axis' position holds for it.
+ *   positions  [axes, tokens] int32; a token with any position outside
+ *              [0, max_position) is left out and sets KDA_DEV_BAD_POSITION
+ *   axes       1 to 4
+ *   pair_axis  [rotary / 2] the axis of every channel pair, HOST memory, read
+ *              during the call; rotary must be positive. Frequencies that start
+ *              afresh on each axis are a matter of the table.
+ * Everything else as there, the workspace of the gradients too.
+ */
+kda_status_t kda_qk_norm_rope_axes(const void *q, const void *k, kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                   const int32_t *positions, int axes, const uint8_t *pair_axis, const float *rope_table,
+                                   int max_position, int rotary, kda_rope_layout_t layout, const float *q_weight,
+                                   const float *k_weight, kda_norm_t norm, float eps, void *q_out, void *k_out,
+                                   int64_t tokens, int H_q, int H_k, int d, int32_t *device_status, kda_stream_t stream);
+kda_status_t kda_qk_norm_rope_axes_backward(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                                            kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                            const int32_t *positions, int axes, const uint8_t *pair_axis,
+                                            const float *rope_table, int max_position, int rotary,
+                                            kda_rope_layout_t layout, const float *q_weight, const float *k_weight,
+                                            kda_norm_t norm, float eps, void *dq, void *dk, float *dq_weight,
+                                            float *dk_weight, int64_t tokens, int H_q, int H_k, int d, void *workspace,
+                                            size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/*
+ * ---- The norms around a block.
+ *
+ * kda_gated_norm - behind a recurrence or an attention: the norm of every head
+ * times a gate,  out = weight * x / norm(x) * a(gate).
+ *   x, gate [tokens, H, d] dtype, token strides as above (d 64 or 128)   (read)
+ *   weight  [d] float32 or NULL (ones), shared by the heads
+ *   out     [tokens, H, d] dtype, contiguous; may be x or gate itself, if that
+ *           is contiguous                                                (written)
+ * eps > 0 unless norm is KDA_NORM_NONE.
+ */
+typedef enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_activation_t;  /* 1 / (1 + e^-g); g / (1 + e^-g) */
+
+kda_status_t kda_gated_norm(const void *x, const void *gate, kda_dtype_t dtype, int64_t x_stride, int64_t gate_stride,
+                            const float *weight, kda_norm_t norm, kda_activation_t activation, float eps, void *out,
+                            int64_t tokens, int H, int d, kda_stream_t stream);
+
+/* kda_gated_norm_backward - its gradients: d_out as out; dx, dgate dtype,
+ * contiguous; dweight [d] float32 or NULL (not wanted), summed over every token
+ * and head in a fixed order. workspace (256-byte aligned) is needed with dweight. */
+kda_status_t kda_gated_norm_backward(const void *x, const void *gate, const void *d_out, kda_dtype_t dtype,
+                                     int64_t x_stride, int64_t gate_stride, const float *weight, kda_norm_t norm,
+                                     kda_activation_t activation, float eps, void *dx, void *dgate, float *dweight,
+                                     int64_t tokens, int H, int d, void *workspace, size_t workspace_bytes,
+                                     kda_stream_t stream);
+
+/* Workspace bytes kda_gated_norm_backward needs for the weight's gradient. */
+size_t kda_gated_norm_backward_workspace_bytes(int d);
+
+/*
+ * kda_residual_norm - between two blocks: the branch of the one, normed or not,
+ * scaled, added to the residual stream, and the norm that the next one reads:
+ *     u = branch_weight * branch / norm(branch)      (branch_norm NONE: no division)
+ *     hidden = residual + scale * channel_scale * u
+ *     out = weight * hidden / sqrt(mean hidden^2 + eps)
+ *   residual, hidden [tokens, D] stream_dtype, contiguous; hidden may be residual
+ *   branch, out      [tokens, D] dtype, contiguous; out may be branch
+ *   weight, branch_weight, channel_scale  [D] float32 or NULL (ones)
+ * stream_dtype is dtype or float32. D is a multiple of 8 up to 8192. out is made
+ * from hidden before it is rounded to stream_dtype.
+ */
+kda_status_t kda_residual_norm(const void *residual, const void *branch, kda_dtype_t stream_dtype, kda_dtype_t dtype,
+                               const float *weight, kda_norm_t branch_norm, const float *branch_weight,
+                               const float *channel_scale, float scale, float eps, void *hidden, void *out,
+                               int64_t tokens, int D, kda_stream_t stream);
+
+/*
+ * kda_residual_norm_backward - its gradients, from the stored hidden: d_out as
+ * out, d_hidden (what reaches hidden by the stream) as hidden or NULL (zero).
+ *   d_residual [tokens, D] stream_dtype, d_branch [tokens, D] dtype     (written)
+ *   dweight, dbranch_weight, dchannel_scale  [D] float32 or NULL (not wanted),
+ *              summed over the tokens in a fixed order
+ * branch may be NULL where branch_norm is NONE and branch_weight, channel_scale
+ * and their gradients are all NULL. workspace (256-byte aligned) is needed for
+ * any of the three sums.
+ */
+kda_status_t kda_residual_norm_backward(const void *hidden, const void *branch, const void *d_out, const void *d_hidden,
+                                        kda_dtype_t stream_dtype, kda_dtype_t dtype, const float *weight,
+                                        kda_norm_t branch_norm, const float *branch_weight, const float *channel_scale,
+                                        float scale, float eps, void *d_residual, void *d_branch, float *dweight,
+                                        float *dbranch_weight, float *dchannel_scale, int64_t tokens, int D,
+                                        void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes kda_residual_norm_backward needs for the sums. */
+size_t kda_residual_norm_backward_workspace_bytes(int D);
+
+/*
+ * ---- Attention with a sliding window and sinks: the layers that look exactly at
+ * the near tokens, between those that carry a state.
+ *
+ * Token i of a sequence sees token j <= i where i - j < window or j < sinks:
+ *     s_ij = scale q_i . k_j,  lse_i = log sum_j e^{s_ij},  o_i = sum_j e^{s_ij - lse_i} v_j
+ * Query head h reads key head h / (H_q / H_k).
+ *   q, o    [.., H_q, d] dtype;  k, v [.., H_k, d] dtype;  d 64 or 128
+ *   lse     [.., H_q] float32: natural logarithm (nullable; the gradients want it)
+ *   window  >= 1, as long as you like;  sinks 0 to 128
+ * q, k, v may be views of a wider tensor (token strides as for linear attention);
+ * outputs are contiguous. Two calls on the same inputs give the same bits, and a
+ * sequence the same ones alone and in a packed batch. fp32 calls are accurate to
+ * fp32 (relative 2-norm below 1e-5); in bf16 calls the weights e^{s - lse} (and the
+ * ds of the gradients) are rounded to bf16 as operands, which stays below the
+ * result's own rounding. Scores are numbers of fp32's range. An infinity or a
+ * NaN in a token's k or v may reach tokens of its own sequence that do not see it
+ * (the products multiply it by zero), but no other sequence or key head.
+ */
+kda_status_t kda_window_attention(const void *q, const void *k, const void *v, kda_dtype_t dtype, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, float scale, int window, int sinks, void *o,
+                                  float *lse, int B, int T, int H_q, int H_k, int d, kda_stream_t stream);
+
+/* kda_window_varlen_attention - N sequences packed along the token axis
+ * (cu_seqlens and device_status as kda_linear_varlen_prefill: on a bad one
+ * nothing is written). workspace 256-byte aligned. */
+kda_status_t kda_window_varlen_attention(const void *q, const void *k, const void *v, kda_dtype_t dtype,
+                                         int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, int window,
+                                         int sinks, void *o, float *lse, const int32_t *cu_seqlens, int N, int T_total,
+                                         int H_q, int H_k, int d, void *workspace, size_t workspace_bytes,
+                                         int32_t *device_status, kda_stream_t stream);
+
+/* Workspace bytes kda_window_varlen_attention needs (0 for invalid arguments). */
+size_t kda_window_varlen_attention_workspace_bytes(int N, int T_total, int H_q, int H_k, int d);
+
+/*
+ * kda_window_attention_backward - the gradients for L = sum <d_o, o>: o and lse
+ * as the forward left them, d_o as o (contiguous).
+ *   dq [B, T, H_q, d], dk, dv [B, T, H_k, d]  dtype, contiguous        (written)
+ * dk and dv are summed over their query heads, in a fixed order. workspace:
+ * 256-byte aligned, kda_window_attention_backward_workspace_bytes.
+ */
+kda_status_t kda_window_attention_backward(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                           const void *d_o, kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                           int64_t v_stride, float scale, int window, int sinks, void *dq, void *dk,
+                                           void *dv, int B, int T, int H_q, int H_k, int d, void *workspace,
+                                           size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes kda_window_attention_backward needs (0 for invalid arguments). */
+size_t kda_window_attention_backward_workspace_bytes(int B, int T, int H_q, int H_k, int d, int sinks);
+
+/* kda_window_varlen_attention_backward - the gradients of
+ * kda_window_varlen_attention; layouts and device_status as there. */
+kda_status_t kda_window_varlen_attention_backward(const void *q, const void *k, const void *v, const void *o,
+                                                  const float *lse, const void *d_o, kda_dtype_t dtype, int64_t q_stride,
+                                                  int64_t k_stride, int64_t v_stride, float scale, int window, int sinks,
+                                                  void *dq, void *dk, void *dv, const int32_t *cu_seqlens, int N,
+                                                  int T_total, int H_q, int H_k, int d, void *workspace,
+                                                  size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
+
+/* Workspace bytes kda_window_varlen_attention_backward needs (0 for invalid arguments). */
+size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, int H_q, int H_k, int d, int sinks);
+
+/*
+ * The cache of a served sequence has a constant size, as a state has: slots of
+ * entries = sinks + window tokens in a pool,
+ *   k_cache, v_cache  [pool_size, entries, H_k, d] dtype, DEVICE
+ *   slots  [N] int32, DEVICE: sequence n uses slot s = slots[n]; -1 - s stands for
+ *          s too, so the slots of a fresh request's states (above) serve here as
+ *          they are. Two sequences of one call must not share a slot. A slot
+ *          outside [0, pool_size) leaves its sequence out and sets KDA_DEV_BAD_SLOT.
+ * The token at position p of a sequence lies in entry p (p < sinks) or
+ * sinks + (p - sinks) mod window.
+ *
+ * kda_window_cache_write - keys and values of N packed prompts, from position 0
+ * on: of each the first `sinks` and the last `window` tokens go into its slot;
+ * the entries that it has no tokens for are left as they are. A bad cu_seqlens
+ * sets KDA_DEV_BAD_CU_SEQLENS and nothing is written.
+ */
+kda_status_t kda_window_cache_write(const void *k, const void *v, kda_dtype_t dtype, int64_t k_stride, int64_t v_stride,
+                                    const int32_t *cu_seqlens, const int32_t *slots, int sinks, void *k_cache,
+                                    void *v_cache, int pool_size, int entries, int N, int T_total, int H_k, int d,
+                                    int32_t *device_status, kda_stream_t stream);
+
+/*
+ * kda_window_decode_step - one token per sequence, at position positions[n] (the
+ * tokens of the sequence before it; int32, DEVICE): k and v [N, H_k, d] are
+ * written to their entry, and q [N, H_q, d] attends over the entries that hold
+ * tokens, this one's included (o [N, H_q, d]). Entries without a token are not
+ * read. A negative position leaves its sequence out and sets
+ * KDA_DEV_BAD_POSITION. The strides are between sequences.
+ */
+kda_status_t kda_window_decode_step(const void *q, const void *k, const void *v, kda_dtype_t dtype, int64_t q_stride,
+                                    int64_t k_stride, int64_t v_stride, float scale, int sinks, void *k_cache,
+                                    void *v_cache, int pool_size, int entries, const int32_t *slots,
+                                    const int32_t *positions, void *o, int N, int H_q, int H_k, int d,
+                                    int32_t *device_status, kda_stream_t stream);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char *kda_last_error(void);
 

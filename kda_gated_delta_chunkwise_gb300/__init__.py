@@ -17,7 +17,12 @@ decay (the update without its erase step): ``linear_prefill``,
 ``linear_varlen_prefill``, their gradients ``linear_prefill_backward`` and
 ``linear_varlen_prefill_backward``, ``linear_decode_step`` and
 ``linear_decode_step_slots``; the norm of query and key heads with the rotary
-positions: ``qk_norm_rope``, ``qk_norm_rope_backward``, ``rope_table``. Build the CUDA library with
+positions: ``qk_norm_rope``, ``qk_norm_rope_backward``, ``rope_table``, and with
+positions on several axes ``qk_norm_rope_axes``, ``qk_norm_rope_axes_backward``.
+Around the blocks: ``gated_norm``, ``residual_norm`` and their ``_backward``.
+Attention with a sliding window and sinks: ``window_attention``,
+``window_varlen_attention``, their ``_backward``, and for serving
+``window_cache_write`` and ``window_decode_step``. Build the CUDA library with
 ``kda_gated_delta_chunkwise_gb300.build.build()`` first.
 """
 from ._binding import (ALGOS, EXPORTS, GATES, KDA_DEV_BAD_CU_SEQLENS, KDA_DEV_BAD_SLOT, KDA_DEV_BAD_POSITION,  # noqa: F401
@@ -30,4 +35,9 @@ from ._linear import (DECAYS, NORMS, ROPE_LAYOUTS, linear_decode_step, linear_de
                       linear_prefill, linear_prefill_backward, linear_prefill_backward_workspace_bytes,
                       linear_prefill_workspace_bytes, linear_varlen_prefill, linear_varlen_prefill_backward,
                       linear_varlen_prefill_backward_workspace_bytes, linear_varlen_prefill_workspace_bytes,
-                      qk_norm_rope, qk_norm_rope_backward, rope_table)
+                      qk_norm_rope, qk_norm_rope_axes, qk_norm_rope_axes_backward, qk_norm_rope_backward, rope_table)
+from ._block import (ACTIVATIONS, gated_norm, gated_norm_backward, residual_norm, residual_norm_backward)  # noqa: F401
+from ._window import (window_attention, window_attention_backward, window_attention_backward_workspace_bytes,  # noqa: F401
+                      window_cache_write, window_decode_step, window_varlen_attention,
+                      window_varlen_attention_backward, window_varlen_attention_backward_workspace_bytes,
+                      window_varlen_attention_workspace_bytes)

@@ -40,7 +40,12 @@ EXPORTS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_gate", "kda_prefill_fp8
            "kda_linear_prefill_backward_workspace_bytes", "kda_linear_varlen_prefill_backward",
            "kda_linear_varlen_prefill_backward_workspace_bytes", "kda_linear_decode_step",
            "kda_linear_decode_step_slots", "kda_qk_norm_rope", "kda_qk_norm_rope_backward",
-           "kda_qk_norm_rope_backward_workspace_bytes",
+           "kda_qk_norm_rope_backward_workspace_bytes", "kda_qk_norm_rope_axes", "kda_qk_norm_rope_axes_backward",
+           "kda_gated_norm", "kda_gated_norm_backward", "kda_gated_norm_backward_workspace_bytes", "kda_residual_norm",
+           "kda_residual_norm_backward", "kda_residual_norm_backward_workspace_bytes", "kda_window_attention",
+           "kda_window_varlen_attention", "kda_window_varlen_attention_workspace_bytes", "kda_window_attention_backward",
+           "kda_window_attention_backward_workspace_bytes", "kda_window_varlen_attention_backward",
+           "kda_window_varlen_attention_backward_workspace_bytes", "kda_window_cache_write", "kda_window_decode_step",
            "kda_device_errors", "kda_last_error", "kda_abi_version")
 
 _lock = threading.Lock()
@@ -145,6 +150,31 @@ def load(path: str | None = None):
             getattr(lib, name + "_workspace_bytes").restype = sz
         lib.kda_qk_norm_rope_backward_workspace_bytes.argtypes = [i]
         lib.kda_qk_norm_rope_backward_workspace_bytes.restype = sz
+        axes = [vp, vp, i, ll, ll, vp, i, ctypes.c_char_p, vp, i, i, i, vp, vp, i, fl]  # positions, axes, pair_axis, table
+        lib.kda_qk_norm_rope_axes.argtypes = axes + [vp, vp, ll, i, i, i, vp, vp]
+        lib.kda_qk_norm_rope_axes_backward.argtypes = ([vp, vp] + axes + [vp, vp, vp, vp, ll, i, i, i, vp, sz, vp, vp])
+        lib.kda_gated_norm.argtypes = [vp, vp, i, ll, ll, vp, i, i, fl, vp, ll, i, i, vp]
+        lib.kda_gated_norm_backward.argtypes = [vp, vp, vp, i, ll, ll, vp, i, i, fl, vp, vp, vp, ll, i, i, vp, sz, vp]
+        lib.kda_residual_norm.argtypes = [vp, vp, i, i, vp, i, vp, vp, fl, fl, vp, vp, ll, i, vp]
+        lib.kda_residual_norm_backward.argtypes = ([vp] * 4 + [i, i, vp, i, vp, vp, fl, fl] + [vp] * 5 +
+                                                   [ll, i, vp, sz, vp])
+        win = [i, ll, ll, ll, fl, i, i]  # dtype, strides, scale, window, sinks
+        lib.kda_window_attention.argtypes = [vp] * 3 + win + [vp, vp] + [i] * 5 + [vp]
+        lib.kda_window_varlen_attention.argtypes = [vp] * 3 + win + [vp] * 3 + [i] * 5 + [vp, sz, vp, vp]
+        lib.kda_window_attention_backward.argtypes = [vp] * 6 + win + [vp] * 3 + [i] * 5 + [vp, sz, vp]
+        lib.kda_window_varlen_attention_backward.argtypes = [vp] * 6 + win + [vp] * 4 + [i] * 5 + [vp, sz, vp, vp]
+        lib.kda_window_cache_write.argtypes = [vp, vp, i, ll, ll, vp, vp, i, vp, vp] + [i] * 6 + [vp, vp]
+        lib.kda_window_decode_step.argtypes = [vp] * 3 + [i, ll, ll, ll, fl, i, vp, vp, i, i, vp, vp, vp] + [i] * 4 + [vp, vp]
+        for name in ("kda_qk_norm_rope_axes", "kda_qk_norm_rope_axes_backward", "kda_gated_norm",
+                     "kda_gated_norm_backward", "kda_residual_norm", "kda_residual_norm_backward",
+                     "kda_window_attention", "kda_window_varlen_attention", "kda_window_attention_backward",
+                     "kda_window_varlen_attention_backward", "kda_window_cache_write", "kda_window_decode_step"):
+            getattr(lib, name).restype = i
+        for name, n in (("kda_gated_norm_backward", 1), ("kda_residual_norm_backward", 1),
+                        ("kda_window_varlen_attention", 5), ("kda_window_attention_backward", 6),
+                        ("kda_window_varlen_attention_backward", 6)):
+            getattr(lib, name + "_workspace_bytes").argtypes = [i] * n
+            getattr(lib, name + "_workspace_bytes").restype = sz
         lib.kda_last_error.restype = ctypes.c_char_p
         lib.kda_last_error.argtypes = []
         lib.kda_abi_version.restype = ctypes.c_int

@@ -15,6 +15,7 @@ though they come from another stream.
 from __future__ import annotations
 
 import functools
+import inspect
 import math
 
 import torch
@@ -150,15 +151,18 @@ def _bytes(name: str, n: int, T: int, H: int, dk: int, dv: int, dtype) -> int:
 
 
 def _on_stream(f):
-    """Runs ``f`` on q's device, with its ``stream`` current where one is given, so that what it allocates belongs to
-    that stream. A launch goes to the current device, whatever the pointers and the stream's handle belong to."""
+    """Runs ``f`` on its first argument's device, with its ``stream`` current where one is given, so that what it
+    allocates belongs to that stream. A launch goes to the current device, whatever the pointers and the stream's
+    handle belong to."""
+    first = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
     def g(*args, stream=None, **kw):
-        q = args[0] if args else kw.get("q")
+        q = args[0] if args else kw.get(first)
         index = q.get_device() if isinstance(q, torch.Tensor) else -1  # -1: not a CUDA tensor, refused by f
         if stream is not None:
             if index >= 0 and stream.device.index != index:
-                raise ValueError(f"stream is on {stream.device}, q on cuda:{index}")
+                raise ValueError(f"stream is on {stream.device}, {first} on cuda:{index}")
             with torch.cuda.stream(stream):
                 out = f(*args, **kw)
             for t in (*args, *kw.values()):  # the allocator keeps their memory until the stream is past the call
@@ -414,7 +418,7 @@ def _weight_grad_bytes(d: int) -> int:
     return int(load().kda_qk_norm_rope_backward_workspace_bytes(d))
 
 
-def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout, device_status):
+def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout, device_status, axes=()):
     if q is None or q.dim() < 3:
         raise ValueError("q must be [.., H_q, d]")
     lead = q.dim() - 2
@@ -428,8 +432,9 @@ def _norm_rope_inputs(q, k, positions, table, q_weight, k_weight, norm, layout, 
     if table is not None:
         _plain(table, "rope_table", torch.float32, index)
         _plain(positions, "positions", torch.int32, index)
-        if table.dim() != 2 or positions.shape != shape[:-2]:
-            raise ValueError("rope_table must be [max_position, rotary] and positions have q's leading axes")
+        if table.dim() != 2 or positions.shape != (*axes, *shape[:-2]):
+            raise ValueError("rope_table must be [max_position, rotary] and positions have q's leading axes"
+                             + (" behind the one of the axes" if axes else ""))
         max_position, rot = table.shape
     elif positions is not None:
         raise ValueError("positions need a rope_table")
@@ -492,4 +497,75 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope_table=None,
                                               ks, _ptr(positions), _ptr(rope_table), P, rot, lay, _ptr(q_weight),
                                               _ptr(k_weight), nk, eps, *(_ptr(t) for t in out.values()), n, hq, hk, d,
                                               _ptr(ws), size, _ptr(device_status), _stream(index)))
+    return out
+
+
+def _axes(pair_axis, positions, table):
+    """Checks the axes; returns (their number, the pairs' axes as bytes)."""
+    if positions is None or table is None:
+        raise ValueError("positions and rope_table are required")
+    if table.dim() != 2 or positions.dim() < 1:
+        raise ValueError("rope_table must be [max_position, rotary] and positions [axes, ..]")
+    pairs, axes = _pair_axes(pair_axis if isinstance(pair_axis, (tuple, bytes)) else tuple(pair_axis)), positions.shape[0]
+    if len(pairs) != table.shape[1] // 2:
+        raise ValueError(f"pair_axis must have {table.shape[1] // 2} entries, one for every channel pair, got {len(pairs)}")
+    return axes, pairs
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axes(pair_axis) -> bytes:
+    if any(not 0 <= a <= 255 for a in pair_axis):
+        raise ValueError("pair_axis must hold axes, 0 <= a < positions.shape[0]")
+    return bytes(pair_axis)
+
+
+@_on_stream
+def qk_norm_rope_axes(q, k, positions, rope_table, pair_axis, q_weight=None, k_weight=None, *, norm: str = "rms",
+                      eps: float = 1e-6, layout: str = "half", q_out=None, k_out=None, device_status=None):
+    """``qk_norm_rope`` with a position on each of several axes (time, height
+    and width of a picture's token, say).
+
+    positions: int32 [axes, ..] (1 to 4 axes, then q's leading axes); pair_axis:
+    the axis of every channel pair, ``rope_table.shape[1] / 2`` ints: pair i turns
+    by the angle that the table's row ``positions[pair_axis[i]]`` holds for it.
+    Everything else as there; a token with a position outside the table on any
+    axis is left out."""
+    lib = load()
+    axes, pairs = _axes(pair_axis, positions, rope_table)
+    index, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
+                                                                           k_weight, norm, layout, device_status,
+                                                                           (axes,))
+    q_out = _out(q_out, "q_out", q, q.shape, q.dtype, index)
+    k_out = _out(k_out, "k_out", k, k.shape, q.dtype, index)
+    _check(lib, lib.kda_qk_norm_rope_axes(q.data_ptr(), k.data_ptr(), code, qs, ks, positions.data_ptr(), axes, pairs,
+                                          rope_table.data_ptr(), P, rot, lay, _ptr(q_weight), _ptr(k_weight), nk, eps,
+                                          q_out.data_ptr(), k_out.data_ptr(), n, hq, hk, d, _ptr(device_status),
+                                          _stream(index)))
+    return q_out, k_out
+
+
+@_on_stream
+def qk_norm_rope_axes_backward(q, k, dq_out, dk_out, positions, rope_table, pair_axis, q_weight=None, k_weight=None, *,
+                               norm: str = "rms", eps: float = 1e-6, layout: str = "half", workspace=None,
+                               device_status=None):
+    """Gradients of ``qk_norm_rope_axes``: the dict of ``qk_norm_rope_backward``."""
+    lib = load()
+    axes, pairs = _axes(pair_axis, positions, rope_table)
+    index, n, d, hq, hk, code, qs, ks, P, rot, lay, nk = _norm_rope_inputs(q, k, positions, rope_table, q_weight,
+                                                                           k_weight, norm, layout, device_status,
+                                                                           (axes,))
+    _plain(dq_out, "dq_out", q.dtype, index, q.shape)
+    _plain(dk_out, "dk_out", q.dtype, index, k.shape)
+    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+           "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
+           "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+           "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
+    ws, size = None, 0
+    if q_weight is not None or k_weight is not None:
+        ws, size = _space(workspace, _weight_grad_bytes(d), q)
+    _check(lib, lib.kda_qk_norm_rope_axes_backward(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), code,
+                                                   qs, ks, positions.data_ptr(), axes, pairs, rope_table.data_ptr(), P,
+                                                   rot, lay, _ptr(q_weight), _ptr(k_weight), nk, eps,
+                                                   *(_ptr(t) for t in out.values()), n, hq, hk, d, _ptr(ws), size,
+                                                   _ptr(device_status), _stream(index)))
     return out

@@ -113,7 +113,7 @@ struct NormRopeArgs {
     int64_t q_stride, k_stride;
     const void *dyq, *dyk;        // backward: gradients of the outputs, contiguous
     void *yq, *yk, *dxq, *dxk;    // contiguous
-    const int32_t *positions;     // [tokens]
+    const int32_t *positions;     // [tokens], of several axes [axes][tokens]
     const float *table;           // [max_position][rot]: cosines, then sines
     const float *wq, *wk;         // [d], nullable
     float *dwq, *dwk, *partial;   // backward: [d], nullable; partial null when neither is wanted
@@ -121,7 +121,11 @@ struct NormRopeArgs {
     int64_t tokens;
     int hq, hk, d, rot, max_position, norm, layout;
     float eps;
+    int axes;                     // 0: one position a token
+    uint64_t axis_bits[2];        // several: the axis of every channel pair, two bits each
+    bool quads;                   // aligned groups of four pairs share an axis
 };
+constexpr int kRopeAxes = 4;      // at most
 cudaError_t launch_norm_rope(const NormRopeArgs &p, bool back, cudaStream_t s);
 
 // ---------------------------------------------------------------- linear attention

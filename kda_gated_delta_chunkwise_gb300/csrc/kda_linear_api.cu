@@ -2,53 +2,12 @@
 // include/kda.h: argument checks, then launches. Nothing here allocates,
 // synchronises or reads device memory; every check comes before the first
 // launch of a call.
-#include <cmath>
-#include <cstdarg>
-#include <cstdio>
-
+#include "kda_checks.cuh"
 #include "kda_linear.cuh"
 
+using namespace kda;
+
 namespace {
-
-kda_status_t fail(kda_status_t st, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    return kda::set_error(st, buf);
-}
-kda_status_t ok() { return kda::set_error(KDA_OK, ""); }
-kda_status_t cuda_status(cudaError_t e, const char *what) {
-    return e == cudaSuccess ? ok() : fail(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-#define KDA_CHECK(x)                                   \
-    do {                                               \
-        const kda_status_t st_ = (x);                  \
-        if (st_ != KDA_OK) return st_;                 \
-    } while (0)
-
-kda_status_t need(const void *p, const char *name, uintptr_t align = 16) {
-    if (!p) return fail(KDA_ERR_INVALID_ARG, "%s must not be NULL", name);
-    if (!aligned(p, align)) return fail(KDA_ERR_INVALID_ARG, "%s must be %d-byte aligned", name, (int)align);
-    return KDA_OK;
-}
-kda_status_t maybe(const void *p, const char *name, uintptr_t align = 16) {
-    return p ? need(p, name, align) : KDA_OK;
-}
-
-// The distance between two tokens of a tensor in elements: 0 stands for the
-// contiguous H * d; rows must start on 16 bytes and must not overlap.
-kda_status_t stride(int64_t &s, int H, int d, kda_dtype_t dt, const char *name) {
-    if (s == 0) s = (int64_t)H * d;
-    const int per = dt == KDA_BF16 ? 8 : 4;
-    if (s < (int64_t)H * d || s % per)
-        return fail(KDA_ERR_INVALID_ARG, "%s must be 0 or at least H * d and a multiple of 16 bytes (got %lld)", name,
-                    (long long)s);
-    return KDA_OK;
-}
 
 kda_status_t common(kda_dtype_t dt, int decay, int N, int64_t T, int H, int dk, int dv, float scale) {
     if (dt != KDA_F32 && dt != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown qkv dtype %d", (int)dt);
@@ -61,12 +20,6 @@ kda_status_t common(kda_dtype_t dt, int decay, int N, int64_t T, int H, int dk, 
     if (N < 0 || T < 0) return fail(KDA_ERR_INVALID_ARG, "the sequence and token counts must be >= 0");
     if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
     return KDA_OK;
-}
-
-// a * b * c <= INT32_MAX, for factors >= 0 whose product may not fit in 64 bits
-bool fits(int64_t a, int64_t b, int64_t c = 1) {
-    if (a == 0 || b == 0 || c == 0) return true;
-    return a <= INT32_MAX && b <= INT32_MAX / a && c <= INT32_MAX / (a * b);
 }
 
 // The token count, and the grids: one block per (chunk, head) at most, and
@@ -82,13 +35,6 @@ kda_status_t sizes(int N, int64_t T, int H, bool packed) {
 
 kda_status_t log_decay_ok(const float *g, int decay) {
     return decay == KDA_DECAY_NONE ? KDA_OK : need(g, "log_decay", 4);
-}
-
-kda_status_t workspace_ok(const void *ws, size_t have, size_t want) {
-    if (!want) return KDA_OK;
-    if (!ws || have < want) return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", want, have);
-    if (!aligned(ws, 256)) return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    return KDA_OK;
 }
 
 // A call on no sequences: of a packed batch with tokens all the same, the
@@ -198,6 +144,24 @@ bool bad_sizes(int N, int64_t T, int H, int dk, int dv, kda_dtype_t dt, bool pac
     return common(dt, KDA_DECAY_NONE, N, T, H, dk, dv, 1.f) != KDA_OK || sizes(N, T, H, packed) != KDA_OK;
 }
 
+// Several axes: each channel pair's axis, from the caller's array.
+kda_status_t axes_of(kda::NormRopeArgs &p, const uint8_t *pair_axis, int axes) {
+    if (axes < 1 || axes > kRopeAxes)
+        return fail(axes < 1 ? KDA_ERR_INVALID_ARG : KDA_ERR_UNSUPPORTED, "1 to %d axes (got %d)", kRopeAxes, axes);
+    if (p.rot <= 0 || p.rot > 128)
+        return fail(KDA_ERR_INVALID_ARG, "positions of several axes need a rotary size up to the head size (got %d)", p.rot);
+    if (!pair_axis) return fail(KDA_ERR_INVALID_ARG, "pair_axis must not be NULL");
+    p.axes = axes;
+    p.quads = true;
+    for (int i = 0; i < p.rot / 2; ++i) {
+        if (pair_axis[i] >= axes)
+            return fail(KDA_ERR_INVALID_ARG, "pair_axis[%d] is %d, there are %d axes", i, pair_axis[i], axes);
+        p.axis_bits[i >> 5] |= (uint64_t)pair_axis[i] << (2 * (i & 31));
+        if (pair_axis[i] != pair_axis[i & ~3]) p.quads = false;
+    }
+    return KDA_OK;
+}
+
 kda_status_t norm_rope(kda::NormRopeArgs &p, int64_t tokens) {
     if (p.dt != KDA_F32 && p.dt != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)p.dt);
     if (p.norm != KDA_NORM_NONE && p.norm != KDA_NORM_L2 && p.norm != KDA_NORM_RMS)
@@ -232,6 +196,45 @@ kda_status_t norm_rope(kda::NormRopeArgs &p, int64_t tokens) {
     KDA_CHECK(maybe(p.wq, "q_weight"));
     KDA_CHECK(maybe(p.wk, "k_weight"));
     return maybe(p.status, "device_status", 4);
+}
+
+kda_status_t norm_rope_forward(kda::NormRopeArgs &p, int64_t tokens, cudaStream_t s) {
+    KDA_CHECK(norm_rope(p, tokens));
+    if (tokens > 0 && p.hq > 0) KDA_CHECK(need(p.yq, "q_out"));
+    if (tokens > 0 && p.hk > 0) KDA_CHECK(need(p.yk, "k_out"));
+    if (p.status) {
+        const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(int32_t), s);
+        if (e != cudaSuccess) return cuda_status(e, "status reset");
+    }
+    if (tokens == 0 || p.hq + p.hk == 0) return ok();
+    return cuda_status(kda::launch_norm_rope(p, false, s), "norm and rotation launch");
+}
+
+kda_status_t norm_rope_backward(kda::NormRopeArgs &p, int64_t tokens, void *workspace, size_t workspace_bytes,
+                                cudaStream_t s) {
+    KDA_CHECK(norm_rope(p, tokens));
+    if (tokens > 0 && p.hq > 0) {
+        KDA_CHECK(need(p.dyq, "dq_out"));
+        KDA_CHECK(need(p.dxq, "dq"));
+    }
+    if (tokens > 0 && p.hk > 0) {
+        KDA_CHECK(need(p.dyk, "dk_out"));
+        KDA_CHECK(need(p.dxk, "dk"));
+    }
+    KDA_CHECK(maybe(p.dwq, "dq_weight", 4));
+    KDA_CHECK(maybe(p.dwk, "dk_weight", 4));
+    if (p.dwq || p.dwk) {
+        KDA_CHECK(workspace_ok(workspace, workspace_bytes, kda_qk_norm_rope_backward_workspace_bytes(p.d)));
+        p.partial = static_cast<float *>(workspace);
+    }
+    cudaError_t e = p.status ? cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) : cudaSuccess;
+    if (tokens == 0 || p.hq + p.hk == 0) {  // the sums over no rows
+        if (e == cudaSuccess && p.dwq) e = cudaMemsetAsync(p.dwq, 0, sizeof(float) * p.d, s);
+        if (e == cudaSuccess && p.dwk) e = cudaMemsetAsync(p.dwk, 0, sizeof(float) * p.d, s);
+        return cuda_status(e, "weight gradient reset");
+    }
+    if (e != cudaSuccess) return cuda_status(e, "status reset");
+    return cuda_status(kda::launch_norm_rope(p, true, s), "norm and rotation backward launch");
 }
 
 }  // namespace
@@ -347,26 +350,34 @@ kda_status_t kda_linear_decode_step_slots(const void *q, const void *k, const vo
                   pool_size, device_status, o, N, H, d_k, d_v, reinterpret_cast<cudaStream_t>(stream));
 }
 
+#define KDA_ROPE_ARGS                                                                                                 \
+    p.dt = dtype; p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride;                                      \
+    p.positions = positions; p.table = rope_table; p.max_position = max_position; p.rot = rotary; p.layout = layout;   \
+    p.wq = q_weight; p.wk = k_weight; p.norm = norm; p.eps = eps; p.hq = H_q; p.hk = H_k; p.d = d;                     \
+    p.status = device_status
+
 kda_status_t kda_qk_norm_rope(const void *q, const void *k, kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
                               const int32_t *positions, const float *rope_table, int max_position, int rotary,
                               kda_rope_layout_t layout, const float *q_weight, const float *k_weight, kda_norm_t norm,
                               float eps, void *q_out, void *k_out, int64_t tokens, int H_q, int H_k, int d,
                               int32_t *device_status, kda_stream_t stream) {
     kda::NormRopeArgs p{};
-    p.dt = dtype; p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride;
-    p.positions = positions; p.table = rope_table; p.max_position = max_position; p.rot = rotary; p.layout = layout;
-    p.wq = q_weight; p.wk = k_weight; p.norm = norm; p.eps = eps;
-    p.yq = q_out; p.yk = k_out; p.hq = H_q; p.hk = H_k; p.d = d; p.status = device_status;
-    KDA_CHECK(norm_rope(p, tokens));
-    if (tokens > 0 && H_q > 0) KDA_CHECK(need(q_out, "q_out"));
-    if (tokens > 0 && H_k > 0) KDA_CHECK(need(k_out, "k_out"));
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (device_status) {
-        const cudaError_t e = cudaMemsetAsync(device_status, 0, sizeof(int32_t), s);
-        if (e != cudaSuccess) return cuda_status(e, "status reset");
-    }
-    if (tokens == 0 || H_q + H_k == 0) return ok();
-    return cuda_status(kda::launch_norm_rope(p, false, s), "norm and rotation launch");
+    KDA_ROPE_ARGS;
+    p.yq = q_out; p.yk = k_out;
+    return norm_rope_forward(p, tokens, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kda_status_t kda_qk_norm_rope_axes(const void *q, const void *k, kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                   const int32_t *positions, int axes, const uint8_t *pair_axis, const float *rope_table,
+                                   int max_position, int rotary, kda_rope_layout_t layout, const float *q_weight,
+                                   const float *k_weight, kda_norm_t norm, float eps, void *q_out, void *k_out,
+                                   int64_t tokens, int H_q, int H_k, int d, int32_t *device_status,
+                                   kda_stream_t stream) {
+    kda::NormRopeArgs p{};
+    KDA_ROPE_ARGS;
+    p.yq = q_out; p.yk = k_out;
+    KDA_CHECK(axes_of(p, pair_axis, axes));
+    return norm_rope_forward(p, tokens, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t kda_qk_norm_rope_backward_workspace_bytes(int d) {
@@ -381,35 +392,24 @@ kda_status_t kda_qk_norm_rope_backward(const void *q, const void *k, const void 
                                        float *dk_weight, int64_t tokens, int H_q, int H_k, int d, void *workspace,
                                        size_t workspace_bytes, int32_t *device_status, kda_stream_t stream) {
     kda::NormRopeArgs p{};
-    p.dt = dtype; p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride;
-    p.positions = positions; p.table = rope_table; p.max_position = max_position; p.rot = rotary; p.layout = layout;
-    p.wq = q_weight; p.wk = k_weight; p.norm = norm; p.eps = eps;
+    KDA_ROPE_ARGS;
     p.dyq = dq_out; p.dyk = dk_out; p.dxq = dq; p.dxk = dk; p.dwq = dq_weight; p.dwk = dk_weight;
-    p.hq = H_q; p.hk = H_k; p.d = d; p.status = device_status;
-    KDA_CHECK(norm_rope(p, tokens));
-    if (tokens > 0 && H_q > 0) {
-        KDA_CHECK(need(dq_out, "dq_out"));
-        KDA_CHECK(need(dq, "dq"));
-    }
-    if (tokens > 0 && H_k > 0) {
-        KDA_CHECK(need(dk_out, "dk_out"));
-        KDA_CHECK(need(dk, "dk"));
-    }
-    KDA_CHECK(maybe(dq_weight, "dq_weight", 4));
-    KDA_CHECK(maybe(dk_weight, "dk_weight", 4));
-    if (dq_weight || dk_weight) {
-        KDA_CHECK(workspace_ok(workspace, workspace_bytes, kda_qk_norm_rope_backward_workspace_bytes(d)));
-        p.partial = static_cast<float *>(workspace);
-    }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = device_status ? cudaMemsetAsync(device_status, 0, sizeof(int32_t), s) : cudaSuccess;
-    if (tokens == 0 || H_q + H_k == 0) {  // the sums over no rows
-        if (e == cudaSuccess && dq_weight) e = cudaMemsetAsync(dq_weight, 0, sizeof(float) * d, s);
-        if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, sizeof(float) * d, s);
-        return cuda_status(e, "weight gradient reset");
-    }
-    if (e != cudaSuccess) return cuda_status(e, "status reset");
-    return cuda_status(kda::launch_norm_rope(p, true, s), "norm and rotation backward launch");
+    return norm_rope_backward(p, tokens, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kda_status_t kda_qk_norm_rope_axes_backward(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                                            kda_dtype_t dtype, int64_t q_stride, int64_t k_stride,
+                                            const int32_t *positions, int axes, const uint8_t *pair_axis,
+                                            const float *rope_table, int max_position, int rotary,
+                                            kda_rope_layout_t layout, const float *q_weight, const float *k_weight,
+                                            kda_norm_t norm, float eps, void *dq, void *dk, float *dq_weight,
+                                            float *dk_weight, int64_t tokens, int H_q, int H_k, int d, void *workspace,
+                                            size_t workspace_bytes, int32_t *device_status, kda_stream_t stream) {
+    kda::NormRopeArgs p{};
+    KDA_ROPE_ARGS;
+    p.dyq = dq_out; p.dyk = dk_out; p.dxq = dq; p.dxk = dk; p.dwq = dq_weight; p.dwk = dk_weight;
+    KDA_CHECK(axes_of(p, pair_axis, axes));
+    return norm_rope_backward(p, tokens, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

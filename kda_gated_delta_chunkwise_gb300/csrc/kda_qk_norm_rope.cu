@@ -24,6 +24,7 @@
 // both weights' gradients 81.3 (5.0 TB/s, 74 %), the last sum (8-10 us on cold caches) included.
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
+#include "kda_rows.cuh"
 
 namespace kda {
 namespace {
@@ -32,53 +33,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPasses = 4;  // row groups of a warp in flight at once
 
-template <typename T> struct Vec {  // 16 bytes of a row: N channels, as loaded and as pairs
-    static constexpr int N = 16 / sizeof(T);
-    uint32_t raw[4];
-    __device__ __forceinline__ void zero() { raw[0] = raw[1] = raw[2] = raw[3] = 0u; }
-    // a plain load: the same kernel may write there
-    __device__ __forceinline__ void load(const T *p) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        raw[0] = x.x, raw[1] = x.y, raw[2] = x.z, raw[3] = x.w;
-    }
-    __device__ __forceinline__ void store(T *p) const {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(raw[0], raw[1], raw[2], raw[3]);
-    }
-    __device__ __forceinline__ F2 get(int i) const {  // channels 2 i, 2 i + 1
-        if constexpr (sizeof(T) == 2) return f2(__uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xffff0000u));
-        else return f2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
-    }
-    __device__ __forceinline__ void put(int i, F2 x) {
-        float lo, hi;
-        f2_get(x, lo, hi);
-        if constexpr (sizeof(T) == 2) {
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(raw[i]) : "f"(hi), "f"(lo));
-        } else {
-            raw[2 * i] = __float_as_uint(lo);
-            raw[2 * i + 1] = __float_as_uint(hi);
-        }
-    }
-};
-
-template <int LANES> __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-
-// From global or shared memory, 4 N-byte aligned.
-template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + e);
-            x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
-        }
-    } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        x[0] = v.x, x[1] = v.y;
-    }
-}
 // This lane's cosines and sines: element e of the lane's channels sits in
 // pair (channel mod rot/2) of the half layout, channel / 2 of the interleaved.
 // sn is signed for the element it multiplies into: the first of a pair takes
@@ -102,6 +56,75 @@ __device__ __forceinline__ void load_angles(const float *row, int c0, int rot, i
         float c[N / 2], t[N / 2];
         load_floats<N / 2>(row + c0 / 2, c);
         load_floats<N / 2>(row + h + c0 / 2, t);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+            cs[2 * e] = cs[2 * e + 1] = c[e];
+            sn[2 * e] = -t[e];
+            sn[2 * e + 1] = t[e];
+        }
+    }
+}
+
+// Positions of several axes: channel pair i turns by the table's row of its own
+// axis' position. Aligned groups of four pairs that share an axis are read with
+// one load (p.quads: all of them do, as with sections of a multiple of four
+// pairs), others pair by pair.
+__device__ __forceinline__ int pair_axis(const NormRopeArgs &p, int pair) {
+    return (int)(p.axis_bits[pair >> 5] >> (2 * (pair & 31))) & 3;
+}
+struct AxisPositions {
+    int at[kRopeAxes];
+    // `mine`: in lane a of the warp, axis a's
+    __device__ __forceinline__ explicit AxisPositions(int mine) {
+#pragma unroll
+        for (int a = 0; a < kRopeAxes; ++a) at[a] = __shfl_sync(0xffffffffu, mine, a);
+    }
+    __device__ __forceinline__ int of(int axis) const {
+        return axis < 2 ? (axis == 0 ? at[0] : at[1]) : (axis == 2 ? at[2] : at[3]);
+    }
+};
+// A token's positions, lane a of the warp axis a's (lanes behind the axes: axis 0's).
+__device__ __forceinline__ int axis_position(const NormRopeArgs &p, int64_t token) {
+    const int lane = threadIdx.x & 31;
+    return __ldg(p.positions + (lane < p.axes ? lane : 0) * p.tokens + token);
+}
+__device__ __forceinline__ bool all_in_table(const NormRopeArgs &p, int mine) {
+    return __all_sync(0xffffffffu, mine >= 0 && mine < p.max_position);
+}
+// N values of pairs i0 .. i0 + N - 1, from column `col` + pair of each pair's row
+template <int N>
+__device__ __forceinline__ void load_pairs(const NormRopeArgs &p, const AxisPositions &pos, int i0, int col, float *x) {
+    constexpr int STEP = N < 4 ? N : 4;
+    if (p.quads) {
+#pragma unroll
+        for (int e = 0; e < N; e += STEP)
+            load_floats<STEP>(p.table + (int64_t)pos.of(pair_axis(p, i0 + e)) * p.rot + col + i0 + e, x + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] = __ldg(p.table + (int64_t)pos.of(pair_axis(p, i0 + e)) * p.rot + col + i0 + e);
+    }
+}
+// load_angles of a row that is put together from every pair's axis.
+template <int N>
+__device__ __forceinline__ void load_axis_angles(const NormRopeArgs &p, const AxisPositions &pos, int c0, float (&cs)[N],
+                                                 float (&sn)[N]) {
+    const int h = p.rot / 2;
+    if (c0 >= p.rot) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) cs[e] = 1.f, sn[e] = 0.f;
+    } else if (p.layout == KDA_ROPE_HALF) {
+        const int i0 = c0 < h ? c0 : c0 - h;
+        load_pairs<N>(p, pos, i0, 0, cs);
+        load_pairs<N>(p, pos, i0, h, sn);
+        if (c0 < h) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) sn[e] = -sn[e];
+        }
+    } else {
+        float c[N / 2], t[N / 2];
+        load_pairs<N / 2>(p, pos, c0 / 2, 0, c);
+        load_pairs<N / 2>(p, pos, c0 / 2, h, t);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
             cs[2 * e] = cs[2 * e + 1] = c[e];
@@ -164,11 +187,6 @@ __device__ __forceinline__ void load_weights(const float *w, int layout, int rot
     }
 }
 
-// rsqrtf is within 2 ulp
-__device__ __forceinline__ float rnorm(float ss, int norm, float inv_d, float eps) {
-    return norm == KDA_NORM_NONE ? 1.f : rsqrtf((norm == KDA_NORM_RMS ? ss * inv_d : ss) + eps);
-}
-
 // A warp's unit: kPasses * ROWS consecutive rows (heads) of one token, taken
 // from q's heads or from k's (never both, so that a weight is one register set).
 template <typename T, int D> constexpr int unit_rows() { return kPasses * (32 / (D / Vec<T>::N)); }
@@ -178,7 +196,7 @@ struct Parts {
     int64_t tokens;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool AXES>
 __global__ void __launch_bounds__(kThreads)
 kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
     constexpr int N = Vec<T>::N, LANES = D / N, ROWS = 32 / LANES;
@@ -191,7 +209,7 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
     const int first = (is_q ? part : part - parts.q) * unit_rows<T, D>(), heads = is_q ? p.hq : p.hk;
     const T *x = is_q ? (const T *)p.q + token * p.q_stride : (const T *)p.k + token * p.k_stride;
     T *y = is_q ? (T *)p.yq + token * (int64_t)p.hq * D : (T *)p.yk + token * (int64_t)p.hk * D;
-    const int pos = p.rot > 0 ? __ldg(p.positions + token) : 0;
+    const int pos = AXES ? axis_position(p, token) : p.rot > 0 ? __ldg(p.positions + token) : 0;
     Vec<T> v[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -203,7 +221,13 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
     {
         float wo[N], wp[N], cs[N], sn[N];
         load_weights<N>(is_q ? p.wq : p.wk, p.layout, p.rot, g, wo, wp);
-        if (p.rot > 0) {
+        if constexpr (AXES) {
+            if (!all_in_table(p, pos)) {
+                if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
+                return;
+            }
+            load_axis_angles<N>(p, AxisPositions(pos), g.c0, cs, sn);
+        } else if (p.rot > 0) {
             if (pos < 0 || pos >= p.max_position) {  // uniform over the warp: the token's rows are left as they are
                 if ((threadIdx.x & 31) == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_POSITION);
                 return;
@@ -247,11 +271,7 @@ constexpr int kStages = 3;
 constexpr int kUnitBytes = 2 * kPasses * 512 + 512;  // x, dy, table row
 constexpr int kBwdSmem = kWarps * kStages * kUnitBytes;
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {  // zeros where not there
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-template <typename T, int D>
+template <typename T, int D, bool AXES>
 __global__ void __launch_bounds__(kThreads, 2)
 kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
     constexpr int N = Vec<T>::N, LANES = D / N, ROWS = 32 / LANES;
@@ -275,7 +295,11 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
         load_weights<N>(is_q ? p.wq : p.wk, p.layout, p.rot, g, wo, wp);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) acc[e] = f2(0.f, 0.f), wv[e] = f2(wo[2 * e], wo[2 * e + 1]);
-        auto position = [&](int64_t u) { return p.rot > 0 && u < units ? __ldg(p.positions + by.div((int)u)) : 0; };
+        // AXES: lane a's is axis a's, and so is what it says of the table
+        auto position = [&](int64_t u) {
+            if constexpr (AXES) return u < units ? axis_position(p, by.div((int)u)) : 0;
+            return p.rot > 0 && u < units ? __ldg(p.positions + by.div((int)u)) : 0;
+        };
         auto in_table = [&](int pos) { return pos >= 0 && pos < p.max_position; };
         auto fetch = [&](int64_t u, int pos, int stage) {  // one group of copies, empty past the last unit
             if (u < units) {
@@ -291,7 +315,22 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
                     copy16(dst + i * 512, x + at, there);
                     copy16(dst + (kPasses + i) * 512, dy + at, there);
                 }
-                if (4 * lane < p.rot)
+                if constexpr (AXES) {  // the row is put together here
+                    const bool good = all_in_table(p, pos);
+                    const AxisPositions at(good ? pos : 0);
+                    if (4 * lane < p.rot) {
+                        const int pair = 4 * lane < p.rot / 2 ? 4 * lane : 4 * lane - p.rot / 2;
+                        const uint32_t row = dst + 2 * kPasses * 512;
+                        if (p.quads) {
+                            copy16(row, p.table + (int64_t)at.of(pair_axis(p, pair)) * p.rot + 4 * lane, good);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                copy4(row + 4 * e,
+                                      p.table + (int64_t)at.of(pair_axis(p, pair + e)) * p.rot + 4 * lane + e, good);
+                        }
+                    }
+                } else if (4 * lane < p.rot)
                     copy16(dst + 2 * kPasses * 512, p.table + (in_table(pos) ? (int64_t)pos * p.rot + 4 * lane : 0),
                            in_table(pos));
             }
@@ -312,7 +351,7 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
             const unsigned char *buf = ring + stage * kUnitBytes;
-            const bool good = p.rot == 0 || in_table(pos[0]);
+            const bool good = AXES ? all_in_table(p, pos[0]) : p.rot == 0 || in_table(pos[0]);
 #pragma unroll
             for (int i = 0; i + 1 < kStages; ++i) pos[i] = pos[i + 1];
             pos[kStages - 1] = ahead;
@@ -409,7 +448,7 @@ kda_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, floa
     if (lane == 0 && dst) dst[o % d] = a;
 }
 
-template <typename T, int D> cudaError_t launch(const NormRopeArgs &p, bool back, cudaStream_t s) {
+template <typename T, int D, bool AXES> cudaError_t launch(const NormRopeArgs &p, bool back, cudaStream_t s) {
     constexpr int R = unit_rows<T, D>();
     Parts parts;
     parts.q = (p.hq + R - 1) / R;
@@ -421,14 +460,14 @@ template <typename T, int D> cudaError_t launch(const NormRopeArgs &p, bool back
     const int64_t units = p.tokens * (parts.q + parts.k), blocks = (units + kWarps - 1) / kWarps;
     if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (!back) {
-        kda_qk_norm_rope_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, (int)units);
+        kda_qk_norm_rope_kernel<T, D, AXES><<<(unsigned)blocks, kThreads, 0, s>>>(p, parts, (int)units);
         return cudaGetLastError();
     }
     const int grid = (int)(blocks < kNormRopeBwdBlocks ? blocks : kNormRopeBwdBlocks);
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(kda_qk_norm_rope_bwd_kernel<T, D>, kBwdSmem, allowed);
+    cudaError_t e = allow_smem(kda_qk_norm_rope_bwd_kernel<T, D, AXES>, kBwdSmem, allowed);
     if (e != cudaSuccess) return e;
-    kda_qk_norm_rope_bwd_kernel<T, D><<<grid, kThreads, kBwdSmem, s>>>(p, parts);
+    kda_qk_norm_rope_bwd_kernel<T, D, AXES><<<grid, kThreads, kBwdSmem, s>>>(p, parts);
     e = cudaGetLastError();
     if (e != cudaSuccess || !p.partial) return e;
     kda_weight_sum_kernel<<<(2 * D + kWarps - 1) / kWarps, kThreads, 0, s>>>(p.partial, grid, D, p.dwq, p.dwk);
@@ -438,9 +477,13 @@ template <typename T, int D> cudaError_t launch(const NormRopeArgs &p, bool back
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs &p, bool back, cudaStream_t s) {
-    if (p.dt == KDA_BF16)
-        return p.d == 128 ? launch<__nv_bfloat16, 128>(p, back, s) : launch<__nv_bfloat16, 64>(p, back, s);
-    return p.d == 128 ? launch<float, 128>(p, back, s) : launch<float, 64>(p, back, s);
+    auto of = [&](auto axes) {
+        constexpr bool AXES = decltype(axes)::value;
+        if (p.dt == KDA_BF16)
+            return p.d == 128 ? launch<__nv_bfloat16, 128, AXES>(p, back, s) : launch<__nv_bfloat16, 64, AXES>(p, back, s);
+        return p.d == 128 ? launch<float, 128, AXES>(p, back, s) : launch<float, 64, AXES>(p, back, s);
+    };
+    return p.axes > 0 ? of(std::true_type{}) : of(std::false_type{});
 }
 
 }  // namespace kda

@@ -1,0 +1,70 @@
+// Pieces shared by the kernels that hold a row of channels in a few lanes: the
+// norms with rotary positions, with a gate, and of the residual stream.
+#pragma once
+
+#include "kda_internal.cuh"
+#include "kda_linear.cuh"
+
+namespace kda {
+
+template <typename T> struct Vec {  // 16 bytes of a row: N channels, as loaded and as pairs
+    static constexpr int N = 16 / sizeof(T);
+    uint32_t raw[4];
+    __device__ __forceinline__ void zero() { raw[0] = raw[1] = raw[2] = raw[3] = 0u; }
+    // a plain load: the same kernel may write there
+    __device__ __forceinline__ void load(const T *p) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        raw[0] = x.x, raw[1] = x.y, raw[2] = x.z, raw[3] = x.w;
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(raw[0], raw[1], raw[2], raw[3]);
+    }
+    __device__ __forceinline__ F2 get(int i) const {  // channels 2 i, 2 i + 1
+        if constexpr (sizeof(T) == 2) return f2(__uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xffff0000u));
+        else return f2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+    }
+    __device__ __forceinline__ void put(int i, F2 x) {
+        float lo, hi;
+        f2_get(x, lo, hi);
+        if constexpr (sizeof(T) == 2) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(raw[i]) : "f"(hi), "f"(lo));
+        } else {
+            raw[2 * i] = __float_as_uint(lo);
+            raw[2 * i + 1] = __float_as_uint(hi);
+        }
+    }
+};
+
+template <int LANES> __device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// From global or shared memory, 4 N-byte aligned.
+template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + e);
+            x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+        }
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x, x[1] = v.y;
+    }
+}
+// rsqrtf is within 2 ulp
+__device__ __forceinline__ float rnorm(float ss, int norm, float inv_d, float eps) {
+    return norm == KDA_NORM_NONE ? 1.f : rsqrtf((norm == KDA_NORM_RMS ? ss * inv_d : ss) + eps);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {  // zeros where not there
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+}  // namespace kda

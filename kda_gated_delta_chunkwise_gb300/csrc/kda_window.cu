@@ -1,0 +1,625 @@
+// Attention with a sliding window and sinks, and its gradients, for any
+// supported type and size; the tile table of packed batches.
+//
+//   s_ij = scale q_i . k_j over the j that i sees,  lse_i = log sum_j e^{s_ij}
+//   p_ij = e^{s_ij - lse_i},  o_i = sum_j p_ij v_j
+//   D_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - D_i)
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+// with dk and dv summed over the query heads of a key head, in their order.
+//
+// One CTA takes 64 rows (queries, or keys for dk and dv), a warp 16 of them, and
+// walks tiles of 32 columns in shared memory with the running maximum and sum of
+// the softmax in registers. The products run on mma.sync tf32; an fp32 operand is
+// split in two tf32 parts, three products for each, and every four steps are
+// summed from zero and then added in fp32, because the tensor core truncates its
+// accumulations. bf16 values are exact in tf32; the weights p and ds of a bf16
+// call keep 11 bits, against the 8 of its result.
+#include <math_constants.h>
+
+#include "kda_window.cuh"
+
+namespace kda {
+namespace {
+
+// ================================================================ packed batches: the table of tiles
+constexpr int kPrepThreads = 1024;
+__global__ void __launch_bounds__(kPrepThreads)
+win_tiles_kernel(const int32_t *cu, int N, int T_total, int ntiles, int4 *tiles, int32_t *seq_tile, int32_t *user_status) {
+    __shared__ int bad;
+    __shared__ int wsum[kPrepThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = (cu[0] != 0 || cu[N] != T_total) ? 1 : 0;
+    __syncthreads();
+    for (int i = tid; i < N; i += kPrepThreads)
+        if (cu[i + 1] < cu[i] || cu[i] < 0 || cu[i + 1] > T_total) atomicOr(&bad, 1);
+    __syncthreads();
+    const bool b = bad != 0;
+    if (tid == 0) {
+        if (user_status) *user_status = b ? KDA_DEV_BAD_CU_SEQLENS : KDA_DEV_OK;
+        seq_tile[0] = 0;
+    }
+    int base = 0;
+    for (int i0 = 0; i0 < N; i0 += kPrepThreads) {
+        const int i = i0 + tid;
+        int x = i < N && !b ? (cu[i + 1] - cu[i] + kWinTile - 1) / kWinTile : 0;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) wsum[warp] = x;
+        __syncthreads();
+        int before = base, all = base;
+        for (int w = 0; w < kPrepThreads / 32; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+        if (i < N) seq_tile[i + 1] = before + x;
+        base = all;
+        __syncthreads();
+    }
+    __threadfence_block();
+    __syncthreads();
+    for (int j = tid; j < ntiles; j += kPrepThreads) {
+        int4 e = make_int4(0, 0, 0, 0);
+        if (j < base) {
+            int lo = 0, hi = N - 1;  // the last sequence whose first tile is <= j
+            while (lo < hi) {
+                const int m = (lo + hi + 1) >> 1;
+                if (seq_tile[m] <= j) lo = m;
+                else hi = m - 1;
+            }
+            e = make_int4(lo, cu[lo], cu[lo + 1] - cu[lo], (j - seq_tile[lo]) * kWinTile);
+        }
+        tiles[j] = e;
+    }
+}
+
+// ================================================================ products
+__device__ __forceinline__ uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A fragment: four values, in one or two tf32 parts.
+template <bool SPLIT> struct Frag {
+    uint32_t hi[4], lo[4];
+    __device__ __forceinline__ void set(int i, float x) {
+        hi[i] = tf32(x);
+        if (SPLIT) lo[i] = tf32(x - __uint_as_float(hi[i]));
+    }
+};
+template <bool SPLIT> __device__ __forceinline__ void product(float (&d)[4], const Frag<SPLIT> &a, float x0, float x1) {
+    const uint32_t h0 = tf32(x0), h1 = tf32(x1);
+    if (SPLIT) {
+        mma(d, a.lo, h0, h1);
+        mma(d, a.hi, tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
+    }
+    mma(d, a.hi, h0, h1);
+}
+
+constexpr int NT = 128, ROWS = 64, COLS = 32;
+
+// Rows of a tile in shared memory, fp32, D + 4 apart (a fragment's reads then
+// touch every bank once). Rows past `rows` are zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t stride, int rows, int want) {
+    constexpr int N = 16 / sizeof(T), PER = D / N;
+    for (int i = threadIdx.x; i < want * PER; i += NT) {
+        const int r = i / PER, c = (i % PER) * N;
+        float x[N];
+        if (r < rows) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + r * stride + c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                x[e] = sizeof(T) == 4 ? __uint_as_float(w[e * 4 / N])
+                                      : __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(dst + r * (D + 4) + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    }
+}
+
+// acc[nb] = the 16 x 32 products of this warp's rows of `a` with the rows of `b`.
+template <bool SPLIT, int D>
+__device__ __forceinline__ void rows_by_rows(float (&acc)[COLS / 8][4], const float *a, const float *b) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+#pragma unroll
+    for (int nb = 0; nb < COLS / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < D; k0 += 32) {
+        float d[COLS / 8][4];
+#pragma unroll
+        for (int nb = 0; nb < COLS / 8; ++nb) d[nb][0] = d[nb][1] = d[nb][2] = d[nb][3] = 0.f;
+#pragma unroll
+        for (int k = k0; k < k0 + 32; k += 8) {
+            Frag<SPLIT> f;
+            f.set(0, a[r0 * (D + 4) + k + t]);
+            f.set(1, a[(r0 + 8) * (D + 4) + k + t]);
+            f.set(2, a[r0 * (D + 4) + k + t + 4]);
+            f.set(3, a[(r0 + 8) * (D + 4) + k + t + 4]);
+#pragma unroll
+            for (int nb = 0; nb < COLS / 8; ++nb)
+                product<SPLIT>(d[nb], f, b[(nb * 8 + g) * (D + 4) + k + t], b[(nb * 8 + g) * (D + 4) + k + t + 4]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < COLS / 8; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nb][e] += d[nb][e];
+        }
+    }
+}
+// acc[nb] += w (16 x 32, as rows_by_rows leaves it) times the rows of b. Columns
+// 2 t and 2 t + 1 of w, which this lane holds, stand for k = t and t + 4 of the
+// product: a sum does not mind the order of its terms.
+template <bool SPLIT, int D>
+__device__ __forceinline__ void weights_by_rows(float (&acc)[D / 8][4], const float (&w)[COLS / 8][4], const float *b) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    Frag<SPLIT> f[COLS / 8];
+#pragma unroll
+    for (int kb = 0; kb < COLS / 8; ++kb) {
+        f[kb].set(0, w[kb][0]);
+        f[kb].set(1, w[kb][2]);
+        f[kb].set(2, w[kb][1]);
+        f[kb].set(3, w[kb][3]);
+    }
+#pragma unroll
+    for (int nb = 0; nb < D / 8; ++nb) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < COLS / 8; ++kb)
+            product<SPLIT>(d, f[kb], b[(kb * 8 + 2 * t) * (D + 4) + nb * 8 + g],
+                           b[(kb * 8 + 2 * t + 1) * (D + 4) + nb * 8 + g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nb][e] += d[e];
+    }
+}
+
+// ================================================================ the general kernels
+struct WinParams {
+    WinGeom geo;
+    const void *q, *k, *v, *out, *d_o;
+    int64_t q_stride, k_stride, v_stride;
+    float scale;
+    void *o, *dq, *dk, *dv;
+    float *lse, *delta;       // [tokens][hq]
+    float *part, *sums;       // far gradients of the sinks: [ntiles][hk][2][sinks][d], [N][hk][2][sinks][d]
+};
+
+// Whether i sees j, among the near pairs or among the far ones.
+__device__ __forceinline__ bool sees(int i, int j, int window, int sinks, bool far) {
+    return far ? j < sinks && i - j >= window : j <= i && i - j < window;
+}
+// Token i sees itself alone: its weight is one whatever its score, so ds is zero.
+__device__ __forceinline__ bool alone(int i, int window, int sinks) { return i == 0 || (window == 1 && sinks == 0); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(NT)
+win_forward_kernel(WinParams p) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sk = sq + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    const WinGeom &geo = p.geo;
+    const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
+    const WinTile tile = win_tile(geo, at >> 2);
+    const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
+    if (rows <= 0) return;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
+    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
+    load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows, ROWS);
+    float acc[D / 8][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int nb = 0; nb < D / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+    auto walk = [&](int from, int to, bool far) {
+        for (int j0 = from; j0 < to; j0 += COLS) {
+            __syncthreads();
+            const int cols = min(COLS, to - j0);
+            load_tile<T, D>(sk, kb + (int64_t)j0 * p.k_stride, p.k_stride, cols, COLS);
+            load_tile<T, D>(sv, vb + (int64_t)j0 * p.v_stride, p.v_stride, cols, COLS);
+            __syncthreads();
+            float s[COLS / 8][4], top[2] = {m[0], m[1]};
+            rows_by_rows<SPLIT, D>(s, sq, sk);
+#pragma unroll
+            for (int nb = 0; nb < COLS / 8; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
+                    s[nb][e] = j < to && sees(i, j, geo.window, geo.sinks, far) ? s[nb][e] * p.scale : -CUDART_INF_F;
+                    top[e >> 1] = fmaxf(top[e >> 1], s[nb][e]);
+                }
+            }
+            float keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                keep[e] = top[e] == -CUDART_INF_F ? 1.f : expf(m[e] - top[e]);  // a row may see nothing of a tile
+                m[e] = top[e];
+                l[e] *= keep[e];
+            }
+#pragma unroll
+            for (int nb = 0; nb < COLS / 8; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[nb][e] = s[nb][e] == -CUDART_INF_F ? 0.f : expf(s[nb][e] - m[e >> 1]);
+                    l[e >> 1] += s[nb][e];
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < D / 8; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nb][e] *= keep[e >> 1];
+            }
+            weights_by_rows<SPLIT, D>(acc, s, sv);
+        }
+    };
+    if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
+    walk(max(0, i0 - geo.window + 1), i0 + rows, false);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = r0 + e * 8;
+        if (r >= rows) continue;
+        const int64_t row = (int64_t)(tile.start + i0 + r) * geo.hq + h;
+        T *o = (T *)p.o + row * D;
+        const float f = 1.f / l[e];
+#pragma unroll
+        for (int nb = 0; nb < D / 8; ++nb) {
+            o[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * f);
+            o[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * f);
+        }
+        if (p.lse && t == 0) p.lse[row] = m[e] + logf(l[e]);
+    }
+}
+
+// D_i = do_i . o_i, a warp a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+win_delta_kernel(const T *o, const T *d_o, float *delta, int64_t rows) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < D; c += 32) s = fmaf(to_f32(o[row * D + c + lane]), to_f32(d_o[row * D + c + lane]), s);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) delta[row] = s;
+}
+
+// dq; or, with DELTA, D_i once more as sum_j p_ij dp_ij, for tokens that see few
+// others: all of a narrow window's (few_keys), else the first 64 of every
+// sequence. There a weight may be close to one, ds = p (dp - D) far smaller than
+// dp, and the rounding of the stored bf16 o, which do . o takes into D, would be
+// seen in dq and dk (1.2e-2 of dq for two tokens).
+__host__ __device__ __forceinline__ bool few_keys(int window, int sinks) { return window + sinks <= 64; }
+
+template <typename T, int D, bool DELTA>
+__global__ void __launch_bounds__(NT)
+win_dq_kernel(WinParams p) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    const WinGeom &geo = p.geo;
+    const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
+    const bool firsts = DELTA && !few_keys(geo.window, geo.sinks);  // `at` counts sequences
+    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) return;
+    const WinTile tile = win_tile(geo, !firsts ? at >> 2 : geo.tiles ? geo.seq_tile[at] : at * geo.per_seq);
+    const int i0 = firsts ? 0 : tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
+    if (rows <= 0) return;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
+    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
+    const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h;
+    load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows, ROWS);
+    load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, rows, ROWS);
+    float acc[D / 8][4], lse[2], delta[2];
+#pragma unroll
+    for (int nb = 0; nb < D / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const bool there = r0 + e * 8 < rows;
+        lse[e] = there ? p.lse[row0 + (int64_t)(r0 + e * 8) * geo.hq] : 0.f;
+        delta[e] = there && !DELTA ? p.delta[row0 + (int64_t)(r0 + e * 8) * geo.hq] : 0.f;
+    }
+    float all[2] = {0.f, 0.f};  // DELTA: the sum of the weights, one but for rounding
+    auto walk = [&](int from, int to, bool far) {
+        for (int j0 = from; j0 < to; j0 += COLS) {
+            __syncthreads();
+            const int cols = min(COLS, to - j0);
+            load_tile<T, D>(sk, kb + (int64_t)j0 * p.k_stride, p.k_stride, cols, COLS);
+            load_tile<T, D>(sv, vb + (int64_t)j0 * p.v_stride, p.v_stride, cols, COLS);
+            __syncthreads();
+            float s[COLS / 8][4], dp[COLS / 8][4];
+            rows_by_rows<SPLIT, D>(s, sq, sk);
+            rows_by_rows<SPLIT, D>(dp, sd, sv);
+#pragma unroll
+            for (int nb = 0; nb < COLS / 8; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
+                    const bool on = j < to && sees(i, j, geo.window, geo.sinks, far) && !alone(i, geo.window, geo.sinks);
+                    s[nb][e] = on ? expf(s[nb][e] * p.scale - lse[e >> 1]) : 0.f;
+                    if (DELTA) {
+                        all[e >> 1] += s[nb][e];
+                        delta[e >> 1] = fmaf(s[nb][e], dp[nb][e], delta[e >> 1]);
+                    } else {
+                        s[nb][e] *= dp[nb][e] - delta[e >> 1];
+                    }
+                }
+            }
+            if (!DELTA) weights_by_rows<SPLIT, D>(acc, s, sk);
+        }
+    };
+    if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
+    walk(max(0, i0 - geo.window + 1), i0 + rows, false);
+    if (DELTA) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int off = 1; off < 4; off *= 2) {
+                all[e] += __shfl_xor_sync(0xffffffffu, all[e], off);
+                delta[e] += __shfl_xor_sync(0xffffffffu, delta[e], off);
+            }
+            if (t == 0 && r0 + e * 8 < rows && all[e] > 0.f)  // not of a token that sees itself alone
+                p.delta[row0 + (int64_t)(r0 + e * 8) * geo.hq] = delta[e] / all[e];
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + e * 8;
+        if (r >= rows) continue;
+        T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
+#pragma unroll
+        for (int nb = 0; nb < D / 8; ++nb) {
+            dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
+            dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
+        }
+    }
+}
+
+// dk and dv of 64 keys. FAR: of the sinks, from the far pairs with one tile of
+// 256 queries; the sums go to `part` in fp32.
+template <typename T, int D, bool FAR>
+__global__ void __launch_bounds__(NT)
+win_dkv_kernel(WinParams p) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sk = sm, *sv = sk + ROWS * (D + 4), *sq = sv + ROWS * (D + 4), *sd = sq + COLS * (D + 4);
+    __shared__ float slse[COLS], sdelta[COLS];
+    const WinGeom &geo = p.geo;
+    const int item = blockIdx.x, at = geo.by_hk.div(item), hk = item - at * geo.hk;
+    const WinTile tile = win_tile(geo, FAR ? at >> 1 : at >> 2);
+    const int j0 = FAR ? (at & 1) * ROWS : tile.first + (at & 3) * ROWS;
+    const int rows = min(ROWS, (FAR ? min(geo.sinks, tile.len) : tile.len) - j0);
+    if (rows <= 0) return;
+    const int from = FAR ? max(tile.first, j0 + geo.window) : j0;
+    const int to = FAR ? min(tile.first + kWinTile, tile.len)
+                       : (int)min((int64_t)tile.len, (int64_t)j0 + rows - 1 + geo.window);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+    load_tile<T, D>(sk, (const T *)p.k + (int64_t)(tile.start + j0) * p.k_stride + hk * D, p.k_stride, rows, ROWS);
+    load_tile<T, D>(sv, (const T *)p.v + (int64_t)(tile.start + j0) * p.v_stride + hk * D, p.v_stride, rows, ROWS);
+    float ak[D / 8][4], av[D / 8][4];
+#pragma unroll
+    for (int nb = 0; nb < D / 8; ++nb) {
+        ak[nb][0] = ak[nb][1] = ak[nb][2] = ak[nb][3] = 0.f;
+        av[nb][0] = av[nb][1] = av[nb][2] = av[nb][3] = 0.f;
+    }
+    for (int h = hk * geo.group; h < (hk + 1) * geo.group; ++h) {
+        for (int i0 = from; i0 < to; i0 += COLS) {
+            __syncthreads();
+            const int cols = min(COLS, to - i0);
+            const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h;
+            load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, cols, COLS);
+            load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, cols, COLS);
+            if (threadIdx.x < COLS) {
+                const bool there = threadIdx.x < cols;
+                slse[threadIdx.x] = there ? p.lse[row0 + (int64_t)threadIdx.x * geo.hq] : 0.f;
+                sdelta[threadIdx.x] = there ? p.delta[row0 + (int64_t)threadIdx.x * geo.hq] : 0.f;
+            }
+            __syncthreads();
+            float s[COLS / 8][4], dp[COLS / 8][4];
+            rows_by_rows<SPLIT, D>(s, sk, sq);
+            rows_by_rows<SPLIT, D>(dp, sv, sd);
+#pragma unroll
+            for (int nb = 0; nb < COLS / 8; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + r0 + (e >> 1) * 8, c = nb * 8 + 2 * t + (e & 1), i = i0 + c;
+                    const bool on = r0 + (e >> 1) * 8 < rows && i < to && sees(i, j, geo.window, geo.sinks, FAR);
+                    s[nb][e] = on ? expf(s[nb][e] * p.scale - slse[c]) : 0.f;
+                    dp[nb][e] = on && !alone(i, geo.window, geo.sinks) ? s[nb][e] * (dp[nb][e] - sdelta[c]) : 0.f;
+                }
+            }
+            weights_by_rows<SPLIT, D>(av, s, sd);
+            weights_by_rows<SPLIT, D>(ak, dp, sq);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + e * 8, j = j0 + r;
+        if (r >= rows) continue;
+        if constexpr (FAR) {
+            float *dk = p.part + (((int64_t)(at >> 1) * geo.hk + hk) * 2 * geo.sinks + j) * D;
+            float *dv = dk + (int64_t)geo.sinks * D;
+#pragma unroll
+            for (int nb = 0; nb < D / 8; ++nb) {
+                *reinterpret_cast<float2 *>(dk + nb * 8 + 2 * t) = make_float2(ak[nb][2 * e] * p.scale, ak[nb][2 * e + 1] * p.scale);
+                *reinterpret_cast<float2 *>(dv + nb * 8 + 2 * t) = make_float2(av[nb][2 * e], av[nb][2 * e + 1]);
+            }
+        } else {
+            const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D;
+            const bool sink = p.sums && j < geo.sinks;
+            const float *fk = p.sums + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D;
+            const float *fv = fk + (int64_t)geo.sinks * D;
+#pragma unroll
+            for (int nb = 0; nb < D / 8; ++nb) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int c = nb * 8 + 2 * t + u;
+                    ((T *)p.dk)[row + c] = from_f32<T>(ak[nb][2 * e + u] * p.scale + (sink ? fk[c] : 0.f));
+                    ((T *)p.dv)[row + c] = from_f32<T>(av[nb][2 * e + u] + (sink ? fv[c] : 0.f));
+                }
+            }
+        }
+    }
+}
+
+// The far gradients of a sequence's sinks: its tiles' parts added in order,
+// lanes over the channels, eight groups of threads over the tiles.
+__global__ void __launch_bounds__(256)
+win_far_sum_kernel(WinGeom geo, const float *part, float *sums, int d) {
+    __shared__ float red[8][33];
+    const int c = blockIdx.y * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;  // c: of [2][sinks][d]
+    const int nh = blockIdx.x, n = geo.by_hk.div(nh), hk = nh - n * geo.hk;
+    const int64_t per = 2ll * geo.sinks * d;
+    int first, last;
+    if (geo.tiles) first = geo.seq_tile[n], last = geo.seq_tile[n + 1];
+    else first = n * geo.per_seq, last = first + geo.per_seq;
+    float a = 0.f;
+    const int sink = c / d % geo.sinks;  // behind a short sequence's end there is none, and no part was written
+    const int len = geo.tiles && first < last ? geo.tiles[first].z : geo.T;
+    if (c < per && sink < len) {
+#pragma unroll 4
+        for (int k = first + group; k < last; k += 8) a += part[((int64_t)k * geo.hk + hk) * per + c];
+    }
+    red[group][threadIdx.x & 31] = a;
+    __syncthreads();
+    if (group == 0 && c < per) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) a += red[k][threadIdx.x];
+        sums[(int64_t)nh * per + c] = a;
+    }
+}
+
+// ================================================================ host side
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct WinPlan {
+    WinGeom geo;
+    int4 *tiles;
+    int32_t *seq_tile;
+    float *delta, *part, *sums;
+    size_t bytes;
+};
+WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks, bool packed, bool back, void *ws) {
+    WinPlan p{};
+    WinGeom &g = p.geo;
+    g.N = N, g.T = (int)T, g.hq = hq, g.hk = hk, g.group = hq / hk;
+    g.window = window, g.sinks = sinks;
+    g.tokens = packed ? T : (int64_t)N * T;
+    g.per_seq = (int)((T + kWinTile - 1) / kWinTile);
+    g.ntiles = packed ? (int)(T / kWinTile) + N : N * g.per_seq;
+    g.by_seq = FastDiv(g.per_seq > 0 ? g.per_seq : 1);
+    g.by_hq = FastDiv(hq), g.by_hk = FastDiv(hk);
+    char *base = static_cast<char *>(ws);
+    auto take = [&](size_t n) {
+        char *at = base ? base + p.bytes : nullptr;
+        p.bytes += round256(n);
+        return at;
+    };
+    if (packed) {
+        p.tiles = reinterpret_cast<int4 *>(take(sizeof(int4) * (size_t)g.ntiles));
+        p.seq_tile = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * ((size_t)N + 1)));
+        g.tiles = p.tiles, g.seq_tile = p.seq_tile;
+    }
+    if (back) {
+        p.delta = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
+        if (sinks > 0) {
+            p.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)g.ntiles * hk * sinks * d));
+            p.sums = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)N * hk * sinks * d));
+        }
+    }
+    return p;
+}
+
+#define KDA_TRY(x)                             \
+    do {                                       \
+        const cudaError_t e_ = (x);            \
+        if (e_ != cudaSuccess) return e_;      \
+    } while (0)
+
+cudaError_t prepare_tiles(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
+    if (!a.cu_seqlens) return cudaSuccess;
+    win_tiles_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, p.geo.ntiles, p.tiles, p.seq_tile, a.status);
+    return cudaGetLastError();
+}
+WinParams params(const WinPlan &p, const WinArgs &a) {
+    WinParams w{};
+    w.geo = p.geo;
+    w.q = a.q, w.k = a.k, w.v = a.v, w.out = a.out, w.d_o = a.d_o;
+    w.q_stride = a.q_stride, w.k_stride = a.k_stride, w.v_stride = a.v_stride;
+    w.scale = a.scale;
+    w.o = a.o, w.dq = a.dq, w.dk = a.dk, w.dv = a.dv;
+    w.lse = a.lse, w.delta = p.delta, w.part = p.part, w.sums = p.sums;
+    return w;
+}
+template <typename... P>
+cudaError_t run(void (*kernel)(P...), std::atomic<uint64_t> &allowed, unsigned grid, size_t smem, cudaStream_t s, P... args) {
+    KDA_TRY(allow_smem(kernel, smem, allowed));
+    kernel<<<grid, NT, smem, s>>>(args...);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> allowed{0};
+    constexpr size_t smem = (ROWS + 2 * COLS) * (D + 4) * sizeof(float);
+    return run(win_forward_kernel<T, D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, params(p, a));
+}
+
+template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> allowed[4];
+    constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(float);
+    const WinParams w = params(p, a);
+    const int64_t rows = p.geo.tokens * a.hq;
+    win_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T *)a.out, (const T *)a.d_o, p.delta, rows);
+    KDA_TRY(cudaGetLastError());
+    if (sizeof(T) == 2) {
+        const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
+        KDA_TRY(run(win_dq_kernel<T, D, true>, allowed[3], (unsigned)(blocks * a.hq), smem, s, w));
+    }
+    if (a.sinks > 0) {
+        KDA_TRY(run(win_dkv_kernel<T, D, true>, allowed[0], (unsigned)(p.geo.ntiles * 2 * a.hk), smem, s, w));
+        win_far_sum_kernel<<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(p.geo, p.part, p.sums, D);
+        KDA_TRY(cudaGetLastError());
+    }
+    KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
+    return run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w);
+}
+
+}  // namespace
+
+size_t window_workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, bool packed, bool back) {
+    return make_plan(N, T, hq, hk, d, 1, sinks, packed, back, nullptr).bytes;
+}
+
+cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
+    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, false, a.workspace);
+    KDA_TRY(prepare_tiles(p, a, s));
+    if (p.geo.tokens == 0) return cudaSuccess;
+    if (a.dt == KDA_BF16) return a.d == 128 ? forward<__nv_bfloat16, 128>(p, a, s) : forward<__nv_bfloat16, 64>(p, a, s);
+    return a.d == 128 ? forward<float, 128>(p, a, s) : forward<float, 64>(p, a, s);
+}
+
+cudaError_t launch_window_backward(const WinArgs &a, cudaStream_t s) {
+    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, true, a.workspace);
+    KDA_TRY(prepare_tiles(p, a, s));
+    if (p.geo.tokens == 0) return cudaSuccess;
+    if (a.dt == KDA_BF16) return a.d == 128 ? backward<__nv_bfloat16, 128>(p, a, s) : backward<__nv_bfloat16, 64>(p, a, s);
+    return a.d == 128 ? backward<float, 128>(p, a, s) : backward<float, 64>(p, a, s);
+}
+
+}  // namespace kda

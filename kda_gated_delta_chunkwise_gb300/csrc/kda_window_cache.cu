@@ -1,0 +1,388 @@
+// The cache of window attention: writing the keys and values of packed prompts
+// into their slots, and one token per sequence against its slot.
+//
+// A slot holds the sinks and then a ring of the last `window` tokens, entry by
+// entry [entries][hk][d]. With the new token written, the tokens that it sees
+// are exactly the first min(position + 1, entries) entries, and a softmax does not
+// mind their order, so a step is an attention over a stretch of memory.
+//
+// The step is bound by memory: every entry of a key head is read once for all
+// its query heads. One warp takes 16 entries (fp32: 8) at a time straight from
+// global memory into the fragments of mma.sync, 16 query heads (or what there
+// are) as the rows of the product: a contraction does not mind the order of its
+// index, so a lane reads 16 bytes of consecutive channels and the query's
+// fragments are read the same way; for the values' product a lane holds the
+// entries and channels that its fragments want, two entries' halves joined by a
+// byte permutation. Nothing goes through shared memory until the warps' sums are
+// joined. Few sequences are cut over the CTAs of a cluster, whose sums are joined
+// through distributed shared memory in rank order.
+#include <math_constants.h>
+
+#include "kda_tc_ptx.cuh"
+#include "kda_window.cuh"
+
+namespace kda {
+namespace {
+
+// ================================================================ prompts into the cache
+constexpr int CT = 256, CTOK = 8;  // tokens a CTA
+__global__ void __launch_bounds__(CT)
+win_cache_write_kernel(WinCacheArgs p, int row16, int es) {  // row16: 16-byte pieces of a token's heads
+    __shared__ int bad;
+    const int tid = threadIdx.x, n = blockIdx.y;
+    if (tid == 0) bad = (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T) ? 1 : 0;
+    __syncthreads();
+    for (int i = tid; i < p.N; i += CT)
+        if (p.cu_seqlens[i + 1] < p.cu_seqlens[i]) atomicOr(&bad, 1);
+    __syncthreads();
+    if (bad) {
+        if (tid == 0 && blockIdx.x == 0 && n == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_CU_SEQLENS);
+        return;
+    }
+    bool fresh;
+    const int64_t slot = slot_of(p.slots, n, fresh);
+    if (slot >= p.pool) {
+        if (tid == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_SLOT);
+        return;
+    }
+    const int start = p.cu_seqlens[n], len = p.cu_seqlens[n + 1] - start, window = p.entries - p.sinks;
+    const int first = min(p.sinks, len), second = max(first, len - window), kept = first + len - second;
+    for (int x0 = blockIdx.x * CTOK; x0 < kept; x0 += gridDim.x * CTOK) {
+        const int count = min(CTOK, kept - x0);
+        for (int i = tid; i < count * row16; i += CT) {
+            const int x = x0 + i / row16, c = i % row16 * (16 / es), token = x < first ? x : second + x - first;
+            const int64_t entry = slot * p.entries + (token < p.sinks ? token : p.sinks + (token - p.sinks) % window);
+            const int64_t dst = (entry * p.hk * p.d + c) * es;
+            const int64_t ks = ((int64_t)(start + token) * p.k_stride + c) * es, vs = ((int64_t)(start + token) * p.v_stride + c) * es;
+            const uint4 k = *reinterpret_cast<const uint4 *>((const char *)p.k + ks);
+            const uint4 v = *reinterpret_cast<const uint4 *>((const char *)p.v + vs);
+            *reinterpret_cast<uint4 *>((char *)p.k_cache + dst) = k;
+            *reinterpret_cast<uint4 *>((char *)p.v_cache + dst) = v;
+        }
+    }
+}
+
+// ================================================================ one token
+constexpr int DT = 128, DW = DT / 32, HEADS = 16;
+
+__device__ __forceinline__ uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += the fp32 product of four values of a with two of b, each in two tf32 parts
+__device__ __forceinline__ void mma_fp32(float (&d)[4], const float (&a)[4], float x0, float x1) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = tf32(a[i]);
+        lo[i] = tf32(a[i] - __uint_as_float(hi[i]));
+    }
+    const uint32_t h0 = tf32(x0), h1 = tf32(x1);
+    mma_tf32(d, lo, h0, h1);
+    mma_tf32(d, hi, tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
+    mma_tf32(d, hi, h0, h1);
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// What a type's fragments look like. Channels: a chunk is 16 bytes, CH channels; a
+// lane's K chunks are 4 CH apart (t within), its V chunks 8 CH apart (g within).
+template <typename T, int D> struct Shape {
+    static constexpr int CH = 16 / sizeof(T);
+    static constexpr int KEYS = sizeof(T) == 2 ? 16 : 8;  // entries a step
+    static constexpr int NB = KEYS / 8;                   // their 8-column blocks
+    static constexpr int KC = D / (4 * CH);               // chunks of a lane and key
+    static constexpr int VC = D / (8 * CH);               // chunks of a lane and value row
+    static constexpr int VR = sizeof(T) == 2 ? 4 : 2;     // value rows of a lane
+    // the value row u of lane t within the step
+    static __device__ __forceinline__ int v_row(int t, int u) { return 2 * t + (u & 1) + (u >> 1) * 8; }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(DT, 2)
+win_decode_kernel(WinCacheArgs p, int cl) {
+    using S = Shape<T, D>;
+    constexpr int CH = S::CH, KEYS = S::KEYS, NB = S::NB, KC = S::KC, VC = S::VC, VR = S::VR;
+    extern __shared__ __align__(16) float sm[];
+    float *part = sm;                            // [DW][HEADS][D]: the warps' sums
+    float *own = part + DW * HEADS * D;          // [HEADS][D]: the CTA's
+    float *stat = own + HEADS * D;               // [DW][HEADS][2]: the warps' maximum and sum
+    float *own_stat = stat + DW * HEADS * 2;     // [HEADS][2]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = blockIdx.x % cl, nh = blockIdx.x / cl, n = nh / p.hk, hk = nh - n * p.hk, group = p.hq / p.hk;
+    bool fresh;
+    const int64_t slot = slot_of(p.slots, n, fresh);
+    const int pos = p.positions[n];
+    if (slot >= p.pool || pos < 0) {  // the same in the whole cluster
+        if (tid == 0 && rank == 0 && p.status) atomicOr(p.status, slot >= p.pool ? KDA_DEV_BAD_SLOT : KDA_DEV_BAD_POSITION);
+        return;
+    }
+    const int window = p.entries - p.sinks;
+    const int fill = pos < p.sinks ? pos : p.sinks + (pos - p.sinks) % window;  // the new token's entry
+    const int count = pos < p.entries ? pos + 1 : p.entries;
+    const T *knew = (const T *)p.k + n * p.k_stride + hk * D, *vnew = (const T *)p.v + n * p.v_stride + hk * D;
+    const int64_t step = (int64_t)p.hk * D, base = (slot * p.entries * p.hk + hk) * D;
+    T *kc = (T *)p.k_cache + base, *vc = (T *)p.v_cache + base;
+    // the new row is read where it came from, by whoever has its entry, so writing it races with nobody
+    if (rank == 0 && tid < 2 * (D / CH)) {
+        const int c = tid % (D / CH) * CH;
+        const bool is_k = tid < D / CH;
+        *reinterpret_cast<uint4 *>((is_k ? kc : vc) + fill * step + c) =
+            *reinterpret_cast<const uint4 *>((is_k ? knew : vnew) + c);
+    }
+    const int tiles = (count + KEYS - 1) / KEYS, per = (tiles + cl - 1) / cl;
+    const int tile0 = rank * per, tile1 = min(tiles, tile0 + per);
+    const float c2 = p.scale * 1.4426950408889634f;  // scores in powers of two
+
+    for (int h0 = 0; h0 < group; h0 += HEADS) {
+        const int heads = min(HEADS, group - h0);
+        const T *q = (const T *)p.q + n * p.q_stride + (int64_t)(hk * group + h0) * D;
+        uint4 qf[2][KC];  // rows g and g + 8
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+                qf[r][j] = g + r * 8 < heads ? *reinterpret_cast<const uint4 *>(q + (g + r * 8) * D + 4 * CH * j + CH * t)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float acc[D / 8][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        auto row = [&](const T *cache, const T *fresh_row, int e) { return e == fill ? fresh_row : cache + e * step; };
+        uint4 kf[NB][KC], vf[VR][VC];
+        auto load_k = [&](int tile) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int e = tile * KEYS + b * 8 + g;
+                const T *src = row(kc, knew, e) + CH * t;
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    kf[b][j] = e < count ? *reinterpret_cast<const uint4 *>(src + 4 * CH * j) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        auto load_v = [&](int tile) {
+#pragma unroll
+            for (int u = 0; u < VR; ++u) {
+                const int e = tile * KEYS + S::v_row(t, u);
+                const T *src = row(vc, vnew, e) + CH * g;
+#pragma unroll
+                for (int i = 0; i < VC; ++i)
+                    vf[u][i] = e < count ? *reinterpret_cast<const uint4 *>(src + 8 * CH * i) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        int tile = tile0 + warp;
+        if (tile < tile1) load_k(tile);
+        for (; tile < tile1; tile += DW) {
+            load_v(tile);
+            float s[NB][4];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < KC; ++j) {
+                    const uint4 x = qf[0][j], y = qf[1][j], k = kf[b][j];
+                    if constexpr (sizeof(T) == 2) {
+                        mma_bf16(s[b], x.x, y.x, x.y, y.y, k.x, k.y);
+                        mma_bf16(s[b], x.z, y.z, x.w, y.w, k.z, k.w);
+                    } else {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        const float a0[4] = {__uint_as_float(x.x), __uint_as_float(y.x), __uint_as_float(x.y), __uint_as_float(y.y)};
+                        const float a1[4] = {__uint_as_float(x.z), __uint_as_float(y.z), __uint_as_float(x.w), __uint_as_float(y.w)};
+                        mma_fp32(d, a0, __uint_as_float(k.x), __uint_as_float(k.y));
+                        mma_fp32(d, a1, __uint_as_float(k.z), __uint_as_float(k.w));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[b][e] += d[e];
+                    }
+                }
+            }
+            if (tile + DW < tile1) load_k(tile + DW);
+            float top[2] = {m[0], m[1]};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[b][e] = tile * KEYS + b * 8 + 2 * t + (e & 1) < count ? s[b][e] * c2 : -CUDART_INF_F;
+                    top[e >> 1] = fmaxf(top[e >> 1], s[b][e]);
+                }
+            }
+            float keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // a step has an entry at least, so the maximum is a number
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                keep[e] = exp2_approx(m[e] - top[e]);
+                l[e] *= keep[e];
+            }
+            if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] *= keep[e >> 1];
+                }
+            }
+            m[0] = top[0], m[1] = top[1];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[b][e] = exp2_approx(s[b][e] - m[e >> 1]);
+                    l[e >> 1] += s[b][e];
+                }
+            }
+            if constexpr (sizeof(T) == 2) {
+                // the weights are rounded to bf16, as the values are: 2^-9 of each, below the result's own rounding
+                const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]), a2 = pack(s[NB - 1][0], s[NB - 1][1]),
+                               a3 = pack(s[NB - 1][2], s[NB - 1][3]);
+#pragma unroll
+                for (int i = 0; i < VC; ++i) {
+                    const uint32_t w[4][4] = {{vf[0][i].x, vf[0][i].y, vf[0][i].z, vf[0][i].w},
+                                              {vf[1][i].x, vf[1][i].y, vf[1][i].z, vf[1][i].w},
+                                              {vf[VR - 2][i].x, vf[VR - 2][i].y, vf[VR - 2][i].z, vf[VR - 2][i].w},
+                                              {vf[VR - 1][i].x, vf[VR - 1][i].y, vf[VR - 1][i].z, vf[VR - 1][i].w}};
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
+                        mma_bf16(acc[i * 8 + b], a0, a1, a2, a3, __byte_perm(w[0][b / 2], w[1][b / 2], sel),
+                                 __byte_perm(w[2][b / 2], w[3][b / 2], sel));
+                    }
+                }
+            } else {
+                const float a[4] = {s[0][0], s[0][2], s[0][1], s[0][3]};
+#pragma unroll
+                for (int i = 0; i < VC; ++i) {
+                    const float w[2][4] = {{__uint_as_float(vf[0][i].x), __uint_as_float(vf[0][i].y),
+                                            __uint_as_float(vf[0][i].z), __uint_as_float(vf[0][i].w)},
+                                           {__uint_as_float(vf[1][i].x), __uint_as_float(vf[1][i].y),
+                                            __uint_as_float(vf[1][i].z), __uint_as_float(vf[1][i].w)}};
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_fp32(d, a, w[0][b], w[1][b]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i * 4 + b][e] += d[e];
+                    }
+                }
+            }
+        }
+        // the warps' sums: lane (g, t) has, of rows g and g + 8, channels 8 CH i + CH (2 t + e) + b
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            const int r = g + e * 8;
+            if (r >= heads) continue;
+            if (t == 0) stat[(warp * HEADS + r) * 2] = m[e], stat[(warp * HEADS + r) * 2 + 1] = l[e];
+            float *dst = part + (warp * HEADS + r) * D;
+#pragma unroll
+            for (int i = 0; i < VC; ++i) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int b = 0; b < CH; b += 4)
+                        *reinterpret_cast<float4 *>(dst + 8 * CH * i + CH * (2 * t + u) + b) =
+                            make_float4(acc[i * CH + b][2 * e + u], acc[i * CH + b + 1][2 * e + u],
+                                        acc[i * CH + b + 2][2 * e + u], acc[i * CH + b + 3][2 * e + u]);
+                }
+            }
+        }
+        __syncthreads();
+        for (int x = tid; x < heads * D; x += DT) {
+            const int r = x / D;
+            float top = -CUDART_INF_F, a = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < DW; ++w) top = fmaxf(top, stat[(w * HEADS + r) * 2]);
+#pragma unroll
+            for (int w = 0; w < DW; ++w) {
+                const float mw = stat[(w * HEADS + r) * 2], f = mw == -CUDART_INF_F ? 0.f : exp2_approx(mw - top);
+                a += f * part[(w * HEADS) * D + x];
+                sum += f * stat[(w * HEADS + r) * 2 + 1];
+            }
+            if (cl == 1) {
+                ((T *)p.o)[((int64_t)n * p.hq + hk * group + h0) * D + x] = from_f32<T>(a / sum);
+            } else {
+                own[x] = a;
+                if (x % D == 0) own_stat[2 * r] = top, own_stat[2 * r + 1] = sum;
+            }
+        }
+        if (cl > 1) {
+            tc::cluster_sync();
+            const uint32_t so = tc::smem_u32(own), ss = tc::smem_u32(own_stat);
+            auto remote = [](uint32_t addr, int r) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::mapa(addr, r)) : "memory");
+                return v;
+            };
+            const int share = (heads * D + cl - 1) / cl;
+            for (int x = rank * share + tid; x < min(heads * D, (rank + 1) * share); x += DT) {
+                const int r = x / D;
+                float top = -CUDART_INF_F, a = 0.f, sum = 0.f;
+                for (int k = 0; k < cl; ++k) top = fmaxf(top, remote(ss + r * 8, k));
+                for (int k = 0; k < cl; ++k) {
+                    const float mk = remote(ss + r * 8, k), f = mk == -CUDART_INF_F ? 0.f : exp2_approx(mk - top);
+                    a += f * remote(so + x * 4, k);
+                    sum += f * remote(ss + r * 8 + 4, k);
+                }
+                ((T *)p.o)[((int64_t)n * p.hq + hk * group + h0) * D + x] = from_f32<T>(a / sum);
+            }
+            tc::cluster_sync();
+        } else {
+            __syncthreads();
+        }
+    }
+}
+
+template <typename T, int D> cudaError_t decode(const WinCacheArgs &a, cudaStream_t s) {
+    constexpr size_t smem = (DW * HEADS * D + HEADS * D + DW * HEADS * 2 + HEADS * 2) * sizeof(float);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(win_decode_kernel<T, D>, smem, allowed);
+    if (e != cudaSuccess) return e;
+    // CTAs of a cluster: until there are two for every SM or a warp has but one step left
+    const int64_t work = (int64_t)a.N * a.hk;
+    int cl = 1;
+    while (cl < 8 && work * cl < 2 * 152 && a.entries >= cl * 2 * DW * Shape<T, D>::KEYS) cl *= 2;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cl;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(work * cl));
+    c.blockDim = dim3(DT);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, win_decode_kernel<T, D>, a, cl);
+}
+
+}  // namespace
+
+cudaError_t launch_window_cache_write(const WinCacheArgs &a, cudaStream_t s) {
+    const int es = a.dt == KDA_BF16 ? 2 : 4, most = a.T < a.entries ? a.T : a.entries;  // tokens kept of one sequence
+    const int blocks = (most + CTOK - 1) / CTOK;
+    win_cache_write_kernel<<<dim3(blocks < 1 ? 1 : blocks, a.N), CT, 0, s>>>(a, a.hk * a.d * es / 16, es);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_window_decode(const WinCacheArgs &a, cudaStream_t s) {
+    if (a.dt == KDA_BF16) return a.d == 128 ? decode<__nv_bfloat16, 128>(a, s) : decode<__nv_bfloat16, 64>(a, s);
+    return a.d == 128 ? decode<float, 128>(a, s) : decode<float, 64>(a, s);
+}
+
+}  // namespace kda
