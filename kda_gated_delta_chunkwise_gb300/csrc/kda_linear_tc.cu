@@ -8,12 +8,12 @@
 // wait is bounded: a wait that runs out sets the device error word and the
 // CTA's abort flag, every role leaves its loop, and the CTA ends normally.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math_constants.h>
 
 #include "kda_linear.cuh"
 #include "kda_linear_tc.cuh"
 #include "kda_tc_ptx.cuh"
+#include "kda_tc_roles.cuh"
 
 namespace kda {
 namespace {
@@ -21,25 +21,7 @@ namespace {
 using namespace tc;
 
 constexpr int D = 128;
-__device__ int g_lin_error;
 
-// ---------------------------------------------------------------- waits
-struct Abort {
-    volatile int *flag;  // shared memory
-    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*flag) return false;
-            if (clock64() - t0 > kWaitCycles) {
-                *flag = 1;
-                atomicOr(&g_lin_error, 1);
-                return false;
-            }
-        }
-        return true;
-    }
-};
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {  // two bf16 products, each rounded once
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -49,35 +31,6 @@ __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) 
     uint32_t r;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
-}
-// One arrival for the warp, after all its lanes have come here.
-__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-// After an abort: copies that were on their way land before the CTA leaves.
-__device__ __forceinline__ void settle(const Abort &ab) {
-    if (*ab.flag) {
-        const long long t0 = clock64();
-        while (clock64() - t0 < 100000) {
-        }
-        __syncthreads();
-    }
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-__device__ __forceinline__ F2 pair_f(uint32_t x) { return f2(lo_f(x), hi_f(x)); }  // two bf16
-__device__ __forceinline__ F2 pair_w(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
-__device__ __forceinline__ uint32_t pack2(F2 x) {
-    float a, b;
-    f2_get(x, a, b);
-    return pack2(a, b);
 }
 __device__ __forceinline__ F2 minus(F2 x, F2 y) { return fma2(y, f2(-1.f, -1.f), x); }
 // x = h + m + l, each a bf16 (24 bits of x kept), two values at a time.
@@ -113,51 +66,6 @@ __device__ __forceinline__ void scale16(uint32_t (&v)[16], float f) {  // the sa
         f2_get(pair_w(v[e], v[e + 1]) * ff, a, b);
         v[e] = __float_as_uint(a), v[e + 1] = __float_as_uint(b);
     }
-}
-__device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {  // one 32-byte sector
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-        : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {  // into L2
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-// D[tmem] += A[tmem] * B[smem]: A holds two bf16 of K per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, 1, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc)
-        : "memory");
-}
-// MMA descriptors of a tile, advanced by constants: the address field counts
-// 16-byte steps. One thread issues every MMA, so its instructions between two
-// of them are time the tensor core waits.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }     // K-major
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, uint32_t atom) { return sdesc_sw128(tile, atom, 1024); }
-// offset of step ks (16 of K): K-major tiles have 64 of K per atom of `atom` bytes
-__device__ __forceinline__ constexpr uint64_t step_k(int ks, uint32_t atom) {
-    return ((ks >> 2) * atom + (ks & 3) * 32) >> 4;
-}
-__device__ __forceinline__ constexpr uint64_t step_mn(int ks) { return (uint64_t)(ks * 2048) >> 4; }
-template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
-        : "memory");
 }
 // NaN log decays among a warp's tokens (laid out as in warp_decay): which of the
 // decays are NaN, by the rule at kMinLogDecay.
@@ -1597,18 +1505,6 @@ lin_roll_tc_kernel(RollTcArgs p, const __grid_constant__ CUtensorMap mx, const _
 }
 
 // ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
 // [tokens][H][128] bf16 with a token stride, boxes of 64 channels x 1 head x 64 tokens.
 bool token_map(CUtensorMap *m, const void *ptr, int64_t stride, int H, int64_t tokens) {
     auto enc = encoder();
@@ -1630,15 +1526,6 @@ bool state_map(CUtensorMap *m, const void *ptr, int64_t rows) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-int sm_count() {
-    static int n = [] {
-        int dev = 0, v = 152;
-        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        return v;
-    }();
-    return n;
-}
-
 #define KDA_TRY(x)                        \
     do {                                  \
         const cudaError_t e_ = (x);       \
@@ -1705,16 +1592,6 @@ cudaError_t launch_attend_tc(const AttendTc &a, Launches &l) {
     return l.whole(k, min(p.items, sm_count()), AT_THREADS, AT_SMEM, p, mx, my, mz, ms, mw);
 }
 
-cudaError_t read_linear_error(int *out, bool reset) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_lin_error, sizeof(int));
-    if (e != cudaSuccess) return e;
-    *out = v;
-    if (reset && v) {
-        const int z = 0;
-        e = cudaMemcpyToSymbol(g_lin_error, &z, sizeof(int));
-    }
-    return e;
-}
+cudaError_t read_linear_error(int *out, bool reset) { return read_tc_error(out, reset); }
 
 }  // namespace kda
