@@ -777,7 +777,7 @@ size_t kda_residual_norm_backward_workspace_bytes(int D);
  * Query head h reads key head h / (H_q / H_k).
  *   q, o    [.., H_q, d] dtype;  k, v [.., H_k, d] dtype;  d 64 or 128
  *   lse     [.., H_q] float32: natural logarithm (nullable; the gradients want it)
- *   window  >= 1, as long as you like;  sinks 0 to 128
+ *   window  >= 1, as long as you like;  sinks 0 to 128;  scale > 0
  * q, k, v may be views of a wider tensor (token strides as for linear attention);
  * outputs are contiguous. Two calls on the same inputs give the same bits, and a
  * sequence the same ones alone and in a packed batch. fp32 calls are accurate to

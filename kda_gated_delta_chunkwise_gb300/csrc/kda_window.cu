@@ -10,13 +10,12 @@
 // One CTA takes 64 rows (queries, or keys for dk and dv), a warp 16 of them, and
 // walks tiles of 32 columns in shared memory with the running maximum and sum of
 // the softmax in registers. The products run on mma.sync tf32; an fp32 operand is
-// split in two tf32 parts, three products for each, and every four steps are
-// summed from zero and then added in fp32, because the tensor core truncates its
-// accumulations. bf16 values are exact in tf32; the weights p and ds of a bf16
+// split in two tf32 parts, three products for each. bf16 values are exact in tf32; the weights p and ds of a bf16
 // call keep 11 bits, against the 8 of its result.
 #include <math_constants.h>
 
 #include "kda_window.cuh"
+#include "kda_window_tc.cuh"
 
 namespace kda {
 namespace {
@@ -94,13 +93,22 @@ template <bool SPLIT> struct Frag {
         if (SPLIT) lo[i] = tf32(x - __uint_as_float(hi[i]));
     }
 };
-template <bool SPLIT> __device__ __forceinline__ void product(float (&d)[4], const Frag<SPLIT> &a, float x0, float x1) {
+// d += the product of four values of a and two of b. In two parts the three
+// products of a step are summed from zero, the small ones first, and then added in
+// fp32: the tensor core truncates what it accumulates, fp32 sums round (carried on
+// through four steps a score was twice as far off).
+template <bool SPLIT> __device__ __forceinline__ void add_product(float (&d)[4], const Frag<SPLIT> &a, float x0, float x1) {
     const uint32_t h0 = tf32(x0), h1 = tf32(x1);
-    if (SPLIT) {
-        mma(d, a.lo, h0, h1);
-        mma(d, a.hi, tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
+    if constexpr (SPLIT) {
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(z, a.lo, h0, h1);
+        mma(z, a.hi, tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
+        mma(z, a.hi, h0, h1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] += z[e];
+    } else {
+        mma(d, a.hi, h0, h1);
     }
-    mma(d, a.hi, h0, h1);
 }
 
 constexpr int NT = 128, ROWS = 64, COLS = 32;
@@ -136,27 +144,16 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[COLS / 8][4], const fl
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
 #pragma unroll
     for (int nb = 0; nb < COLS / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
-#pragma unroll 1
-    for (int k0 = 0; k0 < D; k0 += 32) {
-        float d[COLS / 8][4];
+#pragma unroll 4
+    for (int k = 0; k < D; k += 8) {
+        Frag<SPLIT> f;
+        f.set(0, a[r0 * (D + 4) + k + t]);
+        f.set(1, a[(r0 + 8) * (D + 4) + k + t]);
+        f.set(2, a[r0 * (D + 4) + k + t + 4]);
+        f.set(3, a[(r0 + 8) * (D + 4) + k + t + 4]);
 #pragma unroll
-        for (int nb = 0; nb < COLS / 8; ++nb) d[nb][0] = d[nb][1] = d[nb][2] = d[nb][3] = 0.f;
-#pragma unroll
-        for (int k = k0; k < k0 + 32; k += 8) {
-            Frag<SPLIT> f;
-            f.set(0, a[r0 * (D + 4) + k + t]);
-            f.set(1, a[(r0 + 8) * (D + 4) + k + t]);
-            f.set(2, a[r0 * (D + 4) + k + t + 4]);
-            f.set(3, a[(r0 + 8) * (D + 4) + k + t + 4]);
-#pragma unroll
-            for (int nb = 0; nb < COLS / 8; ++nb)
-                product<SPLIT>(d[nb], f, b[(nb * 8 + g) * (D + 4) + k + t], b[(nb * 8 + g) * (D + 4) + k + t + 4]);
-        }
-#pragma unroll
-        for (int nb = 0; nb < COLS / 8; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nb][e] += d[nb][e];
-        }
+        for (int nb = 0; nb < COLS / 8; ++nb)
+            add_product<SPLIT>(acc[nb], f, b[(nb * 8 + g) * (D + 4) + k + t], b[(nb * 8 + g) * (D + 4) + k + t + 4]);
     }
 }
 // acc[nb] += w (16 x 32, as rows_by_rows leaves it) times the rows of b. Columns
@@ -175,13 +172,10 @@ __device__ __forceinline__ void weights_by_rows(float (&acc)[D / 8][4], const fl
     }
 #pragma unroll
     for (int nb = 0; nb < D / 8; ++nb) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < COLS / 8; ++kb)
-            product<SPLIT>(d, f[kb], b[(kb * 8 + 2 * t) * (D + 4) + nb * 8 + g],
-                           b[(kb * 8 + 2 * t + 1) * (D + 4) + nb * 8 + g]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nb][e] += d[e];
+            add_product<SPLIT>(acc[nb], f[kb], b[(kb * 8 + 2 * t) * (D + 4) + nb * 8 + g],
+                               b[(kb * 8 + 2 * t + 1) * (D + 4) + nb * 8 + g]);
     }
 }
 
@@ -610,7 +604,7 @@ cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, false, a.workspace);
     KDA_TRY(prepare_tiles(p, a, s));
     if (p.geo.tokens == 0) return cudaSuccess;
-    if (a.dt == KDA_BF16) return a.d == 128 ? forward<__nv_bfloat16, 128>(p, a, s) : forward<__nv_bfloat16, 64>(p, a, s);
+    if (a.dt == KDA_BF16) return launch_window_forward_tc(p.geo, a, s);
     return a.d == 128 ? forward<float, 128>(p, a, s) : forward<float, 64>(p, a, s);
 }
 

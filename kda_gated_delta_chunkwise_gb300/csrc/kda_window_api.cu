@@ -34,11 +34,17 @@ kda_status_t strides(int64_t &q, int64_t &k, int64_t &v, int hq, int hk, int d, 
     return stride(v, hk, d, dt, "v_stride");
 }
 
+// A row's largest score is that of its largest product: the scale comes after.
+kda_status_t scale_ok(float scale) {
+    return scale > 0.f && std::isfinite(scale) ? KDA_OK
+                                               : fail(KDA_ERR_INVALID_ARG, "scale must be positive and finite");
+}
+
 kda_status_t attention(WinArgs &a, bool packed, bool back, size_t workspace_bytes, cudaStream_t s) {
     KDA_CHECK(common(a.dt, a.N, a.T, a.hq, a.hk, a.d, a.sinks));
     KDA_CHECK(sizes(a.N, a.T, a.hq, packed));
     if (a.window < 1) return fail(KDA_ERR_INVALID_ARG, "window must be positive (got %d)", a.window);
-    if (!std::isfinite(a.scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    KDA_CHECK(scale_ok(a.scale));
     KDA_CHECK(strides(a.q_stride, a.k_stride, a.v_stride, a.hq, a.hk, a.d, a.dt));
     if (a.T > 0 && a.window > a.T) a.window = a.T;  // as good as any longer one
     const int64_t tokens = packed ? a.T : (int64_t)a.N * a.T;
@@ -199,7 +205,7 @@ kda_status_t kda_window_decode_step(const void *q, const void *k, const void *v,
     a.status = device_status;
     KDA_CHECK(cache(a));
     KDA_CHECK(strides(a.q_stride, a.k_stride, a.v_stride, H_q, H_k, d, dtype));
-    if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    KDA_CHECK(scale_ok(scale));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (N > 0) {
         if (!fits(N, H_k, 16) || !fits(N, H_q)) return fail(KDA_ERR_UNSUPPORTED, "N * H_k * 16 must fit in int32");

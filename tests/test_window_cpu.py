@@ -34,6 +34,7 @@ def test_forward_refusals(lib):
     assert _forward(lib, B=-1) == INVALID and _forward(lib, T=-1) == INVALID
     assert _forward(lib, window=0) == INVALID and _forward(lib, window=-5) == INVALID
     assert _forward(lib, sinks=-1) == INVALID and _forward(lib, sinks=129) == UNSUPPORTED
+    assert _forward(lib, scale=0.0) == INVALID and _forward(lib, scale=-1.0) == INVALID
     assert _forward(lib, scale=math.nan) == INVALID and _forward(lib, scale=math.inf) == INVALID
     assert _forward(lib, q=None) == INVALID and _forward(lib, q=ctypes.c_void_p(0x1008)) == INVALID
     assert _forward(lib, o=None) == INVALID and _forward(lib, lse=ODD) == INVALID
