@@ -144,7 +144,7 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[COLS / 8][4], const fl
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
 #pragma unroll
     for (int nb = 0; nb < COLS / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < D; k += 8) {
         Frag<SPLIT> f;
         f.set(0, a[r0 * (D + 4) + k + t]);
@@ -186,10 +186,17 @@ struct WinParams {
     int64_t q_stride, k_stride, v_stride;
     float scale;
     void *o, *dq, *dk, *dv;
-    float *lse, *delta;       // [tokens][hq]
+    float *lse;               // [tokens][hq], of the forward
+    float *lse2, *delta;      // [hq][tokens], of the gradients: lse (bf16: in powers of two), D
     float *part, *sums;       // far gradients of the sinks: [ntiles][hk][2][sinks][d], [N][hk][2][sinks][d]
 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+// e^{scale s - lse}; of bf16 calls scale and lse come in powers of two (their
+// roundings, 2^-24 of a score, would be seen in an fp32 gradient)
+template <bool SPLIT> __device__ __forceinline__ float weight(float s, float scale, float lse) {
+    return SPLIT ? expf(fmaf(s, scale, -lse)) : exp2_approx(fmaf(s, scale, -lse));
+}
 // Whether i sees j, among the near pairs or among the far ones.
 __device__ __forceinline__ bool sees(int i, int j, int window, int sinks, bool far) {
     return far ? j < sinks && i - j >= window : j <= i && i - j < window;
@@ -278,19 +285,43 @@ win_forward_kernel(WinParams p) {
     }
 }
 
-// D_i = do_i . o_i, a warp a row.
+// D_i = do_i . o_i, and lse (see weight), both by head: a tile of queries is a
+// stretch of memory then. A row is 16 bytes in each of d sizeof(T) / 16 lanes, a
+// block 32 tokens of one head at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-win_delta_kernel(const T *o, const T *d_o, float *delta, int64_t rows) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    float s = 0.f;
+win_delta_kernel(const T *o, const T *d_o, const float *lse, float *lse2, float *delta, int64_t tokens, int hq) {
+    constexpr int N = 16 / sizeof(T), LANES = D / N, PER = 256 / LANES;
+    const int h = blockIdx.y, in = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const int64_t t0 = (int64_t)blockIdx.x * 32;
+    uint4 a[32 / PER], b[32 / PER];
 #pragma unroll
-    for (int c = 0; c < D; c += 32) s = fmaf(to_f32(o[row * D + c + lane]), to_f32(d_o[row * D + c + lane]), s);
+    for (int i = 0; i < 32 / PER; ++i) {
+        const int64_t t = t0 + i * PER + sub, at = (t * hq + h) * D + in * N;
+        a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < tokens) a[i] = *reinterpret_cast<const uint4 *>(o + at), b[i] = *reinterpret_cast<const uint4 *>(d_o + at);
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) delta[row] = s;
+    for (int i = 0; i < 32 / PER; ++i) {
+        const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (sizeof(T) == 4) {
+                s = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), s);
+            } else {
+                s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
+                s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s);
+            }
+        }
+#pragma unroll
+        for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        const int64_t t = t0 + i * PER + sub;
+        if (in == 0 && t < tokens) {
+            delta[h * tokens + t] = s;
+            lse2[h * tokens + t] = lse[t * hq + h] * (sizeof(T) == 2 ? kLog2e : 1.f);
+        }
+    }
 }
 
 // dq; or, with DELTA, D_i once more as sum_j p_ij dp_ij, for tokens that see few
@@ -316,7 +347,7 @@ win_dq_kernel(WinParams p) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
     const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
     const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
-    const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h;
+    const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h, vec0 = (int64_t)h * geo.tokens + tile.start + i0;
     load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows, ROWS);
     load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, rows, ROWS);
     float acc[D / 8][4], lse[2], delta[2];
@@ -325,9 +356,10 @@ win_dq_kernel(WinParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const bool there = r0 + e * 8 < rows;
-        lse[e] = there ? p.lse[row0 + (int64_t)(r0 + e * 8) * geo.hq] : 0.f;
-        delta[e] = there && !DELTA ? p.delta[row0 + (int64_t)(r0 + e * 8) * geo.hq] : 0.f;
+        lse[e] = there ? p.lse2[vec0 + r0 + e * 8] : 0.f;
+        delta[e] = there && !DELTA ? p.delta[vec0 + r0 + e * 8] : 0.f;
     }
+    const float scale = SPLIT ? p.scale : p.scale * kLog2e;
     float all[2] = {0.f, 0.f};  // DELTA: the sum of the weights, one but for rounding
     auto walk = [&](int from, int to, bool far) {
         for (int j0 = from; j0 < to; j0 += COLS) {
@@ -345,7 +377,7 @@ win_dq_kernel(WinParams p) {
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
                     const bool on = j < to && sees(i, j, geo.window, geo.sinks, far) && !alone(i, geo.window, geo.sinks);
-                    s[nb][e] = on ? expf(s[nb][e] * p.scale - lse[e >> 1]) : 0.f;
+                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, lse[e >> 1]) : 0.f;
                     if (DELTA) {
                         all[e >> 1] += s[nb][e];
                         delta[e >> 1] = fmaf(s[nb][e], dp[nb][e], delta[e >> 1]);
@@ -354,12 +386,12 @@ win_dq_kernel(WinParams p) {
                     }
                 }
             }
-            if (!DELTA) weights_by_rows<SPLIT, D>(acc, s, sk);
+            if constexpr (!DELTA) weights_by_rows<SPLIT, D>(acc, s, sk);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
     walk(max(0, i0 - geo.window + 1), i0 + rows, false);
-    if (DELTA) {
+    if constexpr (DELTA) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -368,19 +400,19 @@ win_dq_kernel(WinParams p) {
                 delta[e] += __shfl_xor_sync(0xffffffffu, delta[e], off);
             }
             if (t == 0 && r0 + e * 8 < rows && all[e] > 0.f)  // not of a token that sees itself alone
-                p.delta[row0 + (int64_t)(r0 + e * 8) * geo.hq] = delta[e] / all[e];
+                p.delta[vec0 + r0 + e * 8] = delta[e] / all[e];
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = r0 + e * 8;
-        if (r >= rows) continue;
-        T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + e * 8;
+            if (r >= rows) continue;
+            T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
 #pragma unroll
-        for (int nb = 0; nb < D / 8; ++nb) {
-            dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
-            dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
+            for (int nb = 0; nb < D / 8; ++nb) {
+                dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
+                dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
+            }
         }
     }
 }
@@ -406,6 +438,7 @@ win_dkv_kernel(WinParams p) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
     load_tile<T, D>(sk, (const T *)p.k + (int64_t)(tile.start + j0) * p.k_stride + hk * D, p.k_stride, rows, ROWS);
     load_tile<T, D>(sv, (const T *)p.v + (int64_t)(tile.start + j0) * p.v_stride + hk * D, p.v_stride, rows, ROWS);
+    const float scale = SPLIT ? p.scale : p.scale * kLog2e;
     float ak[D / 8][4], av[D / 8][4];
 #pragma unroll
     for (int nb = 0; nb < D / 8; ++nb) {
@@ -421,8 +454,9 @@ win_dkv_kernel(WinParams p) {
             load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, cols, COLS);
             if (threadIdx.x < COLS) {
                 const bool there = threadIdx.x < cols;
-                slse[threadIdx.x] = there ? p.lse[row0 + (int64_t)threadIdx.x * geo.hq] : 0.f;
-                sdelta[threadIdx.x] = there ? p.delta[row0 + (int64_t)threadIdx.x * geo.hq] : 0.f;
+                const int64_t at = (int64_t)h * geo.tokens + tile.start + i0 + threadIdx.x;
+                slse[threadIdx.x] = there ? p.lse2[at] : 0.f;
+                sdelta[threadIdx.x] = there ? p.delta[at] : 0.f;
             }
             __syncthreads();
             float s[COLS / 8][4], dp[COLS / 8][4];
@@ -434,7 +468,7 @@ win_dkv_kernel(WinParams p) {
                 for (int e = 0; e < 4; ++e) {
                     const int j = j0 + r0 + (e >> 1) * 8, c = nb * 8 + 2 * t + (e & 1), i = i0 + c;
                     const bool on = r0 + (e >> 1) * 8 < rows && i < to && sees(i, j, geo.window, geo.sinks, FAR);
-                    s[nb][e] = on ? expf(s[nb][e] * p.scale - slse[c]) : 0.f;
+                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, slse[c]) : 0.f;
                     dp[nb][e] = on && !alone(i, geo.window, geo.sinks) ? s[nb][e] * (dp[nb][e] - sdelta[c]) : 0.f;
                 }
             }
@@ -506,7 +540,7 @@ struct WinPlan {
     WinGeom geo;
     int4 *tiles;
     int32_t *seq_tile;
-    float *delta, *part, *sums;
+    float *lse2, *delta, *part, *sums;
     size_t bytes;
 };
 WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks, bool packed, bool back, void *ws) {
@@ -531,6 +565,7 @@ WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks
         g.tiles = p.tiles, g.seq_tile = p.seq_tile;
     }
     if (back) {
+        p.lse2 = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         p.delta = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         if (sinks > 0) {
             p.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)g.ntiles * hk * sinks * d));
@@ -558,7 +593,7 @@ WinParams params(const WinPlan &p, const WinArgs &a) {
     w.q_stride = a.q_stride, w.k_stride = a.k_stride, w.v_stride = a.v_stride;
     w.scale = a.scale;
     w.o = a.o, w.dq = a.dq, w.dk = a.dk, w.dv = a.dv;
-    w.lse = a.lse, w.delta = p.delta, w.part = p.part, w.sums = p.sums;
+    w.lse = a.lse, w.lse2 = p.lse2, w.delta = p.delta, w.part = p.part, w.sums = p.sums;
     return w;
 }
 template <typename... P>
@@ -578,8 +613,8 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
     static std::atomic<uint64_t> allowed[4];
     constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(float);
     const WinParams w = params(p, a);
-    const int64_t rows = p.geo.tokens * a.hq;
-    win_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T *)a.out, (const T *)a.d_o, p.delta, rows);
+    win_delta_kernel<T, D><<<dim3((unsigned)((p.geo.tokens + 31) / 32), a.hq), 256, 0, s>>>(
+        (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq);
     KDA_TRY(cudaGetLastError());
     if (sizeof(T) == 2) {
         const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
@@ -590,8 +625,12 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
         win_far_sum_kernel<<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(p.geo, p.part, p.sums, D);
         KDA_TRY(cudaGetLastError());
     }
-    KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
-    return run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w);
+    if constexpr (sizeof(T) == 2) {
+        return launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.sums, s);
+    } else {
+        KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
+        return run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w);
+    }
 }
 
 }  // namespace

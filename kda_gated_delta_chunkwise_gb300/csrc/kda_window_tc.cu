@@ -372,6 +372,587 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     }
 }
 
+// ================================================================ backward: dk, dv
+// An item is 128 keys of one key head; a step is 128 queries of one of its query
+// heads, over the near pairs. Transposed scores, so that keys are the rows:
+//   S^T = K Q^T,  dP^T = V dO^T                      (TMEM)
+//   P^T = 2^{c S^T - lse}, over S^T;  dS^T = P^T (dP^T - D), over dP^T   (bf16)
+//   dV += P^T dO,  dK += dS^T Q                      (TMEM, all steps of the item)
+// so each tile of Q and dO serves as an operand both ways round and nothing is
+// transposed in memory. Issued in the order dV(n), S(n+1), dK(n), dP(n+1): the
+// tensor core has two products to do while P is made and two while dS is.
+// Queries behind the sequence's end count as zeros with an infinite lse.
+//
+// warp 0: TMA; 1: MMA; 2: lse and D of the queries; 4-11: P and dS, two threads a
+// key, 64 queries each (the halves of a bf16 row lie in the front of their 64
+// columns, so that no thread writes over scores that another one reads).
+constexpr int BW_THREADS = 384;
+template <int D> struct Bw {
+    static constexpr int TILE = 128 * D * 2, ATOM = 128 * 128;
+    static constexpr int QS = 3, OS = 2;                  // stages: of the operand of two steps, of one
+    static constexpr int RING_Q = 2 * TILE, RING_O = RING_Q + QS * TILE;
+    static constexpr int VEC = RING_O + OS * TILE;        // 128 of lse, 128 of D
+    static constexpr int BAR = VEC + 1024;
+    static constexpr int B_KF = 0, B_KE = 1, B_SF = 2, B_PR = 3, B_DF = 4, B_DR = 5, B_AF = 6, B_AE = 7, B_QF = 8,
+                         B_QE = B_QF + QS, B_OF = B_QE + QS, B_OE = B_OF + OS, B_LF = B_OE + OS, B_XF = B_LF + 1,
+                         B_LE = B_LF + 2, B_XE = B_LF + 3, COUNT = B_LF + 4;
+    static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+};
+
+struct BwArgs {
+    WinGeom geo;
+    __nv_bfloat16 *dq, *dk, *dv;
+    const float *lse2, *delta;  // [hq][tokens]: lse in powers of two, D
+    const float *sums;          // far gradients of the sinks (see kda_window.cu), nullable
+    float scale, c2;
+    int items;
+};
+
+template <int D>
+__global__ void __launch_bounds__(BW_THREADS, 1)
+win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+    using B = Bw<D>;
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + B::BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + B::COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WinGeom &geo = p.geo;
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < B::COUNT; ++i)
+            mbar_init(bar + i, i == B::B_PR || i == B::B_DR || i == B::B_AE || i >= B::B_LE ? 8 : 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    bool ok = true;
+    struct Item {
+        int seq, start, len, j0, hk, q0, nq, steps;  // q0: the first tile of 128 queries, nq: their number
+        __device__ __forceinline__ Item(const WinGeom &g, int it) {
+            const int t = g.by_hk.div(it);
+            hk = it - t * g.hk;
+            const WinTile x = win_tile(g, t >> 1);
+            seq = x.seq, start = x.start, len = x.len, j0 = x.first + (t & 1) * 128;
+            q0 = j0 >> 7;
+            nq = (int)min((int64_t)len - 1, (int64_t)j0 + 126 + g.window) / 128 - q0 + 1;
+            steps = j0 < len ? nq * g.group : 0;
+        }
+    };
+    struct Step {
+        int h, qt;
+        __device__ __forceinline__ Step(const WinGeom &g, const Item &x) : h(x.hk * g.group), qt(x.q0) {}
+        __device__ __forceinline__ void next(const Item &x) {
+            if (++qt == x.q0 + x.nq) qt = x.q0, ++h;
+        }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int n = 0, k = 0;  // steps, items so far
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const Item x(geo, it);
+                if (x.steps == 0) continue;
+                if (!(ok = ab.wait(bar + B::B_KE, (k & 1) ^ 1))) break;
+                ++k;
+                mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    tma_load_3d(sm + c * B::ATOM, &mk, bar + B::B_KF, 64 * c, x.hk, x.start + x.j0);
+                    tma_load_3d(sm + B::TILE + c * B::ATOM, &mv, bar + B::B_KF, 64 * c, x.hk, x.start + x.j0);
+                }
+                Step st(geo, x);
+                for (int j = 0; j < x.steps; ++j, ++n, st.next(x)) {
+                    const int qs = n % B::QS, os = n % B::OS, row = x.start + st.qt * 128;
+                    if (!(ok = ab.wait(bar + B::B_QE + qs, ((n / B::QS) & 1) ^ 1))) break;
+                    mbar_arrive_expect_tx(bar + B::B_QF + qs, B::TILE);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(sm + B::RING_Q + qs * B::TILE + c * B::ATOM, &mq, bar + B::B_QF + qs, 64 * c, st.h, row);
+                    if (!(ok = ab.wait(bar + B::B_OE + os, ((n / B::OS) & 1) ^ 1))) break;
+                    mbar_arrive_expect_tx(bar + B::B_OF + os, B::TILE);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(sm + B::RING_O + os * B::TILE + c * B::ATOM, &mo, bar + B::B_OF + os, 64 * c, st.h, row);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t I_S = idesc_bf16(128, 128, false, false), I_G = idesc_bf16(128, D, false, true);
+        const uint64_t kd = desc_k(smem_u32(sm)), vd = desc_k(smem_u32(sm + B::TILE));
+        int n = 0, k = 0;
+        auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
+        // scores (of: K, the ring of Q) or dP (V, the ring of dO) of a step's queries
+        auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int rows, int full) {
+            if (rows < 128) zero_rows<D>(tile, rows, 128);
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t b = desc_k(smem_u32(tile));
+                mma_ss<false>(d, a, b, I_S);
+#pragma unroll
+                for (int ks = 1; ks < D / 16; ++ks) mma_ss<true>(d, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), I_S);
+                umma_commit(bar + full);
+            }
+            __syncwarp();
+        };
+        // d (+)= the bf16 rows at `a` times the tile
+        auto gather = [&](uint32_t d, uint32_t a, unsigned char *tile, bool first) {
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t b = desc_mn(smem_u32(tile), B::ATOM);
+                if (first) umma_bf16_ts<false>(d, a, b, I_G);
+                else umma_bf16_ts<true>(d, a, b, I_G);
+#pragma unroll
+                for (int ks = 1; ks < 8; ++ks)
+                    umma_bf16_ts<true>(d, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](int b) {
+            if (lane == 0) umma_commit(bar + b);
+            __syncwarp();
+        };
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            if (!(ok = wait(B::B_KF, k))) break;
+            auto q_tile = [&](int i) { return sm + B::RING_Q + (i % B::QS) * B::TILE; };
+            auto o_tile = [&](int i) { return sm + B::RING_O + (i % B::OS) * B::TILE; };
+            Step st(geo, x);
+            if (!(ok = wait(B::B_QF + n % B::QS, n / B::QS))) break;
+            product(t_s, kd, q_tile(n), x.len - st.qt * 128, B::B_SF);
+            if (!(ok = wait(B::B_OF + n % B::OS, n / B::OS))) break;
+            product(t_dp, vd, o_tile(n), x.len - st.qt * 128, B::B_DF);
+            if (x.steps == 1) commit(B::B_KE);
+            for (int j = 0; j < x.steps; ++j, ++n) {
+                const bool more = j + 1 < x.steps;
+                st.next(x);
+                if (!(ok = wait(B::B_PR, n))) break;
+                if (j == 0 && !(ok = wait(B::B_AE, k + 1))) break;
+                gather(t_dv, t_s, o_tile(n), j == 0);
+                commit(B::B_OE + n % B::OS);
+                if (more) {
+                    if (!(ok = wait(B::B_QF + (n + 1) % B::QS, (n + 1) / B::QS))) break;
+                    product(t_s, kd, q_tile(n + 1), x.len - st.qt * 128, B::B_SF);
+                }
+                if (!(ok = wait(B::B_DR, n))) break;
+                gather(t_dk, t_dp, q_tile(n), j == 0);
+                commit(B::B_QE + n % B::QS);
+                if (more) {
+                    if (!(ok = wait(B::B_OF + (n + 1) % B::OS, (n + 1) / B::OS))) break;
+                    product(t_dp, vd, o_tile(n + 1), x.len - st.qt * 128, B::B_DF);
+                    if (j + 2 == x.steps) commit(B::B_KE);
+                } else {
+                    commit(B::B_AF);
+                }
+            }
+            ++k;
+        }
+    } else if (warp == 2) {
+        // four queries a lane; the next step's are on their way while this one's wait to be let in
+        int n = 0, it = blockIdx.x;
+        float *vec = reinterpret_cast<float *>(sm + B::VEC);
+        float l[4], d[4];
+        auto load = [&](const Item &x, const Step &st) {
+            const int i0 = st.qt * 128 + 4 * lane;
+            const int64_t at = (int64_t)st.h * geo.tokens + x.start + i0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool there = i0 + e < x.len;
+                l[e] = there ? __ldg(p.lse2 + at + e) : CUDART_INF_F;
+                d[e] = there ? __ldg(p.delta + at + e) : 0.f;
+            }
+        };
+        for (; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            Step st(geo, x);
+            load(x, st);
+            for (int j = 0; j < x.steps; ++j, ++n) {
+                const float4 lv = make_float4(l[0], l[1], l[2], l[3]), dv = make_float4(d[0], d[1], d[2], d[3]);
+                st.next(x);
+                if (j + 1 < x.steps) load(x, st);
+                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_LE, (n & 1) ^ 1));
+                if (!ok) break;
+                reinterpret_cast<float4 *>(vec)[lane] = lv;
+                warp_arrive(bar + B::B_LF);
+                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_XE, (n & 1) ^ 1));
+                if (!ok) break;
+                reinterpret_cast<float4 *>(vec + 128)[lane] = dv;
+                warp_arrive(bar + B::B_XF);
+            }
+        }
+    } else if (warp >= 4) {
+        const int half = (warp - 4) >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = t_s + lanes + 64 * half, td = t_dp + lanes + 64 * half;
+        int n = 0, k = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            const int j = x.j0 + row;  // this thread's key
+            Step st(geo, x);
+            for (int u = 0; u < x.steps; ++u, ++n, st.next(x)) {
+                const int i0 = st.qt * 128;
+                const float *vec = reinterpret_cast<const float *>(sm + B::VEC) + 64 * half;
+                const bool masked = i0 < x.j0 + 127 || i0 + 127 - x.j0 >= geo.window;
+                const int lo = j - i0 - 64 * half, hi = lo + geo.window - 1;  // columns of the half that see the key
+                float pr[64];
+                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_LF, n & 1) && ab.wait(bar + B::B_SF, n & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const F2 c2 = f2(p.c2, p.c2);
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t v[32], o[16];
+                    tmem_ld32(ts + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(vec + c + e);
+                        float a, b;
+                        f2_get(fma2(pair_w(v[e], v[e + 1]), c2, f2(-l.x, -l.y)), a, b);
+                        pr[c + e] = exp2_approx(a), pr[c + e + 1] = exp2_approx(b);
+                        f2_get(fma2(pair_w(v[e + 2], v[e + 3]), c2, f2(-l.z, -l.w)), a, b);
+                        pr[c + e + 2] = exp2_approx(a), pr[c + e + 3] = exp2_approx(b);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pr[c + e] = c + e < lo || c + e > hi ? 0.f : pr[c + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = pack2(pr[c + 2 * e], pr[c + 2 * e + 1]);
+                    if (c == 0) tmem_st16(ts, o);  // the second half's columns have not been read yet
+                    else tmem_st16(ts + 16, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar + B::B_PR);
+                warp_arrive(bar + B::B_LE);
+                if (masked) {  // a token that sees itself alone
+                    if (geo.window == 1 && geo.sinks == 0) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) pr[e] = 0.f;
+                    } else if (i0 == 0 && half == 0) {
+                        pr[0] = 0.f;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_XF, n & 1) && ab.wait(bar + B::B_DF, n & 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t v[32], o[16];
+                    tmem_ld32(td + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 d = *reinterpret_cast<const float4 *>(vec + 128 + c + e);
+                        const F2 one = f2(1.f, 1.f);
+                        o[e / 2] = pack2(fma2(pair_w(v[e], v[e + 1]), one, f2(-d.x, -d.y)) * f2(pr[c + e], pr[c + e + 1]));
+                        o[e / 2 + 1] =
+                            pack2(fma2(pair_w(v[e + 2], v[e + 3]), one, f2(-d.z, -d.w)) * f2(pr[c + e + 2], pr[c + e + 3]));
+                    }
+                    if (c == 0) tmem_st16(td, o);
+                    else tmem_st16(td + 16, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar + B::B_DR);
+                warp_arrive(bar + B::B_XE);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_AF, k & 1));
+            if (!ok) break;
+            ++k;
+            tc_fence_after();
+            // half 0: dv, half 1: dk
+            const bool there = j < x.len, sink = p.sums && j < geo.sinks;
+            const uint32_t src = (half ? t_dk : t_dv) + lanes;
+            const float f = half ? p.scale : 1.f;
+            __nv_bfloat16 *dst = (half ? p.dk : p.dv) + ((int64_t)(x.start + j) * geo.hk + x.hk) * D;
+            const float *far = p.sums + (((int64_t)x.seq * geo.hk + x.hk) * 2 * geo.sinks + (half ? 0 : geo.sinks) + j) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(src + c, v);
+                tmem_wait_ld();
+                if (!there) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), f, sink ? far[c + e] : 0.f));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = pack2(pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]));
+                    st_v8(dst + c + 16 * q, r);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(bar + B::B_AE);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ================================================================ backward: dq
+// An item is 128 queries of one head; a step is 128 keys (or the sinks, as in the
+// forward):
+//   S = Q K^T (two of it),  dP = dO V^T,  dS = P (dP - D) over S (bf16),  dQ += dS K
+// issued in the order S(n+1), dP(n+1), dQ(n): dS of a step is made while the tensor
+// core does dQ of the step before and S of the one behind. K is kept for two steps
+// (S and dQ), V for one.
+//
+// warp 0: TMA; 1: MMA; 4-11: dS, two threads a query, 64 keys each.
+template <int D>
+__global__ void __launch_bounds__(BW_THREADS, 1)
+win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                 const __grid_constant__ CUtensorMap mk16, const __grid_constant__ CUtensorMap mv16) {
+    using B = Bw<D>;  // the rings of K (Q's place) and V (dO's); the items' Q and dO in front
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + B::BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + B::COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WinGeom &geo = p.geo;
+    // KF, KE: the items' Q and dO; SF: of the two scores (SF, PR); DF, DR; AF, AE: dQ
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_AE ? 8 : 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm, t_dp = tmem + 256, t_dq = tmem + 384;  // S, S, dP, dQ
+    bool ok = true;
+    struct Item {
+        int start, len, i0, h, hk, far, kw, kt0, steps;
+        __device__ __forceinline__ Item(const WinGeom &g, int it) {
+            const int t = g.by_hq.div(it);
+            h = it - t * g.hq;
+            hk = h / g.group;
+            const WinTile x = win_tile(g, t >> 1);
+            start = x.start, len = x.len, i0 = x.first + (t & 1) * 128;
+            const int last = min(i0 + 128, len) - 1;
+            far = g.sinks > 0 && last >= g.window;
+            kw = far ? (min(g.sinks, last - g.window + 1) + 15) & ~15 : 0;
+            kt0 = max(0, i0 - g.window + 1) >> 7;
+            steps = i0 < len ? far + (i0 >> 7) - kt0 + 1 : 0;
+        }
+        __device__ __forceinline__ bool is_far(int j) const { return j < far; }
+        __device__ __forceinline__ int key0(int j) const { return is_far(j) ? 0 : (kt0 + j - far) * 128; }
+        __device__ __forceinline__ int keys(int j) const { return is_far(j) ? kw : 128; }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int n = 0, k = 0;
+            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+                const Item x(geo, it);
+                if (x.steps == 0) continue;
+                if (!(ok = ab.wait(bar + B::B_KE, (k & 1) ^ 1))) break;
+                ++k;
+                mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    tma_load_3d(sm + c * B::ATOM, &mq, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
+                    tma_load_3d(sm + B::TILE + c * B::ATOM, &mo, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
+                }
+                auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, unsigned char *d, int full, int j) {
+                    mbar_arrive_expect_tx(bar + full, x.keys(j) * D * 2);
+                    const int row = x.start + x.key0(j);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        if (!x.is_far(j)) tma_load_3d(d + c * B::ATOM, whole, bar + full, 64 * c, x.hk, row);
+                        else
+                            for (int r = 0; r < x.kw; r += 16)
+                                tma_load_3d(d + c * B::ATOM + r * 128, few, bar + full, 64 * c, x.hk, row + r);
+                    }
+                };
+                for (int j = 0; j < x.steps; ++j, ++n) {
+                    const int ks = n % B::QS, vs = n % B::OS;
+                    if (!(ok = ab.wait(bar + B::B_QE + ks, ((n / B::QS) & 1) ^ 1))) break;
+                    keys(&mk, &mk16, sm + B::RING_Q + ks * B::TILE, B::B_QF + ks, j);
+                    if (!(ok = ab.wait(bar + B::B_OE + vs, ((n / B::OS) & 1) ^ 1))) break;
+                    keys(&mv, &mv16, sm + B::RING_O + vs * B::TILE, B::B_OF + vs, j);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t I_G = idesc_bf16(128, D, false, true);
+        const uint64_t qd = desc_k(smem_u32(sm)), od = desc_k(smem_u32(sm + B::TILE));
+        int n = 0, k = 0;
+        auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
+        auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int keys, int full) {
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t idesc = idesc_bf16(128, keys, false, false);
+                const uint64_t b = desc_k(smem_u32(tile));
+                mma_ss<false>(d, a, b, idesc);
+#pragma unroll
+                for (int ks = 1; ks < D / 16; ++ks) mma_ss<true>(d, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), idesc);
+                umma_commit(bar + full);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](int b) {
+            if (lane == 0) umma_commit(bar + b);
+            __syncwarp();
+        };
+        auto k_tile = [&](int i) { return sm + B::RING_Q + (i % B::QS) * B::TILE; };
+        auto v_tile = [&](int i) { return sm + B::RING_O + (i % B::OS) * B::TILE; };
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            // keys behind the sequence's end are masked, but their rows of K meet the zeros of dS
+            auto scores = [&](int j, int i) {
+                if (!(ok = wait(B::B_QF + i % B::QS, i / B::QS))) return;
+                const int behind = x.len - x.key0(j);
+                if (behind < x.keys(j)) zero_rows<D>(k_tile(i), behind, x.keys(j));
+                product(tmem + 128 * (i & 1), qd, k_tile(i), x.keys(j), B::B_SF + (i & 1));
+            };
+            auto dp = [&](int j, int i) {
+                if (!(ok = wait(B::B_OF + i % B::OS, i / B::OS))) return;
+                product(t_dp, od, v_tile(i), x.keys(j), B::B_DF);
+                commit(B::B_OE + i % B::OS);
+                if (j + 1 == x.steps) commit(B::B_KE);  // Q and dO have been used for the last time
+            };
+            if (!(ok = wait(B::B_KF, k))) break;
+            scores(0, n);
+            if (ok) dp(0, n);
+            for (int j = 0; j < x.steps && ok; ++j, ++n) {
+                const bool more = j + 1 < x.steps;
+                if (more) {
+                    scores(j + 1, n + 1);
+                    if (!ok) break;
+                }
+                if (!(ok = wait(B::B_DR, n))) break;
+                if (more) {
+                    dp(j + 1, n + 1);
+                    if (!ok) break;
+                }
+                if (j == 0 && !(ok = wait(B::B_AE, k + 1))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t a = tmem + 128 * (n & 1);
+                    const uint64_t b = desc_mn(smem_u32(k_tile(n)), B::ATOM);
+                    if (j == 0) umma_bf16_ts<false>(t_dq, a, b, I_G);
+                    else umma_bf16_ts<true>(t_dq, a, b, I_G);
+                    const int count = x.keys(j) / 16;
+                    for (int ks = 1; ks < count; ++ks)
+                        umma_bf16_ts<true>(t_dq, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G);
+                    umma_commit(bar + B::B_QE + n % B::QS);
+                    if (!more) umma_commit(bar + B::B_AF);
+                }
+                __syncwarp();
+            }
+            ++k;
+        }
+    } else if (warp >= 4) {
+        const int half = (warp - 4) >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, td = t_dp + lanes + 64 * half;
+        int n = 0, k = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            const int i = x.i0 + row;
+            const bool there = i < x.len;
+            const int64_t at = (int64_t)x.h * geo.tokens + x.start + i;
+            const float lse2 = there ? p.lse2[at] : CUDART_INF_F, delta = there ? p.delta[at] : 0.f;
+            const bool single = i == 0 || (geo.window == 1 && geo.sinks == 0);  // sees itself alone
+            const F2 c2 = f2(p.c2, p.c2), l2 = f2(-lse2, -lse2), d2 = f2(-delta, -delta), one = f2(1.f, 1.f);
+            for (int j = 0; j < x.steps; ++j, ++n) {
+                const bool far = x.is_far(j);
+                const int k0 = x.key0(j) + 64 * half, chunks = min(2, (x.keys(j) - 64 * half + 31) >> 5);
+                const int hi = (far ? min(geo.sinks, i - geo.window + 1) - 1 - 64 * half : single ? -1 : i - k0),
+                          lo = far ? 0 : i - geo.window + 1 - k0;
+                const bool masked = far || x.key0(j) + 127 > x.i0 || x.key0(j) < x.i0 + 127 - geo.window + 1;
+                const uint32_t ts = tmem + 128 * (n & 1) + lanes + 64 * half;
+                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_SF + (n & 1), (n >> 1) & 1) && ab.wait(bar + B::B_DF, n & 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u >= chunks) break;
+                    uint32_t v[32], d[32], o[16];
+                    tmem_ld32(ts + 32 * u, v);
+                    tmem_ld32(td + 32 * u, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b, da, db;
+                        f2_get(fma2(pair_w(v[e], v[e + 1]), c2, l2), a, b);
+                        f2_get(fma2(pair_w(d[e], d[e + 1]), one, d2) * f2(exp2_approx(a), exp2_approx(b)), da, db);
+                        if (masked) {
+                            const int c = 32 * u + e;
+                            da = c < lo || c > hi ? 0.f : da;
+                            db = c + 1 < lo || c + 1 > hi ? 0.f : db;
+                        }
+                        o[e / 2] = pack2(da, db);
+                    }
+                    tmem_st16(ts + 16 * u, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar + B::B_DR);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_AF, k & 1));
+            if (!ok) break;
+            ++k;
+            tc_fence_after();
+            __nv_bfloat16 *dst = p.dq + ((int64_t)(x.start + i) * geo.hq + x.h) * D;
+            const F2 sc = f2(p.scale, p.scale);
+#pragma unroll 1
+            for (int c = D / 2 * half; c < D / 2 * (half + 1); c += 32) {
+                uint32_t v[32];
+                tmem_ld32(t_dq + lanes + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = pack2(pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]) * sc);
+                    if (there) st_v8(dst + c + 16 * q, r);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(bar + B::B_AE);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ================================================================ host side
 // [tokens][H][D] bf16 with a token stride, boxes of 64 channels x 1 head x `rows` tokens.
 template <int D> bool token_map(CUtensorMap *m, const void *ptr, int64_t stride, int H, int64_t tokens, int rows) {
@@ -402,7 +983,38 @@ template <int D> cudaError_t forward(const WinGeom &geo, const WinArgs &a, cudaS
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta, const float *sums,
+                     cudaStream_t s) {
+    CUtensorMap mq, mk, mv, mo, mk16, mv16;
+    if (!token_map<D>(&mq, a.q, a.q_stride, a.hq, geo.tokens, 128) ||
+        !token_map<D>(&mk, a.k, a.k_stride, a.hk, geo.tokens, 128) ||
+        !token_map<D>(&mv, a.v, a.v_stride, a.hk, geo.tokens, 128) ||
+        !token_map<D>(&mo, a.d_o, (int64_t)a.hq * D, a.hq, geo.tokens, 128) ||
+        !token_map<D>(&mk16, a.k, a.k_stride, a.hk, geo.tokens, 16) ||
+        !token_map<D>(&mv16, a.v, a.v_stride, a.hk, geo.tokens, 16))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> allowed[2];
+    cudaError_t e = allow_smem(win_dkv_tc_kernel<D>, Bw<D>::SMEM, allowed[0]);
+    if (e == cudaSuccess) e = allow_smem(win_dq_tc_kernel<D>, Bw<D>::SMEM, allowed[1]);
+    if (e != cudaSuccess) return e;
+    BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, sums,
+             a.scale, a.scale * 1.4426950408889634f, geo.ntiles * 2 * geo.hk};
+    const int sms = sm_count();
+    win_dkv_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, s>>>(p, mq, mk, mv, mo);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.items = geo.ntiles * 2 * geo.hq;
+    win_dq_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, s>>>(p, mq, mk, mv, mo, mk16, mv16);
+    return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_window_backward_tc(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta,
+                                      const float *sums, cudaStream_t s) {
+    return a.d == 128 ? backward<128>(geo, a, lse2, delta, sums, s) : backward<64>(geo, a, lse2, delta, sums, s);
+}
 
 cudaError_t launch_window_forward_tc(const WinGeom &geo, const WinArgs &a, cudaStream_t s) {
     return a.d == 128 ? forward<128>(geo, a, s) : forward<64>(geo, a, s);
