@@ -34,16 +34,19 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
 // leave the issue slots to the warps that work. One microsecond keeps a bound
 // on the number of rounds a bound on the time as well.
 constexpr uint32_t kSuspendNs = 1000;
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {  // a shared-memory address
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
     return done != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+    return mbar_try_wait(smem_u32(bar), parity);
 }
 
 // Non-blocking probe of a phase (never suspends).

@@ -32,6 +32,23 @@ struct Abort {
         }
         return true;
     }
+    // The same with the waiting itself out of line, for roles whose loops are to stay short for the instruction
+    // cache; all lanes of a warp.
+    __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) const {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (*flag) return false;
+            if (clock64() - t0 > kWaitCycles) {
+                *flag = 1;
+                atomicOr(&g_tc_error, 1);
+                return false;
+            }
+        }
+        return true;
+    }
+    __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_on(bar, parity));
+    }
 };
 // One arrival for the warp, after all its lanes have come here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {

@@ -15,6 +15,11 @@
 namespace kda {
 namespace {
 
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // Rows first .. 127 of a K-major (or, the same layout, MN-major) tile of D
@@ -41,8 +46,8 @@ template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, 
 // weights are taken against the older maximum until then, up to 2^8, which fp32
 // sums and bf16 weights carry as well.
 //
-// warp 0: TMA; 1: MMA (and zeros behind a sequence's end); 4-7, 8-11: the rows of
-// the contexts, a thread each.
+// warp 0: TMA; 1, 2: MMA of the contexts (and zeros behind a sequence's end); 4-7,
+// 8-11: the rows of the contexts, a thread each.
 constexpr int FW_THREADS = 384;
 template <int D> struct Fw {
     static constexpr int TILE = 128 * D * 2;
@@ -67,9 +72,8 @@ struct FwArgs {
 struct FwItem {
     int start, len, f, rows, h, hk;  // f: the tile's first token in its sequence
     int far, kw;                     // whether there is a step of the sinks, and its keys
-    int kt0, steps;                  // first near tile of 128 keys
-    int nf[2], diag[2];              // near tiles of the contexts
-    bool far_of[2];
+    int nf0, nf1, diag0, steps;      // tiles of 128 keys: the contexts' first near ones, the first's last one
+    bool far0;                       // the first context sees sinks behind its window (the last context does if any)
     __device__ __forceinline__ FwItem(const WinGeom &g, int it) {
         const int t = g.by_hq.div(it);
         h = it - t * g.hq;
@@ -80,22 +84,18 @@ struct FwItem {
         const int last = f + rows - 1;
         far = g.sinks > 0 && last >= g.window;
         kw = far ? (min(g.sinks, last - g.window + 1) + 15) & ~15 : 0;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            nf[w] = max(0, f + 128 * w - g.window + 1) >> 7;
-            diag[w] = (f >> 7) + w;
-            far_of[w] = far && rows > 128 * w && min(last, f + 128 * w + 127) >= g.window;
-        }
-        kt0 = nf[0];
-        steps = rows > 0 ? far + diag[rows > 128] - kt0 + 1 : 0;
+        far0 = far && min(last, f + 127) >= g.window;
+        nf0 = max(0, f - g.window + 1) >> 7;
+        nf1 = max(0, f + 128 - g.window + 1) >> 7;
+        diag0 = f >> 7;
+        steps = rows > 0 ? far + diag0 - nf0 + 1 + (rows > 128) : 0;
     }
     __device__ __forceinline__ bool is_far(int j) const { return j < far; }
-    __device__ __forceinline__ int tile(int j) const { return kt0 + j - far; }
+    __device__ __forceinline__ int tile(int j) const { return nf0 + j - far; }
+    __device__ __forceinline__ int last(int w) const { return far + diag0 - nf0 + w; }  // a context's last step
     __device__ __forceinline__ bool uses(int w, int j) const {
-        if (rows <= 128 * w) return false;
-        if (is_far(j)) return far_of[w];
-        const int kt = tile(j);
-        return kt >= nf[w] && kt <= diag[w];
+        if (w == 0) return is_far(j) ? far0 : j <= last(0);
+        return rows > 128 && (is_far(j) || tile(j) >= nf1);
     }
     __device__ __forceinline__ int key0(int j) const { return is_far(j) ? 0 : tile(j) * 128; }
     __device__ __forceinline__ int keys(int j) const { return is_far(j) ? kw : 128; }
@@ -117,7 +117,9 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     if (tid == 0) {
         *ab.flag = 0;
         for (int i = 0; i < F::COUNT; ++i)
-            mbar_init(bar + i, (i >= F::B_PF && i < F::B_OF) || (i >= F::B_OE && i < F::B_KF) ? 4 : 1);
+            mbar_init(bar + i, (i >= F::B_PF && i < F::B_OF) || (i >= F::B_OE && i < F::B_KF) ? 4
+                               : i == F::B_QE || i >= F::B_KE                                 ? 2
+                                                                                              : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -130,19 +132,20 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     const uint32_t tmem = *tm;  // S_0 | S_1 | O_0 | O_1
     bool ok = true;
 
+    // 384 threads of 168 registers become 128 of 88 and 256 of 208
+    if (warp < 4) regs_dec<88>();
     if (warp == 0) {
-        if (lane == 0) {
-            prefetch_tmap(&mq);
-            prefetch_tmap(&mk);
-            prefetch_tmap(&mv);
-            int n = 0, q = 0;  // stages, items so far
-            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-                const FwItem x(geo, it);
-                if (x.steps == 0) continue;
-                auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, int j) {
-                    const int s = n % F::STAGES;
-                    if (!(ok = ab.wait(bar + F::B_KE + s, ((n / F::STAGES) & 1) ^ 1))) return;
-                    ++n;
+        // A whole warp waits, one lane copies: with one lane in a wait and the others past it the warp is woken by
+        // the wait's time limit alone, microseconds late.
+        int n = 0, q = 0;  // stages, items so far
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const FwItem x(geo, it);
+            if (x.steps == 0) continue;
+            auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, int j) {
+                const int s = n % F::STAGES;
+                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_KE + s, ((n / F::STAGES) & 1) ^ 1)))) return;
+                ++n;
+                if (lane == 0) {
                     unsigned char *d = sm + F::KV + s * F::TILE;
                     uint64_t *full = bar + F::B_KF + s;
                     mbar_arrive_expect_tx(full, x.keys(j) * D * 2);
@@ -154,107 +157,95 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
                             for (int r = 0; r < x.kw; r += 16)
                                 tma_load_3d(d + c * F::ATOM + r * 128, few, full, 64 * c, x.hk, row + r);
                     }
-                };
-                if (!(ok = ab.wait(bar + F::B_QE, (q & 1) ^ 1))) break;
-                ++q;
+                }
+                __syncwarp();
+            };
+            if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_QE, (q & 1) ^ 1)))) break;
+            ++q;
+            if (lane == 0) {
                 const int contexts = x.rows > 128 ? 2 : 1;
                 mbar_arrive_expect_tx(bar + F::B_QF, contexts * F::TILE);
                 for (int w = 0; w < contexts; ++w)
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(sm + w * F::TILE + c * F::ATOM, &mq, bar + F::B_QF, 64 * c, x.h,
-                                    x.start + x.f + 128 * w);
-                for (int j = 0; j < x.steps && ok; ++j) {
-                    keys(&mk, &mk16, j);
-                    if (ok) keys(&mv, &mv16, j);
-                }
+                        tma_load_3d(sm + w * F::TILE + c * F::ATOM, &mq, bar + F::B_QF, 64 * c, x.h, x.start + x.f + 128 * w);
+            }
+            __syncwarp();
+            for (int j = 0; j < x.steps && ok; ++j) {
+                keys(&mk, &mk16, j);
+                if (ok) keys(&mv, &mv16, j);
             }
         }
-    } else if (warp == 1) {
-        constexpr uint32_t I_O = idesc_bf16(128, D, false, true);
-        int n = 0, q = 0;                  // stages, items so far
-        int pv[2] = {0, 0}, oi[2] = {0, 0};  // softmax steps, items of the contexts
+    } else if (warp < 3) {
+        // A context's products. One thread issues them and is held up until the tensor core takes them, so what it
+        // does in between is time without a product of this context: hence two warps, and short loops.
+        const int w = warp - 1;
+        constexpr uint32_t I_O = idesc_bf16(128, D, false, true), I_S = idesc_bf16(128, 128, false, false);
+        const uint32_t bars = smem_u32(bar), kv = smem_u32(sm + F::KV), ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
+        const uint64_t qd = desc_k(smem_u32(sm + w * F::TILE)), kd = desc_k(kv), vd = desc_mn(kv, F::ATOM);
+        auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
+        auto commit = [&](int b) {
+            if (lane == 0) umma_commit(bar + b);
+            __syncwarp();
+        };
+        int s = 0, round = 0;       // the next stage and its phase
+        int q = 0, pv = 0, oi = 0;  // items so far; phases of P and O
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const FwItem x(geo, it);
             if (x.steps == 0) continue;
-            if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_QF, q & 1)))) break;
+            if (!(ok = wait(F::B_QF, q))) break;
             ++q;
-            // scores of step j, whose K is in stage s
-            auto scores = [&](int w, int j, int s) {
-                if (!x.uses(w, j)) return;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t d = tmem + 128 * w, idesc = idesc_bf16(128, x.keys(j), false, false);
-                    const uint64_t a = desc_k(smem_u32(sm + w * F::TILE)), b = desc_k(smem_u32(sm + F::KV + s * F::TILE));
-                    mma_ss<false>(d, a, b, idesc);
-#pragma unroll
-                    for (int ks = 1; ks < D / 16; ++ks)
-                        mma_ss<true>(d, a + step_k(ks, F::ATOM), b + step_k(ks, F::ATOM), idesc);
-                    umma_commit(bar + F::B_SF + w);
-                }
-                __syncwarp();
-            };
-            auto arrived = [&](int i) {  // stage of the i-th tile
-                return __all_sync(0xffffffffu, ab.wait(bar + F::B_KF + i % F::STAGES, (i / F::STAGES) & 1));
-            };
-            auto release = [&](int i) {
-                if (lane == 0) umma_commit(bar + F::B_KE + i % F::STAGES);
-                __syncwarp();
-            };
-            if (!(ok = arrived(n))) break;
-            scores(0, 0, n % F::STAGES);
-            scores(1, 0, n % F::STAGES);
-            release(n);
-            bool first[2] = {true, true};
-            int last[2] = {-1, -1};
-            for (int j = 0; j < x.steps; ++j)
-                for (int w = 0; w < 2; ++w)
-                    if (x.uses(w, j)) last[w] = j;
-            if (x.steps == 1 && lane == 0) umma_commit(bar + F::B_QE);
-            for (int j = 0; j < x.steps && ok; ++j) {
-                const int iv = n + 2 * j + 1, ik = iv + 1;  // this step's V, the next one's K
-                const bool more = j + 1 < x.steps;
-                if (!(ok = arrived(iv))) break;
-                unsigned char *v = sm + F::KV + (iv % F::STAGES) * F::TILE;
-                const int behind = x.len - x.key0(j);  // rows of V past the sequence's end may hold anything
-                if (behind < x.keys(j)) zero_rows<D>(v, behind, x.keys(j));
-                if (more && !(ok = arrived(ik))) break;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
+            bool first = true;
+            for (int j = -1; j < x.steps; ++j) {
+                if (j >= 0) {
+                    if (!(ok = wait(F::B_KF + s, round))) break;
                     if (x.uses(w, j)) {
-                        ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_PF + w, pv[w] & 1));
-                        if (!ok) break;
-                        ++pv[w];
-                        if (first[w] && !(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_OE + w, (oi[w] & 1) ^ 1)))) break;
+                        const int behind = x.len - x.key0(j);  // rows of V past the sequence's end may hold anything
+                        if (behind < x.keys(j)) zero_rows<D>(sm + F::KV + s * F::TILE, behind, x.keys(j));
+                        if (!(ok = wait(F::B_PF + w, pv++))) break;
+                        if (first && !(ok = wait(F::B_OE + w, ++oi))) break;
                         tc_fence_after();
                         if (lane == 0) {
-                            const uint32_t o = tmem + 256 + 128 * w, pt = tmem + 128 * w;
-                            const uint64_t b = desc_mn(smem_u32(v), F::ATOM);
-                            if (first[w]) umma_bf16_ts<false>(o, pt, b, I_O);
-                            else umma_bf16_ts<true>(o, pt, b, I_O);
+                            const uint64_t b = vd + s * (F::TILE >> 4);
+                            if (first) umma_bf16_ts<false>(to, ts, b, I_O);
+                            else umma_bf16_ts<true>(to, ts, b, I_O);
                             if (x.is_far(j)) {
-                                for (int ks = 1; ks < x.kw / 16; ++ks) umma_bf16_ts<true>(o, pt + ks * 8, b + step_mn(ks), I_O);
+#pragma unroll 1
+                                for (int ks = 1; ks < x.kw / 16; ++ks) umma_bf16_ts<true>(to, ts + ks * 8, b + step_mn(ks), I_O);
                             } else {
 #pragma unroll
-                                for (int ks = 1; ks < 8; ++ks) umma_bf16_ts<true>(o, pt + ks * 8, b + step_mn(ks), I_O);
+                                for (int ks = 1; ks < 8; ++ks) umma_bf16_ts<true>(to, ts + ks * 8, b + step_mn(ks), I_O);
                             }
-                            if (j == last[w]) umma_commit(bar + F::B_OF + w);
+                            if (j == x.last(w)) umma_commit(bar + F::B_OF + w);
                         }
                         __syncwarp();
-                        if (j == last[w]) ++oi[w];
-                        first[w] = false;
+                        first = false;
                     }
-                    if (more) scores(w, j + 1, ik % F::STAGES);
+                    commit(F::B_KE + s);
+                    if (++s == F::STAGES) s = 0, round ^= 1;
                 }
-                if (!ok) break;
-                release(iv);
-                if (more) release(ik);
-                if (j + 2 == x.steps && lane == 0) umma_commit(bar + F::B_QE);  // the last scores are on their way
-                __syncwarp();
+                if (j + 1 == x.steps) break;
+                if (!(ok = wait(F::B_KF + s, round))) break;
+                if (x.uses(w, j + 1)) {
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t idesc = x.is_far(j + 1) ? idesc_bf16(128, x.kw, false, false) : I_S;
+                        const uint64_t b = kd + s * (F::TILE >> 4);
+                        mma_ss<false>(ts, qd, b, idesc);
+#pragma unroll
+                        for (int ks = 1; ks < D / 16; ++ks)
+                            mma_ss<true>(ts, qd + step_k(ks, F::ATOM), b + step_k(ks, F::ATOM), idesc);
+                        umma_commit(bar + F::B_SF + w);
+                    }
+                    __syncwarp();
+                }
+                commit(F::B_KE + s);
+                if (++s == F::STAGES) s = 0, round ^= 1;
+                if (j + 2 == x.steps) commit(F::B_QE);  // the last scores are on their way
             }
-            n += 2 * x.steps;
         }
     } else if (warp >= 4) {
+        regs_inc<208>();
         const int w = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
         int sf = 0, of = 0;
@@ -271,65 +262,105 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
                 if (!ok) break;
                 ++sf;
                 tc_fence_after();
-                const bool far = x.is_far(j);
-                const int k0 = x.key0(j), chunks = far ? (x.kw + 31) >> 5 : 4;
-                // columns lo .. hi are seen; the whole tile by every row of the context: no masks
-                const int hi = far ? min(geo.sinks, i - geo.window + 1) - 1 : i - k0, lo = far ? 0 : i - geo.window + 1 - k0;
-                const bool masked = far || k0 + 127 > x.f + 128 * w || k0 < x.f + 128 * w + 127 - geo.window + 1;
-                auto mask = [&](uint32_t (&s)[32], int c) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        s[e] = c + e < lo || c + e > hi ? 0xff800000u : s[e];
-                };
-                float top = -CUDART_INF_F;
-                uint32_t s[32];
-                for (int c = 0; c < chunks; ++c) {
-                    tmem_ld32(ts + 32 * c, s);
-                    tmem_wait_ld();
-                    if (masked) mask(s, 32 * c);
-                    float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-                    for (int e = 2; e < 32; e += 2)
-                        a = fmaxf(a, __uint_as_float(s[e])), b = fmaxf(b, __uint_as_float(s[e + 1]));
-                    top = max3(top, a, b);
-                }
-                const bool grow = (top - m) * p.c2 > 8.f;  // also the first number that a row sees
-                if (!first && __any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? exp2_approx((m - top) * p.c2) : 1.f;
-                    const F2 ff = f2(f, f);
-                    l = l * ff;
+                // O and the sum so far, when the maximum has grown from m to `top` by more than 2^8 (also when the
+                // row sees its first number)
+                auto rescale = [&](float top) {
+                    const bool grow = (top - m) * p.c2 > 8.f;
+                    if (!first && __any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? exp2_approx((m - top) * p.c2) : 1.f;
+                        const F2 ff = f2(f, f);
+                        l = l * ff;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a, b;
-                            f2_get(pair_w(o[e], o[e + 1]) * ff, a, b);
-                            o[e] = __float_as_uint(a), o[e + 1] = __float_as_uint(b);
+                            for (int e = 0; e < 32; e += 2) {
+                                float u, v;
+                                f2_get(pair_w(o[e], o[e + 1]) * ff, u, v);
+                                o[e] = __float_as_uint(u), o[e + 1] = __float_as_uint(v);
+                            }
+                            tmem_st32(to + c, o);
                         }
-                        tmem_st32(to + c, o);
                     }
-                }
-                if (grow) m = top;
-                first = false;
-                const float off = m == -CUDART_INF_F ? 0.f : -m * p.c2;
-                const F2 c2 = f2(p.c2, p.c2), off2 = f2(off, off);
-                for (int c = 0; c < chunks; ++c) {
-                    tmem_ld32(ts + 32 * c, s);
-                    tmem_wait_ld();
-                    if (masked) mask(s, 32 * c);
+                    if (grow) m = top;
+                    first = false;
+                };
+                // 32 weights from their scores, over the front of the columns
+                auto weights = [&](uint32_t (&s)[32], int c) {
+                    const float off = m == -CUDART_INF_F ? 0.f : -m * p.c2;
+                    const F2 c2 = f2(p.c2, p.c2), off2 = f2(off, off);
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        f2_get(fma2(pair_w(s[e], s[e + 1]), c2, off2), a, b);
-                        a = exp2_approx(a), b = exp2_approx(b);
-                        l = fma2(f2(a, b), f2(1.f, 1.f), l);
-                        o[e / 2] = pack2(a, b);
+                        float u, v;
+                        f2_get(fma2(pair_w(s[e], s[e + 1]), c2, off2), u, v);
+                        const F2 w2 = f2(exp2_approx(u), exp2_approx(v));
+                        l = l + w2;
+                        o[e / 2] = pack2(w2);
                     }
-                    tmem_st16(ts + 16 * c, o);  // over columns that have been read
+                    tmem_st16(ts + 16 * c, o);
+                };
+                auto largest = [](const uint32_t (&s)[32]) {
+                    float t[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(s[e]);
+#pragma unroll
+                    for (int e = 4; e < 28; e += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            t[u] = max3(t[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + u + 4]));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) t[u] = fmaxf(t[u], __uint_as_float(s[28 + u]));
+                    return fmaxf(max3(t[0], t[1], t[2]), t[3]);
+                };
+                constexpr uint32_t NONE = 0xff800000u;  // -inf
+                if (x.is_far(j)) {  // the sinks: a few columns, all of them with masks
+                    const int hi = min(geo.sinks, i - geo.window + 1) - 1, chunks = (x.kw + 31) >> 5;
+                    float top = -CUDART_INF_F;
+                    uint32_t s[32];
+                    auto load = [&](int c) {
+                        tmem_ld32(ts + 32 * c, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = 32 * c + e > hi ? NONE : s[e];
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        load(c);
+                        top = fmaxf(top, largest(s));
+                    }
+                    rescale(fmaxf(top, m));
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        load(c);
+                        weights(s, c);
+                    }
+                } else {
+                    // the whole row in registers; a chunk's weights go over columns that have all been read
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+                    tmem_wait_ld();
+                    const int k0 = x.key0(j);
+                    if (k0 + 127 > x.f + 128 * w) {  // some row does not see the last keys, or the first ones
+                        const int hi = i - k0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[c][e] = 32 * c + e > hi ? NONE : s[c][e];
+                    }
+                    if (k0 < x.f + 128 * w + 128 - geo.window) {
+                        const int lo = i - geo.window + 1 - k0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[c][e] = 32 * c + e < lo ? NONE : s[c][e];
+                    }
+                    rescale(fmaxf(max3(largest(s[0]), largest(s[1]), m), fmaxf(largest(s[2]), largest(s[3]))));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) weights(s[c], c);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -395,7 +426,8 @@ template <int D> struct Bw {
     static constexpr int BAR = VEC + 1024;
     static constexpr int B_KF = 0, B_KE = 1, B_SF = 2, B_PR = 3, B_DF = 4, B_DR = 5, B_AF = 6, B_AE = 7, B_QF = 8,
                          B_QE = B_QF + QS, B_OF = B_QE + QS, B_OE = B_OF + OS, B_LF = B_OE + OS, B_XF = B_LF + 1,
-                         B_LE = B_LF + 2, B_XE = B_LF + 3, COUNT = B_LF + 4;
+                         B_LE = B_LF + 2, B_XE = B_LF + 3, COUNT = B_LF + 4,
+                         B_DL = B_LE, B_DR1 = B_XE;  // in dq's kernel, which has no vectors
     static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory of a block");
 };
@@ -456,41 +488,46 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
         }
     };
 
+    auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
+
     if (warp == 0) {
-        if (lane == 0) {
-            int n = 0, k = 0;  // steps, items so far
-            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-                const Item x(geo, it);
-                if (x.steps == 0) continue;
-                if (!(ok = ab.wait(bar + B::B_KE, (k & 1) ^ 1))) break;
-                ++k;
+        int n = 0, k = 0;  // steps, items so far
+        auto tile = [&](unsigned char *d, const CUtensorMap *m, int full, int h, int row) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) tma_load_3d(d + c * B::ATOM, m, bar + full, 64 * c, h, row);
+        };
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            if (!(ok = wait(B::B_KE, k + 1))) break;
+            ++k;
+            if (lane == 0) {
                 mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_3d(sm + c * B::ATOM, &mk, bar + B::B_KF, 64 * c, x.hk, x.start + x.j0);
-                    tma_load_3d(sm + B::TILE + c * B::ATOM, &mv, bar + B::B_KF, 64 * c, x.hk, x.start + x.j0);
-                }
-                Step st(geo, x);
-                for (int j = 0; j < x.steps; ++j, ++n, st.next(x)) {
-                    const int qs = n % B::QS, os = n % B::OS, row = x.start + st.qt * 128;
-                    if (!(ok = ab.wait(bar + B::B_QE + qs, ((n / B::QS) & 1) ^ 1))) break;
+                tile(sm, &mk, B::B_KF, x.hk, x.start + x.j0);
+                tile(sm + B::TILE, &mv, B::B_KF, x.hk, x.start + x.j0);
+            }
+            __syncwarp();
+            Step st(geo, x);
+            for (int j = 0; j < x.steps; ++j, ++n, st.next(x)) {
+                const int qs = n % B::QS, os = n % B::OS, row = x.start + st.qt * 128;
+                if (!(ok = wait(B::B_QE + qs, n / B::QS + 1))) break;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(bar + B::B_QF + qs, B::TILE);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(sm + B::RING_Q + qs * B::TILE + c * B::ATOM, &mq, bar + B::B_QF + qs, 64 * c, st.h, row);
-                    if (!(ok = ab.wait(bar + B::B_OE + os, ((n / B::OS) & 1) ^ 1))) break;
-                    mbar_arrive_expect_tx(bar + B::B_OF + os, B::TILE);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(sm + B::RING_O + os * B::TILE + c * B::ATOM, &mo, bar + B::B_OF + os, 64 * c, st.h, row);
+                    tile(sm + B::RING_Q + qs * B::TILE, &mq, B::B_QF + qs, st.h, row);
                 }
+                __syncwarp();
+                if (!(ok = wait(B::B_OE + os, n / B::OS + 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar + B::B_OF + os, B::TILE);
+                    tile(sm + B::RING_O + os * B::TILE, &mo, B::B_OF + os, st.h, row);
+                }
+                __syncwarp();
             }
         }
     } else if (warp == 1) {
         constexpr uint32_t I_S = idesc_bf16(128, 128, false, false), I_G = idesc_bf16(128, D, false, true);
         const uint64_t kd = desc_k(smem_u32(sm)), vd = desc_k(smem_u32(sm + B::TILE));
         int n = 0, k = 0;
-        auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
         // scores (of: K, the ring of Q) or dP (V, the ring of dO) of a step's queries
         auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int rows, int full) {
             if (rows < 128) zero_rows<D>(tile, rows, 128);
@@ -603,66 +640,68 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
             for (int u = 0; u < x.steps; ++u, ++n, st.next(x)) {
                 const int i0 = st.qt * 128;
                 const float *vec = reinterpret_cast<const float *>(sm + B::VEC) + 64 * half;
-                const bool masked = i0 < x.j0 + 127 || i0 + 127 - x.j0 >= geo.window;
                 const int lo = j - i0 - 64 * half, hi = lo + geo.window - 1;  // columns of the half that see the key
                 float pr[64];
                 ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_LF, n & 1) && ab.wait(bar + B::B_SF, n & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const F2 c2 = f2(p.c2, p.c2);
+                uint32_t v[2][32];
+                tmem_ld32(ts, v[0]);
+                tmem_ld32(ts + 32, v[1]);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t v[32], o[16];
-                    tmem_ld32(ts + c, v);
-                    tmem_wait_ld();
+                for (int c = 0; c < 64; c += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(vec + c);
+                    const uint32_t *y = v[c >> 5] + (c & 31);
+                    float a, b;
+                    f2_get(fma2(pair_w(y[0], y[1]), c2, f2(-l.x, -l.y)), a, b);
+                    pr[c] = exp2_approx(a), pr[c + 1] = exp2_approx(b);
+                    f2_get(fma2(pair_w(y[2], y[3]), c2, f2(-l.z, -l.w)), a, b);
+                    pr[c + 2] = exp2_approx(a), pr[c + 3] = exp2_approx(b);
+                }
+                if (i0 < x.j0 + 127) {  // some query comes before the key, or too far behind it
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 l = *reinterpret_cast<const float4 *>(vec + c + e);
-                        float a, b;
-                        f2_get(fma2(pair_w(v[e], v[e + 1]), c2, f2(-l.x, -l.y)), a, b);
-                        pr[c + e] = exp2_approx(a), pr[c + e + 1] = exp2_approx(b);
-                        f2_get(fma2(pair_w(v[e + 2], v[e + 3]), c2, f2(-l.z, -l.w)), a, b);
-                        pr[c + e + 2] = exp2_approx(a), pr[c + e + 3] = exp2_approx(b);
-                    }
-                    if (masked) {
+                    for (int c = 0; c < 64; ++c) pr[c] = c < lo ? 0.f : pr[c];
+                }
+                if (i0 + 127 - x.j0 >= geo.window) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) pr[c + e] = c + e < lo || c + e > hi ? 0.f : pr[c + e];
-                    }
+                    for (int c = 0; c < 64; ++c) pr[c] = c > hi ? 0.f : pr[c];
+                }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = pack2(pr[c + 2 * e], pr[c + 2 * e + 1]);
-                    if (c == 0) tmem_st16(ts, o);  // the second half's columns have not been read yet
-                    else tmem_st16(ts + 16, o);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = pack2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
+                    tmem_st16(ts + 16 * c, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar + B::B_PR);
                 warp_arrive(bar + B::B_LE);
-                if (masked) {  // a token that sees itself alone
-                    if (geo.window == 1 && geo.sinks == 0) {
+                // a token that sees itself alone has no ds
+                if (i0 == 0 && half == 0) pr[0] = 0.f;
+                if (geo.window == 1 && geo.sinks == 0) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) pr[e] = 0.f;
-                    } else if (i0 == 0 && half == 0) {
-                        pr[0] = 0.f;
-                    }
+                    for (int e = 0; e < 64; ++e) pr[e] = 0.f;
                 }
                 ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_XF, n & 1) && ab.wait(bar + B::B_DF, n & 1));
                 if (!ok) break;
                 tc_fence_after();
+                tmem_ld32(td, v[0]);
+                tmem_ld32(td + 32, v[1]);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t v[32], o[16];
-                    tmem_ld32(td + c, v);
-                    tmem_wait_ld();
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 d = *reinterpret_cast<const float4 *>(vec + 128 + c + e);
-                        const F2 one = f2(1.f, 1.f);
-                        o[e / 2] = pack2(fma2(pair_w(v[e], v[e + 1]), one, f2(-d.x, -d.y)) * f2(pr[c + e], pr[c + e + 1]));
-                        o[e / 2 + 1] =
-                            pack2(fma2(pair_w(v[e + 2], v[e + 3]), one, f2(-d.z, -d.w)) * f2(pr[c + e + 2], pr[c + e + 3]));
+                        const float4 d = *reinterpret_cast<const float4 *>(vec + 128 + 32 * c + e);
+                        const float *w = pr + 32 * c + e;
+                        o[e / 2] = pack2((pair_w(v[c][e], v[c][e + 1]) + f2(-d.x, -d.y)) * f2(w[0], w[1]));
+                        o[e / 2 + 1] = pack2((pair_w(v[c][e + 2], v[c][e + 3]) + f2(-d.z, -d.w)) * f2(w[2], w[3]));
                     }
-                    if (c == 0) tmem_st16(td, o);
-                    else tmem_st16(td + 16, o);
+                    tmem_st16(td + 16 * c, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -715,8 +754,9 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 // An item is 128 queries of one head; a step is 128 keys (or the sinks, as in the
 // forward):
 //   S = Q K^T (two of it),  dP = dO V^T,  dS = P (dP - D) over S (bf16),  dQ += dS K
-// issued in the order S(n+1), dP(n+1), dQ(n): dS of a step is made while the tensor
-// core does dQ of the step before and S of the one behind. K is kept for two steps
+// issued in the order S(n+1), dP(n+1), dQ(n), where dP(n+1) waits until dP(n) is in
+// registers and dQ(n) until dS(n) is made: dS of a step is made while the tensor
+// core does dQ of the step before and S and dP of the one behind. K is kept for two steps
 // (S and dQ), V for one.
 //
 // warp 0: TMA; 1: MMA; 4-11: dS, two threads a query, 64 keys each.
@@ -736,7 +776,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     // KF, KE: the items' Q and dO; SF: of the two scores (SF, PR); DF, DR; AF, AE: dQ
     if (tid == 0) {
         *ab.flag = 0;
-        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_AE ? 8 : 1);
+        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_DR1 || i == B::B_AE || i == B::B_DL ? 8 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -748,6 +788,9 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     tc_fence_after();
     const uint32_t tmem = *tm, t_dp = tmem + 256, t_dq = tmem + 384;  // S, S, dP, dQ
     bool ok = true;
+    // A warp may be through with dS of a step before another is with the step before: dP of it waits for
+    // nobody's dS. So there are two barriers of dS, in turn.
+    auto made = [](int n) { return n & 1 ? B::B_DR1 : B::B_DR; };
     struct Item {
         int start, len, i0, h, hk, far, kw, kt0, steps;
         __device__ __forceinline__ Item(const WinGeom &g, int it) {
@@ -767,21 +810,26 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
         __device__ __forceinline__ int keys(int j) const { return is_far(j) ? kw : 128; }
     };
 
+    auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
+
     if (warp == 0) {
-        if (lane == 0) {
-            int n = 0, k = 0;
-            for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-                const Item x(geo, it);
-                if (x.steps == 0) continue;
-                if (!(ok = ab.wait(bar + B::B_KE, (k & 1) ^ 1))) break;
-                ++k;
+        int n = 0, k = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const Item x(geo, it);
+            if (x.steps == 0) continue;
+            if (!(ok = wait(B::B_KE, k + 1))) break;
+            ++k;
+            if (lane == 0) {
                 mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     tma_load_3d(sm + c * B::ATOM, &mq, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
                     tma_load_3d(sm + B::TILE + c * B::ATOM, &mo, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
                 }
-                auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, unsigned char *d, int full, int j) {
+            }
+            __syncwarp();
+            auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, unsigned char *d, int full, int j) {
+                if (lane == 0) {
                     mbar_arrive_expect_tx(bar + full, x.keys(j) * D * 2);
                     const int row = x.start + x.key0(j);
 #pragma unroll
@@ -791,21 +839,21 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                             for (int r = 0; r < x.kw; r += 16)
                                 tma_load_3d(d + c * B::ATOM + r * 128, few, bar + full, 64 * c, x.hk, row + r);
                     }
-                };
-                for (int j = 0; j < x.steps; ++j, ++n) {
-                    const int ks = n % B::QS, vs = n % B::OS;
-                    if (!(ok = ab.wait(bar + B::B_QE + ks, ((n / B::QS) & 1) ^ 1))) break;
-                    keys(&mk, &mk16, sm + B::RING_Q + ks * B::TILE, B::B_QF + ks, j);
-                    if (!(ok = ab.wait(bar + B::B_OE + vs, ((n / B::OS) & 1) ^ 1))) break;
-                    keys(&mv, &mv16, sm + B::RING_O + vs * B::TILE, B::B_OF + vs, j);
                 }
+                __syncwarp();
+            };
+            for (int j = 0; j < x.steps; ++j, ++n) {
+                const int ks = n % B::QS, vs = n % B::OS;
+                if (!(ok = wait(B::B_QE + ks, n / B::QS + 1))) break;
+                keys(&mk, &mk16, sm + B::RING_Q + ks * B::TILE, B::B_QF + ks, j);
+                if (!(ok = wait(B::B_OE + vs, n / B::OS + 1))) break;
+                keys(&mv, &mv16, sm + B::RING_O + vs * B::TILE, B::B_OF + vs, j);
             }
         }
     } else if (warp == 1) {
         constexpr uint32_t I_G = idesc_bf16(128, D, false, true);
         const uint64_t qd = desc_k(smem_u32(sm)), od = desc_k(smem_u32(sm + B::TILE));
         int n = 0, k = 0;
-        auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
         auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int keys, int full) {
             tc_fence_after();
             if (lane == 0) {
@@ -849,11 +897,12 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                     scores(j + 1, n + 1);
                     if (!ok) break;
                 }
-                if (!(ok = wait(B::B_DR, n))) break;
+                if (!(ok = wait(B::B_DL, n))) break;
                 if (more) {
                     dp(j + 1, n + 1);
                     if (!ok) break;
                 }
+                if (!(ok = wait(made(n), n >> 1))) break;
                 if (j == 0 && !(ok = wait(B::B_AE, k + 1))) break;
                 tc_fence_after();
                 if (lane == 0) {
@@ -883,41 +932,56 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
             const int64_t at = (int64_t)x.h * geo.tokens + x.start + i;
             const float lse2 = there ? p.lse2[at] : CUDART_INF_F, delta = there ? p.delta[at] : 0.f;
             const bool single = i == 0 || (geo.window == 1 && geo.sinks == 0);  // sees itself alone
-            const F2 c2 = f2(p.c2, p.c2), l2 = f2(-lse2, -lse2), d2 = f2(-delta, -delta), one = f2(1.f, 1.f);
+            const F2 c2 = f2(p.c2, p.c2), l2 = f2(-lse2, -lse2), d2 = f2(-delta, -delta);
             for (int j = 0; j < x.steps; ++j, ++n) {
                 const bool far = x.is_far(j);
-                const int k0 = x.key0(j) + 64 * half, chunks = min(2, (x.keys(j) - 64 * half + 31) >> 5);
+                const int k0 = x.key0(j) + 64 * half, chunks = x.keys(j) - 64 * half;  // none of a few sinks' for the second half
                 const int hi = (far ? min(geo.sinks, i - geo.window + 1) - 1 - 64 * half : single ? -1 : i - k0),
                           lo = far ? 0 : i - geo.window + 1 - k0;
-                const bool masked = far || x.key0(j) + 127 > x.i0 || x.key0(j) < x.i0 + 127 - geo.window + 1;
                 const uint32_t ts = tmem + 128 * (n & 1) + lanes + 64 * half;
                 ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_SF + (n & 1), (n >> 1) & 1) && ab.wait(bar + B::B_DF, n & 1));
                 if (!ok) break;
                 tc_fence_after();
+                uint32_t v[2][32], d[2][32];
+                if (chunks > 0) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u >= chunks) break;
-                    uint32_t v[32], d[32], o[16];
-                    tmem_ld32(ts + 32 * u, v);
-                    tmem_ld32(td + 32 * u, d);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a, b, da, db;
-                        f2_get(fma2(pair_w(v[e], v[e + 1]), c2, l2), a, b);
-                        f2_get(fma2(pair_w(d[e], d[e + 1]), one, d2) * f2(exp2_approx(a), exp2_approx(b)), da, db);
-                        if (masked) {
-                            const int c = 32 * u + e;
-                            da = c < lo || c > hi ? 0.f : da;
-                            db = c + 1 < lo || c + 1 > hi ? 0.f : db;
-                        }
-                        o[e / 2] = pack2(da, db);
+                    for (int u = 0; u < 2; ++u) {
+                        tmem_ld32(ts + 32 * u, v[u]);
+                        tmem_ld32(td + 32 * u, d[u]);
                     }
-                    tmem_st16(ts + 16 * u, o);
+                    tmem_wait_ld();
                 }
-                tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar + B::B_DR);
+                warp_arrive(bar + B::B_DL);
+                if (chunks > 0) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            f2_get(fma2(pair_w(v[u][e], v[u][e + 1]), c2, l2), a, b);
+                            f2_get((pair_w(d[u][e], d[u][e + 1]) + d2) * f2(exp2_approx(a), exp2_approx(b)), a, b);
+                            v[u][e] = __float_as_uint(a), v[u][e + 1] = __float_as_uint(b);
+                        }
+                    if (far || x.key0(j) + 127 > x.i0) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) v[c >> 5][c & 31] = c > hi ? 0u : v[c >> 5][c & 31];
+                    }
+                    if (!far && x.key0(j) < x.i0 + 128 - geo.window) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) v[c >> 5][c & 31] = c < lo ? 0u : v[c >> 5][c & 31];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = pack2(pair_w(v[u][2 * e], v[u][2 * e + 1]));
+                        tmem_st16(ts + 16 * u, o);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                warp_arrive(bar + made(n));
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_AF, k & 1));
