@@ -22,6 +22,46 @@ __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+// The same value in every lane, and known as such to the compiler: a role's loop counters and descriptors then
+// stay in the registers that the tensor core's instructions take.
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// MMAs, and the commits behind them, by the lane that holds `e` (see elected), without a branch around them.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(e)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(e)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t e, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(e)
+        : "memory");
+}
+
 // Rows first .. 127 of a K-major (or, the same layout, MN-major) tile of D
 // channels and 128 rows become zeros. A whole warp; the tile has arrived.
 template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, int first, int rows) {
@@ -34,20 +74,21 @@ template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, 
 }
 
 // ================================================================ forward
-// An item is 256 queries of one head, two contexts w of 128 rows: while one
-// context's softmax runs, the tensor core works for the other. A step is a tile of
-// 128 keys (the first one, where there are far pairs: the sinks alone, their
-// number rounded up to 16). For context w:
-//   S_w = Q_w K^T (TMEM), P_w = 2^{c S - m} as bf16 over S_w's own columns,
-//   O_w += P_w V (TMEM).
-// The MMAs of a context go S, PV, S, PV ..., so that S of a step being complete
-// says that PV of the step before is, and the softmax may rescale O. It does so
-// only when a row's maximum has grown by more than 2^8 since the last time: the
-// weights are taken against the older maximum until then, up to 2^8, which fp32
-// sums and bf16 weights carry as well.
+// An item is 256 queries of one head, two contexts w of 128 rows. A context goes
+// through its keys 64 at a time (first, where there are far pairs, the sinks alone,
+// their number rounded up to 16), with two score buffers in turn:
+//   S = Q_w K^T (TMEM), P = 2^{c S - m} as bf16 over S's own columns, O_w += P V (TMEM).
+// The MMAs of a context go S(0), S(1), PV(0), S(2), PV(1), S(3) ..., so the scores
+// of a step are there when the softmax of the one before is through, and the
+// softmax never waits for the tensor core (with one buffer of 128 keys it waited
+// for PV and the next S: 175 us for 4 x 4096 tokens x 16 heads, window 1024).
+// S of step n being complete says that PV of step n - 2 is. The softmax rescales O
+// only when a row's maximum has grown by more than 2^8 since the last time, and
+// then waits for PV of the step before: the weights are taken against the older
+// maximum until then, up to 2^8, which fp32 sums and bf16 weights carry as well.
 //
-// warp 0: TMA; 1, 2: MMA of the contexts (and zeros behind a sequence's end); 4-7,
-// 8-11: the rows of the contexts, a thread each.
+// warp 0: TMA, 128 keys a tile; 1, 2: MMA of the contexts (and zeros behind a
+// sequence's end); 4-7, 8-11: the rows of the contexts, a thread each.
 constexpr int FW_THREADS = 384;
 template <int D> struct Fw {
     static constexpr int TILE = 128 * D * 2;
@@ -55,8 +96,9 @@ template <int D> struct Fw {
     static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V in turn
     static constexpr int KV = 2 * TILE;
     static constexpr int BAR = KV + STAGES * TILE;
-    static constexpr int B_QF = 0, B_QE = 1, B_SF = 2, B_PF = 4, B_OF = 6, B_OE = 8, B_KF = 10, B_KE = B_KF + STAGES,
-                         COUNT = B_KE + STAGES;
+    // S, P: of context w and buffer b at 2 w + b; PV, OF (the last PV), OE: of context w
+    static constexpr int B_QF = 0, B_QE = 1, B_SF = 2, B_PF = 6, B_PV = 10, B_OF = 12, B_OE = 14, B_KF = 16,
+                         B_KE = B_KF + STAGES, COUNT = B_KE + STAGES;
     static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory of a block");
 };
@@ -70,10 +112,9 @@ struct FwArgs {
 };
 
 struct FwItem {
-    int start, len, f, rows, h, hk;  // f: the tile's first token in its sequence
-    int far, kw;                     // whether there is a step of the sinks, and its keys
-    int nf0, nf1, diag0, steps;      // tiles of 128 keys: the contexts' first near ones, the first's last one
-    bool far0;                       // the first context sees sinks behind its window (the last context does if any)
+    int start, len, f, rows, h, hk;  // f: the 256 queries' first one in its sequence
+    int far, kw;                     // whether there is a tile of the sinks, and its keys
+    int nf0, tiles;                  // the first near tile of 128 keys; tiles, the sinks' one counted
     __device__ __forceinline__ FwItem(const WinGeom &g, int it) {
         const int t = g.by_hq.div(it);
         h = it - t * g.hq;
@@ -84,21 +125,25 @@ struct FwItem {
         const int last = f + rows - 1;
         far = g.sinks > 0 && last >= g.window;
         kw = far ? (min(g.sinks, last - g.window + 1) + 15) & ~15 : 0;
-        far0 = far && min(last, f + 127) >= g.window;
         nf0 = max(0, f - g.window + 1) >> 7;
-        nf1 = max(0, f + 128 - g.window + 1) >> 7;
-        diag0 = f >> 7;
-        steps = rows > 0 ? far + diag0 - nf0 + 1 + (rows > 128) : 0;
+        tiles = rows > 0 ? far + (f >> 7) - nf0 + 1 + (rows > 128) : 0;
     }
-    __device__ __forceinline__ bool is_far(int j) const { return j < far; }
-    __device__ __forceinline__ int tile(int j) const { return nf0 + j - far; }
-    __device__ __forceinline__ int last(int w) const { return far + diag0 - nf0 + w; }  // a context's last step
-    __device__ __forceinline__ bool uses(int w, int j) const {
-        if (w == 0) return is_far(j) ? far0 : j <= last(0);
-        return rows > 128 && (is_far(j) || tile(j) >= nf1);
+    __device__ __forceinline__ int key0(int tile) const { return tile < far ? 0 : (nf0 + tile - far) * 128; }
+    __device__ __forceinline__ int keys(int tile) const { return tile < far ? kw : 128; }
+};
+// A context's tiles among the item's: the sinks' one if it sees any behind its window, then near ones.
+struct FwContext {
+    int i0, first, last;  // its first query; its near tiles
+    bool far;
+    int tiles;
+    __device__ __forceinline__ FwContext(const WinGeom &g, const FwItem &x, int w) {
+        i0 = x.f + 128 * w;
+        far = x.far && min(i0 + 127, x.len - 1) >= g.window;
+        first = x.far + (max(0, i0 - g.window + 1) >> 7) - x.nf0;
+        last = x.far + (i0 >> 7) - x.nf0;
+        tiles = x.rows > 128 * w ? far + last - first + 1 : 0;
     }
-    __device__ __forceinline__ int key0(int j) const { return is_far(j) ? 0 : tile(j) * 128; }
-    __device__ __forceinline__ int keys(int j) const { return is_far(j) ? kw : 128; }
+    __device__ __forceinline__ int tile(int n) const { return far ? (n == 0 ? 0 : first + n - 1) : first + n; }
 };
 
 template <int D>
@@ -117,7 +162,7 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     if (tid == 0) {
         *ab.flag = 0;
         for (int i = 0; i < F::COUNT; ++i)
-            mbar_init(bar + i, (i >= F::B_PF && i < F::B_OF) || (i >= F::B_OE && i < F::B_KF) ? 4
+            mbar_init(bar + i, (i >= F::B_PF && i < F::B_PV) || (i >= F::B_OE && i < F::B_KF) ? 4
                                : i == F::B_QE || i >= F::B_KE                                 ? 2
                                                                                               : 1);
         fence_mbar_init();
@@ -129,39 +174,19 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tm;  // S_0 | S_1 | O_0 | O_1
+    const uint32_t tmem = *tm;  // S of context 0, two of 64 columns | of context 1 | O_0 | O_1
+    const uint32_t bars = smem_u32(bar);
+    auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
     bool ok = true;
 
-    // 384 threads of 168 registers become 128 of 88 and 256 of 208
-    if (warp < 4) regs_dec<88>();
     if (warp == 0) {
         // A whole warp waits, one lane copies: with one lane in a wait and the others past it the warp is woken by
         // the wait's time limit alone, microseconds late.
-        int n = 0, q = 0;  // stages, items so far
+        int s = 0, round = 1, q = 0;  // the next stage and its phase, items so far
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const FwItem x(geo, it);
-            if (x.steps == 0) continue;
-            auto keys = [&](const CUtensorMap *whole, const CUtensorMap *few, int j) {
-                const int s = n % F::STAGES;
-                if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_KE + s, ((n / F::STAGES) & 1) ^ 1)))) return;
-                ++n;
-                if (lane == 0) {
-                    unsigned char *d = sm + F::KV + s * F::TILE;
-                    uint64_t *full = bar + F::B_KF + s;
-                    mbar_arrive_expect_tx(full, x.keys(j) * D * 2);
-                    const int row = x.start + x.key0(j);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        if (!x.is_far(j)) tma_load_3d(d + c * F::ATOM, whole, full, 64 * c, x.hk, row);
-                        else
-                            for (int r = 0; r < x.kw; r += 16)
-                                tma_load_3d(d + c * F::ATOM + r * 128, few, full, 64 * c, x.hk, row + r);
-                    }
-                }
-                __syncwarp();
-            };
-            if (!(ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_QE, (q & 1) ^ 1)))) break;
-            ++q;
+            if (x.tiles == 0) continue;
+            if (!(ok = wait(F::B_QE, ++q))) break;
             if (lane == 0) {
                 const int contexts = x.rows > 128 ? 2 : 1;
                 mbar_arrive_expect_tx(bar + F::B_QF, contexts * F::TILE);
@@ -171,207 +196,217 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
                         tma_load_3d(sm + w * F::TILE + c * F::ATOM, &mq, bar + F::B_QF, 64 * c, x.h, x.start + x.f + 128 * w);
             }
             __syncwarp();
-            for (int j = 0; j < x.steps && ok; ++j) {
-                keys(&mk, &mk16, j);
-                if (ok) keys(&mv, &mv16, j);
+            for (int j = 0; j < 2 * x.tiles; ++j) {  // K and V of a tile
+                if (!(ok = wait(F::B_KE + s, round))) break;
+                if (lane == 0) {
+                    const int tile = j >> 1, row = x.start + x.key0(tile);
+                    const bool is_v = j & 1;
+                    unsigned char *d = sm + F::KV + s * F::TILE;
+                    uint64_t *full = bar + F::B_KF + s;
+                    mbar_arrive_expect_tx(full, x.keys(tile) * D * 2);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        if (tile >= x.far) tma_load_3d(d + c * F::ATOM, is_v ? &mv : &mk, full, 64 * c, x.hk, row);
+                        else
+                            for (int r = 0; r < x.kw; r += 16)
+                                tma_load_3d(d + c * F::ATOM + r * 128, is_v ? &mv16 : &mk16, full, 64 * c, x.hk, row + r);
+                    }
+                }
+                __syncwarp();
+                if (++s == F::STAGES) s = 0, round ^= 1;
             }
         }
     } else if (warp < 3) {
         // A context's products. One thread issues them and is held up until the tensor core takes them, so what it
-        // does in between is time without a product of this context: hence two warps, and short loops.
-        const int w = warp - 1;
-        constexpr uint32_t I_O = idesc_bf16(128, D, false, true), I_S = idesc_bf16(128, 128, false, false);
-        const uint32_t bars = smem_u32(bar), kv = smem_u32(sm + F::KV), ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
-        const uint64_t qd = desc_k(smem_u32(sm + w * F::TILE)), kd = desc_k(kv), vd = desc_mn(kv, F::ATOM);
-        auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
-        auto commit = [&](int b) {
-            if (lane == 0) umma_commit(bar + b);
-            __syncwarp();
+        // does in between is time without a product of this context: hence two warps, and as few steps in their
+        // loops as can be.
+        const int w = uni(warp - 1);
+        const uint32_t e = elected();
+        const uint32_t base = uni(tmem), kv = uni(smem_u32(sm + F::KV)), bb = uni(bars);
+        const uint32_t ts = base + 128 * w, to = base + 256 + 128 * w;
+        constexpr uint32_t I_O = idesc_bf16(128, D, false, true), I_S = idesc_bf16(128, 64, false, false);
+        const uint64_t qd = desc_k(kv - F::KV + w * F::TILE), kd = desc_k(kv), vd = desc_mn(kv, F::ATOM);
+        int s = 0, round = 0;            // the next stage and its phase
+        int q = 0, oi = 0, pn[2] = {0, 0};  // items so far, phases of O and of the halves' P
+        auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
+        auto next = [&]() {
+            if (++s == F::STAGES) s = 0, round ^= 1;
         };
-        int s = 0, round = 0;       // the next stage and its phase
-        int q = 0, pv = 0, oi = 0;  // items so far; phases of P and O
+        // the scores of a half of the tile whose K is in stage s
+        auto scores = [&](int u, uint32_t idesc) {
+            const uint64_t b = kd + ((s * F::TILE + u * 8192) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_if(e, ts + 64 * u, qd + step_k(ks, F::ATOM), b + step_k(ks, F::ATOM), idesc, ks > 0);
+            commit_if(e, bb + 8 * (F::B_SF + 2 * w + u));
+        };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const FwItem x(geo, it);
-            if (x.steps == 0) continue;
-            if (!(ok = wait(F::B_QF, q))) break;
-            ++q;
-            bool first = true;
-            for (int j = -1; j < x.steps; ++j) {
-                if (j >= 0) {
-                    if (!(ok = wait(F::B_KF + s, round))) break;
-                    if (x.uses(w, j)) {
-                        const int behind = x.len - x.key0(j);  // rows of V past the sequence's end may hold anything
-                        if (behind < x.keys(j)) zero_rows<D>(sm + F::KV + s * F::TILE, behind, x.keys(j));
-                        if (!(ok = wait(F::B_PF + w, pv++))) break;
-                        if (first && !(ok = wait(F::B_OE + w, ++oi))) break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint64_t b = vd + s * (F::TILE >> 4);
-                            if (first) umma_bf16_ts<false>(to, ts, b, I_O);
-                            else umma_bf16_ts<true>(to, ts, b, I_O);
-                            if (x.is_far(j)) {
-#pragma unroll 1
-                                for (int ks = 1; ks < x.kw / 16; ++ks) umma_bf16_ts<true>(to, ts + ks * 8, b + step_mn(ks), I_O);
-                            } else {
-#pragma unroll
-                                for (int ks = 1; ks < 8; ++ks) umma_bf16_ts<true>(to, ts + ks * 8, b + step_mn(ks), I_O);
-                            }
-                            if (j == x.last(w)) umma_commit(bar + F::B_OF + w);
-                        }
-                        __syncwarp();
-                        first = false;
-                    }
-                    commit(F::B_KE + s);
-                    if (++s == F::STAGES) s = 0, round ^= 1;
+            if (x.tiles == 0) continue;
+            const FwContext y(geo, x, w);
+            const int tiles = uni(x.tiles), mine = uni(y.tiles), kw = uni(x.kw), far = uni(y.far), others = uni(x.far) - far,
+                      lead = uni(y.first) - uni(x.far),  // near tiles in front that the other context alone has use for
+                      len = uni(x.len), behind = uni(x.len - x.key0(y.first));  // tokens; from its first near tile on
+            const int far0 = far ? min(kw, 64) : 64, far1 = far ? kw - 64 : 64;  // keys of its first tile's halves
+            if (!(ok = on(F::B_QF, q++))) break;
+            // K and V of tiles that it has none for
+            auto pass = [&](int count) {
+                for (int i = 0; i < 2 * count && ok; ++i) {
+                    if (!(ok = on(F::B_KF + s, round))) break;
+                    commit_if(e, bb + 8 * (F::B_KE + s));
+                    next();
                 }
-                if (j + 1 == x.steps) break;
-                if (!(ok = wait(F::B_KF + s, round))) break;
-                if (x.uses(w, j + 1)) {
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t idesc = x.is_far(j + 1) ? idesc_bf16(128, x.kw, false, false) : I_S;
-                        const uint64_t b = kd + s * (F::TILE >> 4);
-                        mma_ss<false>(ts, qd, b, idesc);
-#pragma unroll
-                        for (int ks = 1; ks < D / 16; ++ks)
-                            mma_ss<true>(ts, qd + step_k(ks, F::ATOM), b + step_k(ks, F::ATOM), idesc);
-                        umma_commit(bar + F::B_SF + w);
-                    }
-                    __syncwarp();
-                }
-                commit(F::B_KE + s);
-                if (++s == F::STAGES) s = 0, round ^= 1;
-                if (j + 2 == x.steps) commit(F::B_QE);  // the last scores are on their way
+            };
+            if (mine == 0) {
+                commit_if(e, bb + 8 * F::B_QE);
+                pass(tiles);
+                continue;
             }
+            pass(others + (far ? 0 : lead));
+            // K of the first tile
+            if (!ok || !(ok = on(F::B_KF + s, round))) break;
+            tc_fence_after();
+            scores(0, far ? idesc_bf16(128, far0, false, false) : I_S);
+            if (far1 > 0) scores(1, far ? idesc_bf16(128, far1, false, false) : I_S);
+            commit_if(e, bb + 8 * (F::B_KE + s));
+            next();
+            if (mine == 1) commit_if(e, bb + 8 * F::B_QE);
+            for (int n = 0; n < mine; ++n) {
+                const bool sinks = far && n == 0, more = n + 1 < mine;
+                const int sv = s;
+                if (!(ok = on(F::B_KF + s, round))) break;
+                const int rows = sinks ? len : behind - 128 * (n - far);  // up to the sequence's end
+                if (rows < (sinks ? kw : 128)) zero_rows<D>(sm + F::KV + sv * F::TILE, rows, sinks ? kw : 128);
+                next();
+                const uint64_t vb = vd + ((sv * F::TILE) >> 4);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int keys = !sinks ? 64 : u ? far1 : far0;
+                    if (keys > 0) {
+                        if (!(ok = on(F::B_PF + 2 * w + u, pn[u]++))) break;
+                        if (n == 0 && u == 0 && !(ok = on(F::B_OE + w, ++oi))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts_if(keys > 16 * ks ? e : 0u, to, ts + 64 * u + ks * 8, vb + ((u * 8192) >> 4) + step_mn(ks),
+                                      I_O, n > 0 || u > 0 || ks > 0);
+                        commit_if(e, bb + 8 * (F::B_PV + w));
+                    }
+                    if (u == 1) {
+                        commit_if(e, bb + 8 * (F::B_KE + sv));
+                        if (!more) commit_if(e, bb + 8 * (F::B_OF + w));
+                    }
+                    if (more) {
+                        if (u == 0) {
+                            if (sinks) pass(lead);
+                            if (!ok || !(ok = on(F::B_KF + s, round))) break;
+                            tc_fence_after();
+                        }
+                        scores(u, I_S);
+                    }
+                }
+                if (!ok) break;
+                if (more) {
+                    commit_if(e, bb + 8 * (F::B_KE + s));
+                    next();
+                    if (n + 2 == mine) commit_if(e, bb + 8 * F::B_QE);  // the last scores are on their way
+                }
+            }
+            if (!ok) break;
+            pass(tiles - others - lead - mine);
         }
     } else if (warp >= 4) {
-        regs_inc<208>();
         const int w = (warp - 4) >> 2, row = tid & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
-        int sf = 0, of = 0;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts0 = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+        int sn[2] = {0, 0}, of = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const FwItem x(geo, it);
-            if (x.rows <= 128 * w) continue;
-            const int i = x.f + 128 * w + row;
+            const FwContext y(geo, x, w);
+            if (y.tiles == 0) continue;
+            const int i = y.i0 + row;
             float m = -CUDART_INF_F;
-            F2 l = f2(0.f, 0.f);
-            bool first = true;
-            for (int j = 0; j < x.steps && ok; ++j) {
-                if (!x.uses(w, j)) continue;
-                ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_SF + w, sf & 1));
-                if (!ok) break;
-                ++sf;
-                tc_fence_after();
-                // O and the sum so far, when the maximum has grown from m to `top` by more than 2^8 (also when the
-                // row sees its first number)
-                auto rescale = [&](float top) {
-                    const bool grow = (top - m) * p.c2 > 8.f;
-                    if (!first && __any_sync(0xffffffffu, grow)) {
-                        const float f = grow ? exp2_approx((m - top) * p.c2) : 1.f;
-                        const F2 ff = f2(f, f);
-                        l = l * ff;
+            F2 l = f2(0.f, 0.f), l1 = l;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float u, v;
-                                f2_get(pair_w(o[e], o[e + 1]) * ff, u, v);
-                                o[e] = __float_as_uint(u), o[e + 1] = __float_as_uint(v);
-                            }
-                            tmem_st32(to + c, o);
-                        }
-                    }
-                    if (grow) m = top;
-                    first = false;
-                };
-                // 32 weights from their scores, over the front of the columns
-                auto weights = [&](uint32_t (&s)[32], int c) {
-                    const float off = m == -CUDART_INF_F ? 0.f : -m * p.c2;
-                    const F2 c2 = f2(p.c2, p.c2), off2 = f2(off, off);
-                    uint32_t o[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float u, v;
-                        f2_get(fma2(pair_w(s[e], s[e + 1]), c2, off2), u, v);
-                        const F2 w2 = f2(exp2_approx(u), exp2_approx(v));
-                        l = l + w2;
-                        o[e / 2] = pack2(w2);
-                    }
-                    tmem_st16(ts + 16 * c, o);
-                };
-                auto largest = [](const uint32_t (&s)[32]) {
-                    float t[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(s[e]);
-#pragma unroll
-                    for (int e = 4; e < 28; e += 8)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            t[u] = max3(t[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + u + 4]));
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) t[u] = fmaxf(t[u], __uint_as_float(s[28 + u]));
-                    return fmaxf(max3(t[0], t[1], t[2]), t[3]);
-                };
+            for (int h = 0; h < 2 * y.tiles; ++h) {
+                const int u = h & 1;
+                const bool far = y.far && h < 2;
+                if (far && 64 * u >= x.kw) continue;
+                const uint32_t ts = ts0 + 64 * u;
+                if (!(ok = wait(F::B_SF + 2 * w + u, u ? sn[1] : sn[0]))) break;
+                if (u) ++sn[1];
+                else ++sn[0];
+                tc_fence_after();
+                uint32_t s[2][32];
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
+                tmem_wait_ld();
                 constexpr uint32_t NONE = 0xff800000u;  // -inf
-                if (x.is_far(j)) {  // the sinks: a few columns, all of them with masks
-                    const int hi = min(geo.sinks, i - geo.window + 1) - 1, chunks = (x.kw + 31) >> 5;
-                    float top = -CUDART_INF_F;
-                    uint32_t s[32];
-                    auto load = [&](int c) {
-                        tmem_ld32(ts + 32 * c, s);
+                const int k0 = (far ? 0 : x.key0(y.tile(h >> 1))) + 64 * u;
+                if (far || k0 + 63 > y.i0) {  // some row does not see the last keys (the sinks' columns may be stale)
+                    const int hi = (far ? min(geo.sinks, i - geo.window + 1) - 1 : i) - k0;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c >> 5][c & 31] = c > hi ? NONE : s[c >> 5][c & 31];
+                }
+                if (!far && k0 < y.i0 + 128 - geo.window) {  // or the first ones
+                    const int lo = i - geo.window + 1 - k0;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c >> 5][c & 31] = c < lo ? NONE : s[c >> 5][c & 31];
+                }
+                float t[4] = {m, m, m, m};
+#pragma unroll
+                for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        t[v] = max3(t[v], __uint_as_float(s[c >> 5][(c & 31) + v]), __uint_as_float(s[c >> 5][(c & 31) + v + 4]));
+                const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+                const bool grow = (top - m) * p.c2 > 8.f;  // also when the row sees its first number
+                if (h > 0 && __any_sync(0xffffffffu, grow)) {
+                    // PV of the step before the last one is complete, so this waits for that of the last one and no
+                    // other phase
+                    if (!(ok = wait(F::B_PV + w, sn[0] + sn[1]))) break;
+                    tc_fence_after();
+                    const float f = grow ? exp2_approx((m - top) * p.c2) : 1.f;
+                    const F2 ff = f2(f, f);
+                    l = l * ff, l1 = l1 * ff;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = 32 * c + e > hi ? NONE : s[e];
-                    };
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        load(c);
-                        top = fmaxf(top, largest(s));
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            f2_get(pair_w(o[e], o[e + 1]) * ff, a, b);
+                            o[e] = __float_as_uint(a), o[e + 1] = __float_as_uint(b);
+                        }
+                        tmem_st32(to + c, o);
                     }
-                    rescale(fmaxf(top, m));
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        load(c);
-                        weights(s, c);
+                }
+                if (grow) m = top;
+                const float off = m == -CUDART_INF_F ? 0.f : -m * p.c2;
+                const F2 c2 = f2(p.c2, p.c2), off2 = f2(off, off);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        float u0, v0, u1, v1;
+                        f2_get(fma2(pair_w(s[c][e], s[c][e + 1]), c2, off2), u0, v0);
+                        f2_get(fma2(pair_w(s[c][e + 2], s[c][e + 3]), c2, off2), u1, v1);
+                        const F2 a = f2(exp2_approx(u0), exp2_approx(v0)), b = f2(exp2_approx(u1), exp2_approx(v1));
+                        l = l + a, l1 = l1 + b;
+                        o[e / 2] = pack2(a), o[e / 2 + 1] = pack2(b);
                     }
-                } else {
-                    // the whole row in registers; a chunk's weights go over columns that have all been read
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
-                    tmem_wait_ld();
-                    const int k0 = x.key0(j);
-                    if (k0 + 127 > x.f + 128 * w) {  // some row does not see the last keys, or the first ones
-                        const int hi = i - k0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[c][e] = 32 * c + e > hi ? NONE : s[c][e];
-                    }
-                    if (k0 < x.f + 128 * w + 128 - geo.window) {
-                        const int lo = i - geo.window + 1 - k0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[c][e] = 32 * c + e < lo ? NONE : s[c][e];
-                    }
-                    rescale(fmaxf(max3(largest(s[0]), largest(s[1]), m), fmaxf(largest(s[2]), largest(s[3]))));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) weights(s[c], c);
+                    tmem_st16(ts + 16 * c, o);  // over columns that have been read
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar + F::B_PF + w);
+                warp_arrive(bar + F::B_PF + 2 * w + u);
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, ab.wait(bar + F::B_OF + w, of & 1));
-            if (!ok) break;
-            ++of;
+            if (!(ok = wait(F::B_OF + w, of++))) break;
             tc_fence_after();
-            const float sum = f2_sum(l), f = 1.f / sum;
+            const float sum = f2_sum(l + l1), f = 1.f / sum;
             const bool there = i < x.len;
             const int64_t at = (int64_t)(x.start + i) * geo.hq + x.h;
             const F2 ff = f2(f, f);
