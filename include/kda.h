@@ -817,7 +817,8 @@ kda_status_t kda_window_attention_backward(const void *q, const void *k, const v
                                            size_t workspace_bytes, kda_stream_t stream);
 
 /* Workspace bytes kda_window_attention_backward needs (0 for invalid arguments). */
-size_t kda_window_attention_backward_workspace_bytes(int B, int T, int H_q, int H_k, int d, int sinks);
+size_t kda_window_attention_backward_workspace_bytes(int B, int T, int H_q, int H_k, int d, int sinks,
+                                                     kda_dtype_t dtype);
 
 /* kda_window_varlen_attention_backward - the gradients of
  * kda_window_varlen_attention; layouts and device_status as there. */
@@ -829,7 +830,8 @@ kda_status_t kda_window_varlen_attention_backward(const void *q, const void *k, 
                                                   size_t workspace_bytes, int32_t *device_status, kda_stream_t stream);
 
 /* Workspace bytes kda_window_varlen_attention_backward needs (0 for invalid arguments). */
-size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, int H_q, int H_k, int d, int sinks);
+size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, int H_q, int H_k, int d, int sinks,
+                                                            kda_dtype_t dtype);
 
 /*
  * The cache of a served sequence has a constant size, as a state has: slots of

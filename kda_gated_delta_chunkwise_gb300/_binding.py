@@ -171,8 +171,8 @@ def load(path: str | None = None):
                      "kda_window_varlen_attention_backward", "kda_window_cache_write", "kda_window_decode_step"):
             getattr(lib, name).restype = i
         for name, n in (("kda_gated_norm_backward", 1), ("kda_residual_norm_backward", 1),
-                        ("kda_window_varlen_attention", 5), ("kda_window_attention_backward", 6),
-                        ("kda_window_varlen_attention_backward", 6)):
+                        ("kda_window_varlen_attention", 5), ("kda_window_attention_backward", 7),
+                        ("kda_window_varlen_attention_backward", 7)):
             getattr(lib, name + "_workspace_bytes").argtypes = [i] * n
             getattr(lib, name + "_workspace_bytes").restype = sz
         lib.kda_last_error.restype = ctypes.c_char_p

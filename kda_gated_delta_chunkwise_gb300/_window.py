@@ -23,13 +23,15 @@ def window_varlen_attention_workspace_bytes(N: int, T_total: int, H_q: int, H_k:
     return _bytes("kda_window_varlen_attention", N, T_total, H_q, H_k, d)
 
 
-def window_attention_backward_workspace_bytes(B: int, T: int, H_q: int, H_k: int, d: int = 128, sinks: int = 0) -> int:
-    return _bytes("kda_window_attention_backward", B, T, H_q, H_k, d, sinks)
+def window_attention_backward_workspace_bytes(B: int, T: int, H_q: int, H_k: int, d: int = 128, sinks: int = 0,
+                                              dtype=torch.bfloat16) -> int:
+    return _bytes("kda_window_attention_backward", B, T, H_q, H_k, d, sinks, _dtype_code(torch.empty(0, dtype=dtype)))
 
 
 def window_varlen_attention_backward_workspace_bytes(N: int, T_total: int, H_q: int, H_k: int, d: int = 128,
-                                                     sinks: int = 0) -> int:
-    return _bytes("kda_window_varlen_attention_backward", N, T_total, H_q, H_k, d, sinks)
+                                                     sinks: int = 0, dtype=torch.bfloat16) -> int:
+    return _bytes("kda_window_varlen_attention_backward", N, T_total, H_q, H_k, d, sinks,
+                  _dtype_code(torch.empty(0, dtype=dtype)))
 
 
 def _inputs(q, k, v, lead: int, scale):
@@ -101,11 +103,11 @@ def _backward(q, k, v, out, lse, d_o, cu_seqlens, window, sinks, scale, workspac
             *strides, scale, min(window, _MOST), sinks, *(t.data_ptr() for t in grads.values()))
     if packed:
         N, T = _packed(cu_seqlens, device_status, index), lead[0]
-        ws, size = _space(workspace, _bytes("kda_window_varlen_attention_backward", N, T, hq, hk, d, sinks), q)
+        ws, size = _space(workspace, _bytes("kda_window_varlen_attention_backward", N, T, hq, hk, d, sinks, _dtype_code(q)), q)
         st = lib.kda_window_varlen_attention_backward(*head, cu_seqlens.data_ptr(), N, T, hq, hk, d, ws.data_ptr(), size,
                                                       _ptr(device_status), _stream(index))
     else:
-        ws, size = _space(workspace, _bytes("kda_window_attention_backward", *lead, hq, hk, d, sinks), q)
+        ws, size = _space(workspace, _bytes("kda_window_attention_backward", *lead, hq, hk, d, sinks, _dtype_code(q)), q)
         st = lib.kda_window_attention_backward(*head, *lead, hq, hk, d, ws.data_ptr(), size, _stream(index))
     _check(lib, st)
     return grads

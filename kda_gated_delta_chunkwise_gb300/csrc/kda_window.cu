@@ -188,7 +188,7 @@ struct WinParams {
     void *o, *dq, *dk, *dv;
     float *lse;               // [tokens][hq], of the forward
     float *lse2, *delta;      // [hq][tokens], of the gradients: lse (bf16: in powers of two), D
-    float *part, *sums;       // far gradients of the sinks: [ntiles][hk][2][sinks][d], [N][hk][2][sinks][d]
+    float *part, *near;       // gradients of the sinks, see win_far_sum_kernel
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -481,7 +481,7 @@ win_dkv_kernel(WinParams p) {
         const int r = r0 + e * 8, j = j0 + r;
         if (r >= rows) continue;
         if constexpr (FAR) {
-            float *dk = p.part + (((int64_t)(at >> 1) * geo.hk + hk) * 2 * geo.sinks + j) * D;
+            float *dk = p.part + (((int64_t)win_far_slot(at >> 1, tile.seq, 1) * geo.hk + hk) * 2 * geo.sinks + j) * D;
             float *dv = dk + (int64_t)geo.sinks * D;
 #pragma unroll
             for (int nb = 0; nb < D / 8; ++nb) {
@@ -490,46 +490,61 @@ win_dkv_kernel(WinParams p) {
             }
         } else {
             const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D;
-            const bool sink = p.sums && j < geo.sinks;
-            const float *fk = p.sums + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D;
-            const float *fv = fk + (int64_t)geo.sinks * D;
+            const bool sink = j < geo.sinks && tile.len > geo.window;
+            float *fk = p.near + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D;
+            float *fv = fk + (int64_t)geo.sinks * D;
 #pragma unroll
             for (int nb = 0; nb < D / 8; ++nb) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int c = nb * 8 + 2 * t + u;
-                    ((T *)p.dk)[row + c] = from_f32<T>(ak[nb][2 * e + u] * p.scale + (sink ? fk[c] : 0.f));
-                    ((T *)p.dv)[row + c] = from_f32<T>(av[nb][2 * e + u] + (sink ? fv[c] : 0.f));
+                    const float dk = ak[nb][2 * e + u] * p.scale, dv = av[nb][2 * e + u];
+                    if (sink) {
+                        fk[c] = dk, fv[c] = dv;
+                    } else {
+                        ((T *)p.dk)[row + c] = from_f32<T>(dk);
+                        ((T *)p.dv)[row + c] = from_f32<T>(dv);
+                    }
                 }
             }
         }
     }
 }
 
-// The far gradients of a sequence's sinks: its tiles' parts added in order,
-// lanes over the channels, eight groups of threads over the tiles.
+// dk and dv of the sinks that far queries see: `near` [N][hk][2][sinks][d], from
+// the queries within the window, and the far queries' parts [slots][hk][2][sinks][d]
+// (see win_far_slot), added in order: lanes over the channels, eight groups of
+// threads over the parts.
+template <typename T>
 __global__ void __launch_bounds__(256)
-win_far_sum_kernel(WinGeom geo, const float *part, float *sums, int d) {
+win_far_sum_kernel(WinGeom geo, const float *part, const float *near, T *dk, T *dv, int d, int per) {
     __shared__ float red[8][33];
     const int c = blockIdx.y * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;  // c: of [2][sinks][d]
     const int nh = blockIdx.x, n = geo.by_hk.div(nh), hk = nh - n * geo.hk;
-    const int64_t per = 2ll * geo.sinks * d;
-    int first, last;
-    if (geo.tiles) first = geo.seq_tile[n], last = geo.seq_tile[n + 1];
-    else first = n * geo.per_seq, last = first + geo.per_seq;
+    const int64_t size = 2ll * geo.sinks * d;
+    int first = n * geo.per_seq, start = n * geo.T, len = geo.T;
+    if (geo.tiles) {
+        first = geo.seq_tile[n];
+        if (first == geo.seq_tile[n + 1]) return;  // no tokens
+        start = geo.tiles[first].y, len = geo.tiles[first].z;
+    }
+    if (len <= geo.window) return;
+    const int sink = c / d % geo.sinks, queries = per * kWinTile;
+    const bool there = c < size && sink < len;
     float a = 0.f;
-    const int sink = c / d % geo.sinks;  // behind a short sequence's end there is none, and no part was written
-    const int len = geo.tiles && first < last ? geo.tiles[first].z : geo.T;
-    if (c < per && sink < len) {
+    if (there) {
 #pragma unroll 4
-        for (int k = first + group; k < last; k += 8) a += part[((int64_t)k * geo.hk + hk) * per + c];
+        for (int k = geo.window / queries + group; k <= (len - 1) / queries; k += 8)
+            a += part[((int64_t)win_far_slot(first + k * per, n, per) * geo.hk + hk) * size + c];
     }
     red[group][threadIdx.x & 31] = a;
     __syncthreads();
-    if (group == 0 && c < per) {
+    if (group == 0 && there) {
 #pragma unroll
         for (int k = 1; k < 8; ++k) a += red[k][threadIdx.x];
-        sums[(int64_t)nh * per + c] = a;
+        a += near[(int64_t)nh * size + c];
+        T *dst = c < geo.sinks * d ? dk : dv;
+        dst[((int64_t)(start + sink) * geo.hk + hk) * d + c % d] = from_f32<T>(a);
     }
 }
 
@@ -540,10 +555,10 @@ struct WinPlan {
     WinGeom geo;
     int4 *tiles;
     int32_t *seq_tile;
-    float *lse2, *delta, *part, *sums;
+    float *lse2, *delta, *part, *near;
     size_t bytes;
 };
-WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks, bool packed, bool back, void *ws) {
+WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks, bool packed, bool back, bool bf16, void *ws) {
     WinPlan p{};
     WinGeom &g = p.geo;
     g.N = N, g.T = (int)T, g.hq = hq, g.hk = hk, g.group = hq / hk;
@@ -568,8 +583,9 @@ WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks
         p.lse2 = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         p.delta = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         if (sinks > 0) {
-            p.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)g.ntiles * hk * sinks * d));
-            p.sums = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)N * hk * sinks * d));
+            const size_t slots = (size_t)g.ntiles / (bf16 ? kWinFarQueries / kWinTile : 1) + N + 1;
+            p.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * slots * hk * sinks * d));
+            p.near = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)N * hk * sinks * d));
         }
     }
     return p;
@@ -593,7 +609,7 @@ WinParams params(const WinPlan &p, const WinArgs &a) {
     w.q_stride = a.q_stride, w.k_stride = a.k_stride, w.v_stride = a.v_stride;
     w.scale = a.scale;
     w.o = a.o, w.dq = a.dq, w.dk = a.dk, w.dv = a.dv;
-    w.lse = a.lse, w.lse2 = p.lse2, w.delta = p.delta, w.part = p.part, w.sums = p.sums;
+    w.lse = a.lse, w.lse2 = p.lse2, w.delta = p.delta, w.part = p.part, w.near = p.near;
     return w;
 }
 template <typename... P>
@@ -620,27 +636,29 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
         const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
         KDA_TRY(run(win_dq_kernel<T, D, true>, allowed[3], (unsigned)(blocks * a.hq), smem, s, w));
     }
-    if (a.sinks > 0) {
-        KDA_TRY(run(win_dkv_kernel<T, D, true>, allowed[0], (unsigned)(p.geo.ntiles * 2 * a.hk), smem, s, w));
-        win_far_sum_kernel<<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(p.geo, p.part, p.sums, D);
-        KDA_TRY(cudaGetLastError());
-    }
+    const bool far = a.sinks > 0 && a.window < a.T;  // some sequence may be longer than the window
     if constexpr (sizeof(T) == 2) {
-        return launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.sums, s);
+        KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, s));
     } else {
+        if (far) KDA_TRY(run(win_dkv_kernel<T, D, true>, allowed[0], (unsigned)(p.geo.ntiles * 2 * a.hk), smem, s, w));
         KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
-        return run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w);
+        KDA_TRY(run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
     }
+    if (far)
+        win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(
+            p.geo, p.part, p.near, (T *)a.dk, (T *)a.dv, D, sizeof(T) == 2 ? kWinFarQueries / kWinTile : 1);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t window_workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, bool packed, bool back) {
-    return make_plan(N, T, hq, hk, d, 1, sinks, packed, back, nullptr).bytes;
+size_t window_workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, kda_dtype_t dt, bool packed, bool back) {
+    return make_plan(N, T, hq, hk, d, 1, sinks, packed, back, dt == KDA_BF16, nullptr).bytes;
 }
 
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
-    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, false, a.workspace);
+    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, false, a.dt == KDA_BF16,
+                                a.workspace);
     KDA_TRY(prepare_tiles(p, a, s));
     if (p.geo.tokens == 0) return cudaSuccess;
     if (a.dt == KDA_BF16) return launch_window_forward_tc(p.geo, a, s);
@@ -648,7 +666,8 @@ cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_window_backward(const WinArgs &a, cudaStream_t s) {
-    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, true, a.workspace);
+    const WinPlan p = make_plan(a.N, a.T, a.hq, a.hk, a.d, a.window, a.sinks, a.cu_seqlens != nullptr, true, a.dt == KDA_BF16,
+                                a.workspace);
     KDA_TRY(prepare_tiles(p, a, s));
     if (p.geo.tokens == 0) return cudaSuccess;
     if (a.dt == KDA_BF16) return a.d == 128 ? backward<__nv_bfloat16, 128>(p, a, s) : backward<__nv_bfloat16, 64>(p, a, s);

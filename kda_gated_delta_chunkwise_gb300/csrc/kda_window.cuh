@@ -13,6 +13,7 @@ namespace kda {
 
 constexpr int kWinTile = 256;     // tokens of an entry of the tile table
 constexpr int kWinMaxSinks = 128;
+constexpr int kWinFarQueries = 1024;  // queries to a part of the sinks' far gradients, on the tensor cores
 
 struct WinTile {
     int seq;    // sequence
@@ -39,6 +40,10 @@ __device__ __forceinline__ WinTile win_tile(const WinGeom &g, int t) {
     return {n, n * g.T, g.T, (t - n * g.per_seq) * kWinTile};
 }
 
+// The part that far queries from tile t on write to, `per` tiles to a part: every
+// sequence's are numbers in a row, and no two sequences share one.
+__device__ __forceinline__ int win_far_slot(int t, int seq, int per) { return t / per + seq; }
+
 struct WinArgs {
     kda_dtype_t dt;
     const void *q, *k, *v;              // token strides in elements
@@ -55,7 +60,7 @@ struct WinArgs {
     const void *out, *d_o;              // contiguous
     void *dq, *dk, *dv;                 // contiguous
 };
-size_t window_workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, bool packed, bool back);
+size_t window_workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, kda_dtype_t dt, bool packed, bool back);
 cudaError_t launch_window(const WinArgs &a, cudaStream_t s);
 cudaError_t launch_window_backward(const WinArgs &a, cudaStream_t s);
 

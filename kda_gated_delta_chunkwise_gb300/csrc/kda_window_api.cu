@@ -77,14 +77,14 @@ kda_status_t attention(WinArgs &a, bool packed, bool back, size_t workspace_byte
         return ok();
     }
     KDA_CHECK(workspace_ok(a.workspace, workspace_bytes,
-                           window_workspace_bytes(a.N, a.T, a.hq, a.hk, a.d, a.sinks, packed, back)));
+                           window_workspace_bytes(a.N, a.T, a.hq, a.hk, a.d, a.sinks, a.dt, packed, back)));
     return back ? cuda_status(launch_window_backward(a, s), "window attention backward launch")
                 : cuda_status(launch_window(a, s), "window attention launch");
 }
 
-size_t workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, bool packed, bool back) {
-    if (common(KDA_F32, N, T, hq, hk, d, sinks) != KDA_OK || sizes(N, T, hq, packed) != KDA_OK) return 0;
-    return window_workspace_bytes(N, T, hq, hk, d, sinks, packed, back);
+size_t workspace_bytes(int N, int64_t T, int hq, int hk, int d, int sinks, kda_dtype_t dt, bool packed, bool back) {
+    if (common(dt, N, T, hq, hk, d, sinks) != KDA_OK || sizes(N, T, hq, packed) != KDA_OK) return 0;
+    return window_workspace_bytes(N, T, hq, hk, d, sinks, dt, packed, back);
 }
 
 kda_status_t cache(WinCacheArgs &a) {
@@ -111,7 +111,7 @@ kda_status_t kda_window_attention(const void *q, const void *k, const void *v, k
 }
 
 size_t kda_window_varlen_attention_workspace_bytes(int N, int T_total, int H_q, int H_k, int d) {
-    return workspace_bytes(N, T_total, H_q, H_k, d, 0, true, false);
+    return workspace_bytes(N, T_total, H_q, H_k, d, 0, KDA_F32, true, false);
 }
 
 kda_status_t kda_window_varlen_attention(const void *q, const void *k, const void *v, kda_dtype_t dtype,
@@ -127,8 +127,8 @@ kda_status_t kda_window_varlen_attention(const void *q, const void *k, const voi
     return attention(a, true, false, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t kda_window_attention_backward_workspace_bytes(int B, int T, int H_q, int H_k, int d, int sinks) {
-    return workspace_bytes(B, T, H_q, H_k, d, sinks, false, true);
+size_t kda_window_attention_backward_workspace_bytes(int B, int T, int H_q, int H_k, int d, int sinks, kda_dtype_t dtype) {
+    return workspace_bytes(B, T, H_q, H_k, d, sinks, dtype, false, true);
 }
 
 kda_status_t kda_window_attention_backward(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -143,8 +143,9 @@ kda_status_t kda_window_attention_backward(const void *q, const void *k, const v
     return attention(a, false, true, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, int H_q, int H_k, int d, int sinks) {
-    return workspace_bytes(N, T_total, H_q, H_k, d, sinks, true, true);
+size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, int H_q, int H_k, int d, int sinks,
+                                                            kda_dtype_t dtype) {
+    return workspace_bytes(N, T_total, H_q, H_k, d, sinks, dtype, true, true);
 }
 
 kda_status_t kda_window_varlen_attention_backward(const void *q, const void *k, const void *v, const void *o,

@@ -440,18 +440,21 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
 
 // ================================================================ backward: dk, dv
 // An item is 128 keys of one key head; a step is 128 queries of one of its query
-// heads, over the near pairs. Transposed scores, so that keys are the rows:
+// heads. Transposed scores, so that keys are the rows:
 //   S^T = K Q^T,  dP^T = V dO^T                      (TMEM)
 //   P^T = 2^{c S^T - lse}, over S^T;  dS^T = P^T (dP^T - D), over dP^T   (bf16)
 //   dV += P^T dO,  dK += dS^T Q                      (TMEM, all steps of the item)
 // so each tile of Q and dO serves as an operand both ways round and nothing is
-// transposed in memory. Issued in the order dV(n), S(n+1), dK(n), dP(n+1): the
+// transposed in memory. One warp issues dV(n), S(n+1), another dK(n), dP(n+1): the
 // tensor core has two products to do while P is made and two while dS is.
 // Queries behind the sequence's end count as zeros with an infinite lse.
+// The far pairs are items of their own: the sinks against kWinFarQueries queries,
+// whose sums are parts that win_far_sum_kernel adds up.
 //
-// warp 0: TMA; 1: MMA; 2: lse and D of the queries; 4-11: P and dS, two threads a
-// key, 64 queries each (the halves of a bf16 row lie in the front of their 64
-// columns, so that no thread writes over scores that another one reads).
+// warp 0: TMA; 1: MMA of S and dV; 2: of dP and dK; 3: lse and D of the queries;
+// 4-11: P and dS, two threads a key, 64 queries each (the halves of a bf16 row lie
+// in the front of their 64 columns, so that no thread writes over scores that
+// another one reads).
 constexpr int BW_THREADS = 384;
 template <int D> struct Bw {
     static constexpr int TILE = 128 * D * 2, ATOM = 128 * 128;
@@ -471,9 +474,41 @@ struct BwArgs {
     WinGeom geo;
     __nv_bfloat16 *dq, *dk, *dv;
     const float *lse2, *delta;  // [hq][tokens]: lse in powers of two, D
-    const float *sums;          // far gradients of the sinks (see kda_window.cu), nullable
+    float *part, *near;         // gradients of the sinks, see win_far_sum_kernel
     float scale, c2;
-    int items;
+    int fars, items;            // items of far pairs come first
+};
+
+struct DkvItem {
+    int seq, start, len, j0, hk, q0, nq, steps, slot;  // q0: the first tile of 128 queries, nq: their number
+    bool far;
+    __device__ __forceinline__ DkvItem(const WinGeom &g, int it, int fars) {
+        far = it < fars;
+        if (!far) it -= fars;
+        const int t = g.by_hk.div(it);
+        hk = it - t * g.hk;
+        const WinTile x = win_tile(g, far ? t : t >> 1);
+        seq = x.seq, start = x.start, len = x.len, slot = 0;
+        if (far) {
+            j0 = 0;
+            const int end = min(len, x.first + kWinFarQueries), from = max(x.first, g.window);
+            q0 = from >> 7;
+            nq = x.first % kWinFarQueries == 0 && from < end ? ((end - 1) >> 7) - q0 + 1 : 0;
+            slot = win_far_slot(t, seq, kWinFarQueries / kWinTile);
+        } else {
+            j0 = x.first + (t & 1) * 128;
+            q0 = j0 >> 7;
+            nq = j0 < len ? (int)min((int64_t)len - 1, (int64_t)j0 + 126 + g.window) / 128 - q0 + 1 : 0;
+        }
+        steps = nq * g.group;
+    }
+};
+struct DkvStep {
+    int h, qt;
+    __device__ __forceinline__ DkvStep(const WinGeom &g, const DkvItem &x) : h(x.hk * g.group), qt(x.q0) {}
+    __device__ __forceinline__ void next(const DkvItem &x) {
+        if (++qt == x.q0 + x.nq) qt = x.q0, ++h;
+    }
 };
 
 template <int D>
@@ -491,7 +526,9 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
     if (tid == 0) {
         *ab.flag = 0;
         for (int i = 0; i < B::COUNT; ++i)
-            mbar_init(bar + i, i == B::B_PR || i == B::B_DR || i == B::B_AE || i >= B::B_LE ? 8 : 1);
+            mbar_init(bar + i, i == B::B_PR || i == B::B_DR || i == B::B_AE || i >= B::B_LE               ? 8
+                               : i == B::B_KE || i == B::B_AF || (i >= B::B_OE && i < B::B_OE + B::OS) ? 2
+                                                                                                       : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -502,28 +539,9 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tm, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    const uint32_t bars = smem_u32(bar);
+    auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
     bool ok = true;
-    struct Item {
-        int seq, start, len, j0, hk, q0, nq, steps;  // q0: the first tile of 128 queries, nq: their number
-        __device__ __forceinline__ Item(const WinGeom &g, int it) {
-            const int t = g.by_hk.div(it);
-            hk = it - t * g.hk;
-            const WinTile x = win_tile(g, t >> 1);
-            seq = x.seq, start = x.start, len = x.len, j0 = x.first + (t & 1) * 128;
-            q0 = j0 >> 7;
-            nq = (int)min((int64_t)len - 1, (int64_t)j0 + 126 + g.window) / 128 - q0 + 1;
-            steps = j0 < len ? nq * g.group : 0;
-        }
-    };
-    struct Step {
-        int h, qt;
-        __device__ __forceinline__ Step(const WinGeom &g, const Item &x) : h(x.hk * g.group), qt(x.q0) {}
-        __device__ __forceinline__ void next(const Item &x) {
-            if (++qt == x.q0 + x.nq) qt = x.q0, ++h;
-        }
-    };
-
-    auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
 
     if (warp == 0) {
         int n = 0, k = 0;  // steps, items so far
@@ -532,7 +550,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
             for (int c = 0; c < D / 64; ++c) tma_load_3d(d + c * B::ATOM, m, bar + full, 64 * c, h, row);
         };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const Item x(geo, it);
+            const DkvItem x(geo, it, p.fars);
             if (x.steps == 0) continue;
             if (!(ok = wait(B::B_KE, k + 1))) break;
             ++k;
@@ -542,7 +560,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 tile(sm + B::TILE, &mv, B::B_KF, x.hk, x.start + x.j0);
             }
             __syncwarp();
-            Step st(geo, x);
+            DkvStep st(geo, x);
             for (int j = 0; j < x.steps; ++j, ++n, st.next(x)) {
                 const int qs = n % B::QS, os = n % B::OS, row = x.start + st.qt * 128;
                 if (!(ok = wait(B::B_QE + qs, n / B::QS + 1))) break;
@@ -559,82 +577,78 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 __syncwarp();
             }
         }
-    } else if (warp == 1) {
+    } else if (warp < 3) {
+        // Two products of a step each: `a` over the item's own tile, of the step ahead, and the sum over the steps.
+        // first: S and dV; second: dP and dK. Both see every phase of both rings.
+        const int w = uni(warp - 1);
+        const uint32_t e = elected(), base = uni(tmem), sb = uni(smem_u32(sm)), bb = uni(bars);
         constexpr uint32_t I_S = idesc_bf16(128, 128, false, false), I_G = idesc_bf16(128, D, false, true);
-        const uint64_t kd = desc_k(smem_u32(sm)), vd = desc_k(smem_u32(sm + B::TILE));
-        int n = 0, k = 0;
-        // scores (of: K, the ring of Q) or dP (V, the ring of dO) of a step's queries
-        auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int rows, int full) {
-            if (rows < 128) zero_rows<D>(tile, rows, 128);
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t b = desc_k(smem_u32(tile));
-                mma_ss<false>(d, a, b, I_S);
+        const uint32_t t_p = base + 128 * w, t_g = base + 256 + 128 * w;
+        const uint64_t ad = desc_k(sb + w * B::TILE);
+        const uint64_t qk = desc_k(sb + B::RING_Q), qm = desc_mn(sb + B::RING_Q, B::ATOM);
+        const uint64_t ok_ = desc_k(sb + B::RING_O), om = desc_mn(sb + B::RING_O, B::ATOM);
+        auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
+        int k = 0, n = 0;
+        int qs = 0, qr = 0, os = 0, orr = 0;  // the stages and phases of step n's Q and dO
+        auto product = [&](int s) {       // of the tile in stage s of its ring
+            const uint64_t b = (w ? ok_ : qk) + ((s * B::TILE) >> 4);
 #pragma unroll
-                for (int ks = 1; ks < D / 16; ++ks) mma_ss<true>(d, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), I_S);
-                umma_commit(bar + full);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_if(e, t_p, ad + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), I_S, ks > 0);
+            commit_if(e, bb + 8 * (w ? B::B_DF : B::B_SF));
         };
-        // d (+)= the bf16 rows at `a` times the tile
-        auto gather = [&](uint32_t d, uint32_t a, unsigned char *tile, bool first) {
+        // Q and dO of a step have arrived; rows behind the sequence's end may hold anything
+        auto arrived = [&](int rows) {
+            if (!(ok = on(B::B_QF + qs, qr) && on(B::B_OF + os, orr))) return;
+            if (rows < 128) {
+                zero_rows<D>(sm + B::RING_Q + qs * B::TILE, rows, 128);
+                zero_rows<D>(sm + B::RING_O + os * B::TILE, rows, 128);
+            }
             tc_fence_after();
-            if (lane == 0) {
-                const uint64_t b = desc_mn(smem_u32(tile), B::ATOM);
-                if (first) umma_bf16_ts<false>(d, a, b, I_G);
-                else umma_bf16_ts<true>(d, a, b, I_G);
-#pragma unroll
-                for (int ks = 1; ks < 8; ++ks)
-                    umma_bf16_ts<true>(d, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G);
-            }
-            __syncwarp();
-        };
-        auto commit = [&](int b) {
-            if (lane == 0) umma_commit(bar + b);
-            __syncwarp();
         };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const Item x(geo, it);
-            if (x.steps == 0) continue;
-            if (!(ok = wait(B::B_KF, k))) break;
-            auto q_tile = [&](int i) { return sm + B::RING_Q + (i % B::QS) * B::TILE; };
-            auto o_tile = [&](int i) { return sm + B::RING_O + (i % B::OS) * B::TILE; };
-            Step st(geo, x);
-            if (!(ok = wait(B::B_QF + n % B::QS, n / B::QS))) break;
-            product(t_s, kd, q_tile(n), x.len - st.qt * 128, B::B_SF);
-            if (!(ok = wait(B::B_OF + n % B::OS, n / B::OS))) break;
-            product(t_dp, vd, o_tile(n), x.len - st.qt * 128, B::B_DF);
-            if (x.steps == 1) commit(B::B_KE);
-            for (int j = 0; j < x.steps; ++j, ++n) {
-                const bool more = j + 1 < x.steps;
-                st.next(x);
-                if (!(ok = wait(B::B_PR, n))) break;
-                if (j == 0 && !(ok = wait(B::B_AE, k + 1))) break;
-                gather(t_dv, t_s, o_tile(n), j == 0);
-                commit(B::B_OE + n % B::OS);
-                if (more) {
-                    if (!(ok = wait(B::B_QF + (n + 1) % B::QS, (n + 1) / B::QS))) break;
-                    product(t_s, kd, q_tile(n + 1), x.len - st.qt * 128, B::B_SF);
-                }
-                if (!(ok = wait(B::B_DR, n))) break;
-                gather(t_dk, t_dp, q_tile(n), j == 0);
-                commit(B::B_QE + n % B::QS);
-                if (more) {
-                    if (!(ok = wait(B::B_OF + (n + 1) % B::OS, (n + 1) / B::OS))) break;
-                    product(t_dp, vd, o_tile(n + 1), x.len - st.qt * 128, B::B_DF);
-                    if (j + 2 == x.steps) commit(B::B_KE);
+            const DkvItem x(geo, it, p.fars);
+            const int steps = uni(x.steps), len = uni(x.len), q0 = uni(x.q0), nq = uni(x.nq);
+            if (steps == 0) continue;
+            if (!(ok = on(B::B_KF, k))) break;
+            int qt = 0;
+            arrived(len - q0 * 128);
+            if (!ok) break;
+            product(w ? os : qs);
+            if (w) commit_if(e, bb + 8 * (B::B_OE + os));
+            if (steps == 1) commit_if(e, bb + 8 * B::B_KE);
+            for (int j = 0; j < steps; ++j, ++n) {
+                const int qs0 = qs, os0 = os;
+                if (++qs == B::QS) qs = 0, qr ^= 1;
+                if (++os == B::OS) os = 0, orr ^= 1;
+                if (++qt == nq) qt = 0;
+                if (!(ok = on(w ? B::B_DR : B::B_PR, n))) break;
+                if (j == 0 && !(ok = on(B::B_AE, k + 1))) break;
+                tc_fence_after();
+                const uint64_t b = w ? qm + ((qs0 * B::TILE) >> 4) : om + ((os0 * B::TILE) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts_if(e, t_g, t_p + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G, j > 0 || ks > 0);
+                // Q has been used by S long before dK, dO by both
+                commit_if(e, bb + 8 * (w ? B::B_QE + qs0 : B::B_OE + os0));
+                if (j + 1 < steps) {
+                    arrived(len - (q0 + qt) * 128);
+                    if (!ok) break;
+                    product(w ? os : qs);
+                    if (w) commit_if(e, bb + 8 * (B::B_OE + os));
+                    if (j + 2 == steps) commit_if(e, bb + 8 * B::B_KE);
                 } else {
-                    commit(B::B_AF);
+                    commit_if(e, bb + 8 * B::B_AF);
                 }
             }
             ++k;
         }
-    } else if (warp == 2) {
+    } else if (warp == 3) {
         // four queries a lane; the next step's are on their way while this one's wait to be let in
-        int n = 0, it = blockIdx.x;
+        int n = 0;
         float *vec = reinterpret_cast<float *>(sm + B::VEC);
         float l[4], d[4];
-        auto load = [&](const Item &x, const Step &st) {
+        auto load = [&](const DkvItem &x, const DkvStep &st) {
             const int i0 = st.qt * 128 + 4 * lane;
             const int64_t at = (int64_t)st.h * geo.tokens + x.start + i0;
 #pragma unroll
@@ -644,62 +658,64 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 d[e] = there ? __ldg(p.delta + at + e) : 0.f;
             }
         };
-        for (; it < p.items && ok; it += gridDim.x) {
-            const Item x(geo, it);
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const DkvItem x(geo, it, p.fars);
             if (x.steps == 0) continue;
-            Step st(geo, x);
+            DkvStep st(geo, x);
             load(x, st);
             for (int j = 0; j < x.steps; ++j, ++n) {
-                const float4 lv = make_float4(l[0], l[1], l[2], l[3]), dv = make_float4(d[0], d[1], d[2], d[3]);
+                const float4 lv = make_float4(-l[0], -l[1], -l[2], -l[3]), dv = make_float4(-d[0], -d[1], -d[2], -d[3]);
                 st.next(x);
                 if (j + 1 < x.steps) load(x, st);
-                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_LE, (n & 1) ^ 1));
-                if (!ok) break;
+                if (!(ok = wait(B::B_LE, n + 1))) break;
                 reinterpret_cast<float4 *>(vec)[lane] = lv;
                 warp_arrive(bar + B::B_LF);
-                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_XE, (n & 1) ^ 1));
-                if (!ok) break;
+                if (!(ok = wait(B::B_XE, n + 1))) break;
                 reinterpret_cast<float4 *>(vec + 128)[lane] = dv;
                 warp_arrive(bar + B::B_XF);
             }
         }
-    } else if (warp >= 4) {
+    } else {
         const int half = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = t_s + lanes + 64 * half, td = t_dp + lanes + 64 * half;
+        const float *vec = reinterpret_cast<const float *>(sm + B::VEC) + 64 * half;
+        const F2 c2 = f2(p.c2, p.c2);
         int n = 0, k = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-            const Item x(geo, it);
+            const DkvItem x(geo, it, p.fars);
             if (x.steps == 0) continue;
             const int j = x.j0 + row;  // this thread's key
-            Step st(geo, x);
+            DkvStep st(geo, x);
+#pragma unroll 1
             for (int u = 0; u < x.steps; ++u, ++n, st.next(x)) {
                 const int i0 = st.qt * 128;
-                const float *vec = reinterpret_cast<const float *>(sm + B::VEC) + 64 * half;
-                const int lo = j - i0 - 64 * half, hi = lo + geo.window - 1;  // columns of the half that see the key
+                const int d0 = j - i0 - 64 * half;  // the half's column of the key's own token
                 float pr[64];
-                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_LF, n & 1) && ab.wait(bar + B::B_SF, n & 1));
-                if (!ok) break;
+                if (!(ok = wait(B::B_LF, n) && wait(B::B_SF, n))) break;
                 tc_fence_after();
-                const F2 c2 = f2(p.c2, p.c2);
                 uint32_t v[2][32];
                 tmem_ld32(ts, v[0]);
                 tmem_ld32(ts + 32, v[1]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(vec + c);
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(vec + c);
                     const uint32_t *y = v[c >> 5] + (c & 31);
                     float a, b;
-                    f2_get(fma2(pair_w(y[0], y[1]), c2, f2(-l.x, -l.y)), a, b);
+                    f2_get(fma2(pair_w(y[0], y[1]), c2, F2{l.x}), a, b);
                     pr[c] = exp2_approx(a), pr[c + 1] = exp2_approx(b);
-                    f2_get(fma2(pair_w(y[2], y[3]), c2, f2(-l.z, -l.w)), a, b);
+                    f2_get(fma2(pair_w(y[2], y[3]), c2, F2{l.y}), a, b);
                     pr[c + 2] = exp2_approx(a), pr[c + 3] = exp2_approx(b);
                 }
-                if (i0 < x.j0 + 127) {  // some query comes before the key, or too far behind it
+                // far: the queries behind the window see the sinks; near: from the key's own token to the window's end
+                const bool edge = x.far ? true : i0 < x.j0 + 127;
+                if (edge) {
+                    const int lo = !x.far ? d0 : j < geo.sinks ? d0 + geo.window : 64;
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pr[c] = c < lo ? 0.f : pr[c];
                 }
-                if (i0 + 127 - x.j0 >= geo.window) {
+                if (!x.far && i0 + 127 - x.j0 >= geo.window) {
+                    const int hi = d0 + geo.window - 1;
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pr[c] = c > hi ? 0.f : pr[c];
                 }
@@ -720,8 +736,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 #pragma unroll
                     for (int e = 0; e < 64; ++e) pr[e] = 0.f;
                 }
-                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_XF, n & 1) && ab.wait(bar + B::B_DF, n & 1));
-                if (!ok) break;
+                if (!(ok = wait(B::B_XF, n) && wait(B::B_DF, n))) break;
                 tc_fence_after();
                 tmem_ld32(td, v[0]);
                 tmem_ld32(td + 32, v[1]);
@@ -731,10 +746,10 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 d = *reinterpret_cast<const float4 *>(vec + 128 + 32 * c + e);
+                        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(vec + 128 + 32 * c + e);
                         const float *w = pr + 32 * c + e;
-                        o[e / 2] = pack2((pair_w(v[c][e], v[c][e + 1]) + f2(-d.x, -d.y)) * f2(w[0], w[1]));
-                        o[e / 2 + 1] = pack2((pair_w(v[c][e + 2], v[c][e + 3]) + f2(-d.z, -d.w)) * f2(w[2], w[3]));
+                        o[e / 2] = pack2((pair_w(v[c][e], v[c][e + 1]) + F2{d.x}) * f2(w[0], w[1]));
+                        o[e / 2 + 1] = pack2((pair_w(v[c][e + 2], v[c][e + 3]) + F2{d.y}) * f2(w[2], w[3]));
                     }
                     tmem_st16(td + 16 * c, o);
                 }
@@ -744,16 +759,17 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 warp_arrive(bar + B::B_XE);
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_AF, k & 1));
-            if (!ok) break;
-            ++k;
+            if (!(ok = wait(B::B_AF, k++))) break;
             tc_fence_after();
-            // half 0: dv, half 1: dk
-            const bool there = j < x.len, sink = p.sums && j < geo.sinks;
+            // half 0: dv, half 1: dk. Of sinks that far queries see too, in fp32, for the sum of both.
+            const bool there = j < x.len && (!x.far || j < geo.sinks),
+                       sink = x.far || (j < geo.sinks && x.len > geo.window);
             const uint32_t src = (half ? t_dk : t_dv) + lanes;
             const float f = half ? p.scale : 1.f;
             __nv_bfloat16 *dst = (half ? p.dk : p.dv) + ((int64_t)(x.start + j) * geo.hk + x.hk) * D;
-            const float *far = p.sums + (((int64_t)x.seq * geo.hk + x.hk) * 2 * geo.sinks + (half ? 0 : geo.sinks) + j) * D;
+            float *sum = (x.far ? p.part : p.near) +
+                         (((int64_t)(x.far ? x.slot : x.seq) * geo.hk + x.hk) * 2 * geo.sinks + (half ? 0 : geo.sinks) + j) * D;
+            const F2 ff = f2(f, f);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t v[32];
@@ -761,14 +777,19 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 tmem_wait_ld();
                 if (!there) continue;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), f, sink ? far[c + e] : 0.f));
-#pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    uint32_t r[8];
+                    F2 g[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = pack2(pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]));
-                    st_v8(dst + c + 16 * q, r);
+                    for (int e = 0; e < 8; ++e) g[e] = pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]) * ff;
+                    if (sink) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) *reinterpret_cast<unsigned long long *>(sum + c + 16 * q + 2 * e) = g[e].v;
+                    } else {
+                        uint32_t r[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = pack2(g[e]);
+                        st_v8(dst + c + 16 * q, r);
+                    }
                 }
             }
             tc_fence_before();
@@ -789,12 +810,11 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 // An item is 128 queries of one head; a step is 128 keys (or the sinks, as in the
 // forward):
 //   S = Q K^T (two of it),  dP = dO V^T,  dS = P (dP - D) over S (bf16),  dQ += dS K
-// issued in the order S(n+1), dP(n+1), dQ(n), where dP(n+1) waits until dP(n) is in
-// registers and dQ(n) until dS(n) is made: dS of a step is made while the tensor
-// core does dQ of the step before and S and dP of the one behind. K is kept for two steps
-// (S and dQ), V for one.
+// One warp issues S(n+1), dQ(n), another dP(n+1), as soon as dP(n) is in registers:
+// dS of a step is made while the tensor core does dQ of the step before and S and
+// dP of the one behind. K is kept for two steps (S and dQ), V for one.
 //
-// warp 0: TMA; 1: MMA; 4-11: dS, two threads a query, 64 keys each.
+// warp 0: TMA; 1: MMA of S and dQ; 2: of dP; 4-11: dS, two threads a query, 64 keys each.
 template <int D>
 __global__ void __launch_bounds__(BW_THREADS, 1)
 win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -811,7 +831,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     // KF, KE: the items' Q and dO; SF: of the two scores (SF, PR); DF, DR; AF, AE: dQ
     if (tid == 0) {
         *ab.flag = 0;
-        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_DR1 || i == B::B_AE || i == B::B_DL ? 8 : 1);
+        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_DR1 || i == B::B_AE || i == B::B_DL ? 8 : i == B::B_KE ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -845,7 +865,8 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
         __device__ __forceinline__ int keys(int j) const { return is_far(j) ? kw : 128; }
     };
 
-    auto wait = [&](int b, int phase) { return __all_sync(0xffffffffu, ab.wait(bar + b, phase & 1)); };
+    const uint32_t bars = smem_u32(bar);
+    auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
 
     if (warp == 0) {
         int n = 0, k = 0;
@@ -885,73 +906,69 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                 keys(&mv, &mv16, sm + B::RING_O + vs * B::TILE, B::B_OF + vs, j);
             }
         }
-    } else if (warp == 1) {
-        constexpr uint32_t I_G = idesc_bf16(128, D, false, true);
-        const uint64_t qd = desc_k(smem_u32(sm)), od = desc_k(smem_u32(sm + B::TILE));
-        int n = 0, k = 0;
-        auto product = [&](uint32_t d, uint64_t a, unsigned char *tile, int keys, int full) {
+    } else if (warp < 3) {
+        // the first: S a step ahead and dQ; the second: dP. Both see every phase of the keys' ring that they read.
+        const int w = uni(warp - 1);
+        const uint32_t e = elected(), base = uni(tmem), sb = uni(smem_u32(sm)), bb = uni(bars);
+        constexpr uint32_t I_G = idesc_bf16(128, D, false, true), I_S = idesc_bf16(128, 128, false, false);
+        const uint64_t ad = desc_k(sb + w * B::TILE), kd = desc_k(sb + (w ? B::RING_O : B::RING_Q)),
+                       km = desc_mn(sb + B::RING_Q, B::ATOM);
+        auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
+        int n = 0, k = 0, s = 0, round = 0;  // s: the stage of step n + 1's K, or V
+        auto product = [&](uint32_t d, uint32_t idesc, int full) {
+            const uint64_t b = kd + ((s * B::TILE) >> 4);
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t idesc = idesc_bf16(128, keys, false, false);
-                const uint64_t b = desc_k(smem_u32(tile));
-                mma_ss<false>(d, a, b, idesc);
 #pragma unroll
-                for (int ks = 1; ks < D / 16; ++ks) mma_ss<true>(d, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), idesc);
-                umma_commit(bar + full);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_if(e, d, ad + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), idesc, ks > 0);
+            commit_if(e, bb + 8 * full);
         };
-        auto commit = [&](int b) {
-            if (lane == 0) umma_commit(bar + b);
-            __syncwarp();
-        };
-        auto k_tile = [&](int i) { return sm + B::RING_Q + (i % B::QS) * B::TILE; };
-        auto v_tile = [&](int i) { return sm + B::RING_O + (i % B::OS) * B::TILE; };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x(geo, it);
-            if (x.steps == 0) continue;
-            // keys behind the sequence's end are masked, but their rows of K meet the zeros of dS
-            auto scores = [&](int j, int i) {
-                if (!(ok = wait(B::B_QF + i % B::QS, i / B::QS))) return;
-                const int behind = x.len - x.key0(j);
-                if (behind < x.keys(j)) zero_rows<D>(k_tile(i), behind, x.keys(j));
-                product(tmem + 128 * (i & 1), qd, k_tile(i), x.keys(j), B::B_SF + (i & 1));
-            };
-            auto dp = [&](int j, int i) {
-                if (!(ok = wait(B::B_OF + i % B::OS, i / B::OS))) return;
-                product(t_dp, od, v_tile(i), x.keys(j), B::B_DF);
-                commit(B::B_OE + i % B::OS);
-                if (j + 1 == x.steps) commit(B::B_KE);  // Q and dO have been used for the last time
-            };
-            if (!(ok = wait(B::B_KF, k))) break;
-            scores(0, n);
-            if (ok) dp(0, n);
-            for (int j = 0; j < x.steps && ok; ++j, ++n) {
-                const bool more = j + 1 < x.steps;
-                if (more) {
-                    scores(j + 1, n + 1);
-                    if (!ok) break;
+            const int steps = uni(x.steps), far = uni(x.far), kw = uni(x.kw), len = uni(x.len), behind = len - uni(x.kt0) * 128;
+            if (steps == 0) continue;
+            if (!(ok = on(B::B_KF, k))) break;
+            const uint32_t i0 = far ? idesc_bf16(128, kw, false, false) : I_S;  // of the first step
+            if (w == 0) {
+                // keys behind the sequence's end are masked, but their rows of K meet the zeros of dS
+                auto scores = [&](int j) {
+                    if (!(ok = on(B::B_QF + s, round))) return;
+                    const int rows = j < far ? len : behind - 128 * (j - far), keys = j < far ? kw : 128;
+                    if (rows < keys) zero_rows<D>(sm + B::RING_Q + s * B::TILE, rows, keys);
+                    product(base + 128 * ((n + (j > 0)) & 1), j == 0 ? i0 : I_S, B::B_SF + ((n + (j > 0)) & 1));
+                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_KE);  // Q has been used for the last time
+                    if (++s == B::QS) s = 0, round ^= 1;
+                };
+                int sd = s;  // the stage of step n's K
+                scores(0);
+                for (int j = 0; j < steps && ok; ++j, ++n) {
+                    if (j + 1 < steps) {
+                        scores(j + 1);
+                        if (!ok) break;
+                    }
+                    if (!(ok = on(made(n), n >> 1))) break;
+                    if (j == 0 && !(ok = on(B::B_AE, k + 1))) break;
+                    tc_fence_after();
+                    const uint32_t a = base + 128 * (n & 1);
+                    const uint64_t b = km + ((sd * B::TILE) >> 4);
+                    const int keys = j < far ? kw : 128;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts_if(keys > 16 * ks ? e : 0u, base + 384, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G,
+                                  j > 0 || ks > 0);
+                    commit_if(e, bb + 8 * (B::B_QE + sd));
+                    if (++sd == B::QS) sd = 0;
+                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_AF);
                 }
-                if (!(ok = wait(B::B_DL, n))) break;
-                if (more) {
-                    dp(j + 1, n + 1);
-                    if (!ok) break;
+            } else {
+                for (int j = 0; j < steps; ++j, ++n) {
+                    if (!(ok = on(B::B_OF + s, round))) break;
+                    if (n > 0 && !(ok = on(B::B_DL, n - 1))) break;  // dP of the step before is in registers
+                    product(base + 256, j == 0 ? i0 : I_S, B::B_DF);
+                    commit_if(e, bb + 8 * (B::B_OE + s));
+                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_KE);
+                    if (++s == B::OS) s = 0, round ^= 1;
                 }
-                if (!(ok = wait(made(n), n >> 1))) break;
-                if (j == 0 && !(ok = wait(B::B_AE, k + 1))) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a = tmem + 128 * (n & 1);
-                    const uint64_t b = desc_mn(smem_u32(k_tile(n)), B::ATOM);
-                    if (j == 0) umma_bf16_ts<false>(t_dq, a, b, I_G);
-                    else umma_bf16_ts<true>(t_dq, a, b, I_G);
-                    const int count = x.keys(j) / 16;
-                    for (int ks = 1; ks < count; ++ks)
-                        umma_bf16_ts<true>(t_dq, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G);
-                    umma_commit(bar + B::B_QE + n % B::QS);
-                    if (!more) umma_commit(bar + B::B_AF);
-                }
-                __syncwarp();
             }
             ++k;
         }
@@ -974,8 +991,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                 const int hi = (far ? min(geo.sinks, i - geo.window + 1) - 1 - 64 * half : single ? -1 : i - k0),
                           lo = far ? 0 : i - geo.window + 1 - k0;
                 const uint32_t ts = tmem + 128 * (n & 1) + lanes + 64 * half;
-                ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_SF + (n & 1), (n >> 1) & 1) && ab.wait(bar + B::B_DF, n & 1));
-                if (!ok) break;
+                if (!(ok = wait(B::B_SF + (n & 1), n >> 1) && wait(B::B_DF, n))) break;
                 tc_fence_after();
                 uint32_t v[2][32], d[2][32];
                 if (chunks > 0) {
@@ -1019,9 +1035,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                 warp_arrive(bar + made(n));
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, ab.wait(bar + B::B_AF, k & 1));
-            if (!ok) break;
-            ++k;
+            if (!(ok = wait(B::B_AF, k++))) break;
             tc_fence_after();
             __nv_bfloat16 *dst = p.dq + ((int64_t)(x.start + i) * geo.hq + x.h) * D;
             const F2 sc = f2(p.scale, p.scale);
@@ -1083,7 +1097,7 @@ template <int D> cudaError_t forward(const WinGeom &geo, const WinArgs &a, cudaS
 }
 
 template <int D>
-cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta, const float *sums,
+cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta, float *part, float *near,
                      cudaStream_t s) {
     CUtensorMap mq, mk, mv, mo, mk16, mv16;
     if (!token_map<D>(&mq, a.q, a.q_stride, a.hq, geo.tokens, 128) ||
@@ -1097,8 +1111,9 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
     cudaError_t e = allow_smem(win_dkv_tc_kernel<D>, Bw<D>::SMEM, allowed[0]);
     if (e == cudaSuccess) e = allow_smem(win_dq_tc_kernel<D>, Bw<D>::SMEM, allowed[1]);
     if (e != cudaSuccess) return e;
-    BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, sums,
-             a.scale, a.scale * 1.4426950408889634f, geo.ntiles * 2 * geo.hk};
+    const int fars = geo.sinks > 0 && geo.window < geo.T ? geo.ntiles * geo.hk : 0;
+    BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, part, near,
+             a.scale, a.scale * 1.4426950408889634f, fars, fars + geo.ntiles * 2 * geo.hk};
     const int sms = sm_count();
     win_dkv_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, s>>>(p, mq, mk, mv, mo);
     e = cudaGetLastError();
@@ -1111,8 +1126,8 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
 }  // namespace
 
 cudaError_t launch_window_backward_tc(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta,
-                                      const float *sums, cudaStream_t s) {
-    return a.d == 128 ? backward<128>(geo, a, lse2, delta, sums, s) : backward<64>(geo, a, lse2, delta, sums, s);
+                                      float *part, float *near, cudaStream_t s) {
+    return a.d == 128 ? backward<128>(geo, a, lse2, delta, part, near, s) : backward<64>(geo, a, lse2, delta, part, near, s);
 }
 
 cudaError_t launch_window_forward_tc(const WinGeom &geo, const WinArgs &a, cudaStream_t s) {

@@ -158,4 +158,4 @@ def test_workspace_sizes(lib):
     assert kda.window_varlen_attention_workspace_bytes(-1, 10, 4, 2) == 0
     f = kda.window_attention_backward_workspace_bytes
     assert 0 < f(1, 64, 4, 2) < f(1, 4096, 4, 2) < f(1, 4096, 4, 2, 128, 64)
-    assert f(1, 64, 4, 3) == 0 and f(1, 64, 4, 2, 128, 129) == 0
+    assert f(1, 64, 4, 3) == 0 and f(1, 64, 4, 2, 128, 129) == 0 and f(1, 4096, 4, 2, 128, 64, torch.float32) > f(1, 4096, 4, 2, 128, 64)
