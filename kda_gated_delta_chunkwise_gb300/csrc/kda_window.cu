@@ -286,52 +286,157 @@ win_forward_kernel(WinParams p) {
 }
 
 // D_i = do_i . o_i, and lse (see weight), both by head: a tile of queries is a
-// stretch of memory then. A row is 16 bytes in each of d sizeof(T) / 16 lanes, a
-// block 32 tokens of one head at a time.
+// stretch of memory then. A block takes eight tokens of every head, in the order of
+// memory, and writes a sector of each head's; a row is 16 bytes in each of
+// d sizeof(T) / 16 lanes.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 win_delta_kernel(const T *o, const T *d_o, const float *lse, float *lse2, float *delta, int64_t tokens, int hq) {
-    constexpr int N = 16 / sizeof(T), LANES = D / N, PER = 256 / LANES;
-    const int h = blockIdx.y, in = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-    const int64_t t0 = (int64_t)blockIdx.x * 32;
-    uint4 a[32 / PER], b[32 / PER];
+    constexpr int N = 16 / sizeof(T), LANES = D / N, PER = 256 / LANES, FLIGHT = 4;
+    extern __shared__ float sums[];  // [hq][8]
+    const int in = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const int64_t t0 = (int64_t)blockIdx.x * 8;
+    const int count = (int)(tokens - t0 < 8 ? tokens - t0 : 8), rows = count * hq;
+    const T *ob = o + t0 * hq * D + in * N, *db = d_o + t0 * hq * D + in * N;
+    for (int r0 = 0; r0 < rows; r0 += FLIGHT * PER) {
+        uint4 a[FLIGHT], b[FLIGHT];
 #pragma unroll
-    for (int i = 0; i < 32 / PER; ++i) {
-        const int64_t t = t0 + i * PER + sub, at = (t * hq + h) * D + in * N;
-        a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < tokens) a[i] = *reinterpret_cast<const uint4 *>(o + at), b[i] = *reinterpret_cast<const uint4 *>(d_o + at);
-    }
+        for (int i = 0; i < FLIGHT; ++i) {
+            const int r = r0 + i * PER + sub;
+            a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows)
+                a[i] = *reinterpret_cast<const uint4 *>(ob + (int64_t)r * D), b[i] = *reinterpret_cast<const uint4 *>(db + (int64_t)r * D);
+        }
 #pragma unroll
-    for (int i = 0; i < 32 / PER; ++i) {
-        const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-        float s = 0.f;
+        for (int i = 0; i < FLIGHT; ++i) {
+            const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+            float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (sizeof(T) == 4) {
-                s = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), s);
-            } else {
-                s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
-                s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s);
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(T) == 4) {
+                    s = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), s);
+                } else {
+                    s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
+                    s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s);
+                }
             }
-        }
 #pragma unroll
-        for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const int64_t t = t0 + i * PER + sub;
-        if (in == 0 && t < tokens) {
-            delta[h * tokens + t] = s;
-            lse2[h * tokens + t] = lse[t * hq + h] * (sizeof(T) == 2 ? kLog2e : 1.f);
+            for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            const int r = r0 + i * PER + sub;
+            if (in == 0 && r < rows) sums[r % hq * 8 + r / hq] = s;
         }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * hq; i += 256) {
+        const int h = i >> 3, t = i & 7;
+        if (t >= count) continue;
+        delta[h * tokens + t0 + t] = sums[i];
+        lse2[h * tokens + t0 + t] = lse[(t0 + t) * hq + h] * (sizeof(T) == 2 ? kLog2e : 1.f);
     }
 }
 
-// dq; or, with DELTA, D_i once more as sum_j p_ij dp_ij, for tokens that see few
-// others: all of a narrow window's (few_keys), else the first 64 of every
-// sequence. There a weight may be close to one, ds = p (dp - D) far smaller than
-// dp, and the rounding of the stored bf16 o, which do . o takes into D, would be
-// seen in dq and dk (1.2e-2 of dq for two tokens).
+// D_i once more as sum_j p_ij dp_ij, for tokens that see few others: all of a
+// narrow window's (few_keys), else the first 64 of every sequence. There a weight
+// may be close to one, ds = p (dp - D) far smaller than dp, and the rounding of the
+// stored bf16 o, which do . o takes into D, would be seen in dq and dk (1.2e-2 of dq
+// for two tokens). A warp takes 16 queries, 16 keys at a time: s and dp are both
+// products of rows, so the fragments of mma.sync come straight from memory (a
+// contraction does not mind the order of its index: a lane reads 16 bytes of
+// consecutive channels).
 __host__ __device__ __forceinline__ bool few_keys(int window, int sinks) { return window + sinks <= 64; }
 
-template <typename T, int D, bool DELTA>
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(128)
+win_first_delta_kernel(WinParams p) {
+    using T = __nv_bfloat16;
+    constexpr int KC = D / 32;  // 16-byte pieces of a lane and row
+    const WinGeom &geo = p.geo;
+    const bool firsts = !few_keys(geo.window, geo.sinks);  // `at` counts sequences, else 64 queries
+    const int at = geo.by_hq.div(blockIdx.x), h = blockIdx.x - at * geo.hq, hk = h / geo.group;
+    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) return;
+    const WinTile tile = win_tile(geo, !firsts ? at >> 2 : geo.tiles ? geo.seq_tile[at] : at * geo.per_seq);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int i0 = (firsts ? 0 : tile.first + (at & 3) * 64) + (threadIdx.x >> 5) * 16;
+    if (i0 >= tile.len) return;
+    uint4 q[2][KC], d[2][KC];
+    float lse2[2], sum[2] = {0.f, 0.f}, all[2] = {0.f, 0.f};
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = i0 + g + 8 * r;
+        const bool there = i < tile.len;
+        const int64_t token = tile.start + (there ? i : 0);
+        const T *qr = (const T *)p.q + token * p.q_stride + h * D + 8 * t, *dr = (const T *)p.d_o + (token * geo.hq + h) * D + 8 * t;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            q[r][c] = there ? *reinterpret_cast<const uint4 *>(qr + 32 * c) : zero;
+            d[r][c] = there ? *reinterpret_cast<const uint4 *>(dr + 32 * c) : zero;
+        }
+        lse2[r] = there ? p.lse[token * geo.hq + h] * kLog2e : 0.f;
+    }
+    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D + 8 * t;
+    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D + 8 * t;
+    const float c2 = p.scale * kLog2e;
+    auto walk = [&](int from, int to, bool far) {
+        for (int j0 = from; j0 < to; j0 += 16) {
+            float s[2][4], dp[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int j = j0 + 8 * b + g;
+                const bool there = j < to;
+                uint4 k[KC], v[KC];
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    k[c] = there ? *reinterpret_cast<const uint4 *>(kb + (int64_t)j * p.k_stride + 32 * c) : zero;
+                    v[c] = there ? *reinterpret_cast<const uint4 *>(vb + (int64_t)j * p.v_stride + 32 * c) : zero;
+                }
+                s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+                dp[b][0] = dp[b][1] = dp[b][2] = dp[b][3] = 0.f;
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    mma_bf16(s[b], q[0][c].x, q[1][c].x, q[0][c].y, q[1][c].y, k[c].x, k[c].y);
+                    mma_bf16(s[b], q[0][c].z, q[1][c].z, q[0][c].w, q[1][c].w, k[c].z, k[c].w);
+                    mma_bf16(dp[b], d[0][c].x, d[1][c].x, d[0][c].y, d[1][c].y, v[c].x, v[c].y);
+                    mma_bf16(dp[b], d[0][c].z, d[1][c].z, d[0][c].w, d[1][c].w, v[c].z, v[c].w);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + g + 8 * (e >> 1), j = j0 + 8 * b + 2 * t + (e & 1);
+                    const float w = j < to && sees(i, j, geo.window, geo.sinks, far)
+                                        ? exp2_approx(fmaf(s[b][e], c2, -lse2[e >> 1]))
+                                        : 0.f;
+                    all[e >> 1] += w;
+                    sum[e >> 1] = fmaf(w, w > 0.f ? dp[b][e] : 0.f, sum[e >> 1]);
+                }
+        }
+    };
+    const int end = min(i0 + 16, tile.len);
+    if (end > geo.window) walk(0, min(geo.sinks, end - geo.window), true);
+    walk(max(0, i0 - geo.window + 1), end, false);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 1; off < 4; off *= 2) {
+            all[e] += __shfl_xor_sync(0xffffffffu, all[e], off);
+            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], off);
+        }
+        const int i = i0 + g + 8 * e;
+        if (t == 0 && i < tile.len && all[e] > 0.f) p.delta[(int64_t)h * geo.tokens + tile.start + i] = sum[e] / all[e];
+    }
+}
+
+template <typename T, int D>
 __global__ void __launch_bounds__(NT)
 win_dq_kernel(WinParams p) {
     constexpr bool SPLIT = sizeof(T) == 4;
@@ -339,10 +444,8 @@ win_dq_kernel(WinParams p) {
     float *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
     const WinGeom &geo = p.geo;
     const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
-    const bool firsts = DELTA && !few_keys(geo.window, geo.sinks);  // `at` counts sequences
-    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) return;
-    const WinTile tile = win_tile(geo, !firsts ? at >> 2 : geo.tiles ? geo.seq_tile[at] : at * geo.per_seq);
-    const int i0 = firsts ? 0 : tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
+    const WinTile tile = win_tile(geo, at >> 2);
+    const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
     if (rows <= 0) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
     const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
@@ -357,10 +460,9 @@ win_dq_kernel(WinParams p) {
     for (int e = 0; e < 2; ++e) {
         const bool there = r0 + e * 8 < rows;
         lse[e] = there ? p.lse2[vec0 + r0 + e * 8] : 0.f;
-        delta[e] = there && !DELTA ? p.delta[vec0 + r0 + e * 8] : 0.f;
+        delta[e] = there ? p.delta[vec0 + r0 + e * 8] : 0.f;
     }
     const float scale = SPLIT ? p.scale : p.scale * kLog2e;
-    float all[2] = {0.f, 0.f};  // DELTA: the sum of the weights, one but for rounding
     auto walk = [&](int from, int to, bool far) {
         for (int j0 = from; j0 < to; j0 += COLS) {
             __syncthreads();
@@ -377,42 +479,23 @@ win_dq_kernel(WinParams p) {
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
                     const bool on = j < to && sees(i, j, geo.window, geo.sinks, far) && !alone(i, geo.window, geo.sinks);
-                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, lse[e >> 1]) : 0.f;
-                    if (DELTA) {
-                        all[e >> 1] += s[nb][e];
-                        delta[e >> 1] = fmaf(s[nb][e], dp[nb][e], delta[e >> 1]);
-                    } else {
-                        s[nb][e] *= dp[nb][e] - delta[e >> 1];
-                    }
+                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, lse[e >> 1]) * (dp[nb][e] - delta[e >> 1]) : 0.f;
                 }
             }
-            if constexpr (!DELTA) weights_by_rows<SPLIT, D>(acc, s, sk);
+            weights_by_rows<SPLIT, D>(acc, s, sk);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
     walk(max(0, i0 - geo.window + 1), i0 + rows, false);
-    if constexpr (DELTA) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + e * 8;
+        if (r >= rows) continue;
+        T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
 #pragma unroll
-            for (int off = 1; off < 4; off *= 2) {
-                all[e] += __shfl_xor_sync(0xffffffffu, all[e], off);
-                delta[e] += __shfl_xor_sync(0xffffffffu, delta[e], off);
-            }
-            if (t == 0 && r0 + e * 8 < rows && all[e] > 0.f)  // not of a token that sees itself alone
-                p.delta[vec0 + r0 + e * 8] = delta[e] / all[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = r0 + e * 8;
-            if (r >= rows) continue;
-            T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
-#pragma unroll
-            for (int nb = 0; nb < D / 8; ++nb) {
-                dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
-                dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
-            }
+        for (int nb = 0; nb < D / 8; ++nb) {
+            dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
+            dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
         }
     }
 }
@@ -626,15 +709,16 @@ template <typename T, int D> cudaError_t forward(const WinPlan &p, const WinArgs
 }
 
 template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
-    static std::atomic<uint64_t> allowed[4];
+    static std::atomic<uint64_t> allowed[3];
     constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(float);
     const WinParams w = params(p, a);
-    win_delta_kernel<T, D><<<dim3((unsigned)((p.geo.tokens + 31) / 32), a.hq), 256, 0, s>>>(
+    win_delta_kernel<T, D><<<(unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float), s>>>(
         (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq);
     KDA_TRY(cudaGetLastError());
-    if (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
         const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
-        KDA_TRY(run(win_dq_kernel<T, D, true>, allowed[3], (unsigned)(blocks * a.hq), smem, s, w));
+        win_first_delta_kernel<D><<<(unsigned)(blocks * a.hq), 128, 0, s>>>(w);
+        KDA_TRY(cudaGetLastError());
     }
     const bool far = a.sinks > 0 && a.window < a.T;  // some sequence may be longer than the window
     if constexpr (sizeof(T) == 2) {
@@ -642,7 +726,7 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
     } else {
         if (far) KDA_TRY(run(win_dkv_kernel<T, D, true>, allowed[0], (unsigned)(p.geo.ntiles * 2 * a.hk), smem, s, w));
         KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
-        KDA_TRY(run(win_dq_kernel<T, D, false>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
+        KDA_TRY(run(win_dq_kernel<T, D>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
     }
     if (far)
         win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(

@@ -24,7 +24,7 @@ kda_status_t sizes(int N, int64_t T, int hq, bool packed) {
     const int64_t tokens = packed ? T : N * T;
     if (tokens > 1 << 30) return fail(KDA_ERR_UNSUPPORTED, "2^30 tokens at most");
     const int64_t tiles = packed ? T / kWinTile + N : N * ((T + kWinTile - 1) / kWinTile);
-    if (hq > 65535) return fail(KDA_ERR_UNSUPPORTED, "65535 query heads at most (got %d)", hq);
+    if (hq > 1024) return fail(KDA_ERR_UNSUPPORTED, "1024 query heads at most (got %d)", hq);
     if (!fits(tiles, 4, hq) || !fits(N, hq))
         return fail(KDA_ERR_UNSUPPORTED, "the 64-token blocks of all sequences times H_q must fit in int32");
     return KDA_OK;

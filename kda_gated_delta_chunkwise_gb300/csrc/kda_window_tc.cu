@@ -558,6 +558,15 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
                 tile(sm, &mk, B::B_KF, x.hk, x.start + x.j0);
                 tile(sm + B::TILE, &mv, B::B_KF, x.hk, x.start + x.j0);
+                if (it + gridDim.x < p.items) {  // the next item's, into L2
+                    const DkvItem y(geo, it + gridDim.x, p.fars);
+                    if (y.steps > 0)
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_prefetch_3d(&mk, 64 * c, y.hk, y.start + y.j0);
+                            tma_prefetch_3d(&mv, 64 * c, y.hk, y.start + y.j0);
+                        }
+                }
             }
             __syncwarp();
             DkvStep st(geo, x);
@@ -881,6 +890,15 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                 for (int c = 0; c < D / 64; ++c) {
                     tma_load_3d(sm + c * B::ATOM, &mq, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
                     tma_load_3d(sm + B::TILE + c * B::ATOM, &mo, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
+                }
+                if (it + gridDim.x < p.items) {  // the next item's, into L2
+                    const Item y(geo, it + gridDim.x);
+                    if (y.steps > 0)
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_prefetch_3d(&mq, 64 * c, y.h, y.start + y.i0);
+                            tma_prefetch_3d(&mo, 64 * c, y.h, y.start + y.i0);
+                        }
                 }
             }
             __syncwarp();
