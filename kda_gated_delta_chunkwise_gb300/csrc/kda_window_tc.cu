@@ -73,6 +73,37 @@ template <int D> __device__ __forceinline__ void zero_rows(unsigned char *tile, 
     __syncwarp();
 }
 
+// Stores 64 bf16 (32 words) of each of a warp's 32 rows, lane l's being those of row l.
+// A lane that stored its own row would touch a line of its own with every store
+// (4000 cycles for a tile of 128 x 128); four lanes exchange their 32-byte pieces
+// first, so that they store 128 bytes of one row at a time. Rows from `rows` on are
+// left out.
+__device__ __forceinline__ void store_rows(__nv_bfloat16 *first, int64_t stride, int rows, uint32_t (&w)[4][8]) {
+    const int lane = threadIdx.x & 31;
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int a = 0; a < 4; a += 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[a][e] : w[a + 1][e], 1);
+            if (odd) w[a][e] = got;
+            else w[a + 1][e] = got;
+        }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[a][e] : w[a + 2][e], 2);
+            if (high) w[a][e] = got;
+            else w[a + 2][e] = got;
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane & ~3) + i;
+        if (row < rows) st_v8(first + row * stride + 16 * (lane & 3), w[i]);
+    }
+}
+
 // ================================================================ forward
 // An item is 256 queries of one head, two contexts w of 128 rows. A context goes
 // through its keys 64 at a time (first, where there are far pairs, the sinks alone,
@@ -410,18 +441,20 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
             const bool there = i < x.len;
             const int64_t at = (int64_t)(x.start + i) * geo.hq + x.h;
             const F2 ff = f2(f, f);
+            const int r0 = y.i0 + (warp & 3) * 32;  // the warp's first row
+            __nv_bfloat16 *dst = p.o + ((int64_t)(x.start + r0) * geo.hq + x.h) * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
+            for (int c = 0; c < D; c += 64) {
+                uint32_t o[2][32], r[4][8];
+                tmem_ld32(to + c, o[0]);
+                tmem_ld32(to + c + 32, o[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t r[8];
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = pack2(pair_w(o[16 * u + 2 * e], o[16 * u + 2 * e + 1]) * ff);
-                    if (there) st_v8(p.o + at * D + c + 16 * u, r);
-                }
+                    for (int e = 0; e < 8; ++e)
+                        r[u][e] = pack2(pair_w(o[u >> 1][16 * (u & 1) + 2 * e], o[u >> 1][16 * (u & 1) + 2 * e + 1]) * ff);
+                store_rows(dst + c, (int64_t)geo.hq * D, x.len - r0, r);
             }
             tc_fence_before();
             warp_arrive(bar + F::B_OE + w);
@@ -442,30 +475,32 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
 // An item is 128 keys of one key head; a step is 128 queries of one of its query
 // heads. Transposed scores, so that keys are the rows:
 //   S^T = K Q^T,  dP^T = V dO^T                      (TMEM)
-//   P^T = 2^{c S^T - lse}, over S^T;  dS^T = P^T (dP^T - D), over dP^T   (bf16)
+//   P^T = 2^{c S^T - lse}, to shared memory;  dS^T = P^T (dP^T - D), over dP^T   (bf16)
 //   dV += P^T dO,  dK += dS^T Q                      (TMEM, all steps of the item)
 // so each tile of Q and dO serves as an operand both ways round and nothing is
-// transposed in memory. One warp issues dV(n), S(n+1), another dK(n), dP(n+1): the
-// tensor core has two products to do while P is made and two while dS is.
+// transposed in memory. One warp issues S(n+1), as soon as S(n) is in registers, and
+// dV(n), another dK(n) and dP(n+1): S of a step is there when dS of the one before
+// is made (with P^T over S^T it had to wait for dV, and a step took 2800 cycles of
+// which P and dS are 1850 and the four products 2060).
 // Queries behind the sequence's end count as zeros with an infinite lse.
 // The far pairs are items of their own: the sinks against kWinFarQueries queries,
 // whose sums are parts that win_far_sum_kernel adds up.
 //
 // warp 0: TMA; 1: MMA of S and dV; 2: of dP and dK; 3: lse and D of the queries;
-// 4-11: P and dS, two threads a key, 64 queries each (the halves of a bf16 row lie
-// in the front of their 64 columns, so that no thread writes over scores that
-// another one reads).
+// 4-11: P and dS, two threads a key, 64 queries each (the halves of a bf16 row of dS
+// lie in the front of their 64 columns, so that no thread writes over what another
+// one reads).
 constexpr int BW_THREADS = 384;
 template <int D> struct Bw {
     static constexpr int TILE = 128 * D * 2, ATOM = 128 * 128;
-    static constexpr int QS = 3, OS = 2;                  // stages: of the operand of two steps, of one
+    static constexpr int QS = 2, OS = 2;                  // stages of Q and dO
     static constexpr int RING_Q = 2 * TILE, RING_O = RING_Q + QS * TILE;
-    static constexpr int VEC = RING_O + OS * TILE;        // 128 of lse, 128 of D
-    static constexpr int BAR = VEC + 1024;
-    static constexpr int B_KF = 0, B_KE = 1, B_SF = 2, B_PR = 3, B_DF = 4, B_DR = 5, B_AF = 6, B_AE = 7, B_QF = 8,
-                         B_QE = B_QF + QS, B_OF = B_QE + QS, B_OE = B_OF + OS, B_LF = B_OE + OS, B_XF = B_LF + 1,
-                         B_LE = B_LF + 2, B_XE = B_LF + 3, COUNT = B_LF + 4,
-                         B_DL = B_LE, B_DR1 = B_XE;  // in dq's kernel, which has no vectors
+    static constexpr int P = RING_O + OS * TILE;          // P^T, 128 keys of 128 queries
+    static constexpr int VEC = P + 2 * ATOM;              // 128 of lse, of two steps, and 128 of D
+    static constexpr int BAR = VEC + 1536;
+    static constexpr int B_KF = 0, B_KE = 1, B_SF = 2, B_SL = 3, B_PR = 4, B_PE = 5, B_DF = 6, B_DR = 7, B_AF = 8, B_AE = 9,
+                         B_QF = 10, B_QE = B_QF + QS, B_OF = B_QE + QS, B_OE = B_OF + OS, B_LF = B_OE + OS,
+                         B_XF = B_LF + 2, B_LE = B_LF + 3, B_XE = B_LF + 5, COUNT = B_LF + 6;  // LF, LE: of two buffers
     static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory of a block");
 };
@@ -526,7 +561,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
     if (tid == 0) {
         *ab.flag = 0;
         for (int i = 0; i < B::COUNT; ++i)
-            mbar_init(bar + i, i == B::B_PR || i == B::B_DR || i == B::B_AE || i >= B::B_LE               ? 8
+            mbar_init(bar + i, i == B::B_SL || i == B::B_PR || i == B::B_DR || i == B::B_AE || i >= B::B_LE ? 8
                                : i == B::B_KE || i == B::B_AF || (i >= B::B_OE && i < B::B_OE + B::OS) ? 2
                                                                                                        : 1);
         fence_mbar_init();
@@ -587,68 +622,80 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
             }
         }
     } else if (warp < 3) {
-        // Two products of a step each: `a` over the item's own tile, of the step ahead, and the sum over the steps.
-        // first: S and dV; second: dP and dK. Both see every phase of both rings.
+        // first: S, a step ahead, and dV; second: dK, and dP a step ahead
         const int w = uni(warp - 1);
         const uint32_t e = elected(), base = uni(tmem), sb = uni(smem_u32(sm)), bb = uni(bars);
         constexpr uint32_t I_S = idesc_bf16(128, 128, false, false), I_G = idesc_bf16(128, D, false, true);
         const uint32_t t_p = base + 128 * w, t_g = base + 256 + 128 * w;
-        const uint64_t ad = desc_k(sb + w * B::TILE);
-        const uint64_t qk = desc_k(sb + B::RING_Q), qm = desc_mn(sb + B::RING_Q, B::ATOM);
-        const uint64_t ok_ = desc_k(sb + B::RING_O), om = desc_mn(sb + B::RING_O, B::ATOM);
+        const uint64_t ad = desc_k(sb + w * B::TILE), pd = desc_k(sb + B::P);
+        const uint64_t rk = desc_k(sb + (w ? B::RING_O : B::RING_Q)), rm = desc_mn(sb + (w ? B::RING_Q : B::RING_O), B::ATOM);
         auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
-        int k = 0, n = 0;
-        int qs = 0, qr = 0, os = 0, orr = 0;  // the stages and phases of step n's Q and dO
-        auto product = [&](int s) {       // of the tile in stage s of its ring
-            const uint64_t b = (w ? ok_ : qk) + ((s * B::TILE) >> 4);
+        // Two stages a ring, step n's in n & 1. Rows behind the sequence's end may hold anything.
+        auto arrived = [&](int full, int ring, int n, int rows) {
+            if (!(ok = on(full + (n & 1), n >> 1))) return;
+            if (rows < 128) zero_rows<D>(sm + ring + (n & 1) * B::TILE, rows, 128);
+            tc_fence_after();
+        };
+        auto product = [&](int n) {
+            const uint64_t b = rk + (((n & 1) * B::TILE) >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
                 mma_ss_if(e, t_p, ad + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), I_S, ks > 0);
             commit_if(e, bb + 8 * (w ? B::B_DF : B::B_SF));
+            if (w) commit_if(e, bb + 8 * (B::B_OE + (n & 1)));
         };
-        // Q and dO of a step have arrived; rows behind the sequence's end may hold anything
-        auto arrived = [&](int rows) {
-            if (!(ok = on(B::B_QF + qs, qr) && on(B::B_OF + os, orr))) return;
-            if (rows < 128) {
-                zero_rows<D>(sm + B::RING_Q + qs * B::TILE, rows, 128);
-                zero_rows<D>(sm + B::RING_O + os * B::TILE, rows, 128);
-            }
-            tc_fence_after();
-        };
+        int k = 0, n = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const DkvItem x(geo, it, p.fars);
-            const int steps = uni(x.steps), len = uni(x.len), q0 = uni(x.q0), nq = uni(x.nq);
+            const int steps = uni(x.steps), nq = uni(x.nq), rows0 = uni(x.len - x.q0 * 128);
             if (steps == 0) continue;
             if (!(ok = on(B::B_KF, k))) break;
-            int qt = 0;
-            arrived(len - q0 * 128);
+            int qt = 0;  // of the step ahead
+            auto ahead = [&](int n) {
+                arrived(w ? B::B_OF : B::B_QF, w ? B::RING_O : B::RING_Q, n, rows0 - 128 * qt);
+                // the step's lse, or D, is there before its product is, for those who wait for that
+                if (ok && (ok = w ? on(B::B_XF, n) : on(B::B_LF + (n & 1), n >> 1))) product(n);
+            };
+            ahead(n);
             if (!ok) break;
-            product(w ? os : qs);
-            if (w) commit_if(e, bb + 8 * (B::B_OE + os));
             if (steps == 1) commit_if(e, bb + 8 * B::B_KE);
             for (int j = 0; j < steps; ++j, ++n) {
-                const int qs0 = qs, os0 = os;
-                if (++qs == B::QS) qs = 0, qr ^= 1;
-                if (++os == B::OS) os = 0, orr ^= 1;
+                const int rows = rows0 - 128 * qt;
                 if (++qt == nq) qt = 0;
-                if (!(ok = on(w ? B::B_DR : B::B_PR, n))) break;
+                const bool more = j + 1 < steps;
+                if (w == 0) {
+                    if (more) {
+                        if (!(ok = on(B::B_SL, n))) break;
+                        ahead(n + 1);
+                        if (!ok) break;
+                        if (j + 2 == steps) commit_if(e, bb + 8 * B::B_KE);
+                    }
+                    arrived(B::B_OF, B::RING_O, n, rows);
+                    if (!ok || !(ok = on(B::B_PR, n))) break;
+                } else {
+                    if (!(ok = on(B::B_QF + (n & 1), n >> 1) && on(B::B_DR, n))) break;
+                }
                 if (j == 0 && !(ok = on(B::B_AE, k + 1))) break;
                 tc_fence_after();
-                const uint64_t b = w ? qm + ((qs0 * B::TILE) >> 4) : om + ((os0 * B::TILE) >> 4);
+                const uint64_t b = rm + (((n & 1) * B::TILE) >> 4);
+                if (w == 0) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ts_if(e, t_g, t_p + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G, j > 0 || ks > 0);
-                // Q has been used by S long before dK, dO by both
-                commit_if(e, bb + 8 * (w ? B::B_QE + qs0 : B::B_OE + os0));
-                if (j + 1 < steps) {
-                    arrived(len - (q0 + qt) * 128);
-                    if (!ok) break;
-                    product(w ? os : qs);
-                    if (w) commit_if(e, bb + 8 * (B::B_OE + os));
-                    if (j + 2 == steps) commit_if(e, bb + 8 * B::B_KE);
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss_if(e, t_g, pd + step_k(ks, B::ATOM), b + step_mn(ks), I_G, j > 0 || ks > 0);
+                    commit_if(e, bb + 8 * B::B_PE);
+                    commit_if(e, bb + 8 * (B::B_OE + (n & 1)));
                 } else {
-                    commit_if(e, bb + 8 * B::B_AF);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts_if(e, t_g, t_p + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G, j > 0 || ks > 0);
+                    commit_if(e, bb + 8 * (B::B_QE + (n & 1)));  // S has used Q long before
+                    if (more) {
+                        ahead(n + 1);
+                        if (!ok) break;
+                        if (j + 2 == steps) commit_if(e, bb + 8 * B::B_KE);
+                    }
                 }
+                if (!more) commit_if(e, bb + 8 * B::B_AF);
             }
             ++k;
         }
@@ -676,11 +723,11 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 const float4 lv = make_float4(-l[0], -l[1], -l[2], -l[3]), dv = make_float4(-d[0], -d[1], -d[2], -d[3]);
                 st.next(x);
                 if (j + 1 < x.steps) load(x, st);
-                if (!(ok = wait(B::B_LE, n + 1))) break;
-                reinterpret_cast<float4 *>(vec)[lane] = lv;
-                warp_arrive(bar + B::B_LF);
+                if (!(ok = wait(B::B_LE + (n & 1), (n >> 1) + 1))) break;
+                reinterpret_cast<float4 *>(vec)[32 * (n & 1) + lane] = lv;
+                warp_arrive(bar + B::B_LF + (n & 1));
                 if (!(ok = wait(B::B_XE, n + 1))) break;
-                reinterpret_cast<float4 *>(vec + 128)[lane] = dv;
+                reinterpret_cast<float4 *>(vec + 256)[lane] = dv;
                 warp_arrive(bar + B::B_XF);
             }
         }
@@ -688,6 +735,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
         const int half = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21, ts = t_s + lanes + 64 * half, td = t_dp + lanes + 64 * half;
         const float *vec = reinterpret_cast<const float *>(sm + B::VEC) + 64 * half;
+        unsigned char *pt = sm + B::P + half * B::ATOM + (row >> 3) * 1024 + (row & 7) * 128;  // see kmajor_chunk
         const F2 c2 = f2(p.c2, p.c2);
         int n = 0, k = 0;
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
@@ -700,15 +748,17 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 const int i0 = st.qt * 128;
                 const int d0 = j - i0 - 64 * half;  // the half's column of the key's own token
                 float pr[64];
-                if (!(ok = wait(B::B_LF, n) && wait(B::B_SF, n))) break;
+                if (!(ok = wait(B::B_SF, n))) break;  // and lse
                 tc_fence_after();
                 uint32_t v[2][32];
                 tmem_ld32(ts, v[0]);
                 tmem_ld32(ts + 32, v[1]);
                 tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive(bar + B::B_SL);
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
-                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(vec + c);
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(vec + 128 * (n & 1) + c);
                     const uint32_t *y = v[c >> 5] + (c & 31);
                     float a, b;
                     f2_get(fma2(pair_w(y[0], y[1]), c2, F2{l.x}), a, b);
@@ -728,24 +778,25 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pr[c] = c > hi ? 0.f : pr[c];
                 }
+                if (!(ok = wait(B::B_PE, n + 1))) break;  // dV of the step before has read P
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = pack2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
-                    tmem_st16(ts + 16 * c, o);
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4 *>(pt + ((c ^ (row & 7)) << 4)) =
+                        make_uint4(pack2(pr[8 * c], pr[8 * c + 1]), pack2(pr[8 * c + 2], pr[8 * c + 3]),
+                                   pack2(pr[8 * c + 4], pr[8 * c + 5]), pack2(pr[8 * c + 6], pr[8 * c + 7]));
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {  // LE first: no warp then comes to LE of the next step before all have come to this one's
+                    mbar_arrive(bar + B::B_LE + (n & 1));
+                    mbar_arrive(bar + B::B_PR);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(bar + B::B_PR);
-                warp_arrive(bar + B::B_LE);
                 // a token that sees itself alone has no ds
                 if (i0 == 0 && half == 0) pr[0] = 0.f;
                 if (geo.window == 1 && geo.sinks == 0) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e) pr[e] = 0.f;
                 }
-                if (!(ok = wait(B::B_XF, n) && wait(B::B_DF, n))) break;
+                if (!(ok = wait(B::B_DF, n))) break;  // and D
                 tc_fence_after();
                 tmem_ld32(td, v[0]);
                 tmem_ld32(td + 32, v[1]);
@@ -755,7 +806,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(vec + 128 + 32 * c + e);
+                        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(vec + 256 + 32 * c + e);
                         const float *w = pr + 32 * c + e;
                         o[e / 2] = pack2((pair_w(v[c][e], v[c][e + 1]) + F2{d.x}) * f2(w[0], w[1]));
                         o[e / 2 + 1] = pack2((pair_w(v[c][e + 2], v[c][e + 3]) + F2{d.y}) * f2(w[2], w[3]));
@@ -764,8 +815,11 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar + B::B_DR);
-                warp_arrive(bar + B::B_XE);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar + B::B_XE);
+                    mbar_arrive(bar + B::B_DR);
+                }
             }
             if (!ok) break;
             if (!(ok = wait(B::B_AF, k++))) break;
@@ -775,31 +829,27 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
                        sink = x.far || (j < geo.sinks && x.len > geo.window);
             const uint32_t src = (half ? t_dk : t_dv) + lanes;
             const float f = half ? p.scale : 1.f;
-            __nv_bfloat16 *dst = (half ? p.dk : p.dv) + ((int64_t)(x.start + j) * geo.hk + x.hk) * D;
+            __nv_bfloat16 *dst = (half ? p.dk : p.dv) + ((int64_t)(x.start + x.j0 + (warp & 3) * 32) * geo.hk + x.hk) * D;
             float *sum = (x.far ? p.part : p.near) +
                          (((int64_t)(x.far ? x.slot : x.seq) * geo.hk + x.hk) * 2 * geo.sinks + (half ? 0 : geo.sinks) + j) * D;
             const F2 ff = f2(f, f);
+            const int r0 = x.j0 + (warp & 3) * 32;  // the warp's first row
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(src + c, v);
+            for (int c = 0; c < D; c += 64) {
+                uint32_t v[2][32], r[4][8];
+                tmem_ld32(src + c, v[0]);
+                tmem_ld32(src + c + 32, v[1]);
                 tmem_wait_ld();
-                if (!there) continue;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    F2 g[8];
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]) * ff;
-                    if (sink) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) *reinterpret_cast<unsigned long long *>(sum + c + 16 * q + 2 * e) = g[e].v;
-                    } else {
-                        uint32_t r[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) r[e] = pack2(g[e]);
-                        st_v8(dst + c + 16 * q, r);
+                    for (int e = 0; e < 8; ++e) {
+                        const F2 g = pair_w(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]) * ff;
+                        if (sink && there) *reinterpret_cast<unsigned long long *>(sum + c + 16 * u + 2 * e) = g.v;
+                        r[u][e] = pack2(g);
                     }
-                }
+                // a sink's row is written here too, and again when its sums are added up
+                if (!x.far) store_rows(dst + c, (int64_t)geo.hk * D, x.len - r0, r);
             }
             tc_fence_before();
             warp_arrive(bar + B::B_AE);
@@ -824,12 +874,23 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 // dP of the one behind. K is kept for two steps (S and dQ), V for one.
 //
 // warp 0: TMA; 1: MMA of S and dQ; 2: of dP; 4-11: dS, two threads a query, 64 keys each.
+template <int D> struct Bq {
+    static constexpr int TILE = 128 * D * 2, ATOM = 128 * 128;
+    static constexpr int KS = 3, VS = 2;                  // stages of K and V
+    static constexpr int RING_K = 2 * TILE, RING_V = RING_K + KS * TILE, BAR = RING_V + VS * TILE;
+    // QF, QE: the item's Q and dO; SF: of two buffers; DF, DL: dP there, in registers; DR: of two buffers
+    static constexpr int B_QF = 0, B_QE = 1, B_SF = 2, B_DF = 4, B_DL = 5, B_DR = 6, B_AF = 8, B_AE = 9, B_KF = 10,
+                         B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS, COUNT = B_VE + VS;
+    static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+};
+
 template <int D>
 __global__ void __launch_bounds__(BW_THREADS, 1)
 win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
                  const __grid_constant__ CUtensorMap mk16, const __grid_constant__ CUtensorMap mv16) {
-    using B = Bw<D>;  // the rings of K (Q's place) and V (dO's); the items' Q and dO in front
+    using B = Bq<D>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + B::BAR);
@@ -837,10 +898,9 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WinGeom &geo = p.geo;
-    // KF, KE: the items' Q and dO; SF: of the two scores (SF, PR); DF, DR; AF, AE: dQ
     if (tid == 0) {
         *ab.flag = 0;
-        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, i == B::B_DR || i == B::B_DR1 || i == B::B_AE || i == B::B_DL ? 8 : i == B::B_KE ? 2 : 1);
+        for (int i = 0; i < B::COUNT; ++i) mbar_init(bar + i, (i >= B::B_DL && i < B::B_AF) || i == B::B_AE ? 8 : i == B::B_QE ? 2 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -854,7 +914,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     bool ok = true;
     // A warp may be through with dS of a step before another is with the step before: dP of it waits for
     // nobody's dS. So there are two barriers of dS, in turn.
-    auto made = [](int n) { return n & 1 ? B::B_DR1 : B::B_DR; };
+    auto made = [](int n) { return B::B_DR + (n & 1); };
     struct Item {
         int start, len, i0, h, hk, far, kw, kt0, steps;
         __device__ __forceinline__ Item(const WinGeom &g, int it) {
@@ -882,14 +942,14 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const Item x(geo, it);
             if (x.steps == 0) continue;
-            if (!(ok = wait(B::B_KE, k + 1))) break;
+            if (!(ok = wait(B::B_QE, k + 1))) break;
             ++k;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar + B::B_KF, 2 * B::TILE);
+                mbar_arrive_expect_tx(bar + B::B_QF, 2 * B::TILE);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    tma_load_3d(sm + c * B::ATOM, &mq, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
-                    tma_load_3d(sm + B::TILE + c * B::ATOM, &mo, bar + B::B_KF, 64 * c, x.h, x.start + x.i0);
+                    tma_load_3d(sm + c * B::ATOM, &mq, bar + B::B_QF, 64 * c, x.h, x.start + x.i0);
+                    tma_load_3d(sm + B::TILE + c * B::ATOM, &mo, bar + B::B_QF, 64 * c, x.h, x.start + x.i0);
                 }
                 if (it + gridDim.x < p.items) {  // the next item's, into L2
                     const Item y(geo, it + gridDim.x);
@@ -917,11 +977,11 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                 __syncwarp();
             };
             for (int j = 0; j < x.steps; ++j, ++n) {
-                const int ks = n % B::QS, vs = n % B::OS;
-                if (!(ok = wait(B::B_QE + ks, n / B::QS + 1))) break;
-                keys(&mk, &mk16, sm + B::RING_Q + ks * B::TILE, B::B_QF + ks, j);
-                if (!(ok = wait(B::B_OE + vs, n / B::OS + 1))) break;
-                keys(&mv, &mv16, sm + B::RING_O + vs * B::TILE, B::B_OF + vs, j);
+                const int ks = n % B::KS, vs = n % B::VS;
+                if (!(ok = wait(B::B_KE + ks, n / B::KS + 1))) break;
+                keys(&mk, &mk16, sm + B::RING_K + ks * B::TILE, B::B_KF + ks, j);
+                if (!(ok = wait(B::B_VE + vs, n / B::VS + 1))) break;
+                keys(&mv, &mv16, sm + B::RING_V + vs * B::TILE, B::B_VF + vs, j);
             }
         }
     } else if (warp < 3) {
@@ -929,8 +989,8 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
         const int w = uni(warp - 1);
         const uint32_t e = elected(), base = uni(tmem), sb = uni(smem_u32(sm)), bb = uni(bars);
         constexpr uint32_t I_G = idesc_bf16(128, D, false, true), I_S = idesc_bf16(128, 128, false, false);
-        const uint64_t ad = desc_k(sb + w * B::TILE), kd = desc_k(sb + (w ? B::RING_O : B::RING_Q)),
-                       km = desc_mn(sb + B::RING_Q, B::ATOM);
+        const uint64_t ad = desc_k(sb + w * B::TILE), kd = desc_k(sb + (w ? B::RING_V : B::RING_K)),
+                       km = desc_mn(sb + B::RING_K, B::ATOM);
         auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
         int n = 0, k = 0, s = 0, round = 0;  // s: the stage of step n + 1's K, or V
         auto product = [&](uint32_t d, uint32_t idesc, int full) {
@@ -945,17 +1005,17 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
             const Item x(geo, it);
             const int steps = uni(x.steps), far = uni(x.far), kw = uni(x.kw), len = uni(x.len), behind = len - uni(x.kt0) * 128;
             if (steps == 0) continue;
-            if (!(ok = on(B::B_KF, k))) break;
+            if (!(ok = on(B::B_QF, k))) break;
             const uint32_t i0 = far ? idesc_bf16(128, kw, false, false) : I_S;  // of the first step
             if (w == 0) {
                 // keys behind the sequence's end are masked, but their rows of K meet the zeros of dS
                 auto scores = [&](int j) {
-                    if (!(ok = on(B::B_QF + s, round))) return;
+                    if (!(ok = on(B::B_KF + s, round))) return;
                     const int rows = j < far ? len : behind - 128 * (j - far), keys = j < far ? kw : 128;
-                    if (rows < keys) zero_rows<D>(sm + B::RING_Q + s * B::TILE, rows, keys);
+                    if (rows < keys) zero_rows<D>(sm + B::RING_K + s * B::TILE, rows, keys);
                     product(base + 128 * ((n + (j > 0)) & 1), j == 0 ? i0 : I_S, B::B_SF + ((n + (j > 0)) & 1));
-                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_KE);  // Q has been used for the last time
-                    if (++s == B::QS) s = 0, round ^= 1;
+                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_QE);  // Q has been used for the last time
+                    if (++s == B::KS) s = 0, round ^= 1;
                 };
                 int sd = s;  // the stage of step n's K
                 scores(0);
@@ -974,18 +1034,18 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
                     for (int ks = 0; ks < 8; ++ks)
                         mma_ts_if(keys > 16 * ks ? e : 0u, base + 384, a + (ks >> 2) * 64 + (ks & 3) * 8, b + step_mn(ks), I_G,
                                   j > 0 || ks > 0);
-                    commit_if(e, bb + 8 * (B::B_QE + sd));
-                    if (++sd == B::QS) sd = 0;
+                    commit_if(e, bb + 8 * (B::B_KE + sd));
+                    if (++sd == B::KS) sd = 0;
                     if (j + 1 == steps) commit_if(e, bb + 8 * B::B_AF);
                 }
             } else {
                 for (int j = 0; j < steps; ++j, ++n) {
-                    if (!(ok = on(B::B_OF + s, round))) break;
+                    if (!(ok = on(B::B_VF + s, round))) break;
                     if (n > 0 && !(ok = on(B::B_DL, n - 1))) break;  // dP of the step before is in registers
                     product(base + 256, j == 0 ? i0 : I_S, B::B_DF);
-                    commit_if(e, bb + 8 * (B::B_OE + s));
-                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_KE);
-                    if (++s == B::OS) s = 0, round ^= 1;
+                    commit_if(e, bb + 8 * (B::B_VE + s));
+                    if (j + 1 == steps) commit_if(e, bb + 8 * B::B_QE);
+                    if (++s == B::VS) s = 0, round ^= 1;
                 }
             }
             ++k;
@@ -1055,20 +1115,19 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
             if (!ok) break;
             if (!(ok = wait(B::B_AF, k++))) break;
             tc_fence_after();
-            __nv_bfloat16 *dst = p.dq + ((int64_t)(x.start + i) * geo.hq + x.h) * D;
             const F2 sc = f2(p.scale, p.scale);
-#pragma unroll 1
-            for (int c = D / 2 * half; c < D / 2 * (half + 1); c += 32) {
-                uint32_t v[32];
-                tmem_ld32(t_dq + lanes + c, v);
+            const int r0 = x.i0 + (warp & 3) * 32;  // the warp's first row
+            if (D == 128 || half == 0) {  // 64 channels
+                uint32_t v[2][32], r[4][8];
+                tmem_ld32(t_dq + lanes + 64 * half, v[0]);
+                tmem_ld32(t_dq + lanes + 64 * half + 32, v[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t r[8];
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = pack2(pair_w(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]) * sc);
-                    if (there) st_v8(dst + c + 16 * q, r);
-                }
+                    for (int e = 0; e < 8; ++e)
+                        r[u][e] = pack2(pair_w(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]) * sc);
+                store_rows(p.dq + ((int64_t)(x.start + r0) * geo.hq + x.h) * D + 64 * half, (int64_t)geo.hq * D, x.len - r0, r);
             }
             tc_fence_before();
             warp_arrive(bar + B::B_AE);
@@ -1127,7 +1186,7 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed[2];
     cudaError_t e = allow_smem(win_dkv_tc_kernel<D>, Bw<D>::SMEM, allowed[0]);
-    if (e == cudaSuccess) e = allow_smem(win_dq_tc_kernel<D>, Bw<D>::SMEM, allowed[1]);
+    if (e == cudaSuccess) e = allow_smem(win_dq_tc_kernel<D>, Bq<D>::SMEM, allowed[1]);
     if (e != cudaSuccess) return e;
     const int fars = geo.sinks > 0 && geo.window < geo.T ? geo.ntiles * geo.hk : 0;
     BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, part, near,
@@ -1137,7 +1196,7 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     p.items = geo.ntiles * 2 * geo.hq;
-    win_dq_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, s>>>(p, mq, mk, mv, mo, mk16, mv16);
+    win_dq_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bq<D>::SMEM, s>>>(p, mq, mk, mv, mo, mk16, mv16);
     return cudaGetLastError();
 }
 
