@@ -7,17 +7,19 @@
 // mind their order, so a step is an attention over a stretch of memory.
 //
 // The step is bound by memory: every entry of a key head is read once for all
-// its query heads. One warp takes 16 entries (fp32: 8) at a time straight from
-// global memory into the fragments of mma.sync, 16 query heads (or what there
-// are) as the rows of the product: a contraction does not mind the order of its
-// index, so a lane reads 16 bytes of consecutive channels and the query's
-// fragments are read the same way; for the values' product a lane holds the
-// entries and channels that its fragments want, two entries' halves joined by a
-// byte permutation. Nothing goes through shared memory until the warps' sums are
-// joined. Few sequences are cut over the CTAs of a cluster, whose sums are joined
+// its query heads. One warp takes 16 entries (fp32: 8) at a time, 8 KB of keys and
+// values, from a ring of its own that cp.async fills two steps ahead (128 KB in
+// flight on an SM; straight into registers, a step's values were waited for in
+// every step: 451 us for 256 sequences of 32 heads, 8 key heads and 2052 entries).
+// They go into the fragments of mma.sync, 16 query heads (or what there are) as the
+// rows of the product: a contraction does not mind the order of its index, so a
+// lane reads 16 bytes of consecutive channels and the query's fragments are read
+// the same way; for the values' product a lane holds the entries and channels that
+// its fragments want, two entries' halves joined by a byte permutation. Few sequences are cut over the CTAs of a cluster, whose sums are joined
 // through distributed shared memory in rank order.
 #include <math_constants.h>
 
+#include "kda_rows.cuh"
 #include "kda_tc_ptx.cuh"
 #include "kda_window.cuh"
 
@@ -113,6 +115,11 @@ template <typename T, int D> struct Shape {
     static constexpr int VR = sizeof(T) == 2 ? 4 : 2;     // value rows of a lane
     // the value row u of lane t within the step
     static __device__ __forceinline__ int v_row(int t, int u) { return 2 * t + (u & 1) + (u >> 1) * 8; }
+    // The ring: a stage is the step's keys, then its values, entry by entry, 16-byte pieces exchanged so that the
+    // eight lanes that read at a time (two rows of keys, four of values) meet eight different banks of 16 bytes.
+    static constexpr int ROW = D * sizeof(T), STAGE = 2 * KEYS * ROW, STAGES = 3;
+    static __device__ __forceinline__ int k_at(int row, int piece) { return row * ROW + ((piece ^ ((row & 1) << 2)) << 4); }
+    static __device__ __forceinline__ int v_at(int row, int piece) { return (KEYS + row) * ROW + ((piece ^ (row & 7)) << 4); }
 };
 
 template <typename T, int D>
@@ -121,7 +128,7 @@ win_decode_kernel(WinCacheArgs p, int cl) {
     using S = Shape<T, D>;
     constexpr int CH = S::CH, KEYS = S::KEYS, NB = S::NB, KC = S::KC, VC = S::VC, VR = S::VR;
     extern __shared__ __align__(16) float sm[];
-    float *part = sm;                            // [DW][HEADS][D]: the warps' sums
+    float *part = sm;                            // [DW][HEADS][D]: the warps' sums, in the rings' place
     float *own = part + DW * HEADS * D;          // [HEADS][D]: the CTA's
     float *stat = own + HEADS * D;               // [DW][HEADS][2]: the warps' maximum and sum
     float *own_stat = stat + DW * HEADS * 2;     // [HEADS][2]
@@ -165,39 +172,42 @@ win_decode_kernel(WinCacheArgs p, int cl) {
         float acc[D / 8][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        auto row = [&](const T *cache, const T *fresh_row, int e) { return e == fill ? fresh_row : cache + e * step; };
-        uint4 kf[NB][KC], vf[VR][VC];
-        auto load_k = [&](int tile) {
+        unsigned char *ring = reinterpret_cast<unsigned char *>(sm) + warp * S::STAGES * S::STAGE;
+        const uint32_t ring_s = tc::smem_u32(ring);
+        auto fetch = [&](int tile, int stage) {  // one group of copies, empty past the last step
+            if (tile < tile1) {
+                constexpr int PIECES = D / CH;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int e = tile * KEYS + b * 8 + g;
-                const T *src = row(kc, knew, e) + CH * t;
-#pragma unroll
-                for (int j = 0; j < KC; ++j)
-                    kf[b][j] = e < count ? *reinterpret_cast<const uint4 *>(src + 4 * CH * j) : make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < KEYS * PIECES / 32; ++i) {
+                    const int r = (i * 32 + lane) / PIECES, piece = (i * 32 + lane) % PIECES, e = tile * KEYS + r;
+                    const bool there = e < count;
+                    const int64_t at = (there ? e : 0) * step + piece * CH;
+                    const uint32_t dst = ring_s + stage * S::STAGE;
+                    copy16(dst + S::k_at(r, piece), e == fill ? knew + piece * CH : kc + at, there);
+                    copy16(dst + S::v_at(r, piece), e == fill ? vnew + piece * CH : vc + at, there);
+                }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_v = [&](int tile) {
+        int tile = tile0 + warp, stage = 0;
 #pragma unroll
-            for (int u = 0; u < VR; ++u) {
-                const int e = tile * KEYS + S::v_row(t, u);
-                const T *src = row(vc, vnew, e) + CH * g;
-#pragma unroll
-                for (int i = 0; i < VC; ++i)
-                    vf[u][i] = e < count ? *reinterpret_cast<const uint4 *>(src + 8 * CH * i) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        int tile = tile0 + warp;
-        if (tile < tile1) load_k(tile);
+        for (int i = 0; i < S::STAGES - 1; ++i) fetch(tile + i * DW, i);
         for (; tile < tile1; tile += DW) {
-            load_v(tile);
+            __syncwarp();  // the stage that is filled now has been read by every lane
+            fetch(tile + (S::STAGES - 1) * DW, stage == 0 ? S::STAGES - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
+            __syncwarp();
+            const unsigned char *buf = ring + stage * S::STAGE;
+            stage = stage == S::STAGES - 1 ? 0 : stage + 1;
+            uint4 vf[VR][VC];
             float s[NB][4];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
 #pragma unroll
                 for (int j = 0; j < KC; ++j) {
-                    const uint4 x = qf[0][j], y = qf[1][j], k = kf[b][j];
+                    const uint4 x = qf[0][j], y = qf[1][j];
+                    const uint4 k = *reinterpret_cast<const uint4 *>(buf + S::k_at(b * 8 + g, 4 * j + t));
                     if constexpr (sizeof(T) == 2) {
                         mma_bf16(s[b], x.x, y.x, x.y, y.y, k.x, k.y);
                         mma_bf16(s[b], x.z, y.z, x.w, y.w, k.z, k.w);
@@ -212,7 +222,11 @@ win_decode_kernel(WinCacheArgs p, int cl) {
                     }
                 }
             }
-            if (tile + DW < tile1) load_k(tile + DW);
+#pragma unroll
+            for (int u = 0; u < VR; ++u)
+#pragma unroll
+                for (int i = 0; i < VC; ++i)
+                    vf[u][i] = *reinterpret_cast<const uint4 *>(buf + S::v_at(S::v_row(t, u), 8 * i + g));
             float top[2] = {m[0], m[1]};
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -281,6 +295,8 @@ win_decode_kernel(WinCacheArgs p, int cl) {
                 }
             }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the rings have been read
         // the warps' sums: lane (g, t) has, of rows g and g + 8, channels 8 CH i + CH (2 t + e) + b
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -349,7 +365,8 @@ win_decode_kernel(WinCacheArgs p, int cl) {
 }
 
 template <typename T, int D> cudaError_t decode(const WinCacheArgs &a, cudaStream_t s) {
-    constexpr size_t smem = (DW * HEADS * D + HEADS * D + DW * HEADS * 2 + HEADS * 2) * sizeof(float);
+    constexpr size_t sums = (DW * HEADS * D + HEADS * D + DW * HEADS * 2 + HEADS * 2) * sizeof(float);
+    constexpr size_t rings = DW * Shape<T, D>::STAGES * Shape<T, D>::STAGE, smem = sums > rings ? sums : rings;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(win_decode_kernel<T, D>, smem, allowed);
     if (e != cudaSuccess) return e;
