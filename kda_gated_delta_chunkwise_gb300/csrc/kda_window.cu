@@ -1,17 +1,18 @@
-// Attention with a sliding window and sinks, and its gradients, for any
-// supported type and size; the tile table of packed batches.
+// Attention with a sliding window and sinks, and its gradients, in fp32; what both
+// types share: the tile table of packed batches, D, the sinks' sums.
 //
 //   s_ij = scale q_i . k_j over the j that i sees,  lse_i = log sum_j e^{s_ij}
 //   p_ij = e^{s_ij - lse_i},  o_i = sum_j p_ij v_j
 //   D_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - D_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
-// with dk and dv summed over the query heads of a key head, in their order.
+// with dk and dv summed over the query heads of a key head, in their order. (bf16:
+// kda_window_tc.cu.)
 //
-// One CTA takes 64 rows (queries, or keys for dk and dv), a warp 16 of them, and
-// walks tiles of 32 columns in shared memory with the running maximum and sum of
-// the softmax in registers. The products run on mma.sync tf32; an fp32 operand is
-// split in two tf32 parts, three products for each. bf16 values are exact in tf32; the weights p and ds of a bf16
-// call keep 11 bits, against the 8 of its result.
+// One CTA takes 64 rows (queries, or keys for dk and dv) and walks tiles of 32
+// columns in shared memory with the running maximum and sum of the softmax in
+// registers. The products run on mma.sync tf32, every operand split in two tf32
+// parts, three products for each. Bound by instructions: 13 for a product of
+// 16 x 8 x 8.
 #include <math_constants.h>
 
 #include "kda_window.cuh"
@@ -85,97 +86,100 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// A fragment: four values, in one or two tf32 parts.
-template <bool SPLIT> struct Frag {
+// An fp32 value in two tf32 parts, 22 bits.
+__device__ __forceinline__ uint2 split(float x) {
+    const uint32_t hi = tf32(x);
+    return make_uint2(hi, tf32(x - __uint_as_float(hi)));
+}
+struct Frag {
     uint32_t hi[4], lo[4];
-    __device__ __forceinline__ void set(int i, float x) {
-        hi[i] = tf32(x);
-        if (SPLIT) lo[i] = tf32(x - __uint_as_float(hi[i]));
+    __device__ __forceinline__ void set(int i, uint2 x) { hi[i] = x.x, lo[i] = x.y; }
+};
+// d += the product of four values of a and two of b. The three products of a step
+// are summed from zero, the small ones first, and then added in fp32: the tensor
+// core truncates what it accumulates, fp32 sums round (carried on through four steps
+// a score was twice as far off).
+__device__ __forceinline__ void add_product(float (&d)[4], const Frag &a, uint2 b0, uint2 b1) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+    mma(z, a.lo, b0.x, b1.x);
+    mma(z, a.hi, b0.y, b1.y);
+    mma(z, a.hi, b0.x, b1.x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] += z[e];
+}
+
+// 16 warps: four groups of 16 rows times four groups of columns (eight of a tile's
+// 32, a quarter of d in the sums). Four warps of 16 rows and all columns were a
+// third as fast: one warp on a scheduler waits for its own products most of the time.
+constexpr int NT = 512, ROWS = 64, COLS = 32, WS = COLS + 4;  // WS: floats to a row of weights
+
+// Rows of a tile in shared memory, split once for all who read them, D + 4 pairs
+// apart. Rows past `rows` are zeros. In two steps, so that the next tile's loads
+// are on their way while this one is worked on.
+template <int D, int N> struct TileLoad {
+    static constexpr int PER = D / 4, COUNT = N * PER / NT;
+    static_assert(N * PER % NT == 0, "whole rounds");
+    float4 v[COUNT];
+    __device__ __forceinline__ void load(const float *src, int64_t stride, int rows) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int r = (i * NT + threadIdx.x) / PER, c = (i * NT + threadIdx.x) % PER * 4;
+            v[i] = r < rows ? *reinterpret_cast<const float4 *>(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void store(uint2 *dst) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int r = (i * NT + threadIdx.x) / PER, c = (i * NT + threadIdx.x) % PER * 4;
+            uint4 *d = reinterpret_cast<uint4 *>(dst + r * (D + 4) + c);
+            const uint2 x = split(v[i].x), y = split(v[i].y), z = split(v[i].z), w = split(v[i].w);
+            d[0] = make_uint4(x.x, x.y, y.x, y.y);
+            d[1] = make_uint4(z.x, z.y, w.x, w.y);
+        }
     }
 };
-// d += the product of four values of a and two of b. In two parts the three
-// products of a step are summed from zero, the small ones first, and then added in
-// fp32: the tensor core truncates what it accumulates, fp32 sums round (carried on
-// through four steps a score was twice as far off).
-template <bool SPLIT> __device__ __forceinline__ void add_product(float (&d)[4], const Frag<SPLIT> &a, float x0, float x1) {
-    const uint32_t h0 = tf32(x0), h1 = tf32(x1);
-    if constexpr (SPLIT) {
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(z, a.lo, h0, h1);
-        mma(z, a.hi, tf32(x0 - __uint_as_float(h0)), tf32(x1 - __uint_as_float(h1)));
-        mma(z, a.hi, h0, h1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] += z[e];
-    } else {
-        mma(d, a.hi, h0, h1);
-    }
-}
-
-constexpr int NT = 128, ROWS = 64, COLS = 32;
-
-// Rows of a tile in shared memory, fp32, D + 4 apart (a fragment's reads then
-// touch every bank once). Rows past `rows` are zeros.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t stride, int rows, int want) {
-    constexpr int N = 16 / sizeof(T), PER = D / N;
-    for (int i = threadIdx.x; i < want * PER; i += NT) {
-        const int r = i / PER, c = (i % PER) * N;
-        float x[N];
-        if (r < rows) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + r * stride + c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                x[e] = sizeof(T) == 4 ? __uint_as_float(w[e * 4 / N])
-                                      : __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4 *>(dst + r * (D + 4) + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    }
-}
-
-// acc[nb] = the 16 x 32 products of this warp's rows of `a` with the rows of `b`.
-template <bool SPLIT, int D>
-__device__ __forceinline__ void rows_by_rows(float (&acc)[COLS / 8][4], const float *a, const float *b) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
-#pragma unroll
-    for (int nb = 0; nb < COLS / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
-#pragma unroll 2
+struct Place {  // of a thread in the products
+    int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+    // its rows are r0 and r0 + 8; a group of rows has a warp on every scheduler, so that rows that are not there
+    // (few sinks) leave the others more of each
+    int r0 = (warp >> 2) * 16 + g, group = warp & 3;
+    __device__ __forceinline__ bool idle(int rows) const { return (warp >> 2) * 16 >= rows; }
+};
+// acc = the products of this warp's 16 rows of `a` with its eight of b.
+template <int D> __device__ __forceinline__ void rows_by_rows(float (&acc)[4], const Place &w, const uint2 *a, const uint2 *b) {
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    const uint2 *a0 = a + w.r0 * (D + 4) + w.t, *b0 = b + (w.group * 8 + w.g) * (D + 4) + w.t;
+#pragma unroll 4
     for (int k = 0; k < D; k += 8) {
-        Frag<SPLIT> f;
-        f.set(0, a[r0 * (D + 4) + k + t]);
-        f.set(1, a[(r0 + 8) * (D + 4) + k + t]);
-        f.set(2, a[r0 * (D + 4) + k + t + 4]);
-        f.set(3, a[(r0 + 8) * (D + 4) + k + t + 4]);
-#pragma unroll
-        for (int nb = 0; nb < COLS / 8; ++nb)
-            add_product<SPLIT>(acc[nb], f, b[(nb * 8 + g) * (D + 4) + k + t], b[(nb * 8 + g) * (D + 4) + k + t + 4]);
+        Frag f;
+        f.set(0, a0[k]);
+        f.set(1, a0[8 * (D + 4) + k]);
+        f.set(2, a0[k + 4]);
+        f.set(3, a0[8 * (D + 4) + k + 4]);
+        add_product(acc, f, b0[k], b0[k + 4]);
     }
 }
-// acc[nb] += w (16 x 32, as rows_by_rows leaves it) times the rows of b. Columns
-// 2 t and 2 t + 1 of w, which this lane holds, stand for k = t and t + 4 of the
-// product: a sum does not mind the order of its terms.
-template <bool SPLIT, int D>
-__device__ __forceinline__ void weights_by_rows(float (&acc)[D / 8][4], const float (&w)[COLS / 8][4], const float *b) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    Frag<SPLIT> f[COLS / 8];
+// acc[nb] += weights (this warp's 16 rows) times its quarter of the rows of b.
+// Columns 2 t and 2 t + 1 of the weights, which a lane reads at once, stand for k = t
+// and t + 4 of the product: a sum does not mind the order of its terms.
+template <int D> __device__ __forceinline__ void weights_by_rows(float (&acc)[D / 32][4], const Place &w, const Frag (&f)[COLS / 8], const uint2 *b) {
 #pragma unroll
     for (int kb = 0; kb < COLS / 8; ++kb) {
-        f[kb].set(0, w[kb][0]);
-        f[kb].set(1, w[kb][2]);
-        f[kb].set(2, w[kb][1]);
-        f[kb].set(3, w[kb][3]);
+        const uint2 *b0 = b + (kb * 8 + 2 * w.t) * (D + 4) + w.group * (D / 4) + w.g;
+#pragma unroll
+        for (int nb = 0; nb < D / 32; ++nb) add_product(acc[nb], f[kb], b0[nb * 8], b0[D + 4 + nb * 8]);
     }
+}
+__device__ __forceinline__ void put_weights(float *w, const Place &p, const float (&s)[4]) {
+    *reinterpret_cast<float2 *>(w + p.r0 * WS + p.group * 8 + 2 * p.t) = make_float2(s[0], s[1]);
+    *reinterpret_cast<float2 *>(w + (p.r0 + 8) * WS + p.group * 8 + 2 * p.t) = make_float2(s[2], s[3]);
+}
+__device__ __forceinline__ void get_weights(Frag (&f)[COLS / 8], const float *w, const Place &p) {
 #pragma unroll
-    for (int nb = 0; nb < D / 8; ++nb) {
-#pragma unroll
-        for (int kb = 0; kb < COLS / 8; ++kb)
-            add_product<SPLIT>(acc[nb], f[kb], b[(kb * 8 + 2 * t) * (D + 4) + nb * 8 + g],
-                               b[(kb * 8 + 2 * t + 1) * (D + 4) + nb * 8 + g]);
+    for (int kb = 0; kb < COLS / 8; ++kb) {
+        const float2 x = *reinterpret_cast<const float2 *>(w + p.r0 * WS + kb * 8 + 2 * p.t);
+        const float2 y = *reinterpret_cast<const float2 *>(w + (p.r0 + 8) * WS + kb * 8 + 2 * p.t);
+        f[kb].set(0, split(x.x)), f[kb].set(1, split(y.x)), f[kb].set(2, split(x.y)), f[kb].set(3, split(y.y));
     }
 }
 
@@ -189,14 +193,11 @@ struct WinParams {
     float *lse;               // [tokens][hq], of the forward
     float *lse2, *delta;      // [hq][tokens], of the gradients: lse (bf16: in powers of two), D
     float *part, *near;       // gradients of the sinks, see win_far_sum_kernel
+    int fars;                 // blocks of far pairs, which come first
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-// e^{scale s - lse}; of bf16 calls scale and lse come in powers of two (their
-// roundings, 2^-24 of a score, would be seen in an fp32 gradient)
-template <bool SPLIT> __device__ __forceinline__ float weight(float s, float scale, float lse) {
-    return SPLIT ? expf(fmaf(s, scale, -lse)) : exp2_approx(fmaf(s, scale, -lse));
-}
+
 // Whether i sees j, among the near pairs or among the far ones.
 __device__ __forceinline__ bool sees(int i, int j, int window, int sinks, bool far) {
     return far ? j < sinks && i - j >= window : j <= i && i - j < window;
@@ -204,65 +205,88 @@ __device__ __forceinline__ bool sees(int i, int j, int window, int sinks, bool f
 // Token i sees itself alone: its weight is one whatever its score, so ds is zero.
 __device__ __forceinline__ bool alone(int i, int window, int sinks) { return i == 0 || (window == 1 && sinks == 0); }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT)
 win_forward_kernel(WinParams p) {
-    constexpr bool SPLIT = sizeof(T) == 4;
-    extern __shared__ __align__(16) float sm[];
-    float *sq = sm, *sk = sq + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    extern __shared__ __align__(16) uint2 sm[];
+    uint2 *sq = sm, *sk = sq + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
     const WinGeom &geo = p.geo;
     const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
     const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
     if (rows <= 0) return;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
-    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
-    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
-    load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows, ROWS);
-    float acc[D / 8][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    const Place w;
+    const float *kb = (const float *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
+    const float *vb = (const float *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
+    {
+        TileLoad<D, ROWS> q;
+        q.load((const float *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows);
+        q.store(sq);
+    }
+    TileLoad<D, COLS> nk, nv;
+    float acc[D / 32][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int nb = 0; nb < D / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+    for (int nb = 0; nb < D / 32; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
     auto walk = [&](int from, int to, bool far) {
+        auto fetch = [&](int j0) {
+            nk.load(kb + (int64_t)j0 * p.k_stride, p.k_stride, to - j0);
+            nv.load(vb + (int64_t)j0 * p.v_stride, p.v_stride, to - j0);
+        };
+        if (from < to) fetch(from);
         for (int j0 = from; j0 < to; j0 += COLS) {
             __syncthreads();
-            const int cols = min(COLS, to - j0);
-            load_tile<T, D>(sk, kb + (int64_t)j0 * p.k_stride, p.k_stride, cols, COLS);
-            load_tile<T, D>(sv, vb + (int64_t)j0 * p.v_stride, p.v_stride, cols, COLS);
+            nk.store(sk);
+            nv.store(sv);
             __syncthreads();
-            float s[COLS / 8][4], top[2] = {m[0], m[1]};
-            rows_by_rows<SPLIT, D>(s, sq, sk);
-#pragma unroll
-            for (int nb = 0; nb < COLS / 8; ++nb) {
+            if (j0 + COLS < to) fetch(j0 + COLS);
+            if (!w.idle(rows)) {
+                float s[4];
+                rows_by_rows<D>(s, w, sq, sk);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
-                    s[nb][e] = j < to && sees(i, j, geo.window, geo.sinks, far) ? s[nb][e] * p.scale : -CUDART_INF_F;
-                    top[e >> 1] = fmaxf(top[e >> 1], s[nb][e]);
+                    const int i = i0 + w.r0 + (e >> 1) * 8, j = j0 + w.group * 8 + 2 * w.t + (e & 1);
+                    s[e] = j < to && sees(i, j, geo.window, geo.sinks, far) ? s[e] * p.scale : -CUDART_INF_F;
                 }
+                put_weights(ws, w, s);
             }
+            __syncthreads();
+            if (w.idle(rows)) continue;
+            // every warp of the same rows makes their weights and sums, the same ones
+            Frag f[COLS / 8];
+            float x[2][COLS / 4];
             float keep[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-                keep[e] = top[e] == -CUDART_INF_F ? 1.f : expf(m[e] - top[e]);  // a row may see nothing of a tile
-                m[e] = top[e];
-                l[e] *= keep[e];
-            }
+            for (int r = 0; r < 2; ++r) {
+                float top = m[r];
 #pragma unroll
-            for (int nb = 0; nb < COLS / 8; ++nb) {
+                for (int k = 0; k < COLS / 8; ++k) {
+                    const float2 y = *reinterpret_cast<const float2 *>(ws + (w.r0 + 8 * r) * WS + k * 8 + 2 * w.t);
+                    x[r][2 * k] = y.x, x[r][2 * k + 1] = y.y;
+                    top = fmaxf(top, fmaxf(y.x, y.y));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                keep[r] = top == -CUDART_INF_F ? 1.f : expf(m[r] - top);  // a row may see nothing of a tile
+                m[r] = top;
+                l[r] *= keep[r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[nb][e] = s[nb][e] == -CUDART_INF_F ? 0.f : expf(s[nb][e] - m[e >> 1]);
-                    l[e >> 1] += s[nb][e];
+                for (int k = 0; k < COLS / 4; ++k) {
+                    x[r][k] = x[r][k] == -CUDART_INF_F ? 0.f : expf(x[r][k] - top);
+                    l[r] += x[r][k];
                 }
             }
 #pragma unroll
-            for (int nb = 0; nb < D / 8; ++nb) {
+            for (int k = 0; k < COLS / 8; ++k) {
+                f[k].set(0, split(x[0][2 * k])), f[k].set(1, split(x[1][2 * k]));
+                f[k].set(2, split(x[0][2 * k + 1])), f[k].set(3, split(x[1][2 * k + 1]));
+            }
+#pragma unroll
+            for (int nb = 0; nb < D / 32; ++nb) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nb][e] *= keep[e >> 1];
             }
-            weights_by_rows<SPLIT, D>(acc, s, sv);
+            weights_by_rows<D>(acc, w, f, sv);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
@@ -271,21 +295,19 @@ win_forward_kernel(WinParams p) {
     for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        const int r = r0 + e * 8;
+        const int r = w.r0 + e * 8;
         if (r >= rows) continue;
         const int64_t row = (int64_t)(tile.start + i0 + r) * geo.hq + h;
-        T *o = (T *)p.o + row * D;
+        float *o = (float *)p.o + row * D + w.group * (D / 4) + 2 * w.t;
         const float f = 1.f / l[e];
 #pragma unroll
-        for (int nb = 0; nb < D / 8; ++nb) {
-            o[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * f);
-            o[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * f);
-        }
-        if (p.lse && t == 0) p.lse[row] = m[e] + logf(l[e]);
+        for (int nb = 0; nb < D / 32; ++nb)
+            *reinterpret_cast<float2 *>(o + nb * 8) = make_float2(acc[nb][2 * e] * f, acc[nb][2 * e + 1] * f);
+        if (p.lse && w.t == 0 && w.group == 0) p.lse[row] = m[e] + logf(l[e]);
     }
 }
 
-// D_i = do_i . o_i, and lse (see weight), both by head: a tile of queries is a
+// D_i = do_i . o_i, and lse (of bf16 calls in powers of two), both by head: a tile of queries is a
 // stretch of memory then. A block takes eight tokens of every head, in the order of
 // memory, and writes a sector of each head's; a row is 16 bytes in each of
 // d sizeof(T) / 16 lanes.
@@ -436,160 +458,181 @@ win_first_delta_kernel(WinParams p) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT)
 win_dq_kernel(WinParams p) {
-    constexpr bool SPLIT = sizeof(T) == 4;
-    extern __shared__ __align__(16) float sm[];
-    float *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    extern __shared__ __align__(16) uint2 sm[];
+    uint2 *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
+    float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
     const WinGeom &geo = p.geo;
     const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
     const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
     if (rows <= 0) return;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
-    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
-    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
+    const Place w;
+    const float *kb = (const float *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
+    const float *vb = (const float *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
     const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h, vec0 = (int64_t)h * geo.tokens + tile.start + i0;
-    load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows, ROWS);
-    load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, rows, ROWS);
-    float acc[D / 8][4], lse[2], delta[2];
+    {
+        TileLoad<D, ROWS> q, d;
+        q.load((const float *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows);
+        d.load((const float *)p.d_o + row0 * D, (int64_t)geo.hq * D, rows);
+        q.store(sq);
+        d.store(sd);
+    }
+    TileLoad<D, COLS> nk, nv;
+    float acc[D / 32][4], lse[2], delta[2];
 #pragma unroll
-    for (int nb = 0; nb < D / 8; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+    for (int nb = 0; nb < D / 32; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const bool there = r0 + e * 8 < rows;
-        lse[e] = there ? p.lse2[vec0 + r0 + e * 8] : 0.f;
-        delta[e] = there ? p.delta[vec0 + r0 + e * 8] : 0.f;
+        const bool there = w.r0 + e * 8 < rows;
+        lse[e] = there ? p.lse2[vec0 + w.r0 + e * 8] : 0.f;
+        delta[e] = there ? p.delta[vec0 + w.r0 + e * 8] : 0.f;
     }
-    const float scale = SPLIT ? p.scale : p.scale * kLog2e;
     auto walk = [&](int from, int to, bool far) {
+        auto fetch = [&](int j0) {
+            nk.load(kb + (int64_t)j0 * p.k_stride, p.k_stride, to - j0);
+            nv.load(vb + (int64_t)j0 * p.v_stride, p.v_stride, to - j0);
+        };
+        if (from < to) fetch(from);
         for (int j0 = from; j0 < to; j0 += COLS) {
             __syncthreads();
-            const int cols = min(COLS, to - j0);
-            load_tile<T, D>(sk, kb + (int64_t)j0 * p.k_stride, p.k_stride, cols, COLS);
-            load_tile<T, D>(sv, vb + (int64_t)j0 * p.v_stride, p.v_stride, cols, COLS);
+            nk.store(sk);
+            nv.store(sv);
             __syncthreads();
-            float s[COLS / 8][4], dp[COLS / 8][4];
-            rows_by_rows<SPLIT, D>(s, sq, sk);
-            rows_by_rows<SPLIT, D>(dp, sd, sv);
-#pragma unroll
-            for (int nb = 0; nb < COLS / 8; ++nb) {
+            if (j0 + COLS < to) fetch(j0 + COLS);
+            if (!w.idle(rows)) {
+                float s[4], dp[4];
+                rows_by_rows<D>(s, w, sq, sk);
+                rows_by_rows<D>(dp, w, sd, sv);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = i0 + r0 + (e >> 1) * 8, j = j0 + nb * 8 + 2 * t + (e & 1);
+                    const int i = i0 + w.r0 + (e >> 1) * 8, j = j0 + w.group * 8 + 2 * w.t + (e & 1);
                     const bool on = j < to && sees(i, j, geo.window, geo.sinks, far) && !alone(i, geo.window, geo.sinks);
-                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, lse[e >> 1]) * (dp[nb][e] - delta[e >> 1]) : 0.f;
+                    s[e] = on ? expf(fmaf(s[e], p.scale, -lse[e >> 1])) * (dp[e] - delta[e >> 1]) : 0.f;
                 }
+                put_weights(ws, w, s);
             }
-            weights_by_rows<SPLIT, D>(acc, s, sk);
+            __syncthreads();
+            if (w.idle(rows)) continue;
+            Frag f[COLS / 8];
+            get_weights(f, ws, w);
+            weights_by_rows<D>(acc, w, f, sk);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
     walk(max(0, i0 - geo.window + 1), i0 + rows, false);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int r = r0 + e * 8;
+        const int r = w.r0 + e * 8;
         if (r >= rows) continue;
-        T *dq = (T *)p.dq + (row0 + (int64_t)r * geo.hq) * D;
+        float *dq = (float *)p.dq + (row0 + (int64_t)r * geo.hq) * D + w.group * (D / 4) + 2 * w.t;
 #pragma unroll
-        for (int nb = 0; nb < D / 8; ++nb) {
-            dq[nb * 8 + 2 * t] = from_f32<T>(acc[nb][2 * e] * p.scale);
-            dq[nb * 8 + 2 * t + 1] = from_f32<T>(acc[nb][2 * e + 1] * p.scale);
-        }
+        for (int nb = 0; nb < D / 32; ++nb)
+            *reinterpret_cast<float2 *>(dq + nb * 8) = make_float2(acc[nb][2 * e] * p.scale, acc[nb][2 * e + 1] * p.scale);
     }
 }
 
-// dk and dv of 64 keys. FAR: of the sinks, from the far pairs with one tile of
-// 256 queries; the sums go to `part` in fp32.
-template <typename T, int D, bool FAR>
+// dk and dv of 64 keys; the first p.fars blocks: of the sinks, from the far pairs
+// with one tile of 256 queries, whose sums go to `part`.
+template <int D>
 __global__ void __launch_bounds__(NT)
 win_dkv_kernel(WinParams p) {
-    constexpr bool SPLIT = sizeof(T) == 4;
-    extern __shared__ __align__(16) float sm[];
-    float *sk = sm, *sv = sk + ROWS * (D + 4), *sq = sv + ROWS * (D + 4), *sd = sq + COLS * (D + 4);
-    __shared__ float slse[COLS], sdelta[COLS];
+    extern __shared__ __align__(16) uint2 sm[];
+    uint2 *sk = sm, *sv = sk + ROWS * (D + 4), *sq = sv + ROWS * (D + 4), *sd = sq + COLS * (D + 4);
+    float *wp = reinterpret_cast<float *>(sd + COLS * (D + 4)), *wd = wp + ROWS * WS;
     const WinGeom &geo = p.geo;
-    const int item = blockIdx.x, at = geo.by_hk.div(item), hk = item - at * geo.hk;
-    const WinTile tile = win_tile(geo, FAR ? at >> 1 : at >> 2);
-    const int j0 = FAR ? (at & 1) * ROWS : tile.first + (at & 3) * ROWS;
-    const int rows = min(ROWS, (FAR ? min(geo.sinks, tile.len) : tile.len) - j0);
+    const bool far = blockIdx.x < p.fars;
+    const int item = far ? blockIdx.x : blockIdx.x - p.fars, at = geo.by_hk.div(item), hk = item - at * geo.hk;
+    const WinTile tile = win_tile(geo, far ? at >> 1 : at >> 2);
+    const int j0 = far ? (at & 1) * ROWS : tile.first + (at & 3) * ROWS;
+    const int rows = min(ROWS, (far ? min(geo.sinks, tile.len) : tile.len) - j0);
     if (rows <= 0) return;
-    const int from = FAR ? max(tile.first, j0 + geo.window) : j0;
-    const int to = FAR ? min(tile.first + kWinTile, tile.len)
+    const int from = far ? max(tile.first, j0 + geo.window) : j0;
+    const int to = far ? min(tile.first + kWinTile, tile.len)
                        : (int)min((int64_t)tile.len, (int64_t)j0 + rows - 1 + geo.window);
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
-    load_tile<T, D>(sk, (const T *)p.k + (int64_t)(tile.start + j0) * p.k_stride + hk * D, p.k_stride, rows, ROWS);
-    load_tile<T, D>(sv, (const T *)p.v + (int64_t)(tile.start + j0) * p.v_stride + hk * D, p.v_stride, rows, ROWS);
-    const float scale = SPLIT ? p.scale : p.scale * kLog2e;
-    float ak[D / 8][4], av[D / 8][4];
+    const Place w;
+    {
+        TileLoad<D, ROWS> k, v;
+        k.load((const float *)p.k + (int64_t)(tile.start + j0) * p.k_stride + hk * D, p.k_stride, rows);
+        v.load((const float *)p.v + (int64_t)(tile.start + j0) * p.v_stride + hk * D, p.v_stride, rows);
+        k.store(sk);
+        v.store(sv);
+    }
+    TileLoad<D, COLS> nq, nd;
+    float lse[2], delta[2];  // of the step's queries in this thread's columns, and of the next step's
+    float next_lse[2], next_delta[2];
+    float ak[D / 32][4], av[D / 32][4];
 #pragma unroll
-    for (int nb = 0; nb < D / 8; ++nb) {
+    for (int nb = 0; nb < D / 32; ++nb) {
         ak[nb][0] = ak[nb][1] = ak[nb][2] = ak[nb][3] = 0.f;
         av[nb][0] = av[nb][1] = av[nb][2] = av[nb][3] = 0.f;
     }
-    for (int h = hk * geo.group; h < (hk + 1) * geo.group; ++h) {
-        for (int i0 = from; i0 < to; i0 += COLS) {
-            __syncthreads();
-            const int cols = min(COLS, to - i0);
-            const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h;
-            load_tile<T, D>(sq, (const T *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, cols, COLS);
-            load_tile<T, D>(sd, (const T *)p.d_o + row0 * D, (int64_t)geo.hq * D, cols, COLS);
-            if (threadIdx.x < COLS) {
-                const bool there = threadIdx.x < cols;
-                const int64_t at = (int64_t)h * geo.tokens + tile.start + i0 + threadIdx.x;
-                slse[threadIdx.x] = there ? p.lse2[at] : 0.f;
-                sdelta[threadIdx.x] = there ? p.delta[at] : 0.f;
-            }
-            __syncthreads();
-            float s[COLS / 8][4], dp[COLS / 8][4];
-            rows_by_rows<SPLIT, D>(s, sk, sq);
-            rows_by_rows<SPLIT, D>(dp, sv, sd);
+    auto fetch = [&](int h, int i0) {
+        const int64_t row0 = (int64_t)(tile.start + i0) * geo.hq + h;
+        nq.load((const float *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, to - i0);
+        nd.load((const float *)p.d_o + row0 * D, (int64_t)geo.hq * D, to - i0);
 #pragma unroll
-            for (int nb = 0; nb < COLS / 8; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + r0 + (e >> 1) * 8, c = nb * 8 + 2 * t + (e & 1), i = i0 + c;
-                    const bool on = r0 + (e >> 1) * 8 < rows && i < to && sees(i, j, geo.window, geo.sinks, FAR);
-                    s[nb][e] = on ? weight<SPLIT>(s[nb][e], scale, slse[c]) : 0.f;
-                    dp[nb][e] = on && !alone(i, geo.window, geo.sinks) ? s[nb][e] * (dp[nb][e] - sdelta[c]) : 0.f;
-                }
-            }
-            weights_by_rows<SPLIT, D>(av, s, sd);
-            weights_by_rows<SPLIT, D>(ak, dp, sq);
+        for (int e = 0; e < 2; ++e) {
+            const int i = i0 + w.group * 8 + 2 * w.t + e;
+            const int64_t x = (int64_t)h * geo.tokens + tile.start + i;
+            next_lse[e] = i < to ? p.lse2[x] : 0.f;
+            next_delta[e] = i < to ? p.delta[x] : 0.f;
         }
+    };
+    const int h_end = (hk + 1) * geo.group;
+    int h = hk * geo.group, i0 = from;
+    if (from < to) fetch(h, i0);
+    while (from < to && h < h_end) {
+        __syncthreads();
+        nq.store(sq);
+        nd.store(sd);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) lse[e] = next_lse[e], delta[e] = next_delta[e];
+        __syncthreads();
+        const int i_now = i0;
+        if ((i0 += COLS) >= to) i0 = from, ++h;
+        if (h < h_end) fetch(h, i0);
+        if (!w.idle(rows)) {
+            float s[4], dp[4];
+            rows_by_rows<D>(s, w, sk, sq);
+            rows_by_rows<D>(dp, w, sv, sd);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = w.r0 + (e >> 1) * 8, i = i_now + w.group * 8 + 2 * w.t + (e & 1);
+                const bool on = r < rows && i < to && sees(i, j0 + r, geo.window, geo.sinks, far);
+                s[e] = on ? expf(fmaf(s[e], p.scale, -lse[e & 1])) : 0.f;
+                dp[e] = on && !alone(i, geo.window, geo.sinks) ? s[e] * (dp[e] - delta[e & 1]) : 0.f;
+            }
+            put_weights(wp, w, s);
+            put_weights(wd, w, dp);
+        }
+        __syncthreads();
+        if (w.idle(rows)) continue;
+        Frag f[COLS / 8];
+        get_weights(f, wp, w);
+        weights_by_rows<D>(av, w, f, sd);
+        get_weights(f, wd, w);
+        weights_by_rows<D>(ak, w, f, sq);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int r = r0 + e * 8, j = j0 + r;
+        const int r = w.r0 + e * 8, j = j0 + r, c = w.group * (D / 4) + 2 * w.t;
         if (r >= rows) continue;
-        if constexpr (FAR) {
-            float *dk = p.part + (((int64_t)win_far_slot(at >> 1, tile.seq, 1) * geo.hk + hk) * 2 * geo.sinks + j) * D;
-            float *dv = dk + (int64_t)geo.sinks * D;
+        const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D + c;
+        float *dk = (float *)p.dk + row, *dv = (float *)p.dv + row;
+        if (far) {
+            dk = p.part + (((int64_t)win_far_slot(at >> 1, tile.seq, 1) * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
+            dv = dk + (int64_t)geo.sinks * D;
+        } else if (j < geo.sinks && tile.len > geo.window) {
+            dk = p.near + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
+            dv = dk + (int64_t)geo.sinks * D;
+        }
 #pragma unroll
-            for (int nb = 0; nb < D / 8; ++nb) {
-                *reinterpret_cast<float2 *>(dk + nb * 8 + 2 * t) = make_float2(ak[nb][2 * e] * p.scale, ak[nb][2 * e + 1] * p.scale);
-                *reinterpret_cast<float2 *>(dv + nb * 8 + 2 * t) = make_float2(av[nb][2 * e], av[nb][2 * e + 1]);
-            }
-        } else {
-            const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D;
-            const bool sink = j < geo.sinks && tile.len > geo.window;
-            float *fk = p.near + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D;
-            float *fv = fk + (int64_t)geo.sinks * D;
-#pragma unroll
-            for (int nb = 0; nb < D / 8; ++nb) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int c = nb * 8 + 2 * t + u;
-                    const float dk = ak[nb][2 * e + u] * p.scale, dv = av[nb][2 * e + u];
-                    if (sink) {
-                        fk[c] = dk, fv[c] = dv;
-                    } else {
-                        ((T *)p.dk)[row + c] = from_f32<T>(dk);
-                        ((T *)p.dv)[row + c] = from_f32<T>(dv);
-                    }
-                }
-            }
+        for (int nb = 0; nb < D / 32; ++nb) {
+            *reinterpret_cast<float2 *>(dk + nb * 8) = make_float2(ak[nb][2 * e] * p.scale, ak[nb][2 * e + 1] * p.scale);
+            *reinterpret_cast<float2 *>(dv + nb * 8) = make_float2(av[nb][2 * e], av[nb][2 * e + 1]);
         }
     }
 }
@@ -702,16 +745,14 @@ cudaError_t run(void (*kernel)(P...), std::atomic<uint64_t> &allowed, unsigned g
     return cudaGetLastError();
 }
 
-template <typename T, int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
+template <int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    constexpr size_t smem = (ROWS + 2 * COLS) * (D + 4) * sizeof(float);
-    return run(win_forward_kernel<T, D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, params(p, a));
+    constexpr size_t smem = (ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
+    return run(win_forward_kernel<D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, params(p, a));
 }
 
 template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
-    static std::atomic<uint64_t> allowed[3];
-    constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(float);
-    const WinParams w = params(p, a);
+    WinParams w = params(p, a);
     win_delta_kernel<T, D><<<(unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float), s>>>(
         (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq);
     KDA_TRY(cudaGetLastError());
@@ -724,9 +765,12 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
     if constexpr (sizeof(T) == 2) {
         KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, s));
     } else {
-        if (far) KDA_TRY(run(win_dkv_kernel<T, D, true>, allowed[0], (unsigned)(p.geo.ntiles * 2 * a.hk), smem, s, w));
-        KDA_TRY(run(win_dkv_kernel<T, D, false>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hk), smem, s, w));
-        KDA_TRY(run(win_dq_kernel<T, D>, allowed[2], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
+        static std::atomic<uint64_t> allowed[2];
+        constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
+        w.fars = far ? p.geo.ntiles * 2 * a.hk : 0;
+        KDA_TRY(run(win_dkv_kernel<D>, allowed[0], (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), smem + ROWS * WS * sizeof(float),
+                    s, w));
+        KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
     }
     if (far)
         win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(
@@ -746,7 +790,7 @@ cudaError_t launch_window(const WinArgs &a, cudaStream_t s) {
     KDA_TRY(prepare_tiles(p, a, s));
     if (p.geo.tokens == 0) return cudaSuccess;
     if (a.dt == KDA_BF16) return launch_window_forward_tc(p.geo, a, s);
-    return a.d == 128 ? forward<float, 128>(p, a, s) : forward<float, 64>(p, a, s);
+    return a.d == 128 ? forward<128>(p, a, s) : forward<64>(p, a, s);
 }
 
 cudaError_t launch_window_backward(const WinArgs &a, cudaStream_t s) {

@@ -19,14 +19,14 @@ kda_status_t common(kda_dtype_t dt, int N, int64_t T, int hq, int hk, int d, int
         return fail(sinks < 0 ? KDA_ERR_INVALID_ARG : KDA_ERR_UNSUPPORTED, "0 to %d sinks (got %d)", kWinMaxSinks, sinks);
     return KDA_OK;
 }
-// The tokens, and the largest grid: four blocks to a tile of 256 tokens and head.
+// The tokens, and the largest grid: six blocks to a tile of 256 tokens and head.
 kda_status_t sizes(int N, int64_t T, int hq, bool packed) {
     const int64_t tokens = packed ? T : N * T;
     if (tokens > 1 << 30) return fail(KDA_ERR_UNSUPPORTED, "2^30 tokens at most");
     const int64_t tiles = packed ? T / kWinTile + N : N * ((T + kWinTile - 1) / kWinTile);
     if (hq > 1024) return fail(KDA_ERR_UNSUPPORTED, "1024 query heads at most (got %d)", hq);
-    if (!fits(tiles, 4, hq) || !fits(N, hq))
-        return fail(KDA_ERR_UNSUPPORTED, "the 64-token blocks of all sequences times H_q must fit in int32");
+    if (!fits(tiles, 6, hq) || !fits(N, hq))
+        return fail(KDA_ERR_UNSUPPORTED, "the 256-token tiles of all sequences times 6 H_q must fit in int32");
     return KDA_OK;
 }
 kda_status_t strides(int64_t &q, int64_t &k, int64_t &v, int hq, int hk, int d, kda_dtype_t dt) {
