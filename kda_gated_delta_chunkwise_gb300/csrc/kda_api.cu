@@ -7,6 +7,7 @@
 
 #include "kda_internal.cuh"
 #include "kda_linear_tc.cuh"
+#include "kda_block_norm.cuh"
 #include "kda_window_tc.cuh"
 
 namespace {
@@ -134,6 +135,9 @@ kda_status_t kda_device_errors(int *errors, int reset) {
     *errors |= more;
     more = 0;
     if (e == cudaSuccess) e = kda::read_window_error(&more, reset != 0);
+    *errors |= more;
+    more = 0;
+    if (e == cudaSuccess) e = kda::read_block_error(&more, reset != 0);
     *errors |= more;
     return cuda_status(e, "reading the device error word");
 }

@@ -20,6 +20,7 @@
 
 #include "kda_block_norm.cuh"
 #include "kda_rows.cuh"
+#include "kda_tc_roles.cuh"
 
 namespace kda {
 namespace {
@@ -242,8 +243,13 @@ template <typename T> struct Eight {  // eight channels
         for (int i = 0; i < CHUNKS; ++i) v[i].load(p + i * Vec<T>::N);
     }
     __device__ __forceinline__ void store(T *p) const {
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) v[i].store(p + i * Vec<T>::N);
+        if constexpr (CHUNKS == 2) {
+            const uint32_t r[8] = {v[0].raw[0], v[0].raw[1], v[0].raw[2], v[0].raw[3],
+                                   v[1].raw[0], v[1].raw[1], v[1].raw[2], v[1].raw[3]};
+            st_v8(p, r);
+        } else {
+            v[0].store(p);
+        }
     }
     __device__ __forceinline__ F2 get(int i) const { return v[i / (Vec<T>::N / 2)].get(i % (Vec<T>::N / 2)); }
     __device__ __forceinline__ void put(int i, F2 x) { v[i / (Vec<T>::N / 2)].put(i % (Vec<T>::N / 2), x); }
@@ -260,38 +266,57 @@ __device__ __forceinline__ void load_eight(const float *p, int c, F2 (&x)[4]) { 
     }
 }
 
-// Sums of K values over a row's tr threads, the same in all of them. `scratch`
-// [warps of the block][8]; calls in turn take one and the other half of it, so
-// one barrier a call is enough.
-template <int K> __device__ __forceinline__ void row_totals(float (&v)[K], int tr, float *scratch, int group) {
+// The sum of a value over a row's tr threads, the same in all of them. `scratch`
+// [warps of the block]; calls in turn take one and the other half of it, so one
+// barrier a call is enough.
+__device__ __forceinline__ void row_barrier(int tr, int group) {
+    if (tr == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tr) : "memory");
+}
+__device__ __forceinline__ float row_total(float v, int tr, float *scratch, int group) {
+    v = row_sum<32>(v);
+    if (tr == 32) return v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tr >> 5;
+    if (lane == 0) scratch[warp] = v;
+    row_barrier(tr, group);
+    return row_sum<32>(lane < warps ? scratch[group * warps + lane] : 0.f);
+}
+// The same of six values at once, in two halves. In a warp the lanes share the values
+// out as they add them up, nine shuffles in all instead of thirty, and leave them at
+// scratch [16 warps][8]; after a barrier of the row each warp adds up the row's.
+__device__ __forceinline__ void warp_totals(float (&v)[8], float *scratch) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int bit = 16, n = 4; n > 0; bit >>= 1, n >>= 1) {
+        const bool up = lane & bit;
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+        for (int i = 0; i < n; ++i) {
+            const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
     }
-    if (tr == 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tr >> 5, w0 = group * warps;
-    if (lane == 0) {
+    float x = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);  // of value lane / 4
+    if ((lane & 3) == 0) scratch[(threadIdx.x >> 5) * 8 + (lane >> 2)] = x;
+}
+__device__ __forceinline__ void read_totals(float (&v)[6], int tr, const float *scratch, int group) {
+    const int lane = threadIdx.x & 31, warps = tr >> 5;
+    const float *mine = scratch + group * warps * 8 + (lane & 3) * 8 + (lane >> 2);  // four lanes a value
+    float x = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) scratch[warp * 8 + k] = v[k];
+    for (int w = 0; w < 16; w += 4) {
+        if (w + (lane & 3) < warps) x += mine[w * 8];
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tr) : "memory");
-    // lane l reads warp l's; the tree's order is the same in every warp
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < warps ? scratch[(w0 + lane) * 8 + k] : 0.f;
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) {  // 16 warps at most
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
+    for (int k = 0; k < 6; ++k) v[k] = __shfl_sync(0xffffffffu, x, 4 * k);
 }
 
 template <typename S, typename T, int V>
 __global__ void __launch_bounds__(512)
 kda_residual_norm_kernel(ResidualArgs p, int tr) {
-    __shared__ float scratch[2][16 * 8];
+    __shared__ float scratch[2][16];
     const int group = threadIdx.x / tr, in = threadIdx.x % tr;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tr) + group;
     if (row >= p.tokens) return;  // uniform over the row's threads
@@ -315,9 +340,7 @@ kda_residual_norm_kernel(ResidualArgs p, int tr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) ss = fma2(b[v].get(i), b[v].get(i), ss);
         }
-        float sum[1] = {f2_sum(ss)};
-        row_totals(sum, tr, scratch[0], group);
-        rb = rnorm(sum[0], p.branch_norm, inv_d, p.eps);
+        rb = rnorm(row_total(f2_sum(ss), tr, scratch[0], group), p.branch_norm, inv_d, p.eps);
     }
     F2 h[V][4], ss = f2(0.f, 0.f);
     const F2 s2 = f2(p.scale * rb, p.scale * rb);
@@ -336,9 +359,7 @@ kda_residual_norm_kernel(ResidualArgs p, int tr) {
         }
         if (there) x[v].store((S *)p.h + row * p.D + c);
     }
-    float sum[1] = {f2_sum(ss)};
-    row_totals(sum, tr, scratch[1], group);
-    const float r = rnorm(sum[0], KDA_NORM_RMS, inv_d, p.eps);
+    const float r = rnorm(row_total(f2_sum(ss), tr, scratch[1], group), KDA_NORM_RMS, inv_d, p.eps);
     const F2 r2 = f2(r, r);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -353,15 +374,14 @@ kda_residual_norm_kernel(ResidualArgs p, int tr) {
 }
 
 // Persistent: the threads of a row walk the rows with a fixed stride and keep the
-// sums over them in registers. The inputs come by cp.async; a slot of the ring
-// is read by the thread that fills it, and is filled for the next row as soon
-// as its row is in registers, so even one stage keeps a row's loads on their way
-// while the last row is worked on.
+// sums over them in registers. A row's inputs come as bulk copies into a ring of
+// its threads; while a row's gradients are made, the sums of the next one are
+// added up, and one barrier a row serves its totals and the ring. A row that fills
+// the ring by itself stays in registers, and the next one comes meanwhile.
 constexpr int RT = 512;
 template <typename S, typename T, int V> struct ResidualRing {
-    static constexpr int CHUNKS = V * 2 * (Eight<S>::CHUNKS + Eight<T>::CHUNKS);  // a thread's, 16 bytes each
-    static constexpr int STAGE = CHUNKS * RT * 16;
-    static constexpr int STAGES = 3 * STAGE <= 200 * 1024 ? 3 : 2 * STAGE <= 200 * 1024 ? 2 : 1;
+    static constexpr int STAGE = RT * V * 8 * 2 * (sizeof(S) + sizeof(T));  // of the block's rows
+    static constexpr int FIT = 200 * 1024 / STAGE, STAGES = FIT < 4 ? FIT : 4;
     static constexpr int BYTES = STAGES * STAGE;
 };
 
@@ -369,94 +389,114 @@ template <typename S, typename T, int V>
 __global__ void __launch_bounds__(RT, 1)
 kda_residual_norm_bwd_kernel(ResidualArgs p, int tr) {
     using R = ResidualRing<S, T, V>;
-    constexpr int SC = Eight<S>::CHUNKS, TC = Eight<T>::CHUNKS, SN = Vec<S>::N, TN = Vec<T>::N;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float scratch[2][16 * 8];
+    __shared__ __align__(16) float scratch[2][8 * 16];
+    __shared__ uint64_t full[R::STAGES][RT / 32];
+    __shared__ int abort_flag;
+    const Abort stop{&abort_flag};
     const int group = threadIdx.x / tr, in = threadIdx.x % tr, groups = RT / tr;
-    unsigned char *mine = smem + threadIdx.x * 16;
-    const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
     const bool branch = p.branch_norm != KDA_NORM_NONE || p.wb || p.c || p.dwb || p.dc;  // the branch is read
     const float inv_d = 1.f / (float)p.D;
     const int64_t step = (int64_t)gridDim.x * groups;
+    if (in == 0) {
+        for (int i = 0; i < R::STAGES; ++i) mbar_init(&full[i][group], 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) abort_flag = 0;
+    __syncthreads();
     F2 aw[V][4], ab[V][4], ac[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) aw[v][i] = ab[v][i] = ac[v][i] = f2(0.f, 0.f);
     }
-    // chunk k of a thread's stage: h, dh, dy, b of every v
-    auto slot = [&](int stage, int v, int k) { return (stage * R::CHUNKS + v * 2 * (SC + TC) + k) * RT * 16; };
-    auto fetch = [&](int64_t row, int stage) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = (in + v * tr) * 8;
-            const bool there = row < p.tokens && c < p.D;
-            const int64_t at = there ? row * p.D + c : 0;
-#pragma unroll
-            for (int k = 0; k < SC; ++k) {
-                copy16(mine_s + slot(stage, v, k), (const S *)p.x + at + k * SN, there);
-                copy16(mine_s + slot(stage, v, SC + k), (const S *)(p.dh ? p.dh : p.x) + at + k * SN, there && p.dh);
-            }
-#pragma unroll
-            for (int k = 0; k < TC; ++k) {
-                copy16(mine_s + slot(stage, v, 2 * SC + k), (const T *)p.dy + at + k * TN, there);
-                copy16(mine_s + slot(stage, v, 2 * SC + TC + k), (const T *)(branch ? p.b : p.dy) + at + k * TN,
-                       there && branch);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    // the weights of this thread's channels: with eight channels kept, with sixteen read again for every row
+    F2 w[4], wb[4], ch[4];
+    auto weights = [&](int v) {
+        const int c = (in + v * tr) * 8;
+        const bool there = c < p.D;
+        load_eight(there ? p.w : nullptr, c, w);
+        load_eight(there ? p.wb : nullptr, c, wb);
+        load_eight(there ? p.c : nullptr, c, ch);
     };
-    int64_t row = (int64_t)blockIdx.x * groups + group;
+    if constexpr (V == 1) weights(0);
+    // a stage holds a row's h, dh, dy, b one after the other
+    unsigned char *ring = smem + group * (R::STAGE / groups);
+    const uint32_t row_s = p.D * (uint32_t)sizeof(S), row_t = p.D * (uint32_t)sizeof(T);
+    auto fetch = [&](int64_t row, int stage) {  // one thread
+        if (row >= p.tokens) return;
+        uint64_t *bar = &full[stage][group];
+        unsigned char *to = ring + stage * R::STAGE;
+        mbar_arrive_expect_tx(bar, row_s + (p.dh ? row_s : 0u) + row_t + (branch ? row_t : 0u));
+        bulk_load(to, (const S *)p.x + row * p.D, row_s, bar);
+        if (p.dh) bulk_load(to + row_s, (const S *)p.dh + row * p.D, row_s, bar);
+        bulk_load(to + 2 * row_s, (const T *)p.dy + row * p.D, row_t, bar);
+        if (branch) bulk_load(to + 2 * row_s + row_t, (const T *)p.b + row * p.D, row_t, bar);
+    };
+    Eight<S> h[V], dh[V];
+    Eight<T> dy[V], b[V];
+    auto load = [&](int stage, int v) {
+        const int c = (in + v * tr) * 8;
+        const unsigned char *from = ring + stage * R::STAGE;
+        h[v].zero(), dh[v].zero(), dy[v].zero(), b[v].zero();
+        if (c >= p.D) return;
+        h[v].load((const S *)from + c);
+        if (p.dh) dh[v].load((const S *)(from + row_s) + c);
+        dy[v].load((const T *)(from + 2 * row_s) + c);
+        if (branch) b[v].load((const T *)(from + 2 * row_s + row_t) + c);
+    };
+    // a row's sums: h h, h w dy, b b, and q dh, q w dy, q h with q = b w_b c
+    auto sums = [&](int stage, float *at) {
+        F2 a[6];
 #pragma unroll
-    for (int i = 0; i < R::STAGES; ++i) fetch(row + i * step, i);
-    int stage = 0, half = 0;
-    for (; row < p.tokens; row += step, half ^= 1) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(R::STAGES - 1) : "memory");
-        Eight<S> h[V], dh[V];
-        Eight<T> dy[V], b[V];
+        for (int k = 0; k < 6; ++k) a[k] = f2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            load(stage, v);
+            if constexpr (V > 1) weights(v);
 #pragma unroll
-            for (int k = 0; k < SC; ++k) {
-                h[v].v[k].load(reinterpret_cast<const S *>(mine + slot(stage, v, k)));
-                dh[v].v[k].load(reinterpret_cast<const S *>(mine + slot(stage, v, SC + k)));
-            }
-#pragma unroll
-            for (int k = 0; k < TC; ++k) {
-                dy[v].v[k].load(reinterpret_cast<const T *>(mine + slot(stage, v, 2 * SC + k)));
-                b[v].v[k].load(reinterpret_cast<const T *>(mine + slot(stage, v, 2 * SC + TC + k)));
+            for (int i = 0; i < 4; ++i) {
+                const F2 hv = h[v].get(i), bv = b[v].get(i), wd = w[i] * dy[v].get(i), q = bv * wb[i] * ch[i];
+                a[0] = fma2(hv, hv, a[0]);
+                a[1] = fma2(hv, wd, a[1]);
+                a[2] = fma2(bv, bv, a[2]);
+                a[3] = fma2(q, dh[v].get(i), a[3]);
+                a[4] = fma2(q, wd, a[4]);
+                a[5] = fma2(q, hv, a[5]);
             }
         }
-        fetch(row + R::STAGES * step, stage);
-        stage = stage == R::STAGES - 1 ? 0 : stage + 1;
-        float sum[6];  // h h, h w dy, b b, and q dh, q w dy, q h with q = b w_b c
-        {
-            F2 a[6];
+        float sum[8];
 #pragma unroll
-            for (int k = 0; k < 6; ++k) a[k] = f2(0.f, 0.f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = (in + v * tr) * 8;
-                const bool there = c < p.D;
-                F2 w[4], wb[4], ch[4];
-                load_eight(there ? p.w : nullptr, c, w);
-                load_eight(there ? p.wb : nullptr, c, wb);
-                load_eight(there ? p.c : nullptr, c, ch);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 hv = h[v].get(i), bv = b[v].get(i), wd = w[i] * dy[v].get(i), q = bv * wb[i] * ch[i];
-                    a[0] = fma2(hv, hv, a[0]);
-                    a[1] = fma2(hv, wd, a[1]);
-                    a[2] = fma2(bv, bv, a[2]);
-                    a[3] = fma2(q, dh[v].get(i), a[3]);
-                    a[4] = fma2(q, wd, a[4]);
-                    a[5] = fma2(q, hv, a[5]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 6; ++k) sum[k] = f2_sum(a[k]);
+        for (int k = 0; k < 6; ++k) sum[k] = f2_sum(a[k]);
+        sum[6] = sum[7] = 0.f;
+        warp_totals(sum, at);
+    };
+    constexpr bool AHEAD = R::STAGES > 1;  // the sums of the next row are made with a row's gradients
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    if (in == 0) {
+        for (int i = 0; i < (AHEAD ? R::STAGES - 1 : 1); ++i) fetch(row + i * step, i);
+    }
+    int stage = 0, half = 0;
+    uint32_t parity = 0;  // of this row's stage
+    if (AHEAD && row < p.tokens) {
+        stop.wait_warp(smem_u32(&full[0][group]), 0);
+        sums(0, scratch[0]);
+    }
+    for (; row < p.tokens; row += step, half ^= 1) {
+        if constexpr (!AHEAD) {
+            stop.wait_warp(smem_u32(&full[0][group]), parity);
+            sums(0, scratch[half]);
         }
-        row_totals(sum, tr, scratch[half], group);
+        row_barrier(tr, group);
+        // all of the row's threads have read the row before it, or this one if there is one stage
+        const int last = stage == 0 ? R::STAGES - 1 : stage - 1, next = stage == R::STAGES - 1 ? 0 : stage + 1;
+        if (in == 0) fetch(row + (AHEAD ? R::STAGES - 1 : 1) * step, AHEAD ? last : 0);
+        float sum[6];
+        read_totals(sum, tr, scratch[half], group);
+        if (AHEAD && row + step < p.tokens) {
+            stop.wait_warp(smem_u32(&full[next][group]), parity ^ (next == 0));
+            sums(next, scratch[half ^ 1]);
+        }
         const float r = rnorm(sum[0], KDA_NORM_RMS, inv_d, p.eps), c = sum[1] * r * inv_d;
         const float rb = rnorm(sum[2], p.branch_norm, inv_d, p.eps);
         // (m . w_b du) k, without the scale
@@ -469,11 +509,9 @@ kda_residual_norm_bwd_kernel(ResidualArgs p, int tr) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c0 = (in + v * tr) * 8;
+            if constexpr (AHEAD) load(stage, v);
             if (c0 >= p.D) continue;
-            F2 w[4], wb[4], ch[4];
-            load_eight(p.w, c0, w);
-            load_eight(p.wb, c0, wb);
-            load_eight(p.c, c0, ch);
+            if constexpr (V > 1) weights(v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const F2 n = h[v].get(i) * r2, dyv = dy[v].get(i);
@@ -488,8 +526,11 @@ kda_residual_norm_bwd_kernel(ResidualArgs p, int tr) {
             h[v].store((S *)p.dx + row * p.D + c0);
             dy[v].store((T *)p.db + row * p.D + c0);
         }
+        stage = next;
+        parity ^= next == 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    settle(stop);
     if (!p.partial) return;
     // the groups' shares, one set of sums after the other: [groups][D] in shared memory
     float *red = reinterpret_cast<float *>(smem);
@@ -579,5 +620,7 @@ cudaError_t launch_residual_norm(const ResidualArgs &p, bool back, cudaStream_t 
     return p.stream_dt == KDA_F32 ? launch_residual<float, __nv_bfloat16>(p, back, s)
                                   : launch_residual<__nv_bfloat16, __nv_bfloat16>(p, back, s);
 }
+
+cudaError_t read_block_error(int *out, bool reset) { return read_tc_error(out, reset); }
 
 }  // namespace kda

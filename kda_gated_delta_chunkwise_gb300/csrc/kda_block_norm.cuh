@@ -41,5 +41,6 @@ struct ResidualArgs {
     float scale, eps;
 };
 cudaError_t launch_residual_norm(const ResidualArgs &p, bool back, cudaStream_t s);
+cudaError_t read_block_error(int *out, bool reset);
 
 }  // namespace kda

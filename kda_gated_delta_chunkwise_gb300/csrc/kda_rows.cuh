@@ -59,6 +59,20 @@ __device__ __forceinline__ float rnorm(float ss, int norm, float inv_d, float ep
     return norm == KDA_NORM_NONE ? 1.f : rsqrtf((norm == KDA_NORM_RMS ? ss * inv_d : ss) + eps);
 }
 
+// One 32-byte sector; a pointer that is 16-byte aligned alone (an output the
+// caller cut out of a larger tensor) takes two stores.
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {
+    if (reinterpret_cast<uintptr_t>(p) & 16) {
+        uint4 *q = reinterpret_cast<uint4 *>(p);
+        q[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        q[1] = make_uint4(r[4], r[5], r[6], r[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {  // zeros where not there
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }

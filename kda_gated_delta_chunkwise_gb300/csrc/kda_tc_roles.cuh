@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "kda_rows.cuh"
 #include "kda_linear.cuh"
 #include "kda_tc_ptx.cuh"
 
@@ -79,17 +80,11 @@ __device__ __forceinline__ uint32_t pack2(F2 x) {
     f2_get(x, a, b);
     return pack2(a, b);
 }
-// One 32-byte sector; a pointer that is 16-byte aligned alone (an output the
-// caller cut out of a larger tensor) takes two stores.
-__device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {
-    if (reinterpret_cast<uintptr_t>(p) & 16) {
-        uint4 *q = reinterpret_cast<uint4 *>(p);
-        q[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        q[1] = make_uint4(r[4], r[5], r[6], r[7]);
-        return;
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// `bytes` in a row, a multiple of 16, both addresses 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
