@@ -203,30 +203,6 @@ kda_gated_norm_bwd_kernel(GatedArgs p, int rows) {
     }
 }
 
-// ================================================================ the blocks' shares of a weight's gradient
-// dst[s][c] = sum over blocks of partial[block][s][c], lanes over the columns,
-// eight groups of threads over the blocks, their sums added in order.
-constexpr int ST = 256;
-__global__ void __launch_bounds__(ST)
-kda_column_sum_kernel(const float *partial, int blocks, int D, float *d0, float *d1, float *d2) {
-    __shared__ float red[ST / 32][33];
-    after_previous();
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5, s = blockIdx.y;
-    float a = 0.f;
-    if (c < D) {
-#pragma unroll 8
-        for (int b = group; b < blocks; b += ST / 32) a += partial[((int64_t)b * gridDim.y + s) * D + c];
-    }
-    red[group][threadIdx.x & 31] = a;
-    __syncthreads();
-    if (group == 0 && c < D) {
-#pragma unroll
-        for (int k = 1; k < ST / 32; ++k) a += red[k][threadIdx.x];
-        float *dst = s == 0 ? d0 : s == 1 ? d1 : d2;
-        if (dst) dst[c] = a;
-    }
-}
-
 // ================================================================ the residual stream
 // A row is held by `tr` threads, a power of two from a warp up to 512, eight
 // channels V times in each (tr the least that does with V <= 2 forward, V = 1
@@ -575,7 +551,7 @@ template <typename T, int D> cudaError_t launch_gated(const GatedArgs &p, bool b
     Launches l{s};
     e = l.next(kda_gated_norm_bwd_kernel<T, D>, grid, GT, GB_SMEM, p, rows);
     if (e != cudaSuccess || !p.partial) return e;
-    return l.next(kda_column_sum_kernel, dim3((D + 31) / 32, 1), ST, 0, p.partial, grid, D, p.dw, nullptr, nullptr);
+    return column_sum(l, p.partial, grid, D, 1, p.dw);
 }
 
 template <typename S, typename T> cudaError_t launch_residual(const ResidualArgs &p, bool back, cudaStream_t s) {
@@ -604,7 +580,7 @@ template <typename S, typename T> cudaError_t launch_residual(const ResidualArgs
     };
     const cudaError_t e = two ? run(std::integral_constant<int, 2>{}) : run(std::integral_constant<int, 1>{});
     if (e != cudaSuccess || !p.partial) return e;
-    return l.next(kda_column_sum_kernel, dim3((p.D + 31) / 32, 3), ST, 0, p.partial, grid, p.D, p.dw, p.dwb, p.dc);
+    return column_sum(l, p.partial, grid, p.D, 3, p.dw, p.dwb, p.dc);
 }
 
 }  // namespace

@@ -262,7 +262,7 @@ kda_qk_norm_rope_kernel(NormRopeArgs p, Parts parts, int units) {
 // Backward. Persistent: each warp walks the units with a fixed stride and
 // keeps its share of the weight gradients in registers; the block's shares
 // are added in warp order and written to `partial` [blocks][2][D], which
-// kda_weight_sum_kernel adds in block order: the same bits on every call.
+// kda_column_sum_kernel adds in block order: the same bits on every call.
 // x, dy and the token's table row come by cp.async into a ring of the warp's
 // own, kStages units deep: 13 KB in flight per warp at no cost in registers
 // (held in registers instead, two blocks of eight warps fit on an SM with 4 KB
@@ -434,20 +434,6 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
     }
 }
 
-// dw[s][c] = sum over blocks of partial[block][s][c], in a fixed order: one
-// warp per output, lanes striding over the blocks, then a shuffle tree.
-__global__ void __launch_bounds__(kThreads)
-kda_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, float *dwq, float *dwk) {
-    const int o = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (o >= 2 * d) return;
-    float a = 0.f;
-#pragma unroll 10
-    for (int b = lane; b < blocks; b += 32) a += partial[(int64_t)b * 2 * d + o];
-    a = row_sum<32>(a);
-    float *dst = o < d ? dwq : dwk;
-    if (lane == 0 && dst) dst[o % d] = a;
-}
-
 template <typename T, int D, bool AXES> cudaError_t launch(const NormRopeArgs &p, bool back, cudaStream_t s) {
     constexpr int R = unit_rows<T, D>();
     Parts parts;
@@ -467,11 +453,10 @@ template <typename T, int D, bool AXES> cudaError_t launch(const NormRopeArgs &p
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kda_qk_norm_rope_bwd_kernel<T, D, AXES>, kBwdSmem, allowed);
     if (e != cudaSuccess) return e;
-    kda_qk_norm_rope_bwd_kernel<T, D, AXES><<<grid, kThreads, kBwdSmem, s>>>(p, parts);
-    e = cudaGetLastError();
+    Launches l{s};
+    e = l.next(kda_qk_norm_rope_bwd_kernel<T, D, AXES>, grid, kThreads, kBwdSmem, p, parts);
     if (e != cudaSuccess || !p.partial) return e;
-    kda_weight_sum_kernel<<<(2 * D + kWarps - 1) / kWarps, kThreads, 0, s>>>(p.partial, grid, D, p.dwq, p.dwk);
-    return cudaGetLastError();
+    return column_sum(l, p.partial, grid, D, 2, p.dwq, p.dwk);
 }
 
 }  // namespace
