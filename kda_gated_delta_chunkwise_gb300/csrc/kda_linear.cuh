@@ -78,8 +78,11 @@ template <typename F> inline cudaError_t allow_smem(F *kernel, size_t bytes, std
 // kernels, one CTA an SM, are launched by whole, as usual: launched early they
 // made the long forward (131072 tokens) 1502 us from 1372 and the backward of
 // 4 x 4096 x 16 468 from 454.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void after_previous() {
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    await_previous();
 }
 struct Launches {
     cudaStream_t stream;

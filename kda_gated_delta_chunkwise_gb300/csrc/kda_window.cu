@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(256)
 win_delta_kernel(const T *o, const T *d_o, const float *lse, float *lse2, float *delta, int64_t tokens, int hq) {
     constexpr int N = 16 / sizeof(T), LANES = D / N, PER = 256 / LANES, FLIGHT = 4;
     extern __shared__ float sums[];  // [hq][8]
+    let_next_start();
     const int in = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const int64_t t0 = (int64_t)blockIdx.x * 8;
     const int count = (int)(tokens - t0 < 8 ? tokens - t0 : 8), rows = count * hq;
@@ -383,11 +384,18 @@ win_first_delta_kernel(WinParams p) {
     const WinGeom &geo = p.geo;
     const bool firsts = !few_keys(geo.window, geo.sinks);  // `at` counts sequences, else 64 queries
     const int at = geo.by_hq.div(blockIdx.x), h = blockIdx.x - at * geo.hq, hk = h / geo.group;
-    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) return;
+    let_next_start();
+    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) {
+        await_previous();
+        return;
+    }
     const WinTile tile = win_tile(geo, !firsts ? at >> 2 : geo.tiles ? geo.seq_tile[at] : at * geo.per_seq);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int i0 = (firsts ? 0 : tile.first + (at & 3) * 64) + (threadIdx.x >> 5) * 16;
-    if (i0 >= tile.len) return;
+    if (i0 >= tile.len) {
+        await_previous();
+        return;
+    }
     uint4 q[2][KC], d[2][KC];
     float lse2[2], sum[2] = {0.f, 0.f}, all[2] = {0.f, 0.f};
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -446,6 +454,7 @@ win_first_delta_kernel(WinParams p) {
     const int end = min(i0 + 16, tile.len);
     if (end > geo.window) walk(0, min(geo.sinks, end - geo.window), true);
     walk(max(0, i0 - geo.window + 1), end, false);
+    await_previous();  // it writes D of these queries too
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -468,7 +477,10 @@ win_dq_kernel(WinParams p) {
     const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
     const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
-    if (rows <= 0) return;
+    if (rows <= 0) {
+        await_previous();
+        return;
+    }
     const Place w;
     const float *kb = (const float *)p.k + (int64_t)tile.start * p.k_stride + hk * D;
     const float *vb = (const float *)p.v + (int64_t)tile.start * p.v_stride + hk * D;
@@ -532,6 +544,7 @@ win_dq_kernel(WinParams p) {
         for (int nb = 0; nb < D / 32; ++nb)
             *reinterpret_cast<float2 *>(dq + nb * 8) = make_float2(acc[nb][2 * e] * p.scale, acc[nb][2 * e + 1] * p.scale);
     }
+    await_previous();  // whoever comes next waits for both kernels
 }
 
 // dk and dv of 64 keys; the first p.fars blocks: of the sinks, from the far pairs
@@ -542,6 +555,8 @@ win_dkv_kernel(WinParams p) {
     extern __shared__ __align__(16) uint2 sm[];
     uint2 *sk = sm, *sv = sk + ROWS * (D + 4), *sq = sv + ROWS * (D + 4), *sd = sq + COLS * (D + 4);
     float *wp = reinterpret_cast<float *>(sd + COLS * (D + 4)), *wd = wp + ROWS * WS;
+    await_previous();  // in this order: dq starts early and reads what this kernel waited for
+    let_next_start();
     const WinGeom &geo = p.geo;
     const bool far = blockIdx.x < p.fars;
     const int item = far ? blockIdx.x : blockIdx.x - p.fars, at = geo.by_hk.div(item), hk = item - at * geo.hk;
@@ -739,38 +754,37 @@ WinParams params(const WinPlan &p, const WinArgs &a) {
     return w;
 }
 template <typename... P>
-cudaError_t run(void (*kernel)(P...), std::atomic<uint64_t> &allowed, unsigned grid, size_t smem, cudaStream_t s, P... args) {
+cudaError_t run(void (*kernel)(P...), std::atomic<uint64_t> &allowed, unsigned grid, size_t smem, Launches &l, P... args) {
     KDA_TRY(allow_smem(kernel, smem, allowed));
-    kernel<<<grid, NT, smem, s>>>(args...);
-    return cudaGetLastError();
+    return l.next(kernel, grid, NT, smem, args...);
 }
 
 template <int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
     constexpr size_t smem = (ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
-    return run(win_forward_kernel<D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, params(p, a));
+    Launches l{s};
+    return run(win_forward_kernel<D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, l, params(p, a));
 }
 
 template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     WinParams w = params(p, a);
-    win_delta_kernel<T, D><<<(unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float), s>>>(
-        (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq);
-    KDA_TRY(cudaGetLastError());
+    Launches l{s};
+    KDA_TRY(l.next(win_delta_kernel<T, D>, (unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float),
+                   (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq));
     if constexpr (sizeof(T) == 2) {
         const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
-        win_first_delta_kernel<D><<<(unsigned)(blocks * a.hq), 128, 0, s>>>(w);
-        KDA_TRY(cudaGetLastError());
+        KDA_TRY(l.next(win_first_delta_kernel<D>, (unsigned)(blocks * a.hq), 128, 0, w));
     }
     const bool far = a.sinks > 0 && a.window < a.T;  // some sequence may be longer than the window
     if constexpr (sizeof(T) == 2) {
-        KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, s));
+        KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, l));
     } else {
         static std::atomic<uint64_t> allowed[2];
         constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
         w.fars = far ? p.geo.ntiles * 2 * a.hk : 0;
         KDA_TRY(run(win_dkv_kernel<D>, allowed[0], (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), smem + ROWS * WS * sizeof(float),
-                    s, w));
-        KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, s, w));
+                    l, w));
+        KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, l, w));
     }
     if (far)
         win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(

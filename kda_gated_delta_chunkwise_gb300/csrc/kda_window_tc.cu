@@ -573,6 +573,8 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    await_previous();
+    let_next_start();  // after the wait: the next kernel reads what this one waited for
     const uint32_t tmem = *tm, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
     const uint32_t bars = smem_u32(bar);
     auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
@@ -1137,6 +1139,7 @@ win_dq_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid_
     tc_fence_before();
     __syncthreads();
     settle(ab);
+    await_previous();  // whoever comes next waits for both kernels
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1175,7 +1178,7 @@ template <int D> cudaError_t forward(const WinGeom &geo, const WinArgs &a, cudaS
 
 template <int D>
 cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta, float *part, float *near,
-                     cudaStream_t s) {
+                     Launches &l) {
     CUtensorMap mq, mk, mv, mo, mk16, mv16;
     if (!token_map<D>(&mq, a.q, a.q_stride, a.hq, geo.tokens, 128) ||
         !token_map<D>(&mk, a.k, a.k_stride, a.hk, geo.tokens, 128) ||
@@ -1192,19 +1195,17 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
     BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, part, near,
              a.scale, a.scale * 1.4426950408889634f, fars, fars + geo.ntiles * 2 * geo.hk};
     const int sms = sm_count();
-    win_dkv_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, s>>>(p, mq, mk, mv, mo);
-    e = cudaGetLastError();
+    e = l.next(win_dkv_tc_kernel<D>, p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, p, mq, mk, mv, mo);
     if (e != cudaSuccess) return e;
     p.items = geo.ntiles * 2 * geo.hq;
-    win_dq_tc_kernel<D><<<p.items < sms ? p.items : sms, BW_THREADS, Bq<D>::SMEM, s>>>(p, mq, mk, mv, mo, mk16, mv16);
-    return cudaGetLastError();
+    return l.next(win_dq_tc_kernel<D>, p.items < sms ? p.items : sms, BW_THREADS, Bq<D>::SMEM, p, mq, mk, mv, mo, mk16, mv16);
 }
 
 }  // namespace
 
 cudaError_t launch_window_backward_tc(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta,
-                                      float *part, float *near, cudaStream_t s) {
-    return a.d == 128 ? backward<128>(geo, a, lse2, delta, part, near, s) : backward<64>(geo, a, lse2, delta, part, near, s);
+                                      float *part, float *near, Launches &l) {
+    return a.d == 128 ? backward<128>(geo, a, lse2, delta, part, near, l) : backward<64>(geo, a, lse2, delta, part, near, l);
 }
 
 cudaError_t launch_window_forward_tc(const WinGeom &geo, const WinArgs &a, cudaStream_t s) {
