@@ -62,8 +62,7 @@ def gated_norm_backward(x, gate, d_out, weight=None, *, norm: str = "rms", activ
     lib = load()
     index, n, h, d, code, xs, gs, nk, act = _gated_inputs(x, gate, weight, norm, activation)
     _plain(d_out, "d_out", x.dtype, index, x.shape)
-    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-           "dgate": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+    out = {"dx": torch.empty_like(d_out), "dgate": torch.empty_like(d_out),
            "dweight": None if weight is None else torch.empty_like(weight)}
     ws, size = (None, 0) if weight is None else _space(workspace, _gated_bytes(d), x)
     _check(lib, lib.kda_gated_norm_backward(x.data_ptr(), gate.data_ptr(), d_out.data_ptr(), code, xs, gs, _ptr(weight),
@@ -140,8 +139,8 @@ def residual_norm_backward(hidden, branch, d_out, d_hidden=None, weight=None, *,
         _plain(branch, "branch", d_out.dtype, index, hidden.shape)
     if d_hidden is not None:
         _plain(d_hidden, "d_hidden", hidden.dtype, index, hidden.shape)
-    out = {"d_residual": torch.empty(hidden.shape, dtype=hidden.dtype, device=hidden.device),
-           "d_branch": torch.empty(hidden.shape, dtype=d_out.dtype, device=hidden.device),
+    out = {"d_residual": torch.empty_like(hidden),
+           "d_branch": torch.empty_like(d_out),
            "dweight": None if weight is None else torch.empty_like(weight),
            "dbranch_weight": None if branch_weight is None else torch.empty_like(branch_weight),
            "dchannel_scale": None if channel_scale is None else torch.empty_like(channel_scale)}

@@ -556,8 +556,7 @@ def qk_norm_rope_axes_backward(q, k, dq_out, dk_out, positions, rope_table, pair
                                                                            (axes,))
     _plain(dq_out, "dq_out", q.dtype, index, q.shape)
     _plain(dk_out, "dk_out", q.dtype, index, k.shape)
-    out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-           "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
+    out = {"dq": torch.empty_like(dq_out), "dk": torch.empty_like(dk_out),
            "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
            "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
     ws, size = None, 0

@@ -96,7 +96,7 @@ def _backward(q, k, v, out, lse, d_o, cu_seqlens, window, sinks, scale, workspac
     _plain(out, "out", q.dtype, index, q.shape)
     _plain(lse, "lse", torch.float32, index, q.shape[:-1])
     _plain(d_o, "d_o", q.dtype, index, q.shape)
-    grads = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+    grads = {"dq": torch.empty_like(d_o),
              "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
              "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device)}
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_o.data_ptr(), _dtype_code(q),
