@@ -370,10 +370,13 @@ template <typename T, int D> cudaError_t decode(const WinCacheArgs &a, cudaStrea
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(win_decode_kernel<T, D>, smem, allowed);
     if (e != cudaSuccess) return e;
-    // CTAs of a cluster: until there are two for every SM or a warp has but one step left
+    // CTAs of a cluster: as many as still run all at once (two on an SM, less what does not come out even with the
+    // clusters' places: 75 sequences of one head in clusters of four, 300 CTAs, took 25.8 us, in pairs 19.5; 64 in
+    // clusters of four 20.2, of two 21.9), and a step for every warp. A second round costs more than longer
+    // stretches: 100 in clusters of four 38.8, in pairs 31.8.
     const int64_t work = (int64_t)a.N * a.hk;
     int cl = 1;
-    while (cl < 8 && work * cl < 2 * 152 && a.entries >= cl * 2 * DW * Shape<T, D>::KEYS) cl *= 2;
+    while (cl < 8 && work * cl * 2 <= 256 && a.entries >= cl * 2 * DW * Shape<T, D>::KEYS) cl *= 2;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = cl;
