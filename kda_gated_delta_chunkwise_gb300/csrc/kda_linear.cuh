@@ -103,6 +103,24 @@ struct Launches {
         return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
     }
     template <typename... P, typename... A>
+    cudaError_t next_clusters(void (*kernel)(P...), unsigned clusters, unsigned size, int threads, size_t smem, A &&...args) {
+        cudaLaunchAttribute attr[2]{};
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(clusters * size);
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = smem;
+        c.stream = stream;
+        c.attrs = attr;
+        c.numAttrs = first ? 1 : 2;
+        first = false;
+        return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+    }
+    template <typename... P, typename... A>
     cudaError_t whole(void (*kernel)(P...), dim3 grid, int threads, size_t smem, A &&...args) {
         first = false;
         kernel<<<grid, threads, smem, stream>>>(static_cast<P>(args)...);

@@ -15,6 +15,7 @@
 // 16 x 8 x 8.
 #include <math_constants.h>
 
+#include "kda_tc_ptx.cuh"
 #include "kda_window.cuh"
 #include "kda_window_tc.cuh"
 
@@ -105,7 +106,11 @@ __device__ __forceinline__ void add_product(float (&d)[4], const Frag &a, uint2 
     mma(z, a.hi, b0.y, b1.y);
     mma(z, a.hi, b0.x, b1.x);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) d[e] += z[e];
+    for (int e = 0; e < 4; e += 2) {
+        F2 sum;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(sum.v) : "l"(f2(d[e], d[e + 1]).v), "l"(f2(z[e], z[e + 1]).v));
+        f2_get(sum, d[e], d[e + 1]);
+    }
 }
 
 // 16 warps: four groups of 16 rows times four groups of columns (eight of a tile's
@@ -193,7 +198,7 @@ struct WinParams {
     float *lse;               // [tokens][hq], of the forward
     float *lse2, *delta;      // [hq][tokens], of the gradients: lse (bf16: in powers of two), D
     float *part, *near;       // gradients of the sinks, see win_far_sum_kernel
-    int fars;                 // blocks of far pairs, which come first
+    int fars, ranks;          // blocks of far pairs, which come first; CTAs to a block, which share its query heads
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -212,7 +217,7 @@ win_forward_kernel(WinParams p) {
     uint2 *sq = sm, *sk = sq + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
     float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
     const WinGeom &geo = p.geo;
-    const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
+    const int item = gridDim.x - 1 - blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
     const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
     if (rows <= 0) return;
@@ -474,7 +479,7 @@ win_dq_kernel(WinParams p) {
     uint2 *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
     float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
     const WinGeom &geo = p.geo;
-    const int item = blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
+    const int item = gridDim.x - 1 - blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
     const int i0 = tile.first + (at & 3) * ROWS, rows = min(ROWS, tile.len - i0);
     if (rows <= 0) {
@@ -558,8 +563,9 @@ win_dkv_kernel(WinParams p) {
     await_previous();  // in this order: dq starts early and reads what this kernel waited for
     let_next_start();
     const WinGeom &geo = p.geo;
-    const bool far = blockIdx.x < p.fars;
-    const int item = far ? blockIdx.x : blockIdx.x - p.fars, at = geo.by_hk.div(item), hk = item - at * geo.hk;
+    const int rank = blockIdx.x % p.ranks, block = blockIdx.x / p.ranks;
+    const bool far = block < p.fars;
+    const int item = far ? block : block - p.fars, at = geo.by_hk.div(item), hk = item - at * geo.hk;
     const WinTile tile = win_tile(geo, far ? at >> 1 : at >> 2);
     const int j0 = far ? (at & 1) * ROWS : tile.first + (at & 3) * ROWS;
     const int rows = min(ROWS, (far ? min(geo.sinks, tile.len) : tile.len) - j0);
@@ -596,8 +602,9 @@ win_dkv_kernel(WinParams p) {
             next_delta[e] = i < to ? p.delta[x] : 0.f;
         }
     };
-    const int h_end = (hk + 1) * geo.group;
-    int h = hk * geo.group, i0 = from;
+    const int heads = geo.group / p.ranks;
+    int h = hk * geo.group + rank * heads, i0 = from;
+    const int h_end = h + heads;
     if (from < to) fetch(h, i0);
     while (from < to && h < h_end) {
         __syncthreads();
@@ -631,12 +638,11 @@ win_dkv_kernel(WinParams p) {
         get_weights(f, wd, w);
         weights_by_rows<D>(ak, w, f, sq);
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = w.r0 + e * 8, j = j0 + r, c = w.group * (D / 4) + 2 * w.t;
-        if (r >= rows) continue;
+    // where row r of dk goes, and how far behind it that of dv lies
+    auto place = [&](int r, int c, float *&dk, float *&dv) {
+        const int j = j0 + r;
         const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D + c;
-        float *dk = (float *)p.dk + row, *dv = (float *)p.dv + row;
+        dk = (float *)p.dk + row, dv = (float *)p.dv + row;
         if (far) {
             dk = p.part + (((int64_t)win_far_slot(at >> 1, tile.seq, 1) * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
             dv = dk + (int64_t)geo.sinks * D;
@@ -644,12 +650,45 @@ win_dkv_kernel(WinParams p) {
             dk = p.near + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
             dv = dk + (int64_t)geo.sinks * D;
         }
+    };
+    float *own = reinterpret_cast<float *>(sm);  // [2][ROWS][D + 8]: this CTA's dk and dv, for the cluster
+    constexpr int OS = D + 8;
+    if (p.ranks > 1) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = w.r0 + e * 8, c = w.group * (D / 4) + 2 * w.t;
+        if (r >= rows) continue;
+        float *dk = own + r * OS + c, *dv = dk + ROWS * OS;
+        if (p.ranks == 1) place(r, c, dk, dv);
 #pragma unroll
         for (int nb = 0; nb < D / 32; ++nb) {
             *reinterpret_cast<float2 *>(dk + nb * 8) = make_float2(ak[nb][2 * e] * p.scale, ak[nb][2 * e + 1] * p.scale);
             *reinterpret_cast<float2 *>(dv + nb * 8) = make_float2(av[nb][2 * e], av[nb][2 * e + 1]);
         }
     }
+    if (p.ranks == 1) return;
+    tc::cluster_sync();
+    // each CTA adds up its share of the rows, in the order of the heads
+    const uint32_t mine = tc::smem_u32(own);
+    for (int x = rank * NT + threadIdx.x; x < rows * (D / 4); x += p.ranks * NT) {
+        const int r = x / (D / 4), c = x % (D / 4) * 4;
+        float *dst[2];
+        place(r, c, dst[0], dst[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < p.ranks; ++k) {
+                float4 y;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                             : "r"(tc::mapa(mine + ((u * ROWS + r) * OS + c) * 4, k))
+                             : "memory");
+                sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+            }
+            *reinterpret_cast<float4 *>(dst[u]) = sum;
+        }
+    }
+    tc::cluster_sync();  // nobody leaves while others read its rows
 }
 
 // dk and dv of the sinks that far queries see: `near` [N][hk][2][sinks][d], from
@@ -782,8 +821,14 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
         static std::atomic<uint64_t> allowed[2];
         constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
         w.fars = far ? p.geo.ntiles * 2 * a.hk : 0;
-        KDA_TRY(run(win_dkv_kernel<D>, allowed[0], (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), smem + ROWS * WS * sizeof(float),
-                    l, w));
+        // The query heads of a key head go to the CTAs of a cluster, or few key heads would leave most SMs idle. How
+        // many depends on the group alone: a sequence has the same bits in any batch.
+        w.ranks = 1;
+        for (int r = 2; r <= 5; ++r)
+            if (p.geo.group % r == 0) w.ranks = r;
+        const size_t bytes = smem + ROWS * WS * sizeof(float);
+        KDA_TRY(allow_smem(win_dkv_kernel<D>, bytes, allowed[0]));
+        KDA_TRY(l.next_clusters(win_dkv_kernel<D>, (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), w.ranks, NT, bytes, w));
         KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, l, w));
     }
     if (far)
