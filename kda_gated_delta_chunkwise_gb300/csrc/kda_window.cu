@@ -11,8 +11,8 @@
 // One CTA takes 64 rows (queries, or keys for dk and dv) and walks tiles of 32
 // columns in shared memory with the running maximum and sum of the softmax in
 // registers. The products run on mma.sync tf32, every operand split in two tf32
-// parts, three products for each. Bound by instructions: 13 for a product of
-// 16 x 8 x 8.
+// parts, three products for each. Bound by instructions (half of the issue slots) and their
+// latencies: 1474 tokens x 15 heads over 3 key heads, window 1227: 294 us, gradients 949.
 #include <math_constants.h>
 
 #include "kda_tc_ptx.cuh"
@@ -87,6 +87,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // An fp32 value in two tf32 parts, 22 bits.
 __device__ __forceinline__ uint2 split(float x) {
     const uint32_t hi = tf32(x);
@@ -101,8 +107,8 @@ struct Frag {
 // core truncates what it accumulates, fp32 sums round (carried on through four steps
 // a score was twice as far off).
 __device__ __forceinline__ void add_product(float (&d)[4], const Frag &a, uint2 b0, uint2 b1) {
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-    mma(z, a.lo, b0.x, b1.x);
+    float z[4];
+    mma_from_zero(z, a.lo, b0.x, b1.x);
     mma(z, a.hi, b0.y, b1.y);
     mma(z, a.hi, b0.x, b1.x);
 #pragma unroll
@@ -116,11 +122,18 @@ __device__ __forceinline__ void add_product(float (&d)[4], const Frag &a, uint2 
 // 16 warps: four groups of 16 rows times four groups of columns (eight of a tile's
 // 32, a quarter of d in the sums). Four warps of 16 rows and all columns were a
 // third as fast: one warp on a scheduler waits for its own products most of the time.
-constexpr int NT = 512, ROWS = 64, COLS = 32, WS = COLS + 4;  // WS: floats to a row of weights
+constexpr int NT = 512, ROWS = 64, COLS = 32, WS = COLS + 4, PS = COLS + 8;  // WS, PS: floats, pairs to a row of weights
 
-// Rows of a tile in shared memory, split once for all who read them, D + 4 pairs
+// Rows of a tile in shared memory, split once for all who read them, `S` pairs
 // apart. Rows past `rows` are zeros. In two steps, so that the next tile's loads
-// are on their way while this one is worked on.
+// are on their way while this one is worked on. The forward reads 16 bytes of two rows
+// at a time, RS apart in different banks, and for the weights' products rows VS apart,
+// where they are too; a tile that serves as both (in the gradients) is MS apart, read
+// 8 bytes at a time (16 at a time there: 979 us instead of 949 for the gradients of 1474 tokens of 15
+// heads, window 1227).
+template <int D> constexpr int RS = D + 8;
+template <int D> constexpr int VS = D + 2;
+template <int D> constexpr int MS = D + 4;
 template <int D, int N> struct TileLoad {
     static constexpr int PER = D / 4, COUNT = N * PER / NT;
     static_assert(N * PER % NT == 0, "whole rounds");
@@ -132,11 +145,11 @@ template <int D, int N> struct TileLoad {
             v[i] = r < rows ? *reinterpret_cast<const float4 *>(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-    __device__ __forceinline__ void store(uint2 *dst) const {
+    template <int S> __device__ __forceinline__ void store(uint2 *dst) const {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             const int r = (i * NT + threadIdx.x) / PER, c = (i * NT + threadIdx.x) % PER * 4;
-            uint4 *d = reinterpret_cast<uint4 *>(dst + r * (D + 4) + c);
+            uint4 *d = reinterpret_cast<uint4 *>(dst + r * S + c);
             const uint2 x = split(v[i].x), y = split(v[i].y), z = split(v[i].z), w = split(v[i].w);
             d[0] = make_uint4(x.x, x.y, y.x, y.y);
             d[1] = make_uint4(z.x, z.y, w.x, w.y);
@@ -149,30 +162,48 @@ struct Place {  // of a thread in the products
     // (few sinks) leave the others more of each
     int r0 = (warp >> 2) * 16 + g, group = warp & 3;
     __device__ __forceinline__ bool idle(int rows) const { return (warp >> 2) * 16 >= rows; }
+    __device__ __forceinline__ void meet() const {  // the four warps of the same rows
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp >> 2)) : "memory");
+    }
 };
-// acc = the products of this warp's 16 rows of `a` with its eight of b.
-template <int D> __device__ __forceinline__ void rows_by_rows(float (&acc)[4], const Place &w, const uint2 *a, const uint2 *b) {
+// acc = the products of this warp's 16 rows of `a` with its eight of b, S apart.
+template <int D, int S> __device__ __forceinline__ void rows_by_rows(float (&acc)[4], const Place &w, const uint2 *a, const uint2 *b) {
     acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-    const uint2 *a0 = a + w.r0 * (D + 4) + w.t, *b0 = b + (w.group * 8 + w.g) * (D + 4) + w.t;
+    const uint2 *a0 = a + w.r0 * S + w.t, *b0 = b + (w.group * 8 + w.g) * S + w.t;
 #pragma unroll 4
     for (int k = 0; k < D; k += 8) {
         Frag f;
         f.set(0, a0[k]);
-        f.set(1, a0[8 * (D + 4) + k]);
+        f.set(1, a0[8 * S + k]);
         f.set(2, a0[k + 4]);
-        f.set(3, a0[8 * (D + 4) + k + 4]);
+        f.set(3, a0[8 * S + k + 4]);
         add_product(acc, f, b0[k], b0[k + 4]);
     }
 }
-// acc[nb] += weights (this warp's 16 rows) times its quarter of the rows of b.
-// Columns 2 t and 2 t + 1 of the weights, which a lane reads at once, stand for k = t
-// and t + 4 of the product: a sum does not mind the order of its terms.
-template <int D> __device__ __forceinline__ void weights_by_rows(float (&acc)[D / 32][4], const Place &w, const Frag (&f)[COLS / 8], const uint2 *b) {
+// acc = the products of this warp's 16 rows of `a`, RS apart, with its eight of b, S
+// apart. Channels 2 t and 2 t + 1, which a lane reads at once, stand for k = t and
+// t + 4 of the product: a sum does not mind the order of its terms.
+template <int D, int S> __device__ __forceinline__ void rows_by_rows_16(float (&acc)[4], const Place &w, const uint2 *a, const uint2 *b) {
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    const uint2 *a0 = a + w.r0 * RS<D> + 2 * w.t, *b0 = b + (w.group * 8 + w.g) * S + 2 * w.t;
+#pragma unroll 4
+    for (int k = 0; k < D; k += 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(a0 + k), y = *reinterpret_cast<const uint4 *>(a0 + 8 * RS<D> + k),
+                    z = *reinterpret_cast<const uint4 *>(b0 + k);
+        Frag f;
+        f.set(0, make_uint2(x.x, x.y)), f.set(1, make_uint2(y.x, y.y));
+        f.set(2, make_uint2(x.z, x.w)), f.set(3, make_uint2(y.z, y.w));
+        add_product(acc, f, make_uint2(z.x, z.y), make_uint2(z.z, z.w));
+    }
+}
+// acc[nb] += weights (this warp's 16 rows) times its quarter of the rows of b, VS
+// apart; columns 2 t and 2 t + 1 of the weights for k = t and t + 4, as above.
+template <int D, int S> __device__ __forceinline__ void weights_by_rows(float (&acc)[D / 32][4], const Place &w, const Frag (&f)[COLS / 8], const uint2 *b) {
 #pragma unroll
     for (int kb = 0; kb < COLS / 8; ++kb) {
-        const uint2 *b0 = b + (kb * 8 + 2 * w.t) * (D + 4) + w.group * (D / 4) + w.g;
+        const uint2 *b0 = b + (kb * 8 + 2 * w.t) * S + w.group * (D / 4) + w.g;
 #pragma unroll
-        for (int nb = 0; nb < D / 32; ++nb) add_product(acc[nb], f[kb], b0[nb * 8], b0[D + 4 + nb * 8]);
+        for (int nb = 0; nb < D / 32; ++nb) add_product(acc[nb], f[kb], b0[nb * 8], b0[S + nb * 8]);
     }
 }
 __device__ __forceinline__ void put_weights(float *w, const Place &p, const float (&s)[4]) {
@@ -214,8 +245,9 @@ template <int D>
 __global__ void __launch_bounds__(NT)
 win_forward_kernel(WinParams p) {
     extern __shared__ __align__(16) uint2 sm[];
-    uint2 *sq = sm, *sk = sq + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
-    float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
+    uint2 *sq = sm, *sk = sq + ROWS * RS<D>, *sv = sk + COLS * RS<D>;
+    uint2 *ws = sv + COLS * VS<D>;                                // weights, split [ROWS][PS]
+    float *shared = reinterpret_cast<float *>(ws + ROWS * PS);  // [ROWS][4]: of the warps of the same rows
     const WinGeom &geo = p.geo;
     const int item = gridDim.x - 1 - blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
@@ -227,7 +259,7 @@ win_forward_kernel(WinParams p) {
     {
         TileLoad<D, ROWS> q;
         q.load((const float *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows);
-        q.store(sq);
+        q.template store<RS<D>>(sq);
     }
     TileLoad<D, COLS> nk, nv;
     float acc[D / 32][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
@@ -241,65 +273,70 @@ win_forward_kernel(WinParams p) {
         if (from < to) fetch(from);
         for (int j0 = from; j0 < to; j0 += COLS) {
             __syncthreads();
-            nk.store(sk);
-            nv.store(sv);
+            nk.template store<RS<D>>(sk);
+            nv.template store<VS<D>>(sv);
             __syncthreads();
             if (j0 + COLS < to) fetch(j0 + COLS);
-            if (!w.idle(rows)) {
-                float s[4];
-                rows_by_rows<D>(s, w, sq, sk);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = i0 + w.r0 + (e >> 1) * 8, j = j0 + w.group * 8 + 2 * w.t + (e & 1);
-                    s[e] = j < to && sees(i, j, geo.window, geo.sinks, far) ? s[e] * p.scale : -CUDART_INF_F;
-                }
-                put_weights(ws, w, s);
-            }
-            __syncthreads();
             if (w.idle(rows)) continue;
-            // every warp of the same rows makes their weights and sums, the same ones
-            Frag f[COLS / 8];
-            float x[2][COLS / 4];
-            float keep[2];
+            // a warp has eight of the tile's columns: it makes their weights with the rows' maximum over all four
+            float s[4], keep[2];
+            rows_by_rows_16<D, RS<D>>(s, w, sq, sk);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + w.r0 + (e >> 1) * 8, j = j0 + w.group * 8 + 2 * w.t + (e & 1);
+                s[e] = j < to && sees(i, j, geo.window, geo.sinks, far) ? s[e] * p.scale : -CUDART_INF_F;
+            }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float top = m[r];
-#pragma unroll
-                for (int k = 0; k < COLS / 8; ++k) {
-                    const float2 y = *reinterpret_cast<const float2 *>(ws + (w.r0 + 8 * r) * WS + k * 8 + 2 * w.t);
-                    x[r][2 * k] = y.x, x[r][2 * k + 1] = y.y;
-                    top = fmaxf(top, fmaxf(y.x, y.y));
-                }
+                float top = fmaxf(s[2 * r], s[2 * r + 1]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (w.t == 0) shared[(w.r0 + 8 * r) * 4 + w.group] = top;
+            }
+            w.meet();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float4 y = *reinterpret_cast<const float4 *>(shared + (w.r0 + 8 * r) * 4);
+                const float top = fmaxf(m[r], fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
                 keep[r] = top == -CUDART_INF_F ? 1.f : expf(m[r] - top);  // a row may see nothing of a tile
                 m[r] = top;
-                l[r] *= keep[r];
-#pragma unroll
-                for (int k = 0; k < COLS / 4; ++k) {
-                    x[r][k] = x[r][k] == -CUDART_INF_F ? 0.f : expf(x[r][k] - top);
-                    l[r] += x[r][k];
-                }
+                const float a = s[2 * r] == -CUDART_INF_F ? 0.f : expf(s[2 * r] - top),
+                            b = s[2 * r + 1] == -CUDART_INF_F ? 0.f : expf(s[2 * r + 1] - top);
+                l[r] = fmaf(l[r], keep[r], a + b);  // of this lane's columns
+                const uint2 x = split(a), z = split(b);
+                *reinterpret_cast<uint4 *>(ws + (w.r0 + 8 * r) * PS + w.group * 8 + 2 * w.t) = make_uint4(x.x, x.y, z.x, z.y);
             }
+            w.meet();
+            Frag f[COLS / 8];
 #pragma unroll
             for (int k = 0; k < COLS / 8; ++k) {
-                f[k].set(0, split(x[0][2 * k])), f[k].set(1, split(x[1][2 * k]));
-                f[k].set(2, split(x[0][2 * k + 1])), f[k].set(3, split(x[1][2 * k + 1]));
+                const uint4 x = *reinterpret_cast<const uint4 *>(ws + w.r0 * PS + k * 8 + 2 * w.t),
+                            y = *reinterpret_cast<const uint4 *>(ws + (w.r0 + 8) * PS + k * 8 + 2 * w.t);
+                f[k].set(0, make_uint2(x.x, x.y)), f[k].set(1, make_uint2(y.x, y.y));
+                f[k].set(2, make_uint2(x.z, x.w)), f[k].set(3, make_uint2(y.z, y.w));
             }
 #pragma unroll
             for (int nb = 0; nb < D / 32; ++nb) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nb][e] *= keep[e >> 1];
             }
-            weights_by_rows<D>(acc, w, f, sv);
+            weights_by_rows<D, VS<D>>(acc, w, f, sv);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
     walk(max(0, i0 - geo.window + 1), i0 + rows, false);
+    w.meet();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        if (w.t == 0) shared[(w.r0 + 8 * e) * 4 + w.group] = l[e];
+    }
+    w.meet();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float4 y = *reinterpret_cast<const float4 *>(shared + (w.r0 + 8 * e) * 4);
+        l[e] = (y.x + y.y) + (y.z + y.w);
         const int r = w.r0 + e * 8;
         if (r >= rows) continue;
         const int64_t row = (int64_t)(tile.start + i0 + r) * geo.hq + h;
@@ -476,8 +513,8 @@ template <int D>
 __global__ void __launch_bounds__(NT)
 win_dq_kernel(WinParams p) {
     extern __shared__ __align__(16) uint2 sm[];
-    uint2 *sq = sm, *sd = sq + ROWS * (D + 4), *sk = sd + ROWS * (D + 4), *sv = sk + COLS * (D + 4);
-    float *ws = reinterpret_cast<float *>(sv + COLS * (D + 4));
+    uint2 *sq = sm, *sd = sq + ROWS * MS<D>, *sv = sd + ROWS * MS<D>, *sk = sv + COLS * MS<D>;
+    float *ws = reinterpret_cast<float *>(sk + COLS * MS<D>);
     const WinGeom &geo = p.geo;
     const int item = gridDim.x - 1 - blockIdx.x, at = geo.by_hq.div(item), h = item - at * geo.hq, hk = h / geo.group;
     const WinTile tile = win_tile(geo, at >> 2);
@@ -494,8 +531,8 @@ win_dq_kernel(WinParams p) {
         TileLoad<D, ROWS> q, d;
         q.load((const float *)p.q + (int64_t)(tile.start + i0) * p.q_stride + h * D, p.q_stride, rows);
         d.load((const float *)p.d_o + row0 * D, (int64_t)geo.hq * D, rows);
-        q.store(sq);
-        d.store(sd);
+        q.template store<MS<D>>(sq);
+        d.template store<MS<D>>(sd);
     }
     TileLoad<D, COLS> nk, nv;
     float acc[D / 32][4], lse[2], delta[2];
@@ -515,14 +552,14 @@ win_dq_kernel(WinParams p) {
         if (from < to) fetch(from);
         for (int j0 = from; j0 < to; j0 += COLS) {
             __syncthreads();
-            nk.store(sk);
-            nv.store(sv);
+            nk.template store<MS<D>>(sk);
+            nv.template store<MS<D>>(sv);
             __syncthreads();
             if (j0 + COLS < to) fetch(j0 + COLS);
             if (!w.idle(rows)) {
                 float s[4], dp[4];
-                rows_by_rows<D>(s, w, sq, sk);
-                rows_by_rows<D>(dp, w, sd, sv);
+                rows_by_rows<D, MS<D>>(s, w, sq, sk);
+                rows_by_rows<D, MS<D>>(dp, w, sd, sv);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + w.r0 + (e >> 1) * 8, j = j0 + w.group * 8 + 2 * w.t + (e & 1);
@@ -535,7 +572,7 @@ win_dq_kernel(WinParams p) {
             if (w.idle(rows)) continue;
             Frag f[COLS / 8];
             get_weights(f, ws, w);
-            weights_by_rows<D>(acc, w, f, sk);
+            weights_by_rows<D, MS<D>>(acc, w, f, sk);
         }
     };
     if (i0 + rows > geo.window) walk(0, min(geo.sinks, i0 + rows - geo.window), true);
@@ -558,8 +595,8 @@ template <int D>
 __global__ void __launch_bounds__(NT)
 win_dkv_kernel(WinParams p) {
     extern __shared__ __align__(16) uint2 sm[];
-    uint2 *sk = sm, *sv = sk + ROWS * (D + 4), *sq = sv + ROWS * (D + 4), *sd = sq + COLS * (D + 4);
-    float *wp = reinterpret_cast<float *>(sd + COLS * (D + 4)), *wd = wp + ROWS * WS;
+    uint2 *sk = sm, *sv = sk + ROWS * MS<D>, *sq = sv + ROWS * MS<D>, *sd = sq + COLS * MS<D>;
+    float *wp = reinterpret_cast<float *>(sd + COLS * MS<D>), *wd = wp + ROWS * WS;
     await_previous();  // in this order: dq starts early and reads what this kernel waited for
     let_next_start();
     const WinGeom &geo = p.geo;
@@ -578,8 +615,8 @@ win_dkv_kernel(WinParams p) {
         TileLoad<D, ROWS> k, v;
         k.load((const float *)p.k + (int64_t)(tile.start + j0) * p.k_stride + hk * D, p.k_stride, rows);
         v.load((const float *)p.v + (int64_t)(tile.start + j0) * p.v_stride + hk * D, p.v_stride, rows);
-        k.store(sk);
-        v.store(sv);
+        k.template store<MS<D>>(sk);
+        v.template store<MS<D>>(sv);
     }
     TileLoad<D, COLS> nq, nd;
     float lse[2], delta[2];  // of the step's queries in this thread's columns, and of the next step's
@@ -608,8 +645,8 @@ win_dkv_kernel(WinParams p) {
     if (from < to) fetch(h, i0);
     while (from < to && h < h_end) {
         __syncthreads();
-        nq.store(sq);
-        nd.store(sd);
+        nq.template store<MS<D>>(sq);
+        nd.template store<MS<D>>(sd);
 #pragma unroll
         for (int e = 0; e < 2; ++e) lse[e] = next_lse[e], delta[e] = next_delta[e];
         __syncthreads();
@@ -618,8 +655,8 @@ win_dkv_kernel(WinParams p) {
         if (h < h_end) fetch(h, i0);
         if (!w.idle(rows)) {
             float s[4], dp[4];
-            rows_by_rows<D>(s, w, sk, sq);
-            rows_by_rows<D>(dp, w, sv, sd);
+            rows_by_rows<D, MS<D>>(s, w, sk, sq);
+            rows_by_rows<D, MS<D>>(dp, w, sv, sd);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = w.r0 + (e >> 1) * 8, i = i_now + w.group * 8 + 2 * w.t + (e & 1);
@@ -634,9 +671,9 @@ win_dkv_kernel(WinParams p) {
         if (w.idle(rows)) continue;
         Frag f[COLS / 8];
         get_weights(f, wp, w);
-        weights_by_rows<D>(av, w, f, sd);
+        weights_by_rows<D, MS<D>>(av, w, f, sd);
         get_weights(f, wd, w);
-        weights_by_rows<D>(ak, w, f, sq);
+        weights_by_rows<D, MS<D>>(ak, w, f, sq);
     }
     // where row r of dk goes, and how far behind it that of dv lies
     auto place = [&](int r, int c, float *&dk, float *&dv) {
@@ -800,7 +837,7 @@ cudaError_t run(void (*kernel)(P...), std::atomic<uint64_t> &allowed, unsigned g
 
 template <int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    constexpr size_t smem = (ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
+    constexpr size_t smem = ((ROWS + COLS) * RS<D> + COLS * VS<D> + ROWS * PS) * sizeof(uint2) + ROWS * 4 * sizeof(float);
     Launches l{s};
     return run(win_forward_kernel<D>, allowed, (unsigned)(p.geo.ntiles * 4 * a.hq), smem, l, params(p, a));
 }
@@ -819,17 +856,18 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
         KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, l));
     } else {
         static std::atomic<uint64_t> allowed[2];
-        constexpr size_t smem = (2 * ROWS + 2 * COLS) * (D + 4) * sizeof(uint2) + ROWS * WS * sizeof(float);
+        constexpr size_t weights = ROWS * WS * sizeof(float);
+        constexpr size_t dq = (2 * ROWS + 2 * COLS) * MS<D> * sizeof(uint2) + weights, dkv = dq + weights;
+        static_assert(dkv <= 232448 && dq <= 232448 && 2 * ROWS * (D + 8) * sizeof(float) <= dkv, "shared memory of a block");
         w.fars = far ? p.geo.ntiles * 2 * a.hk : 0;
         // The query heads of a key head go to the CTAs of a cluster, or few key heads would leave most SMs idle. How
         // many depends on the group alone: a sequence has the same bits in any batch.
         w.ranks = 1;
         for (int r = 2; r <= 5; ++r)
             if (p.geo.group % r == 0) w.ranks = r;
-        const size_t bytes = smem + ROWS * WS * sizeof(float);
-        KDA_TRY(allow_smem(win_dkv_kernel<D>, bytes, allowed[0]));
-        KDA_TRY(l.next_clusters(win_dkv_kernel<D>, (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), w.ranks, NT, bytes, w));
-        KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), smem, l, w));
+        KDA_TRY(allow_smem(win_dkv_kernel<D>, dkv, allowed[0]));
+        KDA_TRY(l.next_clusters(win_dkv_kernel<D>, (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), w.ranks, NT, dkv, w));
+        KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), dq, l, w));
     }
     if (far)
         win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(
