@@ -782,8 +782,9 @@ size_t kda_residual_norm_backward_workspace_bytes(int D);
  * outputs are contiguous. Two calls on the same inputs give the same bits, and a
  * sequence the same ones alone and in a packed batch. fp32 calls are accurate to
  * fp32 (relative 2-norm below 1e-5); in bf16 calls the weights e^{s - lse} (and the
- * ds of the gradients) are rounded to bf16 as operands, which stays below the
- * result's own rounding. Scores are numbers of fp32's range. An infinity or a
+ * ds of the gradients) are rounded to bf16 as operands, which adds about as much as
+ * the result's own rounding. Scores are numbers of fp32's range. At most 1024 query
+ * heads and 2^30 tokens. An infinity or a
  * NaN in a token's k or v may reach tokens of its own sequence that do not see it
  * (the products multiply it by zero), but no other sequence or key head.
  */
@@ -847,7 +848,7 @@ size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, 
  * kda_window_cache_write - keys and values of N packed prompts, from position 0
  * on: of each the first `sinks` and the last `window` tokens go into its slot;
  * the entries that it has no tokens for are left as they are. A bad cu_seqlens
- * sets KDA_DEV_BAD_CU_SEQLENS and nothing is written.
+ * sets KDA_DEV_BAD_CU_SEQLENS and nothing is written. At most 65535 prompts.
  */
 kda_status_t kda_window_cache_write(const void *k, const void *v, kda_dtype_t dtype, int64_t k_stride, int64_t v_stride,
                                     const int32_t *cu_seqlens, const int32_t *slots, int sinks, void *k_cache,

@@ -71,8 +71,8 @@ def window_attention(q, k, v, *, window: int, sinks: int = 0, scale: float | Non
     i - j < window or j < sinks.
 
     q: [B, T, H_q, d]; k, v: [B, T, H_k, d] (bf16 or fp32, the same type; d 64 or
-    128); query head h reads key head h // (H_q // H_k). scale: d ** -0.5 by
-    default. Returns (o [B, T, H_q, d] in q's type, lse [B, T, H_q] fp32: the
+    128); query head h reads key head h // (H_q // H_k). scale: positive,
+    d ** -0.5 by default. Returns (o [B, T, H_q, d] in q's type, lse [B, T, H_q] fp32: the
     natural logarithm of the sum of e^score, which the gradients want)."""
     return _attention(q, k, v, None, window, sinks, scale, out, lse, None, None)
 

@@ -15,7 +15,9 @@
 //
 // Bound by memory, each input read once and each output written once. Sums and
 // everything in between are fp32; the only rounding to fewer bits is the store
-// (y is made from the unrounded h). Sums over rows have a fixed order.
+// (y is made from the unrounded h). Sums over rows have a fixed order. 16384 rows of
+// 16 x 128 bf16 channels, as calls one after the other: gated 34.5 us (5.8 TB/s), its
+// gradients 66 (5.1); residual with a stream in fp32 66 (6.1), its gradients 101 (6.0).
 #include <type_traits>
 
 #include "kda_block_norm.cuh"
@@ -351,8 +353,10 @@ kda_residual_norm_kernel(ResidualArgs p, int tr) {
 
 // Persistent: the threads of a row walk the rows with a fixed stride and keep the
 // sums over them in registers. A row's inputs come as bulk copies into a ring of
-// its threads; while a row's gradients are made, the sums of the next one are
-// added up, and one barrier a row serves its totals and the ring. A row that fills
+// its threads (copied by the threads themselves, 16 bytes at a time, 16384 rows of
+// 2048 with a stream in fp32 took 137 us instead of 101); while a row's gradients are
+// made, the sums of the next one are added up, and one barrier a row serves its
+// totals and the ring. A row that fills
 // the ring by itself stays in registers, and the next one comes meanwhile.
 constexpr int RT = 512;
 template <typename S, typename T, int V> struct ResidualRing {

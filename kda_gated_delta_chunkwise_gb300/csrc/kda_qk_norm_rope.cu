@@ -21,7 +21,9 @@
 // with A and B made once per token. Sums, norms and the rotation are in fp32;
 // the only rounding to fewer bits is the store. 16384 tokens x (16 + 16) heads
 // of 128 bf16 channels: forward 51.3 us (5.3 TB/s, 78 % of a copy), backward with
-// both weights' gradients 81.3 (5.0 TB/s, 74 %), the last sum (8-10 us on cold caches) included.
+// both weights' gradients 79 (5.1 TB/s, 76 %), the last sum included. With positions
+// of three axes: in blocks of four pairs (16 bytes of the table at a time) 61 and 81,
+// in turn over the pairs (4 bytes at a time) 66 and 85.
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
 #include "kda_rows.cuh"

@@ -22,6 +22,14 @@ CASE is one of:
   linear_decode_256x32       one token of it for 256 sequences x 32 heads
   norm_rope_65536x16  norm and rotary positions of 65,536 tokens, 16 + 16 heads,
                       d = 128, bf16, and their gradients
+  window_4x16x4096    attention over a window of 1024 tokens and 4 sinks, the benchmark's batch
+  window_backward_4x16x4096  its gradients
+  window_fp32_2x15x1474      both in fp32, five query heads to a key head
+  window_decode_256x32       one token of it for 256 sequences, 32 heads over 8 key heads,
+                      a window of 2048
+  block_norms_16384x16       rotary positions of three axes, the gated head norm and
+                      the residual norm of 16,384 tokens, 16 heads of 128 bf16
+                      channels, a stream in fp32, and their gradients
   hostlink            no kernel: the host link's copy rates (page-locked host
                       memory to the device, back, and both at once), printed
 
@@ -35,7 +43,9 @@ import argparse
 import torch
 
 from . import _binding as kda
+from . import _block as block
 from . import _linear as linear
+from . import _window as window
 from . import workloads as W
 
 
@@ -206,7 +216,50 @@ def _norm_rope(tokens: int, heads: int, reps: int):
     torch.cuda.synchronize()
 
 
+def _window(B: int, T: int, hq: int, hk: int, W: int, back: bool, reps: int, dtype=torch.bfloat16):
+    q, d_o = (torch.randn(B, T, hq, 128, device="cuda").to(dtype) for _ in range(2))
+    k, v = (torch.randn(B, T, hk, 128, device="cuda").to(dtype) for _ in range(2))
+    for _ in range(reps):
+        o, lse = window.window_attention(q, k, v, window=W, sinks=4)
+        if back:
+            window.window_attention_backward(q, k, v, o, lse, d_o, window=W, sinks=4)
+    torch.cuda.synchronize()
+
+
+def _window_decode(N: int, reps: int):
+    q = torch.randn(N, 32, 128, device="cuda").bfloat16()
+    k, v = (torch.randn(N, 8, 128, device="cuda").bfloat16() for _ in range(2))
+    caches = [torch.randn(N, 2052, 8, 128, device="cuda").bfloat16() for _ in range(2)]
+    slots = torch.arange(N, dtype=torch.int32, device="cuda")
+    for _ in range(reps):
+        window.window_decode_step(q, k, v, *caches, slots, slots + 3000, sinks=4)
+    torch.cuda.synchronize()
+
+
+def _block_norms(tokens: int, heads: int, reps: int):
+    q, k, g, dy = (torch.randn(tokens, heads, 128, device="cuda").bfloat16() for _ in range(4))
+    x, dh = (torch.randn(tokens, heads * 128, device="cuda") for _ in range(2))
+    w, wd = torch.ones(128, device="cuda"), torch.ones(heads * 128, device="cuda")
+    table = linear.rope_table(4096, 128)
+    pos = (torch.arange(tokens, dtype=torch.int32, device="cuda") % 4096).expand(3, -1).contiguous()
+    axis = tuple(i % 3 for i in range(64))
+    kw = dict(branch_norm="rms", branch_weight=wd, channel_scale=wd)
+    for _ in range(reps):
+        linear.qk_norm_rope_axes(q, k, pos, table, axis, w, w)
+        linear.qk_norm_rope_axes_backward(q, k, g, dy, pos, table, axis, w, w)
+        b = block.gated_norm(q, g, w).view(tokens, -1)
+        block.gated_norm_backward(q, g, dy, w)
+        h, _ = block.residual_norm(x, b, wd, **kw)
+        block.residual_norm_backward(h, b, dy.view(tokens, -1), dh, wd, **kw)
+    torch.cuda.synchronize()
+
+
 CASES = {
+    "window_4x16x4096": lambda r: _window(4, 4096, 16, 16, 1024, False, r),
+    "window_backward_4x16x4096": lambda r: _window(4, 4096, 16, 16, 1024, True, r),
+    "window_fp32_2x15x1474": lambda r: _window(2, 1474, 15, 3, 1227, True, r, torch.float32),
+    "window_decode_256x32": lambda r: _window_decode(256, r),
+    "block_norms_16384x16": lambda r: _block_norms(16384, 16, r),
     "linear_4x16x4096": lambda r: _linear(4, 4096, 16, False, r),
     "linear_1x32x131072": lambda r: _linear(1, 131072, 32, False, r),
     "linear_backward_4x16x4096": lambda r: _linear(4, 4096, 16, True, r),
