@@ -848,7 +848,7 @@ size_t kda_window_varlen_attention_backward_workspace_bytes(int N, int T_total, 
  * kda_window_cache_write - keys and values of N packed prompts, from position 0
  * on: of each the first `sinks` and the last `window` tokens go into its slot;
  * the entries that it has no tokens for are left as they are. A bad cu_seqlens
- * sets KDA_DEV_BAD_CU_SEQLENS and nothing is written. At most 65535 prompts.
+ * sets KDA_DEV_BAD_CU_SEQLENS and nothing is written. At most 65535 prompts and 1024 heads.
  */
 kda_status_t kda_window_cache_write(const void *k, const void *v, kda_dtype_t dtype, int64_t k_stride, int64_t v_stride,
                                     const int32_t *cu_seqlens, const int32_t *slots, int sinks, void *k_cache,
@@ -861,7 +861,7 @@ kda_status_t kda_window_cache_write(const void *k, const void *v, kda_dtype_t dt
  * written to their entry, and q [N, H_q, d] attends over the entries that hold
  * tokens, this one's included (o [N, H_q, d]). Entries without a token are not
  * read. A negative position leaves its sequence out and sets
- * KDA_DEV_BAD_POSITION. The strides are between sequences.
+ * KDA_DEV_BAD_POSITION. The strides are between sequences. At most 1024 query heads.
  */
 kda_status_t kda_window_decode_step(const void *q, const void *k, const void *v, kda_dtype_t dtype, int64_t q_stride,
                                     int64_t k_stride, int64_t v_stride, float scale, int sinks, void *k_cache,

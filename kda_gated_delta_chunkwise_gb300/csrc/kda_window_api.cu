@@ -92,6 +92,7 @@ kda_status_t cache(WinCacheArgs &a) {
     if (a.entries <= a.sinks)
         return fail(KDA_ERR_INVALID_ARG, "a slot must have more entries than sinks (got %d, %d)", a.entries, a.sinks);
     if (a.pool <= 0) return fail(KDA_ERR_INVALID_ARG, "pool_size must be positive");
+    if (a.hq > 1024) return fail(KDA_ERR_UNSUPPORTED, "1024 query heads at most (got %d)", a.hq);
     KDA_CHECK(maybe(a.status, "device_status", 4));
     return KDA_OK;
 }
