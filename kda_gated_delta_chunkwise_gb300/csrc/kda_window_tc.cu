@@ -117,7 +117,7 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16 *first, int64_t stride,
 // only when a row's maximum has grown by more than 2^8 since the last time, and
 // then waits for PV of the step before: the weights are taken against the older
 // maximum until then, up to 2^8, which fp32 sums and bf16 weights carry as well.
-// That case takes 120 us (1.0 PFLOP/s, 52 % of the cuBLAS rate), 65,531 packed
+// That case takes 120 us (1.0 PFLOP/s, 52 % of the measured rate of a large product), 65,531 packed
 // tokens of 32 heads over 8 key heads, window 2048, 1.40 ms (1.23, 63 %): bound by
 // the softmax of a step and the item's start and end, in turn with the products.
 //
