@@ -506,17 +506,15 @@ def _axes(pair_axis, positions, table):
         raise ValueError("positions and rope_table are required")
     if table.dim() != 2 or positions.dim() < 1:
         raise ValueError("rope_table must be [max_position, rotary] and positions [axes, ..]")
-    pairs, axes = _pair_axes(pair_axis if isinstance(pair_axis, (tuple, bytes)) else tuple(pair_axis)), positions.shape[0]
+    try:
+        pairs = pair_axis if type(pair_axis) is bytes else \
+            bytes(pair_axis if isinstance(pair_axis, (list, tuple)) else tuple(pair_axis))
+    except ValueError:
+        raise ValueError("pair_axis must hold axes, 0 <= a < positions.shape[0]") from None
+    axes = positions.shape[0]
     if len(pairs) != table.shape[1] // 2:
         raise ValueError(f"pair_axis must have {table.shape[1] // 2} entries, one for every channel pair, got {len(pairs)}")
     return axes, pairs
-
-
-@functools.lru_cache(maxsize=64)
-def _pair_axes(pair_axis) -> bytes:
-    if any(not 0 <= a <= 255 for a in pair_axis):
-        raise ValueError("pair_axis must hold axes, 0 <= a < positions.shape[0]")
-    return bytes(pair_axis)
 
 
 @_on_stream
