@@ -86,15 +86,17 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool there)
 // block, so that loads are whole lines and most are on their way at once; then a
 // warp adds up a column's 32 sums.
 namespace {
-__global__ void __launch_bounds__(1024)
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
 kda_column_sum_kernel(const float *partial, int blocks, int D, float *d0, float *d1, float *d2) {
-    __shared__ float red[32][33];
+    static_assert(WARPS == 32, "a warp adds up a column's sums");
+    __shared__ float red[WARPS][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, s = blockIdx.y;
     after_previous();
     float a = 0.f;
     if (c < D) {
 #pragma unroll 10
-        for (int b = warp; b < blocks; b += 32) a += partial[((int64_t)b * gridDim.y + s) * D + c];
+        for (int b = warp; b < blocks; b += WARPS) a += partial[((int64_t)b * gridDim.y + s) * D + c];
     }
     red[warp][lane] = a;
     __syncthreads();
@@ -104,7 +106,7 @@ kda_column_sum_kernel(const float *partial, int blocks, int D, float *d0, float 
 }
 inline cudaError_t column_sum(Launches &l, const float *partial, int blocks, int D, int sets, float *d0,
                               float *d1 = nullptr, float *d2 = nullptr) {
-    return l.next(kda_column_sum_kernel, dim3((D + 31) / 32, sets), 1024, 0, partial, blocks, D, d0, d1, d2);
+    return l.next(kda_column_sum_kernel<32>, dim3((D + 31) / 32, sets), 1024, 0, partial, blocks, D, d0, d1, d2);
 }
 }  // namespace
 

@@ -16,10 +16,13 @@
 // lane reads 16 bytes of consecutive channels and the query's fragments are read
 // the same way; for the values' product a lane holds the entries and channels that
 // its fragments want, two entries' halves joined by a byte permutation. That case takes
-// 304 us (7.1 TB/s); fp32, whose products are three of
-// split tf32, half the rate. Few sequences are cut over the CTAs of a cluster, whose sums are joined
+// 304 us (7.1 TB/s). fp32 calls of up to eight heads to a key head go another way (see
+// FourHeads): 256 sequences, 16 heads over 4, 3000 entries 450 us (7.0 TB/s), by split tf32
+// 780; 8 over 1 153 and 219; of 16 over 2, which stay there, 451 (3.5). Few sequences are cut over the CTAs of a cluster, whose sums are joined
 // through distributed shared memory in rank order.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "kda_rows.cuh"
 #include "kda_tc_ptx.cuh"
@@ -124,7 +127,87 @@ template <typename T, int D> struct Shape {
     static __device__ __forceinline__ int v_at(int row, int piece) { return (KEYS + row) * ROW + ((piece ^ (row & 7)) << 4); }
 };
 
-template <typename T, int D>
+// fp32 and up to eight query heads to a key head: fp32 products, four heads at a
+// time. A row is 16 bytes in each of D / 4 lanes; the sums of a step's eight entries
+// and four heads are shared out among the lanes while they are added up, one to a lane.
+template <int D> struct FourHeads {
+    static constexpr int L = D / 4, R = 32 / L, ROWS = 8 / R;  // lanes of a row, rows at a time, times
+    F2 q[4][2], acc[4][2];
+    float m, l;  // of head lane % 4; l: of this lane's entries
+    __device__ __forceinline__ void load(const float *src, int heads, int lane) {
+        m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const float4 x = h < heads ? *reinterpret_cast<const float4 *>(src + h * D + lane % L * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            q[h][0] = f2(x.x, x.y), q[h][1] = f2(x.z, x.w);
+            acc[h][0] = acc[h][1] = f2(0.f, 0.f);
+        }
+    }
+    // the entries' keys at k(row), values at v(row); `there` entries; c2: the scale in powers of two
+    template <typename K, typename V> __device__ __forceinline__ void step(K k, V v, int there, float c2, int lane) {
+        const int sub = lane / L;
+        float s[4 * ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float4 x = k(i * R + sub);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) s[4 * i + h] = f2_sum(fma2(f2(x.z, x.w), q[h][1], f2(x.x, x.y) * q[h][0]));
+        }
+#pragma unroll
+        for (int n = 2 * ROWS, bit = L / 2; bit > 0; n >>= 1, bit >>= 1) {
+            const bool up = lane & bit;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float give = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+                s[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+            }
+        }
+        const float x = lane % L / 4 * R + sub < there ? s[0] * c2 : -CUDART_INF_F;  // of that entry
+        float top = fmaxf(m, x);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float scale = exp2_approx(m - top), w = exp2_approx(x - top);
+        l = fmaf(l, scale, w);
+        if (__any_sync(0xffffffffu, top != m)) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float f = __shfl_sync(0xffffffffu, scale, h);
+                acc[h][0] = acc[h][0] * f2(f, f), acc[h][1] = acc[h][1] * f2(f, f);
+            }
+        }
+        m = top;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float4 y = v(i * R + sub);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float f = __shfl_sync(0xffffffffu, w, sub * L + 4 * i + h);
+                acc[h][0] = fma2(f2(f, f), f2(y.x, y.y), acc[h][0]);
+                acc[h][1] = fma2(f2(f, f), f2(y.z, y.w), acc[h][1]);
+            }
+        }
+    }
+    // the warp's sums: [4][D], and of each head its maximum and sum
+    __device__ __forceinline__ void store(float *part, float *stat, int heads, int lane) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane < 4 && lane < heads) stat[2 * lane] = m, stat[2 * lane + 1] = l;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            float a[4];
+            f2_get(acc[h][0], a[0], a[1]);
+            f2_get(acc[h][1], a[2], a[3]);
+            if (R == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], 16);
+            }
+            if (h < heads && lane < L) *reinterpret_cast<float4 *>(part + h * D + lane * 4) = make_float4(a[0], a[1], a[2], a[3]);
+        }
+    }
+};
+
+// QUADS: of fp32, fours of query heads that go the way above; 0: mma.sync
+template <typename T, int D, int QUADS>
 __global__ void __launch_bounds__(DT, 2)
 win_decode_kernel(WinCacheArgs p, int cl) {
     using S = Shape<T, D>;
@@ -163,13 +246,19 @@ win_decode_kernel(WinCacheArgs p, int cl) {
     for (int h0 = 0; h0 < group; h0 += HEADS) {
         const int heads = min(HEADS, group - h0);
         const T *q = (const T *)p.q + n * p.q_stride + (int64_t)(hk * group + h0) * D;
+        FourHeads<D> four[QUADS > 0 ? QUADS : 1];
         uint4 qf[2][KC];  // rows g and g + 8
+        if constexpr (QUADS > 0) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+            for (int u = 0; u < QUADS; ++u) four[u].load((const float *)q + 4 * u * D, heads - 4 * u, lane);
+        } else {
 #pragma unroll
-            for (int j = 0; j < KC; ++j)
-                qf[r][j] = g + r * 8 < heads ? *reinterpret_cast<const uint4 *>(q + (g + r * 8) * D + 4 * CH * j + CH * t)
-                                             : make_uint4(0u, 0u, 0u, 0u);
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    qf[r][j] = g + r * 8 < heads ? *reinterpret_cast<const uint4 *>(q + (g + r * 8) * D + 4 * CH * j + CH * t)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         float acc[D / 8][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -201,122 +290,136 @@ win_decode_kernel(WinCacheArgs p, int cl) {
             __syncwarp();
             const unsigned char *buf = ring + stage * S::STAGE;
             stage = stage == S::STAGES - 1 ? 0 : stage + 1;
-            uint4 vf[VR][VC];
-            float s[NB][4];
+            if constexpr (QUADS > 0) {
+                const int piece = lane % FourHeads<D>::L;
+                auto k = [&](int row) { return *reinterpret_cast<const float4 *>(buf + S::k_at(row, piece)); };
+                auto v = [&](int row) { return *reinterpret_cast<const float4 *>(buf + S::v_at(row, piece)); };
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
-#pragma unroll
-                for (int j = 0; j < KC; ++j) {
-                    const uint4 x = qf[0][j], y = qf[1][j];
-                    const uint4 k = *reinterpret_cast<const uint4 *>(buf + S::k_at(b * 8 + g, 4 * j + t));
-                    if constexpr (sizeof(T) == 2) {
-                        mma_bf16(s[b], x.x, y.x, x.y, y.y, k.x, k.y);
-                        mma_bf16(s[b], x.z, y.z, x.w, y.w, k.z, k.w);
-                    } else {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        const float a0[4] = {__uint_as_float(x.x), __uint_as_float(y.x), __uint_as_float(x.y), __uint_as_float(y.y)};
-                        const float a1[4] = {__uint_as_float(x.z), __uint_as_float(y.z), __uint_as_float(x.w), __uint_as_float(y.w)};
-                        mma_fp32(d, a0, __uint_as_float(k.x), __uint_as_float(k.y));
-                        mma_fp32(d, a1, __uint_as_float(k.z), __uint_as_float(k.w));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[b][e] += d[e];
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < VR; ++u)
-#pragma unroll
-                for (int i = 0; i < VC; ++i)
-                    vf[u][i] = *reinterpret_cast<const uint4 *>(buf + S::v_at(S::v_row(t, u), 8 * i + g));
-            float top[2] = {m[0], m[1]};
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[b][e] = tile * KEYS + b * 8 + 2 * t + (e & 1) < count ? s[b][e] * c2 : -CUDART_INF_F;
-                    top[e >> 1] = fmaxf(top[e >> 1], s[b][e]);
-                }
-            }
-            float keep[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {  // a step has an entry at least, so the maximum is a number
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-                keep[e] = exp2_approx(m[e] - top[e]);
-                l[e] *= keep[e];
-            }
-            if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][e] *= keep[e >> 1];
-                }
-            }
-            m[0] = top[0], m[1] = top[1];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[b][e] = exp2_approx(s[b][e] - m[e >> 1]);
-                    l[e >> 1] += s[b][e];
-                }
-            }
-            if constexpr (sizeof(T) == 2) {
-                // the weights are rounded to bf16, as the values are: 2^-9 of each, below the result's own rounding
-                const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]), a2 = pack(s[NB - 1][0], s[NB - 1][1]),
-                               a3 = pack(s[NB - 1][2], s[NB - 1][3]);
-#pragma unroll
-                for (int i = 0; i < VC; ++i) {
-                    const uint32_t w[4][4] = {{vf[0][i].x, vf[0][i].y, vf[0][i].z, vf[0][i].w},
-                                              {vf[1][i].x, vf[1][i].y, vf[1][i].z, vf[1][i].w},
-                                              {vf[VR - 2][i].x, vf[VR - 2][i].y, vf[VR - 2][i].z, vf[VR - 2][i].w},
-                                              {vf[VR - 1][i].x, vf[VR - 1][i].y, vf[VR - 1][i].z, vf[VR - 1][i].w}};
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
-                        mma_bf16(acc[i * 8 + b], a0, a1, a2, a3, __byte_perm(w[0][b / 2], w[1][b / 2], sel),
-                                 __byte_perm(w[2][b / 2], w[3][b / 2], sel));
-                    }
-                }
+                for (int u = 0; u < QUADS; ++u) four[u].step(k, v, count - tile * KEYS, c2, lane);
             } else {
-                const float a[4] = {s[0][0], s[0][2], s[0][1], s[0][3]};
+                uint4 vf[VR][VC];
+                float s[NB][4];
 #pragma unroll
-                for (int i = 0; i < VC; ++i) {
-                    const float w[2][4] = {{__uint_as_float(vf[0][i].x), __uint_as_float(vf[0][i].y),
-                                            __uint_as_float(vf[0][i].z), __uint_as_float(vf[0][i].w)},
-                                           {__uint_as_float(vf[1][i].x), __uint_as_float(vf[1][i].y),
-                                            __uint_as_float(vf[1][i].z), __uint_as_float(vf[1][i].w)}};
+                for (int b = 0; b < NB; ++b) {
+                    s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_fp32(d, a, w[0][b], w[1][b]);
+                    for (int j = 0; j < KC; ++j) {
+                        const uint4 x = qf[0][j], y = qf[1][j];
+                        const uint4 k = *reinterpret_cast<const uint4 *>(buf + S::k_at(b * 8 + g, 4 * j + t));
+                        if constexpr (sizeof(T) == 2) {
+                            mma_bf16(s[b], x.x, y.x, x.y, y.y, k.x, k.y);
+                            mma_bf16(s[b], x.z, y.z, x.w, y.w, k.z, k.w);
+                        } else {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            const float a0[4] = {__uint_as_float(x.x), __uint_as_float(y.x), __uint_as_float(x.y), __uint_as_float(y.y)};
+                            const float a1[4] = {__uint_as_float(x.z), __uint_as_float(y.z), __uint_as_float(x.w), __uint_as_float(y.w)};
+                            mma_fp32(d, a0, __uint_as_float(k.x), __uint_as_float(k.y));
+                            mma_fp32(d, a1, __uint_as_float(k.z), __uint_as_float(k.w));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i * 4 + b][e] += d[e];
+                            for (int e = 0; e < 4; ++e) s[b][e] += d[e];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < VR; ++u)
+#pragma unroll
+                    for (int i = 0; i < VC; ++i)
+                        vf[u][i] = *reinterpret_cast<const uint4 *>(buf + S::v_at(S::v_row(t, u), 8 * i + g));
+                float top[2] = {m[0], m[1]};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[b][e] = tile * KEYS + b * 8 + 2 * t + (e & 1) < count ? s[b][e] * c2 : -CUDART_INF_F;
+                        top[e >> 1] = fmaxf(top[e >> 1], s[b][e]);
+                    }
+                }
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // a step has an entry at least, so the maximum is a number
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                    keep[e] = exp2_approx(m[e] - top[e]);
+                    l[e] *= keep[e];
+                }
+                if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][e] *= keep[e >> 1];
+                    }
+                }
+                m[0] = top[0], m[1] = top[1];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[b][e] = exp2_approx(s[b][e] - m[e >> 1]);
+                        l[e >> 1] += s[b][e];
+                    }
+                }
+                if constexpr (sizeof(T) == 2) {
+                    // the weights are rounded to bf16, as the values are: 2^-9 of each, below the result's own rounding
+                    const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]), a2 = pack(s[NB - 1][0], s[NB - 1][1]),
+                                   a3 = pack(s[NB - 1][2], s[NB - 1][3]);
+#pragma unroll
+                    for (int i = 0; i < VC; ++i) {
+                        const uint32_t w[4][4] = {{vf[0][i].x, vf[0][i].y, vf[0][i].z, vf[0][i].w},
+                                                  {vf[1][i].x, vf[1][i].y, vf[1][i].z, vf[1][i].w},
+                                                  {vf[VR - 2][i].x, vf[VR - 2][i].y, vf[VR - 2][i].z, vf[VR - 2][i].w},
+                                                  {vf[VR - 1][i].x, vf[VR - 1][i].y, vf[VR - 1][i].z, vf[VR - 1][i].w}};
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
+                            mma_bf16(acc[i * 8 + b], a0, a1, a2, a3, __byte_perm(w[0][b / 2], w[1][b / 2], sel),
+                                     __byte_perm(w[2][b / 2], w[3][b / 2], sel));
+                        }
+                    }
+                } else {
+                    const float a[4] = {s[0][0], s[0][2], s[0][1], s[0][3]};
+#pragma unroll
+                    for (int i = 0; i < VC; ++i) {
+                        const float w[2][4] = {{__uint_as_float(vf[0][i].x), __uint_as_float(vf[0][i].y),
+                                                __uint_as_float(vf[0][i].z), __uint_as_float(vf[0][i].w)},
+                                               {__uint_as_float(vf[1][i].x), __uint_as_float(vf[1][i].y),
+                                                __uint_as_float(vf[1][i].z), __uint_as_float(vf[1][i].w)}};
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_fp32(d, a, w[0][b], w[1][b]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i * 4 + b][e] += d[e];
+                        }
                     }
                 }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the rings have been read
-        // the warps' sums: lane (g, t) has, of rows g and g + 8, channels 8 CH i + CH (2 t + e) + b
+        if constexpr (QUADS > 0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            const int r = g + e * 8;
-            if (r >= heads) continue;
-            if (t == 0) stat[(warp * HEADS + r) * 2] = m[e], stat[(warp * HEADS + r) * 2 + 1] = l[e];
-            float *dst = part + (warp * HEADS + r) * D;
+            for (int u = 0; u < QUADS; ++u)
+                four[u].store(part + (warp * HEADS + 4 * u) * D, stat + (warp * HEADS + 4 * u) * 2, heads - 4 * u, lane);
+        } else {
+            // the warps' sums: lane (g, t) has, of rows g and g + 8, channels 8 CH i + CH (2 t + e) + b
 #pragma unroll
-            for (int i = 0; i < VC; ++i) {
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                const int r = g + e * 8;
+                if (r >= heads) continue;
+                if (t == 0) stat[(warp * HEADS + r) * 2] = m[e], stat[(warp * HEADS + r) * 2 + 1] = l[e];
+                float *dst = part + (warp * HEADS + r) * D;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int i = 0; i < VC; ++i) {
 #pragma unroll
-                    for (int b = 0; b < CH; b += 4)
-                        *reinterpret_cast<float4 *>(dst + 8 * CH * i + CH * (2 * t + u) + b) =
-                            make_float4(acc[i * CH + b][2 * e + u], acc[i * CH + b + 1][2 * e + u],
-                                        acc[i * CH + b + 2][2 * e + u], acc[i * CH + b + 3][2 * e + u]);
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int b = 0; b < CH; b += 4)
+                            *reinterpret_cast<float4 *>(dst + 8 * CH * i + CH * (2 * t + u) + b) =
+                                make_float4(acc[i * CH + b][2 * e + u], acc[i * CH + b + 1][2 * e + u],
+                                            acc[i * CH + b + 2][2 * e + u], acc[i * CH + b + 3][2 * e + u]);
+                    }
                 }
             }
         }
@@ -366,11 +469,11 @@ win_decode_kernel(WinCacheArgs p, int cl) {
     }
 }
 
-template <typename T, int D> cudaError_t decode(const WinCacheArgs &a, cudaStream_t s) {
+template <typename T, int D, int QUADS> cudaError_t decode(const WinCacheArgs &a, cudaStream_t s) {
     constexpr size_t sums = (DW * HEADS * D + HEADS * D + DW * HEADS * 2 + HEADS * 2) * sizeof(float);
     constexpr size_t rings = DW * Shape<T, D>::STAGES * Shape<T, D>::STAGE, smem = sums > rings ? sums : rings;
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(win_decode_kernel<T, D>, smem, allowed);
+    cudaError_t e = allow_smem(win_decode_kernel<T, D, QUADS>, smem, allowed);
     if (e != cudaSuccess) return e;
     // CTAs of a cluster: as many as still run all at once (two on an SM, less what does not come out even with the
     // clusters' places: 75 sequences of one head in clusters of four, 300 CTAs, took 25.8 us, in pairs 19.5; 64 in
@@ -390,7 +493,7 @@ template <typename T, int D> cudaError_t decode(const WinCacheArgs &a, cudaStrea
     c.stream = s;
     c.attrs = &attr;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, win_decode_kernel<T, D>, a, cl);
+    return cudaLaunchKernelEx(&c, win_decode_kernel<T, D, QUADS>, a, cl);
 }
 
 }  // namespace
@@ -403,8 +506,13 @@ cudaError_t launch_window_cache_write(const WinCacheArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_window_decode(const WinCacheArgs &a, cudaStream_t s) {
-    if (a.dt == KDA_BF16) return a.d == 128 ? decode<__nv_bfloat16, 128>(a, s) : decode<__nv_bfloat16, 64>(a, s);
-    return a.d == 128 ? decode<float, 128>(a, s) : decode<float, 64>(a, s);
+    const int group = a.hq / a.hk;
+    auto of = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (a.dt == KDA_BF16) return decode<__nv_bfloat16, D, 0>(a, s);
+        return group <= 4 ? decode<float, D, 1>(a, s) : group <= 8 ? decode<float, D, 2>(a, s) : decode<float, D, 0>(a, s);
+    };
+    return a.d == 128 ? of(std::integral_constant<int, 128>{}) : of(std::integral_constant<int, 64>{});
 }
 
 }  // namespace kda
