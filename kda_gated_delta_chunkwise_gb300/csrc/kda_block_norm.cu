@@ -17,7 +17,7 @@
 // everything in between are fp32; the only rounding to fewer bits is the store
 // (y is made from the unrounded h). Sums over rows have a fixed order. 16384 rows of
 // 16 x 128 bf16 channels, as calls one after the other: gated 34.5 us (5.8 TB/s), its
-// gradients 66 (5.1); residual with a stream in fp32 66 (6.1), its gradients 101 (6.0).
+// gradients 65 (5.2); residual with a stream in fp32 66 (6.1), its gradients 101 (6.0).
 #include <type_traits>
 
 #include "kda_block_norm.cuh"
@@ -165,10 +165,10 @@ kda_gated_norm_bwd_kernel(GatedArgs p, int rows) {
                 ss = fma2(xe, xe, ss);
                 xd = fma2(xe, ud[e] * wv, xd);
             }
-            const float r = rnorm(row_sum<LANES>(f2_sum(ss)), p.norm, 1.f / D, p.eps);
-            const float c = p.norm == KDA_NORM_NONE
-                                ? 0.f
-                                : row_sum<LANES>(f2_sum(xd)) * r * (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
+            float xx = f2_sum(ss), xdn = f2_sum(xd);
+            row_sums<LANES>(xx, xdn);
+            const float r = rnorm(xx, p.norm, 1.f / D, p.eps);
+            const float c = p.norm == KDA_NORM_NONE ? 0.f : xdn * r * (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
             const F2 r2 = f2(r, r), c2 = f2(-c, -c);
 #pragma unroll
             for (int e = 0; e < N / 2; ++e) {

@@ -21,9 +21,11 @@
 // with A and B made once per token. Sums, norms and the rotation are in fp32;
 // the only rounding to fewer bits is the store. 16384 tokens x (16 + 16) heads
 // of 128 bf16 channels: forward 51.3 us (5.3 TB/s, 78 % of a copy), backward with
-// both weights' gradients 79 (5.1 TB/s, 76 %), the last sum included. With positions
-// of three axes: in blocks of four pairs (16 bytes of the table at a time) 61 and 81,
-// in turn over the pairs (4 bytes at a time) 66 and 85.
+// both weights' gradients 73 (5.5 TB/s, 82 %), the last sum included (79 with the
+// partners and both sums of a row by shuffles of their own: backward, the partners'
+// pieces are in shared memory). With positions of three axes: in blocks of four pairs
+// (16 bytes of the table at a time) 61 and 75, in turn over the pairs (4 bytes at a
+// time) 66 and 79.
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
 #include "kda_rows.cuh"
@@ -382,7 +384,13 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
                 Vec<T> vx, vd;
                 vx.load(reinterpret_cast<const T *>(buf + i * 512 + lane * 16));
                 vd.load(reinterpret_cast<const T *>(buf + (kPasses + i) * 512 + lane * 16));
-                const Vec<T> o = partner(vd, p.layout, g);
+                Vec<T> o;
+                if (p.layout == KDA_ROPE_HALF) {  // another lane's piece
+                    o.load(reinterpret_cast<const T *>(buf + (kPasses + i) * 512 + g.src * 16));
+                    if (p.rot < D && !g.rotated) o.zero();
+                } else {
+                    o = partner(vd, p.layout, g);
+                }
                 F2 d[N / 2], dn[N / 2], ss = f2(0.f, 0.f), xd = ss;
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {
@@ -392,12 +400,14 @@ kda_qk_norm_rope_bwd_kernel(NormRopeArgs p, Parts parts) {
                     ss = fma2(xe, xe, ss);
                     xd = fma2(xe, dn[e], xd);
                 }
-                const float r = rnorm(row_sum<LANES>(f2_sum(ss)), p.norm, 1.f / D, p.eps);
+                float xx = f2_sum(ss), xdn = f2_sum(xd);
+                row_sums<LANES>(xx, xdn);
+                const float r = rnorm(xx, p.norm, 1.f / D, p.eps);
                 // n . dn c: r meets x before it meets itself, since r^3 has a third of fp32's range (a zero row
                 // under eps = 1e-30, a row of 1e13)
                 const float c = p.norm == KDA_NORM_NONE
                                     ? 0.f
-                                    : row_sum<LANES>(f2_sum(xd)) * r * (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
+                                    : xdn * r * (p.norm == KDA_NORM_RMS ? 1.f / D : 1.f);
                 const F2 r2 = f2(r, r), c2 = f2(-c, -c);
 #pragma unroll
                 for (int e = 0; e < N / 2; ++e) {

@@ -41,6 +41,17 @@ template <int LANES> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Two at once: the halves of the lanes carry one each, five shuffles of 16 lanes
+// instead of eight. The same bits.
+template <int LANES> __device__ __forceinline__ void row_sums(float &a, float &b) {
+    const bool up = threadIdx.x & (LANES / 2);
+    const float give = up ? a : b, keep = up ? b : a;
+    const float v = row_sum<LANES / 2>(keep + __shfl_xor_sync(0xffffffffu, give, LANES / 2));
+    const float other = __shfl_xor_sync(0xffffffffu, v, LANES / 2);
+    a = up ? other : v;
+    b = up ? v : other;
+}
+
 // From global or shared memory, 4 N-byte aligned.
 template <int N> __device__ __forceinline__ void load_floats(const float *p, float *x) {
     if constexpr (N % 4 == 0) {
