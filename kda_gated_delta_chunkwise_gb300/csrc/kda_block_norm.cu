@@ -18,6 +18,7 @@
 // (y is made from the unrounded h). Sums over rows have a fixed order. 16384 rows of
 // 16 x 128 bf16 channels, as calls one after the other: gated 34.5 us (5.8 TB/s), its
 // gradients 65 (5.2); residual with a stream in fp32 66 (6.1), its gradients 101 (6.0).
+#include <cfloat>
 #include <type_traits>
 
 #include "kda_block_norm.cuh"
@@ -32,11 +33,9 @@ constexpr int GT = 256, GW = GT / 32;
 constexpr int kPasses = 4;  // row groups of a warp in flight at once (forward)
 
 // e^-g. fp32 gates take the accurate exponential; to a bf16 result the 2^-22 of
-// the approximate one is nothing. A sum 1 + e that overflowed would make
-// e / (1 + e) NaN, so e stops at 5e34, where the sigmoid is nothing.
+// the approximate one is nothing.
 template <typename T> __device__ __forceinline__ float exp_neg(float g) {
-    const float e = sizeof(T) == 2 ? exp2_approx(g * -1.4426950408889634f) : expf(-g);
-    return e > 5e34f ? 5e34f : e;
+    return sizeof(T) == 2 ? exp2_approx(g * -1.4426950408889634f) : expf(-g);
 }
 template <typename T> __device__ __forceinline__ float recip(float x) {
     if constexpr (sizeof(T) == 2) {
@@ -47,11 +46,15 @@ template <typename T> __device__ __forceinline__ float recip(float x) {
         return 1.f / x;
     }
 }
-// the gate's value and its derivative; 1 - sigmoid as e / (1 + e), which keeps its digits
+// The gate's value and its derivative; 1 - sigmoid as e / (1 + e), which keeps its
+// digits, and is one where e is large, infinite even: there the sigmoid is e^g down
+// to nothing. A gate of -inf or the type's lowest value is closed, in silu too, where
+// g is kept finite for that.
 template <typename T> __device__ __forceinline__ void gate_of(float g, int act, float &a, float &da) {
-    const float e = exp_neg<T>(g), s = recip<T>(1.f + e), c = e * s;
-    a = act == KDA_ACT_SILU ? g * s : s;
-    da = act == KDA_ACT_SILU ? s * fmaf(g, c, 1.f) : s * c;
+    const float e = exp_neg<T>(g), s = recip<T>(1.f + e), c = e > 1e30f ? 1.f : e * s;
+    const float f = fmaxf(g, -FLT_MAX);
+    a = act == KDA_ACT_SILU ? f * s : s;
+    da = act == KDA_ACT_SILU ? s * fmaf(f, c, 1.f) : s * c;
 }
 
 // A row (one head of one token) is held by 16 bytes in each of d sizeof(T) / 16
