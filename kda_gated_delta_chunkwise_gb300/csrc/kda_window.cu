@@ -1,5 +1,5 @@
 // Attention with a sliding window and sinks, and its gradients, in fp32; what both
-// types share: the tile table of packed batches, D, the sinks' sums.
+// types share: the tile table of packed batches, the sinks' sums.
 //
 //   s_ij = scale q_i . k_j over the j that i sees,  lse_i = log sum_j e^{s_ij}
 //   p_ij = e^{s_ij - lse_i},  o_i = sum_j p_ij v_j
@@ -227,12 +227,10 @@ struct WinParams {
     float scale;
     void *o, *dq, *dk, *dv;
     float *lse;               // [tokens][hq], of the forward
-    float *lse2, *delta;      // [hq][tokens], of the gradients: lse (bf16: in powers of two), D
+    float *lse_h, *delta;     // [hq][tokens], of the gradients: lse, D
     float *part, *near;       // gradients of the sinks, see win_far_sum_kernel
     int fars, ranks;          // blocks of far pairs, which come first; CTAs to a block, which share its query heads
 };
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Whether i sees j, among the near pairs or among the far ones.
 __device__ __forceinline__ bool sees(int i, int j, int window, int sinks, bool far) {
@@ -349,42 +347,32 @@ win_forward_kernel(WinParams p) {
     }
 }
 
-// D_i = do_i . o_i, and lse (of bf16 calls in powers of two), both by head: a tile of queries is a
-// stretch of memory then. A block takes eight tokens of every head, in the order of
-// memory, and writes a sector of each head's; a row is 16 bytes in each of
-// d sizeof(T) / 16 lanes.
-template <typename T, int D>
+// D_i = do_i . o_i, and lse, both by head: a tile of queries is a stretch of memory
+// then. (bf16 calls, whose o is rounded, take D from the products: kda_window_tc.cu.)
+// A block takes eight tokens of every head, in the order of memory, and writes a
+// sector of each head's; a row is 16 bytes in each of d / 4 lanes.
+template <int D>
 __global__ void __launch_bounds__(256)
-win_delta_kernel(const T *o, const T *d_o, const float *lse, float *lse2, float *delta, int64_t tokens, int hq) {
-    constexpr int N = 16 / sizeof(T), LANES = D / N, PER = 256 / LANES, FLIGHT = 4;
+win_delta_kernel(const float *o, const float *d_o, const float *lse, float *lse_h, float *delta, int64_t tokens, int hq) {
+    constexpr int LANES = D / 4, PER = 256 / LANES, FLIGHT = 4;
     extern __shared__ float sums[];  // [hq][8]
     let_next_start();
     const int in = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const int64_t t0 = (int64_t)blockIdx.x * 8;
     const int count = (int)(tokens - t0 < 8 ? tokens - t0 : 8), rows = count * hq;
-    const T *ob = o + t0 * hq * D + in * N, *db = d_o + t0 * hq * D + in * N;
+    const float *ob = o + t0 * hq * D + in * 4, *db = d_o + t0 * hq * D + in * 4;
     for (int r0 = 0; r0 < rows; r0 += FLIGHT * PER) {
-        uint4 a[FLIGHT], b[FLIGHT];
+        float4 a[FLIGHT], b[FLIGHT];
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
             const int r = r0 + i * PER + sub;
-            a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                a[i] = *reinterpret_cast<const uint4 *>(ob + (int64_t)r * D), b[i] = *reinterpret_cast<const uint4 *>(db + (int64_t)r * D);
+                a[i] = *reinterpret_cast<const float4 *>(ob + (int64_t)r * D), b[i] = *reinterpret_cast<const float4 *>(db + (int64_t)r * D);
         }
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
-            const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (sizeof(T) == 4) {
-                    s = fmaf(__uint_as_float(x[e]), __uint_as_float(y[e]), s);
-                } else {
-                    s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
-                    s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), s);
-                }
-            }
+            float s = fmaf(a[i].w, b[i].w, fmaf(a[i].z, b[i].z, fmaf(a[i].y, b[i].y, a[i].x * b[i].x)));
 #pragma unroll
             for (int off = LANES / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             const int r = r0 + i * PER + sub;
@@ -396,116 +384,7 @@ win_delta_kernel(const T *o, const T *d_o, const float *lse, float *lse2, float 
         const int h = i >> 3, t = i & 7;
         if (t >= count) continue;
         delta[h * tokens + t0 + t] = sums[i];
-        lse2[h * tokens + t0 + t] = lse[(t0 + t) * hq + h] * (sizeof(T) == 2 ? kLog2e : 1.f);
-    }
-}
-
-// D_i once more as sum_j p_ij dp_ij, for tokens that see few others: all of a
-// narrow window's (few_keys), else the first 64 of every sequence. There a weight
-// may be close to one, ds = p (dp - D) far smaller than dp, and the rounding of the
-// stored bf16 o, which do . o takes into D, would be seen in dq and dk (1.2e-2 of dq
-// for two tokens). A warp takes 16 queries, 16 keys at a time: s and dp are both
-// products of rows, so the fragments of mma.sync come straight from memory (a
-// contraction does not mind the order of its index: a lane reads 16 bytes of
-// consecutive channels).
-__host__ __device__ __forceinline__ bool few_keys(int window, int sinks) { return window + sinks <= 64; }
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <int D>
-__global__ void __launch_bounds__(128)
-win_first_delta_kernel(WinParams p) {
-    using T = __nv_bfloat16;
-    constexpr int KC = D / 32;  // 16-byte pieces of a lane and row
-    const WinGeom &geo = p.geo;
-    const bool firsts = !few_keys(geo.window, geo.sinks);  // `at` counts sequences, else 64 queries
-    const int at = geo.by_hq.div(blockIdx.x), h = blockIdx.x - at * geo.hq, hk = h / geo.group;
-    let_next_start();
-    if (firsts && geo.tiles && geo.seq_tile[at] == geo.seq_tile[at + 1]) {
-        await_previous();
-        return;
-    }
-    const WinTile tile = win_tile(geo, !firsts ? at >> 2 : geo.tiles ? geo.seq_tile[at] : at * geo.per_seq);
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int i0 = (firsts ? 0 : tile.first + (at & 3) * 64) + (threadIdx.x >> 5) * 16;
-    if (i0 >= tile.len) {
-        await_previous();
-        return;
-    }
-    uint4 q[2][KC], d[2][KC];
-    float lse2[2], sum[2] = {0.f, 0.f}, all[2] = {0.f, 0.f};
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int i = i0 + g + 8 * r;
-        const bool there = i < tile.len;
-        const int64_t token = tile.start + (there ? i : 0);
-        const T *qr = (const T *)p.q + token * p.q_stride + h * D + 8 * t, *dr = (const T *)p.d_o + (token * geo.hq + h) * D + 8 * t;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            q[r][c] = there ? *reinterpret_cast<const uint4 *>(qr + 32 * c) : zero;
-            d[r][c] = there ? *reinterpret_cast<const uint4 *>(dr + 32 * c) : zero;
-        }
-        lse2[r] = there ? p.lse[token * geo.hq + h] * kLog2e : 0.f;
-    }
-    const T *kb = (const T *)p.k + (int64_t)tile.start * p.k_stride + hk * D + 8 * t;
-    const T *vb = (const T *)p.v + (int64_t)tile.start * p.v_stride + hk * D + 8 * t;
-    const float c2 = p.scale * kLog2e;
-    auto walk = [&](int from, int to, bool far) {
-        for (int j0 = from; j0 < to; j0 += 16) {
-            float s[2][4], dp[2][4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int j = j0 + 8 * b + g;
-                const bool there = j < to;
-                uint4 k[KC], v[KC];
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    k[c] = there ? *reinterpret_cast<const uint4 *>(kb + (int64_t)j * p.k_stride + 32 * c) : zero;
-                    v[c] = there ? *reinterpret_cast<const uint4 *>(vb + (int64_t)j * p.v_stride + 32 * c) : zero;
-                }
-                s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
-                dp[b][0] = dp[b][1] = dp[b][2] = dp[b][3] = 0.f;
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    mma_bf16(s[b], q[0][c].x, q[1][c].x, q[0][c].y, q[1][c].y, k[c].x, k[c].y);
-                    mma_bf16(s[b], q[0][c].z, q[1][c].z, q[0][c].w, q[1][c].w, k[c].z, k[c].w);
-                    mma_bf16(dp[b], d[0][c].x, d[1][c].x, d[0][c].y, d[1][c].y, v[c].x, v[c].y);
-                    mma_bf16(dp[b], d[0][c].z, d[1][c].z, d[0][c].w, d[1][c].w, v[c].z, v[c].w);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = i0 + g + 8 * (e >> 1), j = j0 + 8 * b + 2 * t + (e & 1);
-                    const float w = j < to && sees(i, j, geo.window, geo.sinks, far)
-                                        ? exp2_approx(fmaf(s[b][e], c2, -lse2[e >> 1]))
-                                        : 0.f;
-                    all[e >> 1] += w;
-                    sum[e >> 1] = fmaf(w, w > 0.f ? dp[b][e] : 0.f, sum[e >> 1]);
-                }
-        }
-    };
-    const int end = min(i0 + 16, tile.len);
-    if (end > geo.window) walk(0, min(geo.sinks, end - geo.window), true);
-    walk(max(0, i0 - geo.window + 1), end, false);
-    await_previous();  // it writes D of these queries too
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int off = 1; off < 4; off *= 2) {
-            all[e] += __shfl_xor_sync(0xffffffffu, all[e], off);
-            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], off);
-        }
-        const int i = i0 + g + 8 * e;
-        if (t == 0 && i < tile.len && all[e] > 0.f) p.delta[(int64_t)h * geo.tokens + tile.start + i] = sum[e] / all[e];
+        lse_h[h * tokens + t0 + t] = lse[(t0 + t) * hq + h];
     }
 }
 
@@ -541,7 +420,7 @@ win_dq_kernel(WinParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const bool there = w.r0 + e * 8 < rows;
-        lse[e] = there ? p.lse2[vec0 + w.r0 + e * 8] : 0.f;
+        lse[e] = there ? p.lse_h[vec0 + w.r0 + e * 8] : 0.f;
         delta[e] = there ? p.delta[vec0 + w.r0 + e * 8] : 0.f;
     }
     auto walk = [&](int from, int to, bool far) {
@@ -635,7 +514,7 @@ win_dkv_kernel(WinParams p) {
         for (int e = 0; e < 2; ++e) {
             const int i = i0 + w.group * 8 + 2 * w.t + e;
             const int64_t x = (int64_t)h * geo.tokens + tile.start + i;
-            next_lse[e] = i < to ? p.lse2[x] : 0.f;
+            next_lse[e] = i < to ? p.lse_h[x] : 0.f;
             next_delta[e] = i < to ? p.delta[x] : 0.f;
         }
     };
@@ -772,7 +651,7 @@ struct WinPlan {
     WinGeom geo;
     int4 *tiles;
     int32_t *seq_tile;
-    float *lse2, *delta, *part, *near;
+    float *lse_h, *delta, *part, *near;
     size_t bytes;
 };
 WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks, bool packed, bool back, bool bf16, void *ws) {
@@ -797,7 +676,7 @@ WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks
         g.tiles = p.tiles, g.seq_tile = p.seq_tile;
     }
     if (back) {
-        p.lse2 = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
+        p.lse_h = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         p.delta = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         if (sinks > 0) {
             const size_t slots = (size_t)g.ntiles / (bf16 ? kWinFarQueries / kWinTile : 1) + N + 1;
@@ -826,7 +705,7 @@ WinParams params(const WinPlan &p, const WinArgs &a) {
     w.q_stride = a.q_stride, w.k_stride = a.k_stride, w.v_stride = a.v_stride;
     w.scale = a.scale;
     w.o = a.o, w.dq = a.dq, w.dk = a.dk, w.dv = a.dv;
-    w.lse = a.lse, w.lse2 = p.lse2, w.delta = p.delta, w.part = p.part, w.near = p.near;
+    w.lse = a.lse, w.lse_h = p.lse_h, w.delta = p.delta, w.part = p.part, w.near = p.near;
     return w;
 }
 template <typename... P>
@@ -845,16 +724,12 @@ template <int D> cudaError_t forward(const WinPlan &p, const WinArgs &a, cudaStr
 template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     WinParams w = params(p, a);
     Launches l{s};
-    KDA_TRY(l.next(win_delta_kernel<T, D>, (unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float),
-                   (const T *)a.out, (const T *)a.d_o, a.lse, p.lse2, p.delta, p.geo.tokens, a.hq));
-    if constexpr (sizeof(T) == 2) {
-        const int blocks = few_keys(p.geo.window, p.geo.sinks) ? p.geo.ntiles * 4 : a.N;
-        KDA_TRY(l.next(win_first_delta_kernel<D>, (unsigned)(blocks * a.hq), 128, 0, w));
-    }
     const bool far = a.sinks > 0 && a.window < a.T;  // some sequence may be longer than the window
     if constexpr (sizeof(T) == 2) {
-        KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse2, p.delta, p.part, p.near, l));
+        KDA_TRY(launch_window_backward_tc(p.geo, a, p.lse_h, p.delta, p.part, p.near, l));
     } else {
+        KDA_TRY(l.next(win_delta_kernel<D>, (unsigned)((p.geo.tokens + 7) / 8), 256, a.hq * 8 * sizeof(float),
+                       (const float *)a.out, (const float *)a.d_o, a.lse, p.lse_h, p.delta, p.geo.tokens, a.hq));
         static std::atomic<uint64_t> allowed[2];
         constexpr size_t weights = ROWS * WS * sizeof(float);
         constexpr size_t dq = (2 * ROWS + 2 * COLS) * MS<D> * sizeof(uint2) + weights, dkv = dq + weights;

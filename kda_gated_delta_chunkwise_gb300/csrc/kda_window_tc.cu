@@ -474,6 +474,248 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
     }
 }
 
+// ================================================================ backward: D
+// D_i = sum_j p_ij dp_ij / sum_j p_ij, from both products of rows again, and not
+// do . o from the stored o: ds = p (dp - D) is far smaller than dp where one weight is
+// close to one, as sinks' are, and the rounding of a bf16 o would be seen in dq and dk (1e-2 of
+// them at a weight of 0.8, 2e-1 at 0.999). The weights' sum takes out the rounding of lse,
+// so that the ds of a row add up to nothing.
+//
+// An item is 256 queries of one head, two contexts of 128 as in the forward; a step is
+// 128 keys (or the sinks), whose K and V both contexts use, so that one's products run
+// while the other's rows are at their weights. The rows also write lse by head, in powers
+// of two: a tile of queries is a stretch of memory then. 4 x 4096 x 16, window 1024:
+// 128 us, bound by the rows, whose instructions wait for one another (39 % of the issue
+// slots). Two threads to a row changed nothing; steps of 64 keys, released sooner, took 140
+// to 160, since their products take as long as those of 128.
+//
+// warp 0: TMA; 1, 2: MMA of the contexts; 4-7, 8-11: their rows, a thread each.
+template <int D> struct Bd {
+    static constexpr int TILE = 128 * D * 2, ATOM = 128 * 128;
+    static constexpr int STAGES = D == 128 ? 3 : 8;                    // K and V in turn
+    static constexpr int RING = 4 * TILE, BAR = RING + STAGES * TILE;  // in front of it Q, Q, dO, dO
+    // QF, OF, QE: the item's Q and dO; of context w: PF, L (a step's S and dP there, in registers)
+    static constexpr int B_QF = 0, B_OF = 1, B_QE = 2, B_PF = 3, B_L = 5, B_KF = 7, B_KE = B_KF + STAGES, COUNT = B_KE + STAGES;
+    static constexpr int SMEM = BAR + COUNT * 8 + 16 + 1024;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+};
+
+struct BdArgs {
+    WinGeom geo;
+    const float *lse;     // [tokens][hq]
+    float *lse2, *delta;  // [hq][tokens]: lse in powers of two, D
+    float c2;
+    int items;
+};
+
+// Whether a context has use for the item's tile j.
+__device__ __forceinline__ bool uses(const FwItem &x, const FwContext &y, int j) {
+    return y.tiles > 0 && (j < x.far ? y.far : j >= y.first && j <= y.last);
+}
+
+template <int D>
+__global__ void __launch_bounds__(FW_THREADS, 1)
+win_delta_tc_kernel(BdArgs p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                    const __grid_constant__ CUtensorMap mk16, const __grid_constant__ CUtensorMap mv16) {
+    using B = Bd<D>;
+    extern __shared__ unsigned char raw[];
+    unsigned char *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + B::BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(bar + B::COUNT);
+    const Abort ab{reinterpret_cast<volatile int *>(tm + 1)};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WinGeom &geo = p.geo;
+    let_next_start();
+    if (tid == 0) {
+        *ab.flag = 0;
+        for (int i = 0; i < B::COUNT; ++i)
+            mbar_init(bar + i, i >= B::B_L && i < B::B_KF ? 4 : i == B::B_QE || i >= B::B_KE ? 2 : 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm;  // S and dP of context 0 | of context 1
+    const uint32_t bars = smem_u32(bar);
+    auto wait = [&](int b, int phase) { return ab.wait_warp(bars + 8 * b, phase & 1); };
+    bool ok = true;
+
+    if (warp == 0) {
+        int s = 0, round = 1, q = 0;  // the next stage and its phase, items so far
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const FwItem x(geo, it);
+            if (x.tiles == 0) continue;
+            if (!(ok = wait(B::B_QE, ++q))) break;
+            const int contexts = x.rows > 128 ? 2 : 1;
+            auto queries = [&](int at, const CUtensorMap *m, int full) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar + full, contexts * B::TILE);
+                    for (int w = 0; w < contexts; ++w)
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sm + (at + w) * B::TILE + c * B::ATOM, m, bar + full, 64 * c, x.h, x.start + x.f + 128 * w);
+                }
+                __syncwarp();
+            };
+            queries(0, &mq, B::B_QF);
+            for (int j = 0; j < 2 * x.tiles; ++j) {  // K and V of a tile
+                if (!(ok = wait(B::B_KE + s, round))) break;
+                if (lane == 0) {
+                    const int tile = j >> 1, row = x.start + x.key0(tile);
+                    const bool is_v = j & 1;
+                    unsigned char *d = sm + B::RING + s * B::TILE;
+                    uint64_t *full = bar + B::B_KF + s;
+                    mbar_arrive_expect_tx(full, x.keys(tile) * D * 2);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        if (tile >= x.far) tma_load_3d(d + c * B::ATOM, is_v ? &mv : &mk, full, 64 * c, x.hk, row);
+                        else
+                            for (int r = 0; r < x.kw; r += 16)
+                                tma_load_3d(d + c * B::ATOM + r * 128, is_v ? &mv16 : &mk16, full, 64 * c, x.hk, row + r);
+                    }
+                }
+                __syncwarp();
+                if (j == 0) queries(2, &mo, B::B_OF);
+                if (++s == B::STAGES) s = 0, round ^= 1;
+            }
+            if (ok && lane == 0 && it + gridDim.x < p.items) {  // the next item's, into L2
+                const FwItem y(geo, it + gridDim.x);
+                for (int w = 0; w < (y.tiles == 0 ? 0 : y.rows > 128 ? 2 : 1); ++w)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        tma_prefetch_3d(&mq, 64 * c, y.h, y.start + y.f + 128 * w);
+                        tma_prefetch_3d(&mo, 64 * c, y.h, y.start + y.f + 128 * w);
+                    }
+            }
+            __syncwarp();
+        }
+    } else if (warp < 3) {
+        const int w = uni(warp - 1);
+        const uint32_t e = elected(), base = uni(tmem) + 256 * w, sb = uni(smem_u32(sm)), bb = uni(bars);
+        constexpr uint32_t I_S = idesc_bf16(128, 128, false, false);
+        const uint64_t qd = desc_k(sb + w * B::TILE), od = desc_k(sb + (2 + w) * B::TILE), kd = desc_k(sb + B::RING);
+        auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
+        int s = 0, round = 0, q = 0, n = 0;  // the next stage and its phase; items, steps of this context so far
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const FwItem x(geo, it);
+            if (x.tiles == 0) continue;
+            const FwContext y(geo, x, w);
+            const int tiles = uni(x.tiles);
+            const uint32_t i0 = uni(x.far) ? idesc_bf16(128, uni(x.kw), false, false) : I_S;  // of the first tile
+            // S from K, dP from V
+            for (int j = 0; j < 2 * tiles; ++j) {
+                const bool mine = uni(uses(x, y, j >> 1)), is_v = j & 1;
+                if (j < 2 && !(ok = on(is_v ? B::B_OF : B::B_QF, q))) break;
+                if (!(ok = on(B::B_KF + s, round))) break;
+                if (mine) {
+                    if (!is_v && !(ok = on(B::B_L + w, n + 1))) break;  // the step before is in registers
+                    tc_fence_after();
+                    const uint64_t a = is_v ? od : qd, b = kd + ((s * B::TILE) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ss_if(e, base + 128 * is_v, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), j < 2 ? i0 : I_S, ks > 0);
+                    if (is_v) {
+                        commit_if(e, bb + 8 * (B::B_PF + w));
+                        ++n;
+                    }
+                }
+                commit_if(e, bb + 8 * (B::B_KE + s));
+                if (++s == B::STAGES) s = 0, round ^= 1;
+            }
+            if (!ok) break;
+            commit_if(e, bb + 8 * B::B_QE);
+            ++q;
+        }
+    } else if (warp >= 4) {
+        const int w = (warp - 4) >> 2, row = tid & 127;
+        const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + 256 * w, td = ts + 128;
+        const F2 c2 = f2(p.c2, p.c2);
+        int n = 0;
+        for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+            const FwItem x(geo, it);
+            const FwContext y(geo, x, w);
+            if (y.tiles == 0) continue;
+            const int i = y.i0 + row;
+            const bool there = i < x.len;
+            const float lse2 = there ? p.lse[(int64_t)(x.start + i) * geo.hq + x.h] * 1.4426950408889634f : CUDART_INF_F;
+            const F2 l2 = f2(-lse2, -lse2);
+            F2 sum = f2(0.f, 0.f), sum1 = sum, all = sum, all1 = sum;
+            for (int j = 0; j < x.tiles; ++j) {
+                if (!uses(x, y, j)) continue;
+                const bool far = j < x.far;
+                if (!(ok = wait(B::B_PF + w, n++))) break;
+                tc_fence_after();
+                const int halves = x.keys(j) > 64 ? 2 : 1;
+#pragma unroll 1
+                for (int u = 0; u < halves; ++u) {
+                    uint32_t v[2][32], d[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld32(ts + 64 * u + 32 * c, v[c]);
+                        tmem_ld32(td + 64 * u + 32 * c, d[c]);
+                    }
+                    tmem_wait_ld();
+                    if (u + 1 == halves) {
+                        tc_fence_before();
+                        warp_arrive(bar + B::B_L + w);
+                    }
+                    const int k0 = x.key0(j) + 64 * u;
+                    constexpr uint32_t NONE = 0xff800000u;  // -inf
+                    // what a row does not see has no weight, whatever its dP is (the sinks' columns may be stale)
+                    if (far || k0 + 63 > y.i0) {
+                        const int hi = (far ? min(geo.sinks, i - geo.window + 1) - 1 : i) - k0;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            v[c >> 5][c & 31] = c > hi ? NONE : v[c >> 5][c & 31];
+                            d[c >> 5][c & 31] = c > hi ? 0u : d[c >> 5][c & 31];
+                        }
+                    }
+                    if (!far && k0 < y.i0 + 128 - geo.window) {
+                        const int lo = i - geo.window + 1 - k0;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            v[c >> 5][c & 31] = c < lo ? NONE : v[c >> 5][c & 31];
+                            d[c >> 5][c & 31] = c < lo ? 0u : d[c >> 5][c & 31];
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float a, b;
+                            f2_get(fma2(pair_w(v[c][e], v[c][e + 1]), c2, l2), a, b);
+                            const F2 w0 = f2(exp2_approx(a), exp2_approx(b));
+                            f2_get(fma2(pair_w(v[c][e + 2], v[c][e + 3]), c2, l2), a, b);
+                            const F2 w1 = f2(exp2_approx(a), exp2_approx(b));
+                            sum = fma2(w0, pair_w(d[c][e], d[c][e + 1]), sum);
+                            sum1 = fma2(w1, pair_w(d[c][e + 2], d[c][e + 3]), sum1);
+                            all = all + w0, all1 = all1 + w1;
+                        }
+                }
+            }
+            if (!ok) break;
+            if (there) {
+                const int64_t at = (int64_t)x.h * geo.tokens + x.start + i;
+                p.delta[at] = f2_sum(sum + sum1) / f2_sum(all + all1);
+                p.lse2[at] = lse2;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    settle(ab);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ================================================================ backward: dk, dv
 // An item is 128 keys of one key head; a step is 128 queries of one of its query
 // heads. Transposed scores, so that keys are the rows:
@@ -1183,8 +1425,7 @@ template <int D> cudaError_t forward(const WinGeom &geo, const WinArgs &a, cudaS
 }
 
 template <int D>
-cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta, float *part, float *near,
-                     Launches &l) {
+cudaError_t backward(const WinGeom &geo, const WinArgs &a, float *lse2, float *delta, float *part, float *near, Launches &l) {
     CUtensorMap mq, mk, mv, mo, mk16, mv16;
     if (!token_map<D>(&mq, a.q, a.q_stride, a.hq, geo.tokens, 128) ||
         !token_map<D>(&mk, a.k, a.k_stride, a.hk, geo.tokens, 128) ||
@@ -1193,14 +1434,19 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
         !token_map<D>(&mk16, a.k, a.k_stride, a.hk, geo.tokens, 16) ||
         !token_map<D>(&mv16, a.v, a.v_stride, a.hk, geo.tokens, 16))
         return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> allowed[2];
+    static std::atomic<uint64_t> allowed[3];
     cudaError_t e = allow_smem(win_dkv_tc_kernel<D>, Bw<D>::SMEM, allowed[0]);
     if (e == cudaSuccess) e = allow_smem(win_dq_tc_kernel<D>, Bq<D>::SMEM, allowed[1]);
+    if (e == cudaSuccess) e = allow_smem(win_delta_tc_kernel<D>, Bd<D>::SMEM, allowed[2]);
+    if (e != cudaSuccess) return e;
+    const int sms = sm_count();
+    const float c2 = a.scale * 1.4426950408889634f;
+    const BdArgs b{geo, a.lse, lse2, delta, c2, geo.ntiles * geo.hq};
+    e = l.next(win_delta_tc_kernel<D>, b.items < sms ? b.items : sms, FW_THREADS, Bd<D>::SMEM, b, mq, mk, mv, mo, mk16, mv16);
     if (e != cudaSuccess) return e;
     const int fars = geo.sinks > 0 && geo.window < geo.T ? geo.ntiles * geo.hk : 0;
     BwArgs p{geo, (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk, (__nv_bfloat16 *)a.dv, lse2, delta, part, near,
-             a.scale, a.scale * 1.4426950408889634f, fars, fars + geo.ntiles * 2 * geo.hk};
-    const int sms = sm_count();
+             a.scale, c2, fars, fars + geo.ntiles * 2 * geo.hk};
     e = l.next(win_dkv_tc_kernel<D>, p.items < sms ? p.items : sms, BW_THREADS, Bw<D>::SMEM, p, mq, mk, mv, mo);
     if (e != cudaSuccess) return e;
     p.items = geo.ntiles * 2 * geo.hq;
@@ -1209,8 +1455,8 @@ cudaError_t backward(const WinGeom &geo, const WinArgs &a, const float *lse2, co
 
 }  // namespace
 
-cudaError_t launch_window_backward_tc(const WinGeom &geo, const WinArgs &a, const float *lse2, const float *delta,
-                                      float *part, float *near, Launches &l) {
+cudaError_t launch_window_backward_tc(const WinGeom &geo, const WinArgs &a, float *lse2, float *delta, float *part,
+                                      float *near, Launches &l) {
     return a.d == 128 ? backward<128>(geo, a, lse2, delta, part, near, l) : backward<64>(geo, a, lse2, delta, part, near, l);
 }
 
