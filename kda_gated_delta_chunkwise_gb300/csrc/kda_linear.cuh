@@ -68,16 +68,20 @@ template <typename F> inline cudaError_t allow_smem(F *kernel, size_t bytes, std
     return e;
 }
 
-// The kernels of one call, one after the other. One launched by next, but for
-// the call's first, may be put on the SMs while the one before it runs out; it
-// begins with after_previous, which waits until that one and its writes are done
-// (and so everything before it). What an earlier kernel of the call wrote it reads
-// with plain loads, not through the read-only path. Measured with it and without:
-// the scan of a forward over 4 x 4096 tokens x 16 heads, 122.7 and 125.2 us for
-// the call; a backward over 2 x 999 x 4, fp32, 63.0 and 63.5. The tensor-core
-// kernels, one CTA an SM, are launched by whole, as usual: launched early they
-// made the long forward (131072 tokens) 1502 us from 1372 and the backward of
-// 4 x 4096 x 16 468 from 454.
+// The kernels of one call, one after the other. One launched by next, but for the
+// call's first, may be put on the SMs while the one before it runs out: it waits until
+// that one and its writes are done (and so everything before it), at its start
+// (after_previous) or later (await_previous), and what an earlier kernel of the call
+// wrote it reads behind that, with plain loads, not through the read-only path. It
+// may read without a wait what kernels before the previous one wrote where the
+// previous one lets it start (let_next_start) only behind a wait of its own, as
+// the kernels of dk and dv in front of those of dq do; it still waits before it ends,
+// since whoever comes next waits for it alone. Measured with it and without: the scan
+// of a forward over 4 x 4096 tokens x 16 heads, 122.7 and 125.2 us for the call; a
+// backward over 2 x 999 x 4, fp32, 63.0 and 63.5; the window's gradients of 4 x 4096 x
+// 16, 469 and 474. Linear attention's tensor-core kernels, one CTA an SM, are launched
+// by whole, as usual: launched early they made the long forward (131072 tokens) 1502
+// us from 1372 and the backward of 4 x 4096 x 16 468 from 454.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void after_previous() {

@@ -959,8 +959,8 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool there = i0 + e < x.len;
-                l[e] = there ? __ldg(p.lse2 + at + e) : CUDART_INF_F;
-                d[e] = there ? __ldg(p.delta + at + e) : 0.f;
+                l[e] = there ? p.lse2[at + e] : CUDART_INF_F;  // of kernels that ran a moment ago: not read-only
+                d[e] = there ? p.delta[at + e] : 0.f;
             }
         };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
