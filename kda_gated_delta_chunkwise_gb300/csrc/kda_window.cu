@@ -25,7 +25,8 @@ namespace {
 // ================================================================ packed batches: the table of tiles
 constexpr int kPrepThreads = 1024;
 __global__ void __launch_bounds__(kPrepThreads)
-win_tiles_kernel(const int32_t *cu, int N, int T_total, int ntiles, int4 *tiles, int32_t *seq_tile, int32_t *user_status) {
+win_tiles_kernel(const int32_t *cu, int N, int T_total, int ntiles, int4 *tiles, int32_t *seq_tile, int32_t *seq_row,
+                 int window, int sinks, int32_t *user_status) {
     __shared__ int bad;
     __shared__ int wsum[kPrepThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -35,29 +36,33 @@ win_tiles_kernel(const int32_t *cu, int N, int T_total, int ntiles, int4 *tiles,
         if (cu[i + 1] < cu[i] || cu[i] < 0 || cu[i + 1] > T_total) atomicOr(&bad, 1);
     __syncthreads();
     const bool b = bad != 0;
-    if (tid == 0) {
-        if (user_status) *user_status = b ? KDA_DEV_BAD_CU_SEQLENS : KDA_DEV_OK;
-        seq_tile[0] = 0;
-    }
-    int base = 0;
-    for (int i0 = 0; i0 < N; i0 += kPrepThreads) {
-        const int i = i0 + tid;
-        int x = i < N && !b ? (cu[i + 1] - cu[i] + kWinTile - 1) / kWinTile : 0;
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+    if (tid == 0 && user_status) *user_status = b ? KDA_DEV_BAD_CU_SEQLENS : KDA_DEV_OK;
+    // the sums of what each sequence has, up to every one; returns that of all
+    auto sums = [&](int32_t *out, auto of) {
+        if (tid == 0) out[0] = 0;
+        int base = 0;
+        for (int i0 = 0; i0 < N; i0 += kPrepThreads) {
+            const int i = i0 + tid;
+            int x = i < N && !b ? of(cu[i + 1] - cu[i]) : 0;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            if (lane == 31) wsum[warp] = x;
+            __syncthreads();
+            int before = base, all = base;
+            for (int w = 0; w < kPrepThreads / 32; ++w) {
+                if (w < warp) before += wsum[w];
+                all += wsum[w];
+            }
+            if (i < N) out[i + 1] = before + x;
+            base = all;
+            __syncthreads();
         }
-        if (lane == 31) wsum[warp] = x;
-        __syncthreads();
-        int before = base, all = base;
-        for (int w = 0; w < kPrepThreads / 32; ++w) {
-            if (w < warp) before += wsum[w];
-            all += wsum[w];
-        }
-        if (i < N) seq_tile[i + 1] = before + x;
-        base = all;
-        __syncthreads();
-    }
+        return base;
+    };
+    const int base = sums(seq_tile, [](int len) { return (len + kWinTile - 1) / kWinTile; });
+    if (seq_row) sums(seq_row, [&](int len) { return win_rows_of(len, window, sinks); });
     __threadfence_block();
     __syncthreads();
     for (int j = tid; j < ntiles; j += kPrepThreads) {
@@ -485,7 +490,7 @@ win_dkv_kernel(WinParams p) {
     const WinTile tile = win_tile(geo, far ? at >> 1 : at >> 2);
     const int j0 = far ? (at & 1) * ROWS : tile.first + (at & 3) * ROWS;
     const int rows = min(ROWS, (far ? min(geo.sinks, tile.len) : tile.len) - j0);
-    if (rows <= 0) return;
+    if (rows <= 0 || (far && min(tile.first + kWinTile, tile.len) <= geo.window)) return;  // no far query either
     const int from = far ? max(tile.first, j0 + geo.window) : j0;
     const int to = far ? min(tile.first + kWinTile, tile.len)
                        : (int)min((int64_t)tile.len, (int64_t)j0 + rows - 1 + geo.window);
@@ -560,11 +565,11 @@ win_dkv_kernel(WinParams p) {
         const int64_t row = ((int64_t)(tile.start + j) * geo.hk + hk) * D + c;
         dk = (float *)p.dk + row, dv = (float *)p.dv + row;
         if (far) {
-            dk = p.part + (((int64_t)win_far_slot(at >> 1, tile.seq, 1) * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
-            dv = dk + (int64_t)geo.sinks * D;
+            dk = p.part + ((win_far_row(geo, tile.seq, tile.start, tile.first, kWinTile) + j) * geo.hk + hk) * 2 * D + c;
+            dv = dk + D;
         } else if (j < geo.sinks && tile.len > geo.window) {
-            dk = p.near + (((int64_t)tile.seq * geo.hk + hk) * 2 * geo.sinks + j) * D + c;
-            dv = dk + (int64_t)geo.sinks * D;
+            dk = p.near + ((int64_t)(win_near_row(geo, tile.seq) + j) * geo.hk + hk) * 2 * D + c;
+            dv = dk + D;
         }
     };
     float *own = reinterpret_cast<float *>(sm);  // [2][ROWS][D + 8]: this CTA's dk and dv, for the cluster
@@ -607,40 +612,56 @@ win_dkv_kernel(WinParams p) {
     tc::cluster_sync();  // nobody leaves while others read its rows
 }
 
-// dk and dv of the sinks that far queries see: `near` [N][hk][2][sinks][d], from
-// the queries within the window, and the far queries' parts [slots][hk][2][sinks][d]
-// (see win_far_slot), added in order: lanes over the channels, eight groups of
-// threads over the parts.
+// dk and dv of the sinks that far queries see: the rows of `near`, from the queries
+// within the window, and those of the far queries' parts (see win_far_row), added in
+// order, every eighth part first, so that eight loads are on their way. A thread takes
+// four channels, in the order of memory. (Rows times key heads are below 2^31: as many
+// rows of k, v, dk and dv lie in memory.)
 template <typename T>
 __global__ void __launch_bounds__(256)
-win_far_sum_kernel(WinGeom geo, const float *part, const float *near, T *dk, T *dv, int d, int per) {
-    __shared__ float red[8][33];
-    const int c = blockIdx.y * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;  // c: of [2][sinks][d]
-    const int nh = blockIdx.x, n = geo.by_hk.div(nh), hk = nh - n * geo.hk;
-    const int64_t size = 2ll * geo.sinks * d;
-    int first = n * geo.per_seq, start = n * geo.T, len = geo.T;
-    if (geo.tiles) {
-        first = geo.seq_tile[n];
-        if (first == geo.seq_tile[n + 1]) return;  // no tokens
-        start = geo.tiles[first].y, len = geo.tiles[first].z;
-    }
-    if (len <= geo.window) return;
-    const int sink = c / d % geo.sinks, queries = per * kWinTile;
-    const bool there = c < size && sink < len;
-    float a = 0.f;
-    if (there) {
-#pragma unroll 4
-        for (int k = geo.window / queries + group; k <= (len - 1) / queries; k += 8)
-            a += part[((int64_t)win_far_slot(first + k * per, n, per) * geo.hk + hk) * size + c];
-    }
-    red[group][threadIdx.x & 31] = a;
-    __syncthreads();
-    if (group == 0 && there) {
+win_far_sum_kernel(WinGeom geo, const float *part, const float *near, T *dk, T *dv, int d, int queries) {
+    const int quads = d / 2;  // fours of channels of a row's [2][d]
+    const int64_t all = (int64_t)(geo.seq_row ? geo.seq_row[geo.N] : geo.N * geo.rows_each) * geo.hk * quads;
+    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += (int64_t)gridDim.x * 256) {
+        const int at = (int)(x / quads), c = (int)(x - (int64_t)at * quads) * 4, row = geo.by_hk.div(at), hk = at - row * geo.hk;
+        int n = 0, sink, start, len = geo.T;
+        if (geo.seq_row) {
+            int hi = geo.N - 1;  // the last sequence whose first row is <= row
+            while (n < hi) {
+                const int m = (n + hi + 1) >> 1;
+                if (geo.seq_row[m] <= row) n = m;
+                else hi = m - 1;
+            }
+            sink = row - geo.seq_row[n];
+            const int4 tile = geo.tiles[geo.seq_tile[n]];
+            start = tile.y, len = tile.z;
+        } else {
+            n = row / geo.rows_each, sink = row - n * geo.rows_each, start = n * geo.T;
+        }
+        float4 a[8];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) a += red[k][threadIdx.x];
-        a += near[(int64_t)nh * size + c];
-        T *dst = c < geo.sinks * d ? dk : dv;
-        dst[((int64_t)(start + sink) * geo.hk + hk) * d + c % d] = from_f32<T>(a);
+        for (int g = 0; g < 8; ++g) a[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int last = (len - 1) / queries;
+        for (int k0 = geo.window / queries; k0 <= last; k0 += 8) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                if (k0 + g > last) continue;
+                const int64_t from = win_far_row(geo, n, start, (k0 + g) * queries, queries) + sink;
+                const float4 y = *reinterpret_cast<const float4 *>(part + (from * geo.hk + hk) * 2 * d + c);
+                a[g].x += y.x, a[g].y += y.y, a[g].z += y.z, a[g].w += y.w;
+            }
+        }
+#pragma unroll
+        for (int g = 1; g < 8; ++g) a[0].x += a[g].x, a[0].y += a[g].y, a[0].z += a[g].z, a[0].w += a[g].w;
+        const float4 y = *reinterpret_cast<const float4 *>(near + (int64_t)at * 2 * d + c);
+        T *dst = (c < d ? dk : dv) + ((int64_t)(start + sink) * geo.hk + hk) * d + (c < d ? c : c - d);
+        const float v[4] = {a[0].x + y.x, a[0].y + y.y, a[0].z + y.z, a[0].w + y.w};
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            const __nv_bfloat162 z[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(z);
+        }
     }
 }
 
@@ -650,7 +671,7 @@ constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct WinPlan {
     WinGeom geo;
     int4 *tiles;
-    int32_t *seq_tile;
+    int32_t *seq_tile, *seq_row;
     float *lse_h, *delta, *part, *near;
     size_t bytes;
 };
@@ -679,9 +700,11 @@ WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks
         p.lse_h = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         p.delta = reinterpret_cast<float *>(take(sizeof(float) * (size_t)g.tokens * hq));
         if (sinks > 0) {
-            const size_t slots = (size_t)g.ntiles / (bf16 ? kWinFarQueries / kWinTile : 1) + N + 1;
-            p.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * slots * hk * sinks * d));
-            p.near = reinterpret_cast<float *>(take(sizeof(float) * 2 * (size_t)N * hk * sinks * d));
+            const int64_t rows = win_rows(N, g.tokens, sinks), of = sizeof(float) * 2 * hk * d;
+            g.rows = (int)rows, g.rows_each = win_rows_of(g.T, window, sinks);
+            p.part = reinterpret_cast<float *>(take((rows + win_part_rows(g.tokens, sinks, bf16 ? kWinFarQueries : kWinTile)) * of));
+            p.near = reinterpret_cast<float *>(take(rows * of));
+            if (packed) g.seq_row = p.seq_row = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * ((size_t)N + 1)));
         }
     }
     return p;
@@ -695,7 +718,8 @@ WinPlan make_plan(int N, int64_t T, int hq, int hk, int d, int window, int sinks
 
 cudaError_t prepare_tiles(const WinPlan &p, const WinArgs &a, cudaStream_t s) {
     if (!a.cu_seqlens) return cudaSuccess;
-    win_tiles_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, p.geo.ntiles, p.tiles, p.seq_tile, a.status);
+    win_tiles_kernel<<<1, kPrepThreads, 0, s>>>(a.cu_seqlens, a.N, a.T, p.geo.ntiles, p.tiles, p.seq_tile, p.seq_row, a.window,
+                                                a.sinks, a.status);
     return cudaGetLastError();
 }
 WinParams params(const WinPlan &p, const WinArgs &a) {
@@ -744,9 +768,11 @@ template <typename T, int D> cudaError_t backward(const WinPlan &p, const WinArg
         KDA_TRY(l.next_clusters(win_dkv_kernel<D>, (unsigned)(w.fars + p.geo.ntiles * 4 * a.hk), w.ranks, NT, dkv, w));
         KDA_TRY(run(win_dq_kernel<D>, allowed[1], (unsigned)(p.geo.ntiles * 4 * a.hq), dq, l, w));
     }
-    if (far)
-        win_far_sum_kernel<T><<<dim3(a.N * a.hk, (2 * a.sinks * D + 31) / 32), 256, 0, s>>>(
-            p.geo, p.part, p.near, (T *)a.dk, (T *)a.dv, D, sizeof(T) == 2 ? kWinFarQueries / kWinTile : 1);
+    if (far) {
+        const int64_t blocks = ((int64_t)p.geo.rows * a.hk * (D / 2) + 255) / 256;  // at most; 152 SMs, eight on each
+        win_far_sum_kernel<T><<<blocks < 152 * 8 ? (unsigned)blocks : 152 * 8, 256, 0, s>>>(
+            p.geo, p.part, p.near, (T *)a.dk, (T *)a.dv, D, sizeof(T) == 2 ? kWinFarQueries : kWinTile);
+    }
     return cudaGetLastError();
 }
 

@@ -25,10 +25,12 @@ struct WinTile {
 struct WinGeom {
     const int4 *tiles;         // packed: {seq, start, len, first}, else null
     const int32_t *seq_tile;   // packed: first tile of each sequence [N + 1]
+    const int32_t *seq_row;    // gradients of a packed batch with sinks: see win_near_row [N + 1], else null
     int N, T, hq, hk, group;   // group: query heads to a key head
     int per_seq, ntiles;       // equal lengths: tiles per sequence; tiles (packed: an upper bound)
     int64_t tokens;
     int window, sinks;
+    int rows_each, rows;       // equal lengths: rows of a sequence; of all sequences at most
     FastDiv by_seq, by_hq, by_hk;
 };
 __device__ __forceinline__ WinTile win_tile(const WinGeom &g, int t) {
@@ -40,9 +42,29 @@ __device__ __forceinline__ WinTile win_tile(const WinGeom &g, int t) {
     return {n, n * g.T, g.T, (t - n * g.per_seq) * kWinTile};
 }
 
-// The part that far queries from tile t on write to, `per` tiles to a part: every
-// sequence's are numbers in a row, and no two sequences share one.
-__device__ __forceinline__ int win_far_slot(int t, int seq, int per) { return t / per + seq; }
+// Where dk and dv of the sinks that far queries see are gathered: rows [hk][2][d], one
+// for each sink of each sequence that is longer than the window, sequence after sequence.
+// There are no more of them than tokens, whatever the number of sequences and sinks.
+__host__ __device__ __forceinline__ int win_rows_of(int len, int window, int sinks) {
+    return len > window ? (sinks < len ? sinks : len) : 0;
+}
+__device__ __forceinline__ int win_near_row(const WinGeom &g, int seq) {  // of sink 0
+    return g.seq_row ? g.seq_row[seq] : seq * g.rows_each;
+}
+// The far queries' parts, `queries` of them to a part, cut where the sequence starts: a
+// sequence's first part has such rows too, one that starts `first` > 0 tokens into its
+// sequence those behind them that its place in the batch gives. (Two parts that are not
+// their sequences' first start `queries` tokens apart or more.)
+__device__ __forceinline__ int64_t win_far_row(const WinGeom &g, int seq, int start, int first, int queries) {
+    return first / queries == g.window / queries
+               ? win_near_row(g, seq)
+               : g.rows + (int64_t)((start + first) / queries - 1) * g.sinks;
+}
+// Rows at most: of the sequences, and of parts that are not their sequences' first.
+inline int64_t win_rows(int N, int64_t tokens, int sinks) {
+    return (int64_t)N * sinks < tokens ? (int64_t)N * sinks : tokens;
+}
+inline int64_t win_part_rows(int64_t tokens, int sinks, int queries) { return tokens / queries * sinks; }
 
 struct WinArgs {
     kda_dtype_t dt;

@@ -762,7 +762,7 @@ struct BwArgs {
 };
 
 struct DkvItem {
-    int seq, start, len, j0, hk, q0, nq, steps, slot;  // q0: the first tile of 128 queries, nq: their number
+    int seq, start, len, first, j0, hk, q0, nq, steps;  // q0: the first tile of 128 queries, nq: their number
     bool far;
     __device__ __forceinline__ DkvItem(const WinGeom &g, int it, int fars) {
         far = it < fars;
@@ -770,13 +770,12 @@ struct DkvItem {
         const int t = g.by_hk.div(it);
         hk = it - t * g.hk;
         const WinTile x = win_tile(g, far ? t : t >> 1);
-        seq = x.seq, start = x.start, len = x.len, slot = 0;
+        seq = x.seq, start = x.start, len = x.len, first = x.first;
         if (far) {
             j0 = 0;
             const int end = min(len, x.first + kWinFarQueries), from = max(x.first, g.window);
             q0 = from >> 7;
             nq = x.first % kWinFarQueries == 0 && from < end ? ((end - 1) >> 7) - q0 + 1 : 0;
-            slot = win_far_slot(t, seq, kWinFarQueries / kWinTile);
         } else {
             j0 = x.first + (t & 1) * 128;
             q0 = j0 >> 7;
@@ -1079,8 +1078,11 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
             const uint32_t src = (half ? t_dk : t_dv) + lanes;
             const float f = half ? p.scale : 1.f;
             __nv_bfloat16 *dst = (half ? p.dk : p.dv) + ((int64_t)(x.start + x.j0 + (warp & 3) * 32) * geo.hk + x.hk) * D;
-            float *sum = (x.far ? p.part : p.near) +
-                         (((int64_t)(x.far ? x.slot : x.seq) * geo.hk + x.hk) * 2 * geo.sinks + (half ? 0 : geo.sinks) + j) * D;
+            float *sum = nullptr;
+            if (sink && there) {
+                const int64_t r = x.far ? win_far_row(geo, x.seq, x.start, x.first, kWinFarQueries) : win_near_row(geo, x.seq);
+                sum = (x.far ? p.part : p.near) + (((r + j) * geo.hk + x.hk) * 2 + (half ? 0 : 1)) * D;
+            }
             const F2 ff = f2(f, f);
             const int r0 = x.j0 + (warp & 3) * 32;  // the warp's first row
 #pragma unroll 1
@@ -1094,7 +1096,7 @@ win_dkv_tc_kernel(BwArgs p, const __grid_constant__ CUtensorMap mq, const __grid
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const F2 g = pair_w(v[u >> 1][16 * (u & 1) + 2 * e], v[u >> 1][16 * (u & 1) + 2 * e + 1]) * ff;
-                        if (sink && there) *reinterpret_cast<unsigned long long *>(sum + c + 16 * u + 2 * e) = g.v;
+                        if (sum) *reinterpret_cast<unsigned long long *>(sum + c + 16 * u + 2 * e) = g.v;
                         r[u][e] = pack2(g);
                     }
                 // a sink's row is written here too, and again when its sums are added up
