@@ -32,39 +32,100 @@ namespace kda {
 namespace {
 
 // ================================================================ prompts into the cache
-constexpr int CT = 256, CTOK = 8;  // tokens a CTA
+// A stretch of the tokens that are kept, of all prompts one after the other, to each
+// block. Every block reads all offsets once, since nothing may be written if any is bad,
+// and adds up on the way what each prompt keeps. (A block to each eight tokens that a
+// prompt might keep, which read all offsets too, took 1388 us for 4096 prompts of 16 tokens
+// and slots of 2052, now 31; 256 of 64, eight heads, 65 and 27; 16 of 4096 46 and 48.)
+constexpr int CT = 256, CTOK = 8, CFLIGHT = 4;  // CTOK: tokens of a stretch come in eights; CFLIGHT: pieces on their way
 __global__ void __launch_bounds__(CT)
 win_cache_write_kernel(WinCacheArgs p, int row16, int es) {  // row16: 16-byte pieces of a token's heads
-    __shared__ int bad;
-    const int tid = threadIdx.x, n = blockIdx.y;
-    if (tid == 0) bad = (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T) ? 1 : 0;
-    __syncthreads();
-    for (int i = tid; i < p.N; i += CT)
-        if (p.cu_seqlens[i + 1] < p.cu_seqlens[i]) atomicOr(&bad, 1);
-    __syncthreads();
-    if (bad) {
-        if (tid == 0 && blockIdx.x == 0 && n == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_CU_SEQLENS);
-        return;
+    __shared__ int bad, missing, first_prompt, first_token;
+    __shared__ int64_t sums[CT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        bad = (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T) ? 1 : 0;
+        missing = 0;
     }
+    __syncthreads();
     bool fresh;
-    const int64_t slot = slot_of(p.slots, n, fresh);
-    if (slot >= p.pool) {
-        if (tid == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, KDA_DEV_BAD_SLOT);
-        return;
+    // a warp's prompts, and the tokens that they keep
+    const int each = (p.N + CT - 1) / CT * 32, n0 = min(p.N, warp * each), n1 = min(p.N, n0 + each);
+    int64_t mine = 0;
+    bool down = false, none = false;
+#pragma unroll 4
+    for (int n = n0 + lane; n < n1; n += 32) {
+        const int64_t len = (int64_t)p.cu_seqlens[n + 1] - p.cu_seqlens[n];
+        down |= len < 0;
+        if (blockIdx.x == 0) none |= slot_of(p.slots, n, fresh) >= p.pool;
+        mine += min(len, (int64_t)p.entries);
     }
-    const int start = p.cu_seqlens[n], len = p.cu_seqlens[n + 1] - start, window = p.entries - p.sinks;
-    const int first = min(p.sinks, len), second = max(first, len - window), kept = first + len - second;
-    for (int x0 = blockIdx.x * CTOK; x0 < kept; x0 += gridDim.x * CTOK) {
-        const int count = min(CTOK, kept - x0);
-        for (int i = tid; i < count * row16; i += CT) {
-            const int x = x0 + i / row16, c = i % row16 * (16 / es), token = x < first ? x : second + x - first;
-            const int64_t entry = slot * p.entries + (token < p.sinks ? token : p.sinks + (token - p.sinks) % window);
-            const int64_t dst = (entry * p.hk * p.d + c) * es;
-            const int64_t ks = ((int64_t)(start + token) * p.k_stride + c) * es, vs = ((int64_t)(start + token) * p.v_stride + c) * es;
-            const uint4 k = *reinterpret_cast<const uint4 *>((const char *)p.k + ks);
-            const uint4 v = *reinterpret_cast<const uint4 *>((const char *)p.v + vs);
-            *reinterpret_cast<uint4 *>((char *)p.k_cache + dst) = k;
-            *reinterpret_cast<uint4 *>((char *)p.v_cache + dst) = v;
+    if (down) atomicOr(&bad, 1);
+    if (none) atomicOr(&missing, 1);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    if (bad || missing) {
+        if (tid == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, bad ? KDA_DEV_BAD_CU_SEQLENS : KDA_DEV_BAD_SLOT);
+        if (bad) return;
+    }
+    int64_t before = 0, all = 0;  // of the warps in front; of all
+#pragma unroll
+    for (int w = 0; w < CT / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    // this block's stretch, and where it starts
+    const int64_t per = ((all + CTOK - 1) / CTOK + gridDim.x - 1) / gridDim.x * CTOK;
+    int64_t at = blockIdx.x * per;
+    const int64_t end = min(all, at + per);
+    if (at >= end) return;
+    if (before <= at && at < before + mine) {  // in one of this warp's prompts
+        for (int n = n0 + lane;; n += 32) {
+            const int kept = n < n1 ? min(p.cu_seqlens[n + 1] - p.cu_seqlens[n], p.entries) : 0;
+            int64_t upto = before + kept;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, off) - before;
+                if (lane >= off) upto += y;
+            }
+            if (upto - kept <= at && at < upto) first_prompt = n, first_token = (int)(at - (upto - kept));
+            before = __shfl_sync(0xffffffffu, upto, 31);
+            if (at < before) break;
+        }
+    }
+    __syncthreads();
+    const int window = p.entries - p.sinks;
+    for (int n = first_prompt, skip = first_token; at < end; ++n, skip = 0) {
+        const int start = p.cu_seqlens[n], len = p.cu_seqlens[n + 1] - start;
+        const int first = min(p.sinks, len), second = max(first, len - window), kept = first + len - second;
+        const int upto_here = (int)min((int64_t)kept, skip + end - at);
+        at += upto_here - skip;
+        const int64_t slot = slot_of(p.slots, n, fresh);
+        if (slot >= p.pool) continue;
+        for (int x0 = skip; x0 < upto_here; x0 += 32) {
+            const int pieces = min(32, upto_here - x0) * row16;
+            for (int i0 = tid; i0 < pieces; i0 += CFLIGHT * CT) {
+                uint4 k[CFLIGHT], v[CFLIGHT];
+#pragma unroll
+                for (int u = 0; u < CFLIGHT; ++u) {
+                    const int i = i0 + u * CT, x = x0 + i / row16, c = i % row16 * (16 / es);
+                    if (i >= pieces) continue;
+                    const int64_t token = start + (x < first ? x : second + x - first);
+                    k[u] = *reinterpret_cast<const uint4 *>((const char *)p.k + (token * p.k_stride + c) * es);
+                    v[u] = *reinterpret_cast<const uint4 *>((const char *)p.v + (token * p.v_stride + c) * es);
+                }
+#pragma unroll
+                for (int u = 0; u < CFLIGHT; ++u) {
+                    const int i = i0 + u * CT, x = x0 + i / row16, c = i % row16 * (16 / es), token = x < first ? x : second + x - first;
+                    if (i >= pieces) continue;
+                    const int64_t entry = slot * p.entries + (token < p.sinks ? token : p.sinks + (token - p.sinks) % window);
+                    const int64_t dst = (entry * p.hk * p.d + c) * es;
+                    *reinterpret_cast<uint4 *>((char *)p.k_cache + dst) = k[u];
+                    *reinterpret_cast<uint4 *>((char *)p.v_cache + dst) = v[u];
+                }
+            }
         }
     }
 }
@@ -499,9 +560,10 @@ template <typename T, int D, int QUADS> cudaError_t decode(const WinCacheArgs &a
 }  // namespace
 
 cudaError_t launch_window_cache_write(const WinCacheArgs &a, cudaStream_t s) {
-    const int es = a.dt == KDA_BF16 ? 2 : 4, most = a.T < a.entries ? a.T : a.entries;  // tokens kept of one sequence
-    const int blocks = (most + CTOK - 1) / CTOK;
-    win_cache_write_kernel<<<dim3(blocks < 1 ? 1 : blocks, a.N), CT, 0, s>>>(a, a.hk * a.d * es / 16, es);
+    const int es = a.dt == KDA_BF16 ? 2 : 4;
+    const int64_t kept = (int64_t)a.N * a.entries < a.T ? (int64_t)a.N * a.entries : a.T, blocks = (kept + CTOK - 1) / CTOK;  // at most
+    constexpr int MOST = 152 * 2048 / CT;  // all that run at once
+    win_cache_write_kernel<<<blocks < 1 ? 1 : blocks < MOST ? (unsigned)blocks : MOST, CT, 0, s>>>(a, a.hk * a.d * es / 16, es);
     return cudaGetLastError();
 }
 
