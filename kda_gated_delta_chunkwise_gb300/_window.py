@@ -14,8 +14,19 @@ from ._linear import _on_stream, _out, _packed, _plain, _ptr, _space, _stream, _
 _MOST = (1 << 31) - 1  # a longer window is as good as this one
 
 
+def _counts(window: int, sinks: int) -> tuple:
+    """The two as C ints, which would be given the low 32 bits of what they do not hold; the library refuses the rest."""
+    if not -_MOST <= sinks <= _MOST:
+        raise ValueError(f"sinks must be 0 to 128, got {sinks}")
+    if window < -_MOST:
+        raise ValueError(f"window must be 1 or more, got {window}")
+    return min(window, _MOST), sinks
+
+
 @functools.lru_cache(maxsize=256)
 def _bytes(name: str, *sizes: int) -> int:
+    if not all(-_MOST <= n <= _MOST for n in sizes):
+        raise ValueError(f"the sizes must fit in 32 bits, got {sizes}")
     return int(getattr(load(), name + "_workspace_bytes")(*sizes))
 
 
@@ -47,11 +58,12 @@ def _inputs(q, k, v, lead: int, scale):
 
 def _attention(q, k, v, cu_seqlens, window, sinks, scale, out, lse, workspace, device_status):
     lib = load()
+    window, sinks = _counts(window, sinks)
     packed = cu_seqlens is not None
     index, lead, hq, hk, d, strides, scale = _inputs(q, k, v, 1 if packed else 2, scale)
     out = _out(out, "out", q, q.shape, q.dtype, index)
     lse = _out(lse, "lse", q, q.shape[:-1], torch.float32, index)
-    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), *strides, scale, min(window, _MOST), sinks,
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), *strides, scale, window, sinks,
             out.data_ptr(), lse.data_ptr())
     if packed:
         N, T = _packed(cu_seqlens, device_status, index), lead[0]
@@ -91,6 +103,7 @@ def window_varlen_attention(q, k, v, cu_seqlens, *, window: int, sinks: int = 0,
 
 def _backward(q, k, v, out, lse, d_o, cu_seqlens, window, sinks, scale, workspace, device_status):
     lib = load()
+    window, sinks = _counts(window, sinks)
     packed = cu_seqlens is not None
     index, lead, hq, hk, d, strides, scale = _inputs(q, k, v, 1 if packed else 2, scale)
     _plain(out, "out", q.dtype, index, q.shape)
@@ -100,7 +113,7 @@ def _backward(q, k, v, out, lse, d_o, cu_seqlens, window, sinks, scale, workspac
              "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
              "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device)}
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_o.data_ptr(), _dtype_code(q),
-            *strides, scale, min(window, _MOST), sinks, *(t.data_ptr() for t in grads.values()))
+            *strides, scale, window, sinks, *(t.data_ptr() for t in grads.values()))
     if packed:
         N, T = _packed(cu_seqlens, device_status, index), lead[0]
         ws, size = _space(workspace, _bytes("kda_window_varlen_attention_backward", N, T, hq, hk, d, sinks, _dtype_code(q)), q)
@@ -159,6 +172,7 @@ def window_cache_write(k, v, cu_seqlens, k_cache, v_cache, slots, *, sinks: int 
     KDA_DEV_BAD_SLOT in ``device_status``; after KDA_DEV_BAD_CU_SEQLENS nothing
     is written."""
     lib = load()
+    _counts(1, sinks)
     ks = _view(k, "k", 1)
     index = k.get_device()
     vs = _view(v, "v", 1, k.dtype, index)
@@ -185,6 +199,7 @@ def window_decode_step(q, k, v, k_cache, v_cache, slots, positions, *, sinks: in
     outside [0, P) or a negative position is left out and sets KDA_DEV_BAD_SLOT
     or KDA_DEV_BAD_POSITION in ``device_status``."""
     lib = load()
+    _counts(1, sinks)
     index, (N,), hq, hk, d, strides, scale = _inputs(q, k, v, 1, scale)
     pool, entries = _cache(k, k_cache, v_cache, slots, N, sinks, hk, d, device_status, index)
     _plain(positions, "positions", torch.int32, index, (N,))
