@@ -780,13 +780,16 @@ size_t kda_residual_norm_backward_workspace_bytes(int D);
  *   window  >= 1, as long as you like;  sinks 0 to 128;  scale > 0
  * q, k, v may be views of a wider tensor (token strides as for linear attention);
  * outputs are contiguous. Two calls on the same inputs give the same bits, and a
- * sequence the same ones alone and in a packed batch. fp32 calls are accurate to
- * fp32 (relative 2-norm below 1e-5); in bf16 calls the weights e^{s - lse} (and the
- * ds of the gradients) are rounded to bf16 as operands, which adds about as much as
- * the result's own rounding. Scores are numbers of fp32's range. At most 1024 query
- * heads and 2^30 tokens. An infinity or a
- * NaN in a token's k or v may reach tokens of its own sequence that do not see it
- * (the products multiply it by zero), but no other sequence or key head.
+ * sequence the same ones alone and in a packed batch. In fp32 calls a score is off by
+ * up to 2^-22 |q| |k| scale, and its weight e^{s - lse} by as much relative to itself:
+ * results are within 1e-5 (relative 2-norm) where |q| |k| scale stays below 40, and
+ * dq and dk, in whose ds = p (dp - D) digits cancel, where no weight comes closer to one
+ * than 0.1 as well. In bf16 calls the weights (and the ds of the gradients) are rounded
+ * to bf16 as operands, which adds about as much as the result's own rounding; D is the
+ * sum of p dp, in fp32, whatever o was rounded to. Scores are numbers of fp32's range.
+ * At most 1024 query heads and 2^30 tokens. An infinity or a NaN in a token's k or v
+ * may reach tokens of its own sequence that do not see it (the products multiply it
+ * by zero), but no other sequence or key head.
  */
 kda_status_t kda_window_attention(const void *q, const void *k, const void *v, kda_dtype_t dtype, int64_t q_stride,
                                   int64_t k_stride, int64_t v_stride, float scale, int window, int sinks, void *o,
