@@ -166,7 +166,7 @@ def _on_stream(f):
             with torch.cuda.stream(stream):
                 out = f(*args, **kw)
             for t in (*args, *kw.values()):  # the allocator keeps their memory until the stream is past the call
-                if isinstance(t, torch.Tensor):
+                if isinstance(t, torch.Tensor) and t.is_cuda:  # axes may be a tensor on the host
                     t.record_stream(stream)
             return out
         if index >= 0 and index != torch.cuda.current_device():
