@@ -485,9 +485,11 @@ win_forward_tc_kernel(FwArgs p, const __grid_constant__ CUtensorMap mq, const __
 // 128 keys (or the sinks), whose K and V both contexts use, so that one's products run
 // while the other's rows are at their weights. The rows also write lse by head, in powers
 // of two: a tile of queries is a stretch of memory then. 4 x 4096 x 16, window 1024:
-// 128 us, bound by the rows, whose instructions wait for one another (39 % of the issue
-// slots). Two threads to a row changed nothing; steps of 64 keys, released sooner, took 140
-// to 160, since their products take as long as those of 128.
+// 124 us. A context's step of 3160 cycles (d = 128) is a chain: 1100 until the rows have
+// read S and dP, 350 until the next products are issued, 1650 of products, the other
+// context's among them; d = 64 takes 2250, all of them the rows', whose instructions
+// wait for one another. Two threads to a row changed nothing; steps of 64 keys, read
+// sooner, took 140 to 160 us, since their products take as long as those of 128.
 //
 // warp 0: TMA; 1, 2: MMA of the contexts; 4-7, 8-11: their rows, a thread each.
 template <int D> struct Bd {
@@ -507,11 +509,6 @@ struct BdArgs {
     float c2;
     int items;
 };
-
-// Whether a context has use for the item's tile j.
-__device__ __forceinline__ bool uses(const FwItem &x, const FwContext &y, int j) {
-    return y.tiles > 0 && (j < x.far ? y.far : j >= y.first && j <= y.last);
-}
 
 template <int D>
 __global__ void __launch_bounds__(FW_THREADS, 1)
@@ -601,35 +598,53 @@ win_delta_tc_kernel(BdArgs p, const __grid_constant__ CUtensorMap mq, const __gr
         const uint64_t qd = desc_k(sb + w * B::TILE), od = desc_k(sb + (2 + w) * B::TILE), kd = desc_k(sb + B::RING);
         auto on = [&](int b, int phase) { return ab.wait_warp(bb + 8 * b, phase & 1); };
         int s = 0, round = 0, q = 0, n = 0;  // the next stage and its phase; items, steps of this context so far
+        auto next = [&]() {
+            if (++s == B::STAGES) s = 0, round ^= 1;
+        };
+        // S and dP of a tile, one behind the other: what this warp does in between is time without a product
+        auto step = [&](uint32_t idesc) {
+            const int sk = s;
+            if (!(ok = on(B::B_KF + s, round))) return;
+            next();
+            const int sv = s;
+            if (!(ok = on(B::B_KF + s, round))) return;
+            next();
+            const uint64_t kb = kd + ((sk * B::TILE) >> 4), vb = kd + ((sv * B::TILE) >> 4);
+            if (!(ok = on(B::B_L + w, ++n))) return;  // the step before is in registers
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_if(e, base, qd + step_k(ks, B::ATOM), kb + step_k(ks, B::ATOM), idesc, ks > 0);
+            commit_if(e, bb + 8 * (B::B_KE + sk));
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_if(e, base + 128, od + step_k(ks, B::ATOM), vb + step_k(ks, B::ATOM), idesc, ks > 0);
+            commit_if(e, bb + 8 * (B::B_PF + w));
+            commit_if(e, bb + 8 * (B::B_KE + sv));
+        };
+        auto pass = [&](int tiles) {  // that the other context alone has use for
+            for (int i = 0; i < 2 * tiles && ok; ++i) {
+                if (!(ok = on(B::B_KF + s, round))) break;
+                commit_if(e, bb + 8 * (B::B_KE + s));
+                next();
+            }
+        };
         for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
             const FwItem x(geo, it);
             if (x.tiles == 0) continue;
             const FwContext y(geo, x, w);
-            const int tiles = uni(x.tiles);
-            const uint32_t i0 = uni(x.far) ? idesc_bf16(128, uni(x.kw), false, false) : I_S;  // of the first tile
-            // S from K, dP from V
-            for (int j = 0; j < 2 * tiles; ++j) {
-                const bool mine = uni(uses(x, y, j >> 1)), is_v = j & 1;
-                if (j < 2 && !(ok = on(is_v ? B::B_OF : B::B_QF, q))) break;
-                if (!(ok = on(B::B_KF + s, round))) break;
-                if (mine) {
-                    if (!is_v && !(ok = on(B::B_L + w, n + 1))) break;  // the step before is in registers
-                    tc_fence_after();
-                    const uint64_t a = is_v ? od : qd, b = kd + ((s * B::TILE) >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss_if(e, base + 128 * is_v, a + step_k(ks, B::ATOM), b + step_k(ks, B::ATOM), j < 2 ? i0 : I_S, ks > 0);
-                    if (is_v) {
-                        commit_if(e, bb + 8 * (B::B_PF + w));
-                        ++n;
-                    }
-                }
-                commit_if(e, bb + 8 * (B::B_KE + s));
-                if (++s == B::STAGES) s = 0, round ^= 1;
-            }
+            const int mine = uni(y.tiles), far = mine > 0 ? uni(y.far) : 0, near = mine - far, others = uni(x.far) - far,
+                      lead = mine > 0 ? uni(y.first - x.far) : 0, behind = uni(x.tiles) - mine - others - lead;
+            const uint32_t i0 = far ? idesc_bf16(128, uni(x.kw), false, false) : I_S;
+            if (!(ok = on(B::B_QF, q) && on(B::B_OF, q))) break;
+            ++q;
+            pass(others);
+            if (ok && far) step(i0);
+            pass(lead);
+            for (int j = 0; j < near && ok; ++j) step(I_S);
+            pass(behind);
             if (!ok) break;
             commit_if(e, bb + 8 * B::B_QE);
-            ++q;
         }
     } else if (warp >= 4) {
         const int w = (warp - 4) >> 2, row = tid & 127;
@@ -645,12 +660,12 @@ win_delta_tc_kernel(BdArgs p, const __grid_constant__ CUtensorMap mq, const __gr
             const float lse2 = there ? p.lse[(int64_t)(x.start + i) * geo.hq + x.h] * 1.4426950408889634f : CUDART_INF_F;
             const F2 l2 = f2(-lse2, -lse2);
             F2 sum = f2(0.f, 0.f), sum1 = sum, all = sum, all1 = sum;
-            for (int j = 0; j < x.tiles; ++j) {
-                if (!uses(x, y, j)) continue;
-                const bool far = j < x.far;
+            int key0 = (x.nf0 + y.first - x.far) * 128;  // of the next near tile
+            for (int j = 0; j < y.tiles; ++j) {
+                const bool far = y.far && j == 0;
                 if (!(ok = wait(B::B_PF + w, n++))) break;
                 tc_fence_after();
-                const int halves = x.keys(j) > 64 ? 2 : 1;
+                const int halves = far && x.kw <= 64 ? 1 : 2;
 #pragma unroll 1
                 for (int u = 0; u < halves; ++u) {
                     uint32_t v[2][32], d[2][32];
@@ -664,7 +679,7 @@ win_delta_tc_kernel(BdArgs p, const __grid_constant__ CUtensorMap mq, const __gr
                         tc_fence_before();
                         warp_arrive(bar + B::B_L + w);
                     }
-                    const int k0 = x.key0(j) + 64 * u;
+                    const int k0 = (far ? 0 : key0) + 64 * u;
                     constexpr uint32_t NONE = 0xff800000u;  // -inf
                     // what a row does not see has no weight, whatever its dP is (the sinks' columns may be stale)
                     if (far || k0 + 63 > y.i0) {
@@ -697,6 +712,7 @@ win_delta_tc_kernel(BdArgs p, const __grid_constant__ CUtensorMap mq, const __gr
                             all = all + w0, all1 = all1 + w1;
                         }
                 }
+                if (!far) key0 += 128;
             }
             if (!ok) break;
             if (there) {

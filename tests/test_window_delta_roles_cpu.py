@@ -39,25 +39,35 @@ def _delta(items, seed, stages, waits_for_rows=True):
 
     def products(w):
         slot, phase, n = 0, 0, 0
-        for k, item in enumerate(items):
-            for j in range(2 * item.tiles):
-                values = j & 1
-                if j < 2:
-                    yield (OF if values else QF).wait(k)
-                yield KF[slot].wait(phase)
-                if uses(item, w, j >> 1):
-                    if not values and waits_for_rows:
-                        yield L[w].wait(n + 1)
 
-                    def go(k=k, j=j, values=values, slot=slot):
-                        assert ring[slot] == (k, j) and at["dO" if values else "Q"] == k
-                        made[w][values] = (k, j >> 1)
-                    m.issue(go, *([PF[w]] if values else []))
-                    n += values
-                m.issue(_always, KE[slot])
-                slot += 1
-                if slot == stages:
-                    slot, phase = 0, phase ^ 1
+        def step():
+            nonlocal slot, phase
+            slot += 1
+            if slot == stages:
+                slot, phase = 0, phase ^ 1
+
+        for k, item in enumerate(items):
+            yield QF.wait(k)
+            yield OF.wait(k)
+            for j in range(item.tiles):
+                pair = []
+                for _ in range(2):  # K and V
+                    yield KF[slot].wait(phase)
+                    if uses(item, w, j):
+                        pair.append(slot)
+                    else:
+                        m.issue(_always, KE[slot])
+                    step()
+                if not pair:
+                    continue
+                n += 1
+                if waits_for_rows:
+                    yield L[w].wait(n)
+                for values in (0, 1):
+                    def go(k=k, j=j, values=values, where=pair[values]):
+                        assert ring[where] == (k, 2 * j + values) and at["dO" if values else "Q"] == k
+                        made[w][values] = (k, j)
+                    m.issue(go, *([PF[w]] if values else []), KE[pair[values]])
             m.issue(_always, QE)
 
     def rows(w):
