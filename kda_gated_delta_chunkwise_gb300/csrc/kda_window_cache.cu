@@ -16,10 +16,12 @@
 // lane reads 16 bytes of consecutive channels and the query's fragments are read
 // the same way; for the values' product a lane holds the entries and channels that
 // its fragments want, two entries' halves joined by a byte permutation. That case takes
-// 304 us (7.1 TB/s). fp32 calls of up to eight heads to a key head go another way (see
-// FourHeads): 256 sequences, 16 heads over 4, 3000 entries 450 us (7.0 TB/s), by split tf32
-// 780; 8 over 1 153 and 219; of 16 over 2, which stay there, 451 (3.5). Few sequences are cut over the CTAs of a cluster, whose sums are joined
-// through distributed shared memory in rank order.
+// 304 us (7.1 TB/s). fp32 calls of up to eight query heads to a key head go another way
+// (see FourHeads): 256 sequences of 3000 entries, four heads to each of four key heads 450
+// us (7.0 TB/s), by split tf32 780; eight to one 153 and 219. More heads to a key head stay
+// with split tf32: sixteen to each of two 451 us (3.5 TB/s). Few sequences are cut over the
+// CTAs of a cluster, whose sums are joined through distributed shared memory in rank
+// order.
 #include <math_constants.h>
 
 #include <type_traits>

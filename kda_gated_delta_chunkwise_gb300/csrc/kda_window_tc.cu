@@ -4,8 +4,14 @@
 // The kernels are persistent, one CTA per SM; roles are warps that meet at
 // mbarriers, and every role walks the same items and steps. Every wait is
 // bounded: one that runs out sets the device error word and the CTA's abort flag,
-// every role leaves its loop, and the CTA ends normally. Every waiter of a barrier
-// waits for each of its phases in turn.
+// every role leaves its loop, and the CTA ends normally. A waiter of a barrier waits
+// for each of its phases in turn, since a wait knows a phase by its parity alone. One
+// does not: the forward's rows wait for PV only when they rescale O, and skip phases.
+// There the order of the products stands in: S of step n, which they have waited
+// for, was issued behind PV of step n - 2, whose commit arrives before its own, and PV
+// of step n - 1 is the last one issued until their weights of step n are there: the
+// barrier is in its phase n - 1 or has just ended it. Another order of the products
+// would want a wait for every phase.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -117,9 +123,11 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16 *first, int64_t stride,
 // only when a row's maximum has grown by more than 2^8 since the last time, and
 // then waits for PV of the step before: the weights are taken against the older
 // maximum until then, up to 2^8, which fp32 sums and bf16 weights carry as well.
-// That case takes 120 us (1.0 PFLOP/s, 52 % of the measured rate of a large product), 65,531 packed
-// tokens of 32 heads over 8 key heads, window 2048, 1.40 ms (1.23, 63 %): bound by
-// the softmax of a step and the item's start and end, in turn with the products.
+// That case takes 128 us as calls one after the other (940 TFLOP/s, 48 % of the measured
+// rate of a large product), 65,531 packed tokens of 32 heads over 8 key heads, window
+// 2048, 1.47 ms with the write into the cache (1.17 PFLOP/s, 60 %): bound by the rows, a
+// step's softmax in turn with its products, and O of an item, which they store while the
+// next one's scores wait.
 //
 // warp 0: TMA, 128 keys a tile; 1, 2: MMA of the contexts (and zeros behind a
 // sequence's end); 4-7, 8-11: the rows of the contexts, a thread each.
