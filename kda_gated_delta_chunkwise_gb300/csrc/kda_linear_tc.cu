@@ -503,7 +503,7 @@ lin_scan_tc_kernel(LinGeom geo, const float *__restrict__ own, const float *__re
 //   P = x y^T, scaled by D_ij and the mask, rounded to bf16 in place (each half
 //   of the columns into the front of its own half);
 //   O += P z, P read from TMEM.
-// P and S are the two roundings to bf16 (2^-9 relative each, as small as the
+// P and S are the two roundings to bf16 (2^-8 relative at most, as small as the
 // rounding of the result itself: dv is 2.35e-3 from 64 bits in the 2-norm, the
 // result's rounding alone 1.66e-3); sums are fp32. With DOTS S is exact to 24
 // bits and P alone is rounded: dq and dk 1.9e-3 to 2.3e-3.

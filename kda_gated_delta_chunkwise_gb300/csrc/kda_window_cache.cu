@@ -422,7 +422,8 @@ win_decode_kernel(WinCacheArgs p, int cl) {
                     }
                 }
                 if constexpr (sizeof(T) == 2) {
-                    // the weights are rounded to bf16, as the values are: 2^-9 of each, below the result's own rounding
+                    // the weights are rounded to bf16, as the values are: by 2^-8 of each at most and independently of
+                    // one another, so that their sum is off by no more than the result's own rounding
                     const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]), a2 = pack(s[NB - 1][0], s[NB - 1][1]),
                                    a3 = pack(s[NB - 1][2], s[NB - 1][3]);
 #pragma unroll
